@@ -7,7 +7,9 @@ memory and the stream.  The functions carry the C names:
     kda_prefill_algo, kda_prefill_workspace_bytes, kda_prefill_windows, kda_prefill_segments, kda_prefill,
     kda_prefill_with_events (as kda_prefill(..., stage_events=...)),
     kda_prefill_host_scratch_bytes, kda_prefill_host, kda_decode, kda_decode_multi,
-    kda_workspace_status, kda_status_str
+    kda_decode_tree, kda_tree_commit, kda_workspace_status, kda_status_str,
+    kda_ssm_prefill_algo, kda_ssm_prefill_workspace_bytes, kda_ssm_prefill,
+    kda_ssm_decode_workspace_bytes, kda_ssm_decode
 
 There is no fallback: if ``libkda.so`` is missing the import of this package
 still succeeds, but the first call raises ``KdaLibraryMissing``.
@@ -61,6 +63,23 @@ class kda_params(ctypes.Structure):
     ]
 
 
+class kda_ssm_params(ctypes.Structure):
+    _fields_ = [
+        ("num_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("state_dim", ctypes.c_int32),
+        ("num_groups", ctypes.c_int32),
+        ("conv_kernel", ctypes.c_int32),
+        ("io_dtype", ctypes.c_int32),
+        ("algo", ctypes.c_int32),
+        ("conv_w", _vp),
+        ("conv_b", _vp),
+        ("A_log", _vp),
+        ("dt_bias", _vp),
+        ("D", _vp),
+    ]
+
+
 _lib = None
 
 
@@ -95,6 +114,22 @@ def lib():
         L.kda_prefill_host.argtypes = ([P] + [_vp] * 6 + [ctypes.POINTER(ctypes.c_int64), i32, i64] + [_vp] * 5
                                        + [i64, _vp, sz, _vp, _vp, _vp])
         L.kda_prefill_host.restype = ctypes.c_int
+        L.kda_decode_tree.argtypes = [P, i32, i32] + [_vp] * 6 + [_vp, _vp, i32] + [_vp] * 4
+        L.kda_decode_tree.restype = ctypes.c_int
+        L.kda_tree_commit.argtypes = [P, i32, i32] + [_vp] * 5 + [_vp, _vp, i32, _vp, i32] + [_vp] * 5
+        L.kda_tree_commit.restype = ctypes.c_int
+        SP = ctypes.POINTER(kda_ssm_params)
+        L.kda_ssm_prefill_algo.argtypes = [SP]
+        L.kda_ssm_prefill_algo.restype = i32
+        L.kda_ssm_prefill_workspace_bytes.argtypes = [SP, i32, i64]
+        L.kda_ssm_prefill_workspace_bytes.restype = sz
+        L.kda_ssm_prefill.argtypes = ([SP] + [_vp, i64] * 3 + [ctypes.POINTER(ctypes.c_int64), i32, i64] + [_vp] * 5
+                                      + [_vp, sz, _vp])
+        L.kda_ssm_prefill.restype = ctypes.c_int
+        L.kda_ssm_decode_workspace_bytes.argtypes = [SP, i32]
+        L.kda_ssm_decode_workspace_bytes.restype = sz
+        L.kda_ssm_decode.argtypes = [SP, i32] + [_vp, i64] * 3 + [_vp, i32] + [_vp] * 3 + [_vp, sz, _vp]
+        L.kda_ssm_decode.restype = ctypes.c_int
         L.kda_workspace_status.argtypes = [_vp, _vp]
         L.kda_workspace_status.restype = ctypes.c_int
         L.kda_status_str.argtypes = [ctypes.c_int]
@@ -303,3 +338,217 @@ def kda_decode_multi(params: Params, q, k, v, z, b, gout, S_in, ring_in, S_out=N
 
 def kda_workspace_status(workspace, stream=None) -> int:
     return int(lib().kda_workspace_status(_ptr(workspace), _stream(stream)))
+
+
+# ---- draft trees and the state space mixer -------------------------------------------
+
+def _shaped(name, t, dtype, shape):
+    """A dense CUDA tensor of this type and shape, or ValueError (None in ``shape`` is any size)."""
+    if t.dtype != dtype or t.dim() != len(shape) or any(w is not None and s != w for s, w in zip(t.shape, shape)):
+        raise ValueError(f"{name}: expected {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor")
+    return t
+
+
+def _rows(name, t, dtype, n, width):
+    """Row stride in elements of a [n][width] tensor whose rows may lie apart."""
+    if t.dtype != dtype or tuple(t.shape) != (n, width):
+        raise ValueError(f"{name}: expected {dtype} {[n, width]}, got {t.dtype} {list(t.shape)}")
+    if width > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: the elements of a row have to lie side by side")
+    if n <= 1:
+        return 0
+    if t.stride(0) < width:
+        raise ValueError(f"{name}: rows overlap (stride {t.stride(0)} < {width})")
+    return t.stride(0)
+
+
+def _call(name, dev, f, *args, stream=None):
+    """Calls ``f`` with ``dev`` current, on ``stream`` (default: that device's current stream)."""
+    import torch
+    if dev.type != "cuda":
+        raise ValueError(f"{name}: expected CUDA tensors, got {dev}")
+    if dev.index is not None and dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            st = f(*args, _stream(stream))
+    else:
+        st = f(*args, _stream(stream))
+    if st != KDA_OK:
+        raise KdaError(st, name)
+
+
+def _io_torch(io_dtype):
+    import torch
+    return torch.float32 if io_dtype == KDA_DTYPE_F32 else torch.bfloat16
+
+
+KDA_TREE_MAX_NODES = 64
+
+
+def kda_decode_tree(params: Params, q, k, v, z, b, gout, parents, S, ring, slots=None, o=None, stream=None):
+    """The output rows of a tree of drafted tokens per session; state and ring
+    stay as they are.  q, k, v, z, gout: [n][n_nodes][H*128]; b:
+    [n][n_nodes][H]; parents: int32 [n][n_nodes], -1 under the session's last
+    token, parents before children (any other entry leaves the node and those
+    under it out, their rows untouched).  S / ring: pools [n_slots][...];
+    ``slots``: int32 [n].  Returns o."""
+    import torch
+    t = _io_torch(params.io_dtype)
+    if q.dim() != 3:
+        raise ValueError(f"q: expected [n][n_nodes][H*128], got {list(q.shape)}")
+    n, R, H = int(q.shape[0]), int(q.shape[1]), params.num_heads
+    for name, x in (("q", q), ("k", k), ("v", v), ("z", z), ("gout", gout)):
+        _shaped(name, x, t, (n, R, H * 128))
+    _shaped("b", b, t, (n, R, H))
+    _shaped("parents", parents, torch.int32, (n, R))
+    _shaped("S", S, torch.float32, (None, H, 128, 128))
+    _shaped("ring", ring, t, (S.shape[0], 3, 3, H * 128))
+    if slots is not None:
+        _shaped("slots", slots, torch.int32, (n,))
+    o = torch.empty_like(q) if o is None else _shaped("o", o, t, (n, R, H * 128))
+    _call("kda_decode_tree", q.device, lib().kda_decode_tree, params.ref, n, R, _ptr(q), _ptr(k), _ptr(v), _ptr(z), _ptr(b),
+          _ptr(gout), _ptr(parents), _ptr(slots), int(S.shape[0]), _ptr(S), _ptr(ring), _ptr(o), stream=stream)
+    return o
+
+
+def kda_tree_commit(params: Params, q, k, v, z, b, path, path_len, S_in, ring_in, S_out=None, ring_out=None, slots=None,
+                    stream=None):
+    """Advances each session's state and ring by its accepted path: ``path``
+    int32 [n][max_len] node indices in order, ``path_len`` int32 [n].  The
+    token tensors are those of the kda_decode_tree round.  S_out / ring_out
+    default to the input pools (in place).  Returns (S_out, ring_out)."""
+    import torch
+    t = _io_torch(params.io_dtype)
+    if q.dim() != 3 or path.dim() != 2:
+        raise ValueError(f"q, path: expected [n][n_nodes][H*128] and [n][max_len], got {list(q.shape)}, {list(path.shape)}")
+    n, R, H, m = int(q.shape[0]), int(q.shape[1]), params.num_heads, int(path.shape[1])
+    S_out = S_in if S_out is None else S_out
+    ring_out = ring_in if ring_out is None else ring_out
+    for name, x in (("q", q), ("k", k), ("v", v), ("z", z)):
+        _shaped(name, x, t, (n, R, H * 128))
+    _shaped("b", b, t, (n, R, H))
+    _shaped("path", path, torch.int32, (n, m))
+    _shaped("path_len", path_len, torch.int32, (n,))
+    for name, x in (("S_in", S_in), ("S_out", S_out)):
+        _shaped(name, x, torch.float32, (S_in.shape[0], H, 128, 128))
+    for name, x in (("ring_in", ring_in), ("ring_out", ring_out)):
+        _shaped(name, x, t, (S_in.shape[0], 3, 3, H * 128))
+    if slots is not None:
+        _shaped("slots", slots, torch.int32, (n,))
+    _call("kda_tree_commit", q.device, lib().kda_tree_commit, params.ref, n, R, _ptr(q), _ptr(k), _ptr(v), _ptr(z), _ptr(b),
+          _ptr(path), _ptr(path_len), m, _ptr(slots), int(S_in.shape[0]), _ptr(S_in), _ptr(S_out), _ptr(ring_in),
+          _ptr(ring_out), stream=stream)
+    return S_out, ring_out
+
+
+@dataclass
+class SsmParams:
+    """The state space mixer's parameter tensors and the C struct that points at them."""
+
+    struct: kda_ssm_params
+    tensors: tuple
+    num_heads: int
+    head_dim: int
+    state_dim: int
+    num_groups: int
+    io_dtype: int
+
+    @property
+    def ref(self):
+        return ctypes.byref(self.struct)
+
+    @property
+    def channels(self):
+        """Conv channels of a token: x (H*P) | B (G*N) | C (G*N)."""
+        return self.num_heads * self.head_dim + 2 * self.num_groups * self.state_dim
+
+
+def make_ssm_params(conv_w, A_log, dt_bias, *, head_dim: int, state_dim: int, num_groups: int = 1, D=None, conv_b=None,
+                    io_dtype: str = "bf16", algo: str = "auto") -> SsmParams:
+    """conv_w [H*P + 2*G*N][4], conv_b [H*P + 2*G*N] or None, A_log, dt_bias, D
+    (or None) [H]: fp32 CUDA tensors.  head_dim P and state_dim N are 64 or
+    128; num_groups G divides H."""
+    import torch
+    H = int(A_log.shape[0])
+    ch = H * int(head_dim) + 2 * int(num_groups) * int(state_dim)
+    for name, x, shape in (("conv_w", conv_w, (ch, 4)), ("conv_b", conv_b, (ch,)), ("A_log", A_log, (H,)),
+                           ("dt_bias", dt_bias, (H,)), ("D", D, (H,))):
+        if x is not None and (x.dtype != torch.float32 or tuple(x.shape) != shape):
+            raise ValueError(f"{name}: expected float32 {list(shape)}, got {x.dtype} {list(x.shape)}")
+    dt = {"f32": KDA_DTYPE_F32, "bf16": KDA_DTYPE_BF16}[io_dtype]
+    tensors = tuple(None if x is None else x.contiguous() for x in (conv_w, conv_b, A_log, dt_bias, D))
+    st = kda_ssm_params(H, int(head_dim), int(state_dim), int(num_groups), 4, dt, _ALGOS[algo], *[_ptr(x) for x in tensors])
+    return SsmParams(st, tensors, H, int(head_dim), int(state_dim), int(num_groups), dt)
+
+
+def kda_ssm_prefill_algo(params: SsmParams) -> str:
+    """'scan' or 'chunked': the prefill algorithm these parameters select."""
+    a = int(lib().kda_ssm_prefill_algo(params.ref))
+    if a < 0:
+        raise KdaError(KDA_ERR_INVALID_ARG, "kda_ssm_prefill_algo")
+    return {KDA_ALGO_SCAN: "scan", KDA_ALGO_CHUNKED: "chunked"}[a]
+
+
+def kda_ssm_prefill_workspace_bytes(params: SsmParams, n_seqs: int, total_tokens: int) -> int:
+    return int(lib().kda_ssm_prefill_workspace_bytes(params.ref, int(n_seqs), int(total_tokens)))
+
+
+def kda_ssm_prefill(params: SsmParams, xbc, dt, cu_seqlens, z=None, S_in=None, S_out=None, ring_in=None, ring_out=None,
+                    o=None, workspace=None, stream=None):
+    """Varlen prefill of the state space mixer.  xbc [T][H*P + 2*G*N], dt
+    [T][H] and z [T][H*P] (or None: no gate) may be column ranges of one
+    projection tensor; ``cu_seqlens`` is a host sequence of n+1 ints.  S_in /
+    S_out: [n][H][N][P] fp32, ring_in / ring_out: [n][3][H*P + 2*G*N].
+    Missing outputs and the workspace are allocated with torch.  Returns
+    (o, S_out, ring_out)."""
+    import torch
+    cu, n, T = _cu_array(cu_seqlens)
+    t, H, P, N, ch = _io_torch(params.io_dtype), params.num_heads, params.head_dim, params.state_dim, params.channels
+    dev = xbc.device
+    sx, sd = _rows("xbc", xbc, t, T, ch), _rows("dt", dt, t, T, H)
+    sz = 0 if z is None else _rows("z", z, t, T, H * P)
+    for name, x in (("S_in", S_in), ("S_out", S_out)):
+        if x is not None:
+            _shaped(name, x, torch.float32, (n, H, N, P))
+    for name, x in (("ring_in", ring_in), ("ring_out", ring_out)):
+        if x is not None:
+            _shaped(name, x, t, (n, 3, ch))
+    o = torch.empty(T, H * P, dtype=t, device=dev) if o is None else _shaped("o", o, t, (T, H * P))
+    if S_out is None:
+        S_out = torch.empty(n, H, N, P, dtype=torch.float32, device=dev)
+    if ring_out is None:
+        ring_out = torch.empty(n, 3, ch, dtype=t, device=dev)
+    if workspace is None:
+        workspace = torch.empty(max(kda_ssm_prefill_workspace_bytes(params, n, T), 256), dtype=torch.uint8, device=dev)
+    _call("kda_ssm_prefill", dev, lib().kda_ssm_prefill, params.ref, _ptr(xbc), sx, _ptr(dt), sd, _ptr(z), sz, cu, n, T,
+          _ptr(S_in), _ptr(S_out), _ptr(ring_in), _ptr(ring_out), _ptr(o), _ptr(workspace),
+          workspace.numel() * workspace.element_size(), stream=stream)
+    return o, S_out, ring_out
+
+
+def kda_ssm_decode_workspace_bytes(params: SsmParams, n_sessions: int) -> int:
+    return int(lib().kda_ssm_decode_workspace_bytes(params.ref, int(n_sessions)))
+
+
+def kda_ssm_decode(params: SsmParams, xbc, dt, S, ring, z=None, slots=None, o=None, workspace=None, stream=None):
+    """One token per session; the pools S [n_slots][H][N][P] and ring
+    [n_slots][3][H*P + 2*G*N] are updated in place.  xbc, dt and z hold one row
+    per session, ``slots`` (int32 [n]) its pool slot.  Returns o."""
+    import torch
+    n = int(xbc.shape[0])
+    t, H, P, N, ch = _io_torch(params.io_dtype), params.num_heads, params.head_dim, params.state_dim, params.channels
+    dev = xbc.device
+    sx, sd = _rows("xbc", xbc, t, n, ch), _rows("dt", dt, t, n, H)
+    sz = 0 if z is None else _rows("z", z, t, n, H * P)
+    _shaped("S", S, torch.float32, (None, H, N, P))
+    _shaped("ring", ring, t, (S.shape[0], 3, ch))
+    if slots is not None:
+        _shaped("slots", slots, torch.int32, (n,))
+    o = torch.empty(n, H * P, dtype=t, device=dev) if o is None else _shaped("o", o, t, (n, H * P))
+    if workspace is None:
+        workspace = torch.empty(max(kda_ssm_decode_workspace_bytes(params, n), 256), dtype=torch.uint8, device=dev)
+    _call("kda_ssm_decode", dev, lib().kda_ssm_decode, params.ref, n, _ptr(xbc), sx, _ptr(dt), sd, _ptr(z), sz, _ptr(slots),
+          int(S.shape[0]), _ptr(S), _ptr(ring), _ptr(o), _ptr(workspace), workspace.numel() * workspace.element_size(),
+          stream=stream)
+    return o

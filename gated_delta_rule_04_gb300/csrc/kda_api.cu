@@ -674,6 +674,47 @@ kda_status kda_decode(const kda_params* p, int32_t n_sessions, const void* q, co
                             stream_);
 }
 
+kda_status kda_decode_tree(const kda_params* p, int32_t n_sessions, int32_t n_nodes, const void* q, const void* k,
+                           const void* v, const void* z, const void* b, const void* gout, const int32_t* parents,
+                           const int32_t* slots, int32_t n_slots, const float* S, const void* ring, void* o,
+                           void* stream_) {
+    kda_status st = check_params(p);
+    if (st != KDA_OK) return st;
+    if (n_sessions < 0 || n_nodes < 1 || n_nodes > KDA_TREE_MAX_NODES || n_slots < 0) return KDA_ERR_INVALID_ARG;
+    if (n_sessions == 0) return KDA_OK;
+    if (slots == nullptr && n_slots < n_sessions) return KDA_ERR_INVALID_ARG;
+    const void* ptrs[8] = {q, k, v, z, gout, o, S, ring};
+    for (int i = 0; i < 8; ++i)
+        if (ptrs[i] == nullptr || !aligned16(ptrs[i])) return KDA_ERR_INVALID_ARG;
+    if (b == nullptr || parents == nullptr) return KDA_ERR_INVALID_ARG;
+    if ((int64_t)n_sessions * p->num_heads > (int64_t)INT32_MAX) return KDA_ERR_UNSUPPORTED;
+    TreeArgs ta{q, k, v, z, b, gout, p->conv_w, p->A_log, p->dt_bias, p->norm_w, parents, slots, S, ring, o, n_sessions,
+                p->num_heads, n_nodes, n_slots, p->gate_lower_bound, p->l2_eps, p->norm_eps, resolved_q_scale(p),
+                p->gate_kind};
+    return cuda_status(launch_tree(ta, p->io_dtype == KDA_DTYPE_BF16, static_cast<cudaStream_t>(stream_)));
+}
+
+kda_status kda_tree_commit(const kda_params* p, int32_t n_sessions, int32_t n_nodes, const void* q, const void* k,
+                           const void* v, const void* z, const void* b, const int32_t* path, const int32_t* path_len,
+                           int32_t max_len, const int32_t* slots, int32_t n_slots, const float* S_in, float* S_out,
+                           const void* ring_in, void* ring_out, void* stream_) {
+    kda_status st = check_params(p);
+    if (st != KDA_OK) return st;
+    if (n_sessions < 0 || n_nodes < 1 || n_nodes > KDA_TREE_MAX_NODES || max_len < 1 || max_len > KDA_TREE_MAX_NODES ||
+        n_slots < 0)
+        return KDA_ERR_INVALID_ARG;
+    if (n_sessions == 0) return KDA_OK;
+    if (slots == nullptr && n_slots < n_sessions) return KDA_ERR_INVALID_ARG;
+    const void* ptrs[8] = {q, k, v, z, S_in, S_out, ring_in, ring_out};
+    for (int i = 0; i < 8; ++i)
+        if (ptrs[i] == nullptr || !aligned16(ptrs[i])) return KDA_ERR_INVALID_ARG;
+    if (b == nullptr || path == nullptr || path_len == nullptr) return KDA_ERR_INVALID_ARG;
+    if ((int64_t)n_sessions * p->num_heads > (int64_t)INT32_MAX) return KDA_ERR_UNSUPPORTED;
+    CommitArgs ca{q, k, v, z, b, p->conv_w, p->A_log, p->dt_bias, path, path_len, slots, S_in, S_out, ring_in, ring_out,
+                  n_sessions, p->num_heads, n_nodes, max_len, n_slots, p->gate_lower_bound, p->l2_eps, p->gate_kind};
+    return cuda_status(launch_commit(ca, p->io_dtype == KDA_DTYPE_BF16, static_cast<cudaStream_t>(stream_)));
+}
+
 kda_status kda_workspace_status(void* workspace, void* stream_) {
     if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) % WS_ALIGN)) return KDA_ERR_WORKSPACE;
     cudaStream_t s = static_cast<cudaStream_t>(stream_);

@@ -210,6 +210,37 @@ struct DecodeArgs {
 };
 cudaError_t launch_decode(const DecodeArgs& a, int io_bf16, cudaStream_t s);
 
+// A tree of drafted tokens (kda_decode_tree) and the state after an accepted
+// path (kda_tree_commit).
+struct TreeArgs {
+    const void *q, *k, *v, *z, *b, *gout;   // [n][n_nodes][H*128]; b [n][n_nodes][H]
+    const float *conv_w, *A_log, *dt_bias, *norm_w;
+    const int32_t* parents;                 // [n][n_nodes]
+    const int32_t* slots;                   // [n] or NULL
+    const float* S;                         // pools, read only
+    const void* ring;
+    void* o;                                // [n][n_nodes][H*128]
+    int32_t n, H, n_nodes, n_slots;
+    float lb, l2_eps, norm_eps, q_scale;
+    int32_t gate_kind;                      // kda_gate
+};
+cudaError_t launch_tree(const TreeArgs& a, int io_bf16, cudaStream_t s);
+
+struct CommitArgs {
+    const void *q, *k, *v, *z, *b;          // [n][n_nodes][H*128]; b [n][n_nodes][H]
+    const float *conv_w, *A_log, *dt_bias;
+    const int32_t *path, *path_len;         // [n][max_len], [n]
+    const int32_t* slots;                   // [n] or NULL
+    const float* S_in;                      // pools; S_out may alias S_in, ring_out ring_in
+    float* S_out;
+    const void* ring_in;
+    void* ring_out;
+    int32_t n, H, n_nodes, max_len, n_slots;
+    float lb, l2_eps;
+    int32_t gate_kind;                      // kda_gate
+};
+cudaError_t launch_commit(const CommitArgs& a, int io_bf16, cudaStream_t s);
+
 // Prefill metadata built on the device from values passed as kernel
 // arguments (no host-to-device copy): for a slice of up to META_SEQS sequences
 // seq0 .. seq0 + n - 1, their token offsets, first chunk index, order entry and

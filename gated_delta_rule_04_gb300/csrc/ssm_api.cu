@@ -1,0 +1,185 @@
+// C ABI of the state space mixer: host-side checks, workspace layout and the
+// launch sequence of each entry point.  As for the KDA entry points, every
+// check happens before anything is enqueued.
+#include <math.h>
+
+#include <algorithm>
+#include <new>
+#include <numeric>
+#include <vector>
+
+#include "ssm_common.cuh"
+
+namespace kda {
+namespace ssm {
+namespace {
+
+constexpr size_t WS_ALIGN = 256;
+
+size_t align_up(size_t x) { return (x + WS_ALIGN - 1) / WS_ALIGN * WS_ALIGN; }
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+int64_t channels(const kda_ssm_params* p) {
+    return (int64_t)p->num_heads * p->head_dim + 2ll * p->num_groups * p->state_dim;
+}
+size_t esize(const kda_ssm_params* p) { return p->io_dtype == KDA_DTYPE_BF16 ? 2 : 4; }
+
+kda_status check_params(const kda_ssm_params* p) {
+    if (p == nullptr) return KDA_ERR_INVALID_ARG;
+    if (p->num_heads < 1 || p->num_heads > (1 << 16)) return KDA_ERR_INVALID_ARG;
+    if (p->num_groups < 1 || p->num_heads % p->num_groups != 0) return KDA_ERR_INVALID_ARG;
+    if ((p->head_dim != 64 && p->head_dim != 128) || (p->state_dim != 64 && p->state_dim != 128) ||
+        p->conv_kernel != CONV_K)
+        return KDA_ERR_UNSUPPORTED;
+    if (p->io_dtype != KDA_DTYPE_F32 && p->io_dtype != KDA_DTYPE_BF16) return KDA_ERR_INVALID_ARG;
+    if (p->algo != KDA_ALGO_AUTO && p->algo != KDA_ALGO_SCAN && p->algo != KDA_ALGO_CHUNKED)
+        return p->algo == KDA_ALGO_CHUNKED_SEGMENTS ? KDA_ERR_UNSUPPORTED : KDA_ERR_INVALID_ARG;
+    if (!p->conv_w || !p->A_log || !p->dt_bias) return KDA_ERR_INVALID_ARG;
+    if (!aligned(p->conv_w, 16) || !aligned(p->conv_b, 16) || !aligned(p->A_log, 4) || !aligned(p->dt_bias, 4) ||
+        !aligned(p->D, 4))
+        return KDA_ERR_INVALID_ARG;
+    return KDA_OK;
+}
+
+// KDA_ALGO_SCAN or KDA_ALGO_CHUNKED, for checked parameters.
+kda_status resolve_algo(const kda_ssm_params* p, int* algo) {
+    if (p->algo == KDA_ALGO_CHUNKED) return KDA_ERR_UNSUPPORTED;
+    *algo = KDA_ALGO_SCAN;
+    return KDA_OK;
+}
+
+// Row strides in elements: 0 is packed; otherwise at least the row's width and,
+// for 16-byte rows, a multiple of 16 bytes.
+bool row_stride(int64_t given, int64_t width, size_t es, bool rows16, int64_t* out) {
+    *out = given == 0 ? width : given;
+    if (*out < width || *out > (int64_t)1 << 40) return false;
+    return !rows16 || (*out * (int64_t)es) % 16 == 0;
+}
+
+// The token tensors of a call (rows > 0), and their strides.
+kda_status check_tokens(const kda_ssm_params* p, const void* xbc, int64_t* xbc_stride, const void* dt, int64_t* dt_stride,
+                        const void* z, int64_t* z_stride, const void* o) {
+    const size_t es = esize(p);
+    if (!xbc || !dt || !o || !aligned(xbc, 16) || !aligned(dt, es) || !aligned(z, 16) || !aligned(o, 16))
+        return KDA_ERR_INVALID_ARG;
+    if (!row_stride(*xbc_stride, channels(p), es, true, xbc_stride) ||
+        !row_stride(*dt_stride, p->num_heads, es, false, dt_stride) ||
+        !row_stride(*z_stride, (int64_t)p->num_heads * p->head_dim, es, z != nullptr, z_stride))
+        return KDA_ERR_INVALID_ARG;
+    return KDA_OK;
+}
+
+// Workspace of a prefill: error word | cu_seqlens | first chunks | order.
+struct Layout {
+    size_t cu = 0, coff = 0, order = 0, total = 0;
+};
+Layout layout(int32_t n_seqs) {
+    Layout L;
+    size_t off = WS_ALIGN;
+    L.cu = off; off = align_up(off + sizeof(int64_t) * ((size_t)n_seqs + 1));
+    L.coff = off; off = align_up(off + sizeof(int64_t) * ((size_t)n_seqs + 1));
+    L.order = off; off = align_up(off + sizeof(int32_t) * (size_t)n_seqs);
+    L.total = off;
+    return L;
+}
+
+}  // namespace
+}  // namespace ssm
+}  // namespace kda
+
+using namespace kda;
+using namespace kda::ssm;
+
+extern "C" {
+
+int32_t kda_ssm_prefill_algo(const kda_ssm_params* p) {
+    int algo;
+    if (ssm::check_params(p) != KDA_OK || ssm::resolve_algo(p, &algo) != KDA_OK) return -1;
+    return algo;
+}
+
+size_t kda_ssm_prefill_workspace_bytes(const kda_ssm_params* p, int32_t n_seqs, int64_t total_tokens) {
+    int algo;
+    if (ssm::check_params(p) != KDA_OK || ssm::resolve_algo(p, &algo) != KDA_OK || n_seqs < 0 || total_tokens < 0)
+        return 0;
+    if (n_seqs == 0) return 0;
+    return ssm::layout(n_seqs).total;
+}
+
+kda_status kda_ssm_prefill(const kda_ssm_params* p, const void* xbc, int64_t xbc_stride, const void* dt,
+                           int64_t dt_stride, const void* z, int64_t z_stride, const int64_t* cu, int32_t n_seqs,
+                           int64_t total_tokens, const float* S_in, float* S_out, const void* ring_in, void* ring_out,
+                           void* o, void* workspace, size_t workspace_bytes, void* stream_) {
+    int algo;
+    kda_status st = ssm::check_params(p);
+    if (st != KDA_OK || (st = ssm::resolve_algo(p, &algo)) != KDA_OK) return st;
+    if (n_seqs < 0 || total_tokens < 0 || cu == nullptr || cu[0] != 0 || cu[n_seqs] != total_tokens)
+        return KDA_ERR_INVALID_ARG;
+    for (int32_t i = 0; i < n_seqs; ++i)
+        if (cu[i + 1] < cu[i]) return KDA_ERR_INVALID_ARG;
+    if (total_tokens > (int64_t)INT32_MAX) return KDA_ERR_UNSUPPORTED;
+    if (n_seqs == 0) return KDA_OK;
+    if (total_tokens > 0 && (st = check_tokens(p, xbc, &xbc_stride, dt, &dt_stride, z, &z_stride, o)) != KDA_OK) return st;
+    if (S_out == nullptr || !aligned(S_out, 16) || !aligned(S_in, 16) || !aligned(ring_in, 16) || !aligned(ring_out, 16))
+        return KDA_ERR_INVALID_ARG;
+    if ((int64_t)n_seqs * p->num_heads > (int64_t)INT32_MAX) return KDA_ERR_UNSUPPORTED;
+    if (workspace == nullptr || !aligned(workspace, WS_ALIGN) ||
+        workspace_bytes < kda_ssm_prefill_workspace_bytes(p, n_seqs, total_tokens))
+        return KDA_ERR_WORKSPACE;
+
+    cudaStream_t s = static_cast<cudaStream_t>(stream_);
+    unsigned char* ws = static_cast<unsigned char*>(workspace);
+    const Layout L = ssm::layout(n_seqs);
+    // longest sequences first: their walks take longest
+    std::vector<int32_t> order;
+    try {
+        order.resize(n_seqs);
+        std::iota(order.begin(), order.end(), 0);
+        std::stable_sort(order.begin(), order.end(),
+                         [&](int32_t x, int32_t y) { return cu[x + 1] - cu[x] > cu[y + 1] - cu[y]; });
+    } catch (const std::bad_alloc&) {
+        return KDA_ERR_CUDA;
+    }
+    int64_t* d_cu = reinterpret_cast<int64_t*>(ws + L.cu);
+    int32_t* d_order = reinterpret_cast<int32_t*>(ws + L.order);
+    if (cudaMemsetAsync(ws, 0, WS_ALIGN, s) != cudaSuccess) return KDA_ERR_CUDA;
+    if (build_meta(cu, order.data(), n_seqs, 0, d_cu, reinterpret_cast<int64_t*>(ws + L.coff), d_order, nullptr, s) !=
+        cudaSuccess)
+        return KDA_ERR_CUDA;
+    const int io_bf16 = p->io_dtype == KDA_DTYPE_BF16;
+    ssm::PrefillArgs a{xbc, dt, z, xbc_stride, dt_stride, z_stride, p->conv_w, p->conv_b, p->A_log, p->dt_bias, p->D,
+                       S_in, S_out, ring_in, ring_out, o, d_cu, d_order, n_seqs, p->num_heads, p->num_groups, p->head_dim,
+                       p->state_dim};
+    if (ssm::launch_scan(a, io_bf16, s) != cudaSuccess) return KDA_ERR_CUDA;
+    if (ring_out && ssm::launch_ring(a, io_bf16, s) != cudaSuccess) return KDA_ERR_CUDA;
+    return KDA_OK;
+}
+
+size_t kda_ssm_decode_workspace_bytes(const kda_ssm_params* p, int32_t n_sessions) {
+    if (ssm::check_params(p) != KDA_OK || n_sessions <= 0) return 0;
+    return ssm::align_up((size_t)n_sessions * (size_t)channels(p) * sizeof(float));
+}
+
+kda_status kda_ssm_decode(const kda_ssm_params* p, int32_t n_sessions, const void* xbc, int64_t xbc_stride,
+                          const void* dt, int64_t dt_stride, const void* z, int64_t z_stride, const int32_t* slots,
+                          int32_t n_slots, float* S, void* ring, void* o, void* workspace, size_t workspace_bytes,
+                          void* stream_) {
+    kda_status st = ssm::check_params(p);
+    if (st != KDA_OK) return st;
+    if (n_sessions < 0 || n_slots < 0) return KDA_ERR_INVALID_ARG;
+    if (n_sessions == 0) return KDA_OK;
+    if (slots == nullptr ? n_slots < n_sessions : !aligned(slots, 4)) return KDA_ERR_INVALID_ARG;
+    if ((st = check_tokens(p, xbc, &xbc_stride, dt, &dt_stride, z, &z_stride, o)) != KDA_OK) return st;
+    if (!S || !ring || !aligned(S, 16) || !aligned(ring, 16)) return KDA_ERR_INVALID_ARG;
+    if ((int64_t)n_sessions * channels(p) > (int64_t)INT32_MAX) return KDA_ERR_UNSUPPORTED;
+    if (workspace == nullptr || !aligned(workspace, WS_ALIGN) ||
+        workspace_bytes < kda_ssm_decode_workspace_bytes(p, n_sessions))
+        return KDA_ERR_WORKSPACE;
+    ssm::DecodeArgs a{xbc, dt, z, xbc_stride, dt_stride, z_stride, p->conv_w, p->conv_b, p->A_log, p->dt_bias, p->D,
+                      slots, S, ring, o, static_cast<float*>(workspace), n_sessions, n_slots, p->num_heads, p->num_groups,
+                      p->head_dim, p->state_dim};
+    return ssm::launch_decode(a, p->io_dtype == KDA_DTYPE_BF16, static_cast<cudaStream_t>(stream_)) == cudaSuccess
+               ? KDA_OK : KDA_ERR_CUDA;
+}
+
+}  // extern "C"

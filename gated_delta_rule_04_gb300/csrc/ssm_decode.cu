@@ -1,0 +1,123 @@
+// One token per session of the state space mixer, state and ring updated in
+// place.
+//
+// Two kernels.  B and C of a group are shared by its heads, whose states are
+// spread over many CTAs, so the conv cannot run (and the in-place ring cannot
+// be rolled) where the state is: conv_kernel first takes every channel of
+// every session through the conv + SiLU into the workspace and rolls the ring;
+// state_kernel then runs one CTA per (session, head):
+//   S = a S + dt B x^T,  y = S^T C + D x,  o = y SiLU(z).
+// The state moves through HBM once in each direction and bounds the call: a
+// session's conv channels are 1 to 3 % of its state.
+#include "ssm_common.cuh"
+
+namespace kda {
+namespace ssm {
+namespace {
+
+constexpr int NT = 256;
+
+template <typename TI>
+__global__ void __launch_bounds__(NT) conv_kernel(DecodeArgs g) {
+    constexpr int V = 16 / sizeof(TI);   // channels per thread
+    const int Cx = g.H * g.P + 2 * g.G * g.N;
+    const int per = Cx / V;
+    const int64_t id = (int64_t)blockIdx.x * NT + threadIdx.x;
+    const int n = (int)(id / per), c = (int)(id % per) * V;
+    if (n >= g.n) return;
+    const int slot = g.slots ? g.slots[n] : n;
+    if (slot < 0 || slot >= g.n_slots) return;
+    TI* ring = static_cast<TI*>(g.ring) + (size_t)slot * RING * Cx + c;
+    union Row { uint4 u; TI v[V]; } r[4];
+#pragma unroll
+    for (int s = 0; s < RING; ++s) r[s].u = *reinterpret_cast<const uint4*>(ring + (size_t)s * Cx);
+    r[3].u = *reinterpret_cast<const uint4*>(static_cast<const TI*>(g.xbc) + (size_t)n * g.xbc_stride + c);
+    float y[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const float4 w = __ldg(reinterpret_cast<const float4*>(g.conv_w) + c + i);
+        const float b = g.conv_b ? __ldg(g.conv_b + c + i) : 0.f;
+        y[i] = silu(fmaf(w.w, to_f32(r[3].v[i]), fmaf(w.z, to_f32(r[2].v[i]), fmaf(w.y, to_f32(r[1].v[i]),
+                    fmaf(w.x, to_f32(r[0].v[i]), b)))));
+    }
+    float4* dst = reinterpret_cast<float4*>(g.u + (size_t)n * Cx + c);
+#pragma unroll
+    for (int i = 0; i < V / 4; ++i) dst[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+#pragma unroll
+    for (int s = 0; s < RING; ++s) *reinterpret_cast<uint4*>(ring + (size_t)s * Cx) = r[s + 1].u;
+}
+
+// Thread (rg, cq): state rows rg, rg + RG, ..., columns 4 cq .. 4 cq + 3.
+template <typename TI, int P, int N>
+__global__ void __launch_bounds__(NT) state_kernel(DecodeArgs g) {
+    constexpr int CQ = P / 4, RG = NT / CQ, RN = N / RG;
+    __shared__ float4 part[NT / 32][CQ];
+    const int H = g.H, W = H * P, Cx = W + 2 * g.G * N;
+    const int n = blockIdx.x / H, h = blockIdx.x % H;
+    const int tid = threadIdx.x, cq = tid % CQ, rg = tid / CQ;
+    const int slot = g.slots ? g.slots[n] : n;
+    if (slot < 0 || slot >= g.n_slots) return;
+    float4* Sg = reinterpret_cast<float4*>(g.S + ((size_t)slot * H + h) * N * P) + tid;
+    float4 S[RN];
+#pragma unroll
+    for (int i = 0; i < RN; ++i) S[i] = __ldcs(Sg + i * NT);
+    const float* u = g.u + (size_t)n * Cx;
+    const int grp = h / (H / g.G);
+    const float dt = softplus(to_f32(static_cast<const TI*>(g.dt)[(size_t)n * g.dt_stride + h]) + g.dt_bias[h]);
+    const float a = expf(-expf(g.A_log[h]) * dt);
+    const float4 x4 = *reinterpret_cast<const float4*>(u + h * P + 4 * cq);
+    const float4 xd = make_float4(dt * x4.x, dt * x4.y, dt * x4.z, dt * x4.w);
+    const float* B = u + W + grp * N;
+    const float* C = B + g.G * N;
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < RN; ++i) {
+        const float b = B[rg + i * RG], c = C[rg + i * RG];
+        S[i].x = fmaf(a, S[i].x, b * xd.x); S[i].y = fmaf(a, S[i].y, b * xd.y);
+        S[i].z = fmaf(a, S[i].z, b * xd.z); S[i].w = fmaf(a, S[i].w, b * xd.w);
+        __stcs(Sg + i * NT, S[i]);
+        y.x = fmaf(c, S[i].x, y.x); y.y = fmaf(c, S[i].y, y.y);
+        y.z = fmaf(c, S[i].z, y.z); y.w = fmaf(c, S[i].w, y.w);
+    }
+    if (CQ == 16) {   // two row groups share a warp
+        y.x += __shfl_xor_sync(0xffffffffu, y.x, 16); y.y += __shfl_xor_sync(0xffffffffu, y.y, 16);
+        y.z += __shfl_xor_sync(0xffffffffu, y.z, 16); y.w += __shfl_xor_sync(0xffffffffu, y.w, 16);
+    }
+    if ((tid & 31) < CQ) part[tid >> 5][cq] = y;
+    __syncthreads();
+    if (tid < P) {
+        const float* pf = reinterpret_cast<const float*>(part);
+        float s = 0.f;
+#pragma unroll
+        for (int k = 0; k < NT / 32; ++k) s += pf[k * P + tid];
+        if (g.skip) s = fmaf(g.skip[h], u[h * P + tid], s);
+        if (g.z) s *= silu(to_f32(static_cast<const TI*>(g.z)[(size_t)n * g.z_stride + h * P + tid]));
+        static_cast<TI*>(g.o)[(size_t)n * W + h * P + tid] = from_f32<TI>(s);
+    }
+}
+
+template <typename TI>
+cudaError_t decode(const DecodeArgs& a, cudaStream_t s) {
+    const int64_t per = (int64_t)(a.H * a.P + 2 * a.G * a.N) / (16 / sizeof(TI));
+    conv_kernel<TI><<<(unsigned)((a.n * per + NT - 1) / NT), NT, 0, s>>>(a);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    const unsigned grid = (unsigned)((int64_t)a.n * a.H);
+    if (a.P == 64) {
+        if (a.N == 64) state_kernel<TI, 64, 64><<<grid, NT, 0, s>>>(a);
+        else state_kernel<TI, 64, 128><<<grid, NT, 0, s>>>(a);
+    } else {
+        if (a.N == 64) state_kernel<TI, 128, 64><<<grid, NT, 0, s>>>(a);
+        else state_kernel<TI, 128, 128><<<grid, NT, 0, s>>>(a);
+    }
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_decode(const DecodeArgs& a, int io_bf16, cudaStream_t s) {
+    return io_bf16 ? decode<__nv_bfloat16>(a, s) : decode<float>(a, s);
+}
+
+}  // namespace ssm
+}  // namespace kda

@@ -273,6 +273,147 @@ kda_status kda_decode_multi(const kda_params* p, int32_t n_sessions, int32_t n_t
                             void* o, void* stream);
 
 /*
+ * A tree of drafted tokens against each session's state.
+ *
+ * A speculative round may draft a tree instead of a straight run of tokens.
+ * kda_decode_tree gives the output row of every node: what the mixer would
+ * return for that node's token if the tokens on the path from the session's
+ * last token down to the node, and only those, had been decoded before it.
+ * State and ring are read and never written, so any path can be accepted
+ * afterwards: kda_tree_commit then advances the state and ring by the tokens
+ * of each session's accepted path.  An interface addition of this library: the
+ * sources verify straight runs ("memra-engine 0.124.0, module kda",
+ * kda_verify_rows_cached and kda_verify_rollback_rows).
+ *
+ *   q,k,v,z,gout : device [n_sessions][n_nodes][H*128] io_dtype, raw
+ *                  projections of the nodes' tokens, 1 <= n_nodes <= KDA_TREE_MAX_NODES
+ *   b            : device [n_sessions][n_nodes][H] io_dtype
+ *   parents      : device int32 [n_sessions][n_nodes].  parents[r] is the node
+ *                  that node r follows, -1 for a node that follows the session's
+ *                  last token.  Parents come before their children.  A node
+ *                  whose entry is below -1 or not below r, and every node under
+ *                  it, is unused: its output row is left untouched (the padding
+ *                  of a smaller tree).
+ *   slots, n_slots : as for kda_decode_multi; here slots need not be distinct
+ *   S, ring      : device state and ring pools as for kda_decode_multi, read only
+ *   o            : device [n_sessions][n_nodes][H*128] io_dtype
+ *
+ * The conv of a node reads the raw rows of its parent, grandparent and
+ * great-grandparent, and the session's ring before the root.  For a tree that
+ * is one chain the rows equal those of kda_decode_multi up to rounding.
+ */
+#define KDA_TREE_MAX_NODES 64
+kda_status kda_decode_tree(const kda_params* p, int32_t n_sessions, int32_t n_nodes,
+                           const void* q, const void* k, const void* v, const void* z,
+                           const void* b, const void* gout, const int32_t* parents,
+                           const int32_t* slots, int32_t n_slots, const float* S, const void* ring,
+                           void* o, void* stream);
+
+/*
+ * Advances each session's state and ring by the tokens of its accepted path
+ * through the nodes of a kda_decode_tree round (any rows of the round, in
+ * order: a straight round with a per-session length is path 0, 1, 2, ...).
+ *   q,k,v,z,b    : the nodes' raw projections, as for kda_decode_tree (of q only
+ *                  the ring's rows are read)
+ *   path         : device int32 [n_sessions][max_len], the accepted nodes, first
+ *                  token first; 1 <= max_len <= KDA_TREE_MAX_NODES
+ *   path_len     : device int32 [n_sessions], tokens accepted, 0 <= path_len <= max_len
+ *                  (0 copies state and ring from the input to the output pool)
+ *   slots, S_in, S_out, ring_in, ring_out : as for kda_decode_multi (distinct
+ *                  slots; the pools may alias).  A session with a slot outside
+ *                  [0, n_slots), a path_len outside [0, max_len] or an accepted
+ *                  node outside [0, n_nodes) is skipped: its state and ring are
+ *                  left untouched.
+ */
+kda_status kda_tree_commit(const kda_params* p, int32_t n_sessions, int32_t n_nodes,
+                           const void* q, const void* k, const void* v, const void* z, const void* b,
+                           const int32_t* path, const int32_t* path_len, int32_t max_len,
+                           const int32_t* slots, int32_t n_slots, const float* S_in, float* S_out,
+                           const void* ring_in, void* ring_out, void* stream);
+
+/*
+ * Selective state space mixer: the recurrent mixer with one scalar decay per
+ * head and token and no delta rule, beside which hybrid stacks place KDA.  Per
+ * sequence, head h (of group h / (H/G)) and token t, with the conv channels
+ * x (H*P) | B (G*N) | C (G*N) of one projection row xbc:
+ *   1. u[c] = SiLU(conv_b[c] + sum_{j<4} conv_w[c][j] xbc[t-3+j][c]); inputs
+ *      before the sequence start come from the conv ring (slot 0 oldest)
+ *   2. dt = softplus(dt_raw[t][h] + dt_bias[h]),  a = exp(-exp(A_log[h]) dt)
+ *   3. S = a S + dt B x^T  (S is N x P fp32 per (sequence, head), rows = state
+ *      index, B of the head's group, x of the head)
+ *   4. y = S^T C + D[h] x
+ *   5. o = y * SiLU(z)     (z NULL: o = y)
+ * An interface addition of this library; the conventions above hold.
+ */
+typedef struct {
+    int32_t num_heads;   /* H >= 1 */
+    int32_t head_dim;    /* P: 64 or 128 */
+    int32_t state_dim;   /* N: 64 or 128 */
+    int32_t num_groups;  /* G >= 1, divides H */
+    int32_t conv_kernel; /* must be 4 */
+    int32_t io_dtype;    /* kda_dtype of xbc, dt, z, o and the ring */
+    int32_t algo;        /* kda_algo, prefill only: AUTO, SCAN or CHUNKED (bf16 I/O) */
+    const float* conv_w;  /* device [H*P + 2*G*N][4] fp32; tap 3 = current token */
+    const float* conv_b;  /* device [H*P + 2*G*N] fp32 or NULL (no bias) */
+    const float* A_log;   /* device [H] fp32 */
+    const float* dt_bias; /* device [H] fp32 */
+    const float* D;       /* device [H] fp32 or NULL (no skip) */
+} kda_ssm_params;
+
+/* The prefill algorithm (KDA_ALGO_SCAN or KDA_ALGO_CHUNKED) that
+ * kda_ssm_prefill runs for these parameters, or -1 when it would reject them. */
+int32_t kda_ssm_prefill_algo(const kda_ssm_params* p);
+
+/* Bytes of device workspace kda_ssm_prefill needs (0 when it needs none or
+ * would reject the arguments).  For the chunked algorithm the size covers any
+ * split of total_tokens into n_seqs sequences. */
+size_t kda_ssm_prefill_workspace_bytes(const kda_ssm_params* p, int32_t n_seqs, int64_t total_tokens);
+
+/*
+ * Stateful varlen prefill of the state space mixer over n_seqs packed sequences.
+ *   xbc, xbc_stride : device io_dtype, row t at xbc + t * xbc_stride elements,
+ *                  H*P + 2*G*N channels used.  Strides are in elements and let
+ *                  the three inputs be column ranges of one projection row; 0
+ *                  selects packed rows.  xbc and z rows must start on 16 bytes
+ *                  (stride * element size a multiple of 16).
+ *   dt, dt_stride  : device io_dtype [T][H], element alignment
+ *   z, z_stride    : device io_dtype [T][H*P] gate logits, or NULL
+ *   cu_seqlens_host, n_seqs, total_tokens : as for kda_prefill
+ *   S_in, S_out    : device [n_seqs][H][N][P] fp32; S_in NULL is zero; they may be
+ *                  the same buffer
+ *   ring_in, ring_out : device [n_seqs][3][H*P + 2*G*N] io_dtype; ring_in NULL is
+ *                  zero, ring_out NULL is skipped; they may be the same buffer
+ *   o              : device [T][H*P] io_dtype, packed
+ *   workspace      : device, >= kda_ssm_prefill_workspace_bytes(), 256-byte aligned;
+ *                  its error word is read with kda_workspace_status
+ * Zero-length sequences copy their state and ring through unchanged.
+ */
+kda_status kda_ssm_prefill(const kda_ssm_params* p, const void* xbc, int64_t xbc_stride,
+                           const void* dt, int64_t dt_stride, const void* z, int64_t z_stride,
+                           const int64_t* cu_seqlens_host, int32_t n_seqs, int64_t total_tokens,
+                           const float* S_in, float* S_out, const void* ring_in, void* ring_out,
+                           void* o, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of device workspace kda_ssm_decode needs (0 for rejected arguments). */
+size_t kda_ssm_decode_workspace_bytes(const kda_ssm_params* p, int32_t n_sessions);
+
+/*
+ * One token per session, state and ring updated in place in their pools.
+ *   xbc, dt, z   : as for kda_ssm_prefill with one row per session
+ *   slots        : device int32 [n_sessions] distinct pool slots, or NULL (session
+ *                  i uses slot i).  A slot outside [0, n_slots) skips its session:
+ *                  its state, ring and output row are left untouched.
+ *   S, ring      : device pools [n_slots][H][N][P] fp32 and
+ *                  [n_slots][3][H*P + 2*G*N] io_dtype
+ *   o            : device [n_sessions][H*P] io_dtype
+ *   workspace    : device, >= kda_ssm_decode_workspace_bytes(), 256-byte aligned
+ */
+kda_status kda_ssm_decode(const kda_ssm_params* p, int32_t n_sessions, const void* xbc, int64_t xbc_stride,
+                          const void* dt, int64_t dt_stride, const void* z, int64_t z_stride,
+                          const int32_t* slots, int32_t n_slots, float* S, void* ring, void* o,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * kda_prefill without a workspace, for callers that cannot allocate device
  * memory when they run: a plugin inside an engine that owns every byte of
  * device memory, or a serving loop that must not call cudaMalloc/cudaFree
