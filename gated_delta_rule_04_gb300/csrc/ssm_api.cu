@@ -8,7 +8,7 @@
 #include <numeric>
 #include <vector>
 
-#include "ssm_common.cuh"
+#include "ssm_chunk.cuh"
 
 namespace kda {
 namespace ssm {
@@ -43,8 +43,9 @@ kda_status check_params(const kda_ssm_params* p) {
 
 // KDA_ALGO_SCAN or KDA_ALGO_CHUNKED, for checked parameters.
 kda_status resolve_algo(const kda_ssm_params* p, int* algo) {
-    if (p->algo == KDA_ALGO_CHUNKED) return KDA_ERR_UNSUPPORTED;
-    *algo = KDA_ALGO_SCAN;
+    const bool bf16 = p->io_dtype == KDA_DTYPE_BF16;
+    if (p->algo == KDA_ALGO_CHUNKED && !bf16) return KDA_ERR_UNSUPPORTED;
+    *algo = p->algo == KDA_ALGO_AUTO ? (bf16 ? KDA_ALGO_CHUNKED : KDA_ALGO_SCAN) : p->algo;
     return KDA_OK;
 }
 
@@ -69,18 +70,78 @@ kda_status check_tokens(const kda_ssm_params* p, const void* xbc, int64_t* xbc_s
     return KDA_OK;
 }
 
-// Workspace of a prefill: error word | cu_seqlens | first chunks | order.
+constexpr int SMS_GB300 = 152;
+
+// Units of 128 channels: two heads of 64 or one of 128, within a group.
+int units_per_group(const kda_ssm_params* p) {
+    return (int)(((int64_t)(p->num_heads / p->num_groups) * p->head_dim + 127) / 128);
+}
+
+// The most (sequence, piece) slots a call may cut its sequences into: enough
+// for two CTAs per SM, and none when the sequences alone fill the SMs.
+int64_t piece_slots(const kda_ssm_params* p, int64_t n_seqs) {
+    const int64_t units = (int64_t)units_per_group(p) * p->num_groups;
+    return n_seqs * units >= SMS_GB300 ? 0 : 2 * SMS_GB300 / units;
+}
+
+// Workspace of a prefill: error word | cu_seqlens | first chunks | order, and
+// for the chunked form chunk table | step records | scales | group records |
+// piece end states and decays.
 struct Layout {
-    size_t cu = 0, coff = 0, order = 0, total = 0;
+    size_t cu = 0, coff = 0, order = 0, chunks = 0, step = 0, scale = 0, rec = 0, local = 0, ltot = 0, total = 0;
 };
-Layout layout(int32_t n_seqs) {
+Layout layout(const kda_ssm_params* p, int algo, int64_t n_seqs, int64_t total_tokens) {
     Layout L;
     size_t off = WS_ALIGN;
-    L.cu = off; off = align_up(off + sizeof(int64_t) * ((size_t)n_seqs + 1));
-    L.coff = off; off = align_up(off + sizeof(int64_t) * ((size_t)n_seqs + 1));
-    L.order = off; off = align_up(off + sizeof(int32_t) * (size_t)n_seqs);
+    auto take = [&](size_t bytes) { const size_t at = off; off = align_up(off + bytes); return at; };
+    L.cu = take(sizeof(int64_t) * ((size_t)n_seqs + 1));
+    L.coff = take(sizeof(int64_t) * ((size_t)n_seqs + 1));
+    L.order = take(sizeof(int32_t) * (size_t)n_seqs);
+    if (algo == KDA_ALGO_CHUNKED) {
+        // every sequence may end in a partial chunk
+        const size_t nck = (size_t)(total_tokens / CHUNK_T + std::min(n_seqs, total_tokens));
+        const size_t slots = (size_t)piece_slots(p, n_seqs), H = p->num_heads, G = p->num_groups;
+        L.chunks = take(sizeof(ChunkDesc) * nck);
+        L.step = take(sizeof(float) * STEP_FLOATS * nck * H);
+        L.scale = take(sizeof(int4) * nck * G);
+        L.rec = take(rec_bytes(p->state_dim) * nck * G);
+        L.local = take(sizeof(float) * slots * H * p->state_dim * p->head_dim);
+        L.ltot = take(sizeof(float) * slots * H);
+    }
     L.total = off;
     return L;
+}
+
+// Pieces of lp chunks, np per sequence at most.  A cut costs the lite pass over
+// all pieces but the last (about LITE of a full chunk each); it pays when the
+// sequences' units leave SMs idle.  Times in chunks of one CTA per SM.
+struct Pieces {
+    int np = 1, lp = 1;
+};
+Pieces plan_pieces(const kda_ssm_params* p, const int64_t* cu, int32_t n_seqs) {
+    const int64_t units = (int64_t)units_per_group(p) * p->num_groups, slots = piece_slots(p, n_seqs);
+    int64_t longest = 1, total = 0;
+    for (int32_t i = 0; i < n_seqs; ++i) {
+        const int64_t c = (cu[i + 1] - cu[i] + CHUNK_T - 1) / CHUNK_T;
+        longest = std::max(longest, c);
+        total += c;
+    }
+    constexpr double LITE = 0.6;
+    constexpr int64_t MIN_CHUNKS = 4;
+    Pieces best{1, (int)longest};
+    double best_t = (double)std::max(longest, total * units / SMS_GB300);
+    for (int64_t k = 2; k * n_seqs <= slots && longest >= k * MIN_CHUNKS; ++k) {
+        const int64_t lp = (longest + k - 1) / k;
+        int64_t pieces = 0;
+        for (int32_t i = 0; i < n_seqs; ++i) pieces += std::max<int64_t>(1, ((cu[i + 1] - cu[i] + CHUNK_T - 1) / CHUNK_T + lp - 1) / lp);
+        const int64_t waves = (pieces * units + SMS_GB300 - 1) / SMS_GB300;
+        const double t = (1.0 + LITE) * (double)(waves * lp);
+        if (t < best_t) {
+            best_t = t;
+            best = Pieces{(int)k, (int)lp};
+        }
+    }
+    return best;
 }
 
 }  // namespace
@@ -103,7 +164,7 @@ size_t kda_ssm_prefill_workspace_bytes(const kda_ssm_params* p, int32_t n_seqs, 
     if (ssm::check_params(p) != KDA_OK || ssm::resolve_algo(p, &algo) != KDA_OK || n_seqs < 0 || total_tokens < 0)
         return 0;
     if (n_seqs == 0) return 0;
-    return ssm::layout(n_seqs).total;
+    return ssm::layout(p, algo, n_seqs, total_tokens).total;
 }
 
 kda_status kda_ssm_prefill(const kda_ssm_params* p, const void* xbc, int64_t xbc_stride, const void* dt,
@@ -129,7 +190,7 @@ kda_status kda_ssm_prefill(const kda_ssm_params* p, const void* xbc, int64_t xbc
 
     cudaStream_t s = static_cast<cudaStream_t>(stream_);
     unsigned char* ws = static_cast<unsigned char*>(workspace);
-    const Layout L = ssm::layout(n_seqs);
+    const Layout L = ssm::layout(p, algo, n_seqs, total_tokens);
     // longest sequences first: their walks take longest
     std::vector<int32_t> order;
     try {
@@ -143,14 +204,43 @@ kda_status kda_ssm_prefill(const kda_ssm_params* p, const void* xbc, int64_t xbc
     int64_t* d_cu = reinterpret_cast<int64_t*>(ws + L.cu);
     int32_t* d_order = reinterpret_cast<int32_t*>(ws + L.order);
     if (cudaMemsetAsync(ws, 0, WS_ALIGN, s) != cudaSuccess) return KDA_ERR_CUDA;
-    if (build_meta(cu, order.data(), n_seqs, 0, d_cu, reinterpret_cast<int64_t*>(ws + L.coff), d_order, nullptr, s) !=
-        cudaSuccess)
-        return KDA_ERR_CUDA;
+    const bool chunked = algo == KDA_ALGO_CHUNKED;
+    int64_t* d_coff = reinterpret_cast<int64_t*>(ws + L.coff);
+    ChunkDesc* d_chunks = chunked ? reinterpret_cast<ChunkDesc*>(ws + L.chunks) : nullptr;
+    if (build_meta(cu, order.data(), n_seqs, 0, d_cu, d_coff, d_order, d_chunks, s) != cudaSuccess) return KDA_ERR_CUDA;
     const int io_bf16 = p->io_dtype == KDA_DTYPE_BF16;
     ssm::PrefillArgs a{xbc, dt, z, xbc_stride, dt_stride, z_stride, p->conv_w, p->conv_b, p->A_log, p->dt_bias, p->D,
                        S_in, S_out, ring_in, ring_out, o, d_cu, d_order, n_seqs, p->num_heads, p->num_groups, p->head_dim,
                        p->state_dim};
-    if (ssm::launch_scan(a, io_bf16, s) != cudaSuccess) return KDA_ERR_CUDA;
+    if (chunked) {
+        ChunkArgs c{};
+        c.g = a;
+        const int64_t Cx = channels(p);
+        if (total_tokens > 0 && (!encode_rows_bf16(&c.map67, xbc, total_tokens, Cx, xbc_stride, CHUNK_T + RING) ||
+                                 !encode_rows_bf16(&c.map64, xbc, total_tokens, Cx, xbc_stride, CHUNK_T)))
+            return KDA_ERR_CUDA;
+        int64_t n_chunks = 0;
+        for (int32_t i = 0; i < n_seqs; ++i) n_chunks += (cu[i + 1] - cu[i] + CHUNK_T - 1) / CHUNK_T;
+        const Pieces pc = plan_pieces(p, cu, n_seqs);
+        c.chunks = d_chunks;
+        c.coff = d_coff;
+        c.rec = ws + L.rec;
+        c.step = reinterpret_cast<float*>(ws + L.step);
+        c.scale = reinterpret_cast<int4*>(ws + L.scale);
+        c.status = reinterpret_cast<int32_t*>(ws);
+        c.local = reinterpret_cast<float*>(ws + L.local);
+        c.ltot = reinterpret_cast<float*>(ws + L.ltot);
+        c.np = pc.np;
+        c.lp = pc.lp;
+        c.n_chunks = (int32_t)n_chunks;
+        c.upg = units_per_group(p);
+        c.units = c.upg * p->num_groups;
+        if (ssm::launch_chunk_prep(c, s) != cudaSuccess) return KDA_ERR_CUDA;
+        if (pc.np > 1 && launch_chunks(c, true, s) != cudaSuccess) return KDA_ERR_CUDA;
+        if (launch_chunks(c, false, s) != cudaSuccess) return KDA_ERR_CUDA;
+    } else if (ssm::launch_scan(a, io_bf16, s) != cudaSuccess) {
+        return KDA_ERR_CUDA;
+    }
     if (ring_out && ssm::launch_ring(a, io_bf16, s) != cudaSuccess) return KDA_ERR_CUDA;
     return KDA_OK;
 }

@@ -1,0 +1,597 @@
+// Chunked prefill of the state space mixer on the 5th-generation tensor cores
+// (tcgen05, accumulators in tensor memory), conv, scan, skip and gate in one
+// pass over x, z and o.
+//
+// One CTA walks the 64-token chunks of one unit: 128 channels of x, i.e. two
+// heads of 64 or one of 128, of one group.  With lam the chunk's cumulative
+// log2 decay of a head (lam <= 0, falling), S the state at the chunk start
+// (transposed: lane = channel, column = state index), per chunk
+//   Y^T   = X^T M^T + (S^T C^T) 2^lam_t         M_ts = G_ts 2^(lam_t - lam_s) dt_s
+//                                               (s <= t; + D on the diagonal)
+//   S^T   = 2^lam_63 S^T + (X 2^(lam_63 - lam_s) dt_s)^T B
+// Unlike the delta rule nothing here solves for the update, so the chain from
+// chunk to chunk is one decay and one accumulating MMA.  Everything has M = 128
+// (the unit's channels), and the channel-side operands are MMA operands in
+// tensor memory: a thread convolves its channel's tokens in registers and
+// stores the packed row, with no shared-memory tile for x.
+//   inter  DI = S^T C^T          A = S^T (fp16, TMEM), B = C      N = 64
+//   intra  D_h = X^T M_h^T       A = X (fp16, TMEM),  B = M_h     N = 64, per head (the
+//                                rows of the other head are computed and not used: an
+//                                M = 64 MMA takes as long)
+//   state  S^T += X~^T B         A = X~ hi/lo (fp16, TMEM), B = B^T hi/lo, N = state width;
+//                                hi*hi + hi*lo + lo*hi, since S is an fp32 result
+// Operands are fp16 with exact power-of-two scales, so that they keep 11 bits
+// (22 in pairs) whatever the size of the inputs: B and C by chunk (from the
+// preparation), X by channel and chunk, dt by head and chunk, S by channel from
+// a running upper bound of its row.  The scales leave again where a thread
+// holds its own channel: in the decay of S and in the readout of Y.
+//
+// Warp roles.  Warps 0-7 (X group; warp % 4 = lane quarter, warp / 4 = token
+// half): conv, operands, S.  Warps 8-15 (Y group): M of the next chunk, then
+// the readout of this one: Y through a shared-memory tile to rows, gate,
+// store.  Warp 16 issues the MMAs.  All hand-offs are mbarriers; x, the step
+// records and the group records arrive by TMA and bulk copies, x two chunks
+// ahead.  Every wait is bounded: on timeout the kernel reports it in the
+// workspace's error word, lets its copies and MMAs land, frees its tensor
+// memory and returns.
+//
+// Few units leave SMs idle, so long sequences are cut into pieces of lp chunks
+// that run side by side: a lite pass (no S copy, no Y) first gives each piece's
+// end state from its own start, and a piece's true start is composed from the
+// pieces before it when it begins.
+#include "ssm_chunk.cuh"
+#include "tc_ptx.cuh"
+
+namespace kda {
+namespace ssm {
+namespace {
+
+constexpr int NT = 640;                    // 8 X warps, 8 Y warps, a warpgroup whose first thread issues the MMAs
+// register split: 96 a thread at launch (65536 / 640), moved between the warpgroups
+constexpr int REG_LAUNCH = 96, REG_X = 120, REG_Y = 104, REG_ISSUE = 24;
+static_assert(256 * REG_X + 256 * REG_Y + 128 * REG_ISSUE <= NT * REG_LAUNCH && REG_X % 8 == 0 && REG_Y % 8 == 0,
+              "the split must fit the launch's registers, or setmaxnreg.inc waits forever");
+constexpr int NX = 256, NY = 256;
+constexpr int BAR_X = 1, BAR_Y = 2;        // named barriers
+constexpr uint32_t TM_S = 0, TM_SH = 128, TM_XF = 192, TM_XH = 224, TM_XL = 256, TM_DI = 288, TM_D = 352;
+constexpr uint32_t TMEM_COLS = 512;
+constexpr uint64_t WAIT_LIMIT_NS = 2000000000ull;
+constexpr int LDYS = 132;
+constexpr uint32_t ROW = 256;              // bytes of a unit's 128 channels
+constexpr uint32_t X_SLOT = 17408;         // 67 rows, rounded up to 1 KiB
+constexpr uint32_t STEP_BYTES = STEP_FLOATS * 4;
+constexpr uint32_t STEP_SLOT = 2 * STEP_BYTES + 16;   // two heads' step records, the group's scales
+
+// A slot is refilled for chunk c + 2 while the X group is at chunk c; the Y group
+// may then still read the decays of chunk c - 2, and has left chunk c - 3.
+constexpr int NSTEP = 5;
+
+template <int P, int N>
+struct Map {                               // shared memory, from a 1 KiB aligned base
+    static constexpr int U = 128 / P;      // heads per unit
+    static constexpr uint32_t REC = 0;                                // 2 group records
+    static constexpr uint32_t M = REC + 2 * Rec<N>::BYTES;            // fp16 [2 buffers][U][64 t][64 s]
+    static constexpr uint32_t X = M + 2 * U * 8192;                   // 2 raw x tiles [67][128] bf16
+    static constexpr uint32_t Y = X + 2 * X_SLOT;                     // fp32 [64 t][LDYS]
+    static constexpr uint32_t STEP = Y + 64 * LDYS * 4;               // NSTEP step slots
+    static constexpr uint32_t SX = STEP + NSTEP * STEP_SLOT;          // fp32 [3][128] scale of D_h by channel
+    static constexpr uint32_t SI = SX + 3 * 512;                      // fp32 [3][128] scale of DI
+    static constexpr uint32_t XM = SI + 3 * 512;                      // fp32 [2][128] row maxima by token half
+    static constexpr uint32_t BAR = XM + 1024;
+    static constexpr uint32_t BYTES = BAR + 256 + 1024;
+    static_assert(REC % 1024 == 0 && M % 1024 == 0 && X % 128 == 0 && STEP % 16 == 0 && STEP_SLOT % 16 == 0 && BAR % 8 == 0, "");
+    static_assert(BYTES <= 232448, "shared memory of one CTA");
+};
+
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// Waits for a phase; false after the limit or once another thread gave up.
+__device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+    if (ptx::mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = ptx::globaltimer_ns();
+    while (!ptx::mbar_try_wait(bar, parity)) {
+        if (*abort_flag) return false;
+        if (ptx::globaltimer_ns() - t0 > WAIT_LIMIT_NS) {
+            *abort_flag = 1;
+            return false;
+        }
+    }
+    return true;
+}
+
+// The exponent by which M is scaled down: |G'| <= 512 N / 128, dt < 2^(edt + 1),
+// and D on the diagonal.
+__device__ __forceinline__ int m_exponent(int edt, int eb, int ec, float skip) {
+    const int e = edt + eb + ec, es = expo(fabsf(skip)) - 8;
+    return e > es ? e : es;
+}
+
+template <int P, int N, bool LITE>
+__global__ void __launch_bounds__(NT, 1) chunk_kernel(const __grid_constant__ ChunkArgs a) {
+    using L = Map<P, N>;
+    constexpr int U = L::U;
+    extern __shared__ unsigned char smem_raw[];
+    const PrefillArgs& g = a.g;
+    // ---- this CTA's unit, sequence and piece
+    const int unit = blockIdx.x % a.units, piece = (blockIdx.x / a.units) % a.np;
+    const int seq = g.order[blockIdx.x / a.units / a.np];
+    const int64_t bos = g.cu[seq], len_seq = g.cu[seq + 1] - bos;
+    const int64_t nc_seq = a.coff[seq + 1] - a.coff[seq];
+    const int64_t first = (int64_t)piece * a.lp;                       // first chunk in the sequence
+    const bool last_piece = first + a.lp >= nc_seq;
+    if (first > 0 && first >= nc_seq) return;
+    if (LITE && last_piece) return;
+    const int nc = (int)(nc_seq - first < a.lp ? nc_seq - first : a.lp);
+    const int64_t chunk0 = a.coff[seq] + first;                        // in the chunk table
+    const int HG = g.H / g.G, grp = unit / a.upg, h0 = grp * HG + (unit % a.upg) * U;
+    const int nh = min(U, (grp + 1) * HG - h0);                        // heads of this unit
+    const int c0 = h0 * P, W = g.H * P, Cx = W + 2 * g.G * N;
+
+    const uint32_t raw = ptx::smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
+    unsigned char* sb = smem_raw + (base - raw);
+    const uint32_t bars = base + L::BAR;
+    const uint32_t b_x = bars, b_step = bars + 16, b_rec = bars + 56, b_m = bars + 72;   // [2], [NSTEP], [2], [2]
+    const uint32_t b_xready = bars + 88, b_done = bars + 96, b_dfree = bars + 104, b_drain = bars + 112;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sb + L::BAR + 128);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(sb + L::BAR + 132);
+    volatile int* issued = reinterpret_cast<volatile int*>(sb + L::BAR + 136);   // loads issued: [0] x and steps, [1] records
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    if (warp == 16) {
+        ptx::tmem_alloc(ptx::smem_u32(tmem_slot), TMEM_COLS);
+        ptx::tmem_relinquish();
+    }
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(b_x + 8 * i, 1);
+            ptx::mbar_init(b_rec + 8 * i, 1);
+            ptx::mbar_init(b_m + 8 * i, 1);
+        }
+        for (int i = 0; i < NSTEP; ++i) ptx::mbar_init(b_step + 8 * i, 1);
+        ptx::mbar_init(b_xready, 1);
+        ptx::mbar_init(b_done, 1);
+        ptx::mbar_init(b_dfree, NY / 32);
+        ptx::mbar_init(b_drain, 1);
+        *abort_flag = 0;
+        issued[0] = issued[1] = 0;
+        ptx::fence_mbar_init();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const int quarter = warp & 3, half = (warp >> 2) & 1;
+    const uint32_t tlane = tmem + ((uint32_t)(32 * quarter) << 16);
+
+    // x tile, step records and scales of chunk c
+    auto load_x = [&](int c) {
+        const uint32_t bx = b_x + 8 * (c & 1), bs = b_step + 8 * (c % NSTEP);
+        const int64_t t0 = bos + (first + c) * CHUNK_T;
+        const uint32_t dst = base + L::X + (c & 1) * X_SLOT;
+        if (first + c > 0) {
+            ptx::mbar_expect_tx(bx, (CHUNK_T + RING) * ROW);
+            ptx::tma_load_2d(dst, &a.map67, c0, (int)(t0 - RING), bx);
+        } else {                               // the sequence's first rows: no rows before them
+            ptx::mbar_expect_tx(bx, CHUNK_T * ROW);
+            ptx::tma_load_2d(dst + RING * ROW, &a.map64, c0, (int)t0, bx);
+        }
+        const uint32_t sdst = base + L::STEP + (c % NSTEP) * STEP_SLOT;
+        ptx::mbar_expect_tx(bs, nh * STEP_BYTES + 16);
+        ptx::bulk_g2s(sdst, a.step + ((size_t)(chunk0 + c) * g.H + h0) * STEP_FLOATS, nh * STEP_BYTES, bs);
+        ptx::bulk_g2s(sdst + 2 * STEP_BYTES, a.scale + (size_t)(chunk0 + c) * g.G + grp, 16, bs);
+        issued[0] = c + 1;
+    };
+    auto load_rec = [&](int c) {
+        const uint32_t bar = b_rec + 8 * (c & 1);
+        const uint32_t bytes = LITE ? Rec<N>::OFF_C : Rec<N>::BYTES;
+        const unsigned char* src = a.rec + ((size_t)(chunk0 + c) * g.G + grp) * Rec<N>::BYTES;
+        ptx::mbar_expect_tx(bar, bytes);
+        ptx::bulk_g2s(base + L::REC + (c & 1) * Rec<N>::BYTES, src, bytes / 2, bar);
+        ptx::bulk_g2s(base + L::REC + (c & 1) * Rec<N>::BYTES + bytes / 2, src + bytes / 2, bytes / 2, bar);
+        issued[1] = c + 1;
+    };
+    auto step_of = [&](int c, int hh) { return reinterpret_cast<const float*>(sb + L::STEP + (c % NSTEP) * STEP_SLOT + hh * STEP_BYTES); };
+    auto scale_of = [&](int c) { return *reinterpret_cast<const int2*>(sb + L::STEP + (c % NSTEP) * STEP_SLOT + 2 * STEP_BYTES); };
+
+    if (warp < 8) {
+        // ================================ X group ================================
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REG_X));
+        if (tid == 0)
+            for (int c = 0; c < nc && c < 2; ++c) load_x(c);
+        if (tid == 32)
+            for (int c = 0; c < nc && c < 2; ++c) load_rec(c);
+        const int ch = 32 * quarter + lane;                  // channel of the unit = TMEM lane
+        const int hh = min(ch / P, nh - 1), h = h0 + hh;     // its head (a channel past the group: computed, never stored)
+        const bool valid = ch < nh * P;
+        const int p = ch % P;
+        const float4 w = __ldg(reinterpret_cast<const float4*>(g.conv_w) + c0 + ch);
+        const float bias = g.conv_b ? g.conv_b[c0 + ch] : 0.f;
+        const float skip = g.skip ? g.skip[h] : 0.f;
+        float* xm = reinterpret_cast<float*>(sb + L::XM);
+        float* sSX = reinterpret_cast<float*>(sb + L::SX);
+        float* sSI = reinterpret_cast<float*>(sb + L::SI);
+        const size_t state = (size_t)N * P;
+
+        // ---- starting state: the caller's for the first piece; later ones compose the
+        // end states of the pieces before them (zero in the lite pass)
+        const float* start = piece == 0 && g.S_in ? g.S_in + ((size_t)seq * g.H + h) * state + p : nullptr;
+        const float* loc = a.local + ((size_t)seq * a.np * g.H + h) * state + p;
+        const float* ltot = a.ltot + (size_t)seq * a.np * g.H + h;
+        auto start_value = [&](int n) -> float {
+            if (!valid) return 0.f;
+            if (piece == 0) return start ? start[(size_t)n * P] : 0.f;
+            if (LITE) return 0.f;
+            float s = loc[(size_t)n * P];
+            for (int q = 1; q < piece; ++q)
+                s = fmaf(ex2(ltot[(size_t)q * g.H]), s, loc[(size_t)q * g.H * state + (size_t)n * P]);
+            return s;
+        };
+        constexpr int NH = N / 2;                            // state columns of this thread
+        float sbound = 0.f;
+#pragma unroll 1
+        for (int j = 0; j < NH; j += 32) {
+            float v[32];
+#pragma unroll
+            for (int x = 0; x < 32; ++x) {
+                v[x] = start_value(NH * half + j + x);
+                sbound = fmaxf(sbound, fabsf(v[x]));
+            }
+            ptx::tmem_st32(tlane + TM_S + NH * half + j, v);
+        }
+        xm[128 * half + ch] = sbound;
+        ptx::bar_sync_or(BAR_X, NX, false);
+        sbound = fmaxf(xm[ch], xm[128 + ch]);
+        ptx::bar_sync_or(BAR_X, NX, false);
+        int so = expo(2.f * sbound) - 13;                    // S = S' 2^so, |S'| < 2^14
+        {
+            const float f = pow2(-so);
+#pragma unroll 1
+            for (int j = 0; j < NH; j += 32) {
+                float v[32];
+                ptx::tmem_ld32(tlane + TM_S + NH * half + j, v);
+#pragma unroll
+                for (int x = 0; x < 32; ++x) v[x] *= f;
+                ptx::tmem_st32(tlane + TM_S + NH * half + j, v);
+            }
+        }
+        // the ring's three rows of this channel, for the sequence's first chunk
+        float r0 = 0.f, r1 = 0.f, r2 = 0.f;
+        if (first == 0 && half == 0 && g.ring_in) {
+            const __nv_bfloat16* r = static_cast<const __nv_bfloat16*>(g.ring_in) + (size_t)seq * RING * Cx + c0 + ch;
+            r0 = to_f32(r[0]); r1 = to_f32(r[Cx]); r2 = to_f32(r[2 * (size_t)Cx]);
+        }
+        float lsum = 0.f;
+#pragma unroll 1
+        for (int c = 0; c < nc; ++c) {
+            const int b3 = c % 3;
+            bool bad = !wait_or_abort(b_step + 8 * (c % NSTEP), (uint32_t)(c / NSTEP) & 1u, abort_flag);
+            bad = !wait_or_abort(b_x + 8 * (c & 1), (uint32_t)(c >> 1) & 1u, abort_flag) || bad;
+            const int64_t rem = len_seq - (first + c) * CHUNK_T;
+            const int len = rem < CHUNK_T ? (int)rem : CHUNK_T;
+            // ---- conv + SiLU of this channel's 32 tokens
+            float v[32];
+            {
+                const __nv_bfloat16* xt = reinterpret_cast<const __nv_bfloat16*>(sb + L::X + (c & 1) * X_SLOT) + 32 * half * 128 + ch;
+                float x0 = to_f32(xt[0]), x1 = to_f32(xt[128]), x2 = to_f32(xt[256]);
+                if (first + c == 0 && half == 0) {
+                    x0 = r0; x1 = r1; x2 = r2;
+                }
+#pragma unroll
+                for (int t = 0; t < 32; ++t) {
+                    const float x3 = to_f32(xt[(t + RING) * 128]);
+                    v[t] = silu(fmaf(w.w, x3, fmaf(w.z, x2, fmaf(w.y, x1, fmaf(w.x, x0, bias)))));
+                    x0 = x1; x1 = x2; x2 = x3;
+                }
+            }
+            if (len < CHUNK_T) {                             // rows past the sequence: whatever lies there
+#pragma unroll
+                for (int t = 0; t < 32; ++t)
+                    if (32 * half + t >= len) v[t] = 0.f;
+            }
+            float m = 0.f;
+#pragma unroll
+            for (int t = 0; t < 32; ++t) m = fmaxf(m, fabsf(v[t]));
+            xm[128 * half + ch] = m;
+            if (ptx::bar_sync_or(BAR_X, NX, bad)) break;
+            if (tid == 0 && c + 2 < nc) {                    // the x tile is in registers
+                ptx::fence_async_smem();
+                load_x(c + 2);
+            }
+            // ---- scales
+            const float* st = step_of(c, hh);
+            const float lend = st[ST_LOG], dec = st[ST_DEC];
+            const int edt = __float_as_int(st[ST_EDT]);
+            const int2 ebc = scale_of(c);
+            const int ex = expo(fmaxf(xm[ch], xm[128 + ch]));
+            const float bound = fmaf(dec, sbound, pow2(9 + ex + edt + ebc.x));   // of |S| after this chunk
+            int sn = (int)((__float_as_uint(bound) >> 23) & 255u) - 127 - 13;
+            sn = sn < -100 ? -100 : sn > 100 ? 100 : sn;
+            if (half == 0 && !LITE) {
+                sSX[b3 * 128 + ch] = pow2(m_exponent(edt, ebc.x, ebc.y, skip) + ex);
+                sSI[b3 * 128 + ch] = pow2(so + ebc.y);
+            }
+            // ---- operand rows of this half's tokens
+            uint32_t xf[16], xh[16], xl[16];
+            {
+                const float xs = pow2(-ex), kx = pow2(ebc.x - sn);
+                const float4* wt = reinterpret_cast<const float4*>(st + ST_W + 32 * half);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    const float4 w4 = wt[q];
+                    const float y0 = v[4 * q] * w4.x * kx, y1 = v[4 * q + 1] * w4.y * kx;
+                    const float y2 = v[4 * q + 2] * w4.z * kx, y3 = v[4 * q + 3] * w4.w * kx;
+                    xh[2 * q] = pack2(y0, y1);
+                    xh[2 * q + 1] = pack2(y2, y3);
+                    const float2 h01 = __half22float2(*reinterpret_cast<const __half2*>(&xh[2 * q]));
+                    const float2 h23 = __half22float2(*reinterpret_cast<const __half2*>(&xh[2 * q + 1]));
+                    xl[2 * q] = pack2(y0 - h01.x, y1 - h01.y);
+                    xl[2 * q + 1] = pack2(y2 - h23.x, y3 - h23.y);
+                    if (!LITE) {
+                        xf[2 * q] = pack2(v[4 * q] * xs, v[4 * q + 1] * xs);
+                        xf[2 * q + 1] = pack2(v[4 * q + 2] * xs, v[4 * q + 3] * xs);
+                    }
+                }
+            }
+            // ---- the previous chunk's MMAs have read the operands and written S
+            if (c > 0) {
+                bad = !wait_or_abort(b_done, (uint32_t)(c - 1) & 1u, abort_flag);
+                ptx::tc_fence_after();
+                if (tid == 32 && c + 1 < nc && !bad) load_rec(c + 1);   // its slot's MMAs and M are done too
+            }
+            ptx::tmem_st16u(tlane + TM_XH + 16 * half, xh);
+            ptx::tmem_st16u(tlane + TM_XL + 16 * half, xl);
+            if (!LITE) ptx::tmem_st16u(tlane + TM_XF + 16 * half, xf);
+            const float rs = dec * pow2(so - sn);
+#pragma unroll 1
+            for (int j = 0; j < NH; j += 32) {
+                float s[32];
+                ptx::tmem_ld32(tlane + TM_S + NH * half + j, s);
+                if (!LITE) {
+                    uint32_t sh[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) sh[e] = pack2(s[2 * e], s[2 * e + 1]);
+                    ptx::tmem_st16u(tlane + TM_SH + (NH * half + j) / 2, sh);
+                }
+#pragma unroll
+                for (int x = 0; x < 32; ++x) s[x] *= rs;
+                ptx::tmem_st32(tlane + TM_S + NH * half + j, s);
+            }
+            ptx::tmem_wait_st();
+            ptx::tc_fence_before();
+            if (ptx::bar_sync_or(BAR_X, NX, bad)) break;
+            if (tid == 0) mbar_arrive(b_xready);
+            so = sn;
+            sbound = bound;
+            lsum += lend;
+        }
+        // ---- end state
+        const bool ok = nc == 0 || wait_or_abort(b_done, (uint32_t)(nc - 1) & 1u, abort_flag);
+        ptx::tc_fence_after();
+        if (ok && !*abort_flag && valid && (LITE || last_piece)) {
+            float* out = LITE ? a.local + (((size_t)seq * a.np + piece) * g.H + h) * state + p
+                              : g.S_out + ((size_t)seq * g.H + h) * state + p;
+            const float f = pow2(so);
+#pragma unroll 1
+            for (int j = 0; j < NH; j += 32) {
+                float s[32];
+                ptx::tmem_ld32(tlane + TM_S + NH * half + j, s);
+#pragma unroll
+                for (int x = 0; x < 32; ++x) out[(size_t)(NH * half + j + x) * P] = s[x] * f;
+            }
+            if (LITE && half == 0 && p == 0) a.ltot[((size_t)seq * a.np + piece) * g.H + h] = lsum;
+        }
+    } else if (warp < 16) {
+        // ================================ Y group ================================
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REG_Y));
+        if constexpr (!LITE) {
+            const int yt = tid - NX, ch = 32 * quarter + lane;
+            // M tiles start zero: only pieces up to the diagonal are written below
+            for (int i = yt; i < 2 * U * 512; i += NY) reinterpret_cast<uint4*>(sb + L::M)[i] = make_uint4(0, 0, 0, 0);
+            const int rt = yt >> 3, rseg = yt & 7;           // row pass: rows rt and 32 + rt, values 32 q + 4 rseg ..
+            const __nv_bfloat16* z = static_cast<const __nv_bfloat16*>(g.z);
+            uint2 zc[2][4], zn[2][4];
+            auto load_z = [&](int c, uint2 (&dst)[2][4]) {
+                const int64_t rem = len_seq - (first + c) * CHUNK_T;
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    const int t = 32 * hf + rt;
+                    const bool in = z && c < nc && t < rem;
+                    const __nv_bfloat16* src = z + (bos + (first + c) * CHUNK_T + t) * g.z_stride + c0 + 4 * rseg;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        dst[hf][q] = in && 32 * q + 4 * rseg < nh * P ? __ldg(reinterpret_cast<const uint2*>(src + 32 * q))
+                                                                      : make_uint2(0, 0);
+                }
+            };
+            // M of chunk c: 288 pieces of 8 columns per head (rows r and 63 - r hold nine)
+            auto build_m = [&](int c) -> bool {
+                bool bad = !wait_or_abort(b_step + 8 * (c % NSTEP), (uint32_t)(c / NSTEP) & 1u, abort_flag);
+                bad = !wait_or_abort(b_rec + 8 * (c & 1), (uint32_t)(c >> 1) & 1u, abort_flag) || bad;
+                const unsigned char* G = sb + L::REC + (c & 1) * Rec<N>::BYTES + Rec<N>::OFF_G;
+                const int2 ebc = scale_of(c);
+#pragma unroll 1
+                for (int i = yt; i < 288 * nh; i += NY) {
+                    const int hd = i >= 288, k = i - 288 * hd, pair = k / 9, j0 = k % 9, lo = (pair >> 3) + 1;
+                    const int r = j0 < lo ? pair : 63 - pair, j = j0 < lo ? j0 : j0 - lo;
+                    const float* st = step_of(c, hd);
+                    const float skip = g.skip ? __ldg(g.skip + h0 + hd) : 0.f;
+                    const int em = m_exponent(__float_as_int(st[ST_EDT]), ebc.x, ebc.y, skip);
+                    const float f = pow2(ebc.x + ebc.y - em), lr = st[r];
+                    const uint32_t off = sw128_off(r, 8 * j, CHUNK_T);
+                    const uint4 g4 = *reinterpret_cast<const uint4*>(G + off);
+                    const uint32_t gw[4] = {g4.x, g4.y, g4.z, g4.w};
+                    float mv[8];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 gg = __half22float2(*reinterpret_cast<const __half2*>(&gw[e]));
+                        const int s = 8 * j + 2 * e;
+                        const float2 ls = *reinterpret_cast<const float2*>(st + s), dt = *reinterpret_cast<const float2*>(st + ST_DT + s);
+                        mv[2 * e] = s <= r ? gg.x * ex2(lr - ls.x) * (dt.x * f) : 0.f;
+                        mv[2 * e + 1] = s + 1 <= r ? gg.y * ex2(lr - ls.y) * (dt.y * f) : 0.f;
+                        if (s == r) mv[2 * e] += skip * pow2(-em);
+                        if (s + 1 == r) mv[2 * e + 1] += skip * pow2(-em);
+                    }
+                    *reinterpret_cast<uint4*>(sb + L::M + ((c & 1) * U + hd) * 8192 + off) =
+                        make_uint4(pack2(mv[0], mv[1]), pack2(mv[2], mv[3]), pack2(mv[4], mv[5]), pack2(mv[6], mv[7]));
+                }
+                ptx::fence_async_smem();
+                if (ptx::bar_sync_or(BAR_Y, NY, bad)) return false;
+                if (yt == 0) mbar_arrive(b_m + 8 * (c & 1));
+                return true;
+            };
+            float* ys = reinterpret_cast<float*>(sb + L::Y);
+            __nv_bfloat16* o = static_cast<__nv_bfloat16*>(g.o);
+            load_z(0, zc);
+            bool go = true;
+            ptx::bar_sync_or(BAR_Y, NY, false);              // (the zeros precede every piece)
+            if (nc > 0) go = build_m(0);
+#pragma unroll 1
+            for (int c = 0; go && c < nc; ++c) {
+                if (c + 1 < nc && !build_m(c + 1)) break;
+                load_z(c + 1, zn);
+                const bool bad = !wait_or_abort(b_done, (uint32_t)c & 1u, abort_flag);
+                if (ptx::bar_sync_or(BAR_Y, NY, bad)) break; // (and the rows of the chunk before are written)
+                ptx::tc_fence_after();
+                {
+                    const int b3 = c % 3, th = half;
+                    const float si = reinterpret_cast<const float*>(sb + L::SI)[b3 * 128 + ch];
+                    const float sx = reinterpret_cast<const float*>(sb + L::SX)[b3 * 128 + ch];
+                    const float4* el = reinterpret_cast<const float4*>(step_of(c, min(ch / P, nh - 1)) + ST_EL + 32 * th);
+                    float di[32], dh[32];
+                    ptx::tmem_ld32(tlane + TM_DI + 32 * th, di);
+                    ptx::tmem_ld32(tlane + TM_D + 64 * (ch / P) + 32 * th, dh);
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        const float4 e4 = el[q];
+                        const float ev[4] = {e4.x, e4.y, e4.z, e4.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            ys[(32 * th + 4 * q + e) * LDYS + ch] = fmaf(di[4 * q + e], si * ev[e], sx * dh[4 * q + e]);
+                    }
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(b_dfree);     // D and this chunk's scales are read
+                }
+                ptx::bar_sync_or(BAR_Y, NY, false);
+                const int64_t rem = len_seq - (first + c) * CHUNK_T;
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    const int t = 32 * hf + rt;
+                    if (t < rem) {
+                        __nv_bfloat16* dst = o + (size_t)(bos + (first + c) * CHUNK_T + t) * W + c0 + 4 * rseg;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            if (32 * q + 4 * rseg >= nh * P) continue;
+                            float4 y = *reinterpret_cast<const float4*>(ys + t * LDYS + 32 * q + 4 * rseg);
+                            if (z) {
+                                const __nv_bfloat162* zz = reinterpret_cast<const __nv_bfloat162*>(&zc[hf][q]);
+                                const float2 z0 = __bfloat1622float2(zz[0]), z1 = __bfloat1622float2(zz[1]);
+                                y.x *= silu(z0.x); y.y *= silu(z0.y);
+                                y.z *= silu(z1.x); y.w *= silu(z1.y);
+                            }
+                            const __nv_bfloat162 o0 = __floats2bfloat162_rn(y.x, y.y), o1 = __floats2bfloat162_rn(y.z, y.w);
+                            *reinterpret_cast<uint2*>(dst + 32 * q) =
+                                make_uint2(*reinterpret_cast<const uint32_t*>(&o0), *reinterpret_cast<const uint32_t*>(&o1));
+                        }
+                    }
+                }
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) zc[hf][q] = zn[hf][q];
+            }
+        }
+    } else {
+        // ============================ MMA issue (one thread) ======================
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_ISSUE));
+        if (tid == 512) {
+        constexpr uint32_t ID64 = ptx::idesc_f16_f32(128, 64), IDN = ptx::idesc_f16_f32(128, N);
+#pragma unroll 1
+        for (int c = 0; c < nc; ++c) {
+            const uint32_t rec = base + L::REC + (c & 1) * Rec<N>::BYTES;
+            if (!wait_or_abort(b_rec + 8 * (c & 1), (uint32_t)(c >> 1) & 1u, abort_flag)) break;
+            if (!LITE && c > 0 && !wait_or_abort(b_dfree, (uint32_t)(c - 1) & 1u, abort_flag)) break;
+            if (!wait_or_abort(b_xready, (uint32_t)c & 1u, abort_flag)) break;
+            ptx::tc_fence_after();
+            if (!LITE) {
+#pragma unroll
+                for (int kk = 0; kk < N / 16; ++kk)
+                    ptx::mma_f16_ta(tmem + TM_DI, tmem + TM_SH + 8 * kk,
+                                    ptx::sdesc_sw128(rec + Rec<N>::OFF_C + (kk >> 2) * 8192 + (kk & 3) * 32), ID64, kk > 0);
+            }
+#pragma unroll
+            for (int term = 0; term < 3; ++term) {           // hi hi, hi lo, lo hi
+                const uint32_t at = term == 2 ? TM_XL : TM_XH, bt = rec + (term == 1 ? Rec<N>::OFF_LO : 0);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    ptx::mma_f16_ta(tmem + TM_S, tmem + at + 8 * kk, ptx::sdesc_sw128(bt + kk * 32), IDN, 1);
+            }
+            if (!LITE) {
+                // (an abort here leaves MMAs in flight: the drain below covers them)
+                if (!wait_or_abort(b_m + 8 * (c & 1), (uint32_t)(c >> 1) & 1u, abort_flag)) break;
+                ptx::tc_fence_after();
+#pragma unroll 1
+                for (int hd = 0; hd < nh; ++hd)
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        ptx::mma_f16_ta(tmem + TM_D + 64 * hd, tmem + TM_XF + 8 * kk,
+                                        ptx::sdesc_sw128(base + L::M + ((c & 1) * U + hd) * 8192 + kk * 32), ID64, kk > 0);
+            }
+            ptx::mma_commit(b_done);
+        }
+        // every MMA of this thread lands before its tensor memory is freed
+        ptx::mma_commit(b_drain);
+        ptx::mbar_wait(b_drain, 0, WAIT_LIMIT_NS);
+        }
+    }
+    __syncwarp();
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (*abort_flag && tid == 0) {
+        atomicExch(a.status, ERR_TIMEOUT);
+        // loads in flight land before the CTA leaves: the last one of each barrier
+        for (int c = max(0, issued[0] - NSTEP); c < issued[0]; ++c) {
+            if (c >= issued[0] - 2) ptx::mbar_wait(b_x + 8 * (c & 1), (uint32_t)(c >> 1) & 1u, WAIT_LIMIT_NS);
+            ptx::mbar_wait(b_step + 8 * (c % NSTEP), (uint32_t)(c / NSTEP) & 1u, WAIT_LIMIT_NS);
+        }
+        for (int c = max(0, issued[1] - 2); c < issued[1]; ++c)
+            ptx::mbar_wait(b_rec + 8 * (c & 1), (uint32_t)(c >> 1) & 1u, WAIT_LIMIT_NS);
+    }
+    __syncthreads();
+    if (warp == 16) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, TMEM_COLS);
+    }
+}
+
+template <int P, int N, bool LITE>
+cudaError_t launch(const ChunkArgs& a, cudaStream_t s) {
+    const int64_t blocks = (int64_t)a.units * a.np * a.g.n_seqs;
+    if (blocks > (int64_t)INT32_MAX) return cudaErrorInvalidValue;
+    constexpr int smem = (int)Map<P, N>::BYTES;
+    auto k = chunk_kernel<P, N, LITE>;
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    k<<<(unsigned)blocks, NT, smem, s>>>(a);
+    return cudaGetLastError();
+}
+
+template <bool LITE>
+cudaError_t launch_pn(const ChunkArgs& a, cudaStream_t s) {
+    if (a.g.P == 64) return a.g.N == 64 ? launch<64, 64, LITE>(a, s) : launch<64, 128, LITE>(a, s);
+    return a.g.N == 64 ? launch<128, 64, LITE>(a, s) : launch<128, 128, LITE>(a, s);
+}
+
+}  // namespace
+
+cudaError_t launch_chunks(const ChunkArgs& a, bool lite, cudaStream_t s) {
+    return lite ? launch_pn<true>(a, s) : launch_pn<false>(a, s);
+}
+
+}  // namespace ssm
+}  // namespace kda

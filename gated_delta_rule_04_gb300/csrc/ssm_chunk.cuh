@@ -1,0 +1,82 @@
+// Chunked prefill of the state space mixer: what its two kernels share.
+#pragma once
+
+#include <cuda.h>
+
+#include "kda_chunk_layout.cuh"
+#include "ssm_common.cuh"
+
+namespace kda {
+namespace ssm {
+
+// Record of one (chunk, group): the operand tiles that do not depend on the
+// head, as the byte image of the consumer's shared memory (fp16, K-major,
+// 128-byte swizzle).  B and C are stored scaled by powers of two so that the
+// tile's largest magnitude lies in [1, 2):
+//   B^T hi, B^T lo  [N rows][64 tok]   B' = hi + lo to 22 bits
+//   C               [64 tok rows][N]
+//   G = C' B'^T     [64 tok rows][64]  8-column pieces up to the diagonal only
+template <int N> struct Rec {
+    static constexpr uint32_t BT = N * 128;             // bytes of B^T hi (and of lo)
+    static constexpr uint32_t OFF_LO = BT;
+    static constexpr uint32_t OFF_C = 2 * BT;
+    static constexpr uint32_t OFF_G = OFF_C + (N / 64) * 8192;
+    static constexpr uint32_t BYTES = OFF_G + 8192;
+};
+inline size_t rec_bytes(int N) { return N == 64 ? Rec<64>::BYTES : Rec<128>::BYTES; }
+
+// Step record of one (chunk, head), fp32, with l_s = the log2 decay of token s:
+//   [0, 64)     lam_t: inclusive cumulative sum of max(l_s, -40), for differences
+//               between two tokens of the chunk.  The clamp keeps |lam| <= 2560, so
+//               that a difference of two is good to 2^-13; a decay of 2^-40 and one
+//               of less both vanish in the 11-bit operand they go to.
+//   [64, 128)   dt
+//   [128, 192)  2^(sum_{s > t} l_s) dt_t: the token's weight in the end state, from a
+//               suffix sum (a difference of long prefix sums would cost the fp32
+//               state its last digits)
+//   [192, 256)  2^(sum_{s <= t} l_s)
+//   [256]       2^(sum of all l_s), [257] exponent of the largest dt (int), [258] sum of l_s
+constexpr int STEP_FLOATS = 260;
+constexpr int ST_DT = 64, ST_W = 128, ST_EL = 192, ST_DEC = 256, ST_EDT = 257, ST_LOG = 258;
+constexpr float LAM_MIN = -40.f;
+
+// Exponent e with 2^e <= x < 2^(e+1), clamped to +-40 (so that sums of a few
+// exponents stay inside fp32's range; beyond it precision goes before range).
+__device__ __forceinline__ int expo(float x) {
+    const int e = (int)((__float_as_uint(x) >> 23) & 255u) - 127;
+    return e < -40 ? -40 : e > 40 ? 40 : e;
+}
+// 2^e for any integer e, clamped to fp32's normal range.
+__device__ __forceinline__ float pow2(int e) {
+    e = e < -126 ? -126 : e > 127 ? 127 : e;
+    return __uint_as_float((uint32_t)(e + 127) << 23);
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+struct ChunkArgs {
+    CUtensorMap map67, map64;     // xbc rows: boxes of 67 and 64 rows x 128 channels
+    PrefillArgs g;
+    const ChunkDesc* chunks;      // [n_chunks]
+    const int64_t* coff;          // [n_seqs + 1]
+    unsigned char* rec;           // [n_chunks][G][Rec::BYTES]
+    float* step;                  // [n_chunks][H][STEP_FLOATS]
+    int4* scale;                  // [n_chunks][G] exponents of B and C
+    int32_t* status;
+    // Pieces of lp chunks (np per sequence at most) run side by side; `local`
+    // and `ltot` take each piece's end state from its own start and its log2 decay.
+    float* local;                 // [n_seqs][np][H][N][P]
+    float* ltot;                  // [n_seqs][np][H]
+    int32_t np, lp;
+    int32_t n_chunks, units, upg; // units of 128 channels, in all and per group
+};
+
+cudaError_t launch_chunk_prep(const ChunkArgs& a, cudaStream_t s);
+// lite: only the pieces' end states (all pieces but each sequence's last).
+cudaError_t launch_chunks(const ChunkArgs& a, bool lite, cudaStream_t s);
+
+}  // namespace ssm
+}  // namespace kda

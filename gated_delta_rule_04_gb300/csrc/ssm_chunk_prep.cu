@@ -1,0 +1,232 @@
+// Chunk preparation of the state space mixer's chunked prefill: everything of
+// a 64-token chunk that its heads share, and the steps' cumulative decays.
+//
+// Blocks (chunk, group): conv + SiLU of the group's B and C, their tiles in
+// the consumer's layout and G = C B^T on the tensor cores (tcgen05, M = 128:
+// rows 64-127 read the memory behind the 64 rows of C, their lanes of the
+// result are not used).  A record is 56 KiB at N = 128 and serves every head
+// of the group, so its conv and its G are computed once instead of per head.
+// The other blocks (chunk, 64 heads): dt = softplus(.), its cumulative sum
+// times -exp(A_log) in log2 units, a warp per head.
+//
+// B reaches the fp32 state, whose error the operands' rounding would set: B'
+// goes out as an fp16 pair (22 bits).  C and G reach bf16 outputs only and are
+// rounded once to fp16's 11 bits; bf16's 8 would be as coarse as the output.
+#include "ssm_chunk.cuh"
+#include "tc_ptx.cuh"
+
+namespace kda {
+namespace ssm {
+namespace {
+
+constexpr int NT = 256;
+constexpr int HB = 64;                     // heads of a step block
+constexpr uint32_t TMEM_COLS = 64;
+constexpr uint64_t WAIT_LIMIT_NS = 2000000000ull;
+constexpr float LOG2E = 1.4426950408889634f;
+
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ void steps(const ChunkArgs& a, const ChunkDesc d, int chunk, int hb) {
+    const PrefillArgs& g = a.g;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const __nv_bfloat16* dts = static_cast<const __nv_bfloat16*>(g.dt);
+    for (int h = hb * HB + warp; h < min(g.H, (hb + 1) * HB); h += NT / 32) {
+        const float k = -expf(g.A_log[h]) * LOG2E, bias = g.dt_bias[h];
+        float dt[2], l[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int t = 2 * lane + j;
+            dt[j] = t < d.len ? softplus(to_f32(dts[(size_t)(d.t0 + t) * g.dt_stride + h]) + bias) : 0.f;
+            l[j] = k * dt[j];
+        }
+        const float c0 = fmaxf(l[0], LAM_MIN), c1 = fmaxf(l[1], LAM_MIN);
+        // inclusive prefix (plain and clamped) and suffix sums of the lanes' pairs
+        float pre = l[0] + l[1], cl = c0 + c1, suf = pre, top = fmaxf(dt[0], dt[1]);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const float u = __shfl_up_sync(0xffffffffu, pre, o), v = __shfl_up_sync(0xffffffffu, cl, o);
+            const float w = __shfl_down_sync(0xffffffffu, suf, o);
+            if (lane >= o) {
+                pre += u;
+                cl += v;
+            }
+            if (lane + o < 32) suf += w;
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        }
+        float pb = __shfl_up_sync(0xffffffffu, pre, 1), cb = __shfl_up_sync(0xffffffffu, cl, 1);
+        float sa = __shfl_down_sync(0xffffffffu, suf, 1);
+        if (lane == 0) pb = cb = 0.f;
+        if (lane == 31) sa = 0.f;
+        const float end = __shfl_sync(0xffffffffu, pre, 31);
+        float* out = a.step + ((size_t)chunk * g.H + h) * STEP_FLOATS;
+        *reinterpret_cast<float2*>(out + 2 * lane) = make_float2(cb + c0, cb + c0 + c1);
+        *reinterpret_cast<float2*>(out + ST_DT + 2 * lane) = make_float2(dt[0], dt[1]);
+        *reinterpret_cast<float2*>(out + ST_W + 2 * lane) = make_float2(ex2(l[1] + sa) * dt[0], ex2(sa) * dt[1]);
+        *reinterpret_cast<float2*>(out + ST_EL + 2 * lane) = make_float2(ex2(pb + l[0]), ex2(pb + l[0] + l[1]));
+        if (lane == 0)
+            *reinterpret_cast<float4*>(out + ST_DEC) = make_float4(ex2(end), __int_as_float(expo(top)), end, 0.f);
+    }
+}
+
+template <int N>
+__global__ void __launch_bounds__(NT) prep_kernel(const __grid_constant__ ChunkArgs a) {
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ float wmax[NT / 32];
+    __shared__ __align__(8) unsigned long long bar;
+    __shared__ uint32_t tmem_slot;
+    const PrefillArgs& g = a.g;
+    const int chunk = blockIdx.x, grp = blockIdx.y;
+    const ChunkDesc d = a.chunks[chunk];
+    if (grp >= g.G) {
+        steps(a, d, chunk, grp - g.G);
+        return;
+    }
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t raw = ptx::smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
+    unsigned char* sC = smem_raw + (base - raw);
+    unsigned char* sB = sC + (N / 64) * 8192;
+    const uint32_t bar_a = ptx::smem_u32(&bar);
+    if (warp == 0) {
+        ptx::tmem_alloc(ptx::smem_u32(&tmem_slot), TMEM_COLS);
+        ptx::tmem_relinquish();
+    }
+    if (tid == 0) {
+        ptx::mbar_init(bar_a, 1);
+        ptx::fence_mbar_init();
+    }
+
+    // ---- conv + SiLU: a thread owns a channel of B or C for TP tokens
+    constexpr int PARTS = NT / (2 * N), TP = CHUNK_T / PARTS;
+    const int ch = tid % (2 * N), part = tid / (2 * N);
+    const bool is_c = ch >= N;
+    const int n = is_c ? ch - N : ch;
+    const int W = g.H * g.P, Cx = W + 2 * g.G * N;
+    const int c = W + (is_c ? g.G * N : 0) + grp * N + n;
+    const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(g.xbc) + c;
+    const __nv_bfloat16* ring = static_cast<const __nv_bfloat16*>(g.ring_in);
+    const float4 w = __ldg(reinterpret_cast<const float4*>(g.conv_w) + c);
+    const float bias = g.conv_b ? g.conv_b[c] : 0.f;
+    float v[TP];
+    {
+        float h[RING];
+#pragma unroll
+        for (int j = 0; j < RING; ++j) {
+            const int t = part * TP + j - RING;
+            if (d.pos + t >= 0) h[j] = t < d.len ? to_f32(x[(int64_t)(d.t0 + t) * g.xbc_stride]) : 0.f;
+            else h[j] = ring ? to_f32(ring[((size_t)d.seq * RING + (d.pos + t + RING)) * Cx + c]) : 0.f;
+        }
+        __nv_bfloat16 r[TP];
+#pragma unroll
+        for (int t = 0; t < TP; ++t)
+            r[t] = part * TP + t < d.len ? x[(int64_t)(d.t0 + part * TP + t) * g.xbc_stride] : __nv_bfloat16(0.f);
+#pragma unroll
+        for (int t = 0; t < TP; ++t) {
+            const float x3 = to_f32(r[t]);
+            const float y = silu(fmaf(w.w, x3, fmaf(w.z, h[2], fmaf(w.y, h[1], fmaf(w.x, h[0], bias)))));
+            v[t] = part * TP + t < d.len ? y : 0.f;
+            h[0] = h[1]; h[1] = h[2]; h[2] = x3;
+        }
+    }
+    float m = 0.f;
+#pragma unroll
+    for (int t = 0; t < TP; ++t) m = fmaxf(m, fabsf(v[t]));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (lane == 0) wmax[warp] = m;
+    __syncthreads();
+    float mb = 0.f, mc = 0.f;
+#pragma unroll
+    for (int k = 0; k < NT / 32; ++k) {
+        if ((32 * k) % (2 * N) >= N) mc = fmaxf(mc, wmax[k]);
+        else mb = fmaxf(mb, wmax[k]);
+    }
+    const int eb = expo(mb), ec = expo(mc);
+    if (tid == 0) a.scale[(size_t)chunk * g.G + grp] = make_int4(eb, ec, 0, 0);
+    const float s = pow2(is_c ? -ec : -eb);
+#pragma unroll
+    for (int t = 0; t < TP; ++t) v[t] *= s;
+    unsigned char* rec = a.rec + ((size_t)chunk * g.G + grp) * Rec<N>::BYTES;
+    unsigned char* tile = is_c ? sC : sB;
+#pragma unroll
+    for (int t = 0; t < TP; ++t)
+        *reinterpret_cast<__half*>(tile + sw128_off(part * TP + t, n, CHUNK_T)) = __float2half_rn(v[t]);
+    ptx::fence_async_smem();
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    if (tid == 0) {
+#pragma unroll
+        for (int kk = 0; kk < N / 16; ++kk) {
+            const uint32_t off = (kk >> 2) * 8192 + (kk & 3) * 32;
+            ptx::mma_f16(tmem, ptx::sdesc_sw128(base + off), ptx::sdesc_sw128(base + (N / 64) * 8192 + off),
+                         ptx::idesc_f16_f32(128, 64), kk > 0);
+        }
+        ptx::mma_commit(bar_a);
+    }
+    // ---- B^T hi and lo from registers, the C tile as it lies in shared memory
+    if (!is_c) {
+#pragma unroll
+        for (int q = 0; q < TP / 8; ++q) {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float x0 = v[8 * q + 2 * e], x1 = v[8 * q + 2 * e + 1];
+                hi[e] = pack2(x0, x1);
+                const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hi[e]));
+                lo[e] = pack2(x0 - back.x, x1 - back.y);
+            }
+            const uint32_t off = sw128_off(n, part * TP + 8 * q, N);
+            *reinterpret_cast<uint4*>(rec + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(rec + Rec<N>::OFF_LO + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+    }
+    for (int i = tid; i < (N / 64) * 512; i += NT)
+        reinterpret_cast<uint4*>(rec + Rec<N>::OFF_C)[i] = reinterpret_cast<const uint4*>(sC)[i];
+    // ---- G: rows 0-63 from TMEM lanes 0-63
+    const bool ok = ptx::mbar_wait(bar_a, 0, WAIT_LIMIT_NS);
+    ptx::tc_fence_after();
+    if (ok && warp < 2) {
+        const int row = 32 * warp + lane;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            float f[32];
+            ptx::tmem_ld32(tmem + ((uint32_t)(32 * warp) << 16) + 32 * j, f);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (4 * j + q <= row >> 3)
+                    *reinterpret_cast<uint4*>(rec + Rec<N>::OFF_G + sw128_off(row, 32 * j + 8 * q, CHUNK_T)) =
+                        make_uint4(pack2(f[8 * q], f[8 * q + 1]), pack2(f[8 * q + 2], f[8 * q + 3]),
+                                   pack2(f[8 * q + 4], f[8 * q + 5]), pack2(f[8 * q + 6], f[8 * q + 7]));
+        }
+    }
+    if (!ok && tid == 0) {
+        atomicExch(a.status, ERR_TIMEOUT);
+        ptx::mbar_wait(bar_a, 0, WAIT_LIMIT_NS);   // the MMAs finish before their TMEM is freed
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, TMEM_COLS);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_chunk_prep(const ChunkArgs& a, cudaStream_t s) {
+    if (a.n_chunks == 0) return cudaSuccess;
+    const dim3 grid(a.n_chunks, a.g.G + (a.g.H + HB - 1) / HB);
+    if (grid.y > 65535) return cudaErrorInvalidValue;
+    const size_t smem = (size_t)(a.g.N / 64) * 16384 + 1024;
+    if (a.g.N == 64) prep_kernel<64><<<grid, NT, smem, s>>>(a);
+    else prep_kernel<128><<<grid, NT, smem, s>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace ssm
+}  // namespace kda
