@@ -48,7 +48,7 @@ namespace {
 
 constexpr int NT = 640;                    // 8 X warps, 8 Y warps, a warpgroup whose first thread issues the MMAs
 // register split: 96 a thread at launch (65536 / 640), moved between the warpgroups
-constexpr int REG_LAUNCH = 96, REG_X = 120, REG_Y = 104, REG_ISSUE = 24;
+constexpr int REG_LAUNCH = 96, REG_X = 104, REG_Y = 104, REG_ISSUE = 64;   // (no spills in any variant)
 static_assert(256 * REG_X + 256 * REG_Y + 128 * REG_ISSUE <= NT * REG_LAUNCH && REG_X % 8 == 0 && REG_Y % 8 == 0,
               "the split must fit the launch's registers, or setmaxnreg.inc waits forever");
 constexpr int NX = 256, NY = 256;
@@ -92,9 +92,10 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
 }
 // Waits for a phase; false after the limit or once another thread gave up.
 __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
-    if (ptx::mbar_try_wait(bar, parity)) return true;
+    // (a suspended thread takes no issue slots from the warps at work)
+    if (ptx::mbar_try_wait_sleep(bar, parity, 1000)) return true;
     const uint64_t t0 = ptx::globaltimer_ns();
-    while (!ptx::mbar_try_wait(bar, parity)) {
+    while (!ptx::mbar_try_wait_sleep(bar, parity, 1000)) {
         if (*abort_flag) return false;
         if (ptx::globaltimer_ns() - t0 > WAIT_LIMIT_NS) {
             *abort_flag = 1;
@@ -136,7 +137,7 @@ __global__ void __launch_bounds__(NT, 1) chunk_kernel(const __grid_constant__ Ch
     unsigned char* sb = smem_raw + (base - raw);
     const uint32_t bars = base + L::BAR;
     const uint32_t b_x = bars, b_step = bars + 16, b_rec = bars + 56, b_m = bars + 72;   // [2], [NSTEP], [2], [2]
-    const uint32_t b_xready = bars + 88, b_done = bars + 96, b_dfree = bars + 104, b_drain = bars + 112;
+    const uint32_t b_xready = bars + 88, b_done = bars + 96, b_dfree = bars + 104, b_drain = bars + 112, b_sdone = bars + 120;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sb + L::BAR + 128);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(sb + L::BAR + 132);
     volatile int* issued = reinterpret_cast<volatile int*>(sb + L::BAR + 136);   // loads issued: [0] x and steps, [1] records
@@ -157,6 +158,7 @@ __global__ void __launch_bounds__(NT, 1) chunk_kernel(const __grid_constant__ Ch
         ptx::mbar_init(b_done, 1);
         ptx::mbar_init(b_dfree, NY / 32);
         ptx::mbar_init(b_drain, 1);
+        ptx::mbar_init(b_sdone, 1);
         *abort_flag = 0;
         issued[0] = issued[1] = 0;
         ptx::fence_mbar_init();
@@ -211,6 +213,8 @@ __global__ void __launch_bounds__(NT, 1) chunk_kernel(const __grid_constant__ Ch
         const int p = ch % P;
         const float4 w = __ldg(reinterpret_cast<const float4*>(g.conv_w) + c0 + ch);
         const float bias = g.conv_b ? g.conv_b[c0 + ch] : 0.f;
+        const float2 w0 = make_float2(w.x, w.x), w1 = make_float2(w.y, w.y), w2 = make_float2(w.z, w.z), w3 = make_float2(w.w, w.w);
+        const float2 bias2 = make_float2(bias, bias);
         const float skip = g.skip ? g.skip[h] : 0.f;
         float* xm = reinterpret_cast<float*>(sb + L::XM);
         float* sSX = reinterpret_cast<float*>(sb + L::SX);
@@ -273,29 +277,38 @@ __global__ void __launch_bounds__(NT, 1) chunk_kernel(const __grid_constant__ Ch
             bad = !wait_or_abort(b_x + 8 * (c & 1), (uint32_t)(c >> 1) & 1u, abort_flag) || bad;
             const int64_t rem = len_seq - (first + c) * CHUNK_T;
             const int len = rem < CHUNK_T ? (int)rem : CHUNK_T;
-            // ---- conv + SiLU of this channel's 32 tokens
-            float v[32];
+            // ---- conv + SiLU of this channel's 32 tokens, t and t + 16 as a packed pair
+            float2 v[16];
             {
                 const __nv_bfloat16* xt = reinterpret_cast<const __nv_bfloat16*>(sb + L::X + (c & 1) * X_SLOT) + 32 * half * 128 + ch;
-                float x0 = to_f32(xt[0]), x1 = to_f32(xt[128]), x2 = to_f32(xt[256]);
+                auto pair = [&](int t) { return make_float2(to_f32(xt[(t + RING) * 128]), to_f32(xt[(t + RING + 16) * 128])); };
+                float2 x0 = pair(-3), x1 = pair(-2), x2 = pair(-1);
                 if (first + c == 0 && half == 0) {
-                    x0 = r0; x1 = r1; x2 = r2;
+                    x0.x = r0; x1.x = r1; x2.x = r2;
                 }
 #pragma unroll
-                for (int t = 0; t < 32; ++t) {
-                    const float x3 = to_f32(xt[(t + RING) * 128]);
-                    v[t] = silu(fmaf(w.w, x3, fmaf(w.z, x2, fmaf(w.y, x1, fmaf(w.x, x0, bias)))));
+                for (int t = 0; t < 16; ++t) {
+                    const float2 x3 = pair(t);
+                    v[t] = __ffma2_rn(w0, x0, bias2);
+                    v[t] = __ffma2_rn(w1, x1, v[t]);
+                    v[t] = __ffma2_rn(w2, x2, v[t]);
+                    v[t] = __ffma2_rn(w3, x3, v[t]);
                     x0 = x1; x1 = x2; x2 = x3;
                 }
             }
-            if (len < CHUNK_T) {                             // rows past the sequence: whatever lies there
+            // rows past the sequence hold whatever lies there: out before a pair shares its reciprocal
+            if (len < CHUNK_T) {
 #pragma unroll
-                for (int t = 0; t < 32; ++t)
-                    if (32 * half + t >= len) v[t] = 0.f;
+                for (int t = 0; t < 16; ++t) {
+                    if (32 * half + t >= len) v[t].x = 0.f;
+                    if (32 * half + t + 16 >= len) v[t].y = 0.f;
+                }
             }
             float m = 0.f;
 #pragma unroll
-            for (int t = 0; t < 32; ++t) m = fmaxf(m, fabsf(v[t]));
+            for (int t = 0; t < 16; ++t) v[t] = silu2(v[t]);
+#pragma unroll
+            for (int t = 0; t < 16; ++t) m = fmaxf(m, fmaxf(fabsf(v[t].x), fabsf(v[t].y)));
             xm[128 * half + ch] = m;
             if (ptx::bar_sync_or(BAR_X, NX, bad)) break;
             if (tid == 0 && c + 2 < nc) {                    // the x tile is in registers
@@ -319,33 +332,35 @@ __global__ void __launch_bounds__(NT, 1) chunk_kernel(const __grid_constant__ Ch
             uint32_t xf[16], xh[16], xl[16];
             {
                 const float xs = pow2(-ex), kx = pow2(ebc.x - sn);
+                const float2 xs2 = make_float2(xs, xs), kx2 = make_float2(kx, kx);
                 const float4* wt = reinterpret_cast<const float4*>(st + ST_W + 32 * half);
+                // fp16 pairs hold tokens (t, t + 1): column t / 2 from the low halves, 8 + t / 2 from the high
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {
                     const float4 w4 = wt[q];
-                    const float y0 = v[4 * q] * w4.x * kx, y1 = v[4 * q + 1] * w4.y * kx;
-                    const float y2 = v[4 * q + 2] * w4.z * kx, y3 = v[4 * q + 3] * w4.w * kx;
-                    xh[2 * q] = pack2(y0, y1);
-                    xh[2 * q + 1] = pack2(y2, y3);
-                    const float2 h01 = __half22float2(*reinterpret_cast<const __half2*>(&xh[2 * q]));
-                    const float2 h23 = __half22float2(*reinterpret_cast<const __half2*>(&xh[2 * q + 1]));
-                    xl[2 * q] = pack2(y0 - h01.x, y1 - h01.y);
-                    xl[2 * q + 1] = pack2(y2 - h23.x, y3 - h23.y);
+                    const float2 ya = __fmul2_rn(v[2 * q], __fmul2_rn(make_float2(w4.x, w4.y), kx2));
+                    const float2 yb = __fmul2_rn(v[2 * q + 1], __fmul2_rn(make_float2(w4.z, w4.w), kx2));
+                    xh[q] = pack2(ya.x, yb.x);
+                    xh[8 + q] = pack2(ya.y, yb.y);
+                    const float2 lo = __half22float2(*reinterpret_cast<const __half2*>(&xh[q]));
+                    const float2 hi = __half22float2(*reinterpret_cast<const __half2*>(&xh[8 + q]));
+                    xl[q] = pack2(ya.x - lo.x, yb.x - lo.y);
+                    xl[8 + q] = pack2(ya.y - hi.x, yb.y - hi.y);
                     if (!LITE) {
-                        xf[2 * q] = pack2(v[4 * q] * xs, v[4 * q + 1] * xs);
-                        xf[2 * q + 1] = pack2(v[4 * q + 2] * xs, v[4 * q + 3] * xs);
+                        const float2 xa = __fmul2_rn(v[2 * q], xs2), xb = __fmul2_rn(v[2 * q + 1], xs2);
+                        xf[q] = pack2(xa.x, xb.x);
+                        xf[8 + q] = pack2(xa.y, xb.y);
                     }
                 }
             }
-            // ---- the previous chunk's MMAs have read the operands and written S
+            // ---- the previous chunk's state and inter MMAs have read their operands and
+            // written S (its intra MMAs, which come last, only hold X)
             if (c > 0) {
-                bad = !wait_or_abort(b_done, (uint32_t)(c - 1) & 1u, abort_flag);
+                bad = !wait_or_abort(b_sdone, (uint32_t)(c - 1) & 1u, abort_flag);
                 ptx::tc_fence_after();
-                if (tid == 32 && c + 1 < nc && !bad) load_rec(c + 1);   // its slot's MMAs and M are done too
             }
             ptx::tmem_st16u(tlane + TM_XH + 16 * half, xh);
             ptx::tmem_st16u(tlane + TM_XL + 16 * half, xl);
-            if (!LITE) ptx::tmem_st16u(tlane + TM_XF + 16 * half, xf);
             const float rs = dec * pow2(so - sn);
 #pragma unroll 1
             for (int j = 0; j < NH; j += 32) {
@@ -358,9 +373,19 @@ __global__ void __launch_bounds__(NT, 1) chunk_kernel(const __grid_constant__ Ch
                     ptx::tmem_st16u(tlane + TM_SH + (NH * half + j) / 2, sh);
                 }
 #pragma unroll
-                for (int x = 0; x < 32; ++x) s[x] *= rs;
+                for (int x = 0; x < 32; x += 2) {
+                    const float2 d = __fmul2_rn(make_float2(s[x], s[x + 1]), make_float2(rs, rs));
+                    s[x] = d.x;
+                    s[x + 1] = d.y;
+                }
                 ptx::tmem_st32(tlane + TM_S + NH * half + j, s);
             }
+            if (c > 0) {
+                bad = !wait_or_abort(b_done, (uint32_t)(c - 1) & 1u, abort_flag) || bad;
+                ptx::tc_fence_after();
+                if (tid == 32 && c + 1 < nc && !bad) load_rec(c + 1);   // its slot's MMAs and M are done
+            }
+            if (!LITE) ptx::tmem_st16u(tlane + TM_XF + 16 * half, xf);
             ptx::tmem_wait_st();
             ptx::tc_fence_before();
             if (ptx::bar_sync_or(BAR_X, NX, bad)) break;
@@ -394,50 +419,79 @@ __global__ void __launch_bounds__(NT, 1) chunk_kernel(const __grid_constant__ Ch
             for (int i = yt; i < 2 * U * 512; i += NY) reinterpret_cast<uint4*>(sb + L::M)[i] = make_uint4(0, 0, 0, 0);
             const int rt = yt >> 3, rseg = yt & 7;           // row pass: rows rt and 32 + rt, values 32 q + 4 rseg ..
             const __nv_bfloat16* z = static_cast<const __nv_bfloat16*>(g.z);
-            uint2 zc[2][4], zn[2][4];
-            auto load_z = [&](int c, uint2 (&dst)[2][4]) {
-                const int64_t rem = len_seq - (first + c) * CHUNK_T;
+            // this thread's rows of z and o, one chunk further each time; columns past the
+            // unit's heads (a group's odd head of 64) are left out
+            const int64_t zstep = CHUNK_T * g.z_stride;
+            const __nv_bfloat16* zp = z + (bos + first * CHUNK_T + rt) * g.z_stride + c0 + 4 * rseg;
+            __nv_bfloat16* op = static_cast<__nv_bfloat16*>(g.o) + (size_t)(bos + first * CHUNK_T + rt) * W + c0 + 4 * rseg;
+            const int nq = nh * P / 32;                      // 32-column groups of this unit: 2 or 4
+            const int64_t len_here = len_seq - first * CHUNK_T;
+            uint2 zc[2][4];
+            auto load_z = [&](int c, const __nv_bfloat16* src) {
+                const int rem = (int)(len_here - (int64_t)c * CHUNK_T < CHUNK_T ? len_here - (int64_t)c * CHUNK_T : CHUNK_T);
 #pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    const int t = 32 * hf + rt;
-                    const bool in = z && c < nc && t < rem;
-                    const __nv_bfloat16* src = z + (bos + (first + c) * CHUNK_T + t) * g.z_stride + c0 + 4 * rseg;
+                for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
-                        dst[hf][q] = in && 32 * q + 4 * rseg < nh * P ? __ldg(reinterpret_cast<const uint2*>(src + 32 * q))
-                                                                      : make_uint2(0, 0);
-                }
+                        if (32 * hf + rt < rem && q < nq)
+                            zc[hf][q] = __ldg(reinterpret_cast<const uint2*>(src + 32 * hf * g.z_stride + 32 * q));
             };
+            // the pieces of M this thread builds: row, 8-column piece and head, the same in
+            // every chunk
+            int mi[3];
+#pragma unroll
+            for (int x = 0; x < 3; ++x) {
+                const int i = yt + x * NY, hd = i >= 288, k = i - 288 * hd, pair = k / 9, j0 = k % 9, lo = (pair >> 3) + 1;
+                const int r = j0 < lo ? pair : 63 - pair, j = j0 < lo ? j0 : j0 - lo;
+                mi[x] = i < 288 * nh ? (hd << 16) | (r << 8) | j : -1;
+            }
+            const float skip0 = g.skip ? g.skip[h0] : 0.f, skip1 = g.skip ? g.skip[h0 + nh - 1] : 0.f;
             // M of chunk c: 288 pieces of 8 columns per head (rows r and 63 - r hold nine)
             auto build_m = [&](int c) -> bool {
                 bool bad = !wait_or_abort(b_step + 8 * (c % NSTEP), (uint32_t)(c / NSTEP) & 1u, abort_flag);
                 bad = !wait_or_abort(b_rec + 8 * (c & 1), (uint32_t)(c >> 1) & 1u, abort_flag) || bad;
                 const unsigned char* G = sb + L::REC + (c & 1) * Rec<N>::BYTES + Rec<N>::OFF_G;
                 const int2 ebc = scale_of(c);
-#pragma unroll 1
-                for (int i = yt; i < 288 * nh; i += NY) {
-                    const int hd = i >= 288, k = i - 288 * hd, pair = k / 9, j0 = k % 9, lo = (pair >> 3) + 1;
-                    const int r = j0 < lo ? pair : 63 - pair, j = j0 < lo ? j0 : j0 - lo;
+                float fs[2], ds[2];                          // scale of M and D at that scale, by head
+#pragma unroll
+                for (int hd = 0; hd < U; ++hd) {
+                    const float skip = hd ? skip1 : skip0;
+                    const int em = m_exponent(__float_as_int(step_of(c, min(hd, nh - 1))[ST_EDT]), ebc.x, ebc.y, skip);
+                    fs[hd] = pow2(ebc.x + ebc.y - em);
+                    ds[hd] = skip * pow2(-em);
+                }
+#pragma unroll
+                for (int x = 0; x < 3; ++x) {
+                    if (mi[x] < 0) continue;
+                    const int hd = mi[x] >> 16, r = (mi[x] >> 8) & 255, j = mi[x] & 255;
                     const float* st = step_of(c, hd);
-                    const float skip = g.skip ? __ldg(g.skip + h0 + hd) : 0.f;
-                    const int em = m_exponent(__float_as_int(st[ST_EDT]), ebc.x, ebc.y, skip);
-                    const float f = pow2(ebc.x + ebc.y - em), lr = st[r];
+                    const float f = U == 2 && hd ? fs[1] : fs[0], diag = U == 2 && hd ? ds[1] : ds[0], lr = st[r];
                     const uint32_t off = sw128_off(r, 8 * j, CHUNK_T);
                     const uint4 g4 = *reinterpret_cast<const uint4*>(G + off);
                     const uint32_t gw[4] = {g4.x, g4.y, g4.z, g4.w};
-                    float mv[8];
+                    float ls[8], dt[8];
+                    lds8(st + 8 * j, ls);
+                    lds8(st + ST_DT + 8 * j, dt);
+                    float2 mv[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float2 gg = __half22float2(*reinterpret_cast<const __half2*>(&gw[e]));
-                        const int s = 8 * j + 2 * e;
-                        const float2 ls = *reinterpret_cast<const float2*>(st + s), dt = *reinterpret_cast<const float2*>(st + ST_DT + s);
-                        mv[2 * e] = s <= r ? gg.x * ex2(lr - ls.x) * (dt.x * f) : 0.f;
-                        mv[2 * e + 1] = s + 1 <= r ? gg.y * ex2(lr - ls.y) * (dt.y * f) : 0.f;
-                        if (s == r) mv[2 * e] += skip * pow2(-em);
-                        if (s + 1 == r) mv[2 * e + 1] += skip * pow2(-em);
+                        const float2 d = __ffma2_rn(make_float2(ls[2 * e], ls[2 * e + 1]), make_float2(-1.f, -1.f), make_float2(lr, lr));
+                        const float2 k = __fmul2_rn(__fmul2_rn(make_float2(dt[2 * e], dt[2 * e + 1]), make_float2(f, f)),
+                                                    make_float2(ex2(d.x), ex2(d.y)));
+                        mv[e] = __fmul2_rn(__half22float2(*reinterpret_cast<const __half2*>(&gw[e])), k);
+                    }
+                    // nothing past s = r, D on s = r (selects, not an index into mv: that would put
+                    // it in local memory)
+                    if (j == r >> 3) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int s = 8 * j + 2 * e;
+                            mv[e].x = s > r ? 0.f : s == r ? mv[e].x + diag : mv[e].x;
+                            mv[e].y = s + 1 > r ? 0.f : s + 1 == r ? mv[e].y + diag : mv[e].y;
+                        }
                     }
                     *reinterpret_cast<uint4*>(sb + L::M + ((c & 1) * U + hd) * 8192 + off) =
-                        make_uint4(pack2(mv[0], mv[1]), pack2(mv[2], mv[3]), pack2(mv[4], mv[5]), pack2(mv[6], mv[7]));
+                        make_uint4(pack2(mv[0].x, mv[0].y), pack2(mv[1].x, mv[1].y), pack2(mv[2].x, mv[2].y), pack2(mv[3].x, mv[3].y));
                 }
                 ptx::fence_async_smem();
                 if (ptx::bar_sync_or(BAR_Y, NY, bad)) return false;
@@ -445,15 +499,15 @@ __global__ void __launch_bounds__(NT, 1) chunk_kernel(const __grid_constant__ Ch
                 return true;
             };
             float* ys = reinterpret_cast<float*>(sb + L::Y);
-            __nv_bfloat16* o = static_cast<__nv_bfloat16*>(g.o);
-            load_z(0, zc);
             bool go = true;
             ptx::bar_sync_or(BAR_Y, NY, false);              // (the zeros precede every piece)
             if (nc > 0) go = build_m(0);
 #pragma unroll 1
             for (int c = 0; go && c < nc; ++c) {
                 if (c + 1 < nc && !build_m(c + 1)) break;
-                load_z(c + 1, zn);
+                // (behind M, whose registers would spill these loads and so wait for them)
+                if (z) load_z(c, zp);
+                zp += zstep;
                 const bool bad = !wait_or_abort(b_done, (uint32_t)c & 1u, abort_flag);
                 if (ptx::bar_sync_or(BAR_Y, NY, bad)) break; // (and the rows of the chunk before are written)
                 ptx::tc_fence_after();
@@ -461,49 +515,59 @@ __global__ void __launch_bounds__(NT, 1) chunk_kernel(const __grid_constant__ Ch
                     const int b3 = c % 3, th = half;
                     const float si = reinterpret_cast<const float*>(sb + L::SI)[b3 * 128 + ch];
                     const float sx = reinterpret_cast<const float*>(sb + L::SX)[b3 * 128 + ch];
+                    const float2 si2 = make_float2(si, si), sx2 = make_float2(sx, sx);
                     const float4* el = reinterpret_cast<const float4*>(step_of(c, min(ch / P, nh - 1)) + ST_EL + 32 * th);
-                    float di[32], dh[32];
-                    ptx::tmem_ld32(tlane + TM_DI + 32 * th, di);
-                    ptx::tmem_ld32(tlane + TM_D + 64 * (ch / P) + 32 * th, dh);
+                    // (16 columns at a time: with 32 the thread's registers spill)
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) {
-                        const float4 e4 = el[q];
-                        const float ev[4] = {e4.x, e4.y, e4.z, e4.w};
+                    for (int j = 0; j < 2; ++j) {
+                        float di[16], dh[16];
+                        ptx::tmem_ld16_nw(tlane + TM_DI + 32 * th + 16 * j, di);
+                        ptx::tmem_ld16_nw(tlane + TM_D + 64 * (ch / P) + 32 * th + 16 * j, dh);
+                        ptx::tmem_wait_ld(di, dh);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            ys[(32 * th + 4 * q + e) * LDYS + ch] = fmaf(di[4 * q + e], si * ev[e], sx * dh[4 * q + e]);
+                        for (int q = 0; q < 4; ++q) {
+                            const float4 e4 = el[4 * j + q];
+                            float* yr = ys + (32 * th + 16 * j + 4 * q) * LDYS + ch;
+#pragma unroll
+                            for (int e = 0; e < 4; e += 2) {
+                                const float2 ev = e ? make_float2(e4.z, e4.w) : make_float2(e4.x, e4.y);
+                                const float2 y = __ffma2_rn(make_float2(di[4 * q + e], di[4 * q + e + 1]), __fmul2_rn(ev, si2),
+                                                            __fmul2_rn(make_float2(dh[4 * q + e], dh[4 * q + e + 1]), sx2));
+                                yr[e * LDYS] = y.x;
+                                yr[(e + 1) * LDYS] = y.y;
+                            }
+                        }
                     }
                     ptx::tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(b_dfree);     // D and this chunk's scales are read
                 }
                 ptx::bar_sync_or(BAR_Y, NY, false);
-                const int64_t rem = len_seq - (first + c) * CHUNK_T;
+                const int rem = (int)(len_here - (int64_t)c * CHUNK_T < CHUNK_T ? len_here - (int64_t)c * CHUNK_T : CHUNK_T);
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {
-                    const int t = 32 * hf + rt;
-                    if (t < rem) {
-                        __nv_bfloat16* dst = o + (size_t)(bos + (first + c) * CHUNK_T + t) * W + c0 + 4 * rseg;
+                    float4 y[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        y[q] = *reinterpret_cast<const float4*>(ys + (32 * hf + rt) * LDYS + 32 * q + 4 * rseg);
+                    if (z) {
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
-                            if (32 * q + 4 * rseg >= nh * P) continue;
-                            float4 y = *reinterpret_cast<const float4*>(ys + t * LDYS + 32 * q + 4 * rseg);
-                            if (z) {
-                                const __nv_bfloat162* zz = reinterpret_cast<const __nv_bfloat162*>(&zc[hf][q]);
-                                const float2 z0 = __bfloat1622float2(zz[0]), z1 = __bfloat1622float2(zz[1]);
-                                y.x *= silu(z0.x); y.y *= silu(z0.y);
-                                y.z *= silu(z1.x); y.w *= silu(z1.y);
-                            }
-                            const __nv_bfloat162 o0 = __floats2bfloat162_rn(y.x, y.y), o1 = __floats2bfloat162_rn(y.z, y.w);
-                            *reinterpret_cast<uint2*>(dst + 32 * q) =
-                                make_uint2(*reinterpret_cast<const uint32_t*>(&o0), *reinterpret_cast<const uint32_t*>(&o1));
+                            const __nv_bfloat162* zz = reinterpret_cast<const __nv_bfloat162*>(&zc[hf][q]);
+                            const float2 a = __fmul2_rn(silu2(__bfloat1622float2(zz[0])), make_float2(y[q].x, y[q].y));
+                            const float2 b = __fmul2_rn(silu2(__bfloat1622float2(zz[1])), make_float2(y[q].z, y[q].w));
+                            y[q] = make_float4(a.x, a.y, b.x, b.y);
                         }
                     }
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const __nv_bfloat162 o0 = __floats2bfloat162_rn(y[q].x, y[q].y), o1 = __floats2bfloat162_rn(y[q].z, y[q].w);
+                        if (32 * hf + rt < rem && q < nq)
+                            *reinterpret_cast<uint2*>(op + (size_t)(32 * hf) * W + 32 * q) =
+                                make_uint2(*reinterpret_cast<const uint32_t*>(&o0), *reinterpret_cast<const uint32_t*>(&o1));
+                    }
                 }
-#pragma unroll
-                for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) zc[hf][q] = zn[hf][q];
+                op += (size_t)CHUNK_T * W;
             }
         }
     } else {
@@ -518,29 +582,32 @@ __global__ void __launch_bounds__(NT, 1) chunk_kernel(const __grid_constant__ Ch
             if (!LITE && c > 0 && !wait_or_abort(b_dfree, (uint32_t)(c - 1) & 1u, abort_flag)) break;
             if (!wait_or_abort(b_xready, (uint32_t)c & 1u, abort_flag)) break;
             ptx::tc_fence_after();
+            // descriptors of a tile differ from its first one by their start address (in 16 bytes)
             if (!LITE) {
+                const uint64_t dc = ptx::sdesc_sw128(rec + Rec<N>::OFF_C);
 #pragma unroll
                 for (int kk = 0; kk < N / 16; ++kk)
-                    ptx::mma_f16_ta(tmem + TM_DI, tmem + TM_SH + 8 * kk,
-                                    ptx::sdesc_sw128(rec + Rec<N>::OFF_C + (kk >> 2) * 8192 + (kk & 3) * 32), ID64, kk > 0);
+                    ptx::mma_f16_ta(tmem + TM_DI, tmem + TM_SH + 8 * kk, dc + (kk >> 2) * 512 + (kk & 3) * 2, ID64, kk > 0);
             }
+            const uint64_t db = ptx::sdesc_sw128(rec);
 #pragma unroll
-            for (int term = 0; term < 3; ++term) {           // hi hi, hi lo, lo hi
-                const uint32_t at = term == 2 ? TM_XL : TM_XH, bt = rec + (term == 1 ? Rec<N>::OFF_LO : 0);
+            for (int term = 0; term < 3; ++term)             // hi hi, hi lo, lo hi
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    ptx::mma_f16_ta(tmem + TM_S, tmem + at + 8 * kk, ptx::sdesc_sw128(bt + kk * 32), IDN, 1);
-            }
+                    ptx::mma_f16_ta(tmem + TM_S, tmem + (term == 2 ? TM_XL : TM_XH) + 8 * kk,
+                                    db + (term == 1 ? Rec<N>::OFF_LO / 16 : 0) + kk * 2, IDN, 1);
+            ptx::mma_commit(b_sdone);
             if (!LITE) {
                 // (an abort here leaves MMAs in flight: the drain below covers them)
                 if (!wait_or_abort(b_m + 8 * (c & 1), (uint32_t)(c >> 1) & 1u, abort_flag)) break;
                 ptx::tc_fence_after();
-#pragma unroll 1
-                for (int hd = 0; hd < nh; ++hd)
+                const uint64_t dm = ptx::sdesc_sw128(base + L::M + (c & 1) * U * 8192);
+#pragma unroll
+                for (int hd = 0; hd < U; ++hd)
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        ptx::mma_f16_ta(tmem + TM_D + 64 * hd, tmem + TM_XF + 8 * kk,
-                                        ptx::sdesc_sw128(base + L::M + ((c & 1) * U + hd) * 8192 + kk * 32), ID64, kk > 0);
+                        if (hd < nh)
+                            ptx::mma_f16_ta(tmem + TM_D + 64 * hd, tmem + TM_XF + 8 * kk, dm + hd * 512 + kk * 2, ID64, kk > 0);
             }
             ptx::mma_commit(b_done);
         }

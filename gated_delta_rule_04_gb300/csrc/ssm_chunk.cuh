@@ -33,12 +33,14 @@ inline size_t rec_bytes(int N) { return N == 64 ? Rec<64>::BYTES : Rec<128>::BYT
 //   [64, 128)   dt
 //   [128, 192)  2^(sum_{s > t} l_s) dt_t: the token's weight in the end state, from a
 //               suffix sum (a difference of long prefix sums would cost the fp32
-//               state its last digits)
+//               state its last digits); token t at w_at(t), next to token t + 16
 //   [192, 256)  2^(sum_{s <= t} l_s)
 //   [256]       2^(sum of all l_s), [257] exponent of the largest dt (int), [258] sum of l_s
 constexpr int STEP_FLOATS = 260;
 constexpr int ST_DT = 64, ST_W = 128, ST_EL = 192, ST_DEC = 256, ST_EDT = 257, ST_LOG = 258;
 constexpr float LAM_MIN = -40.f;
+// The X group takes tokens t and t + 16 of a 32-token half as one packed pair.
+__host__ __device__ constexpr int w_at(int t) { return (t & 32) + 2 * (t & 15) + ((t >> 4) & 1); }
 
 // Exponent e with 2^e <= x < 2^(e+1), clamped to +-40 (so that sums of a few
 // exponents stay inside fp32's range; beyond it precision goes before range).
@@ -51,12 +53,6 @@ __device__ __forceinline__ float pow2(int e) {
     e = e < -126 ? -126 : e > 127 ? 127 : e;
     return __uint_as_float((uint32_t)(e + 127) << 23);
 }
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 struct ChunkArgs {
     CUtensorMap map67, map64;     // xbc rows: boxes of 67 and 64 rows x 128 channels
     PrefillArgs g;

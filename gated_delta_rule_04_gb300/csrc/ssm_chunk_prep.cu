@@ -65,7 +65,8 @@ __device__ void steps(const ChunkArgs& a, const ChunkDesc d, int chunk, int hb) 
         float* out = a.step + ((size_t)chunk * g.H + h) * STEP_FLOATS;
         *reinterpret_cast<float2*>(out + 2 * lane) = make_float2(cb + c0, cb + c0 + c1);
         *reinterpret_cast<float2*>(out + ST_DT + 2 * lane) = make_float2(dt[0], dt[1]);
-        *reinterpret_cast<float2*>(out + ST_W + 2 * lane) = make_float2(ex2(l[1] + sa) * dt[0], ex2(sa) * dt[1]);
+        out[ST_W + w_at(2 * lane)] = ex2(l[1] + sa) * dt[0];
+        out[ST_W + w_at(2 * lane + 1)] = ex2(sa) * dt[1];
         *reinterpret_cast<float2*>(out + ST_EL + 2 * lane) = make_float2(ex2(pb + l[0]), ex2(pb + l[0] + l[1]));
         if (lane == 0)
             *reinterpret_cast<float4*>(out + ST_DEC) = make_float4(ex2(end), __int_as_float(expo(top)), end, 0.f);
