@@ -46,13 +46,18 @@ namespace kda {
 namespace ssm {
 namespace {
 
-constexpr int NT = 640;                    // 8 X warps, 8 Y warps, a warpgroup whose first thread issues the MMAs
-// register split: 96 a thread at launch (65536 / 640), moved between the warpgroups
-constexpr int REG_LAUNCH = 96, REG_X = 104, REG_Y = 104, REG_ISSUE = 64;   // (no spills in any variant)
-static_assert(256 * REG_X + 256 * REG_Y + 128 * REG_ISSUE <= NT * REG_LAUNCH && REG_X % 8 == 0 && REG_Y % 8 == 0,
+constexpr int NT = 640;                    // 8 X warps, 8 Y warps, one issuing warp, 3 M warps
+// register split: 96 a thread at launch (65536 / 640, in eights of a warp's share);
+// the issue and M warpgroup gives to the X group, the Y group keeps its own
+constexpr int REG_LAUNCH = 96, REG_X = 112, REG_ISSUE = 64;   // (no spills in the full pass)
+static_assert(256 * REG_X + 256 * REG_LAUNCH + 128 * REG_ISSUE <= NT * REG_LAUNCH && REG_X % 8 == 0,
               "the split must fit the launch's registers, or setmaxnreg.inc waits forever");
+static_assert(REG_X > REG_LAUNCH && REG_ISSUE < REG_LAUNCH && REG_ISSUE >= 24,
+              "setmaxnreg.inc takes no smaller count than the current one, .dec no larger");
 constexpr int NX = 256, NY = 256;
-constexpr int BAR_X = 1, BAR_Y = 2;        // named barriers
+constexpr int NM = 96;                     // M threads: warps 17-19
+constexpr int BAR_X = 1, BAR_Y = 2, BAR_M = 3;   // named barriers
+static_assert(288 % NM == 0, "M pieces per thread");
 constexpr uint32_t TM_S = 0, TM_SH = 128, TM_XF = 192, TM_XH = 224, TM_XL = 256, TM_DI = 288, TM_D = 352;
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint64_t WAIT_LIMIT_NS = 2000000000ull;
@@ -137,10 +142,10 @@ __global__ void __launch_bounds__(NT, 1) chunk_kernel(const __grid_constant__ Ch
     unsigned char* sb = smem_raw + (base - raw);
     const uint32_t bars = base + L::BAR;
     const uint32_t b_x = bars, b_step = bars + 16, b_rec = bars + 56, b_m = bars + 72;   // [2], [NSTEP], [2], [2]
-    const uint32_t b_xready = bars + 88, b_done = bars + 96, b_dfree = bars + 104, b_drain = bars + 112, b_sdone = bars + 120;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sb + L::BAR + 128);
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(sb + L::BAR + 132);
-    volatile int* issued = reinterpret_cast<volatile int*>(sb + L::BAR + 136);   // loads issued: [0] x and steps, [1] records
+    const uint32_t b_xready = bars + 88, b_done = bars + 96, b_dfree = bars + 104, b_drain = bars + 112, b_sdone = bars + 120, b_mfree = bars + 128;   // b_mfree: [2]
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sb + L::BAR + 160);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(sb + L::BAR + 164);
+    volatile int* issued = reinterpret_cast<volatile int*>(sb + L::BAR + 168);   // loads issued: [0] x and steps, [1] records
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     if (warp == 16) {
@@ -152,6 +157,7 @@ __global__ void __launch_bounds__(NT, 1) chunk_kernel(const __grid_constant__ Ch
             ptx::mbar_init(b_x + 8 * i, 1);
             ptx::mbar_init(b_rec + 8 * i, 1);
             ptx::mbar_init(b_m + 8 * i, 1);
+            ptx::mbar_init(b_mfree + 8 * i, 1);
         }
         for (int i = 0; i < NSTEP; ++i) ptx::mbar_init(b_step + 8 * i, 1);
         ptx::mbar_init(b_xready, 1);
@@ -296,7 +302,7 @@ __global__ void __launch_bounds__(NT, 1) chunk_kernel(const __grid_constant__ Ch
                     x0 = x1; x1 = x2; x2 = x3;
                 }
             }
-            // rows past the sequence hold whatever lies there: out before a pair shares its reciprocal
+            // rows past the sequence hold whatever lies there
             if (len < CHUNK_T) {
 #pragma unroll
                 for (int t = 0; t < 16; ++t) {
@@ -412,11 +418,8 @@ __global__ void __launch_bounds__(NT, 1) chunk_kernel(const __grid_constant__ Ch
         }
     } else if (warp < 16) {
         // ================================ Y group ================================
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REG_Y));
         if constexpr (!LITE) {
             const int yt = tid - NX, ch = 32 * quarter + lane;
-            // M tiles start zero: only pieces up to the diagonal are written below
-            for (int i = yt; i < 2 * U * 512; i += NY) reinterpret_cast<uint4*>(sb + L::M)[i] = make_uint4(0, 0, 0, 0);
             const int rt = yt >> 3, rseg = yt & 7;           // row pass: rows rt and 32 + rt, values 32 q + 4 rseg ..
             const __nv_bfloat16* z = static_cast<const __nv_bfloat16*>(g.z);
             // this thread's rows of z and o, one chunk further each time; columns past the
@@ -436,76 +439,9 @@ __global__ void __launch_bounds__(NT, 1) chunk_kernel(const __grid_constant__ Ch
                         if (32 * hf + rt < rem && q < nq)
                             zc[hf][q] = __ldg(reinterpret_cast<const uint2*>(src + 32 * hf * g.z_stride + 32 * q));
             };
-            // the pieces of M this thread builds: row, 8-column piece and head, the same in
-            // every chunk
-            int mi[3];
-#pragma unroll
-            for (int x = 0; x < 3; ++x) {
-                const int i = yt + x * NY, hd = i >= 288, k = i - 288 * hd, pair = k / 9, j0 = k % 9, lo = (pair >> 3) + 1;
-                const int r = j0 < lo ? pair : 63 - pair, j = j0 < lo ? j0 : j0 - lo;
-                mi[x] = i < 288 * nh ? (hd << 16) | (r << 8) | j : -1;
-            }
-            const float skip0 = g.skip ? g.skip[h0] : 0.f, skip1 = g.skip ? g.skip[h0 + nh - 1] : 0.f;
-            // M of chunk c: 288 pieces of 8 columns per head (rows r and 63 - r hold nine)
-            auto build_m = [&](int c) -> bool {
-                bool bad = !wait_or_abort(b_step + 8 * (c % NSTEP), (uint32_t)(c / NSTEP) & 1u, abort_flag);
-                bad = !wait_or_abort(b_rec + 8 * (c & 1), (uint32_t)(c >> 1) & 1u, abort_flag) || bad;
-                const unsigned char* G = sb + L::REC + (c & 1) * Rec<N>::BYTES + Rec<N>::OFF_G;
-                const int2 ebc = scale_of(c);
-                float fs[2], ds[2];                          // scale of M and D at that scale, by head
-#pragma unroll
-                for (int hd = 0; hd < U; ++hd) {
-                    const float skip = hd ? skip1 : skip0;
-                    const int em = m_exponent(__float_as_int(step_of(c, min(hd, nh - 1))[ST_EDT]), ebc.x, ebc.y, skip);
-                    fs[hd] = pow2(ebc.x + ebc.y - em);
-                    ds[hd] = skip * pow2(-em);
-                }
-#pragma unroll
-                for (int x = 0; x < 3; ++x) {
-                    if (mi[x] < 0) continue;
-                    const int hd = mi[x] >> 16, r = (mi[x] >> 8) & 255, j = mi[x] & 255;
-                    const float* st = step_of(c, hd);
-                    const float f = U == 2 && hd ? fs[1] : fs[0], diag = U == 2 && hd ? ds[1] : ds[0], lr = st[r];
-                    const uint32_t off = sw128_off(r, 8 * j, CHUNK_T);
-                    const uint4 g4 = *reinterpret_cast<const uint4*>(G + off);
-                    const uint32_t gw[4] = {g4.x, g4.y, g4.z, g4.w};
-                    float ls[8], dt[8];
-                    lds8(st + 8 * j, ls);
-                    lds8(st + ST_DT + 8 * j, dt);
-                    float2 mv[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float2 d = __ffma2_rn(make_float2(ls[2 * e], ls[2 * e + 1]), make_float2(-1.f, -1.f), make_float2(lr, lr));
-                        const float2 k = __fmul2_rn(__fmul2_rn(make_float2(dt[2 * e], dt[2 * e + 1]), make_float2(f, f)),
-                                                    make_float2(ex2(d.x), ex2(d.y)));
-                        mv[e] = __fmul2_rn(__half22float2(*reinterpret_cast<const __half2*>(&gw[e])), k);
-                    }
-                    // nothing past s = r, D on s = r (selects, not an index into mv: that would put
-                    // it in local memory)
-                    if (j == r >> 3) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int s = 8 * j + 2 * e;
-                            mv[e].x = s > r ? 0.f : s == r ? mv[e].x + diag : mv[e].x;
-                            mv[e].y = s + 1 > r ? 0.f : s + 1 == r ? mv[e].y + diag : mv[e].y;
-                        }
-                    }
-                    *reinterpret_cast<uint4*>(sb + L::M + ((c & 1) * U + hd) * 8192 + off) =
-                        make_uint4(pack2(mv[0].x, mv[0].y), pack2(mv[1].x, mv[1].y), pack2(mv[2].x, mv[2].y), pack2(mv[3].x, mv[3].y));
-                }
-                ptx::fence_async_smem();
-                if (ptx::bar_sync_or(BAR_Y, NY, bad)) return false;
-                if (yt == 0) mbar_arrive(b_m + 8 * (c & 1));
-                return true;
-            };
             float* ys = reinterpret_cast<float*>(sb + L::Y);
-            bool go = true;
-            ptx::bar_sync_or(BAR_Y, NY, false);              // (the zeros precede every piece)
-            if (nc > 0) go = build_m(0);
 #pragma unroll 1
-            for (int c = 0; go && c < nc; ++c) {
-                if (c + 1 < nc && !build_m(c + 1)) break;
-                // (behind M, whose registers would spill these loads and so wait for them)
+            for (int c = 0; c < nc; ++c) {
                 if (z) load_z(c, zp);
                 zp += zstep;
                 const bool bad = !wait_or_abort(b_done, (uint32_t)c & 1u, abort_flag);
@@ -571,9 +507,71 @@ __global__ void __launch_bounds__(NT, 1) chunk_kernel(const __grid_constant__ Ch
             }
         }
     } else {
-        // ============================ MMA issue (one thread) ======================
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_ISSUE));
-        if (tid == 512) {
+        if (warp > 16) {
+            // ============================== M group ==============================
+            if constexpr (!LITE) {
+                const int mt = tid - NT + NM;
+                // M tiles start zero: only pieces up to the diagonal are written below
+                for (int i = mt; i < 2 * U * 512; i += NM) reinterpret_cast<uint4*>(sb + L::M)[i] = make_uint4(0, 0, 0, 0);
+                ptx::bar_sync_or(BAR_M, NM, false);
+                const float skip0 = g.skip ? g.skip[h0] : 0.f, skip1 = g.skip ? g.skip[h0 + nh - 1] : 0.f;
+#pragma unroll 1
+                for (int c = 0; c < nc; ++c) {
+                    bool bad = !wait_or_abort(b_step + 8 * (c % NSTEP), (uint32_t)(c / NSTEP) & 1u, abort_flag);
+                    bad = !wait_or_abort(b_rec + 8 * (c & 1), (uint32_t)(c >> 1) & 1u, abort_flag) || bad;
+                    // the intra MMAs of chunk c - 2 have read this buffer
+                    if (c > 1) bad = !wait_or_abort(b_mfree + 8 * (c & 1), (uint32_t)((c >> 1) - 1) & 1u, abort_flag) || bad;
+                    const unsigned char* G = sb + L::REC + (c & 1) * Rec<N>::BYTES + Rec<N>::OFF_G;
+                    const int2 ebc = scale_of(c);
+                    // 288 pieces of 8 columns per head: rows r and 63 - r hold nine
+#pragma unroll
+                    for (int hd = 0; hd < U; ++hd) {
+                        if (hd >= nh) continue;
+                        const float* st = step_of(c, hd);
+                        const float skip = hd ? skip1 : skip0;
+                        const int em = m_exponent(__float_as_int(st[ST_EDT]), ebc.x, ebc.y, skip);
+                        const float f = pow2(ebc.x + ebc.y - em), diag = skip * pow2(-em);
+#pragma unroll
+                        for (int x = 0; x < 288 / NM; ++x) {
+                            const int k = mt + x * NM, pair = k / 9, j0 = k % 9, lo = (pair >> 3) + 1;
+                            const int r = j0 < lo ? pair : 63 - pair, j = j0 < lo ? j0 : j0 - lo;
+                            const uint32_t off = sw128_off(r, 8 * j, CHUNK_T);
+                            const uint4 g4 = *reinterpret_cast<const uint4*>(G + off);
+                            const uint32_t gw[4] = {g4.x, g4.y, g4.z, g4.w};
+                            const float lr = st[r];
+                            float ls[8], dt[8];
+                            lds8(st + 8 * j, ls);
+                            lds8(st + ST_DT + 8 * j, dt);
+                            float2 mv[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const float2 d = __ffma2_rn(make_float2(ls[2 * e], ls[2 * e + 1]), make_float2(-1.f, -1.f), make_float2(lr, lr));
+                                const float2 k2 = __fmul2_rn(__fmul2_rn(make_float2(dt[2 * e], dt[2 * e + 1]), make_float2(f, f)),
+                                                             make_float2(ex2(d.x), ex2(d.y)));
+                                mv[e] = __fmul2_rn(__half22float2(*reinterpret_cast<const __half2*>(&gw[e])), k2);
+                            }
+                            // nothing past s = r, D on s = r (selects, not an index into mv: that
+                            // would put it in local memory)
+                            if (j == r >> 3) {
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const int s = 8 * j + 2 * e;
+                                    mv[e].x = s > r ? 0.f : s == r ? mv[e].x + diag : mv[e].x;
+                                    mv[e].y = s + 1 > r ? 0.f : s + 1 == r ? mv[e].y + diag : mv[e].y;
+                                }
+                            }
+                            *reinterpret_cast<uint4*>(sb + L::M + ((c & 1) * U + hd) * 8192 + off) = make_uint4(
+                                pack2(mv[0].x, mv[0].y), pack2(mv[1].x, mv[1].y), pack2(mv[2].x, mv[2].y), pack2(mv[3].x, mv[3].y));
+                        }
+                    }
+                    ptx::fence_async_smem();
+                    if (ptx::bar_sync_or(BAR_M, NM, bad)) break;
+                    if (mt == 0) mbar_arrive(b_m + 8 * (c & 1));
+                }
+            }
+        } else if (lane == 0) {
+        // ============================ MMA issue (one thread) ======================
         constexpr uint32_t ID64 = ptx::idesc_f16_f32(128, 64), IDN = ptx::idesc_f16_f32(128, N);
 #pragma unroll 1
         for (int c = 0; c < nc; ++c) {
@@ -608,6 +606,7 @@ __global__ void __launch_bounds__(NT, 1) chunk_kernel(const __grid_constant__ Ch
                     for (int kk = 0; kk < 4; ++kk)
                         if (hd < nh)
                             ptx::mma_f16_ta(tmem + TM_D + 64 * hd, tmem + TM_XF + 8 * kk, dm + hd * 512 + kk * 2, ID64, kk > 0);
+                ptx::mma_commit(b_mfree + 8 * (c & 1));
             }
             ptx::mma_commit(b_done);
         }

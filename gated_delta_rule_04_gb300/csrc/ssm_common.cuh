@@ -47,17 +47,20 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// Two SiLUs at once (packed fp32 arithmetic), with one reciprocal of the
-// product of the denominators, each at most 1 + 2^60: three special-function
-// operations instead of four.  (Below x = -41.6 the result is x 2^-60 instead
-// of something smaller still.)
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Two SiLUs, the arithmetic around the special functions packed.  (One
+// reciprocal for both denominators saves a special-function operation and
+// costs five others; those units are the least used ones here.)
 __device__ __forceinline__ float2 silu2(float2 x) {
     constexpr float L = -1.4426950408889634f;
     const float2 t = __fmul2_rn(x, make_float2(L, L));
-    const float2 d = __fadd2_rn(make_float2(ex2(fminf(t.x, 60.f)), ex2(fminf(t.y, 60.f))), make_float2(1.f, 1.f));
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d.x * d.y));
-    return __fmul2_rn(x, __fmul2_rn(make_float2(d.y, d.x), make_float2(r, r)));
+    const float2 d = __fadd2_rn(make_float2(ex2(t.x), ex2(t.y)), make_float2(1.f, 1.f));
+    return __fmul2_rn(x, make_float2(rcp(d.x), rcp(d.y)));
 }
 
 cudaError_t launch_scan(const PrefillArgs& a, int io_bf16, cudaStream_t s);
