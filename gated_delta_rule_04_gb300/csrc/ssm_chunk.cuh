@@ -68,6 +68,7 @@ struct ChunkArgs {
     float* ltot;                  // [n_seqs][np][H]
     int32_t np, lp;
     int32_t n_chunks, units, upg; // units of 128 channels, in all and per group
+    int32_t prep_blocks;          // blocks of the preparation per chunk (set by launch_chunk_prep)
 };
 
 cudaError_t launch_chunk_prep(const ChunkArgs& a, cudaStream_t s);
