@@ -342,38 +342,46 @@ def kda_workspace_status(workspace, stream=None) -> int:
 
 # ---- draft trees and the state space mixer -------------------------------------------
 
+# These run before every launch of a serving loop's smallest calls, whose kernels take a
+# few microseconds: one comparison each where the argument is right.
+
 def _shaped(name, t, dtype, shape):
-    """A dense CUDA tensor of this type and shape, or ValueError (None in ``shape`` is any size)."""
-    if t.dtype != dtype or t.dim() != len(shape) or any(w is not None and s != w for s, w in zip(t.shape, shape)):
-        raise ValueError(f"{name}: expected {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous tensor")
-    return t
+    """The address of a dense CUDA tensor of this type and shape, or ValueError."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError(f"{name}: expected a contiguous CUDA tensor {dtype} {list(shape)}, got "
+                         f"{'' if t.is_contiguous() else 'non-contiguous '}{t.dtype} {list(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _pool(name, t, dtype, rest):
+    """(address, slots) of a dense CUDA tensor [slots][*rest] of this type."""
+    n = t.shape[0] if t.dim() else 0
+    return _shaped(name, t, dtype, (n, *rest)), n
 
 
 def _rows(name, t, dtype, n, width):
-    """Row stride in elements of a [n][width] tensor whose rows may lie apart."""
-    if t.dtype != dtype or tuple(t.shape) != (n, width):
-        raise ValueError(f"{name}: expected {dtype} {[n, width]}, got {t.dtype} {list(t.shape)}")
-    if width > 1 and t.stride(1) != 1:
+    """(address, row stride in elements) of a [n][width] CUDA tensor whose rows may lie apart."""
+    if t.dtype is not dtype or t.shape != (n, width) or not t.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA tensor {dtype} {[n, width]}, got {t.dtype} {list(t.shape)} on {t.device}")
+    stride, inner = t.stride()
+    if width > 1 and inner != 1:
         raise ValueError(f"{name}: the elements of a row have to lie side by side")
     if n <= 1:
-        return 0
-    if t.stride(0) < width:
-        raise ValueError(f"{name}: rows overlap (stride {t.stride(0)} < {width})")
-    return t.stride(0)
+        return t.data_ptr(), 0
+    if stride < width:
+        raise ValueError(f"{name}: rows overlap (stride {stride} < {width})")
+    return t.data_ptr(), stride
 
 
 def _call(name, dev, f, *args, stream=None):
     """Calls ``f`` with ``dev`` current, on ``stream`` (default: that device's current stream)."""
     import torch
-    if dev.type != "cuda":
-        raise ValueError(f"{name}: expected CUDA tensors, got {dev}")
-    if dev.index is not None and dev.index != torch.cuda.current_device():
-        with torch.cuda.device(dev):
+    index = dev.index
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(index):
             st = f(*args, _stream(stream))
     else:
-        st = f(*args, _stream(stream))
+        st = f(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream))
     if st != KDA_OK:
         raise KdaError(st, name)
 
@@ -397,18 +405,16 @@ def kda_decode_tree(params: Params, q, k, v, z, b, gout, parents, S, ring, slots
     t = _io_torch(params.io_dtype)
     if q.dim() != 3:
         raise ValueError(f"q: expected [n][n_nodes][H*128], got {list(q.shape)}")
-    n, R, H = int(q.shape[0]), int(q.shape[1]), params.num_heads
-    for name, x in (("q", q), ("k", k), ("v", v), ("z", z), ("gout", gout)):
-        _shaped(name, x, t, (n, R, H * 128))
-    _shaped("b", b, t, (n, R, H))
-    _shaped("parents", parents, torch.int32, (n, R))
-    _shaped("S", S, torch.float32, (None, H, 128, 128))
-    _shaped("ring", ring, t, (S.shape[0], 3, 3, H * 128))
-    if slots is not None:
-        _shaped("slots", slots, torch.int32, (n,))
-    o = torch.empty_like(q) if o is None else _shaped("o", o, t, (n, R, H * 128))
-    _call("kda_decode_tree", q.device, lib().kda_decode_tree, params.ref, n, R, _ptr(q), _ptr(k), _ptr(v), _ptr(z), _ptr(b),
-          _ptr(gout), _ptr(parents), _ptr(slots), int(S.shape[0]), _ptr(S), _ptr(ring), _ptr(o), stream=stream)
+    n, R, _ = q.shape
+    H = params.num_heads
+    rows = (n, R, H * 128)
+    S_p, slots_n = _pool("S", S, torch.float32, (H, 128, 128))
+    args = (params.ref, n, R, _shaped("q", q, t, rows), _shaped("k", k, t, rows), _shaped("v", v, t, rows), _shaped("z", z, t, rows),
+            _shaped("b", b, t, (n, R, H)), _shaped("gout", gout, t, rows), _shaped("parents", parents, torch.int32, (n, R)),
+            None if slots is None else _shaped("slots", slots, torch.int32, (n,)), slots_n, S_p,
+            _shaped("ring", ring, t, (slots_n, 3, 3, H * 128)))
+    o = torch.empty_like(q) if o is None else o
+    _call("kda_decode_tree", q.device, lib().kda_decode_tree, *args, _shaped("o", o, t, rows), stream=stream)
     return o
 
 
@@ -422,23 +428,19 @@ def kda_tree_commit(params: Params, q, k, v, z, b, path, path_len, S_in, ring_in
     t = _io_torch(params.io_dtype)
     if q.dim() != 3 or path.dim() != 2:
         raise ValueError(f"q, path: expected [n][n_nodes][H*128] and [n][max_len], got {list(q.shape)}, {list(path.shape)}")
-    n, R, H, m = int(q.shape[0]), int(q.shape[1]), params.num_heads, int(path.shape[1])
+    n, R, _ = q.shape
+    H, m = params.num_heads, path.shape[1]
     S_out = S_in if S_out is None else S_out
     ring_out = ring_in if ring_out is None else ring_out
-    for name, x in (("q", q), ("k", k), ("v", v), ("z", z)):
-        _shaped(name, x, t, (n, R, H * 128))
-    _shaped("b", b, t, (n, R, H))
-    _shaped("path", path, torch.int32, (n, m))
-    _shaped("path_len", path_len, torch.int32, (n,))
-    for name, x in (("S_in", S_in), ("S_out", S_out)):
-        _shaped(name, x, torch.float32, (S_in.shape[0], H, 128, 128))
-    for name, x in (("ring_in", ring_in), ("ring_out", ring_out)):
-        _shaped(name, x, t, (S_in.shape[0], 3, 3, H * 128))
-    if slots is not None:
-        _shaped("slots", slots, torch.int32, (n,))
-    _call("kda_tree_commit", q.device, lib().kda_tree_commit, params.ref, n, R, _ptr(q), _ptr(k), _ptr(v), _ptr(z), _ptr(b),
-          _ptr(path), _ptr(path_len), m, _ptr(slots), int(S_in.shape[0]), _ptr(S_in), _ptr(S_out), _ptr(ring_in),
-          _ptr(ring_out), stream=stream)
+    rows = (n, R, H * 128)
+    S_p, slots_n = _pool("S_in", S_in, torch.float32, (H, 128, 128))
+    ring = (slots_n, 3, 3, H * 128)
+    _call("kda_tree_commit", q.device, lib().kda_tree_commit, params.ref, n, R, _shaped("q", q, t, rows), _shaped("k", k, t, rows),
+          _shaped("v", v, t, rows), _shaped("z", z, t, rows), _shaped("b", b, t, (n, R, H)),
+          _shaped("path", path, torch.int32, (n, m)), _shaped("path_len", path_len, torch.int32, (n,)), m,
+          None if slots is None else _shaped("slots", slots, torch.int32, (n,)), slots_n, S_p,
+          _shaped("S_out", S_out, torch.float32, (slots_n, H, 128, 128)), _shaped("ring_in", ring_in, t, ring),
+          _shaped("ring_out", ring_out, t, ring), stream=stream)
     return S_out, ring_out
 
 
@@ -459,7 +461,7 @@ class SsmParams:
         return ctypes.byref(self.struct)
 
     @property
-    def channels(self):
+    def channels(self) -> int:
         """Conv channels of a token: x (H*P) | B (G*N) | C (G*N)."""
         return self.num_heads * self.head_dim + 2 * self.num_groups * self.state_dim
 
@@ -505,25 +507,23 @@ def kda_ssm_prefill(params: SsmParams, xbc, dt, cu_seqlens, z=None, S_in=None, S
     import torch
     cu, n, T = _cu_array(cu_seqlens)
     t, H, P, N, ch = _io_torch(params.io_dtype), params.num_heads, params.head_dim, params.state_dim, params.channels
-    dev = xbc.device
-    sx, sd = _rows("xbc", xbc, t, T, ch), _rows("dt", dt, t, T, H)
-    sz = 0 if z is None else _rows("z", z, t, T, H * P)
-    for name, x in (("S_in", S_in), ("S_out", S_out)):
-        if x is not None:
-            _shaped(name, x, torch.float32, (n, H, N, P))
-    for name, x in (("ring_in", ring_in), ("ring_out", ring_out)):
-        if x is not None:
-            _shaped(name, x, t, (n, 3, ch))
-    o = torch.empty(T, H * P, dtype=t, device=dev) if o is None else _shaped("o", o, t, (T, H * P))
+    dev, f32 = xbc.device, torch.float32
+    x_p, sx = _rows("xbc", xbc, t, T, ch)
+    d_p, sd = _rows("dt", dt, t, T, H)
+    z_p, sz = (None, 0) if z is None else _rows("z", z, t, T, H * P)
+    S_p = None if S_in is None else _shaped("S_in", S_in, f32, (n, H, N, P))
+    r_p = None if ring_in is None else _shaped("ring_in", ring_in, t, (n, 3, ch))
+    if o is None:
+        o = torch.empty(T, H * P, dtype=t, device=dev)
     if S_out is None:
-        S_out = torch.empty(n, H, N, P, dtype=torch.float32, device=dev)
+        S_out = torch.empty(n, H, N, P, dtype=f32, device=dev)
     if ring_out is None:
         ring_out = torch.empty(n, 3, ch, dtype=t, device=dev)
     if workspace is None:
         workspace = torch.empty(max(kda_ssm_prefill_workspace_bytes(params, n, T), 256), dtype=torch.uint8, device=dev)
-    _call("kda_ssm_prefill", dev, lib().kda_ssm_prefill, params.ref, _ptr(xbc), sx, _ptr(dt), sd, _ptr(z), sz, cu, n, T,
-          _ptr(S_in), _ptr(S_out), _ptr(ring_in), _ptr(ring_out), _ptr(o), _ptr(workspace),
-          workspace.numel() * workspace.element_size(), stream=stream)
+    _call("kda_ssm_prefill", dev, lib().kda_ssm_prefill, params.ref, x_p, sx, d_p, sd, z_p, sz, cu, n, T, S_p,
+          _shaped("S_out", S_out, f32, (n, H, N, P)), r_p, _shaped("ring_out", ring_out, t, (n, 3, ch)),
+          _shaped("o", o, t, (T, H * P)), workspace.data_ptr(), workspace.numel() * workspace.element_size(), stream=stream)
     return o, S_out, ring_out
 
 
@@ -536,19 +536,19 @@ def kda_ssm_decode(params: SsmParams, xbc, dt, S, ring, z=None, slots=None, o=No
     [n_slots][3][H*P + 2*G*N] are updated in place.  xbc, dt and z hold one row
     per session, ``slots`` (int32 [n]) its pool slot.  Returns o."""
     import torch
-    n = int(xbc.shape[0])
+    n = xbc.shape[0]
     t, H, P, N, ch = _io_torch(params.io_dtype), params.num_heads, params.head_dim, params.state_dim, params.channels
     dev = xbc.device
-    sx, sd = _rows("xbc", xbc, t, n, ch), _rows("dt", dt, t, n, H)
-    sz = 0 if z is None else _rows("z", z, t, n, H * P)
-    _shaped("S", S, torch.float32, (None, H, N, P))
-    _shaped("ring", ring, t, (S.shape[0], 3, ch))
-    if slots is not None:
-        _shaped("slots", slots, torch.int32, (n,))
-    o = torch.empty(n, H * P, dtype=t, device=dev) if o is None else _shaped("o", o, t, (n, H * P))
+    x_p, sx = _rows("xbc", xbc, t, n, ch)
+    d_p, sd = _rows("dt", dt, t, n, H)
+    z_p, sz = (None, 0) if z is None else _rows("z", z, t, n, H * P)
+    S_p, slots_n = _pool("S", S, torch.float32, (H, N, P))
+    r_p = _shaped("ring", ring, t, (slots_n, 3, ch))
+    s_p = None if slots is None else _shaped("slots", slots, torch.int32, (n,))
+    if o is None:
+        o = torch.empty(n, H * P, dtype=t, device=dev)
     if workspace is None:
         workspace = torch.empty(max(kda_ssm_decode_workspace_bytes(params, n), 256), dtype=torch.uint8, device=dev)
-    _call("kda_ssm_decode", dev, lib().kda_ssm_decode, params.ref, n, _ptr(xbc), sx, _ptr(dt), sd, _ptr(z), sz, _ptr(slots),
-          int(S.shape[0]), _ptr(S), _ptr(ring), _ptr(o), _ptr(workspace), workspace.numel() * workspace.element_size(),
-          stream=stream)
+    _call("kda_ssm_decode", dev, lib().kda_ssm_decode, params.ref, n, x_p, sx, d_p, sd, z_p, sz, s_p, slots_n, S_p, r_p,
+          _shaped("o", o, t, (n, H * P)), workspace.data_ptr(), workspace.numel() * workspace.element_size(), stream=stream)
     return o
