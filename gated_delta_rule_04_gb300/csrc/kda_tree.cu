@@ -12,213 +12,448 @@
 // <= 0 and no factor leaves fp32's range, with either gate.  Parents come
 // before children, so the solve for u runs over the nodes in order.
 //
-// The tree kernel keeps fp32 throughout; one CTA per (session, head), 256
-// threads.
+// Tree kernel: one CTA per SM (two for trees of up to 32 nodes) walks the
+// (session, head) items; an item's phases are
+//   1. the nodes' raw rows to shared memory as fp32, the state to registers;
+//   2. conv + SiLU and the gate, a thread per channel and plane; a node's window
+//      holds only nodes above it, so the planes are convolved in place, last
+//      node first; L2 norms, a warp per node;
+//   3. A and P, a warp per node walking up its path: the factor
+//      e^{Gam_r - Gam_s} is the running product of e^{g} over the nodes passed, so
+//      a pair costs no exponential, and at the root it is e^{Gam_r};
+//   4. [K e^Gam; Q e^Gam] S0 on the tensor cores, transposed: A = S0^T in
+//      tensor memory (lane = value), B = the rows, N = 2 x nodes, K = keys.  At 64
+//      nodes these products are 80 % of the item's arithmetic, and 8.5 us of
+//      fp32 FMAs per SM; as three tcgen05 products of fp16 pairs (hi hi, hi lo,
+//      lo hi: 22-bit operands, so that fp32 outputs hold too) under 1 us.  S0 is
+//      scaled by an exact power of two per value, the rows by 2^8;
+//   5. u over the nodes in order, a thread per value; o, RMSNormGated, a warp
+//      per node.
+// While an item computes, the next one's state and rows go to L2.
 #include <algorithm>
 #include <atomic>
 
-#include "kda_common.cuh"
+#include "kda_chunk_layout.cuh"
+#include "tc_ptx.cuh"
 
 namespace kda {
 namespace {
 
-constexpr int NT = 256;
+constexpr int NT = 256;                     // commit kernel
+constexpr int RMAX = KDA_TREE_MAX_NODES;
+constexpr uint64_t WAIT_LIMIT_NS = 2000000000ull;
+constexpr uint32_t TM_HI = 0, TM_LO = 64, TM_D = 128, TMEM_COLS = 256;
+constexpr float ROW_SCALE = 256.f;          // of the fp16 rows: unit vectors, so that their low halves are normal
 
-struct TreeSmemHead {
-    unsigned long long anc[KDA_TREE_MAX_NODES];   // ancestors of a node, itself included; 0: unused node
-    int win[KDA_TREE_MAX_NODES][CONV_K];          // its conv window, oldest first: node, or -1 - j for the j-th newest ring row
-    float beta[KDA_TREE_MAX_NODES];
+struct TreeHead {
+    float beta[RMAX];
+    int32_t par[RMAX];
+    int32_t depth[RMAX];                    // nodes on the path, itself included; 0: unused node
+    int32_t win[RMAX][CONV_K];              // conv window, oldest first: node, or -1 - j for the j-th newest ring row
+    float smax[4][D];                       // column maxima of |S0| by key part
+    uint8_t path[RMAX][RMAX];               // node, parent, grandparent, ...
+    unsigned long long bar;
+    uint32_t tmem;
+    int32_t bad;
 };
 
-// The path above node r: its ancestor set and conv window.  False when a link
-// is not a parent (below -1 or not below its child).
-__device__ __forceinline__ bool walk_up(const int32_t* par, int r, unsigned long long* anc, int (&win)[CONV_K]) {
-    unsigned long long m = 1ull << r;
-    int filled = CONV_K - 1;
-    win[filled] = r;
+// Shared memory of a tree of R nodes (rows padded to Rp, a multiple of 8).
+struct TreeMap {
+    uint32_t hi, lo, k, q, v, ap, total;
+    __host__ __device__ explicit TreeMap(int Rp) {
+        const uint32_t plane = (uint32_t)Rp * D * 4;
+        hi = (sizeof(TreeHead) + 1023) / 1024 * 1024;   // fp16 [2 panels][2 Rp rows][64 keys], rows k | q
+        lo = hi + plane;                    // the same of the low halves; before that fp32 [Rp][128] e^g
+        k = lo + plane;                     // fp32 [Rp][128] raw k, then k^, then o
+        q = k + plane;                      // raw q, then q^, then (q e^Gam)^T S0
+        v = q + plane;                      // raw v, then v, then u
+        ap = v + plane;                     // float2 [Rp][Rp] A, P of a node and the d-th node of its path
+        total = ap + (uint32_t)Rp * Rp * 8 + 1024;
+    }
+};
+
+__device__ __forceinline__ uint32_t pack2_f16(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+// fp16 pairs (hi, lo) of two values
+__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
+    hi = pack2_f16(a, b);
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+    lo = pack2_f16(a - f.x, b - f.y);
+}
+
+// The path above node r and its conv window; 0 when a link of it is not a
+// parent (below -1 or not below its child).
+__device__ __forceinline__ int walk_up(const int32_t* par, int r, uint8_t* path, int32_t* win) {
+    int n = 0;
     for (int x = r;;) {
+        path[n] = (uint8_t)x;
+        if (n < CONV_K) win[CONV_K - 1 - n] = x;
+        ++n;
         const int p = par[x];
-        if (p < -1 || p >= x) return false;
+        if (p < -1 || p >= x) return 0;
         if (p < 0) break;
-        m |= 1ull << p;
-        if (filled > 0) win[--filled] = p;
         x = p;
     }
-    for (int j = 0; filled > 0; ++j) win[--filled] = -1 - j;
-    *anc = m;
-    return true;
+    for (int i = n; i < CONV_K; ++i) win[CONV_K - 1 - i] = n - 1 - i;   // -1, -2, -3 past the root
+    return n;
 }
 
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
+
+// Sums of eight values over the warp; lanes 4 i .. 4 i + 3 return value i.
+__device__ __forceinline__ float warp_sum8(float (&v)[8], int lane) {
+#pragma unroll
+    for (int w = 4, o = 16; w > 0; w >>= 1, o >>= 1) {
+        const bool up = lane & o;
+#pragma unroll
+        for (int i = 0; i < w; ++i) {
+            const float send = up ? v[i] : v[i + w], keep = up ? v[i + w] : v[i];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+        }
+    }
+    v[0] += __shfl_xor_sync(0xffffffffu, v[0], 2);
+    return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 1);
+}
+
+// The raw rows of an item, 16 bytes at a time, as fp32.
 template <typename TI>
-__global__ void __launch_bounds__(NT) tree_kernel(TreeArgs a) {
-    extern __shared__ __align__(16) unsigned char smem_raw[];
-    TreeSmemHead& hd = *reinterpret_cast<TreeSmemHead*>(smem_raw);
-    const int R = a.n_nodes, H = a.H, W = H * D;
-    float* kk = reinterpret_cast<float*>(smem_raw + sizeof(TreeSmemHead));   // [R][128] k^, then k^ e^Gam
-    float* qq = kk + R * D;                                                  // [R][128] q^, then q^ e^Gam
-    float* gam = qq + R * D;                                                 // [R][128] Gam, then q^ e^Gam S0
-    float* uu = gam + R * D;                                                 // [R][128] v, then u
-    float* A = uu + R * D;                                                   // [R][R]
-    float* Pm = A + R * R;                                                   // [R][R]
-    __shared__ int32_t par[KDA_TREE_MAX_NODES];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int n = blockIdx.x / H, h = blockIdx.x % H;
-    const int slot = a.slots ? a.slots[n] : n;
-    if (slot < 0 || slot >= a.n_slots) return;
-    const size_t row0 = (size_t)n * R;
-
-    if (tid < R) par[tid] = a.parents[row0 + tid];
-    __syncthreads();
-    if (tid < R) {
-        int win[CONV_K];
-        unsigned long long m = 0;
-        if (!walk_up(par, tid, &m, win)) {
-            m = 0;
-            for (int j = 0; j < CONV_K; ++j) win[j] = tid;   // (in range; the node is not computed further)
-        }
-        hd.anc[tid] = m;
-        for (int j = 0; j < CONV_K; ++j) hd.win[tid][j] = win[j];
-        hd.beta[tid] = sigmoid_fast(to_f32(static_cast<const TI*>(a.b)[(row0 + tid) * H + h]));
-    }
-    __syncthreads();
-
-    // ---- conv + SiLU, gate: a thread owns a channel
-    const int i = tid & (D - 1), half = tid >> 7, c = h * D + i;
-    {
-        const TI* ring = static_cast<const TI*>(a.ring) + (size_t)slot * 3 * RING * W + c;
-        const TI* src[3] = {static_cast<const TI*>(a.q) + row0 * W + c, static_cast<const TI*>(a.k) + row0 * W + c,
-                            static_cast<const TI*>(a.v) + row0 * W + c};
-        float* dst[3] = {qq, kk, uu};
-        for (int p = 0; p < 3; ++p) {
-            const float4 w = __ldg(reinterpret_cast<const float4*>(a.conv_w + ((size_t)p * W + c) * CONV_K));
-            const float wt[4] = {w.x, w.y, w.z, w.w};
-            for (int r = half; r < R; r += 2) {
-                float y = 0.f;
-#pragma unroll
-                for (int j = 0; j < CONV_K; ++j) {
-                    const int x = hd.win[r][j];
-                    const TI raw = x >= 0 ? src[p][(size_t)x * W] : ring[((size_t)p * RING + (RING + x)) * W];
-                    y = fmaf(wt[j], to_f32(raw), y);
-                }
-                dst[p][r * D + i] = silu_fast(y);
-            }
-        }
-        const float eA = expf(a.A_log[h]), dtb = a.dt_bias[c];
-        const TI* z = static_cast<const TI*>(a.z) + row0 * W + c;
-        for (int r = half; r < R; r += 2) gam[r * D + i] = decay_gate(a.gate_kind, a.lb, eA, to_f32(z[(size_t)r * W]) + dtb);
-    }
-    __syncthreads();
-    // ---- Gam along the paths (threads 0-127), L2 norms (a warp per node)
-    if (half == 0) {
-        for (int r = 0; r < R; ++r) {
-            const int p = par[r];
-            if (hd.anc[r] && p >= 0) gam[r * D + i] += gam[p * D + i];
-        }
-    }
-    for (int r = warp; r < R; r += NT / 32) {
-        float4 q4 = *reinterpret_cast<const float4*>(qq + r * D + 4 * lane);
-        float4 k4 = *reinterpret_cast<const float4*>(kk + r * D + 4 * lane);
-        const float sq = warp_sum(q4.x * q4.x + q4.y * q4.y + q4.z * q4.z + q4.w * q4.w);
-        const float sk = warp_sum(k4.x * k4.x + k4.y * k4.y + k4.z * k4.z + k4.w * k4.w);
-        const float rq = rsqrtf(sq + a.l2_eps) * a.q_scale, rk = rsqrtf(sk + a.l2_eps);
-        *reinterpret_cast<float4*>(qq + r * D + 4 * lane) = make_float4(q4.x * rq, q4.y * rq, q4.z * rq, q4.w * rq);
-        *reinterpret_cast<float4*>(kk + r * D + 4 * lane) = make_float4(k4.x * rk, k4.y * rk, k4.z * rk, k4.w * rk);
-    }
-    __syncthreads();
-    // ---- A and P: a warp per row, four channels per lane
-    for (int r = warp; r < R; r += NT / 32) {
-        const float4 q4 = *reinterpret_cast<const float4*>(qq + r * D + 4 * lane);
-        const float4 k4 = *reinterpret_cast<const float4*>(kk + r * D + 4 * lane);
-        const float4 g4 = *reinterpret_cast<const float4*>(gam + r * D + 4 * lane);
-        for (unsigned long long m = hd.anc[r]; m; m &= m - 1) {
-            const int s = __ffsll(m) - 1;
-            const float4 ks = *reinterpret_cast<const float4*>(kk + s * D + 4 * lane);
-            const float4 gs = *reinterpret_cast<const float4*>(gam + s * D + 4 * lane);
-            const float e0 = ks.x * __expf(g4.x - gs.x), e1 = ks.y * __expf(g4.y - gs.y);
-            const float e2 = ks.z * __expf(g4.z - gs.z), e3 = ks.w * __expf(g4.w - gs.w);
-            const float sa = warp_sum(k4.x * e0 + k4.y * e1 + k4.z * e2 + k4.w * e3);
-            const float sp = warp_sum(q4.x * e0 + q4.y * e1 + q4.z * e2 + q4.w * e3);
-            if (lane == 0) {
-                A[r * R + s] = sa;
-                Pm[r * R + s] = sp;
-            }
-        }
-    }
-    __syncthreads();
-    for (int x = tid; x < R * D; x += NT) {
-        const float e = __expf(gam[x]);
-        kk[x] *= e;
-        qq[x] *= e;
-    }
-    __syncthreads();
-    // ---- rows times S0: threads 0-127 take the k rows, 128-255 the q rows; a thread
-    // owns a value column and 16 nodes a pass
-    {
-        const float* S0 = a.S + ((size_t)slot * H + h) * D * D + i;
-        const float* rows = half == 0 ? kk : qq;
-        for (int r0 = 0; r0 < R; r0 += 16) {
-            float acc[16];
-#pragma unroll
-            for (int x = 0; x < 16; ++x) acc[x] = 0.f;
-#pragma unroll 1
-            for (int ch = 0; ch < D; ch += 4) {
-                const float s0 = __ldg(S0 + ch * D), s1 = __ldg(S0 + (ch + 1) * D), s2 = __ldg(S0 + (ch + 2) * D),
-                            s3 = __ldg(S0 + (ch + 3) * D);
-#pragma unroll
-                for (int x = 0; x < 16; ++x) {
-                    const int r = min(r0 + x, R - 1);
-                    const float4 w = *reinterpret_cast<const float4*>(rows + r * D + ch);
-                    acc[x] = fmaf(w.x, s0, fmaf(w.y, s1, fmaf(w.z, s2, fmaf(w.w, s3, acc[x]))));
-                }
-            }
-#pragma unroll
-            for (int x = 0; x < 16; ++x) {
-                const int r = r0 + x;
-                if (r >= R) continue;
-                if (half == 0) uu[r * D + i] = hd.beta[r] * (uu[r * D + i] - acc[x]);
-                else gam[r * D + i] = acc[x];
-            }
-        }
-    }
-    __syncthreads();
-    // ---- u over the nodes in order: a thread owns a value column
-    if (half == 0) {
-        for (int r = 0; r < R; ++r) {
-            const unsigned long long self = hd.anc[r];
-            if (!self) continue;
-            float t = 0.f;
-            for (unsigned long long m = self & ~(1ull << r); m; m &= m - 1) {
-                const int s = __ffsll(m) - 1;
-                t = fmaf(A[r * R + s], uu[s * D + i], t);
-            }
-            uu[r * D + i] = fmaf(-hd.beta[r], t, uu[r * D + i]);
-        }
-    }
-    __syncthreads();
-    // ---- o, RMSNormGated: a warp per node, four channels per lane
-    for (int r = warp; r < R; r += NT / 32) {
-        if (!hd.anc[r]) continue;
-        float4 o4 = *reinterpret_cast<const float4*>(gam + r * D + 4 * lane);
-        for (unsigned long long m = hd.anc[r]; m; m &= m - 1) {
-            const int s = __ffsll(m) - 1;
-            const float w = Pm[r * R + s];
-            const float4 u4 = *reinterpret_cast<const float4*>(uu + s * D + 4 * lane);
-            o4.x = fmaf(w, u4.x, o4.x); o4.y = fmaf(w, u4.y, o4.y);
-            o4.z = fmaf(w, u4.z, o4.z); o4.w = fmaf(w, u4.w, o4.w);
-        }
-        const float ss = warp_sum(o4.x * o4.x + o4.y * o4.y + o4.z * o4.z + o4.w * o4.w);
-        const float rs = rsqrtf(ss * (1.0f / D) + a.norm_eps);
-        const float ov[4] = {o4.x, o4.y, o4.z, o4.w};
-        const size_t at = (row0 + r) * W + (size_t)h * D + 4 * lane;
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-            const float gt = to_f32(static_cast<const TI*>(a.gout)[at + m]);
-            static_cast<TI*>(a.o)[at + m] = from_f32<TI>(ov[m] * rs * a.norm_w[4 * lane + m] * sigmoid_fast(gt));
-        }
+__device__ __forceinline__ void stage16(float* dst, const TI* src) {
+    const uint4 u = *reinterpret_cast<const uint4*>(src);
+    if constexpr (sizeof(TI) == 4) {
+        *reinterpret_cast<uint4*>(dst) = u;
+    } else {
+        const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&u);
+        const float2 a = __bfloat1622float2(h[0]), b = __bfloat1622float2(h[1]), c = __bfloat1622float2(h[2]), d = __bfloat1622float2(h[3]);
+        reinterpret_cast<float4*>(dst)[0] = make_float4(a.x, a.y, b.x, b.y);
+        reinterpret_cast<float4*>(dst)[1] = make_float4(c.x, c.y, d.x, d.y);
     }
 }
 
-size_t tree_smem(int R) { return sizeof(TreeSmemHead) + sizeof(float) * ((size_t)4 * R * D + (size_t)2 * R * R); }
+template <typename TI, int THREADS>
+__global__ void __launch_bounds__(THREADS, 512 / THREADS) tree_kernel(TreeArgs a) {
+    constexpr int NW = THREADS / 32, KP = THREADS / 128, KEYS = D / KP;   // warps; key parts and keys of a part
+    constexpr int ROWS = RMAX / NW;                                      // node rows of a warp, at most
+    extern __shared__ unsigned char smem_raw[];
+    const uint32_t raw = ptx::smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
+    unsigned char* sb = smem_raw + (base - raw);
+    TreeHead& hd = *reinterpret_cast<TreeHead*>(sb);
+    const int R = a.n_nodes, H = a.H, W = H * D, Rp = (R + 7) / 8 * 8;
+    const TreeMap map(Rp);
+    float* kk = reinterpret_cast<float*>(sb + map.k);
+    float* qq = reinterpret_cast<float*>(sb + map.q);
+    float* vv = reinterpret_cast<float*>(sb + map.v);
+    float* eg = reinterpret_cast<float*>(sb + map.lo);
+    float2* ap = reinterpret_cast<float2*>(sb + map.ap);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t bar = ptx::smem_u32(&hd.bar);
+    if (warp == 0) {
+        ptx::tmem_alloc(ptx::smem_u32(&hd.tmem), TMEM_COLS);
+        ptx::tmem_relinquish();
+    }
+    if (tid == 0) {
+        ptx::mbar_init(bar, 1);
+        ptx::fence_mbar_init();
+        hd.bad = 0;
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = hd.tmem;
+    const int quarter = warp & 3, part = warp >> 2;      // TMEM lane quarter; key part
+    const uint32_t tlane = tmem + ((uint32_t)(32 * quarter) << 16);
+    const int j = 32 * quarter + lane;                   // value column = TMEM lane
+    const int i = tid & (D - 1);                         // channel of the conv phase
+
+    const int64_t items = (int64_t)a.n * H;
+    uint32_t phase = 0;
+    int64_t item = blockIdx.x;
+#pragma unroll 1
+    for (; item < items; item += gridDim.x) {
+        const int n = (int)(item / H), h = (int)(item % H);
+        const int slot = a.slots ? a.slots[n] : n;
+        if (item + gridDim.x < items) {                  // the next item's state and rows into L2
+            const int64_t nx = item + gridDim.x;
+            const int nn = (int)(nx / H), nh = (int)(nx % H), ns = a.slots ? a.slots[nn] : nn;
+            if (ns >= 0 && ns < a.n_slots) {
+                if (tid == 0) ptx::bulk_prefetch_l2(a.S + ((size_t)ns * H + nh) * D * D, D * D * 4);
+                constexpr int LINES = D * sizeof(TI) / 128;  // 128-byte lines of a row
+                for (int x = tid; x < 5 * R * LINES; x += THREADS) {
+                    const int pl = x / (R * LINES), r = x / LINES % R;
+                    const void* rows = pl == 0 ? a.q : pl == 1 ? a.k : pl == 2 ? a.v : pl == 3 ? a.z : a.gout;
+                    prefetch_l2(static_cast<const char*>(rows) + (((size_t)nn * R + r) * W + (size_t)nh * D) * sizeof(TI) + x % LINES * 128);
+                }
+            }
+        }
+        if (slot < 0 || slot >= a.n_slots) continue;
+        const size_t row0 = (size_t)n * R;
+        const int c = h * D + i;
+
+        // ---- 1. state into registers, raw rows into shared memory
+        float S[KEYS];
+        {
+            const float* S0 = a.S + ((size_t)slot * H + h) * D * D + (size_t)(KEYS * part) * D + j;
+#pragma unroll
+            for (int x = 0; x < KEYS; ++x) S[x] = __ldg(S0 + (size_t)x * D);
+        }
+        {
+            constexpr int E = 16 / sizeof(TI), CH = D / E;   // elements and chunks of 16 bytes
+            const TI* src[4] = {static_cast<const TI*>(a.q), static_cast<const TI*>(a.k), static_cast<const TI*>(a.v),
+                                static_cast<const TI*>(a.z)};
+            float* dst[4] = {qq, kk, vv, eg};
+#pragma unroll
+            for (int pl = 0; pl < 4; ++pl)
+#pragma unroll 2
+                for (int x = tid; x < R * CH; x += THREADS)
+                    stage16(dst[pl] + (x / CH) * D + (x % CH) * E, src[pl] + (row0 + x / CH) * W + (size_t)h * D + (x % CH) * E);
+        }
+        if (tid < R) hd.par[tid] = a.parents[row0 + tid];
+        // the ring rows and conv weights of this thread's plane(s)
+        float ring[4 / KP][RING];
+        float4 cw[4 / KP];
+#pragma unroll
+        for (int x = 0; x < 4 / KP; ++x) {
+            const int pl = KP * x + (tid >> 7);              // plane q, k, v (3: the gate)
+            cw[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (pl < 3) {
+                cw[x] = __ldg(reinterpret_cast<const float4*>(a.conv_w + ((size_t)pl * W + c) * CONV_K));
+#pragma unroll
+                for (int s = 0; s < RING; ++s)
+                    ring[x][s] = to_f32(static_cast<const TI*>(a.ring)[(((size_t)slot * 3 + pl) * RING + s) * W + c]);
+            }
+        }
+        __syncthreads();
+        if (tid < R) {
+            int win[CONV_K] = {0, 0, 0, 0};
+            hd.depth[tid] = walk_up(hd.par, tid, hd.path[tid], win);
+            for (int x = 0; x < CONV_K; ++x) hd.win[tid][x] = win[x];
+            hd.beta[tid] = sigmoid_fast(to_f32(static_cast<const TI*>(a.b)[(row0 + tid) * H + h]));
+        }
+        {
+            float m = 0.f;
+#pragma unroll
+            for (int x = 0; x < KEYS; ++x) m = fmaxf(m, fabsf(S[x]));
+            hd.smax[part][j] = m;
+        }
+        __syncthreads();
+        // ---- 2. conv + SiLU in place, last node first; e^g
+#pragma unroll
+        for (int x = 0; x < 4 / KP; ++x) {
+            const int pl = KP * x + (tid >> 7);
+            if (pl < 3) {
+                float* dst = (pl == 0 ? qq : pl == 1 ? kk : vv) + i;
+                auto rowv = [&](int w) { return w >= 0 ? dst[w * D] : w == -1 ? ring[x][2] : w == -2 ? ring[x][1] : ring[x][0]; };
+#pragma unroll 2
+                for (int r = R - 1; r >= 0; --r) {
+                    if (hd.depth[r] == 0) continue;
+                    const int4 w = *reinterpret_cast<const int4*>(hd.win[r]);
+                    float y = cw[x].x * rowv(w.x);
+                    y = fmaf(cw[x].y, rowv(w.y), y);
+                    y = fmaf(cw[x].z, rowv(w.z), y);
+                    y = fmaf(cw[x].w, dst[r * D], y);
+                    dst[r * D] = silu_fast(y);
+                }
+            } else {
+                const float eA = expf(a.A_log[h]), dtb = a.dt_bias[c];
+#pragma unroll 4
+                for (int r = 0; r < R; ++r) eg[r * D + i] = __expf(decay_gate(a.gate_kind, a.lb, eA, eg[r * D + i] + dtb));
+            }
+        }
+        // S0^T to tensor memory as fp16 pairs, each value column scaled into [1, 2)
+        float unscale;                                       // of D's lane
+        {
+            float m = hd.smax[0][j];
+#pragma unroll
+            for (int x = 1; x < KP; ++x) m = fmaxf(m, hd.smax[x][j]);
+            int e = (int)((__float_as_uint(m) >> 23) & 255u) - 127;
+            e = e < -100 ? -100 : e > 100 ? 100 : e;
+            const float f = __uint_as_float((uint32_t)(127 - e) << 23);
+            unscale = __uint_as_float((uint32_t)(127 + e) << 23) * (1.f / ROW_SCALE);
+#pragma unroll
+            for (int g = 0; g < KEYS / 32; ++g) {
+                uint32_t hi[16], lo[16];
+#pragma unroll
+                for (int x = 0; x < 16; ++x) split2(S[32 * g + 2 * x] * f, S[32 * g + 2 * x + 1] * f, hi[x], lo[x]);
+                ptx::tmem_st16u(tlane + TM_HI + KEYS / 2 * part + 16 * g, hi);
+                ptx::tmem_st16u(tlane + TM_LO + KEYS / 2 * part + 16 * g, lo);
+            }
+            ptx::tmem_wait_st();
+        }
+        __syncthreads();
+        for (int r = warp; r < R; r += NW) {
+            if (hd.depth[r] == 0) continue;
+            float4 q4 = *reinterpret_cast<const float4*>(qq + r * D + 4 * lane);
+            float4 k4 = *reinterpret_cast<const float4*>(kk + r * D + 4 * lane);
+            const float sq = warp_sum(q4.x * q4.x + q4.y * q4.y + q4.z * q4.z + q4.w * q4.w);
+            const float sk = warp_sum(k4.x * k4.x + k4.y * k4.y + k4.z * k4.z + k4.w * k4.w);
+            const float rq = rsqrtf(sq + a.l2_eps) * a.q_scale, rk = rsqrtf(sk + a.l2_eps);
+            *reinterpret_cast<float4*>(qq + r * D + 4 * lane) = make_float4(q4.x * rq, q4.y * rq, q4.z * rq, q4.w * rq);
+            *reinterpret_cast<float4*>(kk + r * D + 4 * lane) = make_float4(k4.x * rk, k4.y * rk, k4.z * rk, k4.w * rk);
+        }
+        __syncthreads();
+        // ---- 3. A and P along the paths, and the rows e^Gam k^, e^Gam q^
+        uint32_t lo_k[ROWS][2], lo_q[ROWS][2];
+        const uint32_t panel = 2 * (uint32_t)Rp * 128;       // bytes of 64 keys of the 2 Rp rows
+        auto row_off = [&](int row) {                        // 8 bytes: keys 4 lane .. 4 lane + 3 of a row
+            return (4 * lane >= 64 ? panel : 0u) + (uint32_t)row * 128 + ((((4 * lane & 63) >> 3) ^ (row & 7)) << 4) + (lane & 1) * 8;
+        };
+#pragma unroll
+        for (int x = 0; x < ROWS; ++x) {
+            const int r = warp + x * NW;
+            const int depth = r < R ? hd.depth[r] : 0;
+            lo_k[x][0] = lo_k[x][1] = lo_q[x][0] = lo_q[x][1] = 0;
+            if (depth == 0) continue;
+            const float4 q4 = *reinterpret_cast<const float4*>(qq + r * D + 4 * lane);
+            const float4 k4 = *reinterpret_cast<const float4*>(kk + r * D + 4 * lane);
+            const float2 qa = make_float2(q4.x, q4.y), qb = make_float2(q4.z, q4.w), ka = make_float2(k4.x, k4.y), kb = make_float2(k4.z, k4.w);
+            float2 wa = make_float2(1.f, 1.f), wb = wa;      // e^{Gam_r - Gam_s}
+            for (int d0 = 0; d0 < depth; d0 += 4) {
+                float v[8];
+#pragma unroll
+                for (int d = 0; d < 4; ++d) {
+                    v[2 * d] = v[2 * d + 1] = 0.f;
+                    if (d0 + d >= depth) continue;
+                    const int s = hd.path[r][d0 + d];
+                    const float4 ks = *reinterpret_cast<const float4*>(kk + s * D + 4 * lane);
+                    const float4 es = *reinterpret_cast<const float4*>(eg + s * D + 4 * lane);
+                    const float2 xa = __fmul2_rn(make_float2(ks.x, ks.y), wa), xb = __fmul2_rn(make_float2(ks.z, ks.w), wb);
+                    const float2 sa = __ffma2_rn(ka, xa, __fmul2_rn(kb, xb)), sp = __ffma2_rn(qa, xa, __fmul2_rn(qb, xb));
+                    v[2 * d] = sa.x + sa.y;
+                    v[2 * d + 1] = sp.x + sp.y;
+                    wa = __fmul2_rn(wa, make_float2(es.x, es.y));
+                    wb = __fmul2_rn(wb, make_float2(es.z, es.w));
+                }
+                const float sum = warp_sum8(v, lane);
+                const int d = d0 + (lane >> 3);              // values 2 d, 2 d + 1: A and P
+                if ((lane & 3) == 0 && d < depth) reinterpret_cast<float*>(ap + r * Rp + d)[(lane >> 2) & 1] = sum;
+            }
+            const float2 sc = make_float2(ROW_SCALE, ROW_SCALE);
+            wa = __fmul2_rn(wa, sc);
+            wb = __fmul2_rn(wb, sc);
+            uint32_t h0, h1;
+            split2(ka.x * wa.x, ka.y * wa.y, h0, lo_k[x][0]);
+            split2(kb.x * wb.x, kb.y * wb.y, h1, lo_k[x][1]);
+            *reinterpret_cast<uint2*>(sb + map.hi + row_off(r)) = make_uint2(h0, h1);
+            split2(qa.x * wa.x, qa.y * wa.y, h0, lo_q[x][0]);
+            split2(qb.x * wb.x, qb.y * wb.y, h1, lo_q[x][1]);
+            *reinterpret_cast<uint2*>(sb + map.hi + row_off(Rp + r)) = make_uint2(h0, h1);
+        }
+        __syncthreads();                                     // e^g is read: its place takes the low halves
+#pragma unroll
+        for (int x = 0; x < ROWS; ++x) {
+            const int r = warp + x * NW;
+            if (r >= R) continue;
+            *reinterpret_cast<uint2*>(sb + map.lo + row_off(r)) = make_uint2(lo_k[x][0], lo_k[x][1]);
+            *reinterpret_cast<uint2*>(sb + map.lo + row_off(Rp + r)) = make_uint2(lo_q[x][0], lo_q[x][1]);
+        }
+        ptx::fence_async_smem();
+        ptx::tc_fence_before();
+        __syncthreads();
+        ptx::tc_fence_after();
+        // ---- 4. D = S0^T [K e^Gam; Q e^Gam]^T
+        if (tid == 0) {
+            const uint32_t idesc = ptx::idesc_f16_f32(128, 2 * Rp);
+#pragma unroll
+            for (int term = 0; term < 3; ++term) {           // hi hi, hi lo, lo hi
+                const uint64_t db = ptx::sdesc_sw128(base + (term == 1 ? map.lo : map.hi));
+#pragma unroll
+                for (int x = 0; x < D / 16; ++x)
+                    ptx::mma_f16_ta(tmem + TM_D, tmem + (term == 2 ? TM_LO : TM_HI) + 8 * x, db + (x >> 2) * (panel / 16) + (x & 3) * 2, idesc,
+                                    term > 0 || x > 0);
+            }
+            ptx::mma_commit(bar);
+        }
+        if (!ptx::mbar_wait(bar, phase, WAIT_LIMIT_NS)) hd.bad = 1;
+        phase ^= 1u;
+        __syncthreads();
+        if (hd.bad) break;
+        ptx::tc_fence_after();
+        // ---- 5. right sides of the solve, (q e^Gam)^T S0: lane = value, 8 columns at a time
+        for (int col = 8 * part; col < 2 * Rp; col += 8 * KP) {
+            float f[8];
+            ptx::tmem_ld8(tlane + TM_D + col, f);
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                const int r = col + x < Rp ? col + x : col + x - Rp;
+                if (r >= R) continue;
+                if (col < Rp) vv[r * D + j] = hd.beta[r] * (vv[r * D + j] - f[x] * unscale);
+                else qq[r * D + j] = f[x] * unscale;
+            }
+        }
+        ptx::tc_fence_before();
+        __syncthreads();
+        if (tid < D) {
+            for (int r = 0; r < R; ++r) {
+                const int depth = hd.depth[r];
+                float t0 = 0.f, t1 = 0.f;
+#pragma unroll 2
+                for (int d = 1; d < depth; ++d) {
+                    const float u = vv[hd.path[r][d] * D + tid];
+                    if (d & 1) t0 = fmaf(ap[r * Rp + d].x, u, t0);
+                    else t1 = fmaf(ap[r * Rp + d].x, u, t1);
+                }
+                if (depth > 1) vv[r * D + tid] = fmaf(-hd.beta[r], t0 + t1, vv[r * D + tid]);
+            }
+        }
+        __syncthreads();
+        for (int r = warp; r < R; r += NW) {
+            const int depth = hd.depth[r];
+            if (depth == 0) continue;
+            const size_t at = (row0 + r) * W + (size_t)h * D + 4 * lane;
+            float gt[4];
+            if constexpr (sizeof(TI) == 4) {
+                const float4 g = *reinterpret_cast<const float4*>(static_cast<const TI*>(a.gout) + at);
+                gt[0] = g.x; gt[1] = g.y; gt[2] = g.z; gt[3] = g.w;
+            } else {
+                const uint2 g = *reinterpret_cast<const uint2*>(static_cast<const TI*>(a.gout) + at);
+                const float2 g0 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&g.x));
+                const float2 g1 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&g.y));
+                gt[0] = g0.x; gt[1] = g0.y; gt[2] = g1.x; gt[3] = g1.y;
+            }
+            float4 o4 = *reinterpret_cast<const float4*>(qq + r * D + 4 * lane);
+#pragma unroll 2
+            for (int d = 0; d < depth; ++d) {
+                const float w = ap[r * Rp + d].y;
+                const float4 u4 = *reinterpret_cast<const float4*>(vv + hd.path[r][d] * D + 4 * lane);
+                o4.x = fmaf(w, u4.x, o4.x); o4.y = fmaf(w, u4.y, o4.y);
+                o4.z = fmaf(w, u4.z, o4.z); o4.w = fmaf(w, u4.w, o4.w);
+            }
+            const float ss = warp_sum(o4.x * o4.x + o4.y * o4.y + o4.z * o4.z + o4.w * o4.w);
+            const float rs = rsqrtf(ss * (1.0f / D) + a.norm_eps);
+            const float4 nw = __ldg(reinterpret_cast<const float4*>(a.norm_w) + lane);
+            const float y0 = o4.x * rs * nw.x * sigmoid_fast(gt[0]), y1 = o4.y * rs * nw.y * sigmoid_fast(gt[1]);
+            const float y2 = o4.z * rs * nw.z * sigmoid_fast(gt[2]), y3 = o4.w * rs * nw.w * sigmoid_fast(gt[3]);
+            if constexpr (sizeof(TI) == 4) {
+                *reinterpret_cast<float4*>(static_cast<TI*>(a.o) + at) = make_float4(y0, y1, y2, y3);
+            } else {
+                const __nv_bfloat162 b0 = __floats2bfloat162_rn(y0, y1), b1 = __floats2bfloat162_rn(y2, y3);
+                *reinterpret_cast<uint2*>(static_cast<TI*>(a.o) + at) =
+                    make_uint2(*reinterpret_cast<const uint32_t*>(&b0), *reinterpret_cast<const uint32_t*>(&b1));
+            }
+        }
+        __syncthreads();                                     // the next item's rows replace this one's
+    }
+    if (hd.bad) {
+        // the bounded wait gave up: no row of this item and of the CTA's later ones passes
+        // for a result
+        for (; item < items; item += gridDim.x) {
+            const int n = (int)(item / H), h = (int)(item % H), slot = a.slots ? a.slots[n] : n;
+            if (slot < 0 || slot >= a.n_slots) continue;
+            for (int x = tid; x < R * D; x += THREADS)
+                static_cast<TI*>(a.o)[((size_t)n * R + x / D) * W + (size_t)h * D + x % D] = from_f32<TI>(__int_as_float(0x7fc00000));
+        }
+        if (tid == 0) ptx::mbar_wait(bar, phase ^ 1u, WAIT_LIMIT_NS);   // the MMAs finish before their TMEM is freed
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, TMEM_COLS);
+    }
+}
 
 // Opts a kernel into `bytes` of dynamic shared memory, once per device.
 cudaError_t opt_in(const void* f, size_t bytes, std::atomic<uint64_t>& done) {
@@ -230,6 +465,17 @@ cudaError_t opt_in(const void* f, size_t bytes, std::atomic<uint64_t>& done) {
     e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
     if (e == cudaSuccess) done.fetch_or(bit);
     return e;
+}
+
+// SMs of the current device, looked up once per device.
+int sm_count() {
+    static std::atomic<int> cache[64];
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 152;
+    if (dev < 64 && (sms = cache[dev].load()) > 0) return sms;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0) sms = 152;
+    if (dev < 64) cache[dev].store(sms);
+    return sms;
 }
 
 // ---- commit --------------------------------------------------------------------
@@ -362,16 +608,26 @@ __global__ void __launch_bounds__(NT, 2) commit_kernel(CommitArgs a) {
 
 }  // namespace
 
-cudaError_t launch_tree(const TreeArgs& a, int io_bf16, cudaStream_t s) {
-    const size_t bytes = tree_smem(a.n_nodes);
-    const int64_t blocks = (int64_t)a.n * a.H;
-    static std::atomic<uint64_t> done[2];
-    const void* f = io_bf16 ? (const void*)tree_kernel<__nv_bfloat16> : (const void*)tree_kernel<float>;
-    const cudaError_t e = opt_in(f, tree_smem(KDA_TREE_MAX_NODES), done[io_bf16 ? 1 : 0]);
+namespace {
+
+template <typename TI, int THREADS>
+cudaError_t tree(const TreeArgs& a, cudaStream_t s) {
+    static std::atomic<uint64_t> done;
+    const int Rp = (a.n_nodes + 7) / 8 * 8;
+    // up to 32 nodes two CTAs share an SM
+    constexpr int most = THREADS == 256 ? 32 : RMAX;
+    cudaError_t e = opt_in((const void*)tree_kernel<TI, THREADS>, TreeMap(most).total, done);
     if (e != cudaSuccess) return e;
-    if (io_bf16) tree_kernel<__nv_bfloat16><<<(unsigned)blocks, NT, bytes, s>>>(a);
-    else tree_kernel<float><<<(unsigned)blocks, NT, bytes, s>>>(a);
+    const int64_t items = (int64_t)a.n * a.H, ctas = 512 / THREADS * (int64_t)sm_count();
+    tree_kernel<TI, THREADS><<<(unsigned)std::min(items, ctas), THREADS, TreeMap(Rp).total, s>>>(a);
     return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_tree(const TreeArgs& a, int io_bf16, cudaStream_t s) {
+    if (a.n_nodes <= 32) return io_bf16 ? tree<__nv_bfloat16, 256>(a, s) : tree<float, 256>(a, s);
+    return io_bf16 ? tree<__nv_bfloat16, 512>(a, s) : tree<float, 512>(a, s);
 }
 
 cudaError_t launch_commit(const CommitArgs& a, int io_bf16, cudaStream_t s) {

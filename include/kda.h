@@ -301,6 +301,8 @@ kda_status kda_decode_multi(const kda_params* p, int32_t n_sessions, int32_t n_t
  * The conv of a node reads the raw rows of its parent, grandparent and
  * great-grandparent, and the session's ring before the root.  For a tree that
  * is one chain the rows equal those of kda_decode_multi up to rounding.
+ * Should a bounded in-kernel wait give up, the rows it concerns are NaN (there
+ * is no workspace to report it through).
  */
 #define KDA_TREE_MAX_NODES 64
 kda_status kda_decode_tree(const kda_params* p, int32_t n_sessions, int32_t n_nodes,
