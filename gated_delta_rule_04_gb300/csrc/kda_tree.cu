@@ -30,6 +30,8 @@
 //   5. u over the nodes in order, a thread per value; o, RMSNormGated, a warp
 //      per node.
 // While an item computes, the next one's state and rows go to L2.
+#include <stddef.h>
+
 #include <algorithm>
 #include <atomic>
 
@@ -49,13 +51,18 @@ struct TreeHead {
     float beta[RMAX];
     int32_t par[RMAX];
     int32_t depth[RMAX];                    // nodes on the path, itself included; 0: unused node
-    int32_t win[RMAX][CONV_K];              // conv window, oldest first: node, or -1 - j for the j-th newest ring row
+    alignas(16) int32_t win[RMAX][CONV_K];  // conv window, oldest first: node, or -1 - j for the j-th newest ring row
     float smax[4][D];                       // column maxima of |S0| by key part
-    uint8_t path[RMAX][RMAX];               // node, parent, grandparent, ...
+    uint8_t order[RMAX];                    // nodes by depth (unused ones first)
+    int32_t level[RMAX + 1];                // level[l]: nodes of a depth below l (l >= 1)
+    alignas(16) uint8_t path[RMAX][RMAX];   // node, parent, grandparent, ..., then the padding row (read in fours)
     unsigned long long bar;
     uint32_t tmem;
     int32_t bad;
 };
+
+static_assert(offsetof(TreeHead, path) % 16 == 0 && offsetof(TreeHead, win) % 16 == 0 && offsetof(TreeHead, bar) % 8 == 0,
+              "vector accesses");
 
 // Shared memory of a tree of R nodes (rows padded to Rp, a multiple of 8).
 struct TreeMap {
@@ -64,10 +71,12 @@ struct TreeMap {
         const uint32_t plane = (uint32_t)Rp * D * 4;
         hi = (sizeof(TreeHead) + 1023) / 1024 * 1024;   // fp16 [2 panels][2 Rp rows][64 keys], rows k | q
         lo = hi + plane;                    // the same of the low halves; before that fp32 [Rp][128] e^g
-        k = lo + plane;                     // fp32 [Rp][128] raw k, then k^, then o
-        q = k + plane;                      // raw q, then q^, then (q e^Gam)^T S0
-        v = q + plane;                      // raw v, then v, then u
-        ap = v + plane;                     // float2 [Rp][Rp] A, P of a node and the d-th node of its path
+        // k, q, v: the ring's three rows before row 0 (row -1 the newest); e^g, k, v: row Rp,
+        // where a path's padding points (e^g = 1, k = u = 0)
+        k = lo + plane + (RING + 1) * D * 4;    // fp32 [Rp + 1][128] raw k, then k^
+        q = k + plane + (RING + 1) * D * 4;     // raw q, then q^, then (q e^Gam)^T S0
+        v = q + plane + (RING + 1) * D * 4;     // raw v, then v, then u
+        ap = v + plane + D * 4;             //                     // fp32 [Rp][2][Rp] A, then P of a node and the d-th node of its path
         total = ap + (uint32_t)Rp * Rp * 8 + 1024;
     }
 };
@@ -85,8 +94,9 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t&
 
 // The path above node r and its conv window; 0 when a link of it is not a
 // parent (below -1 or not below its child).
-__device__ __forceinline__ int walk_up(const int32_t* par, int r, uint8_t* path, int32_t* win) {
+__device__ __forceinline__ int walk_up(const int32_t* par, int r, int Rp, uint8_t* path, int32_t* win) {
     int n = 0;
+    for (int x = 0; x < RMAX; x += 8) *reinterpret_cast<uint2*>(path + x) = make_uint2(0x01010101u * (uint32_t)Rp, 0x01010101u * (uint32_t)Rp);
     for (int x = r;;) {
         path[n] = (uint8_t)x;
         if (n < CONV_K) win[CONV_K - 1 - n] = x;
@@ -119,10 +129,9 @@ __device__ __forceinline__ float warp_sum8(float (&v)[8], int lane) {
     return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 1);
 }
 
-// The raw rows of an item, 16 bytes at a time, as fp32.
+// 16 bytes of a raw row as fp32.
 template <typename TI>
-__device__ __forceinline__ void stage16(float* dst, const TI* src) {
-    const uint4 u = *reinterpret_cast<const uint4*>(src);
+__device__ __forceinline__ void to_rows(float* dst, uint4 u) {
     if constexpr (sizeof(TI) == 4) {
         *reinterpret_cast<uint4*>(dst) = u;
     } else {
@@ -133,10 +142,23 @@ __device__ __forceinline__ void stage16(float* dst, const TI* src) {
     }
 }
 
+// Four elements of a row as fp32 (16-byte or 8-byte aligned).
+template <typename TI>
+__device__ __forceinline__ float4 load4(const TI* p) {
+    if constexpr (sizeof(TI) == 4) {
+        return *reinterpret_cast<const float4*>(p);
+    } else {
+        const uint2 u = *reinterpret_cast<const uint2*>(p);
+        const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.x));
+        const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.y));
+        return make_float4(a.x, a.y, b.x, b.y);
+    }
+}
+
 template <typename TI, int THREADS>
 __global__ void __launch_bounds__(THREADS, 512 / THREADS) tree_kernel(TreeArgs a) {
     constexpr int NW = THREADS / 32, KP = THREADS / 128, KEYS = D / KP;   // warps; key parts and keys of a part
-    constexpr int ROWS = RMAX / NW;                                      // node rows of a warp, at most
+    constexpr int NODES = THREADS / 8, ROWS = NODES / NW;                // most nodes, and of a warp (4)
     extern __shared__ unsigned char smem_raw[];
     const uint32_t raw = ptx::smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
     unsigned char* sb = smem_raw + (base - raw);
@@ -147,7 +169,7 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) tree_kernel(TreeArgs a
     float* qq = reinterpret_cast<float*>(sb + map.q);
     float* vv = reinterpret_cast<float*>(sb + map.v);
     float* eg = reinterpret_cast<float*>(sb + map.lo);
-    float2* ap = reinterpret_cast<float2*>(sb + map.ap);
+    float* ap = reinterpret_cast<float*>(sb + map.ap);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t bar = ptx::smem_u32(&hd.bar);
     if (warp == 0) {
@@ -168,15 +190,15 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) tree_kernel(TreeArgs a
     const int j = 32 * quarter + lane;                   // value column = TMEM lane
     const int i = tid & (D - 1);                         // channel of the conv phase
 
-    const int64_t items = (int64_t)a.n * H;
+    const uint32_t items = (uint32_t)a.n * H;            // (below 2^31: checked on the host)
     uint32_t phase = 0;
-    int64_t item = blockIdx.x;
+    uint32_t item = blockIdx.x;
 #pragma unroll 1
     for (; item < items; item += gridDim.x) {
         const int n = (int)(item / H), h = (int)(item % H);
         const int slot = a.slots ? a.slots[n] : n;
         if (item + gridDim.x < items) {                  // the next item's state and rows into L2
-            const int64_t nx = item + gridDim.x;
+            const uint32_t nx = item + gridDim.x;
             const int nn = (int)(nx / H), nh = (int)(nx % H), ns = a.slots ? a.slots[nn] : nn;
             if (ns >= 0 && ns < a.n_slots) {
                 if (tid == 0) ptx::bulk_prefetch_l2(a.S + ((size_t)ns * H + nh) * D * D, D * D * 4);
@@ -191,44 +213,68 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) tree_kernel(TreeArgs a
         if (slot < 0 || slot >= a.n_slots) continue;
         const size_t row0 = (size_t)n * R;
         const int c = h * D + i;
+        if (tid == 0 && item == blockIdx.x) ptx::bulk_prefetch_l2(a.S + ((size_t)slot * H + h) * D * D, D * D * 4);
 
-        // ---- 1. state into registers, raw rows into shared memory
+        // ---- 1. raw rows into shared memory, then the state into registers (which would not
+        // hold both at once)
+        {
+            constexpr int E = 16 / sizeof(TI), CH = D / E;   // elements and chunks of 16 bytes
+            const size_t off = row0 * W + (size_t)h * D;
+            const TI* src[4] = {static_cast<const TI*>(a.q) + off, static_cast<const TI*>(a.k) + off, static_cast<const TI*>(a.v) + off,
+                                static_cast<const TI*>(a.z) + off};
+            float* dst[4] = {qq, kk, vv, eg};
+            // (a chunk of each plane in flight per thread: with two the registers spill)
+#pragma unroll 1
+            for (int x = tid; x < R * CH; x += THREADS) {
+                uint4 u[4];
+#pragma unroll
+                for (int p = 0; p < 4; ++p) u[p] = __ldg(reinterpret_cast<const uint4*>(src[p] + (size_t)(x / CH) * W) + x % CH);
+#pragma unroll
+                for (int p = 0; p < 4; ++p) to_rows<TI>(dst[p] + x * E, u[p]);
+            }
+        }
         float S[KEYS];
         {
             const float* S0 = a.S + ((size_t)slot * H + h) * D * D + (size_t)(KEYS * part) * D + j;
 #pragma unroll
             for (int x = 0; x < KEYS; ++x) S[x] = __ldg(S0 + (size_t)x * D);
         }
-        {
-            constexpr int E = 16 / sizeof(TI), CH = D / E;   // elements and chunks of 16 bytes
-            const TI* src[4] = {static_cast<const TI*>(a.q), static_cast<const TI*>(a.k), static_cast<const TI*>(a.v),
-                                static_cast<const TI*>(a.z)};
-            float* dst[4] = {qq, kk, vv, eg};
-#pragma unroll
-            for (int pl = 0; pl < 4; ++pl)
-#pragma unroll 2
-                for (int x = tid; x < R * CH; x += THREADS)
-                    stage16(dst[pl] + (x / CH) * D + (x % CH) * E, src[pl] + (row0 + x / CH) * W + (size_t)h * D + (x % CH) * E);
-        }
         if (tid < R) hd.par[tid] = a.parents[row0 + tid];
-        // the ring rows and conv weights of this thread's plane(s)
-        float ring[4 / KP][RING];
-        float4 cw[4 / KP];
+        // the ring's rows and the padding row; the conv weights of this thread's plane and channels
+        {
+            constexpr int NR = (3 * RING + KP - 1) / KP;     // ring rows of this thread's channel
+            const TI* src = static_cast<const TI*>(a.ring) + (size_t)slot * 3 * RING * W + c;
+            TI v[NR];
 #pragma unroll
-        for (int x = 0; x < 4 / KP; ++x) {
-            const int pl = KP * x + (tid >> 7);              // plane q, k, v (3: the gate)
-            cw[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (pl < 3) {
-                cw[x] = __ldg(reinterpret_cast<const float4*>(a.conv_w + ((size_t)pl * W + c) * CONV_K));
+            for (int x = 0; x < NR; ++x)
+                if (KP * x + (tid >> 7) < 3 * RING) v[x] = src[(size_t)(KP * x + (tid >> 7)) * W];
 #pragma unroll
-                for (int s = 0; s < RING; ++s)
-                    ring[x][s] = to_f32(static_cast<const TI*>(a.ring)[(((size_t)slot * 3 + pl) * RING + s) * W + c]);
+            for (int x = 0; x < NR; ++x) {
+                const int y = KP * x + (tid >> 7), p = y / RING, s = y % RING;
+                if (y < 3 * RING) (p == 0 ? qq : p == 1 ? kk : vv)[(s - RING) * D + i] = to_f32(v[x]);
             }
+        }
+        if (tid < D) {
+            eg[Rp * D + tid] = 1.f;
+            kk[Rp * D + tid] = 0.f;
+            vv[Rp * D + tid] = 0.f;
+        }
+        const int pl = (tid >> 6) & 3, cpair = 2 * (tid & 63), node0 = 32 * (tid >> 8);
+        const int c2 = h * D + cpair;
+        float2 cw[CONV_K];
+        if (pl < 3) {
+            const float4* w = reinterpret_cast<const float4*>(a.conv_w + ((size_t)pl * W + c2) * CONV_K);
+            const float4 wa = __ldg(w), wb = __ldg(w + 1);
+            cw[0] = make_float2(wa.x, wb.x); cw[1] = make_float2(wa.y, wb.y);
+            cw[2] = make_float2(wa.z, wb.z); cw[3] = make_float2(wa.w, wb.w);
+        } else {
+            cw[0] = *reinterpret_cast<const float2*>(a.dt_bias + c2);
+            cw[1] = make_float2(expf(a.A_log[h]), 0.f);
         }
         __syncthreads();
         if (tid < R) {
             int win[CONV_K] = {0, 0, 0, 0};
-            hd.depth[tid] = walk_up(hd.par, tid, hd.path[tid], win);
+            hd.depth[tid] = walk_up(hd.par, tid, Rp, hd.path[tid], win);
             for (int x = 0; x < CONV_K; ++x) hd.win[tid][x] = win[x];
             hd.beta[tid] = sigmoid_fast(to_f32(static_cast<const TI*>(a.b)[(row0 + tid) * H + h]));
         }
@@ -239,29 +285,6 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) tree_kernel(TreeArgs a
             hd.smax[part][j] = m;
         }
         __syncthreads();
-        // ---- 2. conv + SiLU in place, last node first; e^g
-#pragma unroll
-        for (int x = 0; x < 4 / KP; ++x) {
-            const int pl = KP * x + (tid >> 7);
-            if (pl < 3) {
-                float* dst = (pl == 0 ? qq : pl == 1 ? kk : vv) + i;
-                auto rowv = [&](int w) { return w >= 0 ? dst[w * D] : w == -1 ? ring[x][2] : w == -2 ? ring[x][1] : ring[x][0]; };
-#pragma unroll 2
-                for (int r = R - 1; r >= 0; --r) {
-                    if (hd.depth[r] == 0) continue;
-                    const int4 w = *reinterpret_cast<const int4*>(hd.win[r]);
-                    float y = cw[x].x * rowv(w.x);
-                    y = fmaf(cw[x].y, rowv(w.y), y);
-                    y = fmaf(cw[x].z, rowv(w.z), y);
-                    y = fmaf(cw[x].w, dst[r * D], y);
-                    dst[r * D] = silu_fast(y);
-                }
-            } else {
-                const float eA = expf(a.A_log[h]), dtb = a.dt_bias[c];
-#pragma unroll 4
-                for (int r = 0; r < R; ++r) eg[r * D + i] = __expf(decay_gate(a.gate_kind, a.lb, eA, eg[r * D + i] + dtb));
-            }
-        }
         // S0^T to tensor memory as fp16 pairs, each value column scaled into [1, 2)
         float unscale;                                       // of D's lane
         {
@@ -282,16 +305,91 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) tree_kernel(TreeArgs a
             }
             ptx::tmem_wait_st();
         }
+        // ---- 2. conv + SiLU and e^g, in place: a thread owns a plane's channel pair and takes 16
+        // nodes at a time, the last ones first, every window read before they are written
+        {
+            float* plane = (pl == 0 ? qq : pl == 1 ? kk : pl == 2 ? vv : eg) + cpair;
+            auto at = [&](int r) { return *reinterpret_cast<const float2*>(plane + r * D); };
+            float2 y[16];
+            auto compute = [&](int r0) {
+                if (r0 >= R) return;
+                if (pl < 3) {
+#pragma unroll
+                    for (int m = 0; m < 16; ++m) {
+                        const int4 w = *reinterpret_cast<const int4*>(hd.win[min(r0 + m, R - 1)]);
+                        y[m] = __fmul2_rn(cw[0], at(w.x));
+                        y[m] = __ffma2_rn(cw[1], at(w.y), y[m]);
+                        y[m] = __ffma2_rn(cw[2], at(w.z), y[m]);
+                        y[m] = __ffma2_rn(cw[3], at(w.w), y[m]);
+                        if ((m & 3) == 3) asm volatile("" ::: "memory");   // (all windows at once would spill)
+                    }
+#pragma unroll
+                    for (int m = 0; m < 16; ++m) y[m] = make_float2(silu_fast(y[m].x), silu_fast(y[m].y));
+                } else {
+#pragma unroll
+                    for (int m = 0; m < 16; ++m) y[m] = __fadd2_rn(at(min(r0 + m, R - 1)), cw[0]);
+                    if (a.gate_kind == KDA_GATE_BOUNDED) {
+#pragma unroll
+                        for (int m = 0; m < 16; ++m)
+                            y[m] = make_float2(__expf(a.lb * sigmoid_fast(cw[1].x * y[m].x)), __expf(a.lb * sigmoid_fast(cw[1].x * y[m].y)));
+                    } else {
+#pragma unroll
+                        for (int m = 0; m < 16; ++m)
+                            y[m] = make_float2(__expf(decay_gate(1, 0.f, cw[1].x, y[m].x)), __expf(decay_gate(1, 0.f, cw[1].x, y[m].y)));
+                    }
+                }
+            };
+            auto store = [&](int r0) {
+#pragma unroll
+                for (int m = 0; m < 16; ++m)
+                    if (r0 + m < R) *reinterpret_cast<float2*>(plane + (r0 + m) * D) = y[m];
+            };
+            // (with two thread groups to a plane the lower nodes are written only after the
+            // upper ones' windows, which hold them, are read)
+#pragma unroll 1
+            for (int b = 16; b >= 0; b -= 16) {
+                compute(node0 + b);
+                if (THREADS == 512 && node0 == 0 && b) __syncthreads();
+                store(node0 + b);
+            }
+            if (THREADS == 512 && node0 != 0) __syncthreads();
+        }
+        // the nodes by depth, for the solve
+        if (tid >= THREADS - RMAX) {
+            const int r = tid - (THREADS - RMAX);
+            int below = 0, rank = 0;                         // nodes of a depth up to r; r's place
+            const int mine = r < R ? hd.depth[r] : 0;
+            for (int x = 0; x < R; ++x) {
+                const int d = hd.depth[x];
+                below += d <= r;
+                rank += d < mine || (d == mine && x < r);
+            }
+            hd.level[r + 1] = below;
+            if (r < R) hd.order[rank] = (uint8_t)r;
+        }
         __syncthreads();
-        for (int r = warp; r < R; r += NW) {
-            if (hd.depth[r] == 0) continue;
-            float4 q4 = *reinterpret_cast<const float4*>(qq + r * D + 4 * lane);
-            float4 k4 = *reinterpret_cast<const float4*>(kk + r * D + 4 * lane);
-            const float sq = warp_sum(q4.x * q4.x + q4.y * q4.y + q4.z * q4.z + q4.w * q4.w);
-            const float sk = warp_sum(k4.x * k4.x + k4.y * k4.y + k4.z * k4.z + k4.w * k4.w);
-            const float rq = rsqrtf(sq + a.l2_eps) * a.q_scale, rk = rsqrtf(sk + a.l2_eps);
-            *reinterpret_cast<float4*>(qq + r * D + 4 * lane) = make_float4(q4.x * rq, q4.y * rq, q4.z * rq, q4.w * rq);
-            *reinterpret_cast<float4*>(kk + r * D + 4 * lane) = make_float4(k4.x * rk, k4.y * rk, k4.z * rk, k4.w * rk);
+        for (int r0 = warp; r0 < R; r0 += 4 * NW) {          // four rows a pass
+            float4 q4[4], k4[4];
+            float v[8];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const int r = min(r0 + x * NW, R - 1);
+                q4[x] = *reinterpret_cast<const float4*>(qq + r * D + 4 * lane);
+                k4[x] = *reinterpret_cast<const float4*>(kk + r * D + 4 * lane);
+                v[2 * x] = q4[x].x * q4[x].x + q4[x].y * q4[x].y + q4[x].z * q4[x].z + q4[x].w * q4[x].w;
+                v[2 * x + 1] = k4[x].x * k4[x].x + k4[x].y * k4[x].y + k4[x].z * k4[x].z + k4[x].w * k4[x].w;
+            }
+            const float sum = warp_sum8(v, lane);
+            const float rn = rsqrtf(sum + a.l2_eps) * ((lane >> 2) & 1 ? 1.f : a.q_scale);
+            __syncwarp();
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const int r = r0 + x * NW;
+                const float rq = __shfl_sync(0xffffffffu, rn, 8 * x), rk = __shfl_sync(0xffffffffu, rn, 8 * x + 4);
+                if (r >= R) continue;
+                *reinterpret_cast<float4*>(qq + r * D + 4 * lane) = make_float4(q4[x].x * rq, q4[x].y * rq, q4[x].z * rq, q4[x].w * rq);
+                *reinterpret_cast<float4*>(kk + r * D + 4 * lane) = make_float4(k4[x].x * rk, k4[x].y * rk, k4[x].z * rk, k4[x].w * rk);
+            }
         }
         __syncthreads();
         // ---- 3. A and P along the paths, and the rows e^Gam k^, e^Gam q^
@@ -312,11 +410,10 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) tree_kernel(TreeArgs a
             float2 wa = make_float2(1.f, 1.f), wb = wa;      // e^{Gam_r - Gam_s}
             for (int d0 = 0; d0 < depth; d0 += 4) {
                 float v[8];
+                const uint32_t p4 = *reinterpret_cast<const uint32_t*>(hd.path[r] + d0);
 #pragma unroll
                 for (int d = 0; d < 4; ++d) {
-                    v[2 * d] = v[2 * d + 1] = 0.f;
-                    if (d0 + d >= depth) continue;
-                    const int s = hd.path[r][d0 + d];
+                    const int s = p4 >> (8 * d) & 255u;
                     const float4 ks = *reinterpret_cast<const float4*>(kk + s * D + 4 * lane);
                     const float4 es = *reinterpret_cast<const float4*>(eg + s * D + 4 * lane);
                     const float2 xa = __fmul2_rn(make_float2(ks.x, ks.y), wa), xb = __fmul2_rn(make_float2(ks.z, ks.w), wb);
@@ -327,8 +424,8 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) tree_kernel(TreeArgs a
                     wb = __fmul2_rn(wb, make_float2(es.z, es.w));
                 }
                 const float sum = warp_sum8(v, lane);
-                const int d = d0 + (lane >> 3);              // values 2 d, 2 d + 1: A and P
-                if ((lane & 3) == 0 && d < depth) reinterpret_cast<float*>(ap + r * Rp + d)[(lane >> 2) & 1] = sum;
+                const int d = d0 + (lane >> 3);              // values 2 d, 2 d + 1: A and P (0 past the root)
+                if ((lane & 3) == 0) ap[(2 * r + ((lane >> 2) & 1)) * Rp + d] = sum;
             }
             const float2 sc = make_float2(ROW_SCALE, ROW_SCALE);
             wa = __fmul2_rn(wa, sc);
@@ -375,57 +472,83 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) tree_kernel(TreeArgs a
         for (int col = 8 * part; col < 2 * Rp; col += 8 * KP) {
             float f[8];
             ptx::tmem_ld8(tlane + TM_D + col, f);
+            if (col < Rp) {
+                float v[8];
 #pragma unroll
-            for (int x = 0; x < 8; ++x) {
-                const int r = col + x < Rp ? col + x : col + x - Rp;
-                if (r >= R) continue;
-                if (col < Rp) vv[r * D + j] = hd.beta[r] * (vv[r * D + j] - f[x] * unscale);
-                else qq[r * D + j] = f[x] * unscale;
+                for (int x = 0; x < 8; ++x) v[x] = vv[min(col + x, R - 1) * D + j];
+#pragma unroll
+                for (int x = 0; x < 8; ++x)
+                    if (col + x < R) vv[(col + x) * D + j] = hd.beta[col + x] * fmaf(-unscale, f[x], v[x]);
+            } else {
+#pragma unroll
+                for (int x = 0; x < 8; ++x)
+                    if (col - Rp + x < R) qq[(col - Rp + x) * D + j] = f[x] * unscale;
             }
         }
         ptx::tc_fence_before();
         __syncthreads();
-        if (tid < D) {
-            for (int r = 0; r < R; ++r) {
-                const int depth = hd.depth[r];
+        // u: a thread per value; nodes of one depth do not see one another, and the thread
+        // groups share them
+        for (int l = 2; l <= RMAX; ++l) {
+            const int k0 = hd.level[l], k1 = l < RMAX ? hd.level[l + 1] : R;
+            if (k0 >= R) break;
+            for (int k = k0 + part; k < k1; k += KP) {
+                const int r = hd.order[k];
+                const uint8_t* path = hd.path[r];
+                const float* A = ap + 2 * r * Rp;
+                const float self = vv[r * D + j], beta = hd.beta[r];
                 float t0 = 0.f, t1 = 0.f;
 #pragma unroll 2
-                for (int d = 1; d < depth; ++d) {
-                    const float u = vv[hd.path[r][d] * D + tid];
-                    if (d & 1) t0 = fmaf(ap[r * Rp + d].x, u, t0);
-                    else t1 = fmaf(ap[r * Rp + d].x, u, t1);
+                for (int d = 0; d < l; d += 4) {             // (d = 0, the node itself, is left out)
+                    const uint32_t p4 = *reinterpret_cast<const uint32_t*>(path + d);
+                    const float4 a4 = *reinterpret_cast<const float4*>(A + d);
+                    t0 = fmaf(d ? a4.x : 0.f, vv[(p4 & 255u) * D + j], t0);
+                    t1 = fmaf(a4.y, vv[(p4 >> 8 & 255u) * D + j], t1);
+                    t0 = fmaf(a4.z, vv[(p4 >> 16 & 255u) * D + j], t0);
+                    t1 = fmaf(a4.w, vv[(p4 >> 24) * D + j], t1);
                 }
-                if (depth > 1) vv[r * D + tid] = fmaf(-hd.beta[r], t0 + t1, vv[r * D + tid]);
+                vv[r * D + j] = fmaf(-beta, t0 + t1, self);
             }
+            __syncthreads();
         }
-        __syncthreads();
-        for (int r = warp; r < R; r += NW) {
-            const int depth = hd.depth[r];
+        // gate logits of this warp's rows, in flight during the sums
+        float4 gt[ROWS];
+#pragma unroll
+        for (int x = 0; x < ROWS; ++x)
+            if (warp + x * NW < R) gt[x] = load4(static_cast<const TI*>(a.gout) + (row0 + warp + x * NW) * W + (size_t)h * D + 4 * lane);
+        const float4 nw = __ldg(reinterpret_cast<const float4*>(a.norm_w) + lane);
+        float4 o4[ROWS];
+        float ss[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int x = 0; x < ROWS; ++x) {
+            const int r = warp + x * NW;
+            const int depth = r < R ? hd.depth[r] : 0;
             if (depth == 0) continue;
-            const size_t at = (row0 + r) * W + (size_t)h * D + 4 * lane;
-            float gt[4];
-            if constexpr (sizeof(TI) == 4) {
-                const float4 g = *reinterpret_cast<const float4*>(static_cast<const TI*>(a.gout) + at);
-                gt[0] = g.x; gt[1] = g.y; gt[2] = g.z; gt[3] = g.w;
-            } else {
-                const uint2 g = *reinterpret_cast<const uint2*>(static_cast<const TI*>(a.gout) + at);
-                const float2 g0 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&g.x));
-                const float2 g1 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&g.y));
-                gt[0] = g0.x; gt[1] = g0.y; gt[2] = g1.x; gt[3] = g1.y;
-            }
-            float4 o4 = *reinterpret_cast<const float4*>(qq + r * D + 4 * lane);
+            const float* Pr = ap + (2 * r + 1) * Rp;
+            o4[x] = *reinterpret_cast<const float4*>(qq + r * D + 4 * lane);
 #pragma unroll 2
-            for (int d = 0; d < depth; ++d) {
-                const float w = ap[r * Rp + d].y;
-                const float4 u4 = *reinterpret_cast<const float4*>(vv + hd.path[r][d] * D + 4 * lane);
-                o4.x = fmaf(w, u4.x, o4.x); o4.y = fmaf(w, u4.y, o4.y);
-                o4.z = fmaf(w, u4.z, o4.z); o4.w = fmaf(w, u4.w, o4.w);
+            for (int d = 0; d < depth; d += 4) {
+                const uint32_t p4 = *reinterpret_cast<const uint32_t*>(hd.path[r] + d);
+                const float4 w4 = *reinterpret_cast<const float4*>(Pr + d);
+                const float wd[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    const float4 u4 = *reinterpret_cast<const float4*>(vv + (p4 >> (8 * m) & 255u) * D + 4 * lane);
+                    o4[x].x = fmaf(wd[m], u4.x, o4[x].x); o4[x].y = fmaf(wd[m], u4.y, o4[x].y);
+                    o4[x].z = fmaf(wd[m], u4.z, o4[x].z); o4[x].w = fmaf(wd[m], u4.w, o4[x].w);
+                }
             }
-            const float ss = warp_sum(o4.x * o4.x + o4.y * o4.y + o4.z * o4.z + o4.w * o4.w);
-            const float rs = rsqrtf(ss * (1.0f / D) + a.norm_eps);
-            const float4 nw = __ldg(reinterpret_cast<const float4*>(a.norm_w) + lane);
-            const float y0 = o4.x * rs * nw.x * sigmoid_fast(gt[0]), y1 = o4.y * rs * nw.y * sigmoid_fast(gt[1]);
-            const float y2 = o4.z * rs * nw.z * sigmoid_fast(gt[2]), y3 = o4.w * rs * nw.w * sigmoid_fast(gt[3]);
+            ss[x] = o4[x].x * o4[x].x + o4[x].y * o4[x].y + o4[x].z * o4[x].z + o4[x].w * o4[x].w;
+        }
+        const float rms = rsqrtf(warp_sum8(ss, lane) * (1.0f / D) + a.norm_eps);
+#pragma unroll
+        for (int x = 0; x < ROWS; ++x) {
+            const int r = warp + x * NW;
+            const float rs = __shfl_sync(0xffffffffu, rms, 4 * x);
+            if (r >= R || hd.depth[r] == 0) continue;
+            const float y0 = o4[x].x * rs * nw.x * sigmoid_fast(gt[x].x), y1 = o4[x].y * rs * nw.y * sigmoid_fast(gt[x].y);
+            const float y2 = o4[x].z * rs * nw.z * sigmoid_fast(gt[x].z), y3 = o4[x].w * rs * nw.w * sigmoid_fast(gt[x].w);
+            const size_t at = (row0 + r) * W + (size_t)h * D + 4 * lane;
             if constexpr (sizeof(TI) == 4) {
                 *reinterpret_cast<float4*>(static_cast<TI*>(a.o) + at) = make_float4(y0, y1, y2, y3);
             } else {
