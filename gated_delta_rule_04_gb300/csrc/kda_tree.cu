@@ -609,123 +609,158 @@ int sm_count() {
 constexpr int CG = 8;
 
 struct CommitSmem {
-    float kc[CG][D], va[CG][D], e[CG][D], kh[CG][D], av[CG][D];
-    float beta[CG];
+    alignas(16) float kc[CG][D], va[CG][D], e[CG][D], kh[CG][D], av[CG][D];
+    alignas(16) float beta[CG];
     float red[NT / 32][D];
     float d[D];
     int path[KDA_TREE_MAX_NODES];
-    int bad;
 };
 
+// Persistent CTAs: while an item computes, the next one's state goes to L2.
 template <typename TI>
 __global__ void __launch_bounds__(NT, 2) commit_kernel(CommitArgs a) {
     __shared__ CommitSmem sm;
     const int H = a.H, W = H * D;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int n = blockIdx.x / H, h = blockIdx.x % H;
-    const int slot = a.slots ? a.slots[n] : n;
-    if (slot < 0 || slot >= a.n_slots) return;
-    const int len = a.path_len[n];
-    if (len < 0 || len > a.max_len) return;
-    if (len == 0 && a.S_in == a.S_out && a.ring_in == a.ring_out) return;
-    const float* Sg_in = a.S_in + ((size_t)slot * H + h) * D * D;
-    float4 Sr[16];
+    const int i = tid & (D - 1), half = tid >> 7;
+    const uint32_t items = (uint32_t)a.n * H;   // (below 2^31: checked on the host)
+    // slot and length are read an item ahead: the state's address waits for them
+    int next_slot = a.slots ? a.slots[blockIdx.x / H] : blockIdx.x / H, next_len = a.path_len[blockIdx.x / H];
+#pragma unroll 1
+    for (uint32_t item = blockIdx.x; item < items; item += gridDim.x) {
+        const int n = (int)(item / H), h = (int)(item % H), c = h * D + i;
+        const int slot = next_slot, len = next_len;
+        if (item + gridDim.x < items) {
+            const int nn = (int)((item + gridDim.x) / H), nh = (int)((item + gridDim.x) % H);
+            next_slot = a.slots ? a.slots[nn] : nn;
+            next_len = a.path_len[nn];
+            if (tid == 0 && next_slot >= 0 && next_slot < a.n_slots)
+                ptx::bulk_prefetch_l2(a.S_in + ((size_t)next_slot * H + nh) * D * D, D * D * 4);
+        }
+        if (slot < 0 || slot >= a.n_slots) continue;
+        if (len < 0 || len > a.max_len) continue;
+        if (len == 0 && a.S_in == a.S_out && a.ring_in == a.ring_out) continue;
+        const float* Sg_in = a.S_in + ((size_t)slot * H + h) * D * D;
+        float4 Sr[16];
 #pragma unroll
-    for (int r = 0; r < 16; ++r)
-        Sr[r] = __ldcs(reinterpret_cast<const float4*>(Sg_in + (size_t)(16 * warp + r) * D) + lane);
-    if (tid == 0) sm.bad = 0;
-    __syncthreads();
-    if (tid < len) {
-        const int node = a.path[(size_t)n * a.max_len + tid];
-        sm.path[tid] = node;
-        if (node < 0 || node >= a.n_nodes) sm.bad = 1;
-    }
-    __syncthreads();
-    if (sm.bad) return;
+        for (int r = 0; r < 16; ++r)
+            Sr[r] = __ldcs(reinterpret_cast<const float4*>(Sg_in + (size_t)(16 * warp + r) * D) + lane);
+        bool bad = false;
+        if (tid < len) {
+            const int node = a.path[(size_t)n * a.max_len + tid];
+            sm.path[tid] = node;
+            bad = node < 0 || node >= a.n_nodes;
+        }
+        if (__syncthreads_or(bad)) continue;
 
-    const int i = tid & (D - 1), half = tid >> 7, c = h * D + i;
-    const size_t row0 = (size_t)n * a.n_nodes;
-    const TI* ring = static_cast<const TI*>(a.ring_in) + (size_t)slot * 3 * RING * W + c;
-    const TI* plane[3] = {static_cast<const TI*>(a.q) + row0 * W + c, static_cast<const TI*>(a.k) + row0 * W + c,
-                          static_cast<const TI*>(a.v) + row0 * W + c};
-    // raw row of plane p at position t of the path (t < 0: the ring)
-    auto raw = [&](int p, int t) -> TI {
-        return t >= 0 ? plane[p][(size_t)sm.path[t] * W] : ring[((size_t)p * RING + (RING + t)) * W];
-    };
-    const int p = 1 + half;   // threads 0-127 own a channel of k, 128-255 of v and the gate
-    const float4 w = __ldg(reinterpret_cast<const float4*>(a.conv_w + ((size_t)p * W + c) * CONV_K));
-    const float eA = expf(a.A_log[h]), dtb = a.dt_bias[c];
+        const size_t row0 = (size_t)n * a.n_nodes;
+        const TI* ring = static_cast<const TI*>(a.ring_in) + (size_t)slot * 3 * RING * W + c;
+        const TI* plane[3] = {static_cast<const TI*>(a.q) + row0 * W + c, static_cast<const TI*>(a.k) + row0 * W + c,
+                              static_cast<const TI*>(a.v) + row0 * W + c};
+        // raw row of plane p at position t of the path (t < 0: the ring)
+        auto raw = [&](int p, int t) -> TI {
+            const TI* src = t >= 0 ? plane[p] + (size_t)sm.path[t] * W : ring + ((size_t)p * RING + (RING + t)) * W;
+            return *src;
+        };
+        const int p = 1 + half;   // threads 0-127 own a channel of k, 128-255 of v and the gate
+        const float4 w = __ldg(reinterpret_cast<const float4*>(a.conv_w + ((size_t)p * W + c) * CONV_K));
+        const float eA = expf(a.A_log[h]), dtb = a.dt_bias[c];
 
 #pragma unroll 1
-    for (int g0 = 0; g0 < len; g0 += CG) {
-        const int ng = min(CG, len - g0);
-        for (int t = 0; t < ng; ++t) {
-            const int x = g0 + t;
-            float y = w.x * to_f32(raw(p, x - 3));
-            y = fmaf(w.y, to_f32(raw(p, x - 2)), y);
-            y = fmaf(w.z, to_f32(raw(p, x - 1)), y);
-            y = fmaf(w.w, to_f32(raw(p, x)), y);
-            y = silu_fast(y);
-            if (half == 0) {
-                sm.kc[t][i] = y;
-            } else {
-                sm.va[t][i] = y;
-                const float z = to_f32(static_cast<const TI*>(a.z)[(row0 + sm.path[x]) * W + c]);
-                sm.e[t][i] = __expf(decay_gate(a.gate_kind, a.lb, eA, z + dtb));
+        for (int g0 = 0; g0 < len; g0 += CG) {
+            const int ng = min(CG, len - g0);
+            // the group's raw rows and gate logits, all in flight at once
+            TI xs[CG + RING], zs[CG];
+#pragma unroll
+            for (int t = 0; t < CG + RING; ++t) xs[t] = t < ng + RING ? raw(p, g0 + t - RING) : TI(0.f);
+#pragma unroll
+            for (int t = 0; t < CG; ++t)
+                zs[t] = half && t < ng ? static_cast<const TI*>(a.z)[(row0 + sm.path[g0 + t]) * W + c] : TI(0.f);
+            TI bl = TI(0.f);
+            if (tid < ng) bl = static_cast<const TI*>(a.b)[(row0 + sm.path[g0 + tid]) * H + h];
+#pragma unroll
+            for (int t = 0; t < CG; ++t) {
+                if (t >= ng) break;
+                float y = w.x * to_f32(xs[t]);
+                y = fmaf(w.y, to_f32(xs[t + 1]), y);
+                y = fmaf(w.z, to_f32(xs[t + 2]), y);
+                y = fmaf(w.w, to_f32(xs[t + 3]), y);
+                y = silu_fast(y);
+                if (half == 0) {
+                    sm.kc[t][i] = y;
+                } else {
+                    sm.va[t][i] = y;
+                    sm.e[t][i] = __expf(decay_gate(a.gate_kind, a.lb, eA, to_f32(zs[t]) + dtb));
+                }
             }
-        }
-        if (tid < ng) sm.beta[tid] = sigmoid_fast(to_f32(static_cast<const TI*>(a.b)[(row0 + sm.path[g0 + tid]) * H + h]));
-        __syncthreads();
-        if (warp < ng) {
-            const float4 k4 = *reinterpret_cast<const float4*>(&sm.kc[warp][4 * lane]);
-            const float4 e4 = *reinterpret_cast<const float4*>(&sm.e[warp][4 * lane]);
-            const float rk = rsqrtf(warp_sum(k4.x * k4.x + k4.y * k4.y + k4.z * k4.z + k4.w * k4.w) + a.l2_eps);
-            const float4 kh = make_float4(k4.x * rk, k4.y * rk, k4.z * rk, k4.w * rk);
-            *reinterpret_cast<float4*>(&sm.kh[warp][4 * lane]) = kh;
-            *reinterpret_cast<float4*>(&sm.av[warp][4 * lane]) = make_float4(e4.x * kh.x, e4.y * kh.y, e4.z * kh.z, e4.w * kh.w);
-        }
-        __syncthreads();
+            if (tid < ng) sm.beta[tid] = sigmoid_fast(to_f32(bl));
+            __syncthreads();
+            if (warp < ng) {
+                const float4 k4 = *reinterpret_cast<const float4*>(&sm.kc[warp][4 * lane]);
+                const float4 e4 = *reinterpret_cast<const float4*>(&sm.e[warp][4 * lane]);
+                const float rk = rsqrtf(warp_sum(k4.x * k4.x + k4.y * k4.y + k4.z * k4.z + k4.w * k4.w) + a.l2_eps);
+                const float4 kh = make_float4(k4.x * rk, k4.y * rk, k4.z * rk, k4.w * rk);
+                *reinterpret_cast<float4*>(&sm.kh[warp][4 * lane]) = kh;
+                *reinterpret_cast<float4*>(&sm.av[warp][4 * lane]) = make_float4(e4.x * kh.x, e4.y * kh.y, e4.z * kh.z, e4.w * kh.w);
+            }
+            __syncthreads();
 #pragma unroll 1
-        for (int t = 0; t < ng; ++t) {
-            float4 u = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int t = 0; t < ng; ++t) {
+                float2 u01 = make_float2(0.f, 0.f), u23 = u01;
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const float ar = sm.av[t][16 * warp + r];
-                u.x = fmaf(ar, Sr[r].x, u.x); u.y = fmaf(ar, Sr[r].y, u.y);
-                u.z = fmaf(ar, Sr[r].z, u.z); u.w = fmaf(ar, Sr[r].w, u.w);
-            }
-            *reinterpret_cast<float4*>(&sm.red[warp][4 * lane]) = u;
-            __syncthreads();
-            if (tid < D) {
-                float uj = 0.f;
+                for (int r = 0; r < 16; r += 4) {
+                    const float4 a4 = *reinterpret_cast<const float4*>(&sm.av[t][16 * warp + r]);
+                    const float ar[4] = {a4.x, a4.y, a4.z, a4.w};
 #pragma unroll
-                for (int k = 0; k < NT / 32; ++k) uj += sm.red[k][tid];
-                sm.d[tid] = sm.beta[t] * (sm.va[t][tid] - uj);
-            }
-            __syncthreads();
-            const float4 d4 = *reinterpret_cast<const float4*>(&sm.d[4 * lane]);
+                    for (int m = 0; m < 4; ++m) {
+                        const float2 aa = make_float2(ar[m], ar[m]);
+                        u01 = __ffma2_rn(aa, make_float2(Sr[r + m].x, Sr[r + m].y), u01);
+                        u23 = __ffma2_rn(aa, make_float2(Sr[r + m].z, Sr[r + m].w), u23);
+                    }
+                }
+                *reinterpret_cast<float4*>(&sm.red[warp][4 * lane]) = make_float4(u01.x, u01.y, u23.x, u23.y);
+                __syncthreads();
+                if (tid < D) {
+                    float uj = 0.f;
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const float er = sm.e[t][16 * warp + r], kr = sm.kh[t][16 * warp + r];
-                Sr[r].x = fmaf(er, Sr[r].x, kr * d4.x); Sr[r].y = fmaf(er, Sr[r].y, kr * d4.y);
-                Sr[r].z = fmaf(er, Sr[r].z, kr * d4.z); Sr[r].w = fmaf(er, Sr[r].w, kr * d4.w);
+                    for (int k = 0; k < NT / 32; ++k) uj += sm.red[k][tid];
+                    sm.d[tid] = sm.beta[t] * (sm.va[t][tid] - uj);
+                }
+                __syncthreads();
+                const float4 d4 = *reinterpret_cast<const float4*>(&sm.d[4 * lane]);
+                const float2 d01 = make_float2(d4.x, d4.y), d23 = make_float2(d4.z, d4.w);
+#pragma unroll
+                for (int r = 0; r < 16; r += 4) {
+                    const float4 e4 = *reinterpret_cast<const float4*>(&sm.e[t][16 * warp + r]);
+                    const float4 k4 = *reinterpret_cast<const float4*>(&sm.kh[t][16 * warp + r]);
+                    const float er[4] = {e4.x, e4.y, e4.z, e4.w}, kr[4] = {k4.x, k4.y, k4.z, k4.w};
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) {
+                        const float2 ee = make_float2(er[m], er[m]), kk = make_float2(kr[m], kr[m]);
+                        const float2 s01 = __ffma2_rn(ee, make_float2(Sr[r + m].x, Sr[r + m].y), __fmul2_rn(kk, d01));
+                        const float2 s23 = __ffma2_rn(ee, make_float2(Sr[r + m].z, Sr[r + m].w), __fmul2_rn(kk, d23));
+                        Sr[r + m] = make_float4(s01.x, s01.y, s23.x, s23.y);
+                    }
+                }
             }
+            __syncthreads();   // the group's vectors are rewritten
         }
-        __syncthreads();   // the group's vectors are rewritten
-    }
-    float* Sg_out = a.S_out + ((size_t)slot * H + h) * D * D;
+        float* Sg_out = a.S_out + ((size_t)slot * H + h) * D * D;
 #pragma unroll
-    for (int r = 0; r < 16; ++r) __stcs(reinterpret_cast<float4*>(Sg_out + (size_t)(16 * warp + r) * D) + lane, Sr[r]);
+        for (int r = 0; r < 16; ++r) __stcs(reinterpret_cast<float4*>(Sg_out + (size_t)(16 * warp + r) * D) + lane, Sr[r]);
 
-    // ring: the last three raw rows of ring | path, of every plane (every read of the
-    // input ring by the conv is behind the barriers above; a thread owns its channel)
-    TI* rout = static_cast<TI*>(a.ring_out) + (size_t)slot * 3 * RING * W + c;
-    for (int pl = half; pl < 3; pl += 2) {
-        TI row[RING];
+        // ring: the last three raw rows of ring | path, of every plane (a thread reads all
+        // three of its channel before it writes them, and every conv's read of the input
+        // ring is behind the barriers above; without tokens there was none)
+        TI* rout = static_cast<TI*>(a.ring_out) + (size_t)slot * 3 * RING * W + c;
+        for (int pl = half; pl < 3; pl += 2) {
+            TI row[RING];
 #pragma unroll
-        for (int s = 0; s < RING; ++s) row[s] = raw(pl, len - RING + s);
+            for (int s = 0; s < RING; ++s) row[s] = raw(pl, len - RING + s);
 #pragma unroll
-        for (int s = 0; s < RING; ++s) rout[((size_t)pl * RING + s) * W] = row[s];
+            for (int s = 0; s < RING; ++s) rout[((size_t)pl * RING + s) * W] = row[s];
+        }
+        __syncthreads();       // the next item's path replaces this one's
     }
 }
 
@@ -754,7 +789,7 @@ cudaError_t launch_tree(const TreeArgs& a, int io_bf16, cudaStream_t s) {
 }
 
 cudaError_t launch_commit(const CommitArgs& a, int io_bf16, cudaStream_t s) {
-    const unsigned blocks = (unsigned)((int64_t)a.n * a.H);
+    const unsigned blocks = (unsigned)std::min<int64_t>((int64_t)a.n * a.H, 2 * (int64_t)sm_count());
     if (io_bf16) commit_kernel<__nv_bfloat16><<<blocks, NT, 0, s>>>(a);
     else commit_kernel<float><<<blocks, NT, 0, s>>>(a);
     return cudaGetLastError();

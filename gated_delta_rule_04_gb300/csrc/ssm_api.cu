@@ -247,6 +247,7 @@ kda_status kda_ssm_prefill(const kda_ssm_params* p, const void* xbc, int64_t xbc
 
 size_t kda_ssm_decode_workspace_bytes(const kda_ssm_params* p, int32_t n_sessions) {
     if (ssm::check_params(p) != KDA_OK || n_sessions <= 0) return 0;
+    if (!ssm::decode_needs_workspace(p->num_heads, p->num_groups)) return 0;
     return ssm::align_up((size_t)n_sessions * (size_t)channels(p) * sizeof(float));
 }
 
@@ -262,9 +263,10 @@ kda_status kda_ssm_decode(const kda_ssm_params* p, int32_t n_sessions, const voi
     if ((st = check_tokens(p, xbc, &xbc_stride, dt, &dt_stride, z, &z_stride, o)) != KDA_OK) return st;
     if (!S || !ring || !aligned(S, 16) || !aligned(ring, 16)) return KDA_ERR_INVALID_ARG;
     if ((int64_t)n_sessions * channels(p) > (int64_t)INT32_MAX) return KDA_ERR_UNSUPPORTED;
-    if (workspace == nullptr || !aligned(workspace, WS_ALIGN) ||
-        workspace_bytes < kda_ssm_decode_workspace_bytes(p, n_sessions))
+    const size_t need = kda_ssm_decode_workspace_bytes(p, n_sessions);
+    if (need > 0 && (workspace == nullptr || !aligned(workspace, WS_ALIGN) || workspace_bytes < need))
         return KDA_ERR_WORKSPACE;
+    if ((int64_t)n_sessions * p->num_heads * 2 > (int64_t)INT32_MAX) return KDA_ERR_UNSUPPORTED;   // CTAs of the launch
     ssm::DecodeArgs a{xbc, dt, z, xbc_stride, dt_stride, z_stride, p->conv_w, p->conv_b, p->A_log, p->dt_bias, p->D,
                       slots, S, ring, o, static_cast<float*>(workspace), n_sessions, n_slots, p->num_heads, p->num_groups,
                       p->head_dim, p->state_dim};

@@ -31,7 +31,7 @@ struct DecodeArgs {
     float* S;
     void* ring;
     void* o;
-    float* u;                // workspace [n][Cx] fp32: the conv's outputs
+    float* u;                // workspace [n][Cx] fp32: the conv's outputs (large groups only)
     int32_t n, n_slots, H, G, P, N;
 };
 
@@ -66,6 +66,7 @@ __device__ __forceinline__ float2 silu2(float2 x) {
 cudaError_t launch_scan(const PrefillArgs& a, int io_bf16, cudaStream_t s);
 cudaError_t launch_ring(const PrefillArgs& a, int io_bf16, cudaStream_t s);
 cudaError_t launch_decode(const DecodeArgs& a, int io_bf16, cudaStream_t s);
+bool decode_needs_workspace(int H, int G);
 
 }  // namespace ssm
 }  // namespace kda

@@ -396,7 +396,8 @@ kda_status kda_ssm_prefill(const kda_ssm_params* p, const void* xbc, int64_t xbc
                            const float* S_in, float* S_out, const void* ring_in, void* ring_out,
                            void* o, void* workspace, size_t workspace_bytes, void* stream);
 
-/* Bytes of device workspace kda_ssm_decode needs (0 for rejected arguments). */
+/* Bytes of device workspace kda_ssm_decode needs: 0 for groups of up to 32
+ * heads (H <= 32 G), and for rejected arguments. */
 size_t kda_ssm_decode_workspace_bytes(const kda_ssm_params* p, int32_t n_sessions);
 
 /*
@@ -408,7 +409,8 @@ size_t kda_ssm_decode_workspace_bytes(const kda_ssm_params* p, int32_t n_session
  *   S, ring      : device pools [n_slots][H][N][P] fp32 and
  *                  [n_slots][3][H*P + 2*G*N] io_dtype
  *   o            : device [n_sessions][H*P] io_dtype
- *   workspace    : device, >= kda_ssm_decode_workspace_bytes(), 256-byte aligned
+ *   workspace    : device, >= kda_ssm_decode_workspace_bytes(), 256-byte aligned;
+ *                  may be NULL where that is 0
  */
 kda_status kda_ssm_decode(const kda_ssm_params* p, int32_t n_sessions, const void* xbc, int64_t xbc_stride,
                           const void* dt, int64_t dt_stride, const void* z, int64_t z_stride,

@@ -190,7 +190,9 @@ def test_prefill_is_deterministic_on_any_stream_and_in_a_graph(io):
 
 
 @pytest.mark.parametrize("io", ["f32", "bf16"])
-@pytest.mark.parametrize("H, P, N, G, n", [(2, 64, 64, 1, 1), (6, 64, 128, 3, 5), (3, 128, 64, 1, 3), (4, 128, 128, 2, 2)])
+@pytest.mark.parametrize("H, P, N, G, n", [(2, 64, 64, 1, 1), (6, 64, 128, 3, 5), (3, 128, 64, 1, 3), (4, 128, 128, 2, 2),
+                                           (1, 64, 128, 1, 2), (12, 64, 64, 1, 2), (17, 64, 64, 1, 1), (32, 64, 128, 1, 1),
+                                           (33, 64, 64, 1, 2), (80, 64, 64, 2, 1)])
 @pytest.mark.parametrize("gate, bias", [(True, True), (False, False)])
 def test_decode(io, H, P, N, G, n, gate, bias):
     i = make_inputs(n, n, H, P, N, G, IO[io], 21, bias=bias, skip=bias)

@@ -110,9 +110,10 @@ def test_decode_refusals(L, kw):
 
 
 def test_decode_workspace_and_empty(L):
-    p = struct()
+    assert L.kda_ssm_decode_workspace_bytes(ctypes.byref(struct(num_heads=32, num_groups=1)), 3) == 0
+    p = struct(num_heads=33, num_groups=1)
     need = L.kda_ssm_decode_workspace_bytes(ctypes.byref(p), 3)
-    assert need > 0
+    assert need >= 3 * (33 * 64 + 2 * 128) * 4
     assert decode(L, p, ws_bytes=need - 1) == kda.KDA_ERR_WORKSPACE
     assert decode(L, p, ws=None) == kda.KDA_ERR_WORKSPACE
     assert decode(L, p, n=0, ws=None) == kda.KDA_OK
