@@ -247,7 +247,7 @@ kda_status kda_ssm_prefill(const kda_ssm_params* p, const void* xbc, int64_t xbc
 
 size_t kda_ssm_decode_workspace_bytes(const kda_ssm_params* p, int32_t n_sessions) {
     if (ssm::check_params(p) != KDA_OK || n_sessions <= 0) return 0;
-    if (!ssm::decode_needs_workspace(p->num_heads, p->num_groups)) return 0;
+    if (!ssm::decode_needs_workspace(n_sessions, p->num_heads, p->num_groups, p->head_dim, p->state_dim)) return 0;
     return ssm::align_up((size_t)n_sessions * (size_t)channels(p) * sizeof(float));
 }
 

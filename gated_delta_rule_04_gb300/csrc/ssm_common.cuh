@@ -31,7 +31,7 @@ struct DecodeArgs {
     float* S;
     void* ring;
     void* o;
-    float* u;                // workspace [n][Cx] fp32: the conv's outputs (large groups only)
+    float* u;                // workspace [n][Cx] fp32: the conv's outputs (where decode_needs_workspace)
     int32_t n, n_slots, H, G, P, N;
 };
 
@@ -66,7 +66,8 @@ __device__ __forceinline__ float2 silu2(float2 x) {
 cudaError_t launch_scan(const PrefillArgs& a, int io_bf16, cudaStream_t s);
 cudaError_t launch_ring(const PrefillArgs& a, int io_bf16, cudaStream_t s);
 cudaError_t launch_decode(const DecodeArgs& a, int io_bf16, cudaStream_t s);
-bool decode_needs_workspace(int H, int G);
+// Whether a call of n sessions runs in two kernels, through the workspace.
+bool decode_needs_workspace(int64_t n, int H, int G, int P, int N);
 
 }  // namespace ssm
 }  // namespace kda

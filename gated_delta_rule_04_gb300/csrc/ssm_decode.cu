@@ -5,22 +5,30 @@
 // session's conv channels are 1 to 3 % of its state.  B and C of a group are
 // shared by its heads, and their ring is rolled in place, so it may be written
 // only when every head's CTA has read it:
-//   - fused_kernel: the heads of a (session, group) are one thread-block cluster
-//     (up to 16 CTAs of one or two heads).  Every CTA convolves the group's B and C
-//     for itself (6 KiB from L2 beside a 32 KiB state) and its own heads' x, and a
-//     cluster barrier stands between the last read of that ring and its write;
-//   - groups of more heads: conv_kernel takes every channel of every session
-//     through the conv into the workspace and rolls the ring, then state_kernel
-//     runs one CTA per (session, head).
-// One launch instead of two takes a single session's call from 19 to 14 us as
-// the caller sees it.
+//   - fused_kernel, for calls whose states are small enough that latency counts:
+//     the heads of a (session, group) are one thread-block cluster (up to 16 CTAs of
+//     one or two heads).  Every CTA convolves the group's B and C for itself (6 KiB
+//     from L2 beside a 32 KiB state) and its own heads' x, and a cluster barrier
+//     stands between the last read of that ring and its write.  One launch takes a
+//     single session's call from 19 to 15 us as the caller sees it;
+//   - otherwise conv_kernel takes every channel of every session through the conv
+//     into the workspace and rolls the ring, and state_kernel streams the states:
+//     persistent CTAs, the next state's 16 to 64 KiB prefetched into L2, the first
+//     one read while conv_kernel still runs.  256 sessions x 64 heads: 219 us
+//     fused, 192 us this way.
+#include <algorithm>
+
 #include "ssm_common.cuh"
+#include "tc_ptx.cuh"
 
 namespace kda {
 namespace ssm {
 namespace {
 
 constexpr int NT = 256;
+// Resident CTAs of the state kernel.  256 sessions x 64 heads of 128 x 64: 244 us with
+// two, 204 with three, 192 with four, 211 with six.
+constexpr int PER_SM = 4;
 
 template <typename TI>
 __global__ void __launch_bounds__(NT) conv_kernel(DecodeArgs g) {
@@ -29,6 +37,7 @@ __global__ void __launch_bounds__(NT) conv_kernel(DecodeArgs g) {
     const int per = Cx / V;
     const int64_t id = (int64_t)blockIdx.x * NT + threadIdx.x;
     const int n = (int)(id / per), c = (int)(id % per) * V;
+    cudaTriggerProgrammaticLaunchCompletion();   // the state kernel's first loads may start
     if (n >= g.n) return;
     const int slot = g.slots ? g.slots[n] : n;
     if (slot < 0 || slot >= g.n_slots) return;
@@ -53,51 +62,67 @@ __global__ void __launch_bounds__(NT) conv_kernel(DecodeArgs g) {
 }
 
 // Thread (rg, cq): state rows rg, rg + RG, ..., columns 4 cq .. 4 cq + 3.
+// Persistent CTAs walk the (session, head) items; the next item's state goes to
+// L2 while this one computes.
 template <typename TI, int P, int N>
-__global__ void __launch_bounds__(NT) state_kernel(DecodeArgs g) {
+__global__ void __launch_bounds__(NT, PER_SM) state_kernel(DecodeArgs g) {
     constexpr int CQ = P / 4, RG = NT / CQ, RN = N / RG;
-    __shared__ float4 part[NT / 32][CQ];
+    __shared__ float4 part[2][NT / 32][CQ];
     const int H = g.H, W = H * P, Cx = W + 2 * g.G * N;
-    const int n = blockIdx.x / H, h = blockIdx.x % H;
     const int tid = threadIdx.x, cq = tid % CQ, rg = tid / CQ;
-    const int slot = g.slots ? g.slots[n] : n;
-    if (slot < 0 || slot >= g.n_slots) return;
-    float4* Sg = reinterpret_cast<float4*>(g.S + ((size_t)slot * H + h) * N * P) + tid;
-    float4 S[RN];
+    const uint32_t items = (uint32_t)g.n * H;
+    int next_slot = g.slots ? g.slots[blockIdx.x / H] : blockIdx.x / H;
+    int buf = 0;
+#pragma unroll 1
+    for (uint32_t item = blockIdx.x; item < items; item += gridDim.x) {
+        const int n = item / H, h = item % H;
+        const int slot = next_slot;
+        if (item + gridDim.x < items) {
+            const int nn = (item + gridDim.x) / H, nh = (item + gridDim.x) % H;
+            next_slot = g.slots ? g.slots[nn] : nn;
+            if (tid == 0 && next_slot >= 0 && next_slot < g.n_slots)
+                ptx::bulk_prefetch_l2(g.S + ((size_t)next_slot * H + nh) * N * P, N * P * 4);
+        }
+        if (slot < 0 || slot >= g.n_slots) continue;
+        float4* Sg = reinterpret_cast<float4*>(g.S + ((size_t)slot * H + h) * N * P) + tid;
+        float4 S[RN];
 #pragma unroll
-    for (int i = 0; i < RN; ++i) S[i] = __ldcs(Sg + i * NT);
-    const float* u = g.u + (size_t)n * Cx;
-    const int grp = h / (H / g.G);
-    const float dt = softplus(to_f32(static_cast<const TI*>(g.dt)[(size_t)n * g.dt_stride + h]) + g.dt_bias[h]);
-    const float a = expf(-expf(g.A_log[h]) * dt);
-    const float4 x4 = *reinterpret_cast<const float4*>(u + h * P + 4 * cq);
-    const float4 xd = make_float4(dt * x4.x, dt * x4.y, dt * x4.z, dt * x4.w);
-    const float* B = u + W + grp * N;
-    const float* C = B + g.G * N;
-    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i = 0; i < RN; ++i) S[i] = __ldcs(Sg + i * NT);
+        const float* u = g.u + (size_t)n * Cx;
+        const int grp = h / (H / g.G);
+        const float dt = softplus(to_f32(static_cast<const TI*>(g.dt)[(size_t)n * g.dt_stride + h]) + g.dt_bias[h]);
+        const float a = expf(-expf(g.A_log[h]) * dt);
+        cudaGridDependencySynchronize();   // u is there (at once from the second item on)
+        const float4 x4 = *reinterpret_cast<const float4*>(u + h * P + 4 * cq);
+        const float4 xd = make_float4(dt * x4.x, dt * x4.y, dt * x4.z, dt * x4.w);
+        const float* B = u + W + grp * N;
+        const float* C = B + g.G * N;
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int i = 0; i < RN; ++i) {
-        const float b = B[rg + i * RG], c = C[rg + i * RG];
-        S[i].x = fmaf(a, S[i].x, b * xd.x); S[i].y = fmaf(a, S[i].y, b * xd.y);
-        S[i].z = fmaf(a, S[i].z, b * xd.z); S[i].w = fmaf(a, S[i].w, b * xd.w);
-        __stcs(Sg + i * NT, S[i]);
-        y.x = fmaf(c, S[i].x, y.x); y.y = fmaf(c, S[i].y, y.y);
-        y.z = fmaf(c, S[i].z, y.z); y.w = fmaf(c, S[i].w, y.w);
-    }
-    if (CQ == 16) {   // two row groups share a warp
-        y.x += __shfl_xor_sync(0xffffffffu, y.x, 16); y.y += __shfl_xor_sync(0xffffffffu, y.y, 16);
-        y.z += __shfl_xor_sync(0xffffffffu, y.z, 16); y.w += __shfl_xor_sync(0xffffffffu, y.w, 16);
-    }
-    if ((tid & 31) < CQ) part[tid >> 5][cq] = y;
-    __syncthreads();
-    if (tid < P) {
-        const float* pf = reinterpret_cast<const float*>(part);
-        float s = 0.f;
+        for (int i = 0; i < RN; ++i) {
+            const float b = B[rg + i * RG], c = C[rg + i * RG];
+            S[i].x = fmaf(a, S[i].x, b * xd.x); S[i].y = fmaf(a, S[i].y, b * xd.y);
+            S[i].z = fmaf(a, S[i].z, b * xd.z); S[i].w = fmaf(a, S[i].w, b * xd.w);
+            __stcs(Sg + i * NT, S[i]);
+            y.x = fmaf(c, S[i].x, y.x); y.y = fmaf(c, S[i].y, y.y);
+            y.z = fmaf(c, S[i].z, y.z); y.w = fmaf(c, S[i].w, y.w);
+        }
+        if (CQ == 16) {   // two row groups share a warp
+            y.x += __shfl_xor_sync(0xffffffffu, y.x, 16); y.y += __shfl_xor_sync(0xffffffffu, y.y, 16);
+            y.z += __shfl_xor_sync(0xffffffffu, y.z, 16); y.w += __shfl_xor_sync(0xffffffffu, y.w, 16);
+        }
+        if ((tid & 31) < CQ) part[buf][tid >> 5][cq] = y;
+        __syncthreads();   // (two buffers: the one read here is written again behind the next barrier)
+        if (tid < P) {
+            const float* pf = reinterpret_cast<const float*>(part[buf]);
+            float s = 0.f;
 #pragma unroll
-        for (int k = 0; k < NT / 32; ++k) s += pf[k * P + tid];
-        if (g.skip) s = fmaf(g.skip[h], u[h * P + tid], s);
-        if (g.z) s *= silu(to_f32(static_cast<const TI*>(g.z)[(size_t)n * g.z_stride + h * P + tid]));
-        static_cast<TI*>(g.o)[(size_t)n * W + h * P + tid] = from_f32<TI>(s);
+            for (int k = 0; k < NT / 32; ++k) s += pf[k * P + tid];
+            if (g.skip) s = fmaf(g.skip[h], u[h * P + tid], s);
+            if (g.z) s *= silu(to_f32(static_cast<const TI*>(g.z)[(size_t)n * g.z_stride + h * P + tid]));
+            static_cast<TI*>(g.o)[(size_t)n * W + h * P + tid] = from_f32<TI>(s);
+        }
+        buf ^= 1;
     }
 }
 
@@ -210,6 +235,12 @@ int cluster_size(int HG) {
     return HG <= 2 * cs ? cs : 0;
 }
 
+// The cluster size a call runs the fused kernel with, or 0.  Up to 32 MB of
+// states (5 us at HBM rate) a call costs less than its second launch.
+int fused_cluster(int64_t n, int H, int G, int P, int N) {
+    return n * H * N * P * 4 <= ((int64_t)32 << 20) ? cluster_size(H / G) : 0;
+}
+
 template <typename TI, int P, int N>
 cudaError_t fused(const DecodeArgs& a, int cs, cudaStream_t s) {
     auto k = fused_kernel<TI, P, N>;
@@ -230,9 +261,23 @@ cudaError_t fused(const DecodeArgs& a, int cs, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, k, a, cs);
 }
 
+template <typename TI, int P, int N>
+cudaError_t state(const DecodeArgs& a, cudaStream_t s) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)std::min<int64_t>((int64_t)a.n * a.H, 152 * PER_SM));
+    cfg.blockDim = dim3(NT);
+    cfg.stream = s;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, state_kernel<TI, P, N>, a);
+}
+
 template <typename TI>
 cudaError_t decode(const DecodeArgs& a, cudaStream_t s) {
-    if (const int cs = cluster_size(a.H / a.G)) {
+    if (const int cs = fused_cluster(a.n, a.H, a.G, a.P, a.N)) {
         if (a.P == 64) return a.N == 64 ? fused<TI, 64, 64>(a, cs, s) : fused<TI, 64, 128>(a, cs, s);
         return a.N == 64 ? fused<TI, 128, 64>(a, cs, s) : fused<TI, 128, 128>(a, cs, s);
     }
@@ -240,20 +285,13 @@ cudaError_t decode(const DecodeArgs& a, cudaStream_t s) {
     conv_kernel<TI><<<(unsigned)((a.n * per + NT - 1) / NT), NT, 0, s>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    const unsigned grid = (unsigned)((int64_t)a.n * a.H);
-    if (a.P == 64) {
-        if (a.N == 64) state_kernel<TI, 64, 64><<<grid, NT, 0, s>>>(a);
-        else state_kernel<TI, 64, 128><<<grid, NT, 0, s>>>(a);
-    } else {
-        if (a.N == 64) state_kernel<TI, 128, 64><<<grid, NT, 0, s>>>(a);
-        else state_kernel<TI, 128, 128><<<grid, NT, 0, s>>>(a);
-    }
-    return cudaGetLastError();
+    if (a.P == 64) return a.N == 64 ? state<TI, 64, 64>(a, s) : state<TI, 64, 128>(a, s);
+    return a.N == 64 ? state<TI, 128, 64>(a, s) : state<TI, 128, 128>(a, s);
 }
 
 }  // namespace
 
-bool decode_needs_workspace(int H, int G) { return cluster_size(H / G) == 0; }
+bool decode_needs_workspace(int64_t n, int H, int G, int P, int N) { return fused_cluster(n, H, G, P, N) == 0; }
 
 cudaError_t launch_decode(const DecodeArgs& a, int io_bf16, cudaStream_t s) {
     return io_bf16 ? decode<__nv_bfloat16>(a, s) : decode<float>(a, s);

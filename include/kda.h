@@ -396,8 +396,9 @@ kda_status kda_ssm_prefill(const kda_ssm_params* p, const void* xbc, int64_t xbc
                            const float* S_in, float* S_out, const void* ring_in, void* ring_out,
                            void* o, void* workspace, size_t workspace_bytes, void* stream);
 
-/* Bytes of device workspace kda_ssm_decode needs: 0 for groups of up to 32
- * heads (H <= 32 G), and for rejected arguments. */
+/* Bytes of device workspace kda_ssm_decode needs for n_sessions (or fewer, as
+ * long as this size does not shrink to 0): 0 where the call runs as one kernel
+ * (up to 32 MB of states and 32 heads a group), and for rejected arguments. */
 size_t kda_ssm_decode_workspace_bytes(const kda_ssm_params* p, int32_t n_sessions);
 
 /*

@@ -227,9 +227,26 @@ def test_decode_pool_and_skipped_sessions(io):
         assert torch.equal(S[s].cpu(), i["S"][s]) and torch.equal(ring[s].cpu(), i["ring"][s])
 
 
-def test_decode_in_a_graph_with_its_own_workspace():
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("P, N, H, n", [(64, 128, 16, 70), (128, 128, 8, 80), (64, 64, 40, 60)])
+def test_decode_larger_batches(io, P, N, H, n):
+    """More than 32 MB of states (two kernels), more items than resident CTAs."""
+    i = make_inputs(n, n, H, P, N, 4, IO[io], 23)
+    i["slots"] = torch.randperm(n, generator=torch.Generator().manual_seed(1))
+    p = params(i, io)
+    assert kda.kda_ssm_decode_workspace_bytes(p, n) > 0
+    S, ring = dev(i["S"]), dev(i["ring"])
+    o = kda.kda_ssm_decode(p, dev(i["xbc"]), dev(i["dt"]), S, ring, z=dev(i["z"]), slots=i["slots"].int().to(DEV))
+    wo, wS, wr = mixer({**i, "S": i["S"][i["slots"]], "ring": i["ring"][i["slots"]]}, list(range(n + 1)))
+    close("o", o, wo)
+    close("S", S.cpu()[i["slots"]], wS)
+    assert torch.equal(ring.cpu()[i["slots"]], wr)
+
+
+@pytest.mark.parametrize("H, G", [(4, 2), (40, 1)])
+def test_decode_in_a_graph_with_its_own_workspace(H, G):
     """Two captured calls, each with its workspace, replayed in turn."""
-    H, P, N, G = 4, 64, 128, 2
+    P, N = 64, 128
     graphs = []
     for seed in (31, 32):
         i = make_inputs(2, 2, H, P, N, G, torch.bfloat16, seed)
