@@ -645,6 +645,28 @@ __global__ void __launch_bounds__(NT, 2) commit_kernel(CommitArgs a) {
 #pragma unroll
         for (int r = 0; r < 16; ++r)
             Sr[r] = __ldcs(reinterpret_cast<const float4*>(Sg_in + (size_t)(16 * warp + r) * D) + lane);
+        // rows of the next item's path and ring into L2 (behind this state's loads, whose
+        // latency covers the path's)
+        if (item + gridDim.x < items && next_slot >= 0 && next_slot < a.n_slots) {
+            constexpr int LINES = D * sizeof(TI) / 128;
+            const int nn = (int)((item + gridDim.x) / H), nh = (int)((item + gridDim.x) % H);
+            if (tid < next_len && next_len <= a.max_len) {
+                const int node = a.path[(size_t)nn * a.max_len + tid];
+                if (node >= 0 && node < a.n_nodes) {
+                    const size_t off = (((size_t)nn * a.n_nodes + node) * W + (size_t)nh * D) * sizeof(TI);
+#pragma unroll
+                    for (int x = 0; x < LINES; ++x) {
+                        prefetch_l2(static_cast<const char*>(a.k) + off + 128 * x);
+                        prefetch_l2(static_cast<const char*>(a.v) + off + 128 * x);
+                        prefetch_l2(static_cast<const char*>(a.z) + off + 128 * x);
+                    }
+                }
+            } else if (tid >= NT - 3 * RING * LINES) {
+                const int x = tid - (NT - 3 * RING * LINES);
+                prefetch_l2(static_cast<const char*>(a.ring_in) +
+                            (((size_t)next_slot * 3 * RING + x / LINES) * W + (size_t)nh * D) * sizeof(TI) + x % LINES * 128);
+            }
+        }
         bool bad = false;
         if (tid < len) {
             const int node = a.path[(size_t)n * a.max_len + tid];
