@@ -2,14 +2,17 @@
 // the form for fp32 I/O, whose outputs tensor-core operands of 16 bits would
 // not reach.
 //
-// One CTA per (sequence, head), 256 threads; the N x P fp32 state stays in
-// registers over the whole sequence: thread (p, ng) holds the N / NG state
-// rows of group ng in column p, so the decay, the rank-one update and the
-// readout of a token are two FMAs per state element with the token's B and C
-// as shared-memory broadcasts, and no barrier per token.  Tokens go through in
-// blocks of TB: conv + SiLU of the block's x, B and C (each thread walks one
-// channel through the block, its window in registers), TB steps, then the sum
-// over the row groups, the skip and the gate.
+// One CTA of 256 threads per (sequence, head, PS columns of the head); its
+// N x PS part of the fp32 state stays in registers over the whole sequence:
+// thread (p, ng) holds N / NG state rows of column p, so a token costs two FMAs
+// per state element with its B and C as shared-memory broadcasts, and no
+// barrier.  Tokens go through in blocks of TB: conv + SiLU of the block's x, B
+// and C (each thread one channel, the next block's raw values already in
+// flight), TB steps, then the sum over the row groups, the skip and the gate.
+// The walk over a sequence is latency-bound, so few heads run with PS = 16: more
+// CTAs of shorter steps, each repeating the conv of B and C (5 sequences of 601
+// tokens in all, 8 heads of 64 x 64: 121 us with PS = 64, 69 us with 16); with
+// PS = 64 that repetition is gone, which pays once the SMs are full.
 #include "ssm_common.cuh"
 
 namespace kda {
@@ -19,24 +22,26 @@ namespace {
 constexpr int NT = 256;
 constexpr int TB = 16;   // tokens per block
 
-template <int P, int N>
+template <int N, int PS>
 struct ScanSmem {
-    float x[TB][P], B[TB][N], C[TB][N];
-    float part[TB][NT / P][P];   // readout partial sums by row group
-    float a[TB], dt[TB];
+    float x[2][TB][PS], B[2][TB][N], C[2][TB][N];   // two blocks in turn
+    float part[TB][NT / PS][PS];   // readout partial sums by row group
+    float a[2][TB], dt[2][TB];
 };
 
-template <typename TI, int P, int N>
+template <typename TI, int P, int N, int PS>
 __global__ void __launch_bounds__(NT) scan_kernel(PrefillArgs g) {
-    constexpr int NG = NT / P, RN = N / NG;
+    constexpr int NG = NT / PS, RN = N / NG, SL = P / PS;
+    constexpr int CHS = (PS + 2 * N + NT - 1) / NT;      // channels of a thread in the conv
     extern __shared__ __align__(16) unsigned char smem_raw[];
-    ScanSmem<P, N>& sm = *reinterpret_cast<ScanSmem<P, N>*>(smem_raw);
+    ScanSmem<N, PS>& sm = *reinterpret_cast<ScanSmem<N, PS>*>(smem_raw);
     const int H = g.H, W = H * P, Cx = W + 2 * g.G * N;
-    const int n = g.order[blockIdx.x / H], h = blockIdx.x % H;
+    const int slice = blockIdx.x % SL, h = blockIdx.x / SL % H, n = g.order[blockIdx.x / SL / H];
     const int grp = h / (H / g.G);
     const int64_t bos = g.cu[n], L = g.cu[n + 1] - bos;
-    const int tid = threadIdx.x, p = tid % P, ng = tid / P;
-    const size_t soff = ((size_t)n * H + h) * N * P;
+    const int tid = threadIdx.x, p = tid % PS, ng = tid / PS;
+    const int col0 = h * P + slice * PS;                 // this CTA's first channel of x
+    const size_t soff = ((size_t)n * H + h) * N * P + slice * PS;
 
     float S[RN];
 #pragma unroll
@@ -44,45 +49,65 @@ __global__ void __launch_bounds__(NT) scan_kernel(PrefillArgs g) {
 
     const TI* xbc = static_cast<const TI*>(g.xbc);
     const TI* ring = static_cast<const TI*>(g.ring_in);
-    // raw value of channel c at position t of the sequence (t >= -3)
-    auto raw = [&](int64_t t, int c) -> float {
-        if (t >= 0) return to_f32(xbc[(size_t)(bos + t) * g.xbc_stride + c]);
-        return ring ? to_f32(ring[((size_t)n * RING + (t + RING)) * Cx + c]) : 0.f;
-    };
+    // the conv channels of this thread: x of the slice, B, C
+    int c[CHS];
+    float4 w[CHS];
+    float bias[CHS], win[CHS][RING];
+#pragma unroll
+    for (int k = 0; k < CHS; ++k) {
+        const int j = tid + k * NT;
+        c[k] = j < PS ? col0 + j : j < PS + N ? W + grp * N + (j - PS) : j < PS + 2 * N ? W + (g.G + grp) * N + (j - PS - N) : -1;
+        w[k] = c[k] >= 0 ? __ldg(reinterpret_cast<const float4*>(g.conv_w) + c[k]) : make_float4(0.f, 0.f, 0.f, 0.f);
+        bias[k] = c[k] >= 0 && g.conv_b ? g.conv_b[c[k]] : 0.f;
+#pragma unroll
+        for (int s = 0; s < RING; ++s) win[k][s] = c[k] >= 0 && ring ? to_f32(ring[((size_t)n * RING + s) * Cx + c[k]]) : 0.f;
+    }
     const float eA = expf(g.A_log[h]), dtb = g.dt_bias[h], skip = g.skip ? g.skip[h] : 0.f;
-
+    TI raw[CHS][TB], raw_dt = TI(0.f);
+    auto load = [&](int64_t t0) {
+#pragma unroll
+        for (int k = 0; k < CHS; ++k)
+#pragma unroll
+            for (int t = 0; t < TB; ++t)
+                raw[k][t] = c[k] >= 0 && t0 + t < L ? xbc[(size_t)(bos + t0 + t) * g.xbc_stride + c[k]] : TI(0.f);
+        if (tid < TB && t0 + tid < L) raw_dt = static_cast<const TI*>(g.dt)[(size_t)(bos + t0 + tid) * g.dt_stride + h];
+    };
+    load(0);
+    int buf = 0;
 #pragma unroll 1
-    for (int64_t t0 = 0; t0 < L; t0 += TB) {
+    for (int64_t t0 = 0; t0 < L; t0 += TB, buf ^= 1) {
         const int nt = (int)(L - t0 < TB ? L - t0 : TB);
-        // ---- conv + SiLU: channel j of x (j < P), B, C
-        for (int j = tid; j < P + 2 * N; j += NT) {
-            const int c = j < P ? h * P + j : j < P + N ? W + grp * N + (j - P) : W + (g.G + grp) * N + (j - P - N);
-            const float4 w = __ldg(reinterpret_cast<const float4*>(g.conv_w) + c);
-            const float bias = g.conv_b ? g.conv_b[c] : 0.f;
-            float v0 = raw(t0 - 3, c), v1 = raw(t0 - 2, c), v2 = raw(t0 - 1, c);
-            float* dst = j < P ? &sm.x[0][j] : j < P + N ? &sm.B[0][j - P] : &sm.C[0][j - P - N];
-            const int ld = j < P ? P : N;
-            for (int t = 0; t < nt; ++t) {
-                const float v3 = raw(t0 + t, c);
-                dst[t * ld] = silu(fmaf(w.w, v3, fmaf(w.z, v2, fmaf(w.y, v1, fmaf(w.x, v0, bias)))));
-                v0 = v1; v1 = v2; v2 = v3;
+        // ---- conv + SiLU (rows past the sequence: of zeros, not used)
+#pragma unroll
+        for (int k = 0; k < CHS; ++k) {
+            const int j = tid + k * NT;
+            float* dst = j < PS ? &sm.x[buf][0][j] : j < PS + N ? &sm.B[buf][0][j - PS] : &sm.C[buf][0][j - PS - N];
+            const int ld = j < PS ? PS : N;
+            if (c[k] >= 0) {
+#pragma unroll
+                for (int t = 0; t < TB; ++t) {
+                    const float v = to_f32(raw[k][t]);
+                    dst[t * ld] = silu(fmaf(w[k].w, v, fmaf(w[k].z, win[k][2], fmaf(w[k].y, win[k][1], fmaf(w[k].x, win[k][0], bias[k])))));
+                    win[k][0] = win[k][1]; win[k][1] = win[k][2]; win[k][2] = v;
+                }
             }
         }
-        if (tid < nt) {
-            const float dt = softplus(to_f32(static_cast<const TI*>(g.dt)[(size_t)(bos + t0 + tid) * g.dt_stride + h]) + dtb);
-            sm.dt[tid] = dt;
-            sm.a[tid] = expf(-eA * dt);
+        if (tid < TB) {
+            const float dt = softplus(to_f32(raw_dt) + dtb);
+            sm.dt[buf][tid] = dt;
+            sm.a[buf][tid] = expf(-eA * dt);
         }
         __syncthreads();
+        if (t0 + TB < L) load(t0 + TB);
         // ---- the steps
-#pragma unroll 1
+#pragma unroll 4
         for (int t = 0; t < nt; ++t) {
-            const float a = sm.a[t], xd = sm.dt[t] * sm.x[t][p];
+            const float a = sm.a[buf][t], xd = sm.dt[buf][t] * sm.x[buf][t][p];
             float y0 = 0.f, y1 = 0.f;
 #pragma unroll
             for (int i = 0; i < RN; i += 4) {
-                const float4 b4 = *reinterpret_cast<const float4*>(&sm.B[t][ng * RN + i]);
-                const float4 c4 = *reinterpret_cast<const float4*>(&sm.C[t][ng * RN + i]);
+                const float4 b4 = *reinterpret_cast<const float4*>(&sm.B[buf][t][ng * RN + i]);
+                const float4 c4 = *reinterpret_cast<const float4*>(&sm.C[buf][t][ng * RN + i]);
                 S[i] = fmaf(a, S[i], b4.x * xd);
                 S[i + 1] = fmaf(a, S[i + 1], b4.y * xd);
                 S[i + 2] = fmaf(a, S[i + 2], b4.z * xd);
@@ -95,17 +120,16 @@ __global__ void __launch_bounds__(NT) scan_kernel(PrefillArgs g) {
             sm.part[t][ng][p] = y0 + y1;
         }
         __syncthreads();
-        // ---- outputs of the block
-        for (int i = tid; i < nt * P; i += NT) {
-            const int t = i / P, c = i % P;
-            float y = sm.part[t][0][c];
+        // ---- outputs of the block (its buffers are written again behind the next two barriers)
+        for (int i = tid; i < nt * PS; i += NT) {
+            const int t = i / PS, cc = i % PS;
+            float y = sm.part[t][0][cc];
 #pragma unroll
-            for (int k = 1; k < NG; ++k) y += sm.part[t][k][c];
-            y = fmaf(skip, sm.x[t][c], y);
-            if (g.z) y *= silu(to_f32(static_cast<const TI*>(g.z)[(size_t)(bos + t0 + t) * g.z_stride + h * P + c]));
-            static_cast<TI*>(g.o)[(size_t)(bos + t0 + t) * W + h * P + c] = from_f32<TI>(y);
+            for (int k = 1; k < NG; ++k) y += sm.part[t][k][cc];
+            y = fmaf(skip, sm.x[buf][t][cc], y);
+            if (g.z) y *= silu(to_f32(static_cast<const TI*>(g.z)[(size_t)(bos + t0 + t) * g.z_stride + col0 + cc]));
+            static_cast<TI*>(g.o)[(size_t)(bos + t0 + t) * W + col0 + cc] = from_f32<TI>(y);
         }
-        __syncthreads();
     }
 #pragma unroll
     for (int i = 0; i < RN; ++i) g.S_out[soff + (size_t)(ng * RN + i) * P + p] = S[i];
@@ -137,13 +161,23 @@ __global__ void __launch_bounds__(256) ring_kernel(PrefillArgs g) {
     for (int s = 0; s < RING; ++s) *reinterpret_cast<uint4*>(rout + ((size_t)n * RING + s) * Cx + c) = row[s];
 }
 
+template <typename TI, int P, int N, int PS>
+cudaError_t scan_ps(const PrefillArgs& a, cudaStream_t s) {
+    const int64_t blocks = (int64_t)a.n_seqs * a.H * (P / PS);
+    if (blocks > (int64_t)INT32_MAX) return cudaErrorInvalidValue;
+    constexpr int smem = (int)sizeof(ScanSmem<N, PS>);
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(scan_kernel<TI, P, N, PS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+    }
+    scan_kernel<TI, P, N, PS><<<(unsigned)blocks, NT, smem, s>>>(a);
+    return cudaGetLastError();
+}
+
 template <typename TI, int P, int N>
 cudaError_t scan(const PrefillArgs& a, cudaStream_t s) {
-    const int64_t blocks = (int64_t)a.n_seqs * a.H;
-    if (blocks > (int64_t)INT32_MAX) return cudaErrorInvalidValue;
-    static_assert(sizeof(ScanSmem<P, N>) <= 48 * 1024, "static shared memory limit");
-    scan_kernel<TI, P, N><<<(unsigned)blocks, NT, sizeof(ScanSmem<P, N>), s>>>(a);
-    return cudaGetLastError();
+    // narrow slices while their CTAs are at most four to an SM
+    return (int64_t)a.n_seqs * a.H * (P / 16) <= 4 * 152 ? scan_ps<TI, P, N, 16>(a, s) : scan_ps<TI, P, N, 64>(a, s);
 }
 
 template <typename TI>
