@@ -78,10 +78,13 @@ int units_per_group(const kda_ssm_params* p) {
 }
 
 // The most (sequence, piece) slots a call may cut its sequences into: enough
-// for two CTAs per SM, and none when the sequences alone fill the SMs.
+// for two CTAs per SM, or four pieces each where the sequences alone fill the
+// SMs (a long one among short ones still is the last to end); none from eight
+// sequence-units per SM on.
 int64_t piece_slots(const kda_ssm_params* p, int64_t n_seqs) {
     const int64_t units = (int64_t)units_per_group(p) * p->num_groups;
-    return n_seqs * units >= SMS_GB300 ? 0 : 2 * SMS_GB300 / units;
+    if (n_seqs * units >= 8 * SMS_GB300) return 0;
+    return std::max<int64_t>(2 * SMS_GB300 / units, 4 * n_seqs);
 }
 
 // Workspace of a prefill: error word | cu_seqlens | first chunks | order, and
@@ -113,30 +116,41 @@ Layout layout(const kda_ssm_params* p, int algo, int64_t n_seqs, int64_t total_t
 }
 
 // Pieces of lp chunks, np per sequence at most.  A cut costs the lite pass over
-// all pieces but the last (about LITE of a full chunk each); it pays when the
-// sequences' units leave SMs idle.  Times in chunks of one CTA per SM.
+// all pieces but each sequence's last (about LITE of a full chunk each); it pays
+// where the sequences' units leave SMs idle, all along or while the longest one
+// ends.  Times in chunks of one CTA per SM: a pass takes its work spread over
+// the SMs, and at least its longest item behind whatever started before it.
 struct Pieces {
     int np = 1, lp = 1;
 };
 Pieces plan_pieces(const kda_ssm_params* p, const int64_t* cu, int32_t n_seqs) {
     const int64_t units = (int64_t)units_per_group(p) * p->num_groups, slots = piece_slots(p, n_seqs);
-    int64_t longest = 1, total = 0;
-    for (int32_t i = 0; i < n_seqs; ++i) {
-        const int64_t c = (cu[i + 1] - cu[i] + CHUNK_T - 1) / CHUNK_T;
-        longest = std::max(longest, c);
-        total += c;
-    }
-    constexpr double LITE = 0.6;
+    int64_t longest = 1;
+    for (int32_t i = 0; i < n_seqs; ++i) longest = std::max(longest, (cu[i + 1] - cu[i] + CHUNK_T - 1) / CHUNK_T);
+    constexpr double LITE = 0.6, START = 4;              // an item's start (state, first loads), in chunks
     constexpr int64_t MIN_CHUNKS = 4;
-    Pieces best{1, (int)longest};
-    double best_t = (double)std::max(longest, total * units / SMS_GB300);
-    for (int64_t k = 2; k * n_seqs <= slots && longest >= k * MIN_CHUNKS; ++k) {
+    Pieces best;
+    double best_t = 0;
+    for (int64_t k = 1; k == 1 || (k * n_seqs <= slots && longest >= k * MIN_CHUNKS); ++k) {
         const int64_t lp = (longest + k - 1) / k;
-        int64_t pieces = 0;
-        for (int32_t i = 0; i < n_seqs; ++i) pieces += std::max<int64_t>(1, ((cu[i + 1] - cu[i] + CHUNK_T - 1) / CHUNK_T + lp - 1) / lp);
-        const int64_t waves = (pieces * units + SMS_GB300 - 1) / SMS_GB300;
-        const double t = (1.0 + LITE) * (double)(waves * lp);
-        if (t < best_t) {
+        int64_t items[2] = {0, 0}, work[2] = {0, 0};     // full pass, lite pass
+        for (int32_t i = 0; i < n_seqs; ++i) {
+            const int64_t c = (cu[i + 1] - cu[i] + CHUNK_T - 1) / CHUNK_T, pieces = std::max<int64_t>(1, (c + lp - 1) / lp);
+            items[0] += pieces;
+            work[0] += c;
+            items[1] += pieces - 1;
+            work[1] += (pieces - 1) * lp;
+        }
+        double t = 0;
+        for (int pass = 0; pass < 2; ++pass) {
+            if (items[pass] == 0) continue;
+            const double spread = ((double)work[pass] + START * (double)items[pass]) * units / SMS_GB300;
+            // equal items run in waves; a mixed lot ends about half its longest item after
+            // the even spread
+            const double item = (double)lp + START, waves = (double)((items[pass] * units + SMS_GB300 - 1) / SMS_GB300) * item;
+            t += (pass ? LITE : 1.0) * std::max(item, std::min(waves, spread + 0.5 * item));
+        }
+        if (k == 1 || t < best_t) {
             best_t = t;
             best = Pieces{(int)k, (int)lp};
         }
@@ -203,11 +217,16 @@ kda_status kda_ssm_prefill(const kda_ssm_params* p, const void* xbc, int64_t xbc
     }
     int64_t* d_cu = reinterpret_cast<int64_t*>(ws + L.cu);
     int32_t* d_order = reinterpret_cast<int32_t*>(ws + L.order);
-    if (cudaMemsetAsync(ws, 0, WS_ALIGN, s) != cudaSuccess) return KDA_ERR_CUDA;
     const bool chunked = algo == KDA_ALGO_CHUNKED;
     int64_t* d_coff = reinterpret_cast<int64_t*>(ws + L.coff);
     ChunkDesc* d_chunks = chunked ? reinterpret_cast<ChunkDesc*>(ws + L.chunks) : nullptr;
-    if (build_meta(cu, order.data(), n_seqs, 0, d_cu, d_coff, d_order, d_chunks, s) != cudaSuccess) return KDA_ERR_CUDA;
+    int64_t n_chunks = 0;
+    for (int32_t i = 0; i < n_seqs; ++i) n_chunks += (cu[i + 1] - cu[i] + CHUNK_T - 1) / CHUNK_T;
+    const bool in_args = chunked && n_seqs <= INLINE_SEQS;
+    // (the chunk preparation clears the error word itself)
+    if ((!chunked || n_chunks == 0) && cudaMemsetAsync(ws, 0, WS_ALIGN, s) != cudaSuccess) return KDA_ERR_CUDA;
+    if (!in_args && build_meta(cu, order.data(), n_seqs, 0, d_cu, d_coff, d_order, d_chunks, s) != cudaSuccess)
+        return KDA_ERR_CUDA;
     const int io_bf16 = p->io_dtype == KDA_DTYPE_BF16;
     ssm::PrefillArgs a{xbc, dt, z, xbc_stride, dt_stride, z_stride, p->conv_w, p->conv_b, p->A_log, p->dt_bias, p->D,
                        S_in, S_out, ring_in, ring_out, o, d_cu, d_order, n_seqs, p->num_heads, p->num_groups, p->head_dim,
@@ -219,8 +238,14 @@ kda_status kda_ssm_prefill(const kda_ssm_params* p, const void* xbc, int64_t xbc
         if (total_tokens > 0 && (!encode_rows_bf16(&c.map67, xbc, total_tokens, Cx, xbc_stride, CHUNK_T + RING) ||
                                  !encode_rows_bf16(&c.map64, xbc, total_tokens, Cx, xbc_stride, CHUNK_T)))
             return KDA_ERR_CUDA;
-        int64_t n_chunks = 0;
-        for (int32_t i = 0; i < n_seqs; ++i) n_chunks += (cu[i + 1] - cu[i] + CHUNK_T - 1) / CHUNK_T;
+        if (in_args) {
+            c.meta.n = n_seqs;
+            for (int32_t i = 0; i <= n_seqs; ++i) {
+                c.meta.cu[i] = (int32_t)cu[i];
+                c.meta.coff[i] = i == 0 ? 0 : c.meta.coff[i - 1] + (int32_t)((cu[i] - cu[i - 1] + CHUNK_T - 1) / CHUNK_T);
+                if (i < n_seqs) c.meta.order[i] = (uint8_t)order[i];
+            }
+        }
         const Pieces pc = plan_pieces(p, cu, n_seqs);
         c.chunks = d_chunks;
         c.coff = d_coff;
@@ -236,11 +261,14 @@ kda_status kda_ssm_prefill(const kda_ssm_params* p, const void* xbc, int64_t xbc
         c.upg = units_per_group(p);
         c.units = c.upg * p->num_groups;
         if (ssm::launch_chunk_prep(c, s) != cudaSuccess) return KDA_ERR_CUDA;
-        if (pc.np > 1 && launch_chunks(c, true, s) != cudaSuccess) return KDA_ERR_CUDA;
-        if (launch_chunks(c, false, s) != cudaSuccess) return KDA_ERR_CUDA;
-    } else if (ssm::launch_scan(a, io_bf16, s) != cudaSuccess) {
-        return KDA_ERR_CUDA;
+        // the passes may start beside the preparation's end when all its blocks run at once
+        // (2 us of a short call; behind a longer preparation they only take its SMs: 32768
+        // tokens x 96 heads 1.02 ms, without 0.99)
+        const bool beside = n_chunks > 0 && n_chunks * (p->num_groups + p->num_heads / 32 + 1) <= 2 * SMS_GB300;
+        if (pc.np > 1 && launch_chunks(c, true, beside, s) != cudaSuccess) return KDA_ERR_CUDA;
+        return launch_chunks(c, false, beside, s) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
     }
+    if (ssm::launch_scan(a, io_bf16, s) != cudaSuccess) return KDA_ERR_CUDA;
     if (ring_out && ssm::launch_ring(a, io_bf16, s) != cudaSuccess) return KDA_ERR_CUDA;
     return KDA_OK;
 }

@@ -56,14 +56,14 @@ static_assert(REG_X > REG_LAUNCH && REG_ISSUE < REG_LAUNCH && REG_ISSUE >= 24,
               "setmaxnreg.inc takes no smaller count than the current one, .dec no larger");
 constexpr int NX = 256, NY = 256;
 constexpr int NM = 96;                     // M threads: warps 17-19
-constexpr int BAR_X = 1, BAR_Y = 2, BAR_M = 3;   // named barriers
+constexpr int BAR_X = 1, BAR_Y = 2, BAR_M = 3, BAR_PAIR = 4;   // named barriers (BAR_PAIR + lane quarter)
 static_assert(288 % NM == 0, "M pieces per thread");
 constexpr uint32_t TM_S = 0, TM_SH = 128, TM_XF = 192, TM_XH = 224, TM_XL = 256, TM_DI = 288, TM_D = 352;
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint64_t WAIT_LIMIT_NS = 2000000000ull;
 constexpr int LDYS = 132;
 constexpr uint32_t ROW = 256;              // bytes of a unit's 128 channels
-constexpr uint32_t X_SLOT = 17408;         // 67 rows, rounded up to 1 KiB
+constexpr uint32_t X_SLOT = 67 * ROW;
 constexpr uint32_t STEP_BYTES = STEP_FLOATS * 4;
 constexpr uint32_t STEP_SLOT = 2 * STEP_BYTES + 16;   // two heads' step records, the group's scales
 
@@ -81,8 +81,8 @@ struct Map {                               // shared memory, from a 1 KiB aligne
     static constexpr uint32_t STEP = Y + 64 * LDYS * 4;               // NSTEP step slots
     static constexpr uint32_t SX = STEP + NSTEP * STEP_SLOT;          // fp32 [3][128] scale of D_h by channel
     static constexpr uint32_t SI = SX + 3 * 512;                      // fp32 [3][128] scale of DI
-    static constexpr uint32_t XM = SI + 3 * 512;                      // fp32 [2][128] row maxima by token half
-    static constexpr uint32_t BAR = XM + 1024;
+    static constexpr uint32_t XM = SI + 3 * 512;                      // fp32 [2 chunks][2][128] row maxima by token half
+    static constexpr uint32_t BAR = XM + 2048;
     static constexpr uint32_t BYTES = BAR + 256 + 1024;
     static_assert(REC % 1024 == 0 && M % 1024 == 0 && X % 128 == 0 && STEP % 16 == 0 && STEP_SLOT % 16 == 0 && BAR % 8 == 0, "");
     static_assert(BYTES <= 232448, "shared memory of one CTA");
@@ -123,17 +123,19 @@ __global__ void __launch_bounds__(NT, 1) chunk_kernel(const __grid_constant__ Ch
     constexpr int U = L::U;
     extern __shared__ unsigned char smem_raw[];
     const PrefillArgs& g = a.g;
+    cudaTriggerProgrammaticLaunchCompletion();
+    cudaGridDependencySynchronize();                     // the launch before this one has ended
     // ---- this CTA's unit, sequence and piece
     const int unit = blockIdx.x % a.units, piece = (blockIdx.x / a.units) % a.np;
-    const int seq = g.order[blockIdx.x / a.units / a.np];
-    const int64_t bos = g.cu[seq], len_seq = g.cu[seq + 1] - bos;
-    const int64_t nc_seq = a.coff[seq + 1] - a.coff[seq];
+    const int seq = seq_at(a, blockIdx.x / a.units / a.np);
+    const int64_t bos = seq_start(a, seq), len_seq = seq_start(a, seq + 1) - bos;
+    const int64_t nc_seq = first_chunk(a, seq + 1) - first_chunk(a, seq);
     const int64_t first = (int64_t)piece * a.lp;                       // first chunk in the sequence
     const bool last_piece = first + a.lp >= nc_seq;
     if (first > 0 && first >= nc_seq) return;
     if (LITE && last_piece) return;
     const int nc = (int)(nc_seq - first < a.lp ? nc_seq - first : a.lp);
-    const int64_t chunk0 = a.coff[seq] + first;                        // in the chunk table
+    const int64_t chunk0 = first_chunk(a, seq) + first;                // in the chunk table
     const int HG = g.H / g.G, grp = unit / a.upg, h0 = grp * HG + (unit % a.upg) * U;
     const int nh = min(U, (grp + 1) * HG - h0);                        // heads of this unit
     const int c0 = h0 * P, W = g.H * P, Cx = W + 2 * g.G * N;
@@ -142,7 +144,7 @@ __global__ void __launch_bounds__(NT, 1) chunk_kernel(const __grid_constant__ Ch
     unsigned char* sb = smem_raw + (base - raw);
     const uint32_t bars = base + L::BAR;
     const uint32_t b_x = bars, b_step = bars + 16, b_rec = bars + 56, b_m = bars + 72;   // [2], [NSTEP], [2], [2]
-    const uint32_t b_xready = bars + 88, b_done = bars + 96, b_dfree = bars + 104, b_drain = bars + 112, b_sdone = bars + 120, b_mfree = bars + 128;   // b_mfree: [2]
+    const uint32_t b_xready = bars + 88, b_done = bars + 96, b_dfree = bars + 104, b_drain = bars + 112, b_sdone = bars + 120, b_mfree = bars + 128, b_xfree = bars + 144;   // b_mfree: [2]
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sb + L::BAR + 160);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(sb + L::BAR + 164);
     volatile int* issued = reinterpret_cast<volatile int*>(sb + L::BAR + 168);   // loads issued: [0] x and steps, [1] records
@@ -160,7 +162,8 @@ __global__ void __launch_bounds__(NT, 1) chunk_kernel(const __grid_constant__ Ch
             ptx::mbar_init(b_mfree + 8 * i, 1);
         }
         for (int i = 0; i < NSTEP; ++i) ptx::mbar_init(b_step + 8 * i, 1);
-        ptx::mbar_init(b_xready, 1);
+        ptx::mbar_init(b_xready, NX / 32);
+        ptx::mbar_init(b_xfree, NX / 32);
         ptx::mbar_init(b_done, 1);
         ptx::mbar_init(b_dfree, NY / 32);
         ptx::mbar_init(b_drain, 1);
@@ -232,25 +235,23 @@ __global__ void __launch_bounds__(NT, 1) chunk_kernel(const __grid_constant__ Ch
         const float* start = piece == 0 && g.S_in ? g.S_in + ((size_t)seq * g.H + h) * state + p : nullptr;
         const float* loc = a.local + ((size_t)seq * a.np * g.H + h) * state + p;
         const float* ltot = a.ltot + (size_t)seq * a.np * g.H + h;
-        auto start_value = [&](int n) -> float {
-            if (!valid) return 0.f;
-            if (piece == 0) return start ? start[(size_t)n * P] : 0.f;
-            if (LITE) return 0.f;
-            float s = loc[(size_t)n * P];
-            for (int q = 1; q < piece; ++q)
-                s = fmaf(ex2(ltot[(size_t)q * g.H]), s, loc[(size_t)q * g.H * state + (size_t)n * P]);
-            return s;
-        };
         constexpr int NH = N / 2;                            // state columns of this thread
         float sbound = 0.f;
 #pragma unroll 1
         for (int j = 0; j < NH; j += 32) {
             float v[32];
+            // (columns inside, pieces outside: 32 loads in flight)
+            auto read = [&](const float* src, float decay) {
 #pragma unroll
-            for (int x = 0; x < 32; ++x) {
-                v[x] = start_value(NH * half + j + x);
-                sbound = fmaxf(sbound, fabsf(v[x]));
-            }
+                for (int x = 0; x < 32; ++x) v[x] = fmaf(decay, v[x], src[(size_t)(NH * half + j + x) * P]);
+            };
+#pragma unroll
+            for (int x = 0; x < 32; ++x) v[x] = 0.f;
+            if (valid && piece == 0 && start) read(start, 0.f);
+            if (valid && !LITE)
+                for (int q = 0; q < piece; ++q) read(loc + (size_t)q * g.H * state, q ? ex2(ltot[(size_t)q * g.H]) : 0.f);
+#pragma unroll
+            for (int x = 0; x < 32; ++x) sbound = fmaxf(sbound, fabsf(v[x]));
             ptx::tmem_st32(tlane + TM_S + NH * half + j, v);
         }
         xm[128 * half + ch] = sbound;
@@ -274,6 +275,29 @@ __global__ void __launch_bounds__(NT, 1) chunk_kernel(const __grid_constant__ Ch
         if (first == 0 && half == 0 && g.ring_in) {
             const __nv_bfloat16* r = static_cast<const __nv_bfloat16*>(g.ring_in) + (size_t)seq * RING * Cx + c0 + ch;
             r0 = to_f32(r[0]); r1 = to_f32(r[Cx]); r2 = to_f32(r[2 * (size_t)Cx]);
+        }
+        // The ring of this unit's channels and, by a group's first unit, of its B and C: the
+        // sequence's last three raw rows, older slots moved up when it has fewer.  The first
+        // piece does it: no other CTA of this launch reads those entries of ring_in, so
+        // ring_out may be ring_in.
+        if (!LITE && first == 0 && g.ring_out && half == 0) {
+            const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(g.xbc);
+            const __nv_bfloat16* rin = static_cast<const __nv_bfloat16*>(g.ring_in);
+            __nv_bfloat16* rout = static_cast<__nv_bfloat16*>(g.ring_out) + (size_t)seq * RING * Cx;
+            auto carry = [&](int cc) {
+                __nv_bfloat16 row[RING];
+#pragma unroll
+                for (int s = 0; s < RING; ++s) {
+                    const int64_t t = len_seq - RING + s;
+                    row[s] = t >= 0 ? x[(bos + t) * g.xbc_stride + cc]
+                             : rin  ? rin[((size_t)seq * RING + t + RING) * Cx + cc] : __nv_bfloat16(0.f);
+                }
+#pragma unroll
+                for (int s = 0; s < RING; ++s) rout[(size_t)s * Cx + cc] = row[s];
+            };
+            if (valid) carry(c0 + ch);
+            if (unit % a.upg == 0)
+                for (int x2 = ch; x2 < 2 * N; x2 += 128) carry(W + (x2 < N ? grp * N + x2 : g.G * N + grp * N + x2 - N));
         }
         float lsum = 0.f;
 #pragma unroll 1
@@ -315,18 +339,18 @@ __global__ void __launch_bounds__(NT, 1) chunk_kernel(const __grid_constant__ Ch
             for (int t = 0; t < 16; ++t) v[t] = silu2(v[t]);
 #pragma unroll
             for (int t = 0; t < 16; ++t) m = fmaxf(m, fmaxf(fabsf(v[t].x), fabsf(v[t].y)));
-            xm[128 * half + ch] = m;
-            if (ptx::bar_sync_or(BAR_X, NX, bad)) break;
-            if (tid == 0 && c + 2 < nc) {                    // the x tile is in registers
-                ptx::fence_async_smem();
-                load_x(c + 2);
-            }
+            float* xmc = xm + 256 * (c & 1);
+            xmc[128 * half + ch] = m;
+            // the two warps of a lane quarter exchange their maxima; nothing else ties the X
+            // warps together within a chunk
+            if (ptx::bar_sync_or(BAR_PAIR + quarter, 64, bad)) break;
+            if (lane == 0) mbar_arrive(b_xfree);             // this warp's part of the x tile is in registers
             // ---- scales
             const float* st = step_of(c, hh);
             const float lend = st[ST_LOG], dec = st[ST_DEC];
             const int edt = __float_as_int(st[ST_EDT]);
             const int2 ebc = scale_of(c);
-            const int ex = expo(fmaxf(xm[ch], xm[128 + ch]));
+            const int ex = expo(fmaxf(xmc[ch], xmc[128 + ch]));
             const float bound = fmaf(dec, sbound, pow2(9 + ex + edt + ebc.x));   // of |S| after this chunk
             int sn = (int)((__float_as_uint(bound) >> 23) & 255u) - 127 - 13;
             sn = sn < -100 ? -100 : sn > 100 ? 100 : sn;
@@ -359,10 +383,16 @@ __global__ void __launch_bounds__(NT, 1) chunk_kernel(const __grid_constant__ Ch
                     }
                 }
             }
+            if (tid == 0 && c + 2 < nc) {
+                bad = !wait_or_abort(b_xfree, (uint32_t)c & 1u, abort_flag);
+                ptx::fence_async_smem();
+                if (!bad) load_x(c + 2);
+            }
+            __syncwarp();
             // ---- the previous chunk's state and inter MMAs have read their operands and
             // written S (its intra MMAs, which come last, only hold X)
             if (c > 0) {
-                bad = !wait_or_abort(b_sdone, (uint32_t)(c - 1) & 1u, abort_flag);
+                bad = !wait_or_abort(b_sdone, (uint32_t)(c - 1) & 1u, abort_flag) || bad;
                 ptx::tc_fence_after();
             }
             ptx::tmem_st16u(tlane + TM_XH + 16 * half, xh);
@@ -394,8 +424,11 @@ __global__ void __launch_bounds__(NT, 1) chunk_kernel(const __grid_constant__ Ch
             if (!LITE) ptx::tmem_st16u(tlane + TM_XF + 16 * half, xf);
             ptx::tmem_wait_st();
             ptx::tc_fence_before();
-            if (ptx::bar_sync_or(BAR_X, NX, bad)) break;
-            if (tid == 0) mbar_arrive(b_xready);
+            if (__any_sync(0xffffffffu, bad)) {
+                *abort_flag = 1;                             // (the partner warp sees it at its next wait)
+                bad = true;
+            }
+            if (lane == 0 && !bad) mbar_arrive(b_xready);
             so = sn;
             sbound = bound;
             lsum += lend;
@@ -636,27 +669,36 @@ __global__ void __launch_bounds__(NT, 1) chunk_kernel(const __grid_constant__ Ch
 }
 
 template <int P, int N, bool LITE>
-cudaError_t launch(const ChunkArgs& a, cudaStream_t s) {
+cudaError_t launch(const ChunkArgs& a, bool after, cudaStream_t s) {
     const int64_t blocks = (int64_t)a.units * a.np * a.g.n_seqs;
     if (blocks > (int64_t)INT32_MAX) return cudaErrorInvalidValue;
     constexpr int smem = (int)Map<P, N>::BYTES;
     auto k = chunk_kernel<P, N, LITE>;
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    k<<<(unsigned)blocks, NT, smem, s>>>(a);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3(NT);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = after ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, k, a);
 }
 
 template <bool LITE>
-cudaError_t launch_pn(const ChunkArgs& a, cudaStream_t s) {
-    if (a.g.P == 64) return a.g.N == 64 ? launch<64, 64, LITE>(a, s) : launch<64, 128, LITE>(a, s);
-    return a.g.N == 64 ? launch<128, 64, LITE>(a, s) : launch<128, 128, LITE>(a, s);
+cudaError_t launch_pn(const ChunkArgs& a, bool after, cudaStream_t s) {
+    if (a.g.P == 64) return a.g.N == 64 ? launch<64, 64, LITE>(a, after, s) : launch<64, 128, LITE>(a, after, s);
+    return a.g.N == 64 ? launch<128, 64, LITE>(a, after, s) : launch<128, 128, LITE>(a, after, s);
 }
 
 }  // namespace
 
-cudaError_t launch_chunks(const ChunkArgs& a, bool lite, cudaStream_t s) {
-    return lite ? launch_pn<true>(a, s) : launch_pn<false>(a, s);
+cudaError_t launch_chunks(const ChunkArgs& a, bool lite, bool after, cudaStream_t s) {
+    return lite ? launch_pn<true>(a, after, s) : launch_pn<false>(a, after, s);
 }
 
 }  // namespace ssm

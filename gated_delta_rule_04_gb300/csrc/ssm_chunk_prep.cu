@@ -92,7 +92,9 @@ __global__ void __launch_bounds__(NT, 2) prep_kernel(const __grid_constant__ Chu
     const PrefillArgs& g = a.g;
     // the blocks of one chunk side by side: their pieces of a projection row are neighbours
     const int chunk = blockIdx.x / a.prep_blocks, grp = blockIdx.x % a.prep_blocks;
-    const ChunkDesc d = a.chunks[chunk];
+    cudaTriggerProgrammaticLaunchCompletion();   // the next launch's CTAs may take their places
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = ERR_NONE;   // this call's timeouts only
+    const ChunkDesc d = chunk_desc(a, chunk);
     if (grp >= g.G) {
         steps(a, d, chunk, grp - g.G, reinterpret_cast<float (*)[HB + 1]>(smem_raw));
         return;
