@@ -345,24 +345,45 @@ def kda_workspace_status(workspace, stream=None) -> int:
 # These run before every launch of a serving loop's smallest calls, whose kernels take a
 # few microseconds: one comparison each where the argument is right.
 
-def _shaped(name, t, dtype, shape):
-    """The address of a dense CUDA tensor of this type and shape, or ValueError."""
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
-        raise ValueError(f"{name}: expected a contiguous CUDA tensor {dtype} {list(shape)}, got "
+def _shaped(name, t, dtype, shape, dev):
+    """The address of a dense tensor of this type and shape on CUDA device ``dev``, or ValueError."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != dev or dev < 0:
+        raise ValueError(f"{name}: expected a contiguous tensor {dtype} {list(shape)} on CUDA device {max(dev, 0)}, got "
                          f"{'' if t.is_contiguous() else 'non-contiguous '}{t.dtype} {list(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
-def _pool(name, t, dtype, rest):
-    """(address, slots) of a dense CUDA tensor [slots][*rest] of this type."""
+def _pool(name, t, dtype, rest, dev):
+    """(address, slots) of a dense tensor [slots][*rest] of this type."""
     n = t.shape[0] if t.dim() else 0
-    return _shaped(name, t, dtype, (n, *rest)), n
+    return _shaped(name, t, dtype, (n, *rest), dev), n
 
 
-def _rows(name, t, dtype, n, width):
-    """(address, row stride in elements) of a [n][width] CUDA tensor whose rows may lie apart."""
-    if t.dtype is not dtype or t.shape != (n, width) or not t.is_cuda:
-        raise ValueError(f"{name}: expected a CUDA tensor {dtype} {[n, width]}, got {t.dtype} {list(t.shape)} on {t.device}")
+def _empty(like, shape, dtype, stream):
+    """A new tensor on ``like``'s device that belongs to ``stream`` (default: the current one), so
+    that its memory is neither still in use there nor reused before the call's kernels are done."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    import torch
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream, like.device) if isinstance(stream, int) else stream):
+        return like.new_empty(shape, dtype=dtype)
+
+
+def _workspace(t, like, nbytes, params, *sizes, stream=None):
+    """(tensor, address, bytes) of the caller's workspace, or of a new one of ``nbytes(params, *sizes)``."""
+    if t is None:
+        import torch
+        t = _empty(like, max(nbytes(params, *sizes), 256), torch.uint8, stream)
+    elif t.get_device() != like.get_device():
+        raise ValueError(f"workspace: expected a tensor on {like.device}, got {t.device}")
+    return t, t.data_ptr(), t.nbytes
+
+
+def _rows(name, t, dtype, n, width, dev):
+    """(address, row stride in elements) of a [n][width] tensor whose rows may lie apart."""
+    if t.dtype is not dtype or t.shape != (n, width) or t.get_device() != dev or dev < 0:
+        raise ValueError(f"{name}: expected a tensor {dtype} {[n, width]} on CUDA device {max(dev, 0)}, got {t.dtype} "
+                         f"{list(t.shape)} on {t.device}")
     stride, inner = t.stride()
     if width > 1 and inner != 1:
         raise ValueError(f"{name}: the elements of a row have to lie side by side")
@@ -374,14 +395,13 @@ def _rows(name, t, dtype, n, width):
 
 
 def _call(name, dev, f, *args, stream=None):
-    """Calls ``f`` with ``dev`` current, on ``stream`` (default: that device's current stream)."""
+    """Calls ``f`` with CUDA device ``dev`` current, on ``stream`` (default: that device's current stream)."""
     import torch
-    index = dev.index
-    if index != torch.cuda.current_device():
-        with torch.cuda.device(index):
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
             st = f(*args, _stream(stream))
     else:
-        st = f(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream))
+        st = f(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
     if st != KDA_OK:
         raise KdaError(st, name)
 
@@ -406,15 +426,15 @@ def kda_decode_tree(params: Params, q, k, v, z, b, gout, parents, S, ring, slots
     if q.dim() != 3:
         raise ValueError(f"q: expected [n][n_nodes][H*128], got {list(q.shape)}")
     n, R, _ = q.shape
-    H = params.num_heads
+    H, dev = params.num_heads, q.get_device()
     rows = (n, R, H * 128)
-    S_p, slots_n = _pool("S", S, torch.float32, (H, 128, 128))
-    args = (params.ref, n, R, _shaped("q", q, t, rows), _shaped("k", k, t, rows), _shaped("v", v, t, rows), _shaped("z", z, t, rows),
-            _shaped("b", b, t, (n, R, H)), _shaped("gout", gout, t, rows), _shaped("parents", parents, torch.int32, (n, R)),
-            None if slots is None else _shaped("slots", slots, torch.int32, (n,)), slots_n, S_p,
-            _shaped("ring", ring, t, (slots_n, 3, 3, H * 128)))
-    o = torch.empty_like(q) if o is None else o
-    _call("kda_decode_tree", q.device, lib().kda_decode_tree, *args, _shaped("o", o, t, rows), stream=stream)
+    S_p, slots_n = _pool("S", S, torch.float32, (H, 128, 128), dev)
+    args = (params.ref, n, R, _shaped("q", q, t, rows, dev), _shaped("k", k, t, rows, dev), _shaped("v", v, t, rows, dev),
+            _shaped("z", z, t, rows, dev), _shaped("b", b, t, (n, R, H), dev), _shaped("gout", gout, t, rows, dev),
+            _shaped("parents", parents, torch.int32, (n, R), dev), None if slots is None else _shaped("slots", slots, torch.int32, (n,), dev), slots_n, S_p,
+            _shaped("ring", ring, t, (slots_n, 3, 3, H * 128), dev))
+    o = _empty(q, rows, t, stream) if o is None else o
+    _call("kda_decode_tree", dev, lib().kda_decode_tree, *args, _shaped("o", o, t, rows, dev), stream=stream)
     return o
 
 
@@ -429,18 +449,18 @@ def kda_tree_commit(params: Params, q, k, v, z, b, path, path_len, S_in, ring_in
     if q.dim() != 3 or path.dim() != 2:
         raise ValueError(f"q, path: expected [n][n_nodes][H*128] and [n][max_len], got {list(q.shape)}, {list(path.shape)}")
     n, R, _ = q.shape
-    H, m = params.num_heads, path.shape[1]
+    H, m, dev = params.num_heads, path.shape[1], q.get_device()
     S_out = S_in if S_out is None else S_out
     ring_out = ring_in if ring_out is None else ring_out
     rows = (n, R, H * 128)
-    S_p, slots_n = _pool("S_in", S_in, torch.float32, (H, 128, 128))
+    S_p, slots_n = _pool("S_in", S_in, torch.float32, (H, 128, 128), dev)
     ring = (slots_n, 3, 3, H * 128)
-    _call("kda_tree_commit", q.device, lib().kda_tree_commit, params.ref, n, R, _shaped("q", q, t, rows), _shaped("k", k, t, rows),
-          _shaped("v", v, t, rows), _shaped("z", z, t, rows), _shaped("b", b, t, (n, R, H)),
-          _shaped("path", path, torch.int32, (n, m)), _shaped("path_len", path_len, torch.int32, (n,)), m,
-          None if slots is None else _shaped("slots", slots, torch.int32, (n,)), slots_n, S_p,
-          _shaped("S_out", S_out, torch.float32, (slots_n, H, 128, 128)), _shaped("ring_in", ring_in, t, ring),
-          _shaped("ring_out", ring_out, t, ring), stream=stream)
+    _call("kda_tree_commit", dev, lib().kda_tree_commit, params.ref, n, R, _shaped("q", q, t, rows, dev), _shaped("k", k, t, rows, dev),
+          _shaped("v", v, t, rows, dev), _shaped("z", z, t, rows, dev), _shaped("b", b, t, (n, R, H), dev),
+          _shaped("path", path, torch.int32, (n, m), dev), _shaped("path_len", path_len, torch.int32, (n,), dev), m,
+          None if slots is None else _shaped("slots", slots, torch.int32, (n,), dev), slots_n, S_p,
+          _shaped("S_out", S_out, torch.float32, (slots_n, H, 128, 128), dev), _shaped("ring_in", ring_in, t, ring, dev),
+          _shaped("ring_out", ring_out, t, ring, dev), stream=stream)
     return S_out, ring_out
 
 
@@ -455,15 +475,9 @@ class SsmParams:
     state_dim: int
     num_groups: int
     io_dtype: int
-
-    @property
-    def ref(self):
-        return ctypes.byref(self.struct)
-
-    @property
-    def channels(self) -> int:
-        """Conv channels of a token: x (H*P) | B (G*N) | C (G*N)."""
-        return self.num_heads * self.head_dim + 2 * self.num_groups * self.state_dim
+    channels: int         # conv channels of a token: x (H*P) | B (G*N) | C (G*N)
+    torch_dtype: object   # torch type of xbc, dt, z, o and the ring
+    ref: object           # pointer to the struct
 
 
 def make_ssm_params(conv_w, A_log, dt_bias, *, head_dim: int, state_dim: int, num_groups: int = 1, D=None, conv_b=None,
@@ -481,7 +495,7 @@ def make_ssm_params(conv_w, A_log, dt_bias, *, head_dim: int, state_dim: int, nu
     dt = {"f32": KDA_DTYPE_F32, "bf16": KDA_DTYPE_BF16}[io_dtype]
     tensors = tuple(None if x is None else x.contiguous() for x in (conv_w, conv_b, A_log, dt_bias, D))
     st = kda_ssm_params(H, int(head_dim), int(state_dim), int(num_groups), 4, dt, _ALGOS[algo], *[_ptr(x) for x in tensors])
-    return SsmParams(st, tensors, H, int(head_dim), int(state_dim), int(num_groups), dt)
+    return SsmParams(st, tensors, H, int(head_dim), int(state_dim), int(num_groups), dt, ch, _io_torch(dt), ctypes.byref(st))
 
 
 def kda_ssm_prefill_algo(params: SsmParams) -> str:
@@ -506,24 +520,23 @@ def kda_ssm_prefill(params: SsmParams, xbc, dt, cu_seqlens, z=None, S_in=None, S
     (o, S_out, ring_out)."""
     import torch
     cu, n, T = _cu_array(cu_seqlens)
-    t, H, P, N, ch = _io_torch(params.io_dtype), params.num_heads, params.head_dim, params.state_dim, params.channels
-    dev, f32 = xbc.device, torch.float32
-    x_p, sx = _rows("xbc", xbc, t, T, ch)
-    d_p, sd = _rows("dt", dt, t, T, H)
-    z_p, sz = (None, 0) if z is None else _rows("z", z, t, T, H * P)
-    S_p = None if S_in is None else _shaped("S_in", S_in, f32, (n, H, N, P))
-    r_p = None if ring_in is None else _shaped("ring_in", ring_in, t, (n, 3, ch))
+    t, H, P, N, ch = params.torch_dtype, params.num_heads, params.head_dim, params.state_dim, params.channels
+    dev, f32 = xbc.get_device(), torch.float32
+    x_p, sx = _rows("xbc", xbc, t, T, ch, dev)
+    d_p, sd = _rows("dt", dt, t, T, H, dev)
+    z_p, sz = (None, 0) if z is None else _rows("z", z, t, T, H * P, dev)
+    S_p = None if S_in is None else _shaped("S_in", S_in, f32, (n, H, N, P), dev)
+    r_p = None if ring_in is None else _shaped("ring_in", ring_in, t, (n, 3, ch), dev)
     if o is None:
-        o = torch.empty(T, H * P, dtype=t, device=dev)
+        o = _empty(xbc, (T, H * P), t, stream)
     if S_out is None:
-        S_out = torch.empty(n, H, N, P, dtype=f32, device=dev)
+        S_out = _empty(xbc, (n, H, N, P), f32, stream)
     if ring_out is None:
-        ring_out = torch.empty(n, 3, ch, dtype=t, device=dev)
-    if workspace is None:
-        workspace = torch.empty(max(kda_ssm_prefill_workspace_bytes(params, n, T), 256), dtype=torch.uint8, device=dev)
+        ring_out = _empty(xbc, (n, 3, ch), t, stream)
+    _, w_p, w_bytes = _workspace(workspace, xbc, kda_ssm_prefill_workspace_bytes, params, n, T, stream=stream)
     _call("kda_ssm_prefill", dev, lib().kda_ssm_prefill, params.ref, x_p, sx, d_p, sd, z_p, sz, cu, n, T, S_p,
-          _shaped("S_out", S_out, f32, (n, H, N, P)), r_p, _shaped("ring_out", ring_out, t, (n, 3, ch)),
-          _shaped("o", o, t, (T, H * P)), workspace.data_ptr(), workspace.numel() * workspace.element_size(), stream=stream)
+          _shaped("S_out", S_out, f32, (n, H, N, P), dev), r_p, _shaped("ring_out", ring_out, t, (n, 3, ch), dev),
+          _shaped("o", o, t, (T, H * P), dev), w_p, w_bytes, stream=stream)
     return o, S_out, ring_out
 
 
@@ -537,18 +550,17 @@ def kda_ssm_decode(params: SsmParams, xbc, dt, S, ring, z=None, slots=None, o=No
     per session, ``slots`` (int32 [n]) its pool slot.  Returns o."""
     import torch
     n = xbc.shape[0]
-    t, H, P, N, ch = _io_torch(params.io_dtype), params.num_heads, params.head_dim, params.state_dim, params.channels
-    dev = xbc.device
-    x_p, sx = _rows("xbc", xbc, t, n, ch)
-    d_p, sd = _rows("dt", dt, t, n, H)
-    z_p, sz = (None, 0) if z is None else _rows("z", z, t, n, H * P)
-    S_p, slots_n = _pool("S", S, torch.float32, (H, N, P))
-    r_p = _shaped("ring", ring, t, (slots_n, 3, ch))
-    s_p = None if slots is None else _shaped("slots", slots, torch.int32, (n,))
+    t, H, P, N, ch = params.torch_dtype, params.num_heads, params.head_dim, params.state_dim, params.channels
+    dev = xbc.get_device()
+    x_p, sx = _rows("xbc", xbc, t, n, ch, dev)
+    d_p, sd = _rows("dt", dt, t, n, H, dev)
+    z_p, sz = (None, 0) if z is None else _rows("z", z, t, n, H * P, dev)
+    S_p, slots_n = _pool("S", S, torch.float32, (H, N, P), dev)
+    r_p = _shaped("ring", ring, t, (slots_n, 3, ch), dev)
+    s_p = None if slots is None else _shaped("slots", slots, torch.int32, (n,), dev)
     if o is None:
-        o = torch.empty(n, H * P, dtype=t, device=dev)
-    if workspace is None:
-        workspace = torch.empty(max(kda_ssm_decode_workspace_bytes(params, n), 256), dtype=torch.uint8, device=dev)
+        o = _empty(xbc, (n, H * P), t, stream)
+    _, w_p, w_bytes = _workspace(workspace, xbc, kda_ssm_decode_workspace_bytes, params, n, stream=stream)
     _call("kda_ssm_decode", dev, lib().kda_ssm_decode, params.ref, n, x_p, sx, d_p, sd, z_p, sz, s_p, slots_n, S_p, r_p,
-          _shaped("o", o, t, (n, H * P)), workspace.data_ptr(), workspace.numel() * workspace.element_size(), stream=stream)
+          _shaped("o", o, t, (n, H * P), dev), w_p, w_bytes, stream=stream)
     return o

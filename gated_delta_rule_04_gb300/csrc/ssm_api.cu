@@ -53,7 +53,7 @@ kda_status resolve_algo(const kda_ssm_params* p, int* algo) {
 // for 16-byte rows, a multiple of 16 bytes.
 bool row_stride(int64_t given, int64_t width, size_t es, bool rows16, int64_t* out) {
     *out = given == 0 ? width : given;
-    if (*out < width || *out > (int64_t)1 << 40) return false;
+    if (*out < width || *out > (int64_t)INT32_MAX) return false;
     return !rows16 || (*out * (int64_t)es) % 16 == 0;
 }
 
@@ -197,7 +197,11 @@ kda_status kda_ssm_prefill(const kda_ssm_params* p, const void* xbc, int64_t xbc
     if (total_tokens > 0 && (st = check_tokens(p, xbc, &xbc_stride, dt, &dt_stride, z, &z_stride, o)) != KDA_OK) return st;
     if (S_out == nullptr || !aligned(S_out, 16) || !aligned(S_in, 16) || !aligned(ring_in, 16) || !aligned(ring_out, 16))
         return KDA_ERR_INVALID_ARG;
-    if ((int64_t)n_seqs * p->num_heads > (int64_t)INT32_MAX) return KDA_ERR_UNSUPPORTED;
+    // CTAs of the largest launch: pieces of units, the preparation's blocks, column slices
+    const int64_t chunks_most = total_tokens / CHUNK_T + std::min<int64_t>(n_seqs, total_tokens);
+    if ((int64_t)n_seqs * p->num_heads * 8 > (int64_t)INT32_MAX ||
+        chunks_most * (p->num_groups + p->num_heads / 32 + 1) > (int64_t)INT32_MAX)
+        return KDA_ERR_UNSUPPORTED;
     if (workspace == nullptr || !aligned(workspace, WS_ALIGN) ||
         workspace_bytes < kda_ssm_prefill_workspace_bytes(p, n_seqs, total_tokens))
         return KDA_ERR_WORKSPACE;

@@ -260,7 +260,8 @@ __global__ void __launch_bounds__(NT, 1) chunk_kernel(const __grid_constant__ Ch
         ptx::bar_sync_or(BAR_X, NX, false);
         int so = expo(2.f * sbound) - 13;                    // S = S' 2^so, |S'| < 2^14
         {
-            const float f = pow2(-so);
+            // (an infinite state value leaves the rest of its channel no scale: NaN for all of it)
+            const float f = sbound <= 3.4e38f ? pow2(-so) : __int_as_float(0x7fc00000);
 #pragma unroll 1
             for (int j = 0; j < NH; j += 32) {
                 float v[32];

@@ -74,6 +74,8 @@ __device__ void steps(const ChunkArgs& a, const ChunkDesc d, int chunk, int hb, 
         const float end = __shfl_sync(0xffffffffu, pre, 31);
         float* out = a.step + ((size_t)chunk * g.H + h) * STEP_FLOATS;
         *reinterpret_cast<float2*>(out + 2 * lane) = make_float2(cb + c0, cb + c0 + c1);
+        // (an infinite step leaves the others of the chunk no scale: NaN for all of them)
+        if (!(top <= 3.4e38f)) dt[0] = dt[1] = __int_as_float(0x7fc00000);
         *reinterpret_cast<float2*>(out + ST_DT + 2 * lane) = make_float2(dt[0], dt[1]);
         out[ST_W + w_at(2 * lane)] = ex2(l[1] + sa) * dt[0];
         out[ST_W + w_at(2 * lane + 1)] = ex2(sa) * dt[1];
@@ -171,7 +173,9 @@ __global__ void __launch_bounds__(NT, 2) prep_kernel(const __grid_constant__ Chu
     }
     const int eb = expo(mb), ec = expo(mc);
     if (tid == 0) a.scale[(size_t)chunk * g.G + grp] = make_int4(eb, ec, 0, 0);
-    const float s = pow2(is_c ? -ec : -eb);
+    // an infinity leaves no scale for the rest of its tile: all of it NaN, rather than
+    // finite rows that lost their digits
+    const float top = is_c ? mc : mb, s = top <= 3.4e38f ? pow2(is_c ? -ec : -eb) : __int_as_float(0x7fc00000);
     unsigned char* tile = is_c ? sC : sB;
 #pragma unroll
     for (int t = 0; t < TP; ++t) {

@@ -374,7 +374,7 @@ size_t kda_ssm_prefill_workspace_bytes(const kda_ssm_params* p, int32_t n_seqs, 
 /*
  * Stateful varlen prefill of the state space mixer over n_seqs packed sequences.
  *   xbc, xbc_stride : device io_dtype, row t at xbc + t * xbc_stride elements,
- *                  H*P + 2*G*N channels used.  Strides are in elements and let
+ *                  H*P + 2*G*N channels used.  Strides are in elements (below 2^31) and let
  *                  the three inputs be column ranges of one projection row; 0
  *                  selects packed rows.  xbc and z rows must start on 16 bytes
  *                  (stride * element size a multiple of 16).
@@ -389,6 +389,11 @@ size_t kda_ssm_prefill_workspace_bytes(const kda_ssm_params* p, int32_t n_seqs, 
  *   workspace      : device, >= kda_ssm_prefill_workspace_bytes(), 256-byte aligned;
  *                  its error word is read with kda_workspace_status
  * Zero-length sequences copy their state and ring through unchanged.
+ * The chunked algorithm takes 64 tokens at a time as matrix products of scaled
+ * fp16 operands (the state's as pairs): finite inputs up to 2^40 in magnitude
+ * keep their precision, and a NaN or an infinity may turn the outputs of its
+ * whole 64-token chunk in that group NaN, earlier tokens included, besides all
+ * that follows.  Other sequences never see it.
  */
 kda_status kda_ssm_prefill(const kda_ssm_params* p, const void* xbc, int64_t xbc_stride,
                            const void* dt, int64_t dt_stride, const void* z, int64_t z_stride,

@@ -144,6 +144,33 @@ def test_prefill_keeps_sequences_apart(io):
 
 
 @pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("where", ["x", "B", "C", "dt", "S"])
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+def test_prefill_non_finite_inputs_never_look_finite(io, where, value):
+    """Where the definition gives a finite value, the output has that value or
+    (the chunked form, from that chunk on) is not finite; an output the
+    definition has no finite value for is not finite either."""
+    H, P, N, G = 2, 64, 64, 1
+    i = make_inputs(140, 1, H, P, N, G, IO[io], 16)
+    at = {"x": 5, "B": H * P + 7, "C": H * P + N + 9}.get(where)
+    if at is not None:
+        i["xbc"][70, at] = value
+    elif where == "dt":
+        i["dt"][70, 1] = value
+    else:
+        i["S"][0, 1, 3, 4] = value
+    o, S, _ = prefill(i, io, [0, 140])
+    wo, wS, _ = mixer(i, [0, 140])
+    for got, want in ((o.cpu(), wo), (S.cpu(), wS)):
+        assert not (torch.isfinite(got) & ~torch.isfinite(want)).any()
+        both = torch.isfinite(got) & torch.isfinite(want)
+        assert both.any() or want is wS      # (the chunked form may lose a group's whole state)
+        close("finite part", torch.where(both, got, torch.zeros_like(got)), torch.where(both, want, torch.zeros_like(want)))
+    if where != "S":
+        assert torch.isfinite(o[:64]).all()
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
 def test_prefill_in_parts_and_then_tokens(io):
     """A prompt whole, in two parts, and its tail as single tokens."""
     T, H, P, N, G = 150, 4, 64, 128, 2
