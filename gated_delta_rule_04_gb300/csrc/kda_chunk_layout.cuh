@@ -76,9 +76,6 @@ struct PrepArgs {
     CUtensorMap map67[3], map64[3];
     int32_t gate_kind;              // KDA_GATE_BOUNDED or KDA_GATE_SOFTPLUS
 };
-// TMA descriptor of a bf16 tensor of T rows of W channels, `stride` elements
-// apart: boxes of `rows` rows x 128 channels, zero fill out of bounds.
-bool encode_rows_bf16(CUtensorMap* m, const void* base, int64_t T, int64_t W, int64_t stride, uint32_t rows);
 constexpr int PREP_BATCH = 4;        // most items per take from PrepArgs::work_counter
 // PrepArgs::wait_limit_ns from the parameters' test hook (0: the default)
 inline uint64_t prep_wait_limit_ns(const kda_params* p) { return (uint64_t)p->wait_limit_us * 1000ull; }

@@ -1381,19 +1381,20 @@ EncodeTiledFn encode_tiled_fn() {
     return fn;
 }
 
-}  // namespace
-
-bool encode_rows_bf16(CUtensorMap* m, const void* base, int64_t T, int64_t W, int64_t stride, uint32_t rows) {
+// [T][W] bf16 tensor, boxes of `rows` rows x 128 channels, zero fill out of bounds
+bool encode_rows(CUtensorMap* m, const void* base, int64_t T, int64_t W, uint32_t rows) {
     EncodeTiledFn enc = encode_tiled_fn();
     if (enc == nullptr) return false;
     const cuuint64_t dims[2] = {(cuuint64_t)W, (cuuint64_t)T};
-    const cuuint64_t strides[1] = {(cuuint64_t)stride * 2};
+    const cuuint64_t strides[1] = {(cuuint64_t)W * 2};
     const cuuint32_t box[2] = {(cuuint32_t)D, rows};
     const cuuint32_t estr[2] = {1, 1};
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+
+}  // namespace
 
 cudaError_t launch_chunk_prep(const PrepArgs& args, cudaStream_t s, int max_ctas) {
     const int64_t items = (int64_t)args.n_chunks * args.H;
@@ -1402,8 +1403,8 @@ cudaError_t launch_chunk_prep(const PrepArgs& args, cudaStream_t s, int max_ctas
     PrepArgs a = args;
     const void* planes[3] = {a.q, a.k, a.v};
     for (int pl = 0; pl < 3; ++pl)
-        if (!encode_rows_bf16(&a.map67[pl], planes[pl], a.T, (int64_t)a.H * D, (int64_t)a.H * D, C + RING) ||
-            !encode_rows_bf16(&a.map64[pl], planes[pl], a.T, (int64_t)a.H * D, (int64_t)a.H * D, C))
+        if (!encode_rows(&a.map67[pl], planes[pl], a.T, (int64_t)a.H * D, C + RING) ||
+            !encode_rows(&a.map64[pl], planes[pl], a.T, (int64_t)a.H * D, C))
             return cudaErrorInvalidValue;
     void (*kern)(PrepArgs) = a.gate_kind == KDA_GATE_SOFTPLUS ? chunk_prep_kernel<true> : chunk_prep_kernel<false>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);

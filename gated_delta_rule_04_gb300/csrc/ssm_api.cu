@@ -239,8 +239,8 @@ kda_status kda_ssm_prefill(const kda_ssm_params* p, const void* xbc, int64_t xbc
         ChunkArgs c{};
         c.g = a;
         const int64_t Cx = channels(p);
-        if (total_tokens > 0 && (!encode_rows_bf16(&c.map67, xbc, total_tokens, Cx, xbc_stride, CHUNK_T + RING) ||
-                                 !encode_rows_bf16(&c.map64, xbc, total_tokens, Cx, xbc_stride, CHUNK_T)))
+        if (total_tokens > 0 && (!encode_rows(&c.map67, xbc, total_tokens, Cx, xbc_stride, CHUNK_T + RING) ||
+                                 !encode_rows(&c.map64, xbc, total_tokens, Cx, xbc_stride, CHUNK_T)))
             return KDA_ERR_CUDA;
         if (in_args) {
             c.meta.n = n_seqs;

@@ -696,7 +696,27 @@ cudaError_t launch_pn(const ChunkArgs& a, bool after, cudaStream_t s) {
     return a.g.N == 64 ? launch<128, 64, LITE>(a, after, s) : launch<128, 128, LITE>(a, after, s);
 }
 
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
 }  // namespace
+
+bool encode_rows(CUtensorMap* m, const void* base, int64_t T, int64_t W, int64_t stride, uint32_t rows) {
+    static const EncodeTiled encode = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+                        q == cudaDriverEntryPointSuccess;
+        return ok ? reinterpret_cast<EncodeTiled>(f) : nullptr;
+    }();
+    if (encode == nullptr) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)W, (cuuint64_t)T}, strides[1] = {(cuuint64_t)stride * 2};
+    const cuuint32_t box[2] = {128, rows}, ones[2] = {1, 1};
+    return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, ones,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 cudaError_t launch_chunks(const ChunkArgs& a, bool lite, bool after, cudaStream_t s) {
     return lite ? launch_pn<true>(a, after, s) : launch_pn<false>(a, after, s);

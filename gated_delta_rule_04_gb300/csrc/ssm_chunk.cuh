@@ -94,6 +94,10 @@ __device__ __forceinline__ ChunkDesc chunk_desc(const ChunkArgs& a, int chunk) {
     return ChunkDesc{n, t0, left < CHUNK_T ? left : CHUNK_T, pos};
 }
 
+// TMA descriptor of T bf16 rows of W channels, `stride` elements apart: boxes of
+// `rows` rows x 128 channels, zero fill out of bounds.
+bool encode_rows(CUtensorMap* m, const void* base, int64_t T, int64_t W, int64_t stride, uint32_t rows);
+
 cudaError_t launch_chunk_prep(const ChunkArgs& a, cudaStream_t s);
 // lite: only the pieces' end states (all pieces but each sequence's last); the full
 // pass also writes the ring.  `after`: the launch follows another of this call and may
