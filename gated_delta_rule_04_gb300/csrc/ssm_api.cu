@@ -115,46 +115,121 @@ Layout layout(const kda_ssm_params* p, int algo, int64_t n_seqs, int64_t total_t
     return L;
 }
 
-// Pieces of lp chunks, np per sequence at most.  A cut costs the lite pass over
-// all pieces but each sequence's last (about LITE of a full chunk each); it pays
-// where the sequences' units leave SMs idle, all along or while the longest one
-// ends.  Times in chunks of one CTA per SM: a pass takes its work spread over
-// the SMs, and at least its longest item behind whatever started before it.
-struct Pieces {
-    int np = 1, lp = 1;
-};
-Pieces plan_pieces(const kda_ssm_params* p, const int64_t* cu, int32_t n_seqs) {
-    const int64_t units = (int64_t)units_per_group(p) * p->num_groups, slots = piece_slots(p, n_seqs);
-    int64_t longest = 1;
-    for (int32_t i = 0; i < n_seqs; ++i) longest = std::max(longest, (cu[i + 1] - cu[i] + CHUNK_T - 1) / CHUNK_T);
-    constexpr double LITE = 0.6, START = 4;              // an item's start (state, first loads), in chunks
-    constexpr int64_t MIN_CHUNKS = 4;
-    Pieces best;
-    double best_t = 0;
-    for (int64_t k = 1; k == 1 || (k * n_seqs <= slots && longest >= k * MIN_CHUNKS); ++k) {
-        const int64_t lp = (longest + k - 1) / k;
-        int64_t items[2] = {0, 0}, work[2] = {0, 0};     // full pass, lite pass
-        for (int32_t i = 0; i < n_seqs; ++i) {
-            const int64_t c = (cu[i + 1] - cu[i] + CHUNK_T - 1) / CHUNK_T, pieces = std::max<int64_t>(1, (c + lp - 1) / lp);
-            items[0] += pieces;
-            work[0] += c;
-            items[1] += pieces - 1;
-            work[1] += (pieces - 1) * lp;
-        }
-        double t = 0;
-        for (int pass = 0; pass < 2; ++pass) {
-            if (items[pass] == 0) continue;
-            const double spread = ((double)work[pass] + START * (double)items[pass]) * units / SMS_GB300;
-            // equal items run in waves; a mixed lot ends about half its longest item after
-            // the even spread
-            const double item = (double)lp + START, waves = (double)((items[pass] * units + SMS_GB300 - 1) / SMS_GB300) * item;
-            t += (pass ? LITE : 1.0) * std::max(item, std::min(waves, spread + 0.5 * item));
-        }
-        if (k == 1 || t < best_t) {
-            best_t = t;
-            best = Pieces{(int)k, (int)lp};
+// One launch of chunk walks on the SMs, one CTA each, in launch order: every SM
+// takes the next walk when it is free.  SMs that are free at the same time are
+// kept as one entry.
+class Schedule {
+public:
+    void add(int64_t walks, double time) {
+        while (walks > 0) {
+            const Entry e = free_[0];
+            const int64_t each = walks / SMS_GB300;          // whole waves of a large equal lot
+            if (n_ == 1 && each > 0) {
+                free_[0].at += time * (double)each;
+                walks -= each * SMS_GB300;
+                continue;
+            }
+            const int m = (int)std::min<int64_t>(e.count, walks);
+            if (m == e.count) {
+                for (int i = 1; i < n_; ++i) free_[i - 1] = free_[i];
+                --n_;
+            } else {
+                free_[0].count -= m;
+            }
+            int i = n_;                                      // after the entries of at <= e.at + time
+            while (i > 0 && free_[i - 1].at > e.at + time) --i;
+            if (i > 0 && free_[i - 1].at == e.at + time) {
+                free_[i - 1].count += m;
+            } else {
+                for (int x = n_; x > i; --x) free_[x] = free_[x - 1];
+                free_[i] = Entry{e.at + time, m};
+                ++n_;
+            }
+            walks -= m;
         }
     }
+    double end() const { return free_[n_ - 1].at; }
+
+private:
+    struct Entry {
+        double at;
+        int count;
+    };
+    Entry free_[SMS_GB300 + 1] = {{0.0, SMS_GB300}};
+    int n_ = 1;
+};
+
+// Pieces of a sequence: the first of lp0 chunks, then up to np - 1 of lp.  The
+// first launch walks the first pieces in full and, beside them, the pieces up to
+// the last but one for their end state only; the second walks all but the first.
+// A cut pays where the sequences' units leave SMs idle, all along or while the
+// longest one ends.  Both launches are played through for a range of cuts, walks
+// in the order sequence by sequence or piece by piece; the host does it while the
+// preparation runs (3 to 40 us).  With equal pieces and the first ones cut short
+// in the first launch too, 32768 tokens x 96 heads took 0.96 ms instead of 0.83, and
+// 8 sequences of 6 to 388 chunks x 64 heads 1.08 instead of 0.95.
+struct Pieces {
+    int np = 1, lp0 = 1, lp = 1;
+    bool by_piece = false;
+};
+Pieces plan_pieces(const kda_ssm_params* p, const int64_t* cu, const int32_t* order, int32_t n_seqs) {
+    const int64_t units = (int64_t)units_per_group(p) * p->num_groups, slots = piece_slots(p, n_seqs);
+    auto chunks = [&](int32_t i) { return (cu[order[i] + 1] - cu[order[i]] + CHUNK_T - 1) / CHUNK_T; };
+    const int64_t longest = std::max<int64_t>(1, chunks(0));
+    Pieces best;
+    best.lp0 = (int)longest;
+    constexpr int64_t MIN_CHUNKS = 4;                    // of the longest sequence, per piece
+    if (2 * (int64_t)n_seqs > slots || longest < 2 * MIN_CHUNKS) return best;
+    // in chunks of a full walk: a chunk of a walk for the end state, a walk's start (state,
+    // first loads), and the end state of a piece before it that it reads
+    constexpr double LITE = 0.6, START = 4, COMPOSE = 0.5;
+    constexpr int LOTS = 16;                             // more sequences count as lots of neighbours in length
+    int64_t lot[LOTS], lots = 0;
+    const int64_t per = (n_seqs + LOTS - 1) / LOTS;
+    for (int64_t i = 0; i < n_seqs; i += per) lot[lots++] = chunks((int32_t)i);
+    const int64_t walks = units * per;                   // of one piece of a lot
+
+    double best_t = 0;
+    auto play = [&](int64_t np, int64_t lp0, int64_t lp, bool by_piece) {
+        Schedule first, second;
+        auto pieces = [&](int64_t i) { return (std::max<int64_t>(0, lot[i] - lp0) + lp - 1) / lp; };   // but the first
+        auto lead = [&](int64_t i) { first.add(walks, START + (double)std::min(lot[i], lp0)); };
+        auto lite = [&](int64_t n) { first.add(walks * n, START + LITE * (double)lp); };
+        auto full = [&](int64_t i, int64_t q) {              // piece 1 + q of lot i
+            second.add(walks, START + COMPOSE * (double)q + (double)std::min(lp, lot[i] - lp0 - q * lp));
+        };
+        if (by_piece) {
+            for (int64_t i = 0; i < lots; ++i) lead(i);
+            for (int64_t q = 0; q < np - 1; ++q)
+                for (int64_t i = 0; i < lots && pieces(i) > q; ++i) {
+                    if (pieces(i) > q + 1) lite(1);
+                    full(i, q);
+                }
+        } else {
+            for (int64_t i = 0; i < lots; ++i) {
+                const int64_t k = pieces(i);
+                lead(i);
+                if (k == 0) continue;
+                lite(k - 1);
+                for (int64_t q = 0; q < k; ++q) full(i, q);
+            }
+        }
+        const double t = first.end() + second.end();
+        if (best_t == 0 || t < best_t) {
+            best_t = t;
+            best = Pieces{(int)np, (int)lp0, (int)lp, by_piece};
+        }
+    };
+    play(1, longest, 1, false);
+    // np in steps of a quarter, the first piece from as long as a lite walk of another to a
+    // few of them
+    for (int64_t np = 2; np * n_seqs <= slots && longest >= np * MIN_CHUNKS; np += std::max<int64_t>(1, np / 4))
+        for (const double r : {LITE, 1.0, 1.6, 2.4, 3.6}) {
+            const int64_t lp = (int64_t)ceil((double)longest / ((double)(np - 1) + r));
+            const int64_t lp0 = std::max<int64_t>(1, longest - (np - 1) * lp);
+            play(np, lp0, lp, false);
+            if (lots > 1) play(np, lp0, lp, true);
+        }
     return best;
 }
 
@@ -250,8 +325,7 @@ kda_status kda_ssm_prefill(const kda_ssm_params* p, const void* xbc, int64_t xbc
                 if (i < n_seqs) c.meta.order[i] = (uint8_t)order[i];
             }
         }
-        const Pieces pc = plan_pieces(p, cu, n_seqs);
-        c.chunks = d_chunks;
+                c.chunks = d_chunks;
         c.coff = d_coff;
         c.rec = ws + L.rec;
         c.step = reinterpret_cast<float*>(ws + L.step);
@@ -259,18 +333,20 @@ kda_status kda_ssm_prefill(const kda_ssm_params* p, const void* xbc, int64_t xbc
         c.status = reinterpret_cast<int32_t*>(ws);
         c.local = reinterpret_cast<float*>(ws + L.local);
         c.ltot = reinterpret_cast<float*>(ws + L.ltot);
-        c.np = pc.np;
-        c.lp = pc.lp;
         c.n_chunks = (int32_t)n_chunks;
         c.upg = units_per_group(p);
         c.units = c.upg * p->num_groups;
         if (ssm::launch_chunk_prep(c, s) != cudaSuccess) return KDA_ERR_CUDA;
+        const Pieces pc = plan_pieces(p, cu, order.data(), n_seqs);
+        c.np = pc.np;
+        c.lp0 = pc.lp0;
+        c.lp = pc.lp;
+        c.by_piece = pc.by_piece;
         // the passes may start beside the preparation's end when all its blocks run at once
         // (2 us of a short call; behind a longer preparation they only take its SMs: 32768
         // tokens x 96 heads 1.02 ms, without 0.99)
         const bool beside = n_chunks > 0 && n_chunks * (p->num_groups + p->num_heads / 32 + 1) <= 2 * SMS_GB300;
-        if (pc.np > 1 && launch_chunks(c, true, beside, s) != cudaSuccess) return KDA_ERR_CUDA;
-        return launch_chunks(c, false, beside, s) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+        return launch_chunks(c, beside, s) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
     }
     if (ssm::launch_scan(a, io_bf16, s) != cudaSuccess) return KDA_ERR_CUDA;
     if (ring_out && ssm::launch_ring(a, io_bf16, s) != cudaSuccess) return KDA_ERR_CUDA;

@@ -27,18 +27,28 @@
 // holds its own channel: in the decay of S and in the readout of Y.
 //
 // Warp roles.  Warps 0-7 (X group; warp % 4 = lane quarter, warp / 4 = token
-// half): conv, operands, S.  Warps 8-15 (Y group): M of the next chunk, then
-// the readout of this one: Y through a shared-memory tile to rows, gate,
-// store.  Warp 16 issues the MMAs.  All hand-offs are mbarriers; x, the step
-// records and the group records arrive by TMA and bulk copies, x two chunks
-// ahead.  Every wait is bounded: on timeout the kernel reports it in the
-// workspace's error word, lets its copies and MMAs land, frees its tensor
-// memory and returns.
+// half): conv, operands, S; the two warps of a quarter meet once a chunk, for the
+// maxima that set X's scale.  Warps 8-15 (Y group): the readout, Y through a
+// shared-memory tile to rows, gate, store.  Warps 17-19: M of the next chunk.  Warp
+// 16 issues the MMAs.  All hand-offs are mbarriers; x, the step records and the
+// group records arrive by TMA and bulk copies, x two chunks ahead.  Every wait is
+// bounded: on timeout the kernel reports it in the workspace's error word, lets its
+// copies and MMAs land, frees its tensor memory and returns.
 //
-// Few units leave SMs idle, so long sequences are cut into pieces of lp chunks
-// that run side by side: a lite pass (no S copy, no Y) first gives each piece's
-// end state from its own start, and a piece's true start is composed from the
-// pieces before it when it begins.
+// Few units leave SMs idle, so long sequences are cut into pieces that run side
+// by side.  A walk over S alone (LITE: no S copy, no M, no Y) takes 0.6 of a full
+// one and gives a piece's end state from a zero start; a piece's true start is
+// composed from the pieces before it when it begins.  The first piece needs no
+// start, so it is walked in full beside those.
+//
+// Measured: a full walk takes 3.0 us a chunk and a lite one 1.8 (64 tokens x 128
+// channels, N = 128), i.e. 32768 tokens x 96 heads of 64 in 0.67 ms.  The X group
+// sets that: its arithmetic on 64 x 128 values (conv, SiLU, scaling, three fp16
+// packings), the S row through registers, and the latency between them, at 54 % of
+// the issue slots, 43 % of shared memory and 16 % of L2; the tensor cores are at
+// 18 %.  Rows of x through registers rather than a shared tile, the split of M and
+// readout from the X group and packed fp32 pairs took it there from 4.4 us; eight
+// more X warps changed nothing.
 #include "ssm_chunk.cuh"
 #include "tc_ptx.cuh"
 
@@ -117,24 +127,21 @@ __device__ __forceinline__ int m_exponent(int edt, int eb, int ec, float skip) {
     return e > es ? e : es;
 }
 
+// One piece of a sequence's chunks for one unit.  LITE: its end state from a zero start only.
 template <int P, int N, bool LITE>
-__global__ void __launch_bounds__(NT, 1) chunk_kernel(const __grid_constant__ ChunkArgs a) {
+__device__ __forceinline__ void walk(const ChunkArgs& a, const int unit, const int seq, const int piece) {
     using L = Map<P, N>;
     constexpr int U = L::U;
     extern __shared__ unsigned char smem_raw[];
     const PrefillArgs& g = a.g;
-    cudaTriggerProgrammaticLaunchCompletion();
-    cudaGridDependencySynchronize();                     // the launch before this one has ended
-    // ---- this CTA's unit, sequence and piece
-    const int unit = blockIdx.x % a.units, piece = (blockIdx.x / a.units) % a.np;
-    const int seq = seq_at(a, blockIdx.x / a.units / a.np);
     const int64_t bos = seq_start(a, seq), len_seq = seq_start(a, seq + 1) - bos;
     const int64_t nc_seq = first_chunk(a, seq + 1) - first_chunk(a, seq);
-    const int64_t first = (int64_t)piece * a.lp;                       // first chunk in the sequence
-    const bool last_piece = first + a.lp >= nc_seq;
+    const int64_t first = piece == 0 ? 0 : a.lp0 + (int64_t)(piece - 1) * a.lp;   // first chunk in the sequence
+    const int64_t most = piece == 0 ? a.lp0 : a.lp;
+    const bool last_piece = first + most >= nc_seq;
     if (first > 0 && first >= nc_seq) return;
     if (LITE && last_piece) return;
-    const int nc = (int)(nc_seq - first < a.lp ? nc_seq - first : a.lp);
+    const int nc = (int)(nc_seq - first < most ? nc_seq - first : most);
     const int64_t chunk0 = first_chunk(a, seq) + first;                // in the chunk table
     const int HG = g.H / g.G, grp = unit / a.upg, h0 = grp * HG + (unit % a.upg) * U;
     const int nh = min(U, (grp + 1) * HG - h0);                        // heads of this unit
@@ -247,7 +254,7 @@ __global__ void __launch_bounds__(NT, 1) chunk_kernel(const __grid_constant__ Ch
             };
 #pragma unroll
             for (int x = 0; x < 32; ++x) v[x] = 0.f;
-            if (valid && piece == 0 && start) read(start, 0.f);
+            if (valid && !LITE && start) read(start, 0.f);
             if (valid && !LITE)
                 for (int q = 0; q < piece; ++q) read(loc + (size_t)q * g.H * state, q ? ex2(ltot[(size_t)q * g.H]) : 0.f);
 #pragma unroll
@@ -437,9 +444,9 @@ __global__ void __launch_bounds__(NT, 1) chunk_kernel(const __grid_constant__ Ch
         // ---- end state
         const bool ok = nc == 0 || wait_or_abort(b_done, (uint32_t)(nc - 1) & 1u, abort_flag);
         ptx::tc_fence_after();
-        if (ok && !*abort_flag && valid && (LITE || last_piece)) {
-            float* out = LITE ? a.local + (((size_t)seq * a.np + piece) * g.H + h) * state + p
-                              : g.S_out + ((size_t)seq * g.H + h) * state + p;
+        if (ok && !*abort_flag && valid && (LITE || last_piece || piece == 0)) {
+            float* out = last_piece ? g.S_out + ((size_t)seq * g.H + h) * state + p
+                                    : a.local + (((size_t)seq * a.np + piece) * g.H + h) * state + p;
             const float f = pow2(so);
 #pragma unroll 1
             for (int j = 0; j < NH; j += 32) {
@@ -669,12 +676,31 @@ __global__ void __launch_bounds__(NT, 1) chunk_kernel(const __grid_constant__ Ch
     }
 }
 
-template <int P, int N, bool LITE>
+// A call's pieces, in two launches where there is more than one: the first piece
+// of each sequence in full beside the lite walks of the pieces up to the last
+// but one (LEAD), then all pieces but the first (!LEAD).
+template <int P, int N, bool LEAD>
+__global__ void __launch_bounds__(NT, 1) chunk_kernel(const __grid_constant__ ChunkArgs a) {
+    cudaTriggerProgrammaticLaunchCompletion();
+    cudaGridDependencySynchronize();                     // the launch before this one has ended
+    const int per = LEAD && a.np == 1 ? 1 : a.np - 1;    // pieces of a sequence in this launch
+    const int unit = blockIdx.x % a.units, i = blockIdx.x / a.units;
+    const int piece = (a.by_piece ? i / a.g.n_seqs : i % per) + (LEAD ? 0 : 1);
+    const int seq = seq_at(a, a.by_piece ? i % a.g.n_seqs : i / per);
+    if constexpr (LEAD)
+        if (piece > 0) {
+            walk<P, N, true>(a, unit, seq, piece);
+            return;
+        }
+    walk<P, N, false>(a, unit, seq, piece);
+}
+
+template <int P, int N, bool LEAD>
 cudaError_t launch(const ChunkArgs& a, bool after, cudaStream_t s) {
-    const int64_t blocks = (int64_t)a.units * a.np * a.g.n_seqs;
+    const int64_t blocks = (int64_t)a.units * std::max(1, a.np - 1) * a.g.n_seqs;
     if (blocks > (int64_t)INT32_MAX) return cudaErrorInvalidValue;
     constexpr int smem = (int)Map<P, N>::BYTES;
-    auto k = chunk_kernel<P, N, LITE>;
+    auto k = chunk_kernel<P, N, LEAD>;
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
@@ -690,10 +716,10 @@ cudaError_t launch(const ChunkArgs& a, bool after, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, k, a);
 }
 
-template <bool LITE>
+template <bool LEAD>
 cudaError_t launch_pn(const ChunkArgs& a, bool after, cudaStream_t s) {
-    if (a.g.P == 64) return a.g.N == 64 ? launch<64, 64, LITE>(a, after, s) : launch<64, 128, LITE>(a, after, s);
-    return a.g.N == 64 ? launch<128, 64, LITE>(a, after, s) : launch<128, 128, LITE>(a, after, s);
+    if (a.g.P == 64) return a.g.N == 64 ? launch<64, 64, LEAD>(a, after, s) : launch<64, 128, LEAD>(a, after, s);
+    return a.g.N == 64 ? launch<128, 64, LEAD>(a, after, s) : launch<128, 128, LEAD>(a, after, s);
 }
 
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
@@ -718,8 +744,9 @@ bool encode_rows(CUtensorMap* m, const void* base, int64_t T, int64_t W, int64_t
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-cudaError_t launch_chunks(const ChunkArgs& a, bool lite, bool after, cudaStream_t s) {
-    return lite ? launch_pn<true>(a, after, s) : launch_pn<false>(a, after, s);
+cudaError_t launch_chunks(const ChunkArgs& a, bool after, cudaStream_t s) {
+    const cudaError_t e = launch_pn<true>(a, after, s);
+    return e != cudaSuccess || a.np == 1 ? e : launch_pn<false>(a, after, s);
 }
 
 }  // namespace ssm

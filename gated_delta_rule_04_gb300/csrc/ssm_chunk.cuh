@@ -73,11 +73,13 @@ struct ChunkArgs {
     float* step;                  // [n_chunks][H][STEP_FLOATS]
     int4* scale;                  // [n_chunks][G] exponents of B and C
     int32_t* status;
-    // Pieces of lp chunks (np per sequence at most) run side by side; `local`
-    // and `ltot` take each piece's end state from its own start and its log2 decay.
+    // Pieces run side by side, np per sequence at most: the first of lp0 chunks,
+    // the others of lp; `local` and `ltot` take each piece's end state from its own
+    // start (the first piece's: the sequence's) and its log2 decay.
     float* local;                 // [n_seqs][np][H][N][P]
     float* ltot;                  // [n_seqs][np][H]
-    int32_t np, lp;
+    int32_t np, lp0, lp;
+    int32_t by_piece;             // order of the walks: piece by piece, or sequence by sequence
     int32_t n_chunks, units, upg; // units of 128 channels, in all and per group
     int32_t prep_blocks;          // blocks of the preparation per chunk (set by launch_chunk_prep)
 };
@@ -99,10 +101,8 @@ __device__ __forceinline__ ChunkDesc chunk_desc(const ChunkArgs& a, int chunk) {
 bool encode_rows(CUtensorMap* m, const void* base, int64_t T, int64_t W, int64_t stride, uint32_t rows);
 
 cudaError_t launch_chunk_prep(const ChunkArgs& a, cudaStream_t s);
-// lite: only the pieces' end states (all pieces but each sequence's last); the full
-// pass also writes the ring.  `after`: the launch follows another of this call and may
-// start beside its end.
-cudaError_t launch_chunks(const ChunkArgs& a, bool lite, bool after, cudaStream_t s);
+// `after`: the first launch follows another of this call and may start beside its end.
+cudaError_t launch_chunks(const ChunkArgs& a, bool after, cudaStream_t s);
 
 }  // namespace ssm
 }  // namespace kda
