@@ -301,31 +301,31 @@ kda_status kda_ssm_prefill(const kda_ssm_params* p, const void* xbc, int64_t xbc
     ChunkDesc* d_chunks = chunked ? reinterpret_cast<ChunkDesc*>(ws + L.chunks) : nullptr;
     int64_t n_chunks = 0;
     for (int32_t i = 0; i < n_seqs; ++i) n_chunks += (cu[i + 1] - cu[i] + CHUNK_T - 1) / CHUNK_T;
-    const bool in_args = chunked && n_seqs <= INLINE_SEQS;
-    // (the chunk preparation clears the error word itself)
-    if ((!chunked || n_chunks == 0) && cudaMemsetAsync(ws, 0, WS_ALIGN, s) != cudaSuccess) return KDA_ERR_CUDA;
+    const bool in_args = n_seqs <= INLINE_SEQS;
+    // (the chunk preparation and the scan clear the error word themselves)
+    if (chunked && n_chunks == 0 && cudaMemsetAsync(ws, 0, WS_ALIGN, s) != cudaSuccess) return KDA_ERR_CUDA;
     if (!in_args && build_meta(cu, order.data(), n_seqs, 0, d_cu, d_coff, d_order, d_chunks, s) != cudaSuccess)
         return KDA_ERR_CUDA;
     const int io_bf16 = p->io_dtype == KDA_DTYPE_BF16;
     ssm::PrefillArgs a{xbc, dt, z, xbc_stride, dt_stride, z_stride, p->conv_w, p->conv_b, p->A_log, p->dt_bias, p->D,
                        S_in, S_out, ring_in, ring_out, o, d_cu, d_order, n_seqs, p->num_heads, p->num_groups, p->head_dim,
-                       p->state_dim};
+                       p->state_dim, total_tokens, {}};
+    if (in_args) {
+        a.meta.n = n_seqs;
+        for (int32_t i = 0; i <= n_seqs; ++i) {
+            a.meta.cu[i] = (int32_t)cu[i];
+            a.meta.coff[i] = i == 0 ? 0 : a.meta.coff[i - 1] + (int32_t)((cu[i] - cu[i - 1] + CHUNK_T - 1) / CHUNK_T);
+            if (i < n_seqs) a.meta.order[i] = (uint8_t)order[i];
+        }
+    }
     if (chunked) {
         ChunkArgs c{};
         c.g = a;
         const int64_t Cx = channels(p);
-        if (total_tokens > 0 && (!encode_rows(&c.map67, xbc, total_tokens, Cx, xbc_stride, CHUNK_T + RING) ||
-                                 !encode_rows(&c.map64, xbc, total_tokens, Cx, xbc_stride, CHUNK_T)))
+        if (total_tokens > 0 && (!encode_rows(&c.map67, xbc, 2, total_tokens, Cx, xbc_stride, CHUNK_T + RING, 128) ||
+                                 !encode_rows(&c.map64, xbc, 2, total_tokens, Cx, xbc_stride, CHUNK_T, 128)))
             return KDA_ERR_CUDA;
-        if (in_args) {
-            c.meta.n = n_seqs;
-            for (int32_t i = 0; i <= n_seqs; ++i) {
-                c.meta.cu[i] = (int32_t)cu[i];
-                c.meta.coff[i] = i == 0 ? 0 : c.meta.coff[i - 1] + (int32_t)((cu[i] - cu[i - 1] + CHUNK_T - 1) / CHUNK_T);
-                if (i < n_seqs) c.meta.order[i] = (uint8_t)order[i];
-            }
-        }
-                c.chunks = d_chunks;
+        c.chunks = d_chunks;
         c.coff = d_coff;
         c.rec = ws + L.rec;
         c.step = reinterpret_cast<float*>(ws + L.step);
@@ -348,7 +348,7 @@ kda_status kda_ssm_prefill(const kda_ssm_params* p, const void* xbc, int64_t xbc
         const bool beside = n_chunks > 0 && n_chunks * (p->num_groups + p->num_heads / 32 + 1) <= 2 * SMS_GB300;
         return launch_chunks(c, beside, s) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
     }
-    if (ssm::launch_scan(a, io_bf16, s) != cudaSuccess) return KDA_ERR_CUDA;
+    if (ssm::launch_scan(a, io_bf16, reinterpret_cast<int32_t*>(ws), s) != cudaSuccess) return KDA_ERR_CUDA;
     if (ring_out && ssm::launch_ring(a, io_bf16, s) != cudaSuccess) return KDA_ERR_CUDA;
     return KDA_OK;
 }

@@ -134,7 +134,7 @@ __device__ __forceinline__ void walk(const ChunkArgs& a, const int unit, const i
     constexpr int U = L::U;
     extern __shared__ unsigned char smem_raw[];
     const PrefillArgs& g = a.g;
-    const int64_t bos = seq_start(a, seq), len_seq = seq_start(a, seq + 1) - bos;
+    const int64_t bos = seq_start(g, seq), len_seq = seq_start(g, seq + 1) - bos;
     const int64_t nc_seq = first_chunk(a, seq + 1) - first_chunk(a, seq);
     const int64_t first = piece == 0 ? 0 : a.lp0 + (int64_t)(piece - 1) * a.lp;   // first chunk in the sequence
     const int64_t most = piece == 0 ? a.lp0 : a.lp;
@@ -686,7 +686,7 @@ __global__ void __launch_bounds__(NT, 1) chunk_kernel(const __grid_constant__ Ch
     const int per = LEAD && a.np == 1 ? 1 : a.np - 1;    // pieces of a sequence in this launch
     const int unit = blockIdx.x % a.units, i = blockIdx.x / a.units;
     const int piece = (a.by_piece ? i / a.g.n_seqs : i % per) + (LEAD ? 0 : 1);
-    const int seq = seq_at(a, a.by_piece ? i % a.g.n_seqs : i / per);
+    const int seq = seq_at(a.g, a.by_piece ? i % a.g.n_seqs : i / per);
     if constexpr (LEAD)
         if (piece > 0) {
             walk<P, N, true>(a, unit, seq, piece);
@@ -728,7 +728,7 @@ using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, 
 
 }  // namespace
 
-bool encode_rows(CUtensorMap* m, const void* base, int64_t T, int64_t W, int64_t stride, uint32_t rows) {
+bool encode_rows(CUtensorMap* m, const void* base, int es, int64_t T, int64_t W, int64_t stride, uint32_t rows, uint32_t cols) {
     static const EncodeTiled encode = [] {
         void* f = nullptr;
         cudaDriverEntryPointQueryResult q;
@@ -737,9 +737,9 @@ bool encode_rows(CUtensorMap* m, const void* base, int64_t T, int64_t W, int64_t
         return ok ? reinterpret_cast<EncodeTiled>(f) : nullptr;
     }();
     if (encode == nullptr) return false;
-    const cuuint64_t dims[2] = {(cuuint64_t)W, (cuuint64_t)T}, strides[1] = {(cuuint64_t)stride * 2};
-    const cuuint32_t box[2] = {128, rows}, ones[2] = {1, 1};
-    return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, ones,
+    const cuuint64_t dims[2] = {(cuuint64_t)W, (cuuint64_t)T}, strides[1] = {(cuuint64_t)stride * es};
+    const cuuint32_t box[2] = {cols, rows}, ones[2] = {1, 1};
+    return encode(m, es == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<void*>(base), dims, strides, box, ones,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }

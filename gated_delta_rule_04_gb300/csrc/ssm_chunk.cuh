@@ -53,20 +53,9 @@ __device__ __forceinline__ float pow2(int e) {
     e = e < -126 ? -126 : e > 127 ? 127 : e;
     return __uint_as_float((uint32_t)(e + 127) << 23);
 }
-// The tables of a call of a few sequences travel in the kernel arguments; more
-// sequences have them built on the device.
-constexpr int INLINE_SEQS = 16;
-struct InlineMeta {
-    int32_t n;                            // 0: the tables in global memory
-    int32_t cu[INLINE_SEQS + 1];          // token offsets (below 2^31: checked on the host)
-    int32_t coff[INLINE_SEQS + 1];        // first chunk of each sequence
-    uint8_t order[INLINE_SEQS];           // longest first
-};
-
 struct ChunkArgs {
     CUtensorMap map67, map64;     // xbc rows: boxes of 67 and 64 rows x 128 channels
     PrefillArgs g;
-    InlineMeta meta;
     const ChunkDesc* chunks;      // [n_chunks]
     const int64_t* coff;          // [n_seqs + 1]
     unsigned char* rec;           // [n_chunks][G][Rec::BYTES]
@@ -84,21 +73,15 @@ struct ChunkArgs {
     int32_t prep_blocks;          // blocks of the preparation per chunk (set by launch_chunk_prep)
 };
 
-__device__ __forceinline__ int64_t seq_start(const ChunkArgs& a, int n) { return a.meta.n ? a.meta.cu[n] : a.g.cu[n]; }
-__device__ __forceinline__ int64_t first_chunk(const ChunkArgs& a, int n) { return a.meta.n ? a.meta.coff[n] : a.coff[n]; }
-__device__ __forceinline__ int seq_at(const ChunkArgs& a, int i) { return a.meta.n ? a.meta.order[i] : a.g.order[i]; }
+__device__ __forceinline__ int64_t first_chunk(const ChunkArgs& a, int n) { return a.g.meta.n ? a.g.meta.coff[n] : a.coff[n]; }
 __device__ __forceinline__ ChunkDesc chunk_desc(const ChunkArgs& a, int chunk) {
-    if (a.meta.n == 0) return a.chunks[chunk];
+    if (a.g.meta.n == 0) return a.chunks[chunk];
     int n = 0;
     for (int i = 1; i < INLINE_SEQS; ++i)
-        if (i < a.meta.n && a.meta.coff[i] <= chunk) n = i;
-    const int pos = (chunk - a.meta.coff[n]) * CHUNK_T, t0 = a.meta.cu[n] + pos, left = a.meta.cu[n + 1] - t0;
+        if (i < a.g.meta.n && a.g.meta.coff[i] <= chunk) n = i;
+    const int pos = (chunk - a.g.meta.coff[n]) * CHUNK_T, t0 = a.g.meta.cu[n] + pos, left = a.g.meta.cu[n + 1] - t0;
     return ChunkDesc{n, t0, left < CHUNK_T ? left : CHUNK_T, pos};
 }
-
-// TMA descriptor of T bf16 rows of W channels, `stride` elements apart: boxes of
-// `rows` rows x 128 channels, zero fill out of bounds.
-bool encode_rows(CUtensorMap* m, const void* base, int64_t T, int64_t W, int64_t stride, uint32_t rows);
 
 cudaError_t launch_chunk_prep(const ChunkArgs& a, cudaStream_t s);
 // `after`: the first launch follows another of this call and may start beside its end.

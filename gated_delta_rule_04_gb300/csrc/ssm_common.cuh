@@ -1,10 +1,22 @@
 // Shared by the kernels of the selective state space mixer (sm_103a).
 #pragma once
 
+#include <cuda.h>
+
 #include "kda_common.cuh"
 
 namespace kda {
 namespace ssm {
+
+// The tables of a call of a few sequences travel in the kernel arguments; more
+// sequences have them built on the device.
+constexpr int INLINE_SEQS = 16;
+struct InlineMeta {
+    int32_t n;                            // 0: the tables in global memory
+    int32_t cu[INLINE_SEQS + 1];          // token offsets (below 2^31: checked on the host)
+    int32_t coff[INLINE_SEQS + 1];        // first chunk of each sequence (chunked form)
+    uint8_t order[INLINE_SEQS];           // longest first
+};
 
 // One prefill call, as the kernels see it.  Channels: x (W = H*P) | B (G*N) |
 // C (G*N), Cx = W + 2 G N in all; rows of xbc, dt and z are `*_stride`
@@ -21,7 +33,11 @@ struct PrefillArgs {
     const int64_t* cu;       // device [n_seqs + 1]
     const int32_t* order;    // device [n_seqs], longest first
     int32_t n_seqs, H, G, P, N;
+    int64_t T;               // total tokens
+    InlineMeta meta;         // instead of cu and order, if meta.n > 0
 };
+__device__ __forceinline__ int64_t seq_start(const PrefillArgs& g, int n) { return g.meta.n ? g.meta.cu[n] : g.cu[n]; }
+__device__ __forceinline__ int seq_at(const PrefillArgs& g, int i) { return g.meta.n ? g.meta.order[i] : g.order[i]; }
 
 struct DecodeArgs {
     const void *xbc, *dt, *z;
@@ -63,7 +79,12 @@ __device__ __forceinline__ float2 silu2(float2 x) {
     return __fmul2_rn(x, make_float2(rcp(d.x), rcp(d.y)));
 }
 
-cudaError_t launch_scan(const PrefillArgs& a, int io_bf16, cudaStream_t s);
+// TMA descriptor of T rows of W values of `es` bytes (2: bf16, 4: fp32), `stride`
+// values apart: boxes of `rows` rows x `cols` values, zero fill out of bounds.
+bool encode_rows(CUtensorMap* m, const void* base, int es, int64_t T, int64_t W, int64_t stride, uint32_t rows, uint32_t cols);
+
+// `status`: the workspace's error word, which the scan clears.
+cudaError_t launch_scan(const PrefillArgs& a, int io_bf16, int32_t* status, cudaStream_t s);
 cudaError_t launch_ring(const PrefillArgs& a, int io_bf16, cudaStream_t s);
 cudaError_t launch_decode(const DecodeArgs& a, int io_bf16, cudaStream_t s);
 // Whether a call of n sessions runs in two kernels, through the workspace.
