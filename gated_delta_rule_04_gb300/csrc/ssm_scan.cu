@@ -2,17 +2,20 @@
 // the form for fp32 I/O, whose outputs tensor-core operands of 16 bits would
 // not reach.
 //
-// One CTA of 256 threads per (sequence, head, PS columns of the head); its
-// N x PS part of the fp32 state stays in registers over the whole sequence:
-// thread (p, ng) holds N / NG state rows of column p, so a token costs two FMAs
-// per state element with its B and C as shared-memory broadcasts, and no
-// barrier.  Tokens go through in blocks of TB: conv + SiLU of the block's x, B
-// and C (each thread one channel, the next block's raw values already in
-// flight), TB steps, then the sum over the row groups, the skip and the gate.
-// The walk over a sequence is latency-bound, so few heads run with PS = 16: more
-// CTAs of shorter steps, each repeating the conv of B and C (5 sequences of 601
-// tokens in all, 8 heads of 64 x 64: 121 us with PS = 64, 69 us with 16); with
-// PS = 64 that repetition is gone, which pays once the SMs are full.
+// One CTA per (sequence, head, PS columns of the head); its N x PS part of the
+// fp32 state stays in registers over the whole sequence, a block of TB tokens at a
+// time.  Four things run side by side on warps of their own, one barrier a block:
+// the steps of block b, the sums, skip and gate of block b - 1's outputs, conv +
+// SiLU of block b + 1, and the copies (TMA) of the rows of block b + 3 with dt and
+// the decays of block b + 2.  In turn on the same threads they took three times as
+// long: the walk over a sequence is a chain of latencies.
+//
+// Few heads run with PS = 16: more CTAs of shorter steps, each repeating the conv
+// of B and C; with PS = 64 that repetition is gone, which pays once the SMs are
+// full.  5 sequences of 601 tokens in all, 8 heads of 64 x 64, fp32: 35 us (121 with
+// PS = 64 and the phases in turn, 69 with PS = 16), 90 ns a token of the longest;
+// 5000 tokens x 4 heads of 128 x 128: 0.59 ms.  Bound by shared-memory reads: a step
+// reads N values each of B and C for every CP columns, and the conv 7 rows for 4.
 #include <limits.h>
 
 #include "ssm_common.cuh"
@@ -22,16 +25,20 @@ namespace kda {
 namespace ssm {
 namespace {
 
-constexpr int NA = 256;                           // auxiliary threads: outputs, conv, copies
 constexpr int NG = 16;                            // row groups of the stepping threads
 constexpr int STAGES = 4;                         // blocks of raw rows
 constexpr uint64_t WAIT_LIMIT_NS = 2000000000ull;
 
-// CP columns per stepping thread, so that a B or C value read from shared memory
-// serves CP of them: reading those for one column each is what a step took its time on.
-template <int PS> struct Cols {
-    static constexpr int CP = PS == 16 ? 2 : 4, PQ = PS / CP, NS = PQ * NG;
-    static constexpr int PARTS = PS == 16 ? NG : NG / 2;   // partial sums of a column (wide: a warp's two added)
+// Threads by role: NS step, NC convolve, one warp copies, NO write outputs (0: the
+// convolving and copying ones do).  A thread holds CP columns for every B or C value
+// that it reads.  Narrow: CP = 2 with 4 warps (35 us above; one column with 8 warps
+// 49, CP = 4 with 2 warps 49).  Wide: CP = 4 with 8 warps (2048 tokens in 4 sequences,
+// 64 heads of 64 x 128, fp32: 0.24 ms; one column 0.47).
+template <int PS> struct Roles {
+    static constexpr int CP = PS == 16 ? 2 : 4, PQ = PS / CP, NS = PQ * NG, NC = 224, NO = PS == 16 ? 128 : 0;
+    static constexpr int NT = NS + NC + 32 + NO;
+    static constexpr int IN_WARP = PS == 16 ? 1 : 32 / PQ;   // row groups whose partial sums a warp adds
+    static constexpr int PARTS = NG / IN_WARP;
 };
 
 // Tensor maps of TB-row boxes: of PS columns of xbc and of z, of N columns of xbc.
@@ -50,22 +57,21 @@ struct ScanSmem {
     float B[2][TB][N], C[2][TB][N];               // two blocks in turn
     float xd[2][TB][PS];                          // dt x
     float x[3][TB][PS];
-    float part[2][TB][Cols<PS>::PARTS][PS];       // readout partial sums
+    float part[2][TB][Roles<PS>::PARTS][PS];       // readout partial sums
     float a[3][TB], dt[3][TB];
     float bias[CH];
     unsigned long long bar[STAGES];
     int stop;                                     // after a timeout: the block no one begins any more
 };
 
-// The first NS threads step block b while the last eight warps write block b - 1's
-// outputs, then convolve block b + 1 (seven of them) and send for the rows of
-// block b + 3 (one).
+// While block b is stepped, block b - 1's outputs are written, block b + 1 is
+// convolved and the rows of block b + 3 are sent for.
 template <typename TI, int P, int N, int PS, int TB>
-__global__ void __launch_bounds__(Cols<PS>::NS + NA, 2) scan_kernel(const __grid_constant__ PrefillArgs g,
+__global__ void __launch_bounds__(Roles<PS>::NT, 2) scan_kernel(const __grid_constant__ PrefillArgs g,
                                                                     const __grid_constant__ ScanMaps maps, int32_t* status) {
     using Smem = ScanSmem<TI, N, PS, TB>;
-    using K = Cols<PS>;
-    constexpr int NS = K::NS, CP = K::CP, RN = N / NG, SL = P / PS, CH = Smem::CH;
+    using K = Roles<PS>;
+    constexpr int NS = K::NS, CP = K::CP, NC = K::NC, RN = N / NG, SL = P / PS, CH = Smem::CH;
     extern __shared__ __align__(128) unsigned char smem_raw[];
     Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
     if (blockIdx.x == 0 && threadIdx.x == 0) *status = 0;
@@ -136,14 +142,14 @@ __global__ void __launch_bounds__(Cols<PS>::NS + NA, 2) scan_kernel(const __grid
                 }
 #pragma unroll
                 for (int e = 0; e < TG; ++e) {
-                    if constexpr (K::PARTS < NG) {       // the warp's other row group
 #pragma unroll
-                        for (int q = 0; q < CP; ++q) y[e][q] += __shfl_xor_sync(0xffffffffu, y[e][q], K::PQ);
-                        if (ng % 2 == 0)
-                            *reinterpret_cast<float4*>(&sm.part[buf][t + e][ng / 2][p]) = make_float4(y[e][0], y[e][1], y[e][2 % CP], y[e][3 % CP]);
-                    } else {
-                        *reinterpret_cast<float2*>(&sm.part[buf][t + e][ng][p]) = make_float2(y[e][0], y[e][1]);
-                    }
+                    for (int o = K::PQ; o < K::PQ * K::IN_WARP; o <<= 1)
+#pragma unroll
+                        for (int q = 0; q < CP; ++q) y[e][q] += __shfl_xor_sync(0xffffffffu, y[e][q], o);
+                    if (ng % K::IN_WARP == 0)
+#pragma unroll
+                        for (int q = 0; q < CP; q += 2)
+                            *reinterpret_cast<float2*>(&sm.part[buf][t + e][ng / K::IN_WARP][p + q]) = make_float2(y[e][q], y[e][q + 1]);
                 }
             }
             __syncthreads();
@@ -159,12 +165,13 @@ __global__ void __launch_bounds__(Cols<PS>::NS + NA, 2) scan_kernel(const __grid
         return;
     }
     // ---- rows, conv and outputs
-    const int tid = threadIdx.x - NS;
+    const int tid = threadIdx.x - NS, lane = tid - NC, otid = K::NO ? tid - NC - 32 : tid;
+    constexpr int OUT = K::NO ? K::NO : NC + 32;         // output threads
     const TI* dts = static_cast<const TI*>(g.dt) + bos * g.dt_stride + h;
     auto channel = [&](int j) { return j < PS ? col0 + j : j < PS + N ? W + grp * N + (j - PS) : W + (g.G + grp) * N + (j - PS - N); };
     auto raw_at = [&](int j) { return j < PS ? &sm.rx[0][j] : j < PS + N ? &sm.rB[0][j - PS] : &sm.rC[0][j - PS - N]; };
     auto raw_ld = [&](int j) { return j < PS ? PS : N; };
-    for (int j = tid; j < CH; j += NA) {
+    for (int j = tid; j < CH; j += K::NT - NS) {
         const int c = channel(j);
         sm.w[j] = __ldg(reinterpret_cast<const float4*>(g.conv_w) + c);
         sm.bias[j] = g.conv_b ? g.conv_b[c] : 0.f;
@@ -173,12 +180,10 @@ __global__ void __launch_bounds__(Cols<PS>::NS + NA, 2) scan_kernel(const __grid
             *(raw_at(j) + (STAGES * TB - RING + s) * raw_ld(j)) = g.ring_in ? static_cast<const TI*>(g.ring_in)[((size_t)n * RING + s) * Cx + c] : TI(0.f);
     }
     const float eA = expf(g.A_log[h]), dtb = g.dt_bias[h], skip = g.skip ? g.skip[h] : 0.f;
-    // One warp sends for the raw rows of block b and z of the block before it, and has dt and
+    // One warp (lane 0 .. 31) sends for the raw rows of block b and z of the block before it, and has dt and
     // the decays ready a block ahead of the conv, which multiplies x by dt.  A tile is one
     // tensor copy; row by row one warp took longer to send than the steps take.  (Rows past
     // the sequence are another's or zeros, and not used.)
-    constexpr int NC = NA - 32;                          // conv threads
-    const int lane = tid - NC;
     auto bytes = [&](int b) { return (uint32_t)sizeof(TI) * TB * ((b < nb ? CH : 0) + (g.z && b > 0 && b <= nb ? PS : 0)); };
     auto load = [&](int b) {
         const uint32_t bar = ptx::smem_u32(&sm.bar[b % STAGES]), all = bytes(b);
@@ -210,23 +215,31 @@ __global__ void __launch_bounds__(Cols<PS>::NS + NA, 2) scan_kernel(const __grid
             sm.a[b % 3][lane] = in ? expf(-eA * dt) : 1.f;
         }
     };
-    auto conv = [&](int b) {                             // four tokens of a channel; past the sequence: zeros
+    // conv: items of four tokens of a channel, all of a thread's read before the first is
+    // written; past the sequence zeros
+    constexpr int ITEMS = CH * (TB / 4), MINE = (ITEMS + NC - 1) / NC;
+    auto conv = [&](int b) {
         const int buf = b & 1;
-#pragma unroll 2
-        for (int i = tid; i < CH * (TB / 4); i += NC) {
-            const int j = i % CH, t0 = i / CH * 4;
+        float v[MINE][4 + RING];
+#pragma unroll
+        for (int k = 0; k < MINE; ++k) {
+            const int i = min(tid + k * NC, ITEMS - 1), j = i % CH, t0 = i / CH * 4, ld = raw_ld(j);
+            const TI* src = raw_at(j);
+#pragma unroll
+            for (int e = 0; e < 4 + RING; ++e) v[k][e] = to_f32(src[((b * TB + t0 + e - RING) & (STAGES * TB - 1)) * ld]);
+        }
+#pragma unroll
+        for (int k = 0; k < MINE; ++k) {
+            const int i = min(tid + k * NC, ITEMS - 1), j = i % CH, t0 = i / CH * 4, ld = raw_ld(j);
             const float4 w = sm.w[j];
             const float bias = sm.bias[j];
-            const TI* src = raw_at(j);
-            const int ld = raw_ld(j);
-            float v[4 + RING], u[4];
-#pragma unroll
-            for (int k = 0; k < 4 + RING; ++k) v[k] = to_f32(src[((b * TB + t0 + k - RING) & (STAGES * TB - 1)) * ld]);
+            float u[4];
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
-                u[t] = silu(fmaf(w.w, v[t + 3], fmaf(w.z, v[t + 2], fmaf(w.y, v[t + 1], fmaf(w.x, v[t], bias)))));
+                u[t] = silu(fmaf(w.w, v[k][t + 3], fmaf(w.z, v[k][t + 2], fmaf(w.y, v[k][t + 1], fmaf(w.x, v[k][t], bias)))));
                 if ((uint32_t)b * TB + t0 + t >= L) u[t] = 0.f;
             }
+            if (tid + k * NC >= ITEMS) break;
             if (j < PS) {
                 const float4 d4 = *reinterpret_cast<const float4*>(&sm.dt[b % 3][t0]);
                 sm.xd[buf][t0][j] = d4.x * u[0];
@@ -240,7 +253,7 @@ __global__ void __launch_bounds__(Cols<PS>::NS + NA, 2) scan_kernel(const __grid
         }
     };
     auto output = [&](int b) {
-        for (int i = tid; i < TB * PS; i += NA) {
+        for (int i = otid; i < TB * PS; i += OUT) {
             const int tl = i / PS, cc = i % PS;
             const uint32_t t = (uint32_t)b * TB + tl;
             if (t >= L) break;
@@ -253,7 +266,7 @@ __global__ void __launch_bounds__(Cols<PS>::NS + NA, 2) scan_kernel(const __grid
         }
     };
     static_assert((STAGES & (STAGES - 1)) == 0 && (TB & (TB - 1)) == 0, "row slots by mask");
-    const bool sends = lane >= 0;
+    const bool sends = lane >= 0 && lane < 32, convolves = tid < NC, writes = otid >= 0 && otid < OUT;
     if (sends) {
         if (lane == 0) {
             for (int i = 0; i < STAGES; ++i) ptx::mbar_init(ptx::smem_u32(&sm.bar[i]), 1);
@@ -274,7 +287,7 @@ __global__ void __launch_bounds__(Cols<PS>::NS + NA, 2) scan_kernel(const __grid
         steps(1);
         load_dt(2);
         if (!landed(1)) sm.stop = 0;
-    } else {
+    } else if (convolves) {
         conv(0);
     }
     ptx::fence_async_smem();                             // rows -3 .. -1 lie where block 3 goes
@@ -283,18 +296,18 @@ __global__ void __launch_bounds__(Cols<PS>::NS + NA, 2) scan_kernel(const __grid
 #pragma unroll 1
     for (; b < nb && b < *(volatile int*)&sm.stop; ++b) {
         if (sends) load(b + 3);
-        if (b > 0) output(b - 1);
+        if (writes && b > 0) output(b - 1);
         if (sends) {
             steps(b + 2);
             load_dt(b + 3);
             if (!landed(b + 2)) sm.stop = b + 1;         // (and z of block b + 1)
-        } else if (b + 1 < nb) {
+        } else if (convolves && b + 1 < nb) {
             conv(b + 1);
         }
         __syncthreads();
     }
     if (b == nb) {
-        if (nb > 0) output(nb - 1);
+        if (writes && nb > 0) output(nb - 1);
     } else if (lane == 0) {
         atomicExch(status, ERR_TIMEOUT);
         for (int k = b; k < b + 3; ++k) landed(k);       // copies in flight land before the CTA leaves
@@ -344,7 +357,7 @@ cudaError_t scan_ps(const PrefillArgs& a, int32_t* status, cudaStream_t s) {
                     !encode_rows(&m.bc, a.xbc, sizeof(TI), a.T, Cx, a.xbc_stride, TB, N) ||
                     (a.z && !encode_rows(&m.z, a.z, sizeof(TI), a.T, W, a.z_stride, TB, PS))))
         return cudaErrorInvalidValue;
-    scan_kernel<TI, P, N, PS, TB><<<(unsigned)blocks, Cols<PS>::NS + NA, smem, s>>>(a, m, status);
+    scan_kernel<TI, P, N, PS, TB><<<(unsigned)blocks, Roles<PS>::NT, smem, s>>>(a, m, status);
     return cudaGetLastError();
 }
 
