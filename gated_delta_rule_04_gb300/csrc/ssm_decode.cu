@@ -17,6 +17,7 @@
 //     one read while conv_kernel still runs.  256 sessions x 64 heads: 219 us
 //     fused, 192 us this way.
 #include <algorithm>
+#include <atomic>
 
 #include "ssm_common.cuh"
 #include "tc_ptx.cuh"
@@ -244,9 +245,17 @@ int fused_cluster(int64_t n, int H, int G, int P, int N) {
 template <typename TI, int P, int N>
 cudaError_t fused(const DecodeArgs& a, int cs, cudaStream_t s) {
     auto k = fused_kernel<TI, P, N>;
-    if (cs > 8) {   // 16 CTAs are beyond the portable size
-        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (cs > 8) {   // 16 CTAs are beyond the portable size (set once per device)
+        static std::atomic<uint64_t> done{0};
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
         if (e != cudaSuccess) return e;
+        const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+        if (!(done.load() & bit)) {
+            e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+            if (e != cudaSuccess) return e;
+            done.fetch_or(bit);
+        }
     }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)((int64_t)a.n * a.G * cs));
