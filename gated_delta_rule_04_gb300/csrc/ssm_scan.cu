@@ -74,6 +74,7 @@ __global__ void __launch_bounds__(Roles<PS>::NT, 2) scan_kernel(const __grid_con
     constexpr int NS = K::NS, CP = K::CP, NC = K::NC, RN = N / NG, SL = P / PS, CH = Smem::CH;
     extern __shared__ __align__(128) unsigned char smem_raw[];
     Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
+    cudaTriggerProgrammaticLaunchCompletion();           // the ring kernel may read beside this one's end
     if (blockIdx.x == 0 && threadIdx.x == 0) *status = 0;
     const int H = g.H, W = H * P, Cx = W + 2 * g.G * N;
     const int slice = blockIdx.x % SL, h = blockIdx.x / SL % H, n = seq_at(g, blockIdx.x / SL / H);
@@ -336,6 +337,7 @@ __global__ void __launch_bounds__(256) ring_kernel(PrefillArgs g) {
                  : rin  ? *reinterpret_cast<const uint4*>(rin + ((size_t)n * RING + (t + RING)) * Cx + c)
                         : make_uint4(0, 0, 0, 0);
     }
+    cudaGridDependencySynchronize();                     // the scan has read ring_in
 #pragma unroll
     for (int s = 0; s < RING; ++s) *reinterpret_cast<uint4*>(rout + ((size_t)n * RING + s) * Cx + c) = row[s];
 }
@@ -389,9 +391,16 @@ cudaError_t launch_ring(const PrefillArgs& a, int io_bf16, cudaStream_t s) {
         if (a.ring_in) b.ring_in = static_cast<const char*>(a.ring_in) + n0 * row;
         b.ring_out = static_cast<char*>(a.ring_out) + n0 * row;
         const dim3 grid((Cx / v + 255) / 256, a.n_seqs - n0 < 65535 ? a.n_seqs - n0 : 65535);
-        if (io_bf16) ring_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(b);
-        else ring_kernel<float><<<grid, 256, 0, s>>>(b);
-        const cudaError_t e = cudaGetLastError();
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = grid;
+        cfg.blockDim = dim3(256);
+        cfg.stream = s;
+        cudaLaunchAttribute at{};
+        at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at.val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = &at;
+        cfg.numAttrs = 1;
+        const cudaError_t e = io_bf16 ? cudaLaunchKernelEx(&cfg, ring_kernel<__nv_bfloat16>, b) : cudaLaunchKernelEx(&cfg, ring_kernel<float>, b);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
