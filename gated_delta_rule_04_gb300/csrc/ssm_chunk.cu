@@ -67,7 +67,6 @@ static_assert(REG_X > REG_LAUNCH && REG_ISSUE < REG_LAUNCH && REG_ISSUE >= 24,
 constexpr int NX = 256, NY = 256;
 constexpr int NM = 96;                     // M threads: warps 17-19
 constexpr int BAR_X = 1, BAR_Y = 2, BAR_M = 3, BAR_PAIR = 4;   // named barriers (BAR_PAIR + lane quarter)
-static_assert(288 % NM == 0, "M pieces per thread");
 constexpr uint32_t TM_S = 0, TM_SH = 128, TM_XF = 192, TM_XH = 224, TM_XL = 256, TM_DI = 288, TM_D = 352;
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint64_t WAIT_LIMIT_NS = 2000000000ull;
@@ -565,46 +564,87 @@ __device__ __forceinline__ void walk(const ChunkArgs& a, const int unit, const i
                     if (c > 1) bad = !wait_or_abort(b_mfree + 8 * (c & 1), (uint32_t)((c >> 1) - 1) & 1u, abort_flag) || bad;
                     const unsigned char* G = sb + L::REC + (c & 1) * Rec<N>::BYTES + Rec<N>::OFF_G;
                     const int2 ebc = scale_of(c);
-                    // 288 pieces of 8 columns per head: rows r and 63 - r hold nine
-#pragma unroll
-                    for (int hd = 0; hd < U; ++hd) {
-                        if (hd >= nh) continue;
-                        const float* st = step_of(c, hd);
+                    // A piece is 8 columns s of block j of a row r.  On the diagonal (j = r / 8) every
+                    // element takes its own 2^(lam_r - lam_s).  Left of it that splits at the block's
+                    // last token e: 2^(lam_r - lam_e) of the piece times 2^(lam_e - lam_s) dt_s of the
+                    // column, both <= 1 but for dt, so a piece costs one exponential and not eight.
+                    const unsigned char* Gt = G;
+                    unsigned char* Mt = sb + L::M + (c & 1) * U * 8192;
+                    auto head = [&](int hd) { return min(hd, nh - 1); };
+                    auto scale = [&](int hd, float& f, float& diag) {
                         const float skip = hd ? skip1 : skip0;
-                        const int em = m_exponent(__float_as_int(st[ST_EDT]), ebc.x, ebc.y, skip);
-                        const float f = pow2(ebc.x + ebc.y - em), diag = skip * pow2(-em);
+                        const int em = m_exponent(__float_as_int(step_of(c, head(hd))[ST_EDT]), ebc.x, ebc.y, skip);
+                        f = pow2(ebc.x + ebc.y - em);
+                        diag = skip * pow2(-em);
+                    };
 #pragma unroll
-                        for (int x = 0; x < 288 / NM; ++x) {
-                            const int k = mt + x * NM, pair = k / 9, j0 = k % 9, lo = (pair >> 3) + 1;
-                            const int r = j0 < lo ? pair : 63 - pair, j = j0 < lo ? j0 : j0 - lo;
-                            const uint32_t off = sw128_off(r, 8 * j, CHUNK_T);
-                            const uint4 g4 = *reinterpret_cast<const uint4*>(G + off);
-                            const uint32_t gw[4] = {g4.x, g4.y, g4.z, g4.w};
-                            const float lr = st[r];
-                            float ls[8], dt[8];
-                            lds8(st + 8 * j, ls);
-                            lds8(st + ST_DT + 8 * j, dt);
-                            float2 mv[4];
+                    for (int x = 0; x < (U * 64 + NM - 1) / NM; ++x) {
+                        const int i = mt + x * NM, hd = i >> 6, r = i & 63, j = r >> 3;
+                        if (i >= U * 64) break;
+                        float f, diag;
+                        scale(hd, f, diag);
+                        const float* st = step_of(c, head(hd));
+                        const uint32_t off = sw128_off(r, 8 * j, CHUNK_T);
+                        const uint4 g4 = *reinterpret_cast<const uint4*>(Gt + off);
+                        const uint32_t gw[4] = {g4.x, g4.y, g4.z, g4.w};
+                        const float lr = st[r];
+                        float ls[8], dt[8];
+                        lds8(st + 8 * j, ls);
+                        lds8(st + ST_DT + 8 * j, dt);
+                        float2 mv[4];
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const float2 d = __ffma2_rn(make_float2(ls[2 * e], ls[2 * e + 1]), make_float2(-1.f, -1.f), make_float2(lr, lr));
-                                const float2 k2 = __fmul2_rn(__fmul2_rn(make_float2(dt[2 * e], dt[2 * e + 1]), make_float2(f, f)),
-                                                             make_float2(ex2(d.x), ex2(d.y)));
-                                mv[e] = __fmul2_rn(__half22float2(*reinterpret_cast<const __half2*>(&gw[e])), k2);
-                            }
-                            // nothing past s = r, D on s = r (selects, not an index into mv: that
-                            // would put it in local memory)
-                            if (j == r >> 3) {
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    const int s = 8 * j + 2 * e;
-                                    mv[e].x = s > r ? 0.f : s == r ? mv[e].x + diag : mv[e].x;
-                                    mv[e].y = s + 1 > r ? 0.f : s + 1 == r ? mv[e].y + diag : mv[e].y;
-                                }
-                            }
-                            *reinterpret_cast<uint4*>(sb + L::M + ((c & 1) * U + hd) * 8192 + off) = make_uint4(
-                                pack2(mv[0].x, mv[0].y), pack2(mv[1].x, mv[1].y), pack2(mv[2].x, mv[2].y), pack2(mv[3].x, mv[3].y));
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 d = __ffma2_rn(make_float2(ls[2 * e], ls[2 * e + 1]), make_float2(-1.f, -1.f), make_float2(lr, lr));
+                            const float2 k2 = __fmul2_rn(__fmul2_rn(make_float2(dt[2 * e], dt[2 * e + 1]), make_float2(f, f)),
+                                                         make_float2(ex2(d.x), ex2(d.y)));
+                            mv[e] = __fmul2_rn(__half22float2(*reinterpret_cast<const __half2*>(&gw[e])), k2);
+                            // nothing past s = r, D on s = r
+                            const int s = 8 * j + 2 * e;
+                            mv[e].x = s > r ? 0.f : s == r ? mv[e].x + diag : mv[e].x;
+                            mv[e].y = s + 1 > r ? 0.f : s + 1 == r ? mv[e].y + diag : mv[e].y;
                         }
+                        *reinterpret_cast<uint4*>(Mt + hd * 8192 + off) = make_uint4(
+                            pack2(mv[0].x, mv[0].y), pack2(mv[1].x, mv[1].y), pack2(mv[2].x, mv[2].y), pack2(mv[3].x, mv[3].y));
+                    }
+                    // the columns' factors take the place of dt, which nothing else reads
+                    constexpr int MINE = (U * 64 + NM - 1) / NM;
+                    float cf[MINE];
+#pragma unroll
+                    for (int x = 0; x < MINE; ++x) {
+                        const int i = min(mt + x * NM, U * 64 - 1), hd = i >> 6, t = i & 63;
+                        const float* st = step_of(c, head(hd));
+                        float f, diag;
+                        scale(hd, f, diag);
+                        cf[x] = f * st[ST_DT + t] * ex2(st[t | 7] - st[t]);
+                    }
+                    ptx::bar_sync_or(BAR_M, NM, false);
+#pragma unroll
+                    for (int x = 0; x < MINE; ++x) {
+                        const int i = mt + x * NM, hd = i >> 6;
+                        if (i < U * 64 && hd < nh) const_cast<float*>(step_of(c, hd))[ST_DT + (i & 63)] = cf[x];
+                    }
+                    ptx::bar_sync_or(BAR_M, NM, false);
+                    // left of the diagonal: blocks (b, j), j < b, 28 a head, rows 8 b and 8 (8 - b) paired
+#pragma unroll
+                    for (int x = 0; x < (U * 224 + NM - 1) / NM; ++x) {
+                        const int i = mt + x * NM, hd = i >= 224, q = (i - 224 * hd) >> 3, p = q >> 3, t = q & 7;
+                        if (i >= U * 224) break;
+                        const int b = p == 3 ? 4 : t <= p ? p + 1 : 7 - p, j = p == 3 || t <= p ? t : t - p - 1, r = 8 * b + (i & 7);
+                        const float* st = step_of(c, head(hd));
+                        const uint32_t off = sw128_off(r, 8 * j, CHUNK_T);
+                        const uint4 g4 = *reinterpret_cast<const uint4*>(Gt + off);
+                        const uint32_t gw[4] = {g4.x, g4.y, g4.z, g4.w};
+                        const float rf = ex2(st[r] - st[8 * j + 7]);
+                        float k[8];
+                        lds8(st + ST_DT + 8 * j, k);
+                        uint32_t o[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 k2 = __fmul2_rn(make_float2(k[2 * e], k[2 * e + 1]), make_float2(rf, rf));
+                            const float2 mv = __fmul2_rn(__half22float2(*reinterpret_cast<const __half2*>(&gw[e])), k2);
+                            o[e] = pack2(mv.x, mv.y);
+                        }
+                        *reinterpret_cast<uint4*>(Mt + hd * 8192 + off) = make_uint4(o[0], o[1], o[2], o[3]);
                     }
                     ptx::fence_async_smem();
                     if (ptx::bar_sync_or(BAR_M, NM, bad)) break;
