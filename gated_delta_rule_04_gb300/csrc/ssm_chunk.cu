@@ -30,7 +30,7 @@
 // half): conv, operands, S; the two warps of a quarter meet once a chunk, for the
 // maxima that set X's scale.  Warps 8-15 (Y group): the readout, Y through a
 // shared-memory tile to rows, gate, store.  Warps 17-19: M of the next chunk.  Warp
-// 16 issues the MMAs.  All hand-offs are mbarriers; x, the step records and the
+// 16 issues the MMAs and the loads.  All hand-offs are mbarriers; x, the step records and the
 // group records arrive by TMA and bulk copies, x two chunks ahead.  Every wait is
 // bounded: on timeout the kernel reports it in the workspace's error word, lets its
 // copies and MMAs land, frees its tensor memory and returns.
@@ -59,10 +59,10 @@ namespace {
 constexpr int NT = 640;                    // 8 X warps, 8 Y warps, one issuing warp, 3 M warps
 // register split: 96 a thread at launch (65536 / 640, in eights of a warp's share);
 // the issue and M warpgroup gives to the X group, the Y group keeps its own
-constexpr int REG_LAUNCH = 96, REG_X = 112, REG_ISSUE = 64;   // (no spills in the full pass)
-static_assert(256 * REG_X + 256 * REG_LAUNCH + 128 * REG_ISSUE <= NT * REG_LAUNCH && REG_X % 8 == 0,
+constexpr int REG_LAUNCH = 96, REG_X = 112, REG_Y = 88, REG_ISSUE = 80;   // (no spills in the full pass)
+static_assert(256 * REG_X + 256 * REG_Y + 128 * REG_ISSUE <= NT * REG_LAUNCH && REG_X % 8 == 0,
               "the split must fit the launch's registers, or setmaxnreg.inc waits forever");
-static_assert(REG_X > REG_LAUNCH && REG_ISSUE < REG_LAUNCH && REG_ISSUE >= 24,
+static_assert(REG_X > REG_LAUNCH && REG_Y < REG_LAUNCH && REG_ISSUE < REG_LAUNCH && REG_ISSUE >= 24,
               "setmaxnreg.inc takes no smaller count than the current one, .dec no larger");
 constexpr int NX = 256, NY = 256;
 constexpr int NM = 96;                     // M threads: warps 17-19
@@ -150,7 +150,7 @@ __device__ __forceinline__ void walk(const ChunkArgs& a, const int unit, const i
     unsigned char* sb = smem_raw + (base - raw);
     const uint32_t bars = base + L::BAR;
     const uint32_t b_x = bars, b_step = bars + 16, b_rec = bars + 56, b_m = bars + 72;   // [2], [NSTEP], [2], [2]
-    const uint32_t b_xready = bars + 88, b_done = bars + 96, b_dfree = bars + 104, b_drain = bars + 112, b_sdone = bars + 120, b_mfree = bars + 128, b_xfree = bars + 144;   // b_mfree: [2]
+    const uint32_t b_xready = bars + 88, b_done = bars + 96, b_dfree = bars + 104, b_drain = bars + 112, b_sdone = bars + 120, b_mfree = bars + 128;   // b_mfree: [2]
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sb + L::BAR + 160);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(sb + L::BAR + 164);
     volatile int* issued = reinterpret_cast<volatile int*>(sb + L::BAR + 168);   // loads issued: [0] x and steps, [1] records
@@ -169,7 +169,6 @@ __device__ __forceinline__ void walk(const ChunkArgs& a, const int unit, const i
         }
         for (int i = 0; i < NSTEP; ++i) ptx::mbar_init(b_step + 8 * i, 1);
         ptx::mbar_init(b_xready, NX / 32);
-        ptx::mbar_init(b_xfree, NX / 32);
         ptx::mbar_init(b_done, 1);
         ptx::mbar_init(b_dfree, NY / 32);
         ptx::mbar_init(b_drain, 1);
@@ -185,9 +184,9 @@ __device__ __forceinline__ void walk(const ChunkArgs& a, const int unit, const i
     const int quarter = warp & 3, half = (warp >> 2) & 1;
     const uint32_t tlane = tmem + ((uint32_t)(32 * quarter) << 16);
 
-    // x tile, step records and scales of chunk c
+    // x tile of chunk c; its step records and scales
     auto load_x = [&](int c) {
-        const uint32_t bx = b_x + 8 * (c & 1), bs = b_step + 8 * (c % NSTEP);
+        const uint32_t bx = b_x + 8 * (c & 1);
         const int64_t t0 = bos + (first + c) * CHUNK_T;
         const uint32_t dst = base + L::X + (c & 1) * X_SLOT;
         if (first + c > 0) {
@@ -197,11 +196,14 @@ __device__ __forceinline__ void walk(const ChunkArgs& a, const int unit, const i
             ptx::mbar_expect_tx(bx, CHUNK_T * ROW);
             ptx::tma_load_2d(dst + RING * ROW, &a.map64, c0, (int)t0, bx);
         }
+        issued[0] = c + 1;
+    };
+    auto load_step = [&](int c) {
+        const uint32_t bs = b_step + 8 * (c % NSTEP);
         const uint32_t sdst = base + L::STEP + (c % NSTEP) * STEP_SLOT;
         ptx::mbar_expect_tx(bs, nh * STEP_BYTES + 16);
         ptx::bulk_g2s(sdst, a.step + ((size_t)(chunk0 + c) * g.H + h0) * STEP_FLOATS, nh * STEP_BYTES, bs);
         ptx::bulk_g2s(sdst + 2 * STEP_BYTES, a.scale + (size_t)(chunk0 + c) * g.G + grp, 16, bs);
-        issued[0] = c + 1;
     };
     auto load_rec = [&](int c) {
         const uint32_t bar = b_rec + 8 * (c & 1);
@@ -218,10 +220,7 @@ __device__ __forceinline__ void walk(const ChunkArgs& a, const int unit, const i
     if (warp < 8) {
         // ================================ X group ================================
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REG_X));
-        if (tid == 0)
-            for (int c = 0; c < nc && c < 2; ++c) load_x(c);
-        if (tid == 32)
-            for (int c = 0; c < nc && c < 2; ++c) load_rec(c);
+        if (piece > 0) cudaGridDependencySynchronize();      // (end states of the pieces before)
         const int ch = 32 * quarter + lane;                  // channel of the unit = TMEM lane
         const int hh = min(ch / P, nh - 1), h = h0 + hh;     // its head (a channel past the group: computed, never stored)
         const bool valid = ch < nh * P;
@@ -288,6 +287,7 @@ __device__ __forceinline__ void walk(const ChunkArgs& a, const int unit, const i
         // piece does it: no other CTA of this launch reads those entries of ring_in, so
         // ring_out may be ring_in.
         if (!LITE && first == 0 && g.ring_out && half == 0) {
+            cudaGridDependencySynchronize();
             const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(g.xbc);
             const __nv_bfloat16* rin = static_cast<const __nv_bfloat16*>(g.ring_in);
             __nv_bfloat16* rout = static_cast<__nv_bfloat16*>(g.ring_out) + (size_t)seq * RING * Cx;
@@ -351,7 +351,6 @@ __device__ __forceinline__ void walk(const ChunkArgs& a, const int unit, const i
             // the two warps of a lane quarter exchange their maxima; nothing else ties the X
             // warps together within a chunk
             if (ptx::bar_sync_or(BAR_PAIR + quarter, 64, bad)) break;
-            if (lane == 0) mbar_arrive(b_xfree);             // this warp's part of the x tile is in registers
             // ---- scales
             const float* st = step_of(c, hh);
             const float lend = st[ST_LOG], dec = st[ST_DEC];
@@ -390,12 +389,6 @@ __device__ __forceinline__ void walk(const ChunkArgs& a, const int unit, const i
                     }
                 }
             }
-            if (tid == 0 && c + 2 < nc) {
-                bad = !wait_or_abort(b_xfree, (uint32_t)c & 1u, abort_flag);
-                ptx::fence_async_smem();
-                if (!bad) load_x(c + 2);
-            }
-            __syncwarp();
             // ---- the previous chunk's state and inter MMAs have read their operands and
             // written S (its intra MMAs, which come last, only hold X)
             if (c > 0) {
@@ -426,7 +419,6 @@ __device__ __forceinline__ void walk(const ChunkArgs& a, const int unit, const i
             if (c > 0) {
                 bad = !wait_or_abort(b_done, (uint32_t)(c - 1) & 1u, abort_flag) || bad;
                 ptx::tc_fence_after();
-                if (tid == 32 && c + 1 < nc && !bad) load_rec(c + 1);   // its slot's MMAs and M are done
             }
             if (!LITE) ptx::tmem_st16u(tlane + TM_XF + 16 * half, xf);
             ptx::tmem_wait_st();
@@ -458,6 +450,7 @@ __device__ __forceinline__ void walk(const ChunkArgs& a, const int unit, const i
         }
     } else if (warp < 16) {
         // ================================ Y group ================================
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_Y));
         if constexpr (!LITE) {
             const int yt = tid - NX, ch = 32 * quarter + lane;
             const int rt = yt >> 3, rseg = yt & 7;           // row pass: rows rt and 32 + rt, values 32 q + 4 rseg ..
@@ -653,6 +646,16 @@ __device__ __forceinline__ void walk(const ChunkArgs& a, const int unit, const i
             }
         } else if (lane == 0) {
         // ============================ MMA issue (one thread) ======================
+        // The loads are this thread's as well: with chunk c's operands ready the X group has left
+        // x tile c, and chunk c - 1's MMAs and M are done with their record.
+        for (int c = 0; c < nc && c < 2; ++c) load_x(c);
+        // what the launch before this one wrote is read from here on; the start up to here, and
+        // the X group's, may run beside its end
+        cudaGridDependencySynchronize();
+        for (int c = 0; c < nc && c < 2; ++c) {
+            load_step(c);
+            load_rec(c);
+        }
         constexpr uint32_t ID64 = ptx::idesc_f16_f32(128, 64), IDN = ptx::idesc_f16_f32(128, N);
 #pragma unroll 1
         for (int c = 0; c < nc; ++c) {
@@ -676,6 +679,12 @@ __device__ __forceinline__ void walk(const ChunkArgs& a, const int unit, const i
                     ptx::mma_f16_ta(tmem + TM_S, tmem + (term == 2 ? TM_XL : TM_XH) + 8 * kk,
                                     db + (term == 1 ? Rec<N>::OFF_LO / 16 : 0) + kk * 2, IDN, 1);
             ptx::mma_commit(b_sdone);
+            if (c + 2 < nc) {
+                ptx::fence_async_smem();
+                load_x(c + 2);
+                load_step(c + 2);
+            }
+            if (c > 0 && c + 1 < nc) load_rec(c + 1);
             if (!LITE) {
                 // (an abort here leaves MMAs in flight: the drain below covers them)
                 if (!wait_or_abort(b_m + 8 * (c & 1), (uint32_t)(c >> 1) & 1u, abort_flag)) break;
@@ -722,7 +731,6 @@ __device__ __forceinline__ void walk(const ChunkArgs& a, const int unit, const i
 template <int P, int N, bool LEAD>
 __global__ void __launch_bounds__(NT, 1) chunk_kernel(const __grid_constant__ ChunkArgs a) {
     cudaTriggerProgrammaticLaunchCompletion();
-    cudaGridDependencySynchronize();                     // the launch before this one has ended
     const int per = LEAD && a.np == 1 ? 1 : a.np - 1;    // pieces of a sequence in this launch
     const int unit = blockIdx.x % a.units, i = blockIdx.x / a.units;
     const int piece = (a.by_piece ? i / a.g.n_seqs : i % per) + (LEAD ? 0 : 1);
