@@ -794,7 +794,7 @@ bool encode_rows(CUtensorMap* m, const void* base, int es, int64_t T, int64_t W,
 
 cudaError_t launch_chunks(const ChunkArgs& a, bool after, cudaStream_t s) {
     const cudaError_t e = launch_pn<true>(a, after, s);
-    return e != cudaSuccess || a.np == 1 ? e : launch_pn<false>(a, after, s);
+    return e != cudaSuccess || a.np == 1 ? e : launch_pn<false>(a, true, s);
 }
 
 }  // namespace ssm
