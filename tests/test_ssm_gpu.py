@@ -297,3 +297,82 @@ def test_decode_in_a_graph_with_its_own_workspace(H, G):
     torch.cuda.synchronize()
     for g, *_, o, S, ring, S0, r0, want in graphs:
         assert all(torch.equal(a, b) for a, b in zip((o, S, ring), want))
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("H, P, N, lens", [
+    (2, 64, 128, [1500, 30, 700, 0, 300]),                     # one unit: many pieces, of several sequences
+    (3, 128, 64, [1100, 1000, 980]),                           # close lengths
+    (2, 64, 64, [5, 900, 64, 128] + [20 * k for k in range(16)]),   # more sequences than travel with the launch
+    (40, 64, 64, [600, 8, 8, 8])])                             # the longest one alone at the end
+def test_prefill_cut_sequences_in_place(io, H, P, N, lens):
+    """Sequences cut into pieces, whose starts are composed; state and ring updated in place; the
+    rows behind the last sequence are neither read nor written."""
+    cu = cumsum(lens)
+    T, n = cu[-1], len(lens)
+    i = make_inputs(T, n, H, P, N, 1, IO[io], 31 + H)
+    i["A_log"] -= 2.0
+    wo, wS, wr = mixer(i, cu, True)
+    pad = {k: torch.full((T + 70, dev(i[k]).shape[1]), float("nan"), dtype=IO[io], device=DEV) for k in ("xbc", "dt", "z")}
+    for k, t in pad.items():
+        t[:T] = dev(i[k])
+    S, ring = dev(i["S"]), dev(i["ring"])
+    buf = torch.full((T + 70, H * P), 7.0, dtype=IO[io], device=DEV)
+    p = params(i, io)
+    ws = torch.empty(kda.kda_ssm_prefill_workspace_bytes(p, n, T), dtype=torch.uint8, device=DEV)
+    o, S_out, ring_out = kda.kda_ssm_prefill(p, pad["xbc"][:T], pad["dt"][:T], cu, z=pad["z"][:T], S_in=S, S_out=S, ring_in=ring,
+                                             ring_out=ring, o=buf[:T], workspace=ws)
+    assert kda.kda_workspace_status(ws) == kda.KDA_OK
+    assert S_out is S and ring_out is ring
+    close("o", o, wo)
+    close("S", S, wS)
+    assert torch.equal(ring.cpu(), wr)
+    assert bool((buf[T:] == 7.0).all())
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_prefill_two_at_once_and_two_graphs_with_one_workspace(io):
+    sizes = ([700, 65], [33] * 18)
+    cases = []
+    for k, lens in enumerate(sizes):
+        cu = cumsum(lens)
+        i = make_inputs(cu[-1], len(lens), 4, 64, 128, 2, IO[io], 50 + k)
+        p = params(i, io)
+        t = [dev(i[x]) for x in ("xbc", "dt", "z", "S", "ring")]
+        cases.append((p, cu, t, kda.kda_ssm_prefill_workspace_bytes(p, len(lens), cu[-1])))
+
+    def call(c, ws, **kw):
+        p, cu, t, _ = c
+        return kda.kda_ssm_prefill(p, t[0], t[1], cu, z=t[2], S_in=t[3], ring_in=t[4], workspace=ws, **kw)
+
+    space = [torch.empty(c[3], dtype=torch.uint8, device=DEV) for c in cases]
+    want = [call(c, w) for c, w in zip(cases, space)]
+    torch.cuda.synchronize()
+    # two streams, a workspace each
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(3):
+        for k in range(2):
+            got[k].append(call(cases[k], space[k], stream=streams[k]))
+    for s in streams:
+        s.synchronize()
+    for k in range(2):
+        for g in got[k]:
+            assert all(torch.equal(a, b) for a, b in zip(g, want[k]))
+    # two graphs that share a workspace, replayed in turn on one stream
+    shared = torch.empty(max(c[3] for c in cases), dtype=torch.uint8, device=DEV)
+    graphs, outs = [], []
+    for k, c in enumerate(cases):
+        out = dict(o=torch.zeros_like(want[k][0]), S_out=torch.zeros_like(want[k][1]), ring_out=torch.zeros_like(want[k][2]))
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call(c, shared, **out)
+        graphs.append(g)
+        outs.append(out)
+    for k in (0, 1, 0, 1, 1, 0):
+        for t in outs[k].values():
+            t.zero_()
+        graphs[k].replay()
+    torch.cuda.synchronize()
+    for k in range(2):
+        assert all(torch.equal(a, b) for a, b in zip(outs[k].values(), want[k]))
