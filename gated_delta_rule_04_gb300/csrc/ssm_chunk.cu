@@ -41,14 +41,15 @@
 // composed from the pieces before it when it begins.  The first piece needs no
 // start, so it is walked in full beside those.
 //
-// Measured: a full walk takes 3.0 us a chunk and a lite one 1.8 (64 tokens x 128
-// channels, N = 128), i.e. 32768 tokens x 96 heads of 64 in 0.67 ms.  The X group
-// sets that: its arithmetic on 64 x 128 values (conv, SiLU, scaling, three fp16
-// packings), the S row through registers, and the latency between them, at 54 % of
-// the issue slots, 43 % of shared memory and 16 % of L2; the tensor cores are at
-// 18 %.  Rows of x through registers rather than a shared tile, the split of M and
-// readout from the X group and packed fp32 pairs took it there from 4.4 us; eight
-// more X warps changed nothing.
+// Measured: a full walk takes 2.6 us a chunk and a lite one 1.6 (64 tokens x 128
+// channels, N = 128), i.e. 32768 tokens x 96 heads of 64 in 0.61 ms.  The X group
+// sets that, M close behind it: its arithmetic on 64 x 128 values (conv, SiLU,
+// scaling, three fp16 packings), the S row through registers, and the latency
+// between them, at 53 % of the issue slots, 38 % of shared memory and 18 % of L2; the
+// tensor cores are at 25 %.  From 4.4 us it came there by x through registers rather
+// than a shared tile, M and the readout off the X group, packed fp32 pairs, one
+// exponential per piece of M (0.3 us of 3.0) and the loads on the issuing thread
+// (0.1); eight more X warps changed nothing.
 #include "ssm_chunk.cuh"
 #include "tc_ptx.cuh"
 

@@ -12,6 +12,12 @@
 // B reaches the fp32 state, whose error the operands' rounding would set: B'
 // goes out as an fp16 pair (22 bits).  C and G reach bf16 outputs only and are
 // rounded once to fp16's 11 bits; bf16's 8 would be as coarse as the output.
+//
+// 32768 tokens, 96 heads, 8 groups, N = 128: 155 us for 218 MB of records and 0.15
+// GB of inputs, 0.35 of the measured copy rate.  Bound by latency: two blocks of 16
+// warps an SM issue 44 % of the time, the rest is raw rows (each thread's 16 in
+// flight at once) and the barriers of a short block (a block alone takes 4.8 us, 1.9 of
+// them conv).  A thread per channel with 256-thread blocks took 205 us.
 #include <type_traits>
 
 #include "ssm_chunk.cuh"

@@ -9,8 +9,8 @@
 //     the heads of a (session, group) are one thread-block cluster (up to 16 CTAs of
 //     one or two heads).  Every CTA convolves the group's B and C for itself (6 KiB
 //     from L2 beside a 32 KiB state) and its own heads' x, and a cluster barrier
-//     stands between the last read of that ring and its write.  One launch takes a
-//     single session's call from 19 to 15 us as the caller sees it;
+//     stands between the last read of that ring and its write.  One launch of 5 us
+//     takes a single session's call from 19 to 14 us as the caller sees it;
 //   - otherwise conv_kernel takes every channel of every session through the conv
 //     into the workspace and rolls the ring, and state_kernel streams the states:
 //     persistent CTAs, the next state's 16 to 64 KiB prefetched into L2, the first
