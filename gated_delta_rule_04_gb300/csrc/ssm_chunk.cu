@@ -58,9 +58,10 @@ namespace ssm {
 namespace {
 
 constexpr int NT = 640;                    // 8 X warps, 8 Y warps, one issuing warp, 3 M warps
-// register split: 96 a thread at launch (65536 / 640, in eights of a warp's share);
-// the issue and M warpgroup gives to the X group, the Y group keeps its own
-constexpr int REG_LAUNCH = 96, REG_X = 112, REG_Y = 88, REG_ISSUE = 80;   // (no spills in the full pass)
+// register split: 96 a thread at launch (65536 / 640, in eights of a warp's share); the
+// other groups give to the X group (Y 96 and 64 for the last warpgroup spill in M:
+// 32768 tokens x 96 heads 0.80 ms, this way 0.77)
+constexpr int REG_LAUNCH = 96, REG_X = 112, REG_Y = 88, REG_ISSUE = 80;
 static_assert(256 * REG_X + 256 * REG_Y + 128 * REG_ISSUE <= NT * REG_LAUNCH && REG_X % 8 == 0,
               "the split must fit the launch's registers, or setmaxnreg.inc waits forever");
 static_assert(REG_X > REG_LAUNCH && REG_Y < REG_LAUNCH && REG_ISSUE < REG_LAUNCH && REG_ISSUE >= 24,
@@ -77,9 +78,9 @@ constexpr uint32_t X_SLOT = 67 * ROW;
 constexpr uint32_t STEP_BYTES = STEP_FLOATS * 4;
 constexpr uint32_t STEP_SLOT = 2 * STEP_BYTES + 16;   // two heads' step records, the group's scales
 
-// A slot is refilled for chunk c + 2 while the X group is at chunk c; the Y group
-// may then still read the decays of chunk c - 2, and has left chunk c - 3.
-constexpr int NSTEP = 5;
+// A slot is refilled for chunk c + 2 when the X group is done with chunk c and the
+// Y group with the decays of chunk c - 1; M is at chunk c or c + 1.
+constexpr int NSTEP = 3;
 
 template <int P, int N>
 struct Map {                               // shared memory, from a 1 KiB aligned base
@@ -562,7 +563,6 @@ __device__ __forceinline__ void walk(const ChunkArgs& a, const int unit, const i
                     // element takes its own 2^(lam_r - lam_s).  Left of it that splits at the block's
                     // last token e: 2^(lam_r - lam_e) of the piece times 2^(lam_e - lam_s) dt_s of the
                     // column, both <= 1 but for dt, so a piece costs one exponential and not eight.
-                    const unsigned char* Gt = G;
                     unsigned char* Mt = sb + L::M + (c & 1) * U * 8192;
                     auto head = [&](int hd) { return min(hd, nh - 1); };
                     auto scale = [&](int hd, float& f, float& diag) {
@@ -579,7 +579,7 @@ __device__ __forceinline__ void walk(const ChunkArgs& a, const int unit, const i
                         scale(hd, f, diag);
                         const float* st = step_of(c, head(hd));
                         const uint32_t off = sw128_off(r, 8 * j, CHUNK_T);
-                        const uint4 g4 = *reinterpret_cast<const uint4*>(Gt + off);
+                        const uint4 g4 = *reinterpret_cast<const uint4*>(G + off);
                         const uint32_t gw[4] = {g4.x, g4.y, g4.z, g4.w};
                         const float lr = st[r];
                         float ls[8], dt[8];
@@ -626,7 +626,7 @@ __device__ __forceinline__ void walk(const ChunkArgs& a, const int unit, const i
                         const int b = p == 3 ? 4 : t <= p ? p + 1 : 7 - p, j = p == 3 || t <= p ? t : t - p - 1, r = 8 * b + (i & 7);
                         const float* st = step_of(c, head(hd));
                         const uint32_t off = sw128_off(r, 8 * j, CHUNK_T);
-                        const uint4 g4 = *reinterpret_cast<const uint4*>(Gt + off);
+                        const uint4 g4 = *reinterpret_cast<const uint4*>(G + off);
                         const uint32_t gw[4] = {g4.x, g4.y, g4.z, g4.w};
                         const float rf = ex2(st[r] - st[8 * j + 7]);
                         float k[8];
