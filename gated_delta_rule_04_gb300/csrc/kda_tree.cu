@@ -495,27 +495,34 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) tree_kernel(TreeArgs a
         }
         ptx::tc_fence_before();
         __syncthreads();
-        // u: a thread per value; nodes of one depth do not see one another, and the thread
-        // groups share them
+        // u depth by depth, a warp per node (nodes of one depth do not see one another)
         for (int l = 2; l <= RMAX; ++l) {
             const int k0 = hd.level[l], k1 = l < RMAX ? hd.level[l + 1] : R;
             if (k0 >= R) break;
-            for (int k = k0 + part; k < k1; k += KP) {
+            for (int k = k0 + warp; k < k1; k += NW) {
                 const int r = hd.order[k];
                 const uint8_t* path = hd.path[r];
                 const float* A = ap + 2 * r * Rp;
-                const float self = vv[r * D + j], beta = hd.beta[r];
-                float t0 = 0.f, t1 = 0.f;
+                float4* row = reinterpret_cast<float4*>(vv + r * D + 4 * lane);
+                const float4 self = *row;
+                const float beta = hd.beta[r];
+                float2 ta = make_float2(0.f, 0.f), tb = ta;
 #pragma unroll 2
                 for (int d = 0; d < l; d += 4) {             // (d = 0, the node itself, is left out)
                     const uint32_t p4 = *reinterpret_cast<const uint32_t*>(path + d);
                     const float4 a4 = *reinterpret_cast<const float4*>(A + d);
-                    t0 = fmaf(d ? a4.x : 0.f, vv[(p4 & 255u) * D + j], t0);
-                    t1 = fmaf(a4.y, vv[(p4 >> 8 & 255u) * D + j], t1);
-                    t0 = fmaf(a4.z, vv[(p4 >> 16 & 255u) * D + j], t0);
-                    t1 = fmaf(a4.w, vv[(p4 >> 24) * D + j], t1);
+                    const float av[4] = {d ? a4.x : 0.f, a4.y, a4.z, a4.w};
+                    float4 u[4];
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) u[m] = *reinterpret_cast<const float4*>(vv + (p4 >> (8 * m) & 255u) * D + 4 * lane);
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) {
+                        const float2 a2 = make_float2(av[m], av[m]);
+                        ta = __ffma2_rn(a2, make_float2(u[m].x, u[m].y), ta);
+                        tb = __ffma2_rn(a2, make_float2(u[m].z, u[m].w), tb);
+                    }
                 }
-                vv[r * D + j] = fmaf(-beta, t0 + t1, self);
+                *row = make_float4(fmaf(-beta, ta.x, self.x), fmaf(-beta, ta.y, self.y), fmaf(-beta, tb.x, self.z), fmaf(-beta, tb.y, self.w));
             }
             __syncthreads();
         }
