@@ -27,17 +27,17 @@
 //      fp32 FMAs per SM; as three tcgen05 products of fp16 pairs (hi hi, hi lo,
 //      lo hi: 22-bit operands, so that fp32 outputs hold too) under 1 us.  S0 is
 //      scaled by an exact power of two per value, the rows by 2^8;
-//   5. u depth by depth, a thread per value, thread groups sharing a depth's
-//      nodes; o, RMSNormGated, a warp per node.
+//   5. u depth by depth, a warp per node; o, RMSNormGated, a warp per node.
 // While an item computes, the next one's state and rows go to L2.
 //
-// 64 trees of 64 nodes, 32 heads: 357 us, where reading each state and row once
+// 64 trees of 64 nodes, 32 heads: 336 us, where reading each state and row once
 // takes 51.  One CTA fits an SM (200 KB of planes at 64 nodes), so its phases
-// follow one another: of 53 thousand cycles an item, loads take 9, the conv 8.5, A
-// and P 8, the solve 10; some 16 thousand are shared-memory bandwidth (48 % of it).
+// follow one another: of 47 thousand cycles an item, loads take 9, the conv 8.5, A
+// and P 8, the solve 6, the outputs 6; some 16 thousand are shared-memory bandwidth (48 % of it).
 // The first kernel, fp32 throughout and a thread per channel, took 2345 us, tensor
 // cores for phase 4 and running products for phase 3 566, the conv in pairs and the
-// solve by depth 357.  One tree of 16 nodes: 13 us.
+// solve by depth 357, a warp per node in it and the prefetch during the MMAs 336.
+// One tree of 16 nodes: 13 us.
 #include <stddef.h>
 
 #include <algorithm>
@@ -201,23 +201,12 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) tree_kernel(TreeArgs a
     const uint32_t items = (uint32_t)a.n * H;            // (below 2^31: checked on the host)
     uint32_t phase = 0;
     uint32_t item = blockIdx.x;
+    auto slot_of = [&](uint32_t it) { return it >= items ? -1 : a.slots ? a.slots[it / H] : (int)(it / H); };
+    int next_slot = slot_of(item);
 #pragma unroll 1
     for (; item < items; item += gridDim.x) {
-        const int n = (int)(item / H), h = (int)(item % H);
-        const int slot = a.slots ? a.slots[n] : n;
-        if (item + gridDim.x < items) {                  // the next item's state and rows into L2
-            const uint32_t nx = item + gridDim.x;
-            const int nn = (int)(nx / H), nh = (int)(nx % H), ns = a.slots ? a.slots[nn] : nn;
-            if (ns >= 0 && ns < a.n_slots) {
-                if (tid == 0) ptx::bulk_prefetch_l2(a.S + ((size_t)ns * H + nh) * D * D, D * D * 4);
-                constexpr int LINES = D * sizeof(TI) / 128;  // 128-byte lines of a row
-                for (int x = tid; x < 5 * R * LINES; x += THREADS) {
-                    const int pl = x / (R * LINES), r = x / LINES % R;
-                    const void* rows = pl == 0 ? a.q : pl == 1 ? a.k : pl == 2 ? a.v : pl == 3 ? a.z : a.gout;
-                    prefetch_l2(static_cast<const char*>(rows) + (((size_t)nn * R + r) * W + (size_t)nh * D) * sizeof(TI) + x % LINES * 128);
-                }
-            }
-        }
+        const int n = (int)(item / H), h = (int)(item % H), slot = next_slot;
+        next_slot = slot_of(item + gridDim.x);
         if (slot < 0 || slot >= a.n_slots) continue;
         const size_t row0 = (size_t)n * R;
         const int c = h * D + i;
@@ -470,6 +459,17 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) tree_kernel(TreeArgs a
                                     term > 0 || x > 0);
             }
             ptx::mma_commit(bar);
+        }
+        if (next_slot >= 0 && next_slot < a.n_slots) {       // the next item's state and rows into L2
+            const uint32_t nx = item + gridDim.x;
+            const int nn = (int)(nx / H), nh = (int)(nx % H);
+            if (tid == 0) ptx::bulk_prefetch_l2(a.S + ((size_t)next_slot * H + nh) * D * D, D * D * 4);
+            constexpr int LINES = D * sizeof(TI) / 128;      // 128-byte lines of a row
+            for (int x = tid; x < 5 * R * LINES; x += THREADS) {
+                const int pl = x / (R * LINES), r = x / LINES % R;
+                const void* rows = pl == 0 ? a.q : pl == 1 ? a.k : pl == 2 ? a.v : pl == 3 ? a.z : a.gout;
+                prefetch_l2(static_cast<const char*>(rows) + (((size_t)nn * R + r) * W + (size_t)nh * D) * sizeof(TI) + x % LINES * 128);
+            }
         }
         if (!ptx::mbar_wait(bar, phase, WAIT_LIMIT_NS)) hd.bad = 1;
         phase ^= 1u;
