@@ -96,7 +96,7 @@ struct Map {                               // shared memory, from a 1 KiB aligne
     static constexpr uint32_t BAR = XM + 2048;
     static constexpr uint32_t BYTES = BAR + 256 + 1024;
     static_assert(REC % 1024 == 0 && M % 1024 == 0 && X % 128 == 0 && STEP % 16 == 0 && STEP_SLOT % 16 == 0 && BAR % 8 == 0, "");
-    static_assert(BYTES <= 232448, "shared memory of one CTA");
+    static_assert(BYTES <= 232448 && 2 * BYTES > 233472, "one CTA per SM (it takes all of the tensor memory)");
 };
 
 __device__ __forceinline__ uint32_t pack2(float a, float b) {

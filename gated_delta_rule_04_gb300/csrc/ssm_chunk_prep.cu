@@ -100,10 +100,10 @@ __global__ void __launch_bounds__(NT, 2) prep_kernel(const __grid_constant__ Chu
     const PrefillArgs& g = a.g;
     // the blocks of one chunk side by side: their pieces of a projection row are neighbours
     const int chunk = blockIdx.x / a.prep_blocks, grp = blockIdx.x % a.prep_blocks;
-    cudaTriggerProgrammaticLaunchCompletion();   // the next launch's CTAs may take their places
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = ERR_NONE;   // this call's timeouts only
     const ChunkDesc d = chunk_desc(a, chunk);
     if (grp >= g.G) {
+        cudaTriggerProgrammaticLaunchCompletion();
         steps(a, d, chunk, grp - g.G, reinterpret_cast<float (*)[HB + 1]>(smem_raw));
         return;
     }
@@ -116,6 +116,9 @@ __global__ void __launch_bounds__(NT, 2) prep_kernel(const __grid_constant__ Chu
         ptx::tmem_alloc(ptx::smem_u32(&tmem_slot), TMEM_COLS);
         ptx::tmem_relinquish();
     }
+    // The next launch's CTAs may start now.  Not before this block has its tensor memory: one
+    // that shares the SM takes all of it and then waits for this launch to end.
+    cudaTriggerProgrammaticLaunchCompletion();
     if (tid == 0) {
         ptx::mbar_init(bar_a, 1);
         ptx::fence_mbar_init();
