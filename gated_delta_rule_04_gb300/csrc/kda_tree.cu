@@ -621,9 +621,9 @@ int sm_count() {
 // them (warp w: key rows 16w .. 16w+15, lane l: columns 4l .. 4l+3): one read
 // and one write of the state, which bounds the kernel.  Tokens go through the
 // conv, gate and norm in groups of CG.  256 sessions x 32 heads, paths of up to 6:
-// 231 us, 73 % of the measured copy rate (a CTA an item 278 us); the rest is two
-// barriers a token and the walk from conv to state within an item, which two CTAs
-// an SM overlap.
+// 219 us, 78 % of the measured copy rate (a CTA an item 278 us, path and ring read
+// when they are needed 226); the rest is two barriers a token and the walk from conv
+// to state within an item, which two CTAs an SM overlap.
 constexpr int CG = 8;
 
 struct CommitSmem {
@@ -642,16 +642,20 @@ __global__ void __launch_bounds__(NT, 2) commit_kernel(CommitArgs a) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int i = tid & (D - 1), half = tid >> 7;
     const uint32_t items = (uint32_t)a.n * H;   // (below 2^31: checked on the host)
-    // slot and length are read an item ahead: the state's address waits for them
+    // slot, length and path (a node a thread) are read an item ahead: the addresses of the
+    // state and of the rows wait for them
     int next_slot = a.slots ? a.slots[blockIdx.x / H] : blockIdx.x / H, next_len = a.path_len[blockIdx.x / H];
+    auto path_at = [&](int nn) { return tid < next_len && next_len <= a.max_len ? a.path[(size_t)nn * a.max_len + tid] : 0; };
+    int next_node = path_at(blockIdx.x / H);
 #pragma unroll 1
     for (uint32_t item = blockIdx.x; item < items; item += gridDim.x) {
         const int n = (int)(item / H), h = (int)(item % H), c = h * D + i;
-        const int slot = next_slot, len = next_len;
+        const int slot = next_slot, len = next_len, node = next_node;
         if (item + gridDim.x < items) {
             const int nn = (int)((item + gridDim.x) / H), nh = (int)((item + gridDim.x) % H);
             next_slot = a.slots ? a.slots[nn] : nn;
             next_len = a.path_len[nn];
+            next_node = path_at(nn);
             if (tid == 0 && next_slot >= 0 && next_slot < a.n_slots)
                 ptx::bulk_prefetch_l2(a.S_in + ((size_t)next_slot * H + nh) * D * D, D * D * 4);
         }
@@ -669,9 +673,8 @@ __global__ void __launch_bounds__(NT, 2) commit_kernel(CommitArgs a) {
             constexpr int LINES = D * sizeof(TI) / 128;
             const int nn = (int)((item + gridDim.x) / H), nh = (int)((item + gridDim.x) % H);
             if (tid < next_len && next_len <= a.max_len) {
-                const int node = a.path[(size_t)nn * a.max_len + tid];
-                if (node >= 0 && node < a.n_nodes) {
-                    const size_t off = (((size_t)nn * a.n_nodes + node) * W + (size_t)nh * D) * sizeof(TI);
+                if (next_node >= 0 && next_node < a.n_nodes) {
+                    const size_t off = (((size_t)nn * a.n_nodes + next_node) * W + (size_t)nh * D) * sizeof(TI);
 #pragma unroll
                     for (int x = 0; x < LINES; ++x) {
                         prefetch_l2(static_cast<const char*>(a.k) + off + 128 * x);
@@ -687,7 +690,6 @@ __global__ void __launch_bounds__(NT, 2) commit_kernel(CommitArgs a) {
         }
         bool bad = false;
         if (tid < len) {
-            const int node = a.path[(size_t)n * a.max_len + tid];
             sm.path[tid] = node;
             bad = node < 0 || node >= a.n_nodes;
         }
@@ -702,6 +704,12 @@ __global__ void __launch_bounds__(NT, 2) commit_kernel(CommitArgs a) {
             const TI* src = t >= 0 ? plane[p] + (size_t)sm.path[t] * W : ring + ((size_t)p * RING + (RING + t)) * W;
             return *src;
         };
+        // the new ring: the last three raw rows of ring | path, of every plane
+        TI tail[2][RING];
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int s = 0; s < RING; ++s) tail[k][s] = half + 2 * k < 3 ? raw(half + 2 * k, len - RING + s) : TI(0.f);
         const int p = 1 + half;   // threads 0-127 own a channel of k, 128-255 of v and the gate
         const float4 w = __ldg(reinterpret_cast<const float4*>(a.conv_w + ((size_t)p * W + c) * CONV_K));
         const float eA = expf(a.A_log[h]), dtb = a.dt_bias[c];
@@ -789,17 +797,14 @@ __global__ void __launch_bounds__(NT, 2) commit_kernel(CommitArgs a) {
 #pragma unroll
         for (int r = 0; r < 16; ++r) __stcs(reinterpret_cast<float4*>(Sg_out + (size_t)(16 * warp + r) * D) + lane, Sr[r]);
 
-        // ring: the last three raw rows of ring | path, of every plane (a thread reads all
-        // three of its channel before it writes them, and every conv's read of the input
-        // ring is behind the barriers above; without tokens there was none)
+        // (a thread has read all three of its channel, and every conv's read of the input ring is
+        // behind the barriers above; without tokens there was none)
         TI* rout = static_cast<TI*>(a.ring_out) + (size_t)slot * 3 * RING * W + c;
-        for (int pl = half; pl < 3; pl += 2) {
-            TI row[RING];
 #pragma unroll
-            for (int s = 0; s < RING; ++s) row[s] = raw(pl, len - RING + s);
+        for (int k = 0; k < 2; ++k)
 #pragma unroll
-            for (int s = 0; s < RING; ++s) rout[((size_t)pl * RING + s) * W] = row[s];
-        }
+            for (int s = 0; s < RING; ++s)
+                if (half + 2 * k < 3) rout[((size_t)(half + 2 * k) * RING + s) * W] = tail[k][s];
         __syncthreads();       // the next item's path replaces this one's
     }
 }
