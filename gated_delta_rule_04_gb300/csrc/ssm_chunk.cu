@@ -647,8 +647,9 @@ __device__ __forceinline__ void walk(const ChunkArgs& a, const int unit, const i
             }
         } else if (lane == 0) {
         // ============================ MMA issue (one thread) ======================
-        // The loads are this thread's as well: with chunk c's operands ready the X group has left
-        // x tile c, and chunk c - 1's MMAs and M are done with their record.
+        // The loads are this thread's as well.  With chunk c's operands ready the X group has left
+        // x tile c; the next load into it comes behind the chunk's MMAs, which the others wait
+        // for (ahead of them it cost 5 % of the walk).
         for (int c = 0; c < nc && c < 2; ++c) load_x(c);
         // what the launch before this one wrote is read from here on; the start up to here, and
         // the X group's, may run beside its end
@@ -662,8 +663,14 @@ __device__ __forceinline__ void walk(const ChunkArgs& a, const int unit, const i
         for (int c = 0; c < nc; ++c) {
             const uint32_t rec = base + L::REC + (c & 1) * Rec<N>::BYTES;
             if (!wait_or_abort(b_rec + 8 * (c & 1), (uint32_t)(c >> 1) & 1u, abort_flag)) break;
-            if (!LITE && c > 0 && !wait_or_abort(b_dfree, (uint32_t)(c - 1) & 1u, abort_flag)) break;
+            if (!LITE && c > 0) {
+                // chunk c - 1 is read out, so its MMAs and M are done with their record; M waits for
+                // the next one
+                if (!wait_or_abort(b_dfree, (uint32_t)(c - 1) & 1u, abort_flag)) break;
+                if (c + 1 < nc) load_rec(c + 1);
+            }
             if (!wait_or_abort(b_xready, (uint32_t)c & 1u, abort_flag)) break;
+            if (LITE && c > 0 && c + 1 < nc) load_rec(c + 1);
             ptx::tc_fence_after();
             // descriptors of a tile differ from its first one by their start address (in 16 bytes)
             if (!LITE) {
@@ -680,12 +687,6 @@ __device__ __forceinline__ void walk(const ChunkArgs& a, const int unit, const i
                     ptx::mma_f16_ta(tmem + TM_S, tmem + (term == 2 ? TM_XL : TM_XH) + 8 * kk,
                                     db + (term == 1 ? Rec<N>::OFF_LO / 16 : 0) + kk * 2, IDN, 1);
             ptx::mma_commit(b_sdone);
-            if (c + 2 < nc) {
-                ptx::fence_async_smem();
-                load_x(c + 2);
-                load_step(c + 2);
-            }
-            if (c > 0 && c + 1 < nc) load_rec(c + 1);
             if (!LITE) {
                 // (an abort here leaves MMAs in flight: the drain below covers them)
                 if (!wait_or_abort(b_m + 8 * (c & 1), (uint32_t)(c >> 1) & 1u, abort_flag)) break;
@@ -700,6 +701,11 @@ __device__ __forceinline__ void walk(const ChunkArgs& a, const int unit, const i
                 ptx::mma_commit(b_mfree + 8 * (c & 1));
             }
             ptx::mma_commit(b_done);
+            if (c + 2 < nc) {
+                ptx::fence_async_smem();
+                load_x(c + 2);
+                load_step(c + 2);
+            }
         }
         // every MMA of this thread lands before its tensor memory is freed
         ptx::mma_commit(b_drain);
