@@ -166,7 +166,7 @@ private:
 // longest one ends.  Both launches are played through for a range of cuts, walks
 // in the order sequence by sequence or piece by piece; the host does it while the
 // preparation runs (3 to 40 us).  With equal pieces and the first ones cut short
-// in the first launch too, 32768 tokens x 96 heads took 0.96 ms instead of 0.83, and
+// in the first launch too, 32768 tokens x 96 heads took 0.96 ms instead of 0.82, and
 // 8 sequences of 6 to 388 chunks x 64 heads 1.08 instead of 0.95.
 struct Pieces {
     int np = 1, lp0 = 1, lp = 1;
@@ -182,7 +182,7 @@ Pieces plan_pieces(const kda_ssm_params* p, const int64_t* cu, const int32_t* or
     if (2 * (int64_t)n_seqs > slots || longest < 2 * MIN_CHUNKS) return best;
     // in chunks of a full walk: a chunk of a walk for the end state, a walk's start (state,
     // first loads), and the end state of a piece before it that it reads
-    constexpr double LITE = 0.6, START = 4, COMPOSE = 0.5;
+    constexpr double LITE = 0.65, START = 4, COMPOSE = 0.5;
     constexpr int LOTS = 16;                             // more sequences count as lots of neighbours in length
     int64_t lot[LOTS], lots = 0;
     const int64_t per = (n_seqs + LOTS - 1) / LOTS;

@@ -36,20 +36,21 @@
 // copies and MMAs land, frees its tensor memory and returns.
 //
 // Few units leave SMs idle, so long sequences are cut into pieces that run side
-// by side.  A walk over S alone (LITE: no S copy, no M, no Y) takes 0.6 of a full
+// by side.  A walk over S alone (LITE: no S copy, no M, no Y) takes 0.65 of a full
 // one and gives a piece's end state from a zero start; a piece's true start is
 // composed from the pieces before it when it begins.  The first piece needs no
 // start, so it is walked in full beside those.
 //
-// Measured: a full walk takes 2.6 us a chunk and a lite one 1.6 (64 tokens x 128
-// channels, N = 128), i.e. 32768 tokens x 96 heads of 64 in 0.61 ms.  The X group
-// sets that, M close behind it: its arithmetic on 64 x 128 values (conv, SiLU,
-// scaling, three fp16 packings), the S row through registers, and the latency
-// between them, at 53 % of the issue slots, 38 % of shared memory and 18 % of L2; the
-// tensor cores are at 25 %.  From 4.4 us it came there by x through registers rather
-// than a shared tile, M and the readout off the X group, packed fp32 pairs, one
-// exponential per piece of M (0.3 us of 3.0) and the loads on the issuing thread
-// (0.1); eight more X warps changed nothing.
+// Measured: a full walk takes 2.4 us a chunk and a lite one 1.6 (64 tokens x 128
+// channels, N = 128), i.e. 32768 tokens x 96 heads of 64 in 0.57 ms.  No unit is
+// near its limit (issue slots 60 %, shared memory 44 %, tensor cores 29 %, L2 21 %);
+// four chains of about that length run against each other: the X group's arithmetic
+// on 64 x 128 values (conv, SiLU, scaling, three fp16 packings) with the S row, M
+// behind its record, and MMAs -> readout -> next MMAs.  From 4.4 us it came there by
+// x through registers rather than a shared tile, M and the readout off the X group,
+// packed fp32 pairs, one exponential per piece of M, and the loads on the issuing
+// thread, behind the MMAs.  Eight more X warps changed nothing, nor did the S row on
+// the Y group's.
 #include "ssm_chunk.cuh"
 #include "tc_ptx.cuh"
 
