@@ -20,6 +20,11 @@ constexpr size_t WS_ALIGN = 256;
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+// an element of the call's I/O type
+bool aligned_io(const kda_params* p, const void* x) {
+    return (reinterpret_cast<uintptr_t>(x) & (p->io_dtype == KDA_DTYPE_BF16 ? 1u : 3u)) == 0;
+}
 
 int64_t count_chunks(const int64_t* cu, int32_t n) {
     int64_t c = 0;
@@ -686,7 +691,7 @@ kda_status kda_decode_tree(const kda_params* p, int32_t n_sessions, int32_t n_no
     const void* ptrs[8] = {q, k, v, z, gout, o, S, ring};
     for (int i = 0; i < 8; ++i)
         if (ptrs[i] == nullptr || !aligned16(ptrs[i])) return KDA_ERR_INVALID_ARG;
-    if (b == nullptr || parents == nullptr) return KDA_ERR_INVALID_ARG;
+    if (b == nullptr || parents == nullptr || !aligned_io(p, b) || !aligned4(parents) || !aligned4(slots)) return KDA_ERR_INVALID_ARG;
     if ((int64_t)n_sessions * p->num_heads > (int64_t)INT32_MAX) return KDA_ERR_UNSUPPORTED;
     TreeArgs ta{q, k, v, z, b, gout, p->conv_w, p->A_log, p->dt_bias, p->norm_w, parents, slots, S, ring, o, n_sessions,
                 p->num_heads, n_nodes, n_slots, p->gate_lower_bound, p->l2_eps, p->norm_eps, resolved_q_scale(p),
@@ -708,7 +713,9 @@ kda_status kda_tree_commit(const kda_params* p, int32_t n_sessions, int32_t n_no
     const void* ptrs[8] = {q, k, v, z, S_in, S_out, ring_in, ring_out};
     for (int i = 0; i < 8; ++i)
         if (ptrs[i] == nullptr || !aligned16(ptrs[i])) return KDA_ERR_INVALID_ARG;
-    if (b == nullptr || path == nullptr || path_len == nullptr) return KDA_ERR_INVALID_ARG;
+    if (b == nullptr || path == nullptr || path_len == nullptr || !aligned_io(p, b) || !aligned4(path) || !aligned4(path_len) ||
+        !aligned4(slots))
+        return KDA_ERR_INVALID_ARG;
     if ((int64_t)n_sessions * p->num_heads > (int64_t)INT32_MAX) return KDA_ERR_UNSUPPORTED;
     CommitArgs ca{q, k, v, z, b, p->conv_w, p->A_log, p->dt_bias, path, path_len, slots, S_in, S_out, ring_in, ring_out,
                   n_sessions, p->num_heads, n_nodes, max_len, n_slots, p->gate_lower_bound, p->l2_eps, p->gate_kind};

@@ -207,3 +207,13 @@ def test_binding_tree_tensors():
         a = {**rows, "path": par, "path_len": par[:, 0].contiguous(), "S_in": S, "ring_in": ring, **kw}
         with pytest.raises(ValueError):
             kda.kda_tree_commit(p, **a)
+
+
+@pytest.mark.parametrize("name", ["parents", "slots", "b"])
+def test_tree_refuses_misaligned_indices(L, name):
+    assert tree(L, kda_struct(), **{name: FAKE + 1}) == kda.KDA_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("name", ["path", "path_len", "slots", "b"])
+def test_commit_refuses_misaligned_indices(L, name):
+    assert commit(L, kda_struct(), **{name: FAKE + 1}) == kda.KDA_ERR_INVALID_ARG
