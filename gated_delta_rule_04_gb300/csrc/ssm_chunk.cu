@@ -129,6 +129,14 @@ __device__ __forceinline__ int m_exponent(int edt, int eb, int ec, float skip) {
     return e > es ? e : es;
 }
 
+// The exponent by which a state row of at most `bound` is scaled down, to below 2^14.  It
+// takes the whole range of a state (products of inputs, not an input): fp16 holds the
+// row up to 2^115, 2^-100 is far below what an fp32 state of such inputs resolves.
+__device__ __forceinline__ int state_exponent(float bound) {
+    const int e = (int)((__float_as_uint(bound) >> 23) & 255u) - 127 - 13;
+    return e < -100 ? -100 : e > 100 ? 100 : e;
+}
+
 // One piece of a sequence's chunks for one unit.  LITE: its end state from a zero start only.
 template <int P, int N, bool LITE>
 __device__ __forceinline__ void walk(const ChunkArgs& a, const int unit, const int seq, const int piece) {
@@ -266,7 +274,7 @@ __device__ __forceinline__ void walk(const ChunkArgs& a, const int unit, const i
         ptx::bar_sync_or(BAR_X, NX, false);
         sbound = fmaxf(xm[ch], xm[128 + ch]);
         ptx::bar_sync_or(BAR_X, NX, false);
-        int so = expo(2.f * sbound) - 13;                    // S = S' 2^so, |S'| < 2^14
+        int so = state_exponent(2.f * sbound);               // S = S' 2^so, |S'| < 2^14
         {
             // (an infinite state value leaves the rest of its channel no scale: NaN for all of it)
             const float f = sbound <= 3.4e38f ? pow2(-so) : __int_as_float(0x7fc00000);
@@ -361,8 +369,7 @@ __device__ __forceinline__ void walk(const ChunkArgs& a, const int unit, const i
             const int2 ebc = scale_of(c);
             const int ex = expo(fmaxf(xmc[ch], xmc[128 + ch]));
             const float bound = fmaf(dec, sbound, pow2(9 + ex + edt + ebc.x));   // of |S| after this chunk
-            int sn = (int)((__float_as_uint(bound) >> 23) & 255u) - 127 - 13;
-            sn = sn < -100 ? -100 : sn > 100 ? 100 : sn;
+            const int sn = state_exponent(bound);
             if (half == 0 && !LITE) {
                 sSX[b3 * 128 + ch] = pow2(m_exponent(edt, ebc.x, ebc.y, skip) + ex);
                 sSI[b3 * 128 + ch] = pow2(so + ebc.y);

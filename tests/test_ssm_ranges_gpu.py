@@ -1,0 +1,67 @@
+"""The state space mixer away from inputs of ordinary size: large and tiny
+values, states that only pass through, decays without bound, tokens of very
+unlike size in one chunk.  Against its definition token by token in 64 bits,
+with the tolerances of ``ssm_ref`` unless a test derives its own."""
+import math
+
+import pytest
+import torch
+
+import gated_delta_rule_04_gb300 as kda
+from ssm_ref import TOL, close, make_inputs, mixer
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+IO = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from gated_delta_rule_04_gb300 import build as kbuild
+    kbuild.build()
+    kda.lib()
+
+
+def dev(x):
+    return None if x is None else x.to(DEV)
+
+
+def params(i, io, algo="auto"):
+    return kda.make_ssm_params(dev(i["conv_w"]), dev(i["A_log"]), dev(i["dt_bias"]), head_dim=i["P"], state_dim=i["N"],
+                               num_groups=i["G"], D=dev(i["D"]), conv_b=dev(i["conv_b"]), io_dtype=io, algo=algo)
+
+
+def cumsum(lens):
+    cu = [0]
+    for x in lens:
+        cu.append(cu[-1] + x)
+    return cu
+
+
+def prefill(i, io, cu, rows=slice(None), **kw):
+    kw = {"S_in": dev(i["S"]), "ring_in": dev(i["ring"]), **kw}
+    return kda.kda_ssm_prefill(params(i, io), dev(i["xbc"][rows]), dev(i["dt"][rows]), cu, z=dev(i["z"][rows]), **kw)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("scale", [2.0 ** 22, 2.0 ** 25])
+def test_large_states_of_cut_and_continued_sequences(io, scale):
+    """Inputs whose states pass 2^44: every piece of a cut sequence and every continued
+    prompt starts from one, and its first chunk's outputs read it."""
+    cu = cumsum([1500, 40])
+    i = make_inputs(cu[-1], 2, 2, 64, 128, 1, IO[io], 61, bias=False)
+    i["A_log"] -= 2.0
+    i["xbc"] = (i["xbc"].float() * scale).to(IO[io])
+    i["ring"] = (i["ring"].float() * scale).to(IO[io])
+    i["S"] *= scale ** 2
+    wo, wS, _ = mixer(i, cu)
+    assert float(wS.abs().max()) > 2.0 ** 44
+    o, S, _ = prefill(i, io, cu)
+    close("o", o, wo)
+    close("S", S, wS)
+    # the same sequence in two parts, the second from the first one's state
+    T = 300
+    o1, S1, ring = prefill(i, io, [0, T], slice(0, T), S_in=dev(i["S"][:1]), ring_in=dev(i["ring"][:1]))
+    o2, S2, _ = prefill(i, io, [0, 1500 - T], slice(T, 1500), S_in=S1, ring_in=ring)
+    close("o in parts", torch.cat([o1, o2]), wo[:1500])
+    close("S in parts", S2, wS[:1])
