@@ -246,6 +246,12 @@ __device__ __forceinline__ void walk(const ChunkArgs& a, const int unit, const i
         float* sSI = reinterpret_cast<float*>(sb + L::SI);
         const size_t state = (size_t)N * P;
 
+        // ---- a sequence without tokens: the state as it is, bit by bit (the scales below would
+        // lose values far from their row's largest)
+        if (nc == 0 && valid) {
+            const size_t at = ((size_t)seq * g.H + h) * state + p;
+            for (int x = (N / 2) * half; x < (N / 2) * (half + 1); ++x) g.S_out[at + (size_t)x * P] = g.S_in ? g.S_in[at + (size_t)x * P] : 0.f;
+        }
         // ---- starting state: the caller's for the first piece; later ones compose the
         // end states of the pieces before them (zero in the lite pass)
         const float* start = piece == 0 && g.S_in ? g.S_in + ((size_t)seq * g.H + h) * state + p : nullptr;
@@ -443,7 +449,7 @@ __device__ __forceinline__ void walk(const ChunkArgs& a, const int unit, const i
             lsum += lend;
         }
         // ---- end state
-        const bool ok = nc == 0 || wait_or_abort(b_done, (uint32_t)(nc - 1) & 1u, abort_flag);
+        const bool ok = nc > 0 && wait_or_abort(b_done, (uint32_t)(nc - 1) & 1u, abort_flag);
         ptx::tc_fence_after();
         if (ok && !*abort_flag && valid && (LITE || last_piece || piece == 0)) {
             float* out = last_piece ? g.S_out + ((size_t)seq * g.H + h) * state + p

@@ -65,3 +65,23 @@ def test_large_states_of_cut_and_continued_sequences(io, scale):
     o2, S2, _ = prefill(i, io, [0, 1500 - T], slice(T, 1500), S_in=S1, ring_in=ring)
     close("o in parts", torch.cat([o1, o2]), wo[:1500])
     close("S in parts", S2, wS[:1])
+
+
+@pytest.mark.parametrize("io, algo", [("f32", "auto"), ("bf16", "auto"), ("bf16", "scan")])
+@pytest.mark.parametrize("lens", [[0, 5, 0], [0], [0, 0] + [3] * 16])
+def test_states_of_empty_sequences_pass_through_bit_by_bit(io, algo, lens):
+    H, P, N = 3, 64, 64
+    cu = cumsum(lens)
+    i = make_inputs(cu[-1], len(lens), H, P, N, 1, IO[io], 62)
+    empty = [s for s, n in enumerate(lens) if n == 0]
+    for s in empty:
+        i["S"][s, 0, 3, 5] = float("inf")
+        i["S"][s, 1, 60, 7] = float("nan")
+        i["S"][s, 2, 1, :] = 1e-42        # below fp32's normal range
+        i["S"][s, 2, 2, :] = 3e38
+    S_in, ring_in = dev(i["S"]), dev(i["ring"])
+    _, S, ring = kda.kda_ssm_prefill(params(i, io, algo), dev(i["xbc"]), dev(i["dt"]), cu, z=dev(i["z"]), S_in=S_in,
+                                     ring_in=ring_in)
+    for s in empty:
+        assert torch.equal(S[s].view(torch.int32), S_in[s].view(torch.int32))
+        assert torch.equal(ring[s].view(torch.uint8), ring_in[s].view(torch.uint8))
