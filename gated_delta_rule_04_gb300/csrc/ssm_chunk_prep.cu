@@ -57,7 +57,7 @@ __device__ void steps(const ChunkArgs& a, const ChunkDesc d, int chunk, int hb, 
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             dt[j] = sdt[2 * lane + j][hh];
-            l[j] = k * dt[j];
+            l[j] = 2 * lane + j < d.len ? k * dt[j] : 0.f;   // (k may be infinite: past the sequence nothing decays)
         }
         const float c0 = fmaxf(l[0], LAM_MIN), c1 = fmaxf(l[1], LAM_MIN);
         // inclusive prefix (plain and clamped) and suffix sums of the lanes' pairs

@@ -85,3 +85,17 @@ def test_states_of_empty_sequences_pass_through_bit_by_bit(io, algo, lens):
     for s in empty:
         assert torch.equal(S[s].view(torch.int32), S_in[s].view(torch.int32))
         assert torch.equal(ring[s].view(torch.uint8), ring_in[s].view(torch.uint8))
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("lens", [[64], [70, 3], [1], [200]])
+def test_a_decay_without_bound(io, lens):
+    """exp(A_log) past fp32's range: each of that head's tokens leaves only its own update,
+    in a chunk that the sequence fills and in one that it does not."""
+    cu = cumsum(lens)
+    i = make_inputs(cu[-1], len(lens), 4, 64, 64, 2, IO[io], 63)
+    i["A_log"][1] = 90.0
+    wo, wS, _ = mixer(i, cu)
+    o, S, _ = prefill(i, io, cu)
+    close("o", o, wo)
+    close("S", S, wS)
