@@ -123,10 +123,10 @@ __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, vol
 }
 
 // The exponent by which M is scaled down: |G'| <= 512 N / 128, dt < 2^(edt + 1),
-// and D on the diagonal.
+// and D on the diagonal, if there is one.
 __device__ __forceinline__ int m_exponent(int edt, int eb, int ec, float skip) {
     const int e = edt + eb + ec, es = expo(fabsf(skip)) - 8;
-    return e > es ? e : es;
+    return skip == 0.f || e > es ? e : es;
 }
 
 // The exponent by which a state row of at most `bound` is scaled down, to below 2^14.  It

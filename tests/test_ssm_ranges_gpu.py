@@ -99,3 +99,22 @@ def test_a_decay_without_bound(io, lens):
     o, S, _ = prefill(i, io, cu)
     close("o", o, wo)
     close("S", S, wS)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("skip", [True, False])
+def test_small_matrices_beside_large_rows(io, skip):
+    """B and C near 2^-38, x near 2^20: without the skip term the outputs are the scan's alone,
+    whose weights are near 2^-76."""
+    H, P, N = 2, 64, 128
+    cu = cumsum([140, 20])
+    i = make_inputs(cu[-1], 2, H, P, N, 1, IO[io], 64, bias=False, skip=skip)
+    scale = torch.full((H * P + 2 * N,), 2.0 ** -38)
+    scale[:H * P] = 2.0 ** 20
+    for k in ("xbc", "ring"):
+        i[k] = (i[k].float() * scale).to(IO[io])
+    i["S"] *= 2.0 ** -18
+    wo, wS, _ = mixer(i, cu)
+    o, S, _ = prefill(i, io, cu)
+    close("o", o, wo)
+    close("S", S, wS)
