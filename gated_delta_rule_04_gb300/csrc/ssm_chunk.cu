@@ -23,7 +23,8 @@
 // Operands are fp16 with exact power-of-two scales, so that they keep 11 bits
 // (22 in pairs) whatever the size of the inputs: B and C by chunk (from the
 // preparation), X by channel and chunk, dt by head and chunk, S by channel from
-// a running upper bound of its row.  The scales leave again where a thread
+// a running upper bound of its row.  Each lies as far up fp16's range as its sums allow, so
+// that a token may be small beside the largest of its chunk.  The scales leave again where a thread
 // holds its own channel: in the decay of S and in the readout of Y.
 //
 // Warp roles.  Warps 0-7 (X group; warp % 4 = lane quarter, warp / 4 = token
@@ -122,8 +123,10 @@ __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, vol
     return true;
 }
 
-// The exponent by which M is scaled down: |G'| <= 512 N / 128, dt < 2^(edt + 1),
-// and D on the diagonal, if there is one.
+// The exponent by which M is scaled down: |G'| <= 512 N / 128, dt < 2^(edt + 1), and D on the
+// diagonal, if there is one, so that |M'| < 2^10 + 2^9; M_TOP more and it fills fp16's range, for
+// the tokens whose row is small.
+constexpr int M_TOP = 5;
 __device__ __forceinline__ int m_exponent(int edt, int eb, int ec, float skip) {
     const int e = edt + eb + ec, es = expo(fabsf(skip)) - 8;
     return skip == 0.f || e > es ? e : es;
@@ -377,13 +380,14 @@ __device__ __forceinline__ void walk(const ChunkArgs& a, const int unit, const i
             const float bound = fmaf(dec, sbound, pow2(9 + ex + edt + ebc.x));   // of |S| after this chunk
             const int sn = state_exponent(bound);
             if (half == 0 && !LITE) {
-                sSX[b3 * 128 + ch] = pow2(m_exponent(edt, ebc.x, ebc.y, skip) + ex);
-                sSI[b3 * 128 + ch] = pow2(so + ebc.y);
+                // (products, so that they are infinite or zero past fp32's range: |em| <= 120, |so| <= 100)
+                sSX[b3 * 128 + ch] = pow2n(m_exponent(edt, ebc.x, ebc.y, skip) - M_TOP) * pow2n(ex);
+                sSI[b3 * 128 + ch] = pow2n(so) * pow2n(ebc.y - C_TOP);
             }
             // ---- operand rows of this half's tokens
             uint32_t xf[16], xh[16], xl[16];
             {
-                const float xs = pow2(-ex), kx = pow2(ebc.x - sn);
+                const float xs = pow2n(-ex), kx = pow2(ebc.x - B_TOP - sn);
                 const float2 xs2 = make_float2(xs, xs), kx2 = make_float2(kx, kx);
                 const float4* wt = reinterpret_cast<const float4*>(st + ST_W + 32 * half);
                 // fp16 pairs hold tokens (t, t + 1): column t / 2 from the low halves, 8 + t / 2 from the high
@@ -582,8 +586,8 @@ __device__ __forceinline__ void walk(const ChunkArgs& a, const int unit, const i
                     auto scale = [&](int hd, float& f, float& diag) {
                         const float skip = hd ? skip1 : skip0;
                         const int em = m_exponent(__float_as_int(step_of(c, head(hd))[ST_EDT]), ebc.x, ebc.y, skip);
-                        f = pow2(ebc.x + ebc.y - em);
-                        diag = skip * pow2(-em);
+                        f = pow2n(ebc.x + ebc.y - em + M_TOP - G_TOP);
+                        diag = skip * pow2n(M_TOP - em);
                     };
 #pragma unroll
                     for (int x = 0; x < (U * 64 + NM - 1) / NM; ++x) {

@@ -11,11 +11,16 @@ namespace ssm {
 
 // Record of one (chunk, group): the operand tiles that do not depend on the
 // head, as the byte image of the consumer's shared memory (fp16, K-major,
-// 128-byte swizzle).  B and C are stored scaled by powers of two so that the
-// tile's largest magnitude lies in [1, 2):
-//   B^T hi, B^T lo  [N rows][64 tok]   B' = hi + lo to 22 bits
-//   C               [64 tok rows][N]
-//   G = C' B'^T     [64 tok rows][64]  8-column pieces up to the diagonal only
+// 128-byte swizzle).  B and C are stored scaled by powers of two, the exponents of the
+// tile's largest magnitude and how far up fp16's range that comes to lie:
+//   B^T hi, B^T lo  [N rows][64 tok]   B' = hi + lo to 22 bits, below 2^(B_TOP + 1)
+//   C               [64 tok rows][N]   below 2^(C_TOP + 1)
+//   G = C B^T       [64 tok rows][64]  below 512 x 2^G_TOP; 8-column pieces up to the diagonal only
+// The further up, the smaller a token's row may be beside the chunk's largest before it
+// falls out of fp16's normal range and loses digits.  C has no other limit than that range;
+// B shares the scale of the state that its product with X~ goes to (S' below 2^14), which
+// leaves X~ less for every bit here; G lies as high as its sum of N products allows.
+constexpr int B_TOP = 4, C_TOP = 14, G_TOP = 6;
 template <int N> struct Rec {
     static constexpr uint32_t BT = N * 128;             // bytes of B^T hi (and of lo)
     static constexpr uint32_t OFF_LO = BT;
@@ -48,6 +53,8 @@ __device__ __forceinline__ int expo(float x) {
     const int e = (int)((__float_as_uint(x) >> 23) & 255u) - 127;
     return e < -40 ? -40 : e > 40 ? 40 : e;
 }
+// 2^e for an e within fp32's normal range.
+__device__ __forceinline__ float pow2n(int e) { return __int_as_float((e + 127) << 23); }
 // 2^e for any integer e, clamped to fp32's normal range.
 __device__ __forceinline__ float pow2(int e) {
     e = e < -126 ? -126 : e > 127 ? 127 : e;

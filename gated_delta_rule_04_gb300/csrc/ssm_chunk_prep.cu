@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(NT, 2) prep_kernel(const __grid_constant__ Chu
     if (tid == 0) a.scale[(size_t)chunk * g.G + grp] = make_int4(eb, ec, 0, 0);
     // an infinity leaves no scale for the rest of its tile: all of it NaN, rather than
     // finite rows that lost their digits
-    const float top = is_c ? mc : mb, s = top <= 3.4e38f ? pow2(is_c ? -ec : -eb) : __int_as_float(0x7fc00000);
+    const float top = is_c ? mc : mb, s = top <= 3.4e38f ? pow2(is_c ? C_TOP - ec : B_TOP - eb) : __int_as_float(0x7fc00000);
     unsigned char* tile = is_c ? sC : sB;
 #pragma unroll
     for (int t = 0; t < TP; ++t) {
@@ -238,6 +238,8 @@ __global__ void __launch_bounds__(NT, 2) prep_kernel(const __grid_constant__ Chu
             for (int j = 0; j < 2; ++j) {
                 float f[32];
                 ptx::tmem_ld32(tmem + ((uint32_t)(32 * warp) << 16) + 32 * j, f);
+#pragma unroll
+                for (int x = 0; x < 32; ++x) f[x] *= pow2(G_TOP - C_TOP - B_TOP);
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
                     if (4 * j + q <= row >> 3)

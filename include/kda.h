@@ -389,10 +389,16 @@ size_t kda_ssm_prefill_workspace_bytes(const kda_ssm_params* p, int32_t n_seqs, 
  *   workspace      : device, >= kda_ssm_prefill_workspace_bytes(), 256-byte aligned;
  *                  its error word is read with kda_workspace_status
  * Zero-length sequences copy their state and ring through unchanged.
- * The chunked algorithm takes 64 tokens at a time as matrix products of scaled
- * fp16 operands (the state's as pairs): finite inputs up to 2^40 in magnitude
- * keep their precision, and a NaN or an infinity may turn the outputs of its
- * whole 64-token chunk in that group NaN, earlier tokens included, besides all
+ * The chunked algorithm takes 64 tokens at a time as matrix products of fp16
+ * operands: 11 bits for the outputs, which are bf16, pairs of 22 bits for the
+ * state, which is fp32 (KDA_ALGO_SCAN computes in fp32 throughout).  The operands
+ * are scaled by powers of two: B and C per chunk, x per channel and chunk, dt per
+ * head and chunk, the state per channel.  The scales cover values from 2^-40 to 2^40
+ * and states from 2^-100 to 2^110; products past fp32's range come out infinite or
+ * NaN.  Beside the largest of its chunk a token keeps its digits down to 2^-18 of it
+ * in C and in dt |B| |C|, and to 2^-12 in x; in the state, what a B of 2^-10 of
+ * its chunk's largest adds keeps 19 bits.  A NaN or an infinity may turn the outputs
+ * of its whole 64-token chunk in that group NaN, earlier tokens included, besides all
  * that follows.  Other sequences never see it.
  */
 kda_status kda_ssm_prefill(const kda_ssm_params* p, const void* xbc, int64_t xbc_stride,

@@ -118,3 +118,63 @@ def test_small_matrices_beside_large_rows(io, skip):
     o, S, _ = prefill(i, io, cu)
     close("o", o, wo)
     close("S", S, wS)
+
+
+def test_outputs_past_the_range_never_look_finite():
+    """C and state so large that their product passes fp32's range: what the definition puts
+    past it comes out infinite or NaN, and the tokens of ordinary size in its chunk as they are."""
+    H, P, N, T = 2, 64, 64, 80
+    i = make_inputs(T, 1, H, P, N, 1, torch.bfloat16, 65, bias=False)
+    i["A_log"] -= 6.0
+    i["S"] *= 2.0 ** 108
+    i["xbc"][:, H * P + N:] = (i["xbc"][:, H * P + N:].float() * 2.0 ** 22).to(torch.bfloat16)
+    i["xbc"][66:, H * P + N:] = 0.25                     # (from token 69 on the whole conv window)
+    wo, wS, _ = mixer(i, [0, T])
+    o, S, _ = prefill(i, "bf16", [0, T])
+    top = float(torch.finfo(torch.bfloat16).max)
+    o = o.cpu().double()
+    assert not (torch.isfinite(o) & (wo.abs() > 1.01 * top)).any()
+    assert torch.isfinite(wo[69:].bfloat16()).all()
+    close("o", o[69:], wo[69:], TOL[torch.bfloat16])
+    close("S", S, wS)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("at", [0, 17, 63, 64, 90])
+@pytest.mark.parametrize("what", ["B", "C", "BC", "x"])
+def test_one_large_token_leaves_the_others_their_digits(io, at, what):
+    """A token whose B or x is 2^10, whose C 2^18, or B and C 2^9 each larger than the others' of
+    its chunk.  Outputs of the other tokens are held to the tolerance each by itself, where
+    the large one has not reached them (C: nowhere; x and B: before it)."""
+    H, P, N, T = 2, 64, 128, 130
+    i = make_inputs(T, 1, H, P, N, 1, IO[io], 66, bias=False)
+    i["conv_w"][:, :3] = 0.0                              # (a token's rows are its own)
+    cols = {"x": [slice(0, H * P)], "B": [slice(H * P, H * P + N)], "C": [slice(H * P + N, H * P + 2 * N)]}
+    for w in what:
+        for c in cols[w]:
+            i["xbc"][at, c] = (i["xbc"][at, c].float() * {'C': 2 ** 18, 'BC': 2 ** 9}.get(what, 2 ** 10)).to(IO[io])
+    wo, wS, _ = mixer(i, [0, T])
+    o, S, _ = prefill(i, io, [0, T])
+    close("S", S, wS)
+    o = o.cpu()
+    for t in range(T):
+        if t != at and (what == "C" or t < at):
+            close(f"o[{t}]", o[t], wo[t])
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_a_large_token_that_decays_leaves_the_state_its_digits(io):
+    """The first token's B is 2^10 larger, and gone after a few steps: what the later ones
+    leave in the state keeps an fp32 state's precision."""
+    H, P, N, T = 2, 64, 64, 64
+    i = make_inputs(T, 1, H, P, N, 1, IO[io], 67, state=False)
+    i["A_log"][:] = 2.0
+    i["dt_bias"][:] = 0.5                                 # a step's decay is about e^-7
+    i["conv_w"][:, :3] = 0.0
+    c = slice(H * P, H * P + N)
+    i["xbc"][0, c] = (i["xbc"][0, c].float() * 1024).to(IO[io])
+    wo, wS, _ = mixer(i, [0, T])
+    o, S, _ = prefill(i, io, [0, T])
+    close("S", S, wS)
+    for t in (0, 20, 40, 63):
+        close(f"o[{t}]", o[t], wo[t])
