@@ -126,7 +126,7 @@ __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, vol
 // The exponent by which M is scaled down: |G'| <= 512 N / 128, dt < 2^(edt + 1), and D on the
 // diagonal, if there is one, so that |M'| < 2^10 + 2^9; M_TOP more and it fills fp16's range, for
 // the tokens whose row is small.
-constexpr int M_TOP = 5;
+constexpr int M_TOP = 5, X_TOP = 14;       // (X by channel, below 2^(X_TOP + 1): their products are summed in fp32)
 __device__ __forceinline__ int m_exponent(int edt, int eb, int ec, float skip) {
     const int e = edt + eb + ec, es = expo(fabsf(skip)) - 8;
     return skip == 0.f || e > es ? e : es;
@@ -377,17 +377,19 @@ __device__ __forceinline__ void walk(const ChunkArgs& a, const int unit, const i
             const int edt = __float_as_int(st[ST_EDT]);
             const int2 ebc = scale_of(c);
             const int ex = expo(fmaxf(xmc[ch], xmc[128 + ch]));
-            const float bound = fmaf(dec, sbound, pow2(9 + ex + edt + ebc.x));   // of |S| after this chunk
+            // of |S| after this chunk.  (The weights' sum knows the decay: 64 times the largest dt is
+            // 2^9 more for a head that forgets a token within 10, digits that its state then lacks.)
+            const float bound = fmaf(dec, sbound, pow2n(2 + ex + ebc.x) * st[ST_WSUM]);
             const int sn = state_exponent(bound);
             if (half == 0 && !LITE) {
                 // (products, so that they are infinite or zero past fp32's range: |em| <= 120, |so| <= 100)
-                sSX[b3 * 128 + ch] = pow2n(m_exponent(edt, ebc.x, ebc.y, skip) - M_TOP) * pow2n(ex);
+                sSX[b3 * 128 + ch] = pow2n(m_exponent(edt, ebc.x, ebc.y, skip) - M_TOP) * pow2n(ex - X_TOP);
                 sSI[b3 * 128 + ch] = pow2n(so) * pow2n(ebc.y - C_TOP);
             }
             // ---- operand rows of this half's tokens
             uint32_t xf[16], xh[16], xl[16];
             {
-                const float xs = pow2n(-ex), kx = pow2(ebc.x - B_TOP - sn);
+                const float xs = pow2n(X_TOP - ex), kx = pow2(ebc.x - B_TOP - sn);
                 const float2 xs2 = make_float2(xs, xs), kx2 = make_float2(kx, kx);
                 const float4* wt = reinterpret_cast<const float4*>(st + ST_W + 32 * half);
                 // fp16 pairs hold tokens (t, t + 1): column t / 2 from the low halves, 8 + t / 2 from the high

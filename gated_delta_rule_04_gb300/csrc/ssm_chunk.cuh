@@ -40,9 +40,11 @@ inline size_t rec_bytes(int N) { return N == 64 ? Rec<64>::BYTES : Rec<128>::BYT
 //               suffix sum (a difference of long prefix sums would cost the fp32
 //               state its last digits); token t at w_at(t), next to token t + 16
 //   [192, 256)  2^(sum_{s <= t} l_s)
-//   [256]       2^(sum of all l_s), [257] exponent of the largest dt (int), [258] sum of l_s
+//   [256]       2^(sum of all l_s), [257] exponent of the largest dt (int), [258] sum of l_s,
+//               [259] sum of the tokens' weights (at least 2^-40): what bounds the chunk's
+//               addition to the state
 constexpr int STEP_FLOATS = 260;
-constexpr int ST_DT = 64, ST_W = 128, ST_EL = 192, ST_DEC = 256, ST_EDT = 257, ST_LOG = 258;
+constexpr int ST_DT = 64, ST_W = 128, ST_EL = 192, ST_DEC = 256, ST_EDT = 257, ST_LOG = 258, ST_WSUM = 259;
 constexpr float LAM_MIN = -40.f;
 // The X group takes tokens t and t + 16 of a 32-token half as one packed pair.
 __host__ __device__ constexpr int w_at(int t) { return (t & 32) + 2 * (t & 15) + ((t >> 4) & 1); }

@@ -83,11 +83,15 @@ __device__ void steps(const ChunkArgs& a, const ChunkDesc d, int chunk, int hb, 
         // (an infinite step leaves the others of the chunk no scale: NaN for all of them)
         if (!(top <= 3.4e38f)) dt[0] = dt[1] = __int_as_float(0x7fc00000);
         *reinterpret_cast<float2*>(out + ST_DT + 2 * lane) = make_float2(dt[0], dt[1]);
-        out[ST_W + w_at(2 * lane)] = ex2(l[1] + sa) * dt[0];
-        out[ST_W + w_at(2 * lane + 1)] = ex2(sa) * dt[1];
+        const float w0 = ex2(l[1] + sa) * dt[0], w1 = ex2(sa) * dt[1];
+        float wsum = w0 + w1;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) wsum += __shfl_xor_sync(0xffffffffu, wsum, o);
+        out[ST_W + w_at(2 * lane)] = w0;
+        out[ST_W + w_at(2 * lane + 1)] = w1;
         *reinterpret_cast<float2*>(out + ST_EL + 2 * lane) = make_float2(ex2(pb + l[0]), ex2(pb + l[0] + l[1]));
         if (lane == 0)
-            *reinterpret_cast<float4*>(out + ST_DEC) = make_float4(ex2(end), __int_as_float(expo(top)), end, 0.f);
+            *reinterpret_cast<float4*>(out + ST_DEC) = make_float4(ex2(end), __int_as_float(expo(top)), end, fmaxf(wsum, pow2n(-40)));
     }
 }
 

@@ -396,8 +396,9 @@ size_t kda_ssm_prefill_workspace_bytes(const kda_ssm_params* p, int32_t n_seqs, 
  * head and chunk, the state per channel.  The scales cover values from 2^-40 to 2^40
  * and states from 2^-100 to 2^110; products past fp32's range come out infinite or
  * NaN.  Beside the largest of its chunk a token keeps its digits down to 2^-18 of it
- * in C and in dt |B| |C|, and to 2^-12 in x; in the state, what a B of 2^-10 of
- * its chunk's largest adds keeps 19 bits.  A NaN or an infinity may turn the outputs
+ * in x, in C and in dt |B| |C|.  A chunk leaves the state an error of at most 2^-25 of
+ * its largest x times its largest B times the sum of its steps (as decayed to its end)
+ * in a channel, beside the 22 bits.  A NaN or an infinity may turn the outputs
  * of its whole 64-token chunk in that group NaN, earlier tokens included, besides all
  * that follows.  Other sequences never see it.
  */

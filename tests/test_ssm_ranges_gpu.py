@@ -178,3 +178,43 @@ def test_a_large_token_that_decays_leaves_the_state_its_digits(io):
     close("S", S, wS)
     for t in (0, 20, 40, 63):
         close(f"o[{t}]", o[t], wo[t])
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("at", [17, 63, 90])
+def test_an_x_far_larger_than_those_before_it(io, at):
+    """The same with an x 2^18 larger, whose channels' earlier values share its scale.
+
+    The state: an operand pair ends at 2^-25 where the state is scaled to below 2^14, by a
+    bound of at most 4 max|x| max|B| sum(dt) beside what there was: 64 tokens of it, times a
+    B of less than 2^5, are 2^-25 max|x| max|B| sum(dt) an element."""
+    H, P, N, T = 2, 64, 64, 130
+    i = make_inputs(T, 1, H, P, N, 1, IO[io], 69, bias=False)
+    i["conv_w"][:, :3] = 0.0
+    i["xbc"][at, :H * P] = (i["xbc"][at, :H * P].float() * 2 ** 18).to(IO[io])
+    wo, wS, _ = mixer(i, [0, T])
+    o, S, _ = prefill(i, io, [0, T])
+    u = i["xbc"].double() * i["conv_w"][:, 3].double()
+    u = (u * torch.sigmoid(u)).abs()
+    steps = torch.nn.functional.softplus(i["dt"].double() + i["dt_bias"].double())[64 * (at // 64):][:64].sum(0).max()
+    most = float(u[:, :H * P].max() * u[:, H * P:H * P + N].max() * steps)
+    close("S", S, wS, TOL[torch.float32] + 2.0 ** -25 * most * math.sqrt(wS.numel()) / float(wS.norm()))
+    o = o.cpu()
+    for t in range(at):
+        close(f"o[{t}]", o[t], wo[t])
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_a_large_x_that_decays_leaves_the_state_its_digits(io):
+    """As with B above, of an x: the bound that scales the state knows the decay."""
+    H, P, N, T = 2, 64, 64, 64
+    i = make_inputs(T, 1, H, P, N, 1, IO[io], 70, state=False)
+    i["A_log"][:] = 2.0
+    i["dt_bias"][:] = 0.5
+    i["conv_w"][:, :3] = 0.0
+    i["xbc"][0, :H * P] = (i["xbc"][0, :H * P].float() * 1024).to(IO[io])
+    wo, wS, _ = mixer(i, [0, T])
+    o, S, _ = prefill(i, io, [0, T])
+    close("S", S, wS)
+    for t in (0, 20, 40, 63):
+        close(f"o[{t}]", o[t], wo[t])
