@@ -218,3 +218,28 @@ def test_a_large_x_that_decays_leaves_the_state_its_digits(io):
     close("S", S, wS)
     for t in (0, 20, 40, 63):
         close(f"o[{t}]", o[t], wo[t])
+
+
+@pytest.mark.parametrize("call", ["prefill", "token", "tokens in two kernels"])
+def test_silu_to_fp32_rounding(call):
+    """fp32 I/O, one token from a zero state: every element of the state is dt * SiLU(b) * SiLU(x).
+
+    Roundings of 2^-24 each, at most: SiLU 8 (exp 2 ulp = 4, the sum 1, a reciprocal of 1 ulp = 2,
+    the product 1), of B and of x; softplus 8 (exp 4, log1p 2 ulp = 4); two products 2: 26."""
+    H, P, N = 2, 64, 64
+    i = make_inputs(1, 1, H, P, N, 1, torch.float32, 68, state=False, bias=False)
+    i["conv_w"][:] = torch.tensor([0.0, 0.0, 0.0, 1.0])
+    i["xbc"][0, :H * P] = torch.linspace(-40, 40, H * P)
+    i["xbc"][0, H * P:H * P + N] = torch.linspace(-30, 30, N)
+    _, want, _ = mixer(i, [0, 1])
+    n = 1100 if call == "tokens in two kernels" else 1     # (more than 32 MB of states)
+    p = params(i, "f32")
+    if call == "prefill":
+        _, S, _ = prefill(i, "f32", [0, 1])
+    else:
+        assert (kda.kda_ssm_decode_workspace_bytes(p, n) > 0) == (n > 1)
+        S = torch.zeros(n, H, N, P, device=DEV)
+        ring = torch.zeros(n, 3, H * P + 2 * N, device=DEV)
+        kda.kda_ssm_decode(p, dev(i["xbc"]).repeat(n, 1), dev(i["dt"]).repeat(n, 1), S, ring, z=dev(i["z"]).repeat(n, 1))
+    err = ((S.cpu().double() - want) / want).abs().max()
+    assert float(err) <= 26 * 2.0 ** -24
