@@ -53,7 +53,9 @@ constexpr int NT = 256;                     // commit kernel
 constexpr int RMAX = KDA_TREE_MAX_NODES;
 constexpr uint64_t WAIT_LIMIT_NS = 2000000000ull;
 constexpr uint32_t TM_HI = 0, TM_LO = 64, TM_D = 128, TMEM_COLS = 256;
-constexpr float ROW_SCALE = 256.f;          // of the fp16 rows: unit vectors, so that their low halves are normal
+// of the fp16 rows, so that their low halves are normal: unit vectors, k^ and q^ alike (q_scale,
+// which may be of any size, multiplies the outputs)
+constexpr float ROW_SCALE = 256.f;
 
 struct TreeHead {
     float beta[RMAX];
@@ -377,7 +379,7 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) tree_kernel(TreeArgs a
                 v[2 * x + 1] = k4[x].x * k4[x].x + k4[x].y * k4[x].y + k4[x].z * k4[x].z + k4[x].w * k4[x].w;
             }
             const float sum = warp_sum8(v, lane);
-            const float rn = rsqrtf(sum + a.l2_eps) * ((lane >> 2) & 1 ? 1.f : a.q_scale);
+            const float rn = rsqrtf(sum + a.l2_eps);
             __syncwarp();
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
@@ -553,6 +555,7 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) tree_kernel(TreeArgs a
                     o4[x].z = fmaf(wd[m], u4.z, o4[x].z); o4[x].w = fmaf(wd[m], u4.w, o4[x].w);
                 }
             }
+            o4[x].x *= a.q_scale; o4[x].y *= a.q_scale; o4[x].z *= a.q_scale; o4[x].w *= a.q_scale;
             ss[x] = o4[x].x * o4[x].x + o4[x].y * o4[x].y + o4[x].z * o4[x].z + o4[x].w * o4[x].w;
         }
         const float rms = rsqrtf(warp_sum8(ss, lane) * (1.0f / D) + a.norm_eps);

@@ -10,7 +10,7 @@ import pytest
 import torch
 
 import gated_delta_rule_04_gb300 as kda
-from kda_testlib import rel_l2
+from kda_testlib import kda_params, rel_l2
 from test_tree_gpu import DEV, TOL, Round, check_rows, path_to, tree
 
 pytestmark = pytest.mark.gpu
@@ -81,3 +81,16 @@ def test_several_commits_a_cta(io, separate):
         assert bool((S2[rest] == 9.0).all()) and bool((r2[rest] == 9.0).all())
     else:
         assert torch.equal(S2[rest].cpu(), rd.S[rest]) and torch.equal(r2[rest].cpu(), rd.ring[rest])
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("q_scale", [1e-6, 1.0, 3000.0, 1e12])
+def test_any_q_scale(io, q_scale):
+    """q^ is a unit vector times q_scale, whatever its size; the output's norm takes its eps
+    from outside the range of the squares, so that the scale is seen."""
+    rd = Round(io, 2, 11, seed=31)
+    rd.p.q_scale, rd.p.norm_eps = q_scale, 1e-5 * q_scale * q_scale
+    rd.kp = kda_params(rd.p, io)
+    rng = random.Random(31)
+    parents = [tree("bushy", 11, rng) for _ in range(2)]
+    check_rows(rd, rd.decode(parents), parents)
