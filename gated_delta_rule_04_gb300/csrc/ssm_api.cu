@@ -86,6 +86,12 @@ int64_t piece_slots(const kda_ssm_params* p, int64_t n_seqs) {
     if (n_seqs * units >= 8 * SMS_GB300) return 0;
     return std::max<int64_t>(2 * SMS_GB300 / units, 4 * n_seqs);
 }
+// The most of any call of up to n_seqs sequences: a workspace for a full batch serves the
+// smaller ones, whose sequences are the ones that are cut.
+int64_t most_piece_slots(const kda_ssm_params* p, int64_t n_seqs) {
+    const int64_t units = (int64_t)units_per_group(p) * p->num_groups;
+    return piece_slots(p, std::min(n_seqs, (8 * SMS_GB300 - 1) / units));
+}
 
 // Workspace of a prefill: error word | cu_seqlens | first chunks | order, and
 // for the chunked form chunk table | step records | scales | group records |
@@ -93,7 +99,7 @@ int64_t piece_slots(const kda_ssm_params* p, int64_t n_seqs) {
 struct Layout {
     size_t cu = 0, coff = 0, order = 0, chunks = 0, step = 0, scale = 0, rec = 0, local = 0, ltot = 0, total = 0;
 };
-Layout layout(const kda_ssm_params* p, int algo, int64_t n_seqs, int64_t total_tokens) {
+Layout layout(const kda_ssm_params* p, int algo, int64_t n_seqs, int64_t total_tokens, int64_t slots) {
     Layout L;
     size_t off = WS_ALIGN;
     auto take = [&](size_t bytes) { const size_t at = off; off = align_up(off + bytes); return at; };
@@ -103,13 +109,13 @@ Layout layout(const kda_ssm_params* p, int algo, int64_t n_seqs, int64_t total_t
     if (algo == KDA_ALGO_CHUNKED) {
         // every sequence may end in a partial chunk
         const size_t nck = (size_t)(total_tokens / CHUNK_T + std::min(n_seqs, total_tokens));
-        const size_t slots = (size_t)piece_slots(p, n_seqs), H = p->num_heads, G = p->num_groups;
+        const size_t H = p->num_heads, G = p->num_groups;
         L.chunks = take(sizeof(ChunkDesc) * nck);
         L.step = take(sizeof(float) * STEP_FLOATS * nck * H);
         L.scale = take(sizeof(int4) * nck * G);
         L.rec = take(rec_bytes(p->state_dim) * nck * G);
-        L.local = take(sizeof(float) * slots * H * p->state_dim * p->head_dim);
-        L.ltot = take(sizeof(float) * slots * H);
+        L.local = take(sizeof(float) * (size_t)slots * H * p->state_dim * p->head_dim);
+        L.ltot = take(sizeof(float) * (size_t)slots * H);
     }
     L.total = off;
     return L;
@@ -253,7 +259,7 @@ size_t kda_ssm_prefill_workspace_bytes(const kda_ssm_params* p, int32_t n_seqs, 
     if (ssm::check_params(p) != KDA_OK || ssm::resolve_algo(p, &algo) != KDA_OK || n_seqs < 0 || total_tokens < 0)
         return 0;
     if (n_seqs == 0) return 0;
-    return ssm::layout(p, algo, n_seqs, total_tokens).total;
+    return ssm::layout(p, algo, n_seqs, total_tokens, ssm::most_piece_slots(p, n_seqs)).total;
 }
 
 kda_status kda_ssm_prefill(const kda_ssm_params* p, const void* xbc, int64_t xbc_stride, const void* dt,
@@ -278,12 +284,12 @@ kda_status kda_ssm_prefill(const kda_ssm_params* p, const void* xbc, int64_t xbc
         chunks_most * (p->num_groups + p->num_heads / 32 + 1) > (int64_t)INT32_MAX)
         return KDA_ERR_UNSUPPORTED;
     if (workspace == nullptr || !aligned(workspace, WS_ALIGN) ||
-        workspace_bytes < kda_ssm_prefill_workspace_bytes(p, n_seqs, total_tokens))
+        workspace_bytes < ssm::layout(p, algo, n_seqs, total_tokens, ssm::piece_slots(p, n_seqs)).total)
         return KDA_ERR_WORKSPACE;
 
     cudaStream_t s = static_cast<cudaStream_t>(stream_);
     unsigned char* ws = static_cast<unsigned char*>(workspace);
-    const Layout L = ssm::layout(p, algo, n_seqs, total_tokens);
+    const Layout L = ssm::layout(p, algo, n_seqs, total_tokens, ssm::piece_slots(p, n_seqs));
     // longest sequences first: their walks take longest
     std::vector<int32_t> order;
     try {

@@ -367,8 +367,9 @@ typedef struct {
 int32_t kda_ssm_prefill_algo(const kda_ssm_params* p);
 
 /* Bytes of device workspace kda_ssm_prefill needs (0 when it needs none or
- * would reject the arguments).  For the chunked algorithm the size covers any
- * split of total_tokens into n_seqs sequences. */
+ * would reject the arguments), for any split of total_tokens into n_seqs
+ * sequences.  It never falls with more sequences or tokens, so a workspace for the
+ * largest call serves every smaller one. */
 size_t kda_ssm_prefill_workspace_bytes(const kda_ssm_params* p, int32_t n_seqs, int64_t total_tokens);
 
 /*
@@ -408,9 +409,9 @@ kda_status kda_ssm_prefill(const kda_ssm_params* p, const void* xbc, int64_t xbc
                            const float* S_in, float* S_out, const void* ring_in, void* ring_out,
                            void* o, void* workspace, size_t workspace_bytes, void* stream);
 
-/* Bytes of device workspace kda_ssm_decode needs for n_sessions (or fewer, as
- * long as this size does not shrink to 0): 0 where the call runs as one kernel
- * (up to 32 MB of states and 32 heads a group), and for rejected arguments. */
+/* Bytes of device workspace kda_ssm_decode needs for n_sessions or fewer: 0 where
+ * the call runs as one kernel (up to 32 MB of states and 32 heads a group), and
+ * for rejected arguments. */
 size_t kda_ssm_decode_workspace_bytes(const kda_ssm_params* p, int32_t n_sessions);
 
 /*
