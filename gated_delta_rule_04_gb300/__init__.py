@@ -167,10 +167,19 @@ class Params:
     tensors: tuple
     num_heads: int
     io_dtype: int
+    device: int           # CUDA device of the tensors (-1: none)
 
     @property
     def ref(self):
         return ctypes.byref(self.struct)
+
+
+def _params_device(tensors):
+    """The CUDA device (-1: none) that all of the parameter tensors are on, or ValueError."""
+    devs = {t.device for t in tensors if t is not None}
+    if len(devs) > 1:
+        raise ValueError(f"parameters: expected one device, got {sorted(map(str, devs))}")
+    return tensors[0].get_device()
 
 
 KDA_GATE_BOUNDED, KDA_GATE_SOFTPLUS = 0, 1
@@ -189,7 +198,7 @@ def make_params(conv_w, A_log, dt_bias, norm_w, *, io_dtype: str = "bf16", algo:
     tensors = tuple(t.contiguous() for t in (conv_w, A_log, dt_bias, norm_w))
     st = kda_params(H, 128, 4, dt, _ALGOS[algo], gate_lower_bound, l2_eps, norm_eps, q_scale,
                     *[t.data_ptr() for t in tensors], _GATES[gate], int(wait_limit_us))
-    return Params(st, tensors, H, dt)
+    return Params(st, tensors, H, dt, _params_device(tensors))
 
 
 def kda_prefill_algo(params: Params) -> str:
@@ -402,6 +411,12 @@ def _rows(name, t, dtype, n, width, dev):
     return t.data_ptr(), stride
 
 
+def _same_device(params, dev):
+    if params.device != dev:
+        raise ValueError(f"parameters: they are on {'no CUDA device' if params.device < 0 else f'cuda:{params.device}'}, the "
+                         f"call's tensors on {'none' if dev < 0 else f'cuda:{dev}'}")
+
+
 def _call(name, dev, f, *args, stream=None):
     """Calls ``f`` with CUDA device ``dev`` current, on ``stream`` (default: that device's current stream)."""
     import torch
@@ -435,6 +450,7 @@ def kda_decode_tree(params: Params, q, k, v, z, b, gout, parents, S, ring, slots
         raise ValueError(f"q: expected [n][n_nodes][H*128], got {list(q.shape)}")
     n, R, _ = q.shape
     H, dev = params.num_heads, q.get_device()
+    _same_device(params, dev)
     rows = (n, R, H * 128)
     S_p, slots_n = _pool("S", S, torch.float32, (H, 128, 128), dev)
     args = (params.ref, n, R, _shaped("q", q, t, rows, dev), _shaped("k", k, t, rows, dev), _shaped("v", v, t, rows, dev),
@@ -458,6 +474,7 @@ def kda_tree_commit(params: Params, q, k, v, z, b, path, path_len, S_in, ring_in
         raise ValueError(f"q, path: expected [n][n_nodes][H*128] and [n][max_len], got {list(q.shape)}, {list(path.shape)}")
     n, R, _ = q.shape
     H, m, dev = params.num_heads, path.shape[1], q.get_device()
+    _same_device(params, dev)
     S_out = S_in if S_out is None else S_out
     ring_out = ring_in if ring_out is None else ring_out
     rows = (n, R, H * 128)
@@ -485,6 +502,7 @@ class SsmParams:
     io_dtype: int
     channels: int         # conv channels of a token: x (H*P) | B (G*N) | C (G*N)
     torch_dtype: object   # torch type of xbc, dt, z, o and the ring
+    device: int           # CUDA device of the parameter tensors (-1: none)
     ref: object           # pointer to the struct
 
 
@@ -503,7 +521,8 @@ def make_ssm_params(conv_w, A_log, dt_bias, *, head_dim: int, state_dim: int, nu
     dt = {"f32": KDA_DTYPE_F32, "bf16": KDA_DTYPE_BF16}[io_dtype]
     tensors = tuple(None if x is None else x.contiguous() for x in (conv_w, conv_b, A_log, dt_bias, D))
     st = kda_ssm_params(H, int(head_dim), int(state_dim), int(num_groups), 4, dt, _ALGOS[algo], *[_ptr(x) for x in tensors])
-    return SsmParams(st, tensors, H, int(head_dim), int(state_dim), int(num_groups), dt, ch, _io_torch(dt), ctypes.byref(st))
+    return SsmParams(st, tensors, H, int(head_dim), int(state_dim), int(num_groups), dt, ch, _io_torch(dt), _params_device(tensors),
+                     ctypes.byref(st))
 
 
 def kda_ssm_prefill_algo(params: SsmParams) -> str:
@@ -530,6 +549,7 @@ def kda_ssm_prefill(params: SsmParams, xbc, dt, cu_seqlens, z=None, S_in=None, S
     cu, n, T = _cu_array(cu_seqlens)
     t, H, P, N, ch = params.torch_dtype, params.num_heads, params.head_dim, params.state_dim, params.channels
     dev, f32 = xbc.get_device(), torch.float32
+    _same_device(params, dev)
     x_p, sx = _rows("xbc", xbc, t, T, ch, dev)
     d_p, sd = _rows("dt", dt, t, T, H, dev)
     z_p, sz = (None, 0) if z is None else _rows("z", z, t, T, H * P, dev)
@@ -556,6 +576,7 @@ def kda_ssm_decode(params: SsmParams, xbc, dt, S, ring, z=None, slots=None, o=No
     n = xbc.shape[0]
     t, H, P, N, ch = params.torch_dtype, params.num_heads, params.head_dim, params.state_dim, params.channels
     dev = xbc.get_device()
+    _same_device(params, dev)
     x_p, sx = _rows("xbc", xbc, t, n, ch, dev)
     d_p, sd = _rows("dt", dt, t, n, H, dev)
     z_p, sz = (None, 0) if z is None else _rows("z", z, t, n, H * P, dev)

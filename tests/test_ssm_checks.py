@@ -37,3 +37,53 @@ def test_decode_workspace_grows_with_the_batch(L):
         p = struct(num_heads=H, num_groups=G)
         sizes = [L.kda_ssm_decode_workspace_bytes(ctypes.byref(p), n) for n in range(0, 600)]
         assert sizes == sorted(sizes)
+
+
+# ---- the binding's own checks (CPU and meta tensors: nothing reaches the library) ----
+
+def ssm_params(device="cpu", **kw):
+    import torch
+    t = dict(conv_w=torch.zeros(768, 4, device=device), A_log=torch.zeros(4, device=device), dt_bias=torch.zeros(4, device=device))
+    t.update(kw)
+    return kda.make_ssm_params(**t, head_dim=64, state_dim=128, num_groups=2)
+
+
+def kda_params(**kw):
+    import torch
+    t = dict(conv_w=torch.zeros(3, 256, 4), A_log=torch.zeros(2), dt_bias=torch.zeros(256), norm_w=torch.zeros(128))
+    t.update(kw)
+    return kda.make_params(**t)
+
+
+@pytest.mark.parametrize("name, shape", [("conv_w", (768, 4)), ("conv_b", (768,)), ("A_log", (4,)), ("dt_bias", (4,)), ("D", (4,))])
+def test_ssm_parameters_lie_on_one_device(name, shape):
+    import torch
+    with pytest.raises(ValueError, match="one device"):
+        ssm_params(**{name: torch.zeros(shape, device="meta")})
+
+
+@pytest.mark.parametrize("name, shape", [("conv_w", (3, 256, 4)), ("A_log", (2,)), ("dt_bias", (256,)), ("norm_w", (128,))])
+def test_kda_parameters_lie_on_one_device(name, shape):
+    import torch
+    with pytest.raises(ValueError, match="one device"):
+        kda_params(**{name: torch.zeros(shape, device="meta")})
+
+
+def test_parameters_lie_on_the_device_of_the_call():
+    """Parameters of another device (their struct says so here) are refused before anything else
+    is looked at."""
+    import torch
+    bf = torch.bfloat16
+    p, k = ssm_params(), kda_params()
+    assert p.device == -1 and k.device == -1
+    p.device = k.device = 1
+    x, d = torch.zeros(5, 768, dtype=bf), torch.zeros(5, 4, dtype=bf)
+    rows = {n: torch.zeros(2, 5, 256, dtype=bf) for n in ("q", "k", "v", "z")}
+    b, par = torch.zeros(2, 5, 2, dtype=bf), torch.zeros(2, 5, dtype=torch.int32)
+    S, ring = torch.zeros(2, 2, 128, 128), torch.zeros(2, 3, 3, 256, dtype=bf)
+    for call in (lambda: kda.kda_ssm_prefill(p, x, d, [0, 5]),
+                 lambda: kda.kda_ssm_decode(p, x, d, torch.zeros(5, 4, 128, 64), torch.zeros(5, 3, 768, dtype=bf)),
+                 lambda: kda.kda_decode_tree(k, **rows, b=b, gout=rows["q"], parents=par, S=S, ring=ring),
+                 lambda: kda.kda_tree_commit(k, **rows, b=b, path=par, path_len=par[:, 0].contiguous(), S_in=S, ring_in=ring)):
+        with pytest.raises(ValueError, match="on cuda:1"):
+            call()
