@@ -391,8 +391,9 @@ def _workspace(t, like, nbytes, params, *sizes, stream=None):
     if t is None:
         import torch
         t = _empty(like, max(nbytes(params, *sizes), 256), torch.uint8, stream)
-    elif t.get_device() != like.get_device():
-        raise ValueError(f"workspace: expected a tensor on {like.device}, got {t.device}")
+    elif t.get_device() != like.get_device() or not t.is_contiguous():
+        raise ValueError(f"workspace: expected a contiguous tensor on {like.device}, got "
+                         f"{'' if t.is_contiguous() else 'a non-contiguous one '}on {t.device}")
     return t, t.data_ptr(), t.nbytes
 
 

@@ -87,3 +87,14 @@ def test_parameters_lie_on_the_device_of_the_call():
                  lambda: kda.kda_tree_commit(k, **rows, b=b, path=par, path_len=par[:, 0].contiguous(), S_in=S, ring_in=ring)):
         with pytest.raises(ValueError, match="on cuda:1"):
             call()
+
+
+def test_workspaces_are_dense():
+    """An expanded or strided workspace has more bytes by its shape than it owns."""
+    import torch
+    like = torch.zeros(1)
+    for ws in (torch.zeros(1, dtype=torch.uint8).expand(1 << 20), torch.zeros(512, dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError, match="workspace"):
+            kda._workspace(ws, like, None, None)
+    ws = torch.zeros(512, dtype=torch.uint8)
+    assert kda._workspace(ws, like, None, None) == (ws, ws.data_ptr(), 512)
