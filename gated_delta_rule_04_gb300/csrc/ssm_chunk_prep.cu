@@ -119,10 +119,12 @@ __global__ void __launch_bounds__(NT, 2) prep_kernel(const __grid_constant__ Chu
     if (warp == 0) {
         ptx::tmem_alloc(ptx::smem_u32(&tmem_slot), TMEM_COLS);
         ptx::tmem_relinquish();
+        // The next launch's CTAs may start now, and not before this block has its tensor memory: one
+        // that shared the SM would take all of it and then wait for this launch to end.  A block
+        // counts from its first thread that gets here on, so this warp says it, behind its
+        // allocation.  (Registers keep the two apart as well: 512 x 64 and 640 x 96 exceed an SM's.)
+        cudaTriggerProgrammaticLaunchCompletion();
     }
-    // The next launch's CTAs may start now.  Not before this block has its tensor memory: one
-    // that shares the SM takes all of it and then waits for this launch to end.
-    cudaTriggerProgrammaticLaunchCompletion();
     if (tid == 0) {
         ptx::mbar_init(bar_a, 1);
         ptx::fence_mbar_init();
