@@ -31,10 +31,10 @@ template <int N> struct Rec {
 inline size_t rec_bytes(int N) { return N == 64 ? Rec<64>::BYTES : Rec<128>::BYTES; }
 
 // Step record of one (chunk, head), fp32, with l_s = the log2 decay of token s:
-//   [0, 64)     lam_t: inclusive cumulative sum of max(l_s, -40), for differences
-//               between two tokens of the chunk.  The clamp keeps |lam| <= 2560, so
-//               that a difference of two is good to 2^-13; a decay of 2^-40 and one
-//               of less both vanish in the 11-bit operand they go to.
+//   [0, 64)     lam_t: inclusive cumulative sum of max(l_s, -48), for differences
+//               between two tokens of the chunk.  The clamp keeps |lam| <= 3072, so
+//               that a difference of two is good to 2^-12; a decay of 2^-48 and one
+//               of less both vanish in the fp16 operand they go to (below 2^16 before).
 //   [64, 128)   dt
 //   [128, 192)  2^(sum_{s > t} l_s) dt_t: the token's weight in the end state, from a
 //               suffix sum (a difference of long prefix sums would cost the fp32
@@ -45,7 +45,7 @@ inline size_t rec_bytes(int N) { return N == 64 ? Rec<64>::BYTES : Rec<128>::BYT
 //               addition to the state
 constexpr int STEP_FLOATS = 260;
 constexpr int ST_DT = 64, ST_W = 128, ST_EL = 192, ST_DEC = 256, ST_EDT = 257, ST_LOG = 258, ST_WSUM = 259;
-constexpr float LAM_MIN = -40.f;
+constexpr float LAM_MIN = -48.f;
 // The X group takes tokens t and t + 16 of a 32-token half as one packed pair.
 __host__ __device__ constexpr int w_at(int t) { return (t & 32) + 2 * (t & 15) + ((t >> 4) & 1); }
 
