@@ -362,7 +362,7 @@ kda_status kda_ssm_prefill(const kda_ssm_params* p, const void* xbc, int64_t xbc
 size_t kda_ssm_decode_workspace_bytes(const kda_ssm_params* p, int32_t n_sessions) {
     if (ssm::check_params(p) != KDA_OK || n_sessions <= 0) return 0;
     if (!ssm::decode_needs_workspace(n_sessions, p->num_heads, p->num_groups, p->head_dim, p->state_dim)) return 0;
-    return ssm::align_up((size_t)n_sessions * (size_t)channels(p) * sizeof(float));
+    return ssm::align_up((size_t)n_sessions * ((size_t)channels(p) * sizeof(float) + (size_t)p->num_heads * sizeof(float2)));
 }
 
 kda_status kda_ssm_decode(const kda_ssm_params* p, int32_t n_sessions, const void* xbc, int64_t xbc_stride,
@@ -381,9 +381,11 @@ kda_status kda_ssm_decode(const kda_ssm_params* p, int32_t n_sessions, const voi
     if (need > 0 && (workspace == nullptr || !aligned(workspace, WS_ALIGN) || workspace_bytes < need))
         return KDA_ERR_WORKSPACE;
     if ((int64_t)n_sessions * p->num_heads * 2 > (int64_t)INT32_MAX) return KDA_ERR_UNSUPPORTED;   // CTAs of the launch
+    float* const u = need > 0 ? static_cast<float*>(workspace) : nullptr;
+    float2* const step = u ? reinterpret_cast<float2*>(u + (size_t)n_sessions * channels(p)) : nullptr;   // (8-byte aligned)
     ssm::DecodeArgs a{xbc, dt, z, xbc_stride, dt_stride, z_stride, p->conv_w, p->conv_b, p->A_log, p->dt_bias, p->D,
-                      slots, S, ring, o, static_cast<float*>(workspace), n_sessions, n_slots, p->num_heads, p->num_groups,
-                      p->head_dim, p->state_dim};
+                      slots, S, ring, o, u, step, n_sessions, n_slots, p->num_heads, p->num_groups, p->head_dim,
+                      p->state_dim};
     return ssm::launch_decode(a, p->io_dtype == KDA_DTYPE_BF16, static_cast<cudaStream_t>(stream_)) == cudaSuccess
                ? KDA_OK : KDA_ERR_CUDA;
 }

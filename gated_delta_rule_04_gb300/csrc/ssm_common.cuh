@@ -48,6 +48,7 @@ struct DecodeArgs {
     void* ring;
     void* o;
     float* u;                // workspace [n][Cx] fp32: the conv's outputs (where decode_needs_workspace)
+    float2* step;            // workspace [n][H]: dt and the decay
     int32_t n, n_slots, H, G, P, N;
 };
 
@@ -64,6 +65,17 @@ __device__ __forceinline__ float rcp(float x) {
     float y;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// exp(x) of a token's decay, x <= 0, next to 1 rounded to nearest: expf's error there has one
+// sign, and a state that takes the factor at every token adds it up (3e-5 after 3000 tokens of
+// a decay of 1.7e-4 each, 1.3e-6 this way).  The Taylor polynomial of degree 4 leaves 5e-10 of
+// the distance from 1; below it a state forgets the errors.  (1 + expm1f(x): the same, fp32
+// prompts of 601 tokens x 8 heads 32.5 us, not 30.8.)
+__device__ __forceinline__ float decay(float x) {
+    if (x <= -1.f / 64) return expf(x);
+    const float p = fmaf(fmaf(fmaf(1.f / 24, x, 1.f / 6), x, 0.5f), x, 1.f);
+    return fmaf(p, x, 1.f);
 }
 
 // SiLU to fp32 rounding, 8 x 2^-24 at any x (zero below -87): these values reach the fp32

@@ -12,7 +12,7 @@
 //     stands between the last read of that ring and its write.  One launch of 5 us
 //     takes a single session's call from 19 to 14 us as the caller sees it;
 //   - otherwise conv_kernel takes every channel of every session through the conv
-//     into the workspace and rolls the ring, and state_kernel streams the states:
+//     into the workspace, with the heads' steps and decays, and rolls the ring, and state_kernel streams the states:
 //     persistent CTAs, the next state's 16 to 64 KiB prefetched into L2, the first
 //     one read while conv_kernel still runs.  256 sessions x 64 heads: 219 us
 //     fused, 192 us this way.
@@ -37,10 +37,16 @@ __global__ void __launch_bounds__(NT) conv_kernel(DecodeArgs g) {
     constexpr int V = 16 / sizeof(TI);   // channels per thread
     const int Cx = g.H * g.P + 2 * g.G * g.N;
     const int per = Cx / V;
-    const int64_t id = (int64_t)blockIdx.x * NT + threadIdx.x;
-    const int n = (int)(id / per), c = (int)(id % per) * V;
+    const int64_t id = (int64_t)blockIdx.x * NT + threadIdx.x, channels = (int64_t)g.n * per;
     cudaTriggerProgrammaticLaunchCompletion();   // the state kernel's first loads may start
-    if (n >= g.n) return;
+    if (id >= channels) {                        // the threads behind the channels: a session's head each
+        if (id >= channels + (int64_t)g.n * g.H) return;
+        const int n = (int)((id - channels) / g.H), h = (int)((id - channels) % g.H);
+        const float dt = softplus(to_f32(static_cast<const TI*>(g.dt)[(size_t)n * g.dt_stride + h]) + g.dt_bias[h]);
+        g.step[id - channels] = make_float2(dt, decay(-expf(g.A_log[h]) * dt));
+        return;
+    }
+    const int n = (int)(id / per), c = (int)(id % per) * V;
     const int slot = g.slots ? g.slots[n] : n;
     if (slot < 0 || slot >= g.n_slots) return;
     TI* ring = static_cast<TI*>(g.ring) + (size_t)slot * RING * Cx + c;
@@ -92,9 +98,9 @@ __global__ void __launch_bounds__(NT, PER_SM) state_kernel(DecodeArgs g) {
         for (int i = 0; i < RN; ++i) S[i] = __ldcs(Sg + i * NT);
         const float* u = g.u + (size_t)n * Cx;
         const int grp = h / (H / g.G);
-        const float dt = softplus(to_f32(static_cast<const TI*>(g.dt)[(size_t)n * g.dt_stride + h]) + g.dt_bias[h]);
-        const float a = expf(-expf(g.A_log[h]) * dt);
         cudaGridDependencySynchronize();   // u is there (at once from the second item on)
+        const float2 step = g.step[item];
+        const float dt = step.x, a = step.y;
         const float4 x4 = *reinterpret_cast<const float4*>(u + h * P + 4 * cq);
         const float4 xd = make_float4(dt * x4.x, dt * x4.y, dt * x4.z, dt * x4.w);
         const float* B = u + W + grp * N;
@@ -187,7 +193,7 @@ __global__ void __launch_bounds__(NT) fused_kernel(DecodeArgs g, int cs) {
     for (int x = 0; x < heads; ++x) {
         const int h = h0 + x * cs;
         const float dt = softplus(to_f32(static_cast<const TI*>(g.dt)[(size_t)n * g.dt_stride + h]) + g.dt_bias[h]);
-        const float a = expf(-expf(g.A_log[h]) * dt);
+        const float a = decay(-expf(g.A_log[h]) * dt);
         const float4 x4 = *reinterpret_cast<const float4*>(&sx[x][4 * cq]);
         const float4 xd = make_float4(dt * x4.x, dt * x4.y, dt * x4.z, dt * x4.w);
         float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -292,7 +298,7 @@ cudaError_t decode(const DecodeArgs& a, cudaStream_t s) {
         return a.N == 64 ? fused<TI, 128, 64>(a, cs, s) : fused<TI, 128, 128>(a, cs, s);
     }
     const int64_t per = (int64_t)(a.H * a.P + 2 * a.G * a.N) / (16 / sizeof(TI));
-    conv_kernel<TI><<<(unsigned)((a.n * per + NT - 1) / NT), NT, 0, s>>>(a);
+    conv_kernel<TI><<<(unsigned)((a.n * (per + a.H) + NT - 1) / NT), NT, 0, s>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     if (a.P == 64) return a.N == 64 ? state<TI, 64, 64>(a, s) : state<TI, 64, 128>(a, s);

@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(Roles<PS>::NT, 2) scan_kernel(const __grid_con
             const bool in = (uint32_t)b * TB + lane < L;
             const float dt = in ? softplus(to_f32(raw_dt) + dtb) : 0.f;
             sm.dt[b % 3][lane] = dt;
-            sm.a[b % 3][lane] = in ? expf(-eA * dt) : 1.f;
+            sm.a[b % 3][lane] = in ? decay(-eA * dt) : 1.f;
         }
     };
     // conv: items of four tokens of a channel, all of a thread's read before the first is

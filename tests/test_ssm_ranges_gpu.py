@@ -243,3 +243,26 @@ def test_silu_to_fp32_rounding(call):
         kda.kda_ssm_decode(p, dev(i["xbc"]).repeat(n, 1), dev(i["dt"]).repeat(n, 1), S, ring, z=dev(i["z"]).repeat(n, 1))
     err = ((S.cpu().double() - want) / want).abs().max()
     assert float(err) <= 26 * 2.0 ** -24
+
+
+@pytest.mark.parametrize("call", ["prefill f32", "prefill bf16", "prefill bf16 scan", "tokens f32", "tokens bf16",
+                                  "tokens f32 in two kernels"])
+def test_a_slow_decay_over_many_tokens(call):
+    """A decay of about 1.5e-4 a token: its distance from 1 is a few thousand steps of fp32, so a
+    rounding of one sign would show in a state that is multiplied by it 3000 times."""
+    H, P, N, T = 33 if "two" in call else 2, 64, 64, 3000
+    io = "f32" if "f32" in call else "bf16"
+    i = make_inputs(T, 1, H, P, N, 1, IO[io], 72)
+    i["A_log"][:] = -3.0
+    i["dt_bias"][:] = math.log(math.expm1(0.003))
+    _, wS, _ = mixer(i, [0, T])
+    if "prefill" in call:
+        p = params(i, io, "scan" if "scan" in call else "auto")
+        _, S, _ = kda.kda_ssm_prefill(p, dev(i["xbc"]), dev(i["dt"]), [0, T], S_in=dev(i["S"]), ring_in=dev(i["ring"]))
+    else:
+        p, S, ring, x, d = params(i, io), dev(i["S"]), dev(i["ring"]), dev(i["xbc"]), dev(i["dt"])
+        assert (kda.kda_ssm_decode_workspace_bytes(p, 1) > 0) == ("two" in call)
+        for t in range(T):
+            kda.kda_ssm_decode(p, x[t:t + 1], d[t:t + 1], S, ring)
+    for h in range(H):
+        close(f"S[{h}]", S[:, h], wS[:, h])
