@@ -249,15 +249,9 @@ __device__ __forceinline__ void walk(const ChunkArgs& a, const int unit, const i
         float* sSI = reinterpret_cast<float*>(sb + L::SI);
         const size_t state = (size_t)N * P;
 
-        // ---- a sequence without tokens: the state as it is, bit by bit (the scales below would
-        // lose values far from their row's largest)
-        if (nc == 0 && valid) {
-            const size_t at = ((size_t)seq * g.H + h) * state + p;
-            for (int x = (N / 2) * half; x < (N / 2) * (half + 1); ++x) g.S_out[at + (size_t)x * P] = g.S_in ? g.S_in[at + (size_t)x * P] : 0.f;
-        }
         // ---- starting state: the caller's for the first piece; later ones compose the
         // end states of the pieces before them (zero in the lite pass)
-        const float* start = piece == 0 && g.S_in ? g.S_in + ((size_t)seq * g.H + h) * state + p : nullptr;
+        const float* start = piece == 0 && nc > 0 && g.S_in ? g.S_in + ((size_t)seq * g.H + h) * state + p : nullptr;
         const float* loc = a.local + ((size_t)seq * a.np * g.H + h) * state + p;
         const float* ltot = a.ltot + (size_t)seq * a.np * g.H + h;
         constexpr int NH = N / 2;                            // state columns of this thread
@@ -475,6 +469,22 @@ __device__ __forceinline__ void walk(const ChunkArgs& a, const int unit, const i
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_Y));
         if constexpr (!LITE) {
             const int yt = tid - NX, ch = 32 * quarter + lane;
+            // a sequence without tokens: the unit's states as they are, bit by bit (X's scales would
+            // lose values far from their row's largest)
+            if (nc == 0) {
+                const size_t at = ((size_t)seq * g.H + h0) * N * P;
+                const uint4* src = g.S_in ? reinterpret_cast<const uint4*>(g.S_in + at) : nullptr;
+                uint4* dst = reinterpret_cast<uint4*>(g.S_out + at);
+#pragma unroll 1
+                for (int x0 = yt; x0 < nh * N * P / 4; x0 += 8 * NY) {
+                    uint4 v[8];                              // (in flight at once: dst may be src)
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) v[x] = src && x0 + x * NY < nh * N * P / 4 ? src[x0 + x * NY] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                    for (int x = 0; x < 8; ++x)
+                        if (x0 + x * NY < nh * N * P / 4) dst[x0 + x * NY] = v[x];
+                }
+            }
             const int rt = yt >> 3, rseg = yt & 7;           // row pass: rows rt and 32 + rt, values 32 q + 4 rseg ..
             const __nv_bfloat16* z = static_cast<const __nv_bfloat16*>(g.z);
             // this thread's rows of z and o, one chunk further each time; columns past the
