@@ -42,9 +42,9 @@
 // composed from the pieces before it when it begins.  The first piece needs no
 // start, so it is walked in full beside those.
 //
-// Measured: a full walk takes 2.4 us a chunk and a lite one 1.6 (64 tokens x 128
-// channels, N = 128), i.e. 32768 tokens x 96 heads of 64 in 0.57 ms.  No unit is
-// near its limit (issue slots 60 %, shared memory 44 %, tensor cores 29 %, L2 21 %);
+// Measured: a full walk takes 2.3 us a chunk and a lite one 1.6 (64 tokens x 128
+// channels, N = 128), i.e. 32768 tokens x 96 heads of 64 in 0.54 ms.  No unit is
+// near its limit (issue slots 62 %, shared memory 47 %, tensor cores 30 %, L2 22 %);
 // four chains of about that length run against each other: the X group's arithmetic
 // on 64 x 128 values (conv, SiLU, scaling, three fp16 packings) with the S row, M
 // behind its record, and MMAs -> readout -> next MMAs.  From 4.4 us it came there by

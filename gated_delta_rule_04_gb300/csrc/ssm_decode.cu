@@ -29,7 +29,7 @@ namespace {
 constexpr int NT = 256;
 // Resident CTAs of the state kernel.  256 sessions x 64 heads of 128 x 64: 244 us with
 // two, 204 with three, 192 with four, 211 with six.  (Heads of 128 x 128 hold twice the state a
-// thread and spill 180 bytes of it: 128 sessions x 64 heads 240 us, of the same bytes.)
+// thread and spill 176 bytes of it: 128 sessions x 64 heads 240 to 247 us, of the same bytes.)
 constexpr int PER_SM = 4;
 
 template <typename TI>
