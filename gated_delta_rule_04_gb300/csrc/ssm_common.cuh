@@ -85,7 +85,7 @@ __device__ __forceinline__ float decay(float x) {
 // us where this takes 31 (fp32 prompts, 601 tokens x 8 heads).
 __device__ __forceinline__ float silu(float x) {
     const float c = fminf(fmaxf(x, -88.f), 88.f), h = c * -1.44269504f;
-    float t = fmaf(h, -0.693359375f, -c);                    // ln(2) to 10 bits: h times it loses little
+    float t = fmaf(h, -0.693359375f, -c);                    // ln(2) in a few bits
     t = fmaf(h, 2.12194440e-4f, t);                          // and the rest of it
     const float e = ex2(h);
     return x * rcp(1.f + fmaf(e, t, e));

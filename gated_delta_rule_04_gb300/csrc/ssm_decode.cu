@@ -12,8 +12,8 @@
 //     stands between the last read of that ring and its write.  One launch of 5 us
 //     takes a single session's call from 19 to 14 us as the caller sees it;
 //   - otherwise conv_kernel takes every channel of every session through the conv
-//     into the workspace, with the heads' steps and decays, and rolls the ring, and state_kernel streams the states:
-//     persistent CTAs, the next state's 16 to 64 KiB prefetched into L2, the first
+//     into the workspace, with the heads' steps and decays, and rolls the ring, and
+//     state_kernel streams the states: persistent CTAs, the next state's 16 to 64 KiB prefetched into L2, the first
 //     one read while conv_kernel still runs.  256 sessions x 64 heads: 219 us
 //     fused, 192 us this way.
 #include <algorithm>

@@ -336,8 +336,8 @@ kda_status kda_tree_commit(const kda_params* p, int32_t n_sessions, int32_t n_no
 /*
  * Selective state space mixer: a recurrent mixer with one scalar decay per
  * head and token and no delta rule, whose cache has KDA's shape (a state and a
- * conv ring per session).  Per sequence, head h (of group h / (H/G)) and token t, with the conv channels
- * x (H*P) | B (G*N) | C (G*N) of one projection row xbc:
+ * conv ring per session).  Per sequence, head h (of group h / (H/G)) and token t,
+ * with the conv channels x (H*P) | B (G*N) | C (G*N) of one projection row xbc:
  *   1. u[c] = SiLU(conv_b[c] + sum_{j<4} conv_w[c][j] xbc[t-3+j][c]); inputs
  *      before the sequence start come from the conv ring (slot 0 oldest)
  *   2. dt = softplus(dt_raw[t][h] + dt_bias[h]),  a = exp(-exp(A_log[h]) dt)
