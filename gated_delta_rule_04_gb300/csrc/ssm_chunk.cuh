@@ -32,7 +32,7 @@ inline size_t rec_bytes(int N) { return N == 64 ? Rec<64>::BYTES : Rec<128>::BYT
 
 // Step record of one (chunk, head), fp32, with l_s = the log2 decay of token s:
 //   [0, 64)     lam_t: inclusive cumulative sum of max(l_s, -48), for differences
-//               between two tokens of the chunk.  The clamp keeps |lam| <= 3072, so
+//               between two tokens of the chunk.  The clamp keeps |lam| below 2^12, so
 //               that a difference of two is good to 2^-12; a decay of 2^-48 and one
 //               of less both vanish in the fp16 operand they go to (below 2^16 before).
 //   [64, 128)   dt
