@@ -9,7 +9,9 @@ memory and the stream.  The functions carry the C names:
     kda_prefill_host_scratch_bytes, kda_prefill_host, kda_decode, kda_decode_multi,
     kda_decode_tree, kda_tree_commit, kda_workspace_status, kda_status_str,
     kda_ssm_prefill_algo, kda_ssm_prefill_workspace_bytes, kda_ssm_prefill,
-    kda_ssm_decode_workspace_bytes, kda_ssm_decode
+    kda_ssm_decode_workspace_bytes, kda_ssm_decode,
+    kda_glr_prefill_workspace_bytes, kda_glr_prefill, kda_glr_backward_workspace_bytes, kda_glr_backward,
+    kda_glr_decode, kda_glr_commit, kda_draft_verify
 
 There is no fallback: if ``libkda.so`` is missing the import of this package
 still succeeds, but the first call raises ``KdaLibraryMissing``.
@@ -80,6 +82,16 @@ class kda_ssm_params(ctypes.Structure):
     ]
 
 
+class kda_glr_params(ctypes.Structure):
+    _fields_ = [
+        ("channels", ctypes.c_int32),
+        ("io_dtype", ctypes.c_int32),
+        ("A_log", _vp),
+        ("r_bias", _vp),
+        ("i_bias", _vp),
+    ]
+
+
 _lib = None
 
 
@@ -130,6 +142,20 @@ def lib():
         L.kda_ssm_decode_workspace_bytes.restype = sz
         L.kda_ssm_decode.argtypes = [SP, i32] + [_vp, i64] * 3 + [_vp, i32] + [_vp] * 3 + [_vp, sz, _vp]
         L.kda_ssm_decode.restype = ctypes.c_int
+        GP = ctypes.POINTER(kda_glr_params)
+        row, cu = [_vp, i64], [ctypes.POINTER(i64), i32, i64]
+        for f in (L.kda_glr_prefill_workspace_bytes, L.kda_glr_backward_workspace_bytes):
+            f.argtypes, f.restype = [GP, i32, i64], sz
+        L.kda_glr_prefill.argtypes = [GP] + row * 4 + cu + [_vp] * 4 + [_vp, sz, _vp]
+        L.kda_glr_prefill.restype = ctypes.c_int
+        L.kda_glr_backward.argtypes = [GP] + row * 4 + cu + [_vp] * 2 + row + [_vp] + row * 4 + [_vp] * 4 + [_vp, sz, _vp]
+        L.kda_glr_backward.restype = ctypes.c_int
+        L.kda_glr_decode.argtypes = [GP, i32, i32] + row * 4 + [_vp, i32] + [_vp] * 4
+        L.kda_glr_decode.restype = ctypes.c_int
+        L.kda_glr_commit.argtypes = [GP, i32, i32] + row * 3 + [_vp, _vp, i32, _vp, i32] + [_vp] * 3
+        L.kda_glr_commit.restype = ctypes.c_int
+        L.kda_draft_verify.argtypes = ([i32] * 4 + [_vp, i64, i64, _vp, i64] * 2 + [_vp] * 4 + [i32] + [_vp] * 4)
+        L.kda_draft_verify.restype = ctypes.c_int
         L.kda_workspace_status.argtypes = [_vp, _vp]
         L.kda_workspace_status.restype = ctypes.c_int
         L.kda_status_str.argtypes = [ctypes.c_int]
@@ -589,3 +615,226 @@ def kda_ssm_decode(params: SsmParams, xbc, dt, S, ring, z=None, slots=None, o=No
     _call("kda_ssm_decode", dev, lib().kda_ssm_decode, params.ref, n, x_p, sx, d_p, sd, z_p, sz, s_p, slots_n, S_p, r_p,
           o_p, w_p, w_bytes, stream=stream)
     return o
+
+
+# ---- gated linear recurrence ---------------------------------------------------------
+
+KDA_GLR_CHUNK = 64
+
+
+@dataclass
+class GlrParams:
+    """The gated linear recurrence's parameter tensors and the C struct that points at them."""
+
+    struct: kda_glr_params
+    tensors: tuple
+    channels: int
+    io_dtype: int
+    torch_dtype: object   # torch type of x, r, i, z, o and their gradients
+    device: int           # CUDA device of the parameter tensors (-1: none)
+    ref: object           # pointer to the struct
+
+
+def make_glr_params(A_log, *, r_bias=None, i_bias=None, io_dtype: str = "bf16") -> GlrParams:
+    """A_log, r_bias and i_bias (or None) [C]: fp32 CUDA tensors."""
+    import torch
+    C = int(A_log.shape[0]) if A_log.dim() == 1 else -1
+    for name, x in (("A_log", A_log), ("r_bias", r_bias), ("i_bias", i_bias)):
+        if x is not None and (x.dtype != torch.float32 or tuple(x.shape) != (C,)):
+            raise ValueError(f"{name}: expected float32 [C], got {x.dtype} {list(x.shape)}")
+    dt = {"f32": KDA_DTYPE_F32, "bf16": KDA_DTYPE_BF16}[io_dtype]
+    tensors = tuple(None if x is None else x.contiguous() for x in (A_log, r_bias, i_bias))
+    st = kda_glr_params(C, dt, *[_ptr(x) for x in tensors])
+    return GlrParams(st, tensors, C, dt, _io_torch(dt), _params_device(tensors), ctypes.byref(st))
+
+
+def kda_glr_prefill_workspace_bytes(params: GlrParams, n_seqs: int, total_tokens: int) -> int:
+    return int(lib().kda_glr_prefill_workspace_bytes(params.ref, int(n_seqs), int(total_tokens)))
+
+
+def kda_glr_backward_workspace_bytes(params: GlrParams, n_seqs: int, total_tokens: int) -> int:
+    return int(lib().kda_glr_backward_workspace_bytes(params.ref, int(n_seqs), int(total_tokens)))
+
+
+def kda_glr_prefill(params: GlrParams, x, r, i, cu_seqlens, z=None, S_in=None, S_out=None, states=None, o=None,
+                    workspace=None, stream=None):
+    """Varlen prefill of the gated linear recurrence.  x, r, i and z (or None:
+    no output gate) [T][C] may be column ranges of projection tensors;
+    ``cu_seqlens`` is a host sequence of n+1 ints.  S_in / S_out: [n][C] fp32;
+    ``states`` [ceil(T / 64)][C] fp32, if given, receives what kda_glr_backward
+    starts from.  Missing outputs and the workspace are allocated with torch.
+    Returns (o, S_out)."""
+    import torch
+    cu, n, T = _cu_array(cu_seqlens)
+    t, C, dev, f32 = params.torch_dtype, params.channels, x.get_device(), torch.float32
+    _same_device(params, dev)
+    rows = (*_rows("x", x, t, T, C, dev), *_rows("r", r, t, T, C, dev), *_rows("i", i, t, T, C, dev),
+            *((None, 0) if z is None else _rows("z", z, t, T, C, dev)))
+    S_p = None if S_in is None else _shaped("S_in", S_in, f32, (n, C), dev)
+    st_p = None if states is None else _shaped("states", states, f32, (-(-T // KDA_GLR_CHUNK), C), dev)
+    o, o_p = _output("o", o, x, (T, C), t, dev, stream)
+    S_out, So_p = _output("S_out", S_out, x, (n, C), f32, dev, stream)
+    _, w_p, w_bytes = _workspace(workspace, x, kda_glr_prefill_workspace_bytes, params, n, T, stream=stream)
+    _call("kda_glr_prefill", dev, lib().kda_glr_prefill, params.ref, *rows, cu, n, T, S_p, So_p, st_p, o_p, w_p, w_bytes,
+          stream=stream)
+    return o, S_out
+
+
+@dataclass
+class GlrGradients:
+    """What kda_glr_backward returns: dz is None without z."""
+
+    dx: object
+    dr: object
+    di: object
+    dz: object
+    dS_in: object
+    dA_log: object
+    dr_bias: object
+    di_bias: object
+
+
+def kda_glr_backward(params: GlrParams, x, r, i, cu_seqlens, states, do, z=None, S_in=None, dS_out=None, dx=None, dr=None,
+                     di=None, dz=None, dS_in=None, dA_log=None, dr_bias=None, di_bias=None, workspace=None,
+                     stream=None) -> GlrGradients:
+    """The gradients of kda_glr_prefill from its inputs, the ``states`` it left,
+    the gradient ``do`` [T][C] of o and ``dS_out`` [n][C] (or None: zero) of
+    S_out.  dx, dr, di, dz [T][C] may be column ranges of wider tensors; dS_in
+    [n][C], dA_log, dr_bias, di_bias [C] fp32.  Missing ones are allocated."""
+    import torch
+    cu, n, T = _cu_array(cu_seqlens)
+    t, C, dev, f32 = params.torch_dtype, params.channels, x.get_device(), torch.float32
+    _same_device(params, dev)
+    if z is None and dz is not None:
+        raise ValueError("dz: there is no z")
+
+    def ins(name, v):
+        return _rows(name, v, t, T, C, dev)
+
+    def out(name, v):
+        if v is None:
+            v = _empty(x, (T, C), t, stream)
+        return v, *_rows(name, v, t, T, C, dev)
+
+    def sums(name, v, shape):
+        return _output(name, v, x, shape, f32, dev, stream)
+
+    rows = (*ins("x", x), *ins("r", r), *ins("i", i), *((None, 0) if z is None else ins("z", z)))
+    S_p = None if S_in is None else _shaped("S_in", S_in, f32, (n, C), dev)
+    st_p = _shaped("states", states, f32, (-(-T // KDA_GLR_CHUNK), C), dev)
+    dS_p = None if dS_out is None else _shaped("dS_out", dS_out, f32, (n, C), dev)
+    do_p = ins("do", do)
+    (dx, *dx_p), (dr, *dr_p), (di, *di_p) = out("dx", dx), out("dr", dr), out("di", di)
+    dz, *dz_p = (None, None, 0) if z is None else out("dz", dz)
+    dS_in, dSi_p = sums("dS_in", dS_in, (n, C))
+    (dA_log, dA_p), (dr_bias, drb_p), (di_bias, dib_p) = (sums("dA_log", dA_log, (C,)), sums("dr_bias", dr_bias, (C,)),
+                                                          sums("di_bias", di_bias, (C,)))
+    _, w_p, w_bytes = _workspace(workspace, x, kda_glr_backward_workspace_bytes, params, n, T, stream=stream)
+    _call("kda_glr_backward", dev, lib().kda_glr_backward, params.ref, *rows, cu, n, T, S_p, st_p, *do_p, dS_p, *dx_p, *dr_p,
+          *di_p, *dz_p, dSi_p, dA_p, drb_p, dib_p, w_p, w_bytes, stream=stream)
+    return GlrGradients(dx, dr, di, dz, dS_in, dA_log, dr_bias, di_bias)
+
+
+def _run_rows(name, t, dtype, n, R, width, dev):
+    """(address, row stride in elements) of a [n][R][width] tensor whose n * R rows lie evenly apart."""
+    if t.dtype is not dtype or t.shape != (n, R, width) or t.get_device() != dev or dev < 0:
+        raise ValueError(f"{name}: expected a tensor {dtype} {[n, R, width]} on CUDA device {max(dev, 0)}, got {t.dtype} "
+                         f"{list(t.shape)} on {t.device}")
+    if t.is_contiguous():
+        return t.data_ptr(), 0
+    session, stride, inner = t.stride()
+    if R == 1:
+        stride = session
+    if width > 1 and inner != 1:
+        raise ValueError(f"{name}: the elements of a row have to lie side by side")
+    if n > 1 and R > 1 and session != R * stride:
+        raise ValueError(f"{name}: the rows have to lie evenly apart (strides {session} and {stride}, {R} rows a session)")
+    if n * R > 1 and stride < width:
+        raise ValueError(f"{name}: rows overlap (stride {stride} < {width})")
+    return t.data_ptr(), stride if n * R > 1 else 0
+
+
+def kda_glr_decode(params: GlrParams, x, r, i, S, z=None, slots=None, S_out=None, o=None, keep_state=False, stream=None):
+    """1 to 64 consecutive tokens per session: x, r, i, z [n][n_tokens][C], whose
+    rows may be column ranges of projection rows.  The pool S [n_slots][C] is
+    updated in place, or S_out is written instead; with ``keep_state`` no state
+    is written (a verify round, whose accepted tokens kda_glr_commit applies).
+    ``slots`` (int32 [n]) maps sessions to pool slots.  Returns o [n][n_tokens][C]."""
+    import torch
+    if x.dim() != 3:
+        raise ValueError(f"x: expected [n][n_tokens][C], got {list(x.shape)}")
+    n, R, _ = x.shape
+    t, C, dev = params.torch_dtype, params.channels, x.get_device()
+    _same_device(params, dev)
+    if keep_state and S_out is not None:
+        raise ValueError("S_out: no state is written with keep_state")
+    S_p, slots_n = _pool("S", S, torch.float32, (C,), dev)
+    So_p = None if keep_state else S_p if S_out is None else _shaped("S_out", S_out, torch.float32, (slots_n, C), dev)
+    rows = (*_run_rows("x", x, t, n, R, C, dev), *_run_rows("r", r, t, n, R, C, dev), *_run_rows("i", i, t, n, R, C, dev),
+            *((None, 0) if z is None else _run_rows("z", z, t, n, R, C, dev)))
+    s_p = None if slots is None else _shaped("slots", slots, torch.int32, (n,), dev)
+    o, o_p = _output("o", o, x, (n, R, C), t, dev, stream)
+    _call("kda_glr_decode", dev, lib().kda_glr_decode, params.ref, n, R, *rows, s_p, slots_n, S_p, So_p, o_p, stream=stream)
+    return o
+
+
+def kda_glr_commit(params: GlrParams, x, r, i, path, path_len, S_in, S_out=None, slots=None, stream=None):
+    """Advances each session's state by its accepted path: ``path`` int32
+    [n][max_len] node indices in order, ``path_len`` int32 [n] (those of
+    kda_draft_verify).  x, r, i are the round's rows, as for kda_glr_decode.
+    S_out defaults to the input pool (in place).  Returns S_out."""
+    import torch
+    if x.dim() != 3 or path.dim() != 2:
+        raise ValueError(f"x, path: expected [n][n_nodes][C] and [n][max_len], got {list(x.shape)}, {list(path.shape)}")
+    n, R, _ = x.shape
+    t, C, m, dev = params.torch_dtype, params.channels, path.shape[1], x.get_device()
+    _same_device(params, dev)
+    S_out = S_in if S_out is None else S_out
+    S_p, slots_n = _pool("S_in", S_in, torch.float32, (C,), dev)
+    _call("kda_glr_commit", dev, lib().kda_glr_commit, params.ref, n, R, *_run_rows("x", x, t, n, R, C, dev),
+          *_run_rows("r", r, t, n, R, C, dev), *_run_rows("i", i, t, n, R, C, dev), _shaped("path", path, torch.int32, (n, m), dev),
+          _shaped("path_len", path_len, torch.int32, (n,), dev), m,
+          None if slots is None else _shaped("slots", slots, torch.int32, (n,), dev), slots_n, S_p,
+          _shaped("S_out", S_out, torch.float32, (slots_n, C), dev), stream=stream)
+    return S_out
+
+
+# ---- verification of drafts ------------------------------------------------------------
+
+def _probabilities(name, t, dtype, shape, dev):
+    """(address, strides but the last) of a tensor of probability rows."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or dev < 0:
+        raise ValueError(f"{name}: expected a tensor {dtype} {list(shape)} on CUDA device {max(dev, 0)}, got {t.dtype} "
+                         f"{list(t.shape)} on {t.device}")
+    *strides, inner = t.stride()
+    if shape[-1] > 1 and inner != 1:
+        raise ValueError(f"{name}: the elements of a row have to lie side by side")
+    return t.data_ptr(), *strides
+
+
+def kda_draft_verify(p, tokens, parents, u, u_next, q=None, p_last=None, q_last=None, max_len=None, path=None, path_len=None,
+                     next_token=None, stream=None):
+    """Verifies a round's drafted tokens against the target's probabilities.
+    p [n][n_nodes][V]: of the token after each node, fp32 or bf16; p_last [n][V]:
+    after the session's last token, or None where the first node of parent -1
+    is a token already chosen; q, q_last: those that the drafts were drawn from,
+    or None for chosen drafts.  tokens, parents: int32 [n][n_nodes]; u [n][n_nodes] and u_next
+    [n]: fp32 in [0, 1).  Returns (path [n][max_len], path_len [n], next_token
+    [n]), int32; max_len defaults to n_nodes."""
+    import torch
+    if p.dim() != 3 or p.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"p: expected float32 or bfloat16 [n][n_nodes][V], got {p.dtype} {list(p.shape)}")
+    n, R, V = p.shape
+    t, dev, i32 = p.dtype, p.get_device(), torch.int32
+    m = path.shape[1] if max_len is None and path is not None and path.dim() == 2 else R if max_len is None else int(max_len)
+    args = (KDA_DTYPE_F32 if t is torch.float32 else KDA_DTYPE_BF16, n, R, V, *_probabilities("p", p, t, (n, R, V), dev),
+            *((None, 0) if p_last is None else _probabilities("p_last", p_last, t, (n, V), dev)),
+            *((None, 0, 0) if q is None else _probabilities("q", q, t, (n, R, V), dev)),
+            *((None, 0) if q_last is None else _probabilities("q_last", q_last, t, (n, V), dev)),
+            _shaped("tokens", tokens, i32, (n, R), dev), _shaped("parents", parents, i32, (n, R), dev),
+            _shaped("u", u, torch.float32, (n, R), dev), _shaped("u_next", u_next, torch.float32, (n,), dev), m)
+    path, path_p = _output("path", path, p, (n, max(m, 0)), i32, dev, stream)
+    path_len, len_p = _output("path_len", path_len, p, (n,), i32, dev, stream)
+    next_token, next_p = _output("next_token", next_token, p, (n,), i32, dev, stream)
+    _call("kda_draft_verify", dev, lib().kda_draft_verify, *args, path_p, len_p, next_p, stream=stream)
+    return path, path_len, next_token

@@ -432,6 +432,173 @@ kda_status kda_ssm_decode(const kda_ssm_params* p, int32_t n_sessions, const voi
                           void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * Gated linear recurrence: a recurrent mixer whose state is one value per
+ * channel, with its backward pass.  Per sequence, channel c and token t:
+ *   1. w = sigmoid(r[t][c] + r_bias[c]),  v = sigmoid(i[t][c] + i_bias[c])
+ *   2. la = -exp(A_log[c]) w,  a = exp(la)
+ *   3. h_t = a h_{t-1} + sqrt(1 - a^2) v x[t][c]     (h: C fp32 per sequence)
+ *   4. o = h_t SiLU(z[t][c])                         (z NULL: o = h_t)
+ * x, the gate logits r and i and the output gate z are column ranges of the
+ * layer's projections.  An interface addition of this library; the conventions
+ * above hold, but for the alignment: tensors of this mixer need that of their
+ * elements only.  Rows that start on 16 bytes (address and stride) are read
+ * and written 16 bytes at a time, others an element at a time.
+ */
+typedef struct {
+    int32_t channels;    /* C >= 1 */
+    int32_t io_dtype;    /* kda_dtype of x, r, i, z, o and their gradients */
+    const float* A_log;  /* device [C] fp32 */
+    const float* r_bias; /* device [C] fp32 or NULL (none) */
+    const float* i_bias; /* device [C] fp32 or NULL (none) */
+} kda_glr_params;
+
+/* Tokens between two of the states that kda_glr_backward starts from. */
+#define KDA_GLR_CHUNK 64
+
+/* Bytes of device workspace kda_glr_prefill and kda_glr_backward need for any
+ * split of total_tokens into n_seqs sequences (0 for arguments they would
+ * reject, and where n_seqs is 0).  Neither falls with more sequences or tokens. */
+size_t kda_glr_prefill_workspace_bytes(const kda_glr_params* p, int32_t n_seqs, int64_t total_tokens);
+size_t kda_glr_backward_workspace_bytes(const kda_glr_params* p, int32_t n_seqs, int64_t total_tokens);
+
+/*
+ * Stateful varlen prefill of the gated linear recurrence over n_seqs packed
+ * sequences.
+ *   x, r, i, z   : device io_dtype, row t at base + t * stride elements, C used;
+ *                  strides (below 2^31) as for kda_ssm_prefill, 0 is packed rows
+ *   cu_seqlens_host, n_seqs, total_tokens : as for kda_prefill
+ *   S_in, S_out  : device [n_seqs][C] fp32; S_in NULL is zero; they may be the
+ *                  same buffer
+ *   states       : device [ceil(total_tokens / KDA_GLR_CHUNK)][C] fp32 or NULL.
+ *                  Row j receives the state that token KDA_GLR_CHUNK * j of the
+ *                  packed batch finds (of a sequence's first token: S_in or
+ *                  zero), for kda_glr_backward
+ *   o            : device [total_tokens][C] io_dtype, packed
+ *   workspace    : device, >= kda_glr_prefill_workspace_bytes(), 256-byte aligned;
+ *                  its error word is read with kda_workspace_status
+ * Zero-length sequences copy their state through.  Gates, states and sums are
+ * fp32.  A NaN or an infinity stays in its sequence and channel, from its token on.
+ */
+kda_status kda_glr_prefill(const kda_glr_params* p, const void* x, int64_t x_stride, const void* r, int64_t r_stride,
+                           const void* i, int64_t i_stride, const void* z, int64_t z_stride,
+                           const int64_t* cu_seqlens_host, int32_t n_seqs, int64_t total_tokens,
+                           const float* S_in, float* S_out, float* states, void* o,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Gradients of kda_glr_prefill, from the same inputs, the states it left and
+ * the gradients of its outputs.
+ *   x, r, i, z, cu_seqlens_host, S_in, states : as given to and left by the call
+ *   d_o          : device io_dtype, row t at d_o + t * do_stride
+ *   dS_out       : device [n_seqs][C] fp32, gradient of S_out, or NULL (zero)
+ *   dx, dr, di, dz : device io_dtype, rows strided as the inputs' (so that dr and
+ *                  di can be the halves of one row); dz is written where z is
+ *                  given, and both are NULL otherwise
+ *   dS_in        : device [n_seqs][C] fp32 or NULL (skipped); may be dS_out
+ *   dA_log, dr_bias, di_bias : device [C] fp32, sums over all tokens; the last two
+ *                  may be NULL (skipped)
+ *   workspace    : as for the prefill, of kda_glr_backward_workspace_bytes()
+ * The gradients may not overlap one another or the inputs; each is overwritten.
+ */
+kda_status kda_glr_backward(const kda_glr_params* p, const void* x, int64_t x_stride, const void* r, int64_t r_stride,
+                            const void* i, int64_t i_stride, const void* z, int64_t z_stride,
+                            const int64_t* cu_seqlens_host, int32_t n_seqs, int64_t total_tokens,
+                            const float* S_in, const float* states, const void* d_o, int64_t do_stride,
+                            const float* dS_out, void* dx, int64_t dx_stride, void* dr, int64_t dr_stride,
+                            void* di, int64_t di_stride, void* dz, int64_t dz_stride, float* dS_in,
+                            float* dA_log, float* dr_bias, float* di_bias,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * 1 to KDA_DECODE_MAX_TOKENS consecutive tokens per session over a state pool.
+ *   x, r, i, z   : device io_dtype, row (session, token) n_tokens * session + token
+ *                  at base + row * stride (0: packed); z may be NULL
+ *   slots, n_slots : as for kda_decode_multi (distinct where S_out is written); a
+ *                  session with a slot outside [0, n_slots) is skipped, its state
+ *                  and output rows left untouched
+ *   S_in, S_out  : device pools [n_slots][C] fp32; they may alias.  S_out NULL
+ *                  keeps the states: the rows of a verify round, whose accepted
+ *                  tokens kda_glr_commit applies
+ *   o            : device [n_sessions][n_tokens][C] io_dtype, packed
+ */
+kda_status kda_glr_decode(const kda_glr_params* p, int32_t n_sessions, int32_t n_tokens, const void* x, int64_t x_stride,
+                          const void* r, int64_t r_stride, const void* i, int64_t i_stride, const void* z,
+                          int64_t z_stride, const int32_t* slots, int32_t n_slots, const float* S_in, float* S_out,
+                          void* o, void* stream);
+
+/*
+ * Advances each session's state by the accepted tokens of a round: as
+ * kda_tree_commit, for this mixer.
+ *   x, r, i      : the round's rows, as for kda_glr_decode with n_nodes tokens
+ *                  (1 to KDA_TREE_MAX_NODES)
+ *   path, path_len, max_len, slots, n_slots, S_in, S_out : as for kda_tree_commit;
+ *                  a session with a slot, path_len or accepted node out of range
+ *                  is skipped
+ */
+kda_status kda_glr_commit(const kda_glr_params* p, int32_t n_sessions, int32_t n_nodes, const void* x, int64_t x_stride,
+                          const void* r, int64_t r_stride, const void* i, int64_t i_stride, const int32_t* path,
+                          const int32_t* path_len, int32_t max_len, const int32_t* slots, int32_t n_slots,
+                          const float* S_in, float* S_out, void* stream);
+
+/*
+ * Verification of a round's drafted tokens: which path through each session's
+ * nodes is accepted, and the token that follows it, so that the tokens of a
+ * session are distributed as if drawn one by one from the target's
+ * probabilities.  The random numbers are inputs.  path and path_len are those
+ * that kda_tree_commit and kda_glr_commit take.
+ *
+ * Nodes and parents are as for kda_decode_tree (a straight draft: parents -1, 0,
+ * 1, ...).  Row r of `p` holds the target's probabilities of the token after node
+ * r, p_last those after the session's last token, for the nodes of parent -1.
+ * With p_last NULL the node that follows the last token is one that is already
+ * chosen: the first of parent -1 is accepted untested (the common round, whose
+ * first row is the last sampled token itself).  Rows of q and q_last hold the
+ * probabilities that the children of a node were drawn from, one after the
+ * other and each from the whole row; q NULL is a draft of chosen tokens, e.g. the
+ * drafter's best ones: q is then one at the child's own token.
+ *
+ * From the last token (coefficient c = 0, mass T = 1) the children of the current
+ * node are tested in the order of their index.  With W(y) = max(p(y) - c q(y), 0)
+ * child r with token y is accepted if W(y) > 0 and u[r] T q(y) < W(y); it is then the
+ * current node, with c = 0 and T = 1.  Otherwise c <- c + T and T <- sum over the
+ * vocabulary of W with that c.  (Each refusal takes T q off what the target
+ * still has to give, down to zero, and q >= 0, so one coefficient holds for any number of
+ * refused siblings.)  For chosen tokens: accepted if u[r] T < W(y), where W is p without
+ * the refused siblings' tokens, otherwise T <- T - W(y).  Where no child is accepted,
+ * or the path holds max_len nodes, the walk ends, and the token that follows is the smallest y with
+ * W(y) > 0 and W(0) + ... + W(y) > u_next (W(0) + ... + W(V - 1)); if rounding leaves none, the
+ * last with W(y) > 0.  If W is zero everywhere it is p itself; if that is, the token is -1.
+ * Sums and tests are as good as in 64 bits.
+ *
+ *   dtype        : kda_dtype of p, p_last, q and q_last
+ *   n_nodes      : 1 to KDA_TREE_MAX_NODES
+ *   vocab        : V, 1 to 2^30
+ *   p, q         : device; the row of node r of session s at
+ *                  base + s * session_stride + r * row_stride elements.  Values that are
+ *                  NaN, infinite or not above zero count as zero.  Rows of nodes that are not
+ *                  reached, and rows of q where no child was refused, are not read, but for their
+ *                  entries at the children's tokens
+ *   p_last, q_last : device, the row of session s at base + s * stride.  q_last is
+ *                  given if and only if p_last and q are
+ *   tokens       : device int32 [n_sessions][n_nodes].  A node whose token is outside
+ *                  [0, V) is left out, like one whose parent is out of range
+ *   parents      : device int32 [n_sessions][n_nodes]
+ *   u            : device fp32 [n_sessions][n_nodes], uniform in [0, 1), one per node
+ *   u_next       : device fp32 [n_sessions], uniform in [0, 1)
+ *   path         : device int32 [n_sessions][max_len], the accepted nodes, -1 behind them;
+ *                  1 <= max_len <= KDA_TREE_MAX_NODES
+ *   path_len, next_token : device int32 [n_sessions]
+ * All pointers need the alignment of their elements.
+ */
+kda_status kda_draft_verify(int32_t dtype, int32_t n_sessions, int32_t n_nodes, int32_t vocab,
+                            const void* p, int64_t p_session_stride, int64_t p_row_stride,
+                            const void* p_last, int64_t p_last_stride,
+                            const void* q, int64_t q_session_stride, int64_t q_row_stride,
+                            const void* q_last, int64_t q_last_stride,
+                            const int32_t* tokens, const int32_t* parents, const float* u, const float* u_next,
+                            int32_t max_len, int32_t* path, int32_t* path_len, int32_t* next_token, void* stream);
+
+/*
  * kda_prefill without a workspace, for callers that cannot allocate device
  * memory when they run: a plugin inside an engine that owns every byte of
  * device memory, or a serving loop that must not call cudaMalloc/cudaFree
