@@ -1,7 +1,8 @@
 // C ABI of the gated linear recurrence: host-side checks, workspace layout and
 // the launch sequence of each entry point.  Every check happens before anything
 // is enqueued.
-#include <algorithm>
+#include <new>
+#include <vector>
 
 #include "glr_common.cuh"
 
@@ -40,27 +41,88 @@ kda_status check_batch(const int64_t* cu, int32_t n_seqs, int64_t total_tokens) 
     return total_tokens > (int64_t)INT32_MAX ? KDA_ERR_UNSUPPORTED : KDA_OK;
 }
 
-// Workspace: error word | cu_seqlens | partial sums (backward pass).
+// Workspace: error word | ticket | flags | token offsets, rows and tile table of the sequences |
+// the tiles' maps and values | partial sums (backward pass).
 struct Layout {
-    size_t cu = 0, part = 0, total = 0;
+    size_t flags = 0, cu = 0, id = 0, tile = 0, agg = 0, pre = 0, part = 0, total = 0;
+    int64_t tiles_t = 0, tiles_c = 0;
 };
-Layout layout(const kda_glr_params* p, int32_t n_seqs, int64_t, bool backward) {
+Layout layout(const kda_glr_params* p, int32_t n_seqs, int64_t total_tokens, bool backward) {
     Layout L;
-    size_t off = WS_ALIGN;
+    L.tiles_t = (total_tokens + CHUNK - 1) / CHUNK;
+    L.tiles_c = (p->channels + TILE_C - 1) / TILE_C;
+    const size_t tiles = (size_t)L.tiles_t * L.tiles_c;
+    size_t off = 2 * WS_ALIGN;
     auto take = [&](size_t bytes) { const size_t at = off; off = align_up(off + bytes); return at; };
+    L.flags = take(sizeof(int32_t) * tiles);
     L.cu = take(sizeof(int64_t) * ((size_t)n_seqs + 1));
-    if (backward) L.part = take(sizeof(float) * 3 * (size_t)n_seqs * p->channels);
+    L.id = take(sizeof(int32_t) * (size_t)n_seqs);
+    L.tile = take(sizeof(int32_t) * (size_t)L.tiles_t);
+    L.agg = take(sizeof(float) * 2 * TILE_C * tiles);
+    L.pre = take(sizeof(float) * TILE_C * tiles);
+    if (backward) L.part = take(sizeof(float) * 3 * (size_t)L.tiles_t * p->channels);
     L.total = off;
     return L;
 }
 
-// The token offsets, in the arguments or built on the device.
-cudaError_t offsets(const int64_t* cu, int32_t n_seqs, int64_t* d_cu, Offsets* f, cudaStream_t s) {
-    f->n = n_seqs;
-    f->d_cu = d_cu;
-    if (n_seqs > INLINE_SEQS) return build_meta(cu, nullptr, n_seqs, 0, d_cu, nullptr, nullptr, nullptr, s);
-    for (int32_t i = 0; i <= n_seqs; ++i) f->cu[i] = (int32_t)cu[i];
-    return cudaSuccess;
+// What the two walks share: the sequences with tokens, the workspace's parts, a cleared error
+// word, ticket and flags.
+cudaError_t prepare(const kda_glr_params* p, const int64_t* cu, int32_t n_seqs, unsigned char* ws, const Layout& L,
+                    ScanArgs* a, cudaStream_t s) {
+    a->status = reinterpret_cast<int32_t*>(ws);
+    a->ticket = reinterpret_cast<uint32_t*>(ws + WS_ALIGN);
+    a->flags = reinterpret_cast<int32_t*>(ws + L.flags);
+    a->agg = reinterpret_cast<float*>(ws + L.agg);
+    a->pre = reinterpret_cast<float*>(ws + L.pre);
+    a->part = reinterpret_cast<float*>(ws + L.part);
+    a->tiles_t = (int32_t)L.tiles_t;
+    a->tiles_c = (int32_t)L.tiles_c;
+    cudaError_t e = cudaMemsetAsync(ws, 0, L.flags + sizeof(int32_t) * (size_t)(L.tiles_t * L.tiles_c), s);
+    if (e != cudaSuccess || L.tiles_t == 0) return e;
+    Sequences& f = a->f;
+    f.d_cu = reinterpret_cast<int64_t*>(ws + L.cu);
+    f.d_id = reinterpret_cast<int32_t*>(ws + L.id);
+    f.d_tile = reinterpret_cast<int32_t*>(ws + L.tile);
+    f.n = 0;
+    for (int32_t i = 0; i < n_seqs; ++i) f.n += cu[i + 1] > cu[i];
+    if (f.n <= INLINE_SEQS) {
+        int k = 0;
+        for (int32_t i = 0; i < n_seqs; ++i)
+            if (cu[i + 1] > cu[i]) {
+                f.cu[k] = (int32_t)cu[i];
+                f.id[k++] = i;
+            }
+        f.cu[k] = (int32_t)cu[n_seqs];
+        return cudaSuccess;
+    }
+    std::vector<int64_t> start;
+    std::vector<int32_t> id;
+    try {
+        start.reserve((size_t)f.n + 1);
+        id.reserve((size_t)f.n);
+        for (int32_t i = 0; i < n_seqs; ++i)
+            if (cu[i + 1] > cu[i]) {
+                start.push_back(cu[i]);
+                id.push_back(i);
+            }
+        start.push_back(cu[n_seqs]);
+    } catch (const std::bad_alloc&) {
+        return cudaErrorMemoryAllocation;
+    }
+    e = build_meta(start.data(), id.data(), f.n, 0, const_cast<int64_t*>(f.d_cu), nullptr, const_cast<int32_t*>(f.d_id),
+                   nullptr, s);
+    return e != cudaSuccess ? e : launch_tile_table(f.d_cu, f.n, const_cast<int32_t*>(f.d_tile), a->tiles_t, s);
+}
+
+// Copies the state of sequences without tokens, if there are any (all states: the walk then
+// writes those of the others).
+cudaError_t copy_states(const kda_glr_params* p, const int64_t* cu, int32_t n_seqs, const float* from, float* to,
+                        cudaStream_t s) {
+    bool any = false;
+    for (int32_t i = 0; i < n_seqs; ++i) any |= cu[i + 1] == cu[i];
+    if (!any || from == to) return cudaSuccess;
+    const size_t bytes = sizeof(float) * (size_t)n_seqs * p->channels;
+    return from ? cudaMemcpyAsync(to, from, bytes, cudaMemcpyDeviceToDevice, s) : cudaMemsetAsync(to, 0, bytes, s);
 }
 
 }  // namespace
@@ -94,8 +156,8 @@ kda_status kda_glr_prefill(const kda_glr_params* p, const void* x, int64_t x_str
         !glr::rows(p, z, false, &z_stride) || (any && !o) || !aligned(o, esize(p)))
         return KDA_ERR_INVALID_ARG;
     if (!S_out || !aligned(S_out, 4) || !aligned(S_in, 4) || !aligned(states, 4)) return KDA_ERR_INVALID_ARG;
-    if ((int64_t)n_seqs * ((p->channels + 127) / 128) > (int64_t)INT32_MAX) return KDA_ERR_UNSUPPORTED;
     const Layout L = glr::layout(p, n_seqs, total_tokens, false);
+    if (L.tiles_t * L.tiles_c > (int64_t)INT32_MAX / 2) return KDA_ERR_UNSUPPORTED;
     if (workspace == nullptr || !aligned(workspace, WS_ALIGN) || workspace_bytes < L.total) return KDA_ERR_WORKSPACE;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     unsigned char* ws = static_cast<unsigned char*>(workspace);
@@ -105,9 +167,10 @@ kda_status kda_glr_prefill(const kda_glr_params* p, const void* x, int64_t x_str
     a.A_log = p->A_log; a.r_bias = p->r_bias; a.i_bias = p->i_bias;
     a.S_in = S_in; a.S_out = S_out; a.states = states; a.o = o;
     a.T = total_tokens; a.C = p->channels;
-    if (cudaMemsetAsync(ws, 0, WS_ALIGN, s) != cudaSuccess ||
-        offsets(cu, n_seqs, reinterpret_cast<int64_t*>(ws + L.cu), &a.f, s) != cudaSuccess)
+    if (glr::prepare(p, cu, n_seqs, ws, L, &a, s) != cudaSuccess ||
+        copy_states(p, cu, n_seqs, S_in, S_out, s) != cudaSuccess)
         return KDA_ERR_CUDA;
+    if (!any) return KDA_OK;
     return glr::launch_scan(a, p->io_dtype == KDA_DTYPE_BF16, s) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
@@ -126,6 +189,7 @@ kda_status kda_glr_backward(const kda_glr_params* p, const void* x, int64_t x_st
         !glr::rows(p, dr, any, &dr_stride) || !glr::rows(p, di, any, &di_stride) ||
         !glr::rows(p, dz, any && z != nullptr, &dz_stride) || (dz != nullptr && z == nullptr) || (any && !states))
         return KDA_ERR_INVALID_ARG;
+    if (dS_in != nullptr && dS_in == dS_out) return KDA_ERR_INVALID_ARG;   // (a tile may write the one before it reads the other)
     if (!dA_log || !aligned(S_in, 4) || !aligned(states, 4) || !aligned(dS_out, 4) || !aligned(dS_in, 4) ||
         !aligned(dA_log, 4) || !aligned(dr_bias, 4) || !aligned(di_bias, 4))
         return KDA_ERR_INVALID_ARG;
@@ -135,8 +199,8 @@ kda_status kda_glr_backward(const kda_glr_params* p, const void* x, int64_t x_st
                 return KDA_ERR_CUDA;
         return KDA_OK;
     }
-    if ((int64_t)n_seqs * ((p->channels + 127) / 128) > (int64_t)INT32_MAX) return KDA_ERR_UNSUPPORTED;
     const Layout L = glr::layout(p, n_seqs, total_tokens, true);
+    if (L.tiles_t * L.tiles_c > (int64_t)INT32_MAX / 2) return KDA_ERR_UNSUPPORTED;
     if (workspace == nullptr || !aligned(workspace, WS_ALIGN) || workspace_bytes < L.total) return KDA_ERR_WORKSPACE;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     unsigned char* ws = static_cast<unsigned char*>(workspace);
@@ -149,10 +213,9 @@ kda_status kda_glr_backward(const kda_glr_params* p, const void* x, int64_t x_st
     a.dx = dx; a.dr = dr; a.di = di; a.dz = dz;
     a.dx_s = dx_stride; a.dr_s = dr_stride; a.di_s = di_stride; a.dz_s = dz_stride;
     a.dS_in = dS_in; a.dA_log = dA_log; a.dr_bias = dr_bias; a.di_bias = di_bias;
-    a.part = reinterpret_cast<float*>(ws + L.part);
     a.T = total_tokens; a.C = p->channels;
-    if (cudaMemsetAsync(ws, 0, WS_ALIGN, s) != cudaSuccess ||
-        offsets(cu, n_seqs, reinterpret_cast<int64_t*>(ws + L.cu), &a.f, s) != cudaSuccess)
+    if (glr::prepare(p, cu, n_seqs, ws, L, &a, s) != cudaSuccess ||
+        (dS_in && copy_states(p, cu, n_seqs, dS_out, dS_in, s) != cudaSuccess))
         return KDA_ERR_CUDA;
     return glr::launch_backward(a, p->io_dtype == KDA_DTYPE_BF16, s) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }

@@ -1,94 +1,246 @@
 // Backward pass of the gated linear recurrence.  With m = sqrt(1 - a^2),
 // b = m v x and G = do SiLU(z):
-//   g_t = G_t + a_{t+1} g_{t+1}            (the last token: + dS_out)
+//   g_t = G_t + a_{t+1} g_{t+1}            (the last token of a sequence: + dS_out)
 //   dz = do h SiLU'(z)      dx = g m v      di = g b (1 - v)
 //   dla = g (a h_{t-1} - (a / m)^2 b)       dr = dla la (1 - w)
 //   dA_log = sum dla la,  dr_bias = sum dr,  di_bias = sum di,  dS_in = a_1 g_1
-// One thread per (sequence, channel): the states of 64 tokens are computed again
-// from the one the prefill left, then the tokens are walked backwards.
-#include "glr_common.cuh"
+//
+// The prefill's tiles (glr_scan.cu), walked from the last to the first.  The
+// states of a tile come from the one the prefill left at its first token: a
+// thread's forward run meets the earlier warps' maps in shared memory and waits
+// for nothing, while one warp walks along the tiles for the gradient a g that comes
+// in from the right.  What the gates give is computed once and held in
+// registers between the sweeps.  Sums over the tokens go to the workspace by tile
+// and are added up in order by a second kernel.
+#include <atomic>
+
+#include "glr_tile.cuh"
 
 namespace kda {
 namespace glr {
 namespace {
 
-constexpr int NT = 128;
+enum { OUT_X = 1, OUT_R = 2, OUT_I = 4, OUT_Z = 8 };   // gradients whose rows take pairs
 
-template <typename TI>
-__global__ void __launch_bounds__(NT) backward_kernel(const __grid_constant__ ScanArgs g) {
-    const int blocks = (g.C + NT - 1) / NT;
-    const int n = blockIdx.x / blocks, c = blockIdx.x % blocks * NT + threadIdx.x;
-    if (c >= g.C) return;
-    const int64_t t0 = seq_start(g.f, n), t1 = seq_start(g.f, n + 1);
-    const float ea = -expf(g.A_log[c]), rb = g.r_bias ? g.r_bias[c] : 0.f, ib = g.i_bias ? g.i_bias[c] : 0.f;
-    float carry = g.dS_out ? g.dS_out[(size_t)n * g.C + c] : 0.f, sA = 0.f, sr = 0.f, si = 0.f;
-    float hb[CHUNK];                                  // the states before the tokens of a chunk
-    auto at = [&](int64_t t) {
-        return step_of(to_f32(static_cast<const TI*>(g.r)[t * g.r_s + c]) + rb,
-                       to_f32(static_cast<const TI*>(g.i)[t * g.i_s + c]) + ib, ea);
+template <typename TI, int MODE, int STAGES, int PER_SM>
+__global__ void __launch_bounds__(NT, PER_SM) backward_kernel(const __grid_constant__ ScanArgs g, int pairs) {
+    using R = Rows<TI, MODE>;
+    extern __shared__ __align__(128) unsigned char tiles_smem[];   // [STAGES][x, r, i, do, z]
+    __shared__ uint32_t tk[STAGES];
+    __shared__ float2 sA[WARPS][32], sB[WARPS][32], sAr[WARPS][32], sBr[WARPS][32], sIn[32];
+    __shared__ float2 sums[3][WARPS][32];
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    const uint32_t tiles = (uint32_t)g.tiles_t * (uint32_t)g.tiles_c;
+    auto issue = [&](int stage, uint32_t tile) {
+        if (tile < tiles) {
+            const int64_t t0 = (int64_t)(g.tiles_t - 1 - (int)(tile / g.tiles_c)) * CHUNK;
+            const int c0 = (int)(tile % g.tiles_c) * TILE_C;
+            unsigned char* s = tiles_smem + stage * 5 * R::BYTES;
+            R::load(s, g.x, g.x_s, t0, c0, g);
+            R::load(s + R::BYTES, g.r, g.r_s, t0, c0, g);
+            R::load(s + 2 * R::BYTES, g.i, g.i_s, t0, c0, g);
+            R::load(s + 3 * R::BYTES, g.d_o, g.do_s, t0, c0, g);
+            if (g.z) R::load(s + 4 * R::BYTES, g.z, g.z_s, t0, c0, g);
+        }
+        ptx::cp_async_commit();
     };
-    for (int64_t end = t1; end > t0;) {
-        const int64_t first = (end - 1) / CHUNK * CHUNK, from = first > t0 ? first : t0;
-        float h = from == first ? g.states[(size_t)(first / CHUNK) * g.C + c] : g.S_in ? g.S_in[(size_t)n * g.C + c] : 0.f;
-        for (int64_t t = from; t < end; ++t) {
-            hb[t - first] = h;
-            const Step s = at(t);
-            h = fmaf(s.a, h, s.m * s.v * to_f32(static_cast<const TI*>(g.x)[t * g.x_s + c]));
-        }
-        for (int64_t t = end - 1; t >= from; --t) {
-            const Step s = at(t);
-            const float x = to_f32(static_cast<const TI*>(g.x)[t * g.x_s + c]), b = s.m * s.v * x;
-            float G = to_f32(static_cast<const TI*>(g.d_o)[t * g.do_s + c]);
-            if (g.z) {
-                const float z = to_f32(static_cast<const TI*>(g.z)[t * g.z_s + c]), e = sigmoid(z);
-                static_cast<TI*>(g.dz)[t * g.dz_s + c] = from_f32<TI>(G * fmaf(s.a, hb[t - first], b) * e * fmaf(z, 1.f - e, 1.f));
-                G *= z * e;
+    if (tid == 0)
+        for (int k = 0; k < STAGES; ++k) tk[k] = atomicAdd(g.ticket, 1u);
+    __syncthreads();
+    for (int k = 0; k < STAGES; ++k) issue(k, tk[k]);
+
+    for (int stage = 0;; stage = stage + 1 == STAGES ? 0 : stage + 1) {
+        const uint32_t tile = tk[stage];
+        if (tile >= tiles) break;
+        const int order = tile / g.tiles_c, tt = g.tiles_t - 1 - order, tc = tile % g.tiles_c;
+        const int64_t t = (int64_t)tt * CHUNK + warp * SUB;
+        const int c0 = tc * TILE_C, c = c0 + 2 * lane;
+        auto pair_of = [&](const float* p, size_t row) {
+            float2 h = f2(0.f);
+            if (p && c < g.C) h.x = p[row * g.C + c];
+            if (p && c + 1 < g.C) h.y = p[row * g.C + c + 1];
+            return h;
+        };
+        const Gate k = load_gate(g, c);
+        float2 h = pair_of(g.states, tt);
+        const Borders bd = borders(g, tt, t);
+        auto seq_of = [&](int j) { return (size_t)seq_id(g.f, bd.seq + __popc((bd.start >> 1) & ((1u << j) - 1))); };
+        asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
+        __syncthreads();
+
+        const unsigned char* s = tiles_smem + stage * 5 * R::BYTES + warp * SUB * R::PITCH;
+        const typename R::Odd ox = R::odd(g.x, g.x_s, t, c0), orr = R::odd(g.r, g.r_s, t, c0), oi = R::odd(g.i, g.i_s, t, c0),
+                              od = R::odd(g.d_o, g.do_s, t, c0), oz = R::odd(g.z, g.z_s, t, c0);
+        auto x_of = [&](int j) { return R::get(s, j, ox); };
+        auto do_of = [&](int j) { return R::get(s + 3 * R::BYTES, j, od); };
+        auto z_of = [&](int j) { return R::get(s + 4 * R::BYTES, j, oz); };
+        // of each token: a, E = m v, w (with 1 - w), 1 - v, sigmoid(z), and D = dA_log / g
+        float2 a[SUB], E[SUB], ww[SUB], v_[SUB], e[SUB], D[SUB];
+        float2 A = f2(1.f), B = f2(0.f);
+#pragma unroll
+        for (int j = 0; j < SUB; ++j) {
+            float2 rest;
+            const float2 w = sigmoid_of(fma2(R::get(s + R::BYTES, j, orr), f2(-LOG2E), k.rb), rest);
+            const float2 v = sigmoid_of(fma2(R::get(s + 2 * R::BYTES, j, oi), f2(-LOG2E), k.ib), v_[j]);
+            ww[j] = smaller(w, rest);
+            if (g.z) e[j] = sigmoid_of(mul2(z_of(j), f2(-LOG2E)));
+            float2 m2;
+            const float2 la = mul2(k.ea, w);
+            decay_of(la, a[j], m2);
+            const float2 im = inv_root(m2);
+            E[j] = mul2(mul2(m2, im), v);
+            D[j] = mul2(mul2(mul2(a[j], a[j]), mul2(la, im)), v);   // (a / m)^2 b la / x
+            const float2 b = mul2(E[j], x_of(j));
+            if (bd.start >> j & 1) {
+                A = f2(-1.f);
+                B = fma2(a[j], pair_of(g.S_in, seq_of(j)), b);
+            } else {
+                A = A.x < 0.f ? A : mul2(A, a[j]);
+                B = fma2(a[j], B, b);
             }
-            const float gt = G + carry;
-            carry = s.a * gt;
-            static_cast<TI*>(g.dx)[t * g.dx_s + c] = from_f32<TI>(gt * s.m * s.v);
-            const float di = gt * b * sigmoid(-(to_f32(static_cast<const TI*>(g.i)[t * g.i_s + c]) + ib));
-            // (a / m)^2 b la = a^2 v x (la / m), zero where la is
-            const float la_m = s.m > 0.f ? s.la / s.m : 0.f;
-            const float dA = gt * fmaf(s.a * hb[t - first], s.la, -s.a * s.a * s.v * x * la_m);
-            const float dr = dA * sigmoid(-(to_f32(static_cast<const TI*>(g.r)[t * g.r_s + c]) + rb));
-            static_cast<TI*>(g.di)[t * g.di_s + c] = from_f32<TI>(di);
-            static_cast<TI*>(g.dr)[t * g.dr_s + c] = from_f32<TI>(dr);
-            sA += dA;
-            sr += dr;
-            si += di;
         }
-        end = from;
+        sA[warp][lane] = A;
+        sB[warp][lane] = B;
+        auto G_of = [&](int j) { return g.z ? mul2(do_of(j), mul2(z_of(j), e[j])) : do_of(j); };
+        A = f2(1.f);
+        B = f2(0.f);
+#pragma unroll
+        for (int j = SUB - 1; j >= 0; --j) {
+            if (bd.end >> j & 1) {
+                A = f2(-1.f);
+                B = pair_of(g.dS_out, seq_of(j));
+            } else if (A.x >= 0.f) {
+                A = mul2(A, a[j]);
+            }
+            B = mul2(a[j], add2(G_of(j), B));
+        }
+        sAr[warp][lane] = A;
+        sBr[warp][lane] = B;
+        __syncthreads();
+        if (warp == 0) {
+            A = sAr[WARPS - 1][lane];
+            B = sBr[WARPS - 1][lane];
+            for (int u = WARPS - 2; u >= 0; --u) {
+                const float2 Aw = sAr[u][lane], Bw = sBr[u][lane];
+                B = apply(Aw, Bw, B);
+                A = Aw.x < 0.f ? Aw : A.x < 0.f ? A : mul2(A, Aw);
+            }
+            sIn[lane] = walk(g, order, tc, A, B);
+        } else if (tid == 32) {
+            tk[stage] = atomicAdd(g.ticket, 1u);
+        }
+        for (int u = 0; u < warp; ++u) h = apply(sA[u][lane], sB[u][lane], h);
+#pragma unroll
+        for (int j = 0; j < SUB; ++j) {
+            if (bd.start >> j & 1) h = pair_of(g.S_in, seq_of(j));
+            const float2 x = x_of(j), ah = mul2(a[j], h);
+            D[j] = fma2(ah, mul2(k.ea, sigmoid_from(ww[j])), neg2(mul2(D[j], x)));
+            h = fma2(E[j], x, ah);
+            if (g.z && t + j < g.T) {
+                const float2 z = z_of(j), s1 = add2(f2(1.f), neg2(e[j]));
+                put<TI>(g.dz, g.dz_s, t + j, c, g.C, pairs & OUT_Z, mul2(mul2(do_of(j), h), mul2(e[j], fma2(z, s1, f2(1.f)))));
+            }
+        }
+        __syncthreads();
+        float2 carry = sIn[lane], sa = f2(0.f), sr = f2(0.f), si = f2(0.f);
+        for (int u = WARPS - 1; u > warp; --u) carry = apply(sAr[u][lane], sBr[u][lane], carry);
+#pragma unroll
+        for (int j = SUB - 1; j >= 0; --j) {
+            if (bd.end >> j & 1) carry = pair_of(g.dS_out, seq_of(j));
+            const float2 gt = add2(G_of(j), carry), dx = mul2(gt, E[j]);
+            carry = mul2(a[j], gt);
+            const float2 di = mul2(mul2(dx, x_of(j)), v_[j]);
+            const float2 dA = mul2(gt, D[j]), dr = mul2(dA, rest_from(ww[j]));
+            if (t + j < g.T) {
+                put<TI>(g.dx, g.dx_s, t + j, c, g.C, pairs & OUT_X, dx);
+                put<TI>(g.dr, g.dr_s, t + j, c, g.C, pairs & OUT_R, dr);
+                put<TI>(g.di, g.di_s, t + j, c, g.C, pairs & OUT_I, di);
+                sa = add2(sa, dA);
+                sr = add2(sr, dr);
+                si = add2(si, di);
+            }
+            if (g.dS_in && (bd.start >> j & 1)) put<float>(g.dS_in, g.C, seq_of(j), c, g.C, false, carry);
+        }
+        sums[0][warp][lane] = sa;
+        sums[1][warp][lane] = sr;
+        sums[2][warp][lane] = si;
+        __syncthreads();                             // the tile's rows and maps are read
+        issue(stage, tk[stage]);
+        if (tid < 96) {
+            const int q = tid / 32;
+            float2 sum = sums[q][0][lane];
+#pragma unroll
+            for (int u = 1; u < WARPS; ++u) sum = add2(sum, sums[q][u][lane]);
+            put<float>(g.part, g.C, (int64_t)tt * 3 + q, c, g.C, false, sum);
+        }
     }
-    if (g.dS_in) g.dS_in[(size_t)n * g.C + c] = carry;
-    float* p = g.part + (size_t)n * 3 * g.C + c;
-    p[0] = sA;
-    p[g.C] = sr;
-    p[2 * (size_t)g.C] = si;
 }
 
-// The sums over the sequences, in their order.
-__global__ void __launch_bounds__(NT) params_kernel(const __grid_constant__ ScanArgs g) {
-    const int c = blockIdx.x * NT + threadIdx.x;
-    if (c >= g.C) return;
-    double s[3] = {0.0, 0.0, 0.0};
-    for (int n = 0; n < g.f.n; ++n)
-        for (int k = 0; k < 3; ++k) s[k] += g.part[((size_t)n * 3 + k) * g.C + c];
-    g.dA_log[c] = (float)s[0];
-    if (g.dr_bias) g.dr_bias[c] = (float)s[1];
-    if (g.di_bias) g.di_bias[c] = (float)s[2];
+// The parameters' gradients: the tiles' sums, added up in order with the error of each
+// addition kept (Knuth's two-sum).  A block takes 32 channels of one gradient, its 8 warps
+// every eighth tile.
+__global__ void __launch_bounds__(256) params_kernel(const __grid_constant__ ScanArgs g) {
+    __shared__ float2 part[8][32];
+    const int c = blockIdx.x * 32 + threadIdx.x % 32, q = blockIdx.y, w = threadIdx.x / 32;
+    float* out = q == 0 ? g.dA_log : q == 1 ? g.dr_bias : g.di_bias;
+    if (out == nullptr) return;
+    float s = 0.f, err = 0.f;
+    auto add = [&](float x) {
+        const float n = __fadd_rn(s, x), b = __fsub_rn(n, s);
+        err += __fadd_rn(__fsub_rn(s, __fsub_rn(n, b)), __fsub_rn(x, b));
+        s = n;
+    };
+    if (c < g.C) {
+#pragma unroll 8
+        for (int tt = w; tt < g.tiles_t; tt += 8) add(g.part[((size_t)tt * 3 + q) * g.C + c]);
+    }
+    part[w][threadIdx.x % 32] = make_float2(s, err);
+    __syncthreads();
+    if (w == 0 && c < g.C) {
+        for (int u = 1; u < 8; ++u) {
+            add(part[u][threadIdx.x].x);
+            err += part[u][threadIdx.x].y;
+        }
+        out[c] = s + err;
+    }
+}
+
+template <typename TI, int MODE>
+cudaError_t backward(const ScanArgs& a, int pairs, cudaStream_t s) {
+    constexpr int STAGES = sizeof(TI) == 2 ? 2 : 1, PER_SM = 2;
+    auto k = backward_kernel<TI, MODE, STAGES, PER_SM>;
+    constexpr int SMEM = STAGES * 5 * Rows<TI, MODE>::BYTES;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    static std::atomic<uint64_t> done{0};            // (set once per device)
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    if (!(done.load() & bit)) {
+        e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+        if (e != cudaSuccess) return e;
+        done.fetch_or(bit);
+    }
+    const int64_t tiles = (int64_t)a.tiles_t * a.tiles_c;
+    k<<<(unsigned)(tiles < SMS * PER_SM ? tiles : SMS * PER_SM), NT, SMEM, s>>>(a, pairs);
+    return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_backward(const ScanArgs& a, int io_bf16, cudaStream_t s) {
-    const unsigned blocks = (unsigned)((a.C + NT - 1) / NT);
-    const unsigned grid = (unsigned)a.f.n * blocks;
-    if (io_bf16) backward_kernel<__nv_bfloat16><<<grid, NT, 0, s>>>(a);
-    else backward_kernel<float><<<grid, NT, 0, s>>>(a);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    params_kernel<<<blocks, NT, 0, s>>>(a);
+    const int es = io_bf16 ? 2 : 4;
+    cudaError_t e = cudaSuccess;
+    if (a.tiles_t > 0) {
+        const int mode = std::max({row_mode(a.x, a.x_s, es), row_mode(a.r, a.r_s, es), row_mode(a.i, a.i_s, es),
+                                   row_mode(a.d_o, a.do_s, es), a.z ? row_mode(a.z, a.z_s, es) : 0});
+        const int pairs = (row_pairs(a.dx, a.dx_s, es) ? OUT_X : 0) | (row_pairs(a.dr, a.dr_s, es) ? OUT_R : 0) |
+                          (row_pairs(a.di, a.di_s, es) ? OUT_I : 0) | (a.z && row_pairs(a.dz, a.dz_s, es) ? OUT_Z : 0);
+        if (!io_bf16) e = mode == M16 ? backward<float, M16>(a, pairs, s) : backward<float, M4>(a, pairs, s);
+        else e = mode == M16 ? backward<__nv_bfloat16, M16>(a, pairs, s)
+               : mode == M4 ? backward<__nv_bfloat16, M4>(a, pairs, s) : backward<__nv_bfloat16, MODD>(a, pairs, s);
+        if (e != cudaSuccess) return e;
+    }
+    params_kernel<<<dim3((unsigned)((a.C + 31) / 32), 3), 256, 0, s>>>(a);
     return cudaGetLastError();
 }
 

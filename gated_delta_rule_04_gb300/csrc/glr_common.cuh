@@ -8,17 +8,19 @@ namespace glr {
 
 constexpr int CHUNK = KDA_GLR_CHUNK;
 constexpr int INLINE_SEQS = 16;
+constexpr int TILE_C = 64;           // channels of a tile; its tokens are a CHUNK
 
-// The token offsets of a call of few sequences travel in the kernel arguments;
-// those of more are built on the device.
-struct Offsets {
-    int32_t n;                       // sequences
-    int32_t cu[INLINE_SEQS + 1];     // where n <= INLINE_SEQS
-    const int64_t* d_cu;             // device [n + 1] otherwise
+// The sequences of a call that have tokens, in order.  Few travel in the kernel
+// arguments; more are built on the device, with the sequence of each tile's first token.
+struct Sequences {
+    int32_t n;                       // sequences with tokens
+    int32_t cu[INLINE_SEQS + 1];     // where n <= INLINE_SEQS: their first tokens, and T
+    int32_t id[INLINE_SEQS];         // their rows of S_in and S_out
+    const int64_t* d_cu;             // device [n + 1] and [n] otherwise
+    const int32_t* d_id;
+    const int32_t* d_tile;           // device [tiles along T]
 };
-__device__ __forceinline__ int64_t seq_start(const Offsets& f, int n) {
-    return f.n <= INLINE_SEQS ? f.cu[n] : f.d_cu[n];
-}
+__device__ __forceinline__ int seq_id(const Sequences& f, int s) { return f.n <= INLINE_SEQS ? f.id[s] : f.d_id[s]; }
 
 // One prefill or backward call, as the kernels see it.  Rows of the token
 // tensors are `*_s` elements apart, rows of o packed.
@@ -36,10 +38,17 @@ struct ScanArgs {
     void *dx, *dr, *di, *dz;
     int64_t dx_s, dr_s, di_s, dz_s;
     float *dS_in, *dA_log, *dr_bias, *di_bias;
-    float* part;                     // workspace: partial sums of the parameters' gradients
     int64_t T;
     int32_t C;
-    Offsets f;
+    Sequences f;
+    // workspace
+    int32_t* status;                 // error word
+    uint32_t* ticket;                // the next tile to be taken
+    int32_t* flags;                  // [tiles along T][tiles along C]
+    float* agg;                      // [tiles along T][tiles along C][TILE_C][2]
+    float* pre;                      // [tiles along T][tiles along C][TILE_C]
+    float* part;                     // [tiles along T][3][C]: partial sums of the parameters' gradients
+    int32_t tiles_t, tiles_c;
 };
 
 struct TokenArgs {
@@ -58,21 +67,7 @@ cudaError_t launch_scan(const ScanArgs& a, int io_bf16, cudaStream_t s);
 cudaError_t launch_backward(const ScanArgs& a, int io_bf16, cudaStream_t s);
 cudaError_t launch_tokens(const TokenArgs& a, int io_bf16, cudaStream_t s);
 
-__device__ __forceinline__ float sigmoid(float x) { return 1.f / (1.f + expf(-x)); }
-
-// What a token does to a channel's state: h -> a h + m v x.
-struct Step {
-    float w, v, la, a, m;
-};
-__device__ __forceinline__ Step step_of(float r, float i, float neg_ea) {
-    Step s;
-    s.w = sigmoid(r);
-    s.v = sigmoid(i);
-    s.la = neg_ea * s.w;
-    s.a = expf(s.la);
-    s.m = sqrtf(-expm1f(2.f * s.la));
-    return s;
-}
+cudaError_t launch_tile_table(const int64_t* d_cu, int32_t n, int32_t* d_tile, int32_t tiles_t, cudaStream_t s);
 
 }  // namespace glr
 }  // namespace kda

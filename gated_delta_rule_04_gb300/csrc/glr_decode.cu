@@ -1,7 +1,8 @@
 // Tokens of the gated linear recurrence over a pool of states: straight runs of
-// 1 to 64 tokens per session, and the accepted paths of a round.  A thread per
-// (session, channel) walks the tokens with its state in a register.
-#include "glr_common.cuh"
+// 1 to 64 tokens per session, and the accepted paths of a round.  A thread holds
+// the states of V neighbouring channels and walks the tokens, the next one's
+// rows on the way while it computes.  The rows move once and bound the call.
+#include "glr_math.cuh"
 
 namespace kda {
 namespace glr {
@@ -9,48 +10,142 @@ namespace {
 
 constexpr int NT = 128;
 
-template <typename TI>
-__global__ void __launch_bounds__(NT) token_kernel(const __grid_constant__ TokenArgs g) {
-    const int blocks = (g.C + NT - 1) / NT;
-    const int n = blockIdx.x / blocks, c = blockIdx.x % blocks * NT + threadIdx.x;
-    const int slot = g.slots ? g.slots[n] : n;
-    if (slot < 0 || slot >= g.n_slots) return;
-    int len = g.n_tokens;
-    const int32_t* path = g.path ? g.path + (size_t)n * g.max_len : nullptr;
-    if (path) {                                       // a session with an entry out of range is skipped
-        len = g.path_len[n];
-        if (len < 0 || len > g.max_len) return;
-        bool bad = false;
-        for (int j = 0; j < len; ++j) bad |= path[j] < 0 || path[j] >= g.n_tokens;
-        if (bad) return;
+template <int BYTES> struct Word;
+template <> struct Word<2> { using T = uint16_t; };
+template <> struct Word<4> { using T = uint32_t; };
+template <> struct Word<8> { using T = uint2; };
+template <> struct Word<16> { using T = uint4; };
+
+// V neighbouring values as pairs (V = 1: the second of the pair is zero).
+template <typename TI, int V> struct Values {
+    static constexpr int PAIRS = (V + 1) / 2;
+    union Raw {
+        typename Word<V * sizeof(TI)>::T w;
+        TI v[V];
+        __device__ Raw() {}
+    };
+    static __device__ __forceinline__ void load(Raw& r, const void* base, int64_t at) {
+        r.w = *reinterpret_cast<const typename Word<V * sizeof(TI)>::T*>(static_cast<const TI*>(base) + at);
     }
-    if (c >= g.C) return;
-    const float ea = -expf(g.A_log[c]), rb = g.r_bias ? g.r_bias[c] : 0.f, ib = g.i_bias ? g.i_bias[c] : 0.f;
-    float h = g.S_in[(size_t)slot * g.C + c];
-    for (int j = 0; j < len; ++j) {
-        const int64_t row = (int64_t)n * g.n_tokens + (path ? path[j] : j);
-        const Step s = step_of(to_f32(static_cast<const TI*>(g.r)[row * g.r_s + c]) + rb,
-                               to_f32(static_cast<const TI*>(g.i)[row * g.i_s + c]) + ib, ea);
-        h = fmaf(s.a, h, s.m * s.v * to_f32(static_cast<const TI*>(g.x)[row * g.x_s + c]));
-        if (g.o) {
-            float o = h;
-            if (g.z) {
-                const float z = to_f32(static_cast<const TI*>(g.z)[row * g.z_s + c]);
-                o *= z * sigmoid(z);
-            }
-            static_cast<TI*>(g.o)[row * g.C + c] = from_f32<TI>(o);
+    static __device__ __forceinline__ float2 pair(const Raw& r, int p) {
+        return make_float2(to_f32(r.v[2 * p]), 2 * p + 1 < V ? to_f32(r.v[2 * p + 1 < V ? 2 * p + 1 : 0]) : 0.f);
+    }
+    static __device__ __forceinline__ void store(void* base, int64_t at, const float2 (&x)[PAIRS]) {
+        Raw r;
+#pragma unroll
+        for (int p = 0; p < PAIRS; ++p) {
+            r.v[2 * p] = from_f32<TI>(x[p].x);
+            if (2 * p + 1 < V) r.v[2 * p + 1 < V ? 2 * p + 1 : 0] = from_f32<TI>(x[p].y);
+        }
+        *reinterpret_cast<typename Word<V * sizeof(TI)>::T*>(static_cast<TI*>(base) + at) = r.w;
+    }
+};
+
+template <typename TI, int V>
+__global__ void __launch_bounds__(NT) token_kernel(const __grid_constant__ TokenArgs g, int blocks) {
+    using X = Values<TI, V>;
+    constexpr int PAIRS = X::PAIRS;
+    const int n = blockIdx.x / blocks, c = (blockIdx.x % blocks * blockDim.x + threadIdx.x) * V, lane = threadIdx.x & 31;
+    const int slot = g.slots ? g.slots[n] : n;
+    int len = g.n_tokens, p1 = 0, p2 = 0;
+    if (g.path) {                                     // lane j has the path's tokens j and 32 + j
+        len = g.path_len[n];
+        const int32_t* path = g.path + (size_t)n * g.max_len;
+        if (lane < g.max_len) p1 = path[lane];
+        if (lane + 32 < g.max_len) p2 = path[lane + 32];
+        bool bad = len < 0 || len > g.max_len;
+        bad |= lane < len && (p1 < 0 || p1 >= g.n_tokens);
+        bad |= lane + 32 < len && (p2 < 0 || p2 >= g.n_tokens);
+        if (__any_sync(0xffffffffu, bad)) return;     // the session is skipped (by every warp alike)
+    }
+    if (slot < 0 || slot >= g.n_slots) return;
+    const bool in = c < g.C;
+    float2 h[PAIRS];
+    Gate k[PAIRS];
+    if (in) {
+        const size_t at = (size_t)slot * g.C + c;
+        typename Values<float, V == 8 ? 4 : V>::Raw s[V == 8 ? 2 : 1];
+#pragma unroll
+        for (int q = 0; q < (V == 8 ? 2 : 1); ++q) Values<float, V == 8 ? 4 : V>::load(s[q], g.S_in, at + 4 * q);
+#pragma unroll
+        for (int p = 0; p < PAIRS; ++p) {
+            h[p] = Values<float, V == 8 ? 4 : V>::pair(s[p / 2], V == 8 ? p % 2 : p);
+            k[p] = load_gate(g, c + 2 * p);
         }
     }
-    if (g.S_out) g.S_out[(size_t)slot * g.C + c] = h;
+    auto row_of = [&](int j) {
+        const int node = !g.path ? j : j < 32 ? __shfl_sync(0xffffffffu, p1, j) : __shfl_sync(0xffffffffu, p2, j - 32);
+        return (int64_t)n * g.n_tokens + node;
+    };
+    typename X::Raw x, r, i, z;
+    auto load = [&](int64_t row) {
+        X::load(x, g.x, row * g.x_s + c);
+        X::load(r, g.r, row * g.r_s + c);
+        X::load(i, g.i, row * g.i_s + c);
+        if (g.z) X::load(z, g.z, row * g.z_s + c);
+    };
+    int64_t row = len > 0 ? row_of(0) : 0;
+    if (in && len > 0) load(row);
+    for (int j = 0; j < len; ++j) {
+        const typename X::Raw xj = x, rj = r, ij = i, zj = z;
+        const int64_t here = row;
+        if (j + 1 < len) {
+            row = row_of(j + 1);
+            if (in) load(row);
+        }
+        if (!in) continue;
+        float2 o[PAIRS];
+#pragma unroll
+        for (int p = 0; p < PAIRS; ++p) {
+            const Step s = step_of(k[p], X::pair(xj, p), X::pair(rj, p), X::pair(ij, p));
+            h[p] = fma2(s.a, h[p], s.b);
+            o[p] = g.z ? gated(h[p], X::pair(zj, p)) : h[p];
+        }
+        if (g.o) X::store(g.o, here * g.C + c, o);
+    }
+    if (in && g.S_out) {
+        const size_t at = (size_t)slot * g.C + c;
+        if constexpr (V == 8) {
+            const float2 lo[2] = {h[0], h[1]}, hi[2] = {h[2], h[3]};
+            Values<float, 4>::store(g.S_out, at, lo);
+            Values<float, 4>::store(g.S_out, at + 4, hi);
+        } else {
+            Values<float, V>::store(g.S_out, at, h);
+        }
+    }
+}
+
+template <typename TI, int V>
+cudaError_t tokens(const TokenArgs& a, cudaStream_t s) {
+    const int64_t per = ((int64_t)a.C + V - 1) / V;
+    const int nt = (int)(per < NT ? (per + 31) / 32 * 32 : NT), blocks = (int)((per + nt - 1) / nt);
+    token_kernel<TI, V><<<(unsigned)((int64_t)a.n * blocks), nt, 0, s>>>(a, blocks);
+    return cudaGetLastError();
+}
+
+// The most neighbouring channels (1, 2, 4, 8) that every row and state can be taken by.
+int widest(const TokenArgs& a, int es) {
+    uint64_t rows = 0, states = 0;                    // the addresses and strides, or'ed
+    auto row = [&](const void* p, int64_t stride) {
+        if (p) rows |= reinterpret_cast<uintptr_t>(p) | (uint64_t)(stride * es);
+    };
+    row(a.x, a.x_s); row(a.r, a.r_s); row(a.i, a.i_s); row(a.z, a.z_s); row(a.o, a.C);
+    states |= reinterpret_cast<uintptr_t>(a.S_in) | reinterpret_cast<uintptr_t>(a.S_out);
+    int v = 16 / es;
+    while (v > 1 && (rows % (v * es) != 0 || states % ((v < 4 ? v : 4) * 4) != 0 || a.C % v != 0)) v /= 2;
+    return v;
 }
 
 }  // namespace
 
 cudaError_t launch_tokens(const TokenArgs& a, int io_bf16, cudaStream_t s) {
-    const unsigned grid = (unsigned)((int64_t)a.n * ((a.C + NT - 1) / NT));
-    if (io_bf16) token_kernel<__nv_bfloat16><<<grid, NT, 0, s>>>(a);
-    else token_kernel<float><<<grid, NT, 0, s>>>(a);
-    return cudaGetLastError();
+    int v = widest(a, io_bf16 ? 2 : 4);
+    // few sessions: pairs, as many threads as there are
+    while (v > 2 && (int64_t)a.n * a.C / v < SMS * 256) v /= 2;
+    if (!io_bf16)
+        return v == 4 ? tokens<float, 4>(a, s) : v == 2 ? tokens<float, 2>(a, s) : tokens<float, 1>(a, s);
+    return v == 8 ? tokens<__nv_bfloat16, 8>(a, s) : v == 4 ? tokens<__nv_bfloat16, 4>(a, s)
+         : v == 2 ? tokens<__nv_bfloat16, 2>(a, s) : tokens<__nv_bfloat16, 1>(a, s);
 }
 
 }  // namespace glr

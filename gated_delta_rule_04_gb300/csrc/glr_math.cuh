@@ -1,0 +1,110 @@
+// Arithmetic of the gated linear recurrence, in channel pairs (sm_103a).
+#pragma once
+
+#include "glr_common.cuh"
+
+namespace kda {
+namespace glr {
+
+constexpr int SMS = 152;
+
+// ---- arithmetic of channel pairs ------------------------------------------------------
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rsq(float x) {
+    float y;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float2 f2(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float2 neg2(float2 a) { return make_float2(-a.x, -a.y); }
+
+constexpr float LOG2E = 1.4426950408889634f;
+// 1 / (1 + 2^t): sigmoid(x) for t = -x log2(e)
+__device__ __forceinline__ float2 sigmoid_of(float2 t) {
+    const float2 d = add2(make_float2(ex2(t.x), ex2(t.y)), f2(1.f));
+    return make_float2(rcp(d.x), rcp(d.y));
+}
+// The same, with 1 - sigmoid(x) = 2^t sigmoid(x) to its own digits.
+__device__ __forceinline__ float2 sigmoid_of(float2 t, float2& rest) {
+    // (up to 2^126, whose reciprocal is not flushed to zero)
+    const float2 e = make_float2(fminf(ex2(t.x), 8.5e37f), fminf(ex2(t.y), 8.5e37f));
+    const float2 d = add2(e, f2(1.f)), s = make_float2(rcp(d.x), rcp(d.y));
+    rest = mul2(e, s);
+    return s;
+}
+// A sigmoid and its rest in one number, both to their digits: the smaller of them, with a minus if it is the rest.
+__device__ __forceinline__ float smaller(float s, float rest) { return s < rest ? s : -rest; }
+__device__ __forceinline__ float sigmoid_from(float k) { return __float_as_int(k) < 0 ? 1.f + k : k; }
+__device__ __forceinline__ float rest_from(float k) { return __float_as_int(k) < 0 ? -k : 1.f - k; }
+__device__ __forceinline__ float2 smaller(float2 s, float2 r) { return make_float2(smaller(s.x, r.x), smaller(s.y, r.y)); }
+__device__ __forceinline__ float2 sigmoid_from(float2 k) { return make_float2(sigmoid_from(k.x), sigmoid_from(k.y)); }
+__device__ __forceinline__ float2 rest_from(float2 k) { return make_float2(rest_from(k.x), rest_from(k.y)); }
+
+// What a channel needs besides its rows: -exp(A_log), and the biases times -log2(e).
+struct Gate {
+    float2 ea, rb, ib;
+};
+template <typename Args> __device__ __forceinline__ Gate load_gate(const Args& g, int c) {
+    Gate k;
+    float* f = reinterpret_cast<float*>(&k);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const bool in = c + e < g.C;
+        f[e] = in ? -expf(g.A_log[c + e]) : 0.f;
+        f[2 + e] = in && g.r_bias ? -LOG2E * g.r_bias[c + e] : 0.f;
+        f[4 + e] = in && g.i_bias ? -LOG2E * g.i_bias[c + e] : 0.f;
+    }
+    return k;
+}
+
+// A token's decay a = exp(la) and m^2 = 1 - a^2, for la <= 0.  Near 1 both come from
+// q = exp(la) - 1 by its Taylor polynomial (relative error y^7 / 8! < 2e-9 at 1/4):
+// a = 1 + q is then rounded to nearest, where an exponential's error has one sign that a
+// state adds up at every token, and m^2 = -q (2 + q) keeps its digits.
+__device__ __forceinline__ void decay_of(float2 la, float2& a, float2& m2) {
+    float2 p = fma2(la, f2(1.f / 7), f2(1.f));
+    p = fma2(mul2(la, f2(1.f / 6)), p, f2(1.f));
+    p = fma2(mul2(la, f2(1.f / 5)), p, f2(1.f));
+    p = fma2(mul2(la, f2(1.f / 4)), p, f2(1.f));
+    p = fma2(mul2(la, f2(1.f / 3)), p, f2(1.f));
+    p = fma2(mul2(la, f2(1.f / 2)), p, f2(1.f));
+    const float2 q = mul2(la, p), qa = add2(q, f2(1.f)), qm = mul2(neg2(q), add2(q, f2(2.f)));
+    const float2 t = mul2(la, f2(LOG2E)), e = make_float2(ex2(t.x), ex2(t.y)), em = fma2(neg2(e), e, f2(1.f));
+    a = make_float2(la.x < -0.25f ? e.x : qa.x, la.y < -0.25f ? e.y : qa.y);
+    m2 = make_float2(la.x < -0.25f ? em.x : qm.x, la.y < -0.25f ? em.y : qm.y);
+}
+// 1 / m, finite at m = 0 (there m2 / m is 0)
+__device__ __forceinline__ float2 inv_root(float2 m2) { return make_float2(rsq(fmaxf(m2.x, 1e-36f)), rsq(fmaxf(m2.y, 1e-36f))); }
+
+// h -> A h + B of a run of tokens; A < 0 marks a run that starts anew (a decay never is).
+__device__ __forceinline__ float apply(float A, float B, float h) { return A < 0.f ? B : fmaf(A, h, B); }
+__device__ __forceinline__ float2 apply(float2 A, float2 B, float2 h) { return make_float2(apply(A.x, B.x, h.x), apply(A.y, B.y, h.y)); }
+
+// What a token does to a channel pair: h -> a h + b.
+struct Step {
+    float2 a, b;
+};
+__device__ __forceinline__ Step step_of(const Gate& k, float2 x, float2 r, float2 i) {
+    const float2 w = sigmoid_of(fma2(r, f2(-LOG2E), k.rb)), v = sigmoid_of(fma2(i, f2(-LOG2E), k.ib));
+    Step s;
+    float2 m2;
+    decay_of(mul2(k.ea, w), s.a, m2);
+    s.b = mul2(mul2(mul2(m2, inv_root(m2)), v), x);
+    return s;
+}
+__device__ __forceinline__ float2 gated(float2 h, float2 z) { return mul2(h, mul2(z, sigmoid_of(mul2(z, f2(-LOG2E))))); }
+
+}  // namespace glr
+}  // namespace kda

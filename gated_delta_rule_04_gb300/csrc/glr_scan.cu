@@ -1,43 +1,165 @@
 // Prefill of the gated linear recurrence: h_t = a_t h_{t-1} + m_t v_t x_t,
-// o_t = h_t SiLU(z_t).  One thread per (sequence, channel), token by token.
-#include "glr_common.cuh"
+// o_t = h_t SiLU(z_t), with m = sqrt(1 - a^2).
+//
+// One pass over the data.  Tiles of 64 tokens x 64 channels lie in shared memory
+// in their own type, copied some tiles ahead; a thread holds 8 tokens of 2
+// channels, computes their a and b = m v x once, and the map h -> A h + B of its
+// run.  The maps meet in shared memory, the tile's value comes from the walk along
+// the tiles (glr_tile.cuh), and the second sweep over the 8 tokens is one multiply-add
+// a token and the output gate.  Sequences lie anywhere in the tiles: a token
+// that begins one starts its run anew from S_in.
+#include <atomic>
+
+#include "glr_tile.cuh"
 
 namespace kda {
 namespace glr {
 namespace {
 
-constexpr int NT = 128;
-
-template <typename TI>
-__global__ void __launch_bounds__(NT) scan_kernel(const __grid_constant__ ScanArgs g) {
-    const int blocks = (g.C + NT - 1) / NT;
-    const int n = blockIdx.x / blocks, c = blockIdx.x % blocks * NT + threadIdx.x;
-    if (c >= g.C) return;
-    const int64_t t0 = seq_start(g.f, n), t1 = seq_start(g.f, n + 1);
-    const float ea = -expf(g.A_log[c]), rb = g.r_bias ? g.r_bias[c] : 0.f, ib = g.i_bias ? g.i_bias[c] : 0.f;
-    float h = g.S_in ? g.S_in[(size_t)n * g.C + c] : 0.f;
-    for (int64_t t = t0; t < t1; ++t) {
-        if (g.states && t % CHUNK == 0) g.states[(size_t)(t / CHUNK) * g.C + c] = h;
-        const Step s = step_of(to_f32(static_cast<const TI*>(g.r)[t * g.r_s + c]) + rb,
-                               to_f32(static_cast<const TI*>(g.i)[t * g.i_s + c]) + ib, ea);
-        h = fmaf(s.a, h, s.m * s.v * to_f32(static_cast<const TI*>(g.x)[t * g.x_s + c]));
-        float o = h;
-        if (g.z) {
-            const float z = to_f32(static_cast<const TI*>(g.z)[t * g.z_s + c]);
-            o *= z * sigmoid(z);
+template <typename TI, int MODE, int STAGES, int PER_SM>
+__global__ void __launch_bounds__(NT, PER_SM) scan_kernel(const __grid_constant__ ScanArgs g, bool pairs) {
+    using R = Rows<TI, MODE>;
+    extern __shared__ __align__(128) unsigned char tiles_smem[];   // [STAGES][x, r, i, z]
+    __shared__ uint32_t tk[STAGES];
+    __shared__ float2 sA[WARPS][32], sB[WARPS][32], sIn[32];
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    const uint32_t tiles = (uint32_t)g.tiles_t * (uint32_t)g.tiles_c;
+    auto issue = [&](int stage, uint32_t tile) {
+        if (tile < tiles) {
+            const int64_t t0 = (int64_t)(tile / g.tiles_c) * CHUNK;
+            const int c0 = (int)(tile % g.tiles_c) * TILE_C;
+            unsigned char* s = tiles_smem + stage * 4 * R::BYTES;
+            R::load(s, g.x, g.x_s, t0, c0, g);
+            R::load(s + R::BYTES, g.r, g.r_s, t0, c0, g);
+            R::load(s + 2 * R::BYTES, g.i, g.i_s, t0, c0, g);
+            if (g.z) R::load(s + 3 * R::BYTES, g.z, g.z_s, t0, c0, g);
         }
-        static_cast<TI*>(g.o)[t * g.C + c] = from_f32<TI>(o);
+        ptx::cp_async_commit();
+    };
+    if (tid == 0)
+        for (int k = 0; k < STAGES; ++k) tk[k] = atomicAdd(g.ticket, 1u);
+    __syncthreads();
+    for (int k = 0; k < STAGES; ++k) issue(k, tk[k]);
+
+    for (int stage = 0;; stage = stage + 1 == STAGES ? 0 : stage + 1) {
+        const uint32_t tile = tk[stage];
+        if (tile >= tiles) break;                    // (tickets only grow)
+        const int tt = tile / g.tiles_c, tc = tile % g.tiles_c;
+        const int64_t t = (int64_t)tt * CHUNK + warp * SUB;
+        const int c0 = tc * TILE_C, c = c0 + 2 * lane;
+        const Gate k = load_gate(g, c);
+        const Borders bd = borders(g, tt, t);
+        auto seq_of = [&](int j) { return bd.seq + __popc((bd.start >> 1) & ((1u << j) - 1)); };
+        auto state_in = [&](int j) {
+            float2 h = f2(0.f);
+            if (g.S_in) {
+                const float* p = g.S_in + (size_t)seq_id(g.f, seq_of(j)) * g.C + c;
+                if (c < g.C) h.x = p[0];
+                if (c + 1 < g.C) h.y = p[1];
+            }
+            return h;
+        };
+        asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
+        __syncthreads();
+
+        const unsigned char* s = tiles_smem + stage * 4 * R::BYTES;
+        const typename R::Odd ox = R::odd(g.x, g.x_s, t, c0), orr = R::odd(g.r, g.r_s, t, c0), oi = R::odd(g.i, g.i_s, t, c0),
+                              oz = R::odd(g.z, g.z_s, t, c0);
+        float2 a[SUB], b[SUB], A = f2(1.f), B = f2(0.f), first = f2(0.f);
+        s += warp * SUB * R::PITCH;
+#pragma unroll
+        for (int j = 0; j < SUB; ++j) {
+            const Step st = step_of(k, R::get(s, j, ox), R::get(s + R::BYTES, j, orr), R::get(s + 2 * R::BYTES, j, oi));
+            a[j] = st.a;
+            b[j] = st.b;
+            if (bd.start >> j & 1) {
+                const float2 h = state_in(j);        // (S_out, written behind the barriers, may be S_in)
+                if (j == 0) first = h;
+                b[j] = fma2(a[j], h, b[j]);
+                A = f2(-1.f);
+                B = b[j];
+            } else {
+                A = A.x < 0.f ? A : mul2(A, a[j]);
+                B = fma2(a[j], B, b[j]);
+            }
+        }
+        sA[warp][lane] = A;
+        sB[warp][lane] = B;
+        __syncthreads();
+        if (warp == 0) {
+            for (int w = 1; w < WARPS; ++w) {
+                const float2 Aw = sA[w][lane], Bw = sB[w][lane];
+                B = apply(Aw, Bw, B);
+                A = Aw.x < 0.f ? Aw : A.x < 0.f ? A : mul2(A, Aw);
+            }
+            sIn[lane] = walk(g, tt, tc, A, B);
+        } else if (tid == 32) {
+            tk[stage] = atomicAdd(g.ticket, 1u);
+        }
+        __syncthreads();
+        float2 h = sIn[lane];
+        if (g.states && warp == 0) put<float>(g.states, g.C, tt, c, g.C, false, bd.start & 1 ? first : h);
+        for (int w = 0; w < warp; ++w) h = apply(sA[w][lane], sB[w][lane], h);
+#pragma unroll
+        for (int j = 0; j < SUB; ++j) {
+            h = bd.start >> j & 1 ? b[j] : fma2(a[j], h, b[j]);
+            float2 o = h;
+            if (g.z) o = gated(o, R::get(s + 3 * R::BYTES, j, oz));
+            if (t + j < g.T) put<TI>(g.o, g.C, t + j, c, g.C, pairs, o);
+            if (bd.end >> j & 1) put<float>(g.S_out, g.C, seq_id(g.f, seq_of(j)), c, g.C, false, h);
+        }
+        __syncthreads();                             // the tile's rows and maps are read
+        issue(stage, tk[stage]);
     }
-    g.S_out[(size_t)n * g.C + c] = h;
+}
+
+template <typename TI, int MODE>
+cudaError_t scan(const ScanArgs& a, bool pairs, cudaStream_t s) {
+    constexpr int STAGES = sizeof(TI) == 2 ? 3 : 1, PER_SM = sizeof(TI) == 2 ? 2 : 3;
+    auto k = scan_kernel<TI, MODE, STAGES, PER_SM>;
+    constexpr int SMEM = STAGES * 4 * Rows<TI, MODE>::BYTES;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    static std::atomic<uint64_t> done{0};            // (set once per device)
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    if (!(done.load() & bit)) {
+        e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+        if (e != cudaSuccess) return e;
+        done.fetch_or(bit);
+    }
+    const int64_t tiles = (int64_t)a.tiles_t * a.tiles_c;
+    k<<<(unsigned)(tiles < SMS * PER_SM ? tiles : SMS * PER_SM), NT, SMEM, s>>>(a, pairs);
+    return cudaGetLastError();
+}
+
+// The first sequence of each tile along T: the last one that begins at or before its first token.
+__global__ void __launch_bounds__(NT) tile_table_kernel(const int64_t* cu, int n, int32_t* table, int tiles) {
+    const int tt = blockIdx.x * NT + threadIdx.x;
+    if (tt >= tiles) return;
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (cu[mid] <= (int64_t)tt * CHUNK) lo = mid; else hi = mid - 1;
+    }
+    table[tt] = lo;
 }
 
 }  // namespace
 
-cudaError_t launch_scan(const ScanArgs& a, int io_bf16, cudaStream_t s) {
-    const unsigned grid = (unsigned)((int64_t)a.f.n * ((a.C + NT - 1) / NT));
-    if (io_bf16) scan_kernel<__nv_bfloat16><<<grid, NT, 0, s>>>(a);
-    else scan_kernel<float><<<grid, NT, 0, s>>>(a);
+cudaError_t launch_tile_table(const int64_t* d_cu, int32_t n, int32_t* d_tile, int32_t tiles_t, cudaStream_t s) {
+    tile_table_kernel<<<(unsigned)((tiles_t + NT - 1) / NT), NT, 0, s>>>(d_cu, n, d_tile, tiles_t);
     return cudaGetLastError();
+}
+
+cudaError_t launch_scan(const ScanArgs& a, int io_bf16, cudaStream_t s) {
+    const int es = io_bf16 ? 2 : 4;
+    const int mode = std::max({row_mode(a.x, a.x_s, es), row_mode(a.r, a.r_s, es), row_mode(a.i, a.i_s, es),
+                               a.z ? row_mode(a.z, a.z_s, es) : 0});
+    const bool pairs = row_pairs(a.o, a.C, es);
+    if (!io_bf16) return mode == M16 ? scan<float, M16>(a, pairs, s) : scan<float, M4>(a, pairs, s);
+    return mode == M16 ? scan<__nv_bfloat16, M16>(a, pairs, s)
+         : mode == M4 ? scan<__nv_bfloat16, M4>(a, pairs, s) : scan<__nv_bfloat16, MODD>(a, pairs, s);
 }
 
 }  // namespace glr

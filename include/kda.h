@@ -494,11 +494,12 @@ kda_status kda_glr_prefill(const kda_glr_params* p, const void* x, int64_t x_str
  *   dx, dr, di, dz : device io_dtype, rows strided as the inputs' (so that dr and
  *                  di can be the halves of one row); dz is written where z is
  *                  given, and both are NULL otherwise
- *   dS_in        : device [n_seqs][C] fp32 or NULL (skipped); may be dS_out
+ *   dS_in        : device [n_seqs][C] fp32 or NULL (skipped)
  *   dA_log, dr_bias, di_bias : device [C] fp32, sums over all tokens; the last two
  *                  may be NULL (skipped)
  *   workspace    : as for the prefill, of kda_glr_backward_workspace_bytes()
- * The gradients may not overlap one another or the inputs; each is overwritten.
+ * The gradients may not overlap one another, the inputs or dS_out; each is
+ * overwritten.
  */
 kda_status kda_glr_backward(const kda_glr_params* p, const void* x, int64_t x_stride, const void* r, int64_t r_stride,
                             const void* i, int64_t i_stride, const void* z, int64_t z_stride,

@@ -44,7 +44,7 @@ def prefill(L, p, cu=(0, 64), T=None, ws=FAKE, ws_bytes=1 << 40, null_cu=False, 
 
 
 def backward(L, p, cu=(0, 64), T=None, ws=FAKE, ws_bytes=1 << 40, null_cu=False, **kw):
-    a = tensors("x r i z S_in states do dS_out dx dr di dz dS_in dA_log dr_bias di_bias".split(), kw)
+    a = tensors("x r i z S_in states do dS_out dx dr di dz dS_in dA_log dr_bias di_bias".split(), kw, dS_in=kw.get("dS_in"))
     two = lambda *names: [v for n in names for v in (a[n], a[n + "_s"])]
     return L.kda_glr_backward(ctypes.byref(p), *two(*"xriz"), *batch(cu, T, null_cu), a["S_in"], a["states"], *two("do"),
                               a["dS_out"], *two("dx", "dr", "di", "dz"), a["dS_in"], a["dA_log"], a["dr_bias"], a["di_bias"], ws,
@@ -103,10 +103,10 @@ def test_prefill_refusals(L, kw):
                                        dict(states=None), dict(dA_log=None), dict(do_s=39), dict(dx_s=3), dict(dr_s=39),
                                        dict(di_s=-1), dict(dz_s=39), dict(do=FAKE + 1), dict(dx=FAKE + 1), dict(dz=FAKE + 1),
                                        dict(dS_out=FAKE + 2), dict(dS_in=FAKE + 1), dict(dA_log=FAKE + 2), dict(dr_bias=FAKE + 2),
-                                       dict(di_bias=FAKE + 2), dict(states=FAKE + 2), dict(S_in=FAKE + 2)])
+                                       dict(di_bias=FAKE + 2), dict(states=FAKE + 2), dict(S_in=FAKE + 2), dict(dS_in=FAKE)])
 def test_backward_refusals(L, kw):
-    """dz without z (z=None here) is among them, and z without dz."""
-    assert backward(L, struct(), **kw) == kda.KDA_ERR_INVALID_ARG
+    """dz without z (z=None here) is among them, z without dz, and dS_in in the place of dS_out."""
+    assert backward(L, struct(), **{"dS_in": FAKE + 4096, **kw}) == kda.KDA_ERR_INVALID_ARG
 
 
 def test_too_many_tokens(L):
