@@ -41,10 +41,10 @@ kda_status check_batch(const int64_t* cu, int32_t n_seqs, int64_t total_tokens) 
     return total_tokens > (int64_t)INT32_MAX ? KDA_ERR_UNSUPPORTED : KDA_OK;
 }
 
-// Workspace: error word | ticket | flags | token offsets, rows and tile table of the sequences |
-// the tiles' maps and values | partial sums (backward pass).
+// Workspace: error word | ticket | the tiles' maps and values | token offsets, rows and tile table
+// of the sequences | partial sums (backward pass).
 struct Layout {
-    size_t flags = 0, cu = 0, id = 0, tile = 0, agg = 0, pre = 0, part = 0, total = 0;
+    size_t map = 0, val = 0, cu = 0, id = 0, tile = 0, part = 0, total = 0;
     int64_t tiles_t = 0, tiles_c = 0;
 };
 Layout layout(const kda_glr_params* p, int32_t n_seqs, int64_t total_tokens, bool backward) {
@@ -54,31 +54,32 @@ Layout layout(const kda_glr_params* p, int32_t n_seqs, int64_t total_tokens, boo
     const size_t tiles = (size_t)L.tiles_t * L.tiles_c;
     size_t off = 2 * WS_ALIGN;
     auto take = [&](size_t bytes) { const size_t at = off; off = align_up(off + bytes); return at; };
-    L.flags = take(sizeof(int32_t) * tiles);
+    L.map = take(sizeof(float) * 2 * TILE_C * tiles);
+    L.val = take(sizeof(float) * TILE_C * tiles);
     L.cu = take(sizeof(int64_t) * ((size_t)n_seqs + 1));
     L.id = take(sizeof(int32_t) * (size_t)n_seqs);
     L.tile = take(sizeof(int32_t) * (size_t)L.tiles_t);
-    L.agg = take(sizeof(float) * 2 * TILE_C * tiles);
-    L.pre = take(sizeof(float) * TILE_C * tiles);
     if (backward) L.part = take(sizeof(float) * 3 * (size_t)L.tiles_t * p->channels);
     L.total = off;
     return L;
 }
 
-// What the two walks share: the sequences with tokens, the workspace's parts, a cleared error
-// word, ticket and flags.
+// What the two walks share: the sequences with tokens, and the workspace's parts, with ticket, maps and
+// values set to EMPTY (all ones).  The first tile clears the error word.
 cudaError_t prepare(const kda_glr_params* p, const int64_t* cu, int32_t n_seqs, unsigned char* ws, const Layout& L,
                     ScanArgs* a, cudaStream_t s) {
     a->status = reinterpret_cast<int32_t*>(ws);
     a->ticket = reinterpret_cast<uint32_t*>(ws + WS_ALIGN);
-    a->flags = reinterpret_cast<int32_t*>(ws + L.flags);
-    a->agg = reinterpret_cast<float*>(ws + L.agg);
-    a->pre = reinterpret_cast<float*>(ws + L.pre);
+    a->map = reinterpret_cast<float*>(ws + L.map);
+    a->val = reinterpret_cast<float*>(ws + L.val);
     a->part = reinterpret_cast<float*>(ws + L.part);
     a->tiles_t = (int32_t)L.tiles_t;
     a->tiles_c = (int32_t)L.tiles_c;
-    cudaError_t e = cudaMemsetAsync(ws, 0, L.flags + sizeof(int32_t) * (size_t)(L.tiles_t * L.tiles_c), s);
-    if (e != cudaSuccess || L.tiles_t == 0) return e;
+    if (L.tiles_t == 0) return cudaMemsetAsync(ws, 0, WS_ALIGN, s);
+    // one place along T waits for nothing: the ticket alone
+    const size_t to = L.tiles_t > 1 ? L.val + sizeof(float) * TILE_C * (size_t)(L.tiles_t * L.tiles_c) : 2 * WS_ALIGN;
+    cudaError_t e = cudaMemsetAsync(ws + WS_ALIGN, 0xff, to - WS_ALIGN, s);
+    if (e != cudaSuccess) return e;
     Sequences& f = a->f;
     f.d_cu = reinterpret_cast<int64_t*>(ws + L.cu);
     f.d_id = reinterpret_cast<int32_t*>(ws + L.id);

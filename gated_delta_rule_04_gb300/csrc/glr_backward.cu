@@ -13,6 +13,7 @@
 // registers between the sweeps.  Sums over the tokens go to the workspace by tile
 // and are added up in order by a second kernel.
 #include <atomic>
+#include <type_traits>
 
 #include "glr_tile.cuh"
 
@@ -25,50 +26,49 @@ enum { OUT_X = 1, OUT_R = 2, OUT_I = 4, OUT_Z = 8 };   // gradients whose rows t
 template <typename TI, int MODE, int STAGES, int PER_SM>
 __global__ void __launch_bounds__(NT, PER_SM) backward_kernel(const __grid_constant__ ScanArgs g, int pairs) {
     using R = Rows<TI, MODE>;
-    extern __shared__ __align__(128) unsigned char tiles_smem[];   // [STAGES][x, r, i, do, z]
+    extern __shared__ __align__(128) unsigned char rows_smem[];    // [WARPS][STAGES][x, r, i, do, z]
     __shared__ uint32_t tk[STAGES];
-    __shared__ float2 sA[WARPS][32], sB[WARPS][32], sAr[WARPS][32], sBr[WARPS][32], sIn[32];
+    __shared__ float2 sA[2][WARPS][32], sB[2][WARPS][32], sAr[2][WARPS][32], sBr[2][WARPS][32], sIn[2][32];
     __shared__ float2 sums[3][WARPS][32];
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const uint32_t tiles = (uint32_t)g.tiles_t * (uint32_t)g.tiles_c;
+    unsigned char* const mine = rows_smem + warp * STAGES * 5 * R::BYTES;
+    const uint32_t mine_u = ptx::smem_u32(mine);
     auto issue = [&](int stage, uint32_t tile) {
         if (tile < tiles) {
-            const int64_t t0 = (int64_t)(g.tiles_t - 1 - (int)(tile / g.tiles_c)) * CHUNK;
+            const int64_t t = (int64_t)(g.tiles_t - 1 - (int)(tile / g.tiles_c)) * CHUNK + warp * SUB;
             const int c0 = (int)(tile % g.tiles_c) * TILE_C;
-            unsigned char* s = tiles_smem + stage * 5 * R::BYTES;
-            R::load(s, g.x, g.x_s, t0, c0, g);
-            R::load(s + R::BYTES, g.r, g.r_s, t0, c0, g);
-            R::load(s + 2 * R::BYTES, g.i, g.i_s, t0, c0, g);
-            R::load(s + 3 * R::BYTES, g.d_o, g.do_s, t0, c0, g);
-            if (g.z) R::load(s + 4 * R::BYTES, g.z, g.z_s, t0, c0, g);
+            const int rows = (int)min((int64_t)SUB, g.T - t), cols = min(TILE_C, g.C - c0);
+            const uint32_t s = mine_u + stage * 5 * R::BYTES;
+            R::load(s, g.x, g.x_s, t, c0, rows, cols);
+            R::load(s + R::BYTES, g.r, g.r_s, t, c0, rows, cols);
+            R::load(s + 2 * R::BYTES, g.i, g.i_s, t, c0, rows, cols);
+            R::load(s + 3 * R::BYTES, g.d_o, g.do_s, t, c0, rows, cols);
+            if (g.z) R::load(s + 4 * R::BYTES, g.z, g.z_s, t, c0, rows, cols);
         }
         ptx::cp_async_commit();
     };
     if (tid == 0)
-        for (int k = 0; k < STAGES; ++k) tk[k] = atomicAdd(g.ticket, 1u);
+        for (int k = 0; k < STAGES; ++k) tk[k] = next_ticket(g);
     __syncthreads();
+    if (tk[0] == 0 && tid == 0) *g.status = ERR_NONE;
     for (int k = 0; k < STAGES; ++k) issue(k, tk[k]);
 
-    for (int stage = 0;; stage = stage + 1 == STAGES ? 0 : stage + 1) {
+    int buf = 0;
+    for (int stage = 0;; stage = stage + 1 == STAGES ? 0 : stage + 1, buf ^= 1) {
         const uint32_t tile = tk[stage];
         if (tile >= tiles) break;
         const int order = tile / g.tiles_c, tt = g.tiles_t - 1 - order, tc = tile % g.tiles_c;
         const int64_t t = (int64_t)tt * CHUNK + warp * SUB;
-        const int c0 = tc * TILE_C, c = c0 + 2 * lane;
-        auto pair_of = [&](const float* p, size_t row) {
-            float2 h = f2(0.f);
-            if (p && c < g.C) h.x = p[row * g.C + c];
-            if (p && c + 1 < g.C) h.y = p[row * g.C + c + 1];
-            return h;
-        };
+        const int c0 = tc * TILE_C, c = c0 + 2 * lane, rows = (int)min((int64_t)SUB, g.T - t), left = g.C - c;
         const Gate k = load_gate(g, c);
-        float2 h = pair_of(g.states, tt);
+        float2 h = pair_at(g.states, tt, c, g.C);
         const Borders bd = borders(g, tt, t);
         auto seq_of = [&](int j) { return (size_t)seq_id(g.f, bd.seq + __popc((bd.start >> 1) & ((1u << j) - 1))); };
         asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
-        __syncthreads();
+        __syncwarp();
 
-        const unsigned char* s = tiles_smem + stage * 5 * R::BYTES + warp * SUB * R::PITCH;
+        const unsigned char* s = mine + stage * 5 * R::BYTES;
         const typename R::Odd ox = R::odd(g.x, g.x_s, t, c0), orr = R::odd(g.r, g.r_s, t, c0), oi = R::odd(g.i, g.i_s, t, c0),
                               od = R::odd(g.d_o, g.do_s, t, c0), oz = R::odd(g.z, g.z_s, t, c0);
         auto x_of = [&](int j) { return R::get(s, j, ox); };
@@ -77,101 +77,128 @@ __global__ void __launch_bounds__(NT, PER_SM) backward_kernel(const __grid_const
         // of each token: a, E = m v, w (with 1 - w), 1 - v, sigmoid(z), and D = dA_log / g
         float2 a[SUB], E[SUB], ww[SUB], v_[SUB], e[SUB], D[SUB];
         float2 A = f2(1.f), B = f2(0.f);
-#pragma unroll
-        for (int j = 0; j < SUB; ++j) {
+        auto token = [&](int j, auto wide) {
             float2 rest;
             const float2 w = sigmoid_of(fma2(R::get(s + R::BYTES, j, orr), f2(-LOG2E), k.rb), rest);
             const float2 v = sigmoid_of(fma2(R::get(s + 2 * R::BYTES, j, oi), f2(-LOG2E), k.ib), v_[j]);
             ww[j] = smaller(w, rest);
-            if (g.z) e[j] = sigmoid_of(mul2(z_of(j), f2(-LOG2E)));
             float2 m2;
             const float2 la = mul2(k.ea, w);
-            decay_of(la, a[j], m2);
+            decay_of<decltype(wide)::value>(la, a[j], m2);
             const float2 im = inv_root(m2);
             E[j] = mul2(mul2(m2, im), v);
             D[j] = mul2(mul2(mul2(a[j], a[j]), mul2(la, im)), v);   // (a / m)^2 b la / x
-            const float2 b = mul2(E[j], x_of(j));
-            if (bd.start >> j & 1) {
-                A = f2(-1.f);
-                B = fma2(a[j], pair_of(g.S_in, seq_of(j)), b);
-            } else {
-                A = A.x < 0.f ? A : mul2(A, a[j]);
-                B = fma2(a[j], B, b);
-            }
-        }
-        sA[warp][lane] = A;
-        sB[warp][lane] = B;
-        auto G_of = [&](int j) { return g.z ? mul2(do_of(j), mul2(z_of(j), e[j])) : do_of(j); };
-        A = f2(1.f);
-        B = f2(0.f);
+        };
+        if (any_wide(k)) {
 #pragma unroll
-        for (int j = SUB - 1; j >= 0; --j) {
-            if (bd.end >> j & 1) {
-                A = f2(-1.f);
-                B = pair_of(g.dS_out, seq_of(j));
-            } else if (A.x >= 0.f) {
-                A = mul2(A, a[j]);
-            }
-            B = mul2(a[j], add2(G_of(j), B));
+            for (int j = 0; j < SUB; ++j) token(j, std::true_type{});
+        } else {
+#pragma unroll
+            for (int j = 0; j < SUB; ++j) token(j, std::false_type{});
         }
-        sAr[warp][lane] = A;
-        sBr[warp][lane] = B;
+        if (g.z) {
+#pragma unroll
+            for (int j = 0; j < SUB; ++j) e[j] = sigmoid_of(mul2(z_of(j), f2(-LOG2E)));
+        }
+        auto G_of = [&](int j) { return g.z ? mul2(do_of(j), mul2(z_of(j), e[j])) : do_of(j); };
+        float2 Ar = f2(1.f), Br = f2(0.f);
+        if ((bd.start | bd.end) == 0) {
+#pragma unroll
+            for (int j = 0; j < SUB; ++j) {
+                A = mul2(A, a[j]);
+                B = fma2(a[j], B, mul2(E[j], x_of(j)));
+            }
+            Ar = A;
+#pragma unroll
+            for (int j = SUB - 1; j >= 0; --j) Br = mul2(a[j], add2(G_of(j), Br));
+        } else {
+#pragma unroll
+            for (int j = 0; j < SUB; ++j) {
+                const float2 b = mul2(E[j], x_of(j));
+                if (bd.start >> j & 1) {
+                    A = f2(-1.f);
+                    B = fma2(a[j], pair_at(g.S_in, seq_of(j), c, g.C), b);
+                } else {
+                    A = A.x < 0.f ? A : mul2(A, a[j]);
+                    B = fma2(a[j], B, b);
+                }
+            }
+#pragma unroll
+            for (int j = SUB - 1; j >= 0; --j) {
+                if (bd.end >> j & 1) {
+                    Ar = f2(-1.f);
+                    Br = pair_at(g.dS_out, seq_of(j), c, g.C);
+                } else if (Ar.x >= 0.f) {
+                    Ar = mul2(Ar, a[j]);
+                }
+                Br = mul2(a[j], add2(G_of(j), Br));
+            }
+        }
+        sA[buf][warp][lane] = A;
+        sB[buf][warp][lane] = B;
+        sAr[buf][warp][lane] = Ar;
+        sBr[buf][warp][lane] = Br;
         __syncthreads();
         if (warp == 0) {
-            A = sAr[WARPS - 1][lane];
-            B = sBr[WARPS - 1][lane];
+            Ar = sAr[buf][WARPS - 1][lane];
+            Br = sBr[buf][WARPS - 1][lane];
+#pragma unroll
             for (int u = WARPS - 2; u >= 0; --u) {
-                const float2 Aw = sAr[u][lane], Bw = sBr[u][lane];
-                B = apply(Aw, Bw, B);
-                A = Aw.x < 0.f ? Aw : A.x < 0.f ? A : mul2(A, Aw);
+                const float2 Aw = sAr[buf][u][lane], Bw = sBr[buf][u][lane];
+                Br = apply(Aw, Bw, Br);
+                Ar = Aw.x < 0.f ? Aw : Ar.x < 0.f ? Ar : mul2(Ar, Aw);
             }
-            sIn[lane] = walk(g, order, tc, A, B);
+            sIn[buf][lane] = walk(g, order, tc, Ar, Br);
         } else if (tid == 32) {
-            tk[stage] = atomicAdd(g.ticket, 1u);
+            tk[stage] = next_ticket(g);
         }
-        for (int u = 0; u < warp; ++u) h = apply(sA[u][lane], sB[u][lane], h);
+        for (int u = 0; u < warp; ++u) h = apply(sA[buf][u][lane], sB[buf][u][lane], h);
+        TI* dz = g.z ? static_cast<TI*>(g.dz) + t * g.dz_s + c : nullptr;
 #pragma unroll
         for (int j = 0; j < SUB; ++j) {
-            if (bd.start >> j & 1) h = pair_of(g.S_in, seq_of(j));
+            if (bd.start >> j & 1) h = pair_at(g.S_in, seq_of(j), c, g.C);
             const float2 x = x_of(j), ah = mul2(a[j], h);
             D[j] = fma2(ah, mul2(k.ea, sigmoid_from(ww[j])), neg2(mul2(D[j], x)));
             h = fma2(E[j], x, ah);
-            if (g.z && t + j < g.T) {
-                const float2 z = z_of(j), s1 = add2(f2(1.f), neg2(e[j]));
-                put<TI>(g.dz, g.dz_s, t + j, c, g.C, pairs & OUT_Z, mul2(mul2(do_of(j), h), mul2(e[j], fma2(z, s1, f2(1.f)))));
+            if (g.z && j < rows) {
+                const float2 z = z_of(j), s1 = fma2(e[j], f2(-1.f), f2(1.f));
+                put(dz + j * g.dz_s, left, (pairs & OUT_Z) && left > 1, mul2(mul2(do_of(j), h), mul2(e[j], fma2(z, s1, f2(1.f)))));
             }
         }
         __syncthreads();
-        float2 carry = sIn[lane], sa = f2(0.f), sr = f2(0.f), si = f2(0.f);
-        for (int u = WARPS - 1; u > warp; --u) carry = apply(sAr[u][lane], sBr[u][lane], carry);
+        float2 carry = sIn[buf][lane], sa = f2(0.f), sr = f2(0.f), si = f2(0.f);
+        for (int u = WARPS - 1; u > warp; --u) carry = apply(sAr[buf][u][lane], sBr[buf][u][lane], carry);
+        TI *dx = static_cast<TI*>(g.dx) + t * g.dx_s + c, *dr = static_cast<TI*>(g.dr) + t * g.dr_s + c,
+           *di = static_cast<TI*>(g.di) + t * g.di_s + c;
+        const bool px = (pairs & OUT_X) && left > 1, pr = (pairs & OUT_R) && left > 1, pi = (pairs & OUT_I) && left > 1;
 #pragma unroll
         for (int j = SUB - 1; j >= 0; --j) {
-            if (bd.end >> j & 1) carry = pair_of(g.dS_out, seq_of(j));
-            const float2 gt = add2(G_of(j), carry), dx = mul2(gt, E[j]);
+            if (bd.end >> j & 1) carry = pair_at(g.dS_out, seq_of(j), c, g.C);
+            const float2 gt = add2(G_of(j), carry), gx = mul2(gt, E[j]);
             carry = mul2(a[j], gt);
-            const float2 di = mul2(mul2(dx, x_of(j)), v_[j]);
-            const float2 dA = mul2(gt, D[j]), dr = mul2(dA, rest_from(ww[j]));
-            if (t + j < g.T) {
-                put<TI>(g.dx, g.dx_s, t + j, c, g.C, pairs & OUT_X, dx);
-                put<TI>(g.dr, g.dr_s, t + j, c, g.C, pairs & OUT_R, dr);
-                put<TI>(g.di, g.di_s, t + j, c, g.C, pairs & OUT_I, di);
-                sa = add2(sa, dA);
-                sr = add2(sr, dr);
-                si = add2(si, di);
+            const float2 gi = mul2(mul2(gx, x_of(j)), v_[j]);
+            const float2 gA = mul2(gt, D[j]), gr = mul2(gA, rest_from(ww[j]));
+            if (j < rows) {
+                put(dx + j * g.dx_s, left, px, gx);
+                put(dr + j * g.dr_s, left, pr, gr);
+                put(di + j * g.di_s, left, pi, gi);
+                sa = add2(sa, gA);
+                sr = add2(sr, gr);
+                si = add2(si, gi);
             }
-            if (g.dS_in && (bd.start >> j & 1)) put<float>(g.dS_in, g.C, seq_of(j), c, g.C, false, carry);
+            if (g.dS_in && (bd.start >> j & 1)) put(g.dS_in + seq_of(j) * g.C + c, left, false, carry);
         }
+        issue(stage, tk[stage]);                     // (the warp has read its rows)
         sums[0][warp][lane] = sa;
         sums[1][warp][lane] = sr;
         sums[2][warp][lane] = si;
-        __syncthreads();                             // the tile's rows and maps are read
-        issue(stage, tk[stage]);
+        __syncthreads();
         if (tid < 96) {
             const int q = tid / 32;
             float2 sum = sums[q][0][lane];
 #pragma unroll
             for (int u = 1; u < WARPS; ++u) sum = add2(sum, sums[q][u][lane]);
-            put<float>(g.part, g.C, (int64_t)tt * 3 + q, c, g.C, false, sum);
+            put(g.part + ((size_t)tt * 3 + q) * g.C + c, left, false, sum);
         }
     }
 }
@@ -209,7 +236,7 @@ template <typename TI, int MODE>
 cudaError_t backward(const ScanArgs& a, int pairs, cudaStream_t s) {
     constexpr int STAGES = sizeof(TI) == 2 ? 2 : 1, PER_SM = 2;
     auto k = backward_kernel<TI, MODE, STAGES, PER_SM>;
-    constexpr int SMEM = STAGES * 5 * Rows<TI, MODE>::BYTES;
+    constexpr int SMEM = WARPS * STAGES * 5 * Rows<TI, MODE>::BYTES;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;

@@ -44,9 +44,8 @@ struct ScanArgs {
     // workspace
     int32_t* status;                 // error word
     uint32_t* ticket;                // the next tile to be taken
-    int32_t* flags;                  // [tiles along T][tiles along C]
-    float* agg;                      // [tiles along T][tiles along C][TILE_C][2]
-    float* pre;                      // [tiles along T][tiles along C][TILE_C]
+    float* map;                      // [tiles along T][tiles along C][TILE_C][2]
+    float* val;                      // [tiles along T][tiles along C][TILE_C]
     float* part;                     // [tiles along T][3][C]: partial sums of the parameters' gradients
     int32_t tiles_t, tiles_c;
 };

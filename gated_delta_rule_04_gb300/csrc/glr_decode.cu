@@ -97,9 +97,9 @@ __global__ void __launch_bounds__(NT) token_kernel(const __grid_constant__ Token
         float2 o[PAIRS];
 #pragma unroll
         for (int p = 0; p < PAIRS; ++p) {
-            const Step s = step_of(k[p], X::pair(xj, p), X::pair(rj, p), X::pair(ij, p));
+            const Step s = step_of<true>(k[p], X::pair(xj, p), X::pair(rj, p), X::pair(ij, p));
             h[p] = fma2(s.a, h[p], s.b);
-            o[p] = g.z ? gated(h[p], X::pair(zj, p)) : h[p];
+            o[p] = g.z ? mul2(h[p], silu(X::pair(zj, p))) : h[p];
         }
         if (g.o) X::store(g.o, here * g.C + c, o);
     }

@@ -70,23 +70,35 @@ template <typename Args> __device__ __forceinline__ Gate load_gate(const Args& g
 }
 
 // A token's decay a = exp(la) and m^2 = 1 - a^2, for la <= 0.  Near 1 both come from
-// q = exp(la) - 1 by its Taylor polynomial (relative error y^7 / 8! < 2e-9 at 1/4):
+// q = exp(la) - 1 by its Taylor polynomial (relative error la^8 / 9! < 1.1e-8 at 1/2):
 // a = 1 + q is then rounded to nearest, where an exponential's error has one sign that a
-// state adds up at every token, and m^2 = -q (2 + q) keeps its digits.
-__device__ __forceinline__ void decay_of(float2 la, float2& a, float2& m2) {
-    float2 p = fma2(la, f2(1.f / 7), f2(1.f));
-    p = fma2(mul2(la, f2(1.f / 6)), p, f2(1.f));
-    p = fma2(mul2(la, f2(1.f / 5)), p, f2(1.f));
-    p = fma2(mul2(la, f2(1.f / 4)), p, f2(1.f));
-    p = fma2(mul2(la, f2(1.f / 3)), p, f2(1.f));
-    p = fma2(mul2(la, f2(1.f / 2)), p, f2(1.f));
-    const float2 q = mul2(la, p), qa = add2(q, f2(1.f)), qm = mul2(neg2(q), add2(q, f2(2.f)));
-    const float2 t = mul2(la, f2(LOG2E)), e = make_float2(ex2(t.x), ex2(t.y)), em = fma2(neg2(e), e, f2(1.f));
-    a = make_float2(la.x < -0.25f ? e.x : qa.x, la.y < -0.25f ? e.y : qa.y);
-    m2 = make_float2(la.x < -0.25f ? em.x : qm.x, la.y < -0.25f ? em.y : qm.y);
+// state adds up at every token, and m^2 = -q (2 + q) keeps its digits.  WIDE: la may
+// lie below -1/2; a channel whose exp(A_log) is at most 1/2 never gets there.
+constexpr float NEAR = 0.5f;
+template <bool WIDE> __device__ __forceinline__ void decay_of(float2 la, float2& a, float2& m2) {
+    float2 p = fma2(la, f2(-1.f / 40320), f2(-1.f / 5040));     // (of -q)
+    p = fma2(la, p, f2(-1.f / 720));
+    p = fma2(la, p, f2(-1.f / 120));
+    p = fma2(la, p, f2(-1.f / 24));
+    p = fma2(la, p, f2(-1.f / 6));
+    p = fma2(la, p, f2(-1.f / 2));
+    p = fma2(la, p, f2(-1.f));
+    const float2 q = mul2(la, p);
+    a = fma2(q, f2(-1.f), f2(1.f));
+    m2 = mul2(q, fma2(q, f2(-1.f), f2(2.f)));
+    if (WIDE) {
+        const float2 t = mul2(la, f2(LOG2E)), e = make_float2(ex2(t.x), ex2(t.y)), em = fma2(mul2(e, f2(-1.f)), e, f2(1.f));
+        a = make_float2(la.x < -NEAR ? e.x : a.x, la.y < -NEAR ? e.y : a.y);
+        m2 = make_float2(la.x < -NEAR ? em.x : m2.x, la.y < -NEAR ? em.y : m2.y);
+    }
 }
 // 1 / m, finite at m = 0 (there m2 / m is 0)
-__device__ __forceinline__ float2 inv_root(float2 m2) { return make_float2(rsq(fmaxf(m2.x, 1e-36f)), rsq(fmaxf(m2.y, 1e-36f))); }
+__device__ __forceinline__ float2 inv_root(float2 m2) {
+    const float2 x = add2(m2, f2(1e-36f));
+    return make_float2(rsq(x.x), rsq(x.y));
+}
+// Whether any of the warp's channels may have a decay's logarithm below -NEAR.
+__device__ __forceinline__ bool any_wide(const Gate& k) { return __any_sync(0xffffffffu, !(k.ea.x >= -NEAR && k.ea.y >= -NEAR)); }
 
 // h -> A h + B of a run of tokens; A < 0 marks a run that starts anew (a decay never is).
 __device__ __forceinline__ float apply(float A, float B, float h) { return A < 0.f ? B : fmaf(A, h, B); }
@@ -96,15 +108,15 @@ __device__ __forceinline__ float2 apply(float2 A, float2 B, float2 h) { return m
 struct Step {
     float2 a, b;
 };
-__device__ __forceinline__ Step step_of(const Gate& k, float2 x, float2 r, float2 i) {
+template <bool WIDE> __device__ __forceinline__ Step step_of(const Gate& k, float2 x, float2 r, float2 i) {
     const float2 w = sigmoid_of(fma2(r, f2(-LOG2E), k.rb)), v = sigmoid_of(fma2(i, f2(-LOG2E), k.ib));
     Step s;
     float2 m2;
-    decay_of(mul2(k.ea, w), s.a, m2);
+    decay_of<WIDE>(mul2(k.ea, w), s.a, m2);
     s.b = mul2(mul2(mul2(m2, inv_root(m2)), v), x);
     return s;
 }
-__device__ __forceinline__ float2 gated(float2 h, float2 z) { return mul2(h, mul2(z, sigmoid_of(mul2(z, f2(-LOG2E))))); }
+__device__ __forceinline__ float2 silu(float2 z) { return mul2(z, sigmoid_of(mul2(z, f2(-LOG2E)))); }
 
 }  // namespace glr
 }  // namespace kda

@@ -9,6 +9,7 @@
 // a token and the output gate.  Sequences lie anywhere in the tiles: a token
 // that begins one starts its run anew from S_in.
 #include <atomic>
+#include <type_traits>
 
 #include "glr_tile.cuh"
 
@@ -19,105 +20,133 @@ namespace {
 template <typename TI, int MODE, int STAGES, int PER_SM>
 __global__ void __launch_bounds__(NT, PER_SM) scan_kernel(const __grid_constant__ ScanArgs g, bool pairs) {
     using R = Rows<TI, MODE>;
-    extern __shared__ __align__(128) unsigned char tiles_smem[];   // [STAGES][x, r, i, z]
+    extern __shared__ __align__(128) unsigned char rows_smem[];    // [WARPS][STAGES][x, r, i, z]
     __shared__ uint32_t tk[STAGES];
-    __shared__ float2 sA[WARPS][32], sB[WARPS][32], sIn[32];
+    __shared__ float2 sA[2][WARPS][32], sB[2][WARPS][32], sIn[2][32];
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const uint32_t tiles = (uint32_t)g.tiles_t * (uint32_t)g.tiles_c;
+    unsigned char* const mine = rows_smem + warp * STAGES * 4 * R::BYTES;
+    const uint32_t mine_u = ptx::smem_u32(mine);
     auto issue = [&](int stage, uint32_t tile) {
         if (tile < tiles) {
-            const int64_t t0 = (int64_t)(tile / g.tiles_c) * CHUNK;
+            const int64_t t = (int64_t)(tile / g.tiles_c) * CHUNK + warp * SUB;
             const int c0 = (int)(tile % g.tiles_c) * TILE_C;
-            unsigned char* s = tiles_smem + stage * 4 * R::BYTES;
-            R::load(s, g.x, g.x_s, t0, c0, g);
-            R::load(s + R::BYTES, g.r, g.r_s, t0, c0, g);
-            R::load(s + 2 * R::BYTES, g.i, g.i_s, t0, c0, g);
-            if (g.z) R::load(s + 3 * R::BYTES, g.z, g.z_s, t0, c0, g);
+            const int rows = (int)min((int64_t)SUB, g.T - t), cols = min(TILE_C, g.C - c0);
+            const uint32_t s = mine_u + stage * 4 * R::BYTES;
+            R::load(s, g.x, g.x_s, t, c0, rows, cols);
+            R::load(s + R::BYTES, g.r, g.r_s, t, c0, rows, cols);
+            R::load(s + 2 * R::BYTES, g.i, g.i_s, t, c0, rows, cols);
+            if (g.z) R::load(s + 3 * R::BYTES, g.z, g.z_s, t, c0, rows, cols);
         }
         ptx::cp_async_commit();
     };
     if (tid == 0)
-        for (int k = 0; k < STAGES; ++k) tk[k] = atomicAdd(g.ticket, 1u);
+        for (int k = 0; k < STAGES; ++k) tk[k] = next_ticket(g);
     __syncthreads();
+    if (tk[0] == 0 && tid == 0) *g.status = ERR_NONE;
     for (int k = 0; k < STAGES; ++k) issue(k, tk[k]);
 
-    for (int stage = 0;; stage = stage + 1 == STAGES ? 0 : stage + 1) {
+    int buf = 0;
+    for (int stage = 0;; stage = stage + 1 == STAGES ? 0 : stage + 1, buf ^= 1) {
         const uint32_t tile = tk[stage];
         if (tile >= tiles) break;                    // (tickets only grow)
         const int tt = tile / g.tiles_c, tc = tile % g.tiles_c;
         const int64_t t = (int64_t)tt * CHUNK + warp * SUB;
-        const int c0 = tc * TILE_C, c = c0 + 2 * lane;
+        const int c0 = tc * TILE_C, c = c0 + 2 * lane, rows = (int)min((int64_t)SUB, g.T - t);
         const Gate k = load_gate(g, c);
         const Borders bd = borders(g, tt, t);
-        auto seq_of = [&](int j) { return bd.seq + __popc((bd.start >> 1) & ((1u << j) - 1)); };
-        auto state_in = [&](int j) {
-            float2 h = f2(0.f);
-            if (g.S_in) {
-                const float* p = g.S_in + (size_t)seq_id(g.f, seq_of(j)) * g.C + c;
-                if (c < g.C) h.x = p[0];
-                if (c + 1 < g.C) h.y = p[1];
-            }
-            return h;
-        };
+        auto seq_of = [&](int j) { return (size_t)seq_id(g.f, bd.seq + __popc((bd.start >> 1) & ((1u << j) - 1))); };
         asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
-        __syncthreads();
+        __syncwarp();
 
-        const unsigned char* s = tiles_smem + stage * 4 * R::BYTES;
-        const typename R::Odd ox = R::odd(g.x, g.x_s, t, c0), orr = R::odd(g.r, g.r_s, t, c0), oi = R::odd(g.i, g.i_s, t, c0),
-                              oz = R::odd(g.z, g.z_s, t, c0);
+        const unsigned char* s = mine + stage * 4 * R::BYTES;
         float2 a[SUB], b[SUB], A = f2(1.f), B = f2(0.f), first = f2(0.f);
-        s += warp * SUB * R::PITCH;
-#pragma unroll
-        for (int j = 0; j < SUB; ++j) {
-            const Step st = step_of(k, R::get(s, j, ox), R::get(s + R::BYTES, j, orr), R::get(s + 2 * R::BYTES, j, oi));
+        const typename R::Odd ox = R::odd(g.x, g.x_s, t, c0), orr = R::odd(g.r, g.r_s, t, c0), oi = R::odd(g.i, g.i_s, t, c0);
+        auto token = [&](int j, auto wide) {
+            const Step st = step_of<decltype(wide)::value>(k, R::get(s, j, ox), R::get(s + R::BYTES, j, orr),
+                                                           R::get(s + 2 * R::BYTES, j, oi));
             a[j] = st.a;
             b[j] = st.b;
-            if (bd.start >> j & 1) {
-                const float2 h = state_in(j);        // (S_out, written behind the barriers, may be S_in)
-                if (j == 0) first = h;
-                b[j] = fma2(a[j], h, b[j]);
-                A = f2(-1.f);
-                B = b[j];
-            } else {
-                A = A.x < 0.f ? A : mul2(A, a[j]);
+        };
+        if (any_wide(k)) {
+#pragma unroll
+            for (int j = 0; j < SUB; ++j) token(j, std::true_type{});
+        } else {
+#pragma unroll
+            for (int j = 0; j < SUB; ++j) token(j, std::false_type{});
+        }
+        if (bd.start == 0) {
+#pragma unroll
+            for (int j = 0; j < SUB; ++j) {
+                A = mul2(A, a[j]);
                 B = fma2(a[j], B, b[j]);
             }
+        } else {
+#pragma unroll
+            for (int j = 0; j < SUB; ++j) {
+                if (bd.start >> j & 1) {
+                    const float2 h = pair_at(g.S_in, seq_of(j), c, g.C);   // (S_out, written behind the barriers, may be S_in)
+                    if (j == 0) first = h;
+                    b[j] = fma2(a[j], h, b[j]);
+                    A = f2(-1.f);
+                    B = b[j];
+                } else {
+                    A = A.x < 0.f ? A : mul2(A, a[j]);
+                    B = fma2(a[j], B, b[j]);
+                }
+            }
         }
-        sA[warp][lane] = A;
-        sB[warp][lane] = B;
+        sA[buf][warp][lane] = A;
+        sB[buf][warp][lane] = B;
         __syncthreads();
         if (warp == 0) {
+#pragma unroll
             for (int w = 1; w < WARPS; ++w) {
-                const float2 Aw = sA[w][lane], Bw = sB[w][lane];
+                const float2 Aw = sA[buf][w][lane], Bw = sB[buf][w][lane];
                 B = apply(Aw, Bw, B);
                 A = Aw.x < 0.f ? Aw : A.x < 0.f ? A : mul2(A, Aw);
             }
-            sIn[lane] = walk(g, tt, tc, A, B);
+            sIn[buf][lane] = walk(g, tt, tc, A, B);
         } else if (tid == 32) {
-            tk[stage] = atomicAdd(g.ticket, 1u);
+            tk[stage] = next_ticket(g);
+        }
+        float2 gate[SUB];
+        if (g.z) {
+            const typename R::Odd oz = R::odd(g.z, g.z_s, t, c0);
+#pragma unroll
+            for (int j = 0; j < SUB; ++j) gate[j] = silu(R::get(s + 3 * R::BYTES, j, oz));
         }
         __syncthreads();
-        float2 h = sIn[lane];
-        if (g.states && warp == 0) put<float>(g.states, g.C, tt, c, g.C, false, bd.start & 1 ? first : h);
-        for (int w = 0; w < warp; ++w) h = apply(sA[w][lane], sB[w][lane], h);
+        issue(stage, tk[stage]);                     // (the warp has read its rows)
+        float2 h = sIn[buf][lane];
+        if (g.states && warp == 0) put(g.states + (size_t)tt * g.C + c, g.C - c, false, bd.start & 1 ? first : h);
+        for (int w = 0; w < warp; ++w) h = apply(sA[buf][w][lane], sB[buf][w][lane], h);
+        TI* o = static_cast<TI*>(g.o) + t * g.C + c;
+        const bool pair = pairs && c + 1 < g.C;
+        if ((bd.start | bd.end) == 0 && rows == SUB) {
 #pragma unroll
-        for (int j = 0; j < SUB; ++j) {
-            h = bd.start >> j & 1 ? b[j] : fma2(a[j], h, b[j]);
-            float2 o = h;
-            if (g.z) o = gated(o, R::get(s + 3 * R::BYTES, j, oz));
-            if (t + j < g.T) put<TI>(g.o, g.C, t + j, c, g.C, pairs, o);
-            if (bd.end >> j & 1) put<float>(g.S_out, g.C, seq_id(g.f, seq_of(j)), c, g.C, false, h);
+            for (int j = 0; j < SUB; ++j) {
+                h = fma2(a[j], h, b[j]);
+                put(o, g.C - c, pair, g.z ? mul2(h, gate[j]) : h);
+                o += g.C;
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < SUB; ++j) {
+                h = bd.start >> j & 1 ? b[j] : fma2(a[j], h, b[j]);
+                if (j < rows) put(o, g.C - c, pair, g.z ? mul2(h, gate[j]) : h);
+                if (bd.end >> j & 1) put(g.S_out + seq_of(j) * g.C + c, g.C - c, false, h);
+                o += g.C;
+            }
         }
-        __syncthreads();                             // the tile's rows and maps are read
-        issue(stage, tk[stage]);
     }
 }
 
 template <typename TI, int MODE>
 cudaError_t scan(const ScanArgs& a, bool pairs, cudaStream_t s) {
-    constexpr int STAGES = sizeof(TI) == 2 ? 3 : 1, PER_SM = sizeof(TI) == 2 ? 2 : 3;
+    constexpr int STAGES = sizeof(TI) == 2 ? 2 : 1, PER_SM = 3;
     auto k = scan_kernel<TI, MODE, STAGES, PER_SM>;
-    constexpr int SMEM = STAGES * 4 * Rows<TI, MODE>::BYTES;
+    constexpr int SMEM = WARPS * STAGES * 4 * Rows<TI, MODE>::BYTES;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;

@@ -18,53 +18,67 @@ static_assert(TILE_C == 64 && SUB == 8, "lanes hold channel pairs, warps 8 token
 
 // ---- tiles in shared memory -------------------------------------------------------------
 // How rows are copied: 16 bytes at a time, 4 bytes at a time, or (16-bit elements whose rows
-// start on odd ones) 4 bytes at a time from the word that holds the row's first element.
+// may start on odd ones) 4 bytes at a time from the word that holds the row's first element.
 enum Mode { M16 = 0, M4 = 1, MODD = 2 };
 
+// A warp's 8 rows of one tensor.  Each warp copies, waits for and reads its own.
 template <typename TI, int MODE> struct Rows {
-    static constexpr int PITCH = TILE_C * (int)sizeof(TI) + (MODE == MODD ? 4 : 0);
-    static constexpr int BYTES = CHUNK * PITCH;
+    static constexpr int ES = sizeof(TI);
+    static constexpr int PITCH = TILE_C * ES + (MODE == MODD ? 4 : 0);
+    static constexpr int BYTES = SUB * PITCH;
 
-    // Starts the copies of tile rows t0 .. t0 + 63 (those below T), channels c0 .. c0 + 63 (those below C).
-    static __device__ __forceinline__ void load(unsigned char* dst, const void* base, int64_t stride, int64_t t0, int c0,
-                                                const ScanArgs& g) {
-        const uint32_t s = ptx::smem_u32(dst);
-        constexpr int ES = sizeof(TI), PIECE = MODE == M16 ? 16 : 4, PER = (PITCH + PIECE - 1) / PIECE;
-        constexpr int ALL = CHUNK * PER;
-        static_assert(MODE == MODD || PITCH % PIECE == 0, "whole pieces");
-#pragma unroll 4
-        for (int k = threadIdx.x; k < ALL; k += NT) {
-            const int row = k / PER, piece = k % PER;
-            const int64_t t = t0 + row;
-            const char* p = static_cast<const char*>(base) + ((t < g.T ? t : 0) * stride + c0) * ES;
-            int bytes = (g.C - c0) * ES;                        // of the row, from c0 on
-            if (MODE == MODD) {
-                const int odd = (int)(reinterpret_cast<uintptr_t>(p) & 2);
-                p -= odd;
-                bytes += odd;
+    template <int N> static __device__ __forceinline__ void copy(uint32_t dst, const char* p, int bytes) {
+        if constexpr (N == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(p), "r"(bytes) : "memory");
+        else asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(p), "r"(bytes) : "memory");
+    }
+
+    // Starts the copies of rows t .. t + rows - 1, channels c0 .. c0 + cols - 1; the rest becomes zero.
+    static __device__ __forceinline__ void load(uint32_t dst, const void* base, int64_t stride, int64_t t, int c0, int rows, int cols) {
+        const int lane = threadIdx.x & 31;
+        const char* const first = static_cast<const char*>(base);
+        if constexpr (MODE == M16) {
+            constexpr int PER = PITCH / 16, STEP = 32 / PER;    // pieces of a row, rows of a copy
+            const int piece = lane % PER, row = lane / PER, bytes = min(max(cols * ES - piece * 16, 0), 16);
+            const char* p = first + ((t + row) * stride + c0) * ES + piece * 16;
+#pragma unroll
+            for (int k = 0; k < SUB / STEP; ++k) {
+                const int n = row + k * STEP < rows ? bytes : 0;
+                copy<16>(dst + (row + k * STEP) * PITCH + piece * 16, n > 0 ? p : first, n);
+                p += STEP * stride * ES;
             }
-            bytes = t < g.T ? min(max(bytes - piece * PIECE, 0), PIECE) : 0;
-            if (bytes > 0) p += piece * PIECE;                  // (an address is formed in bounds only)
-            if (MODE == M16)
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(s + row * PITCH + piece * PIECE), "l"(p), "r"(bytes) : "memory");
-            else
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(s + row * PITCH + piece * PIECE), "l"(p), "r"(bytes) : "memory");
+        } else {
+            constexpr int PER = PITCH / 4;                      // 32, 33 or 64 words of a row
+#pragma unroll
+            for (int k = 0; k < SUB; ++k) {
+                const char* p = first + ((t + k) * stride + c0) * ES;
+                int bytes = k < rows ? cols * ES : 0;
+                if (MODE == MODD) {                             // from the word that holds the first element: the half
+                    const int odd = (int)(reinterpret_cast<uintptr_t>(p) & 2);   // before it is copied and not used
+                    p -= odd;
+                    bytes += bytes > 0 ? odd : 0;
+                }
+#pragma unroll
+                for (int w = lane; w < PER; w += 32) {
+                    const int n = min(max(bytes - w * 4, 0), 4);
+                    copy<4>(dst + k * PITCH + w * 4, n > 0 ? p + w * 4 : first - (reinterpret_cast<uintptr_t>(first) & 2), n);
+                }
+            }
         }
     }
 
-    // Whether the first element of row t0 (channel c0) is the second of its word, and how that changes by row.
+    // Whether the first element of row t (channel c0) is the second of its word, and how that changes by row.
     struct Odd {
         int first, step;
     };
-    static __device__ __forceinline__ Odd odd(const void* base, int64_t stride, int64_t t0, int c0) {
+    static __device__ __forceinline__ Odd odd(const void* base, int64_t stride, int64_t t, int c0) {
         if (MODE != MODD) return Odd{0, 0};
-        return Odd{(int)((reinterpret_cast<uintptr_t>(base) >> 1) + (uintptr_t)(t0 * stride + c0)) & 1, (int)(stride & 1)};
+        return Odd{(int)((reinterpret_cast<uintptr_t>(base) >> 1) + (uintptr_t)(t * stride + c0)) & 1, (int)(stride & 1)};
     }
     // The lane's channel pair of a row.
-    static __device__ __forceinline__ float2 get(const unsigned char* tile, int row, Odd odd) {
-        const unsigned char* p = tile + row * PITCH;
+    static __device__ __forceinline__ float2 get(const unsigned char* rows, int row, Odd odd) {
+        const unsigned char* p = rows + row * PITCH;
         const int lane = threadIdx.x & 31;
-        if constexpr (sizeof(TI) == 4) {
+        if constexpr (ES == 4) {
             return reinterpret_cast<const float2*>(p)[lane];
         } else {
             const uint32_t* w = reinterpret_cast<const uint32_t*>(p) + lane;
@@ -85,21 +99,22 @@ inline bool row_pairs(const void* base, int64_t stride, int es) {
     return (reinterpret_cast<uintptr_t>(base) | (uintptr_t)(stride * es)) % (2 * es) == 0;
 }
 
-// Stores a lane's pair at channel c of row t; `pairs`: every row's pairs lie on their size.
-template <typename TI>
-__device__ __forceinline__ void put(void* base, int64_t stride, int64_t t, int c, int C, bool pairs, float2 v) {
-    TI* p = static_cast<TI*>(base) + t * stride + c;
-    if (pairs) {                                                // (C may be odd: the last pair's second channel)
-        if (c + 1 < C) {
-            if constexpr (sizeof(TI) == 4) *reinterpret_cast<float2*>(p) = v;
-            else *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(v.x, v.y);
-            return;
-        }
-        if (c < C) p[0] = from_f32<TI>(v.x);
+// Stores a lane's pair at p; `left` channels are left of the row, `pair`: both go as one.
+template <typename TI> __device__ __forceinline__ void put(TI* p, int left, bool pair, float2 v) {
+    if (pair) {
+        if constexpr (sizeof(TI) == 4) *reinterpret_cast<float2*>(p) = v;
+        else *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(v.x, v.y);
         return;
     }
-    if (c < C) p[0] = from_f32<TI>(v.x);
-    if (c + 1 < C) p[1] = from_f32<TI>(v.y);
+    if (left > 0) p[0] = from_f32<TI>(v.x);
+    if (left > 1) p[1] = from_f32<TI>(v.y);
+}
+// The lane's pair of row `row` of an fp32 tensor [rows][C] (NULL: zero), or its place.
+__device__ __forceinline__ float2 pair_at(const float* p, size_t row, int c, int C) {
+    float2 h = f2(0.f);
+    if (p && c < C) h.x = p[row * C + c];
+    if (p && c + 1 < C) h.y = p[row * C + c + 1];
+    return h;
 }
 
 // ---- sequence borders -------------------------------------------------------------------
@@ -126,18 +141,15 @@ __device__ __forceinline__ Borders borders(const ScanArgs& g, int tile_t, int64_
         if (n > INLINE_SEQS) s += __popc(__ballot_sync(0xffffffffu, c2 <= x));
         return s;
     };
-    Borders b{0, 0, 0};
     int prev = of(t - 1);
-    if (t == 0) prev = -1;
+    if (of(t + SUB) == prev) return Borders{0, 0, prev};        // (t = 0: before the first sequence, -1)
     int cur = of(t);
-    b.seq = cur;
-#pragma unroll
-    for (int j = 0; j < SUB; ++j) {
+    Borders b{0, 0, cur};
+#pragma unroll 1
+    for (int j = 0; j < SUB && t + j < g.T; ++j) {
         const int next = of(t + j + 1);
-        if (t + j < g.T) {
-            b.start |= (cur != prev ? 1u : 0u) << j;
-            b.end |= (next != cur ? 1u : 0u) << j;
-        }
+        b.start |= (cur != prev ? 1u : 0u) << j;
+        b.end |= (next != cur ? 1u : 0u) << j;
         prev = cur;
         cur = next;
     }
@@ -147,86 +159,98 @@ __device__ __forceinline__ Borders borders(const ScanArgs& g, int tile_t, int64_
 // ---- the walk along the tiles -------------------------------------------------------------
 // Tiles are taken in the order of a ticket, all of one place along T before the next, so a
 // tile's predecessors have been taken, by CTAs that are running, and every wait ends.  A
-// tile publishes its map h -> A h + B, looks back over at most 32 predecessors for
-// the nearest one whose outgoing value is known, and applies the maps in between in their order:
+// tile publishes its map h -> A h + B, then looks back for the nearest of 4
+// predecessors whose outgoing value is known, and applies the maps in between in their order:
 // the same operations in any timing, so results do not depend on it.
+// Maps and values are their own flags: the words are set to EMPTY, a NaN that is never
+// published, before the call, and a reader takes each as soon as it is another one, so no
+// fence stands between a tile and the next.  (With flags beside them, two fences and one
+// more read: 5 us more a tile.)
 constexpr uint64_t WAIT_NS = 2000000000ull;
+constexpr uint32_t EMPTY = 0xffffffffu;
+constexpr int BACK = 4;
 
-__device__ __forceinline__ int ld_acquire(const int32_t* p) {
-    int v;
-    asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+__device__ __forceinline__ uint32_t word_of(float x) {
+    const uint32_t u = __float_as_uint(x);
+    return u == EMPTY ? 0x7fffffffu : u;
+}
+__device__ __forceinline__ void publish(float* p, float2 v) {
+    asm volatile("st.relaxed.gpu.global.v2.b32 [%0], {%1, %2};" ::"l"(p), "r"(word_of(v.x)), "r"(word_of(v.y)) : "memory");
+}
+__device__ __forceinline__ void publish(float* p, float2 A, float2 B) {
+    asm volatile("st.relaxed.gpu.global.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(word_of(A.x)), "r"(word_of(B.x)),
+                 "r"(word_of(A.y)), "r"(word_of(B.y)) : "memory");
+}
+__device__ __forceinline__ uint2 peek2(const float* p) {
+    uint2 v;
+    asm volatile("ld.relaxed.gpu.global.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p) : "memory");
     return v;
 }
-__device__ __forceinline__ void st_release(int32_t* p, int v) {
-    asm volatile("st.release.gpu.global.s32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+__device__ __forceinline__ uint4 peek4(const float* p) {
+    uint4 v;
+    asm volatile("ld.relaxed.gpu.global.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+    return v;
 }
-constexpr int HAS_MAP = 1, HAS_VALUE = 2;
 
 // By one whole warp.  order: the tile's place in the walk (0: the first).  Returns the value
 // that comes into the tile.
 __device__ __forceinline__ float2 walk(const ScanArgs& g, int order, int tile_c, float2 A, float2 B) {
     const int lane = threadIdx.x & 31;
-    auto slot = [&](int o) { return (size_t)o * g.tiles_c + tile_c; };
-    const size_t me = slot(order);
-    float2* pre = reinterpret_cast<float2*>(g.pre) + me * (TILE_C / 2) + lane;
-    const bool anew = A.x < 0.f;                                // (both channels: borders are the tokens')
+    const size_t me = ((size_t)order * g.tiles_c + tile_c) * TILE_C + 2 * lane;
+    const size_t step = (size_t)g.tiles_c * TILE_C;
+    const bool anew = A.x < 0.f;                                // (in all channels: borders are the tokens')
+    if (anew) publish(g.val + me, B);
+    else publish(g.map + 2 * me, A, B);
     float2 in = f2(0.f);
-    if (anew) {
-        *pre = B;
-        __syncwarp();
-        if (lane == 0) {
-            __threadfence();
-            st_release(g.flags + me, HAS_VALUE);
-        }
-    } else {
-        reinterpret_cast<float4*>(g.agg)[me * (TILE_C / 2) + lane] = make_float4(A.x, B.x, A.y, B.y);
-        __syncwarp();
-        if (lane == 0) {
-            __threadfence();
-            st_release(g.flags + me, HAS_MAP);
-        }
-    }
     if (order == 0) return in;
-    // the nearest predecessor with a value, all maps in between known
+    bool done = false;
     uint64_t begin = 0;
-    int back;
     for (uint32_t turn = 1;; ++turn) {
-        const int o = order - 1 - lane;
-        const int f = o >= 0 ? ld_acquire(g.flags + slot(o)) : 0;
-        const uint32_t value = __ballot_sync(0xffffffffu, f == HAS_VALUE), none = __ballot_sync(0xffffffffu, f == 0);
-        back = __ffs(value) - 1;
-        if (back >= 0 && (none & ((1u << back) - 1)) == 0) break;
+        if (!done) {
+            uint2 v[BACK];
+            uint4 m[BACK - 1];
+#pragma unroll
+            for (int k = 0; k < BACK; ++k) {
+                v[k] = make_uint2(EMPTY, EMPTY);
+                if (k < order) v[k] = peek2(g.val + me - (k + 1) * step);
+                if (k + 1 < BACK) {
+                    m[k] = make_uint4(EMPTY, EMPTY, EMPTY, EMPTY);
+                    if (k < order) m[k] = peek4(g.map + 2 * (me - (k + 1) * step));
+                }
+            }
+            int from = -1;
+            bool maps = true;                                   // of the tiles nearer than k
+#pragma unroll
+            for (int k = 0; k < BACK; ++k) {
+                if (from < 0 && maps && v[k].x != EMPTY && v[k].y != EMPTY) {
+                    from = k;
+                    in = make_float2(__uint_as_float(v[k].x), __uint_as_float(v[k].y));
+                }
+                if (k + 1 < BACK) maps = maps && m[k].x != EMPTY && m[k].y != EMPTY && m[k].z != EMPTY && m[k].w != EMPTY;
+            }
+            done = from >= 0;
+#pragma unroll
+            for (int k = BACK - 2; k >= 0; --k)
+                if (k < from) in = make_float2(fmaf(__uint_as_float(m[k].x), in.x, __uint_as_float(m[k].y)),
+                                               fmaf(__uint_as_float(m[k].z), in.y, __uint_as_float(m[k].w)));
+        }
+        if (__all_sync(0xffffffffu, done)) break;
         if (turn % 64 == 0) {
             const uint64_t now = ptx::globaltimer_ns();
             if (begin == 0) begin = now;
             if (__any_sync(0xffffffffu, now - begin > WAIT_NS)) {   // gives up: the error word, and NaN from here on
                 if (lane == 0) atomicExch(g.status, ERR_TIMEOUT);
-                back = -1;
+                in = f2(__int_as_float(0x7fffffff));
                 break;
             }
         }
     }
-    __syncwarp();
-    if (back < 0) {
-        in = f2(__int_as_float(0x7fffffff));
-    } else {
-        in = __ldcg(reinterpret_cast<const float2*>(g.pre) + slot(order - 1 - back) * (TILE_C / 2) + lane);
-#pragma unroll 4
-        for (int k = back - 1; k >= 0; --k) {
-            const float4 m = __ldcg(reinterpret_cast<const float4*>(g.agg) + slot(order - 1 - k) * (TILE_C / 2) + lane);
-            in = make_float2(fmaf(m.x, in.x, m.y), fmaf(m.z, in.y, m.w));
-        }
-    }
-    if (!anew) {
-        *pre = make_float2(fmaf(A.x, in.x, B.x), fmaf(A.y, in.y, B.y));
-        __syncwarp();
-        if (lane == 0) {
-            __threadfence();
-            st_release(g.flags + me, HAS_VALUE);
-        }
-    }
+    if (!anew) publish(g.val + me, make_float2(fmaf(A.x, in.x, B.x), fmaf(A.y, in.y, B.y)));
     return in;
 }
+
+// The next ticket (the counter starts at EMPTY, like everything else that is set before a call).
+__device__ __forceinline__ uint32_t next_ticket(const ScanArgs& g) { return atomicAdd(g.ticket, 1u) + 1u; }
 
 }  // namespace glr
 }  // namespace kda
