@@ -41,10 +41,10 @@ kda_status check_batch(const int64_t* cu, int32_t n_seqs, int64_t total_tokens) 
     return total_tokens > (int64_t)INT32_MAX ? KDA_ERR_UNSUPPORTED : KDA_OK;
 }
 
-// Workspace: error word | ticket | the tiles' maps and values | token offsets, rows and tile table
+// Workspace: error word | gates | ticket | the tiles' maps and values | token offsets, rows and tile table
 // of the sequences | partial sums (backward pass).
 struct Layout {
-    size_t map = 0, val = 0, cu = 0, id = 0, tile = 0, part = 0, total = 0;
+    size_t gates = 0, ticket = 0, map = 0, val = 0, cu = 0, id = 0, tile = 0, part = 0, total = 0;
     int64_t tiles_t = 0, tiles_c = 0;
 };
 Layout layout(const kda_glr_params* p, int32_t n_seqs, int64_t total_tokens, bool backward) {
@@ -52,8 +52,10 @@ Layout layout(const kda_glr_params* p, int32_t n_seqs, int64_t total_tokens, boo
     L.tiles_t = (total_tokens + CHUNK - 1) / CHUNK;
     L.tiles_c = (p->channels + TILE_C - 1) / TILE_C;
     const size_t tiles = (size_t)L.tiles_t * L.tiles_c;
-    size_t off = 2 * WS_ALIGN;
+    size_t off = WS_ALIGN;
     auto take = [&](size_t bytes) { const size_t at = off; off = align_up(off + bytes); return at; };
+    L.gates = take(sizeof(float) * 3 * TILE_C * (size_t)L.tiles_c);
+    L.ticket = take(WS_ALIGN);
     L.map = take(sizeof(float) * 2 * TILE_C * tiles);
     L.val = take(sizeof(float) * TILE_C * tiles);
     L.cu = take(sizeof(int64_t) * ((size_t)n_seqs + 1));
@@ -64,23 +66,22 @@ Layout layout(const kda_glr_params* p, int32_t n_seqs, int64_t total_tokens, boo
     return L;
 }
 
-// What the two walks share: the sequences with tokens, and the workspace's parts, with ticket, maps and
-// values set to EMPTY (all ones).  The first tile clears the error word.
+// What the two walks share: the sequences with tokens, and the workspace's parts, set up.
+// The walk clears the error word.
 cudaError_t prepare(const kda_glr_params* p, const int64_t* cu, int32_t n_seqs, unsigned char* ws, const Layout& L,
                     ScanArgs* a, cudaStream_t s) {
     a->status = reinterpret_cast<int32_t*>(ws);
-    a->ticket = reinterpret_cast<uint32_t*>(ws + WS_ALIGN);
+    a->ticket = reinterpret_cast<uint32_t*>(ws + L.ticket);
+    a->gates = reinterpret_cast<float2*>(ws + L.gates);
     a->map = reinterpret_cast<float*>(ws + L.map);
     a->val = reinterpret_cast<float*>(ws + L.val);
     a->part = reinterpret_cast<float*>(ws + L.part);
     a->tiles_t = (int32_t)L.tiles_t;
     a->tiles_c = (int32_t)L.tiles_c;
     if (L.tiles_t == 0) return cudaMemsetAsync(ws, 0, WS_ALIGN, s);
-    // one place along T waits for nothing: the ticket alone
-    const size_t to = L.tiles_t > 1 ? L.val + sizeof(float) * TILE_C * (size_t)(L.tiles_t * L.tiles_c) : 2 * WS_ALIGN;
-    cudaError_t e = cudaMemsetAsync(ws + WS_ALIGN, 0xff, to - WS_ALIGN, s);
-    if (e != cudaSuccess) return e;
     Sequences& f = a->f;
+    // one place along T waits for nothing: the ticket alone
+    const size_t empty = L.tiles_t > 1 ? L.val + sizeof(float) * TILE_C * (size_t)(L.tiles_t * L.tiles_c) - L.ticket : WS_ALIGN;
     f.d_cu = reinterpret_cast<int64_t*>(ws + L.cu);
     f.d_id = reinterpret_cast<int32_t*>(ws + L.id);
     f.d_tile = reinterpret_cast<int32_t*>(ws + L.tile);
@@ -94,7 +95,7 @@ cudaError_t prepare(const kda_glr_params* p, const int64_t* cu, int32_t n_seqs, 
                 f.id[k++] = i;
             }
         f.cu[k] = (int32_t)cu[n_seqs];
-        return cudaSuccess;
+        return launch_setup(*a, empty / sizeof(uint4), s);
     }
     std::vector<int64_t> start;
     std::vector<int32_t> id;
@@ -110,9 +111,9 @@ cudaError_t prepare(const kda_glr_params* p, const int64_t* cu, int32_t n_seqs, 
     } catch (const std::bad_alloc&) {
         return cudaErrorMemoryAllocation;
     }
-    e = build_meta(start.data(), id.data(), f.n, 0, const_cast<int64_t*>(f.d_cu), nullptr, const_cast<int32_t*>(f.d_id),
+    const cudaError_t e = build_meta(start.data(), id.data(), f.n, 0, const_cast<int64_t*>(f.d_cu), nullptr, const_cast<int32_t*>(f.d_id),
                    nullptr, s);
-    return e != cudaSuccess ? e : launch_tile_table(f.d_cu, f.n, const_cast<int32_t*>(f.d_tile), a->tiles_t, s);
+    return e != cudaSuccess ? e : launch_setup(*a, empty / sizeof(uint4), s);
 }
 
 // Copies the state of sequences without tokens, if there are any (all states: the walk then
@@ -168,8 +169,8 @@ kda_status kda_glr_prefill(const kda_glr_params* p, const void* x, int64_t x_str
     a.A_log = p->A_log; a.r_bias = p->r_bias; a.i_bias = p->i_bias;
     a.S_in = S_in; a.S_out = S_out; a.states = states; a.o = o;
     a.T = total_tokens; a.C = p->channels;
-    if (glr::prepare(p, cu, n_seqs, ws, L, &a, s) != cudaSuccess ||
-        copy_states(p, cu, n_seqs, S_in, S_out, s) != cudaSuccess)
+    // (the setup is the last before the walk, which starts beside its end)
+    if (copy_states(p, cu, n_seqs, S_in, S_out, s) != cudaSuccess || glr::prepare(p, cu, n_seqs, ws, L, &a, s) != cudaSuccess)
         return KDA_ERR_CUDA;
     if (!any) return KDA_OK;
     return glr::launch_scan(a, p->io_dtype == KDA_DTYPE_BF16, s) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
@@ -215,8 +216,8 @@ kda_status kda_glr_backward(const kda_glr_params* p, const void* x, int64_t x_st
     a.dx_s = dx_stride; a.dr_s = dr_stride; a.di_s = di_stride; a.dz_s = dz_stride;
     a.dS_in = dS_in; a.dA_log = dA_log; a.dr_bias = dr_bias; a.di_bias = di_bias;
     a.T = total_tokens; a.C = p->channels;
-    if (glr::prepare(p, cu, n_seqs, ws, L, &a, s) != cudaSuccess ||
-        (dS_in && copy_states(p, cu, n_seqs, dS_out, dS_in, s) != cudaSuccess))
+    if ((dS_in && copy_states(p, cu, n_seqs, dS_out, dS_in, s) != cudaSuccess) ||
+        glr::prepare(p, cu, n_seqs, ws, L, &a, s) != cudaSuccess)
         return KDA_ERR_CUDA;
     return glr::launch_backward(a, p->io_dtype == KDA_DTYPE_BF16, s) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }

@@ -23,52 +23,53 @@ namespace {
 
 enum { OUT_X = 1, OUT_R = 2, OUT_I = 4, OUT_Z = 8 };   // gradients whose rows take pairs
 
-template <typename TI, int MODE, int STAGES, int PER_SM>
+template <typename TI, int MODE, bool GATED, int STAGES, int PER_SM>
 __global__ void __launch_bounds__(NT, PER_SM) backward_kernel(const __grid_constant__ ScanArgs g, int pairs) {
     using R = Rows<TI, MODE>;
+    constexpr int TENSORS = GATED ? 5 : 4;
     extern __shared__ __align__(128) unsigned char rows_smem[];    // [WARPS][STAGES][x, r, i, do, z]
-    __shared__ uint32_t tk[STAGES];
+    __shared__ int2 tk[STAGES];
     __shared__ float2 sA[2][WARPS][32], sB[2][WARPS][32], sAr[2][WARPS][32], sBr[2][WARPS][32], sIn[2][32];
     __shared__ float2 sums[3][WARPS][32];
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-    const uint32_t tiles = (uint32_t)g.tiles_t * (uint32_t)g.tiles_c;
-    unsigned char* const mine = rows_smem + warp * STAGES * 5 * R::BYTES;
+    unsigned char* const mine = rows_smem + warp * STAGES * TENSORS * R::BYTES;
     const uint32_t mine_u = ptx::smem_u32(mine);
-    auto issue = [&](int stage, uint32_t tile) {
-        if (tile < tiles) {
-            const int64_t t = (int64_t)(g.tiles_t - 1 - (int)(tile / g.tiles_c)) * CHUNK + warp * SUB;
-            const int c0 = (int)(tile % g.tiles_c) * TILE_C;
+    auto issue = [&](int stage) {
+        const int2 tile = tk[stage];
+        if (tile.x >= 0) {
+            const int64_t t = (int64_t)(g.tiles_t - 1 - tile.x) * CHUNK + warp * SUB;
+            const int c0 = tile.y * TILE_C;
             const int rows = (int)min((int64_t)SUB, g.T - t), cols = min(TILE_C, g.C - c0);
-            const uint32_t s = mine_u + stage * 5 * R::BYTES;
+            const uint32_t s = mine_u + stage * TENSORS * R::BYTES;
             R::load(s, g.x, g.x_s, t, c0, rows, cols);
             R::load(s + R::BYTES, g.r, g.r_s, t, c0, rows, cols);
             R::load(s + 2 * R::BYTES, g.i, g.i_s, t, c0, rows, cols);
             R::load(s + 3 * R::BYTES, g.d_o, g.do_s, t, c0, rows, cols);
-            if (g.z) R::load(s + 4 * R::BYTES, g.z, g.z_s, t, c0, rows, cols);
+            if (GATED) R::load(s + 4 * R::BYTES, g.z, g.z_s, t, c0, rows, cols);
         }
         ptx::cp_async_commit();
     };
+    cudaGridDependencySynchronize();
     if (tid == 0)
-        for (int k = 0; k < STAGES; ++k) tk[k] = next_ticket(g);
+        for (int k = 0; k < STAGES; ++k) tk[k] = next_tile(g);
     __syncthreads();
-    if (tk[0] == 0 && tid == 0) *g.status = ERR_NONE;
-    for (int k = 0; k < STAGES; ++k) issue(k, tk[k]);
+    if (tk[0].x == 0 && tk[0].y == 0 && tid == 0) *g.status = ERR_NONE;
+    for (int k = 0; k < STAGES; ++k) issue(k);
 
     int buf = 0;
     for (int stage = 0;; stage = stage + 1 == STAGES ? 0 : stage + 1, buf ^= 1) {
-        const uint32_t tile = tk[stage];
-        if (tile >= tiles) break;
-        const int order = tile / g.tiles_c, tt = g.tiles_t - 1 - order, tc = tile % g.tiles_c;
+        const int order = tk[stage].x, tc = tk[stage].y, tt = g.tiles_t - 1 - order;
+        if (order < 0) break;
         const int64_t t = (int64_t)tt * CHUNK + warp * SUB;
         const int c0 = tc * TILE_C, c = c0 + 2 * lane, rows = (int)min((int64_t)SUB, g.T - t), left = g.C - c;
-        const Gate k = load_gate(g, c);
+        const Gate k = load_gate(g, tc);
         float2 h = pair_at(g.states, tt, c, g.C);
         const Borders bd = borders(g, tt, t);
         auto seq_of = [&](int j) { return (size_t)seq_id(g.f, bd.seq + __popc((bd.start >> 1) & ((1u << j) - 1))); };
         asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
         __syncwarp();
 
-        const unsigned char* s = mine + stage * 5 * R::BYTES;
+        const unsigned char* s = mine + stage * TENSORS * R::BYTES;
         const typename R::Odd ox = R::odd(g.x, g.x_s, t, c0), orr = R::odd(g.r, g.r_s, t, c0), oi = R::odd(g.i, g.i_s, t, c0),
                               od = R::odd(g.d_o, g.do_s, t, c0), oz = R::odd(g.z, g.z_s, t, c0);
         auto x_of = [&](int j) { return R::get(s, j, ox); };
@@ -83,11 +84,11 @@ __global__ void __launch_bounds__(NT, PER_SM) backward_kernel(const __grid_const
             const float2 v = sigmoid_of(fma2(R::get(s + 2 * R::BYTES, j, oi), f2(-LOG2E), k.ib), v_[j]);
             ww[j] = smaller(w, rest);
             float2 m2;
-            const float2 la = mul2(k.ea, w);
+            const float2 la = mul2(k.ea, w), neg_la = mul2(mul2(k.ea, f2(-1.f)), w);
             decay_of<decltype(wide)::value>(la, a[j], m2);
             const float2 im = inv_root(m2);
             E[j] = mul2(mul2(m2, im), v);
-            D[j] = mul2(mul2(mul2(a[j], a[j]), mul2(la, im)), v);   // (a / m)^2 b la / x
+            D[j] = mul2(mul2(mul2(a[j], a[j]), mul2(neg_la, im)), v);   // -(a / m)^2 b la / x
         };
         if (any_wide(k)) {
 #pragma unroll
@@ -96,11 +97,11 @@ __global__ void __launch_bounds__(NT, PER_SM) backward_kernel(const __grid_const
 #pragma unroll
             for (int j = 0; j < SUB; ++j) token(j, std::false_type{});
         }
-        if (g.z) {
+        if (GATED) {
 #pragma unroll
             for (int j = 0; j < SUB; ++j) e[j] = sigmoid_of(mul2(z_of(j), f2(-LOG2E)));
         }
-        auto G_of = [&](int j) { return g.z ? mul2(do_of(j), mul2(z_of(j), e[j])) : do_of(j); };
+        auto G_of = [&](int j) { return GATED ? mul2(do_of(j), mul2(z_of(j), e[j])) : do_of(j); };
         float2 Ar = f2(1.f), Br = f2(0.f);
         if ((bd.start | bd.end) == 0) {
 #pragma unroll
@@ -150,45 +151,57 @@ __global__ void __launch_bounds__(NT, PER_SM) backward_kernel(const __grid_const
             }
             sIn[buf][lane] = walk(g, order, tc, Ar, Br);
         } else if (tid == 32) {
-            tk[stage] = next_ticket(g);
+            tk[stage] = next_tile(g);
         }
         for (int u = 0; u < warp; ++u) h = apply(sA[buf][u][lane], sB[buf][u][lane], h);
-        TI* dz = g.z ? static_cast<TI*>(g.dz) + t * g.dz_s + c : nullptr;
+        TI* dz = GATED ? static_cast<TI*>(g.dz) + t * g.dz_s + c : nullptr;
+        const bool whole = (bd.start | bd.end) == 0 && rows == SUB;
+        auto forward = [&](auto plain) {
+            constexpr bool PLAIN = decltype(plain)::value;
+            const bool pz = (pairs & OUT_Z) && left > 1;
 #pragma unroll
-        for (int j = 0; j < SUB; ++j) {
-            if (bd.start >> j & 1) h = pair_at(g.S_in, seq_of(j), c, g.C);
-            const float2 x = x_of(j), ah = mul2(a[j], h);
-            D[j] = fma2(ah, mul2(k.ea, sigmoid_from(ww[j])), neg2(mul2(D[j], x)));
-            h = fma2(E[j], x, ah);
-            if (g.z && j < rows) {
-                const float2 z = z_of(j), s1 = fma2(e[j], f2(-1.f), f2(1.f));
-                put(dz + j * g.dz_s, left, (pairs & OUT_Z) && left > 1, mul2(mul2(do_of(j), h), mul2(e[j], fma2(z, s1, f2(1.f)))));
+            for (int j = 0; j < SUB; ++j) {
+                if (!PLAIN && (bd.start >> j & 1)) h = pair_at(g.S_in, seq_of(j), c, g.C);
+                const float2 x = x_of(j), ah = mul2(a[j], h);
+                D[j] = fma2(ah, mul2(k.ea, sigmoid_from(ww[j])), mul2(D[j], x));
+                h = fma2(E[j], x, ah);
+                if (GATED && (PLAIN || j < rows)) {
+                    const float2 z = z_of(j), s1 = fma2(e[j], f2(-1.f), f2(1.f));
+                    put(dz + j * g.dz_s, left, pz, mul2(mul2(do_of(j), h), mul2(e[j], fma2(z, s1, f2(1.f)))));
+                }
             }
-        }
+        };
+        if (whole) forward(std::true_type{});
+        else forward(std::false_type{});
         __syncthreads();
         float2 carry = sIn[buf][lane], sa = f2(0.f), sr = f2(0.f), si = f2(0.f);
         for (int u = WARPS - 1; u > warp; --u) carry = apply(sAr[buf][u][lane], sBr[buf][u][lane], carry);
         TI *dx = static_cast<TI*>(g.dx) + t * g.dx_s + c, *dr = static_cast<TI*>(g.dr) + t * g.dr_s + c,
            *di = static_cast<TI*>(g.di) + t * g.di_s + c;
         const bool px = (pairs & OUT_X) && left > 1, pr = (pairs & OUT_R) && left > 1, pi = (pairs & OUT_I) && left > 1;
+        auto backward = [&](auto plain) {
+            constexpr bool PLAIN = decltype(plain)::value;
 #pragma unroll
-        for (int j = SUB - 1; j >= 0; --j) {
-            if (bd.end >> j & 1) carry = pair_at(g.dS_out, seq_of(j), c, g.C);
-            const float2 gt = add2(G_of(j), carry), gx = mul2(gt, E[j]);
-            carry = mul2(a[j], gt);
-            const float2 gi = mul2(mul2(gx, x_of(j)), v_[j]);
-            const float2 gA = mul2(gt, D[j]), gr = mul2(gA, rest_from(ww[j]));
-            if (j < rows) {
-                put(dx + j * g.dx_s, left, px, gx);
-                put(dr + j * g.dr_s, left, pr, gr);
-                put(di + j * g.di_s, left, pi, gi);
-                sa = add2(sa, gA);
-                sr = add2(sr, gr);
-                si = add2(si, gi);
+            for (int j = SUB - 1; j >= 0; --j) {
+                if (!PLAIN && (bd.end >> j & 1)) carry = pair_at(g.dS_out, seq_of(j), c, g.C);
+                const float2 gt = add2(G_of(j), carry), gx = mul2(gt, E[j]);
+                carry = mul2(a[j], gt);
+                const float2 gi = mul2(mul2(gx, x_of(j)), v_[j]);
+                const float2 gA = mul2(gt, D[j]), gr = mul2(gA, rest_from(ww[j]));
+                if (PLAIN || j < rows) {
+                    put(dx + j * g.dx_s, left, px, gx);
+                    put(dr + j * g.dr_s, left, pr, gr);
+                    put(di + j * g.di_s, left, pi, gi);
+                    sa = add2(sa, gA);
+                    sr = add2(sr, gr);
+                    si = add2(si, gi);
+                }
+                if (!PLAIN && g.dS_in && (bd.start >> j & 1)) put(g.dS_in + seq_of(j) * g.C + c, left, false, carry);
             }
-            if (g.dS_in && (bd.start >> j & 1)) put(g.dS_in + seq_of(j) * g.C + c, left, false, carry);
-        }
-        issue(stage, tk[stage]);                     // (the warp has read its rows)
+        };
+        if (whole) backward(std::true_type{});
+        else backward(std::false_type{});
+        issue(stage);                     // (the warp has read its rows)
         sums[0][warp][lane] = sa;
         sums[1][warp][lane] = sr;
         sums[2][warp][lane] = si;
@@ -232,11 +245,11 @@ __global__ void __launch_bounds__(256) params_kernel(const __grid_constant__ Sca
     }
 }
 
-template <typename TI, int MODE>
+template <typename TI, int MODE, bool GATED>
 cudaError_t backward(const ScanArgs& a, int pairs, cudaStream_t s) {
     constexpr int STAGES = sizeof(TI) == 2 ? 2 : 1, PER_SM = 2;
-    auto k = backward_kernel<TI, MODE, STAGES, PER_SM>;
-    constexpr int SMEM = WARPS * STAGES * 5 * Rows<TI, MODE>::BYTES;
+    auto k = backward_kernel<TI, MODE, GATED, STAGES, PER_SM>;
+    constexpr int SMEM = WARPS * STAGES * (GATED ? 5 : 4) * Rows<TI, MODE>::BYTES;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -247,9 +260,11 @@ cudaError_t backward(const ScanArgs& a, int pairs, cudaStream_t s) {
         if (e != cudaSuccess) return e;
         done.fetch_or(bit);
     }
-    const int64_t tiles = (int64_t)a.tiles_t * a.tiles_c;
-    k<<<(unsigned)(tiles < SMS * PER_SM ? tiles : SMS * PER_SM), NT, SMEM, s>>>(a, pairs);
-    return cudaGetLastError();
+    return launch_behind(k, std::min<int64_t>((int64_t)a.tiles_t * a.tiles_c, SMS * PER_SM), NT, SMEM, s, a, pairs);
+}
+
+template <typename TI, int MODE> cudaError_t backward(const ScanArgs& a, int pairs, cudaStream_t s) {
+    return a.z ? backward<TI, MODE, true>(a, pairs, s) : backward<TI, MODE, false>(a, pairs, s);
 }
 
 }  // namespace

@@ -44,6 +44,7 @@ struct ScanArgs {
     // workspace
     int32_t* status;                 // error word
     uint32_t* ticket;                // the next tile to be taken
+    float2* gates;                   // [tiles along C][3][TILE_C / 2]: see load_gate
     float* map;                      // [tiles along T][tiles along C][TILE_C][2]
     float* val;                      // [tiles along T][tiles along C][TILE_C]
     float* part;                     // [tiles along T][3][C]: partial sums of the parameters' gradients
@@ -66,7 +67,9 @@ cudaError_t launch_scan(const ScanArgs& a, int io_bf16, cudaStream_t s);
 cudaError_t launch_backward(const ScanArgs& a, int io_bf16, cudaStream_t s);
 cudaError_t launch_tokens(const TokenArgs& a, int io_bf16, cudaStream_t s);
 
-cudaError_t launch_tile_table(const int64_t* d_cu, int32_t n, int32_t* d_tile, int32_t tiles_t, cudaStream_t s);
+// What a walk finds in its workspace: ticket, maps and values set to EMPTY (`empty` words from the
+// ticket on), the gates' table, and for many sequences that of the tiles' first ones.
+cudaError_t launch_setup(const ScanArgs& a, size_t empty, cudaStream_t s);
 
 }  // namespace glr
 }  // namespace kda

@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(NT) token_kernel(const __grid_constant__ Token
 #pragma unroll
         for (int p = 0; p < PAIRS; ++p) {
             h[p] = Values<float, V == 8 ? 4 : V>::pair(s[p / 2], V == 8 ? p % 2 : p);
-            k[p] = load_gate(g, c + 2 * p);
+            k[p] = make_gate(g, c + 2 * p);
         }
     }
     auto row_of = [&](int j) {

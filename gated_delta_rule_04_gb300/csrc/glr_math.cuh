@@ -56,7 +56,7 @@ __device__ __forceinline__ float2 rest_from(float2 k) { return make_float2(rest_
 struct Gate {
     float2 ea, rb, ib;
 };
-template <typename Args> __device__ __forceinline__ Gate load_gate(const Args& g, int c) {
+template <typename Args> __device__ __forceinline__ Gate make_gate(const Args& g, int c) {
     Gate k;
     float* f = reinterpret_cast<float*>(&k);
 #pragma unroll

@@ -2,12 +2,13 @@
 // o_t = h_t SiLU(z_t), with m = sqrt(1 - a^2).
 //
 // One pass over the data.  Tiles of 64 tokens x 64 channels lie in shared memory
-// in their own type, copied some tiles ahead; a thread holds 8 tokens of 2
+// in their own type, copied two tiles ahead; a thread holds 8 tokens of 2
 // channels, computes their a and b = m v x once, and the map h -> A h + B of its
-// run.  The maps meet in shared memory, the tile's value comes from the walk along
-// the tiles (glr_tile.cuh), and the second sweep over the 8 tokens is one multiply-add
-// a token and the output gate.  Sequences lie anywhere in the tiles: a token
-// that begins one starts its run anew from S_in.
+// run.  A ninth warp composes the maps and walks along the tiles (glr_tile.cuh) for the
+// value that comes in, while the others are at the next tile's maps; the second
+// sweep over the 8 tokens is one multiply-add a token and the output gate.
+// Sequences lie anywhere in the tiles: a token that begins one starts its run
+// anew from S_in.
 #include <atomic>
 #include <type_traits>
 
@@ -17,56 +18,95 @@ namespace kda {
 namespace glr {
 namespace {
 
-template <typename TI, int MODE, int STAGES, int PER_SM>
-__global__ void __launch_bounds__(NT, PER_SM) scan_kernel(const __grid_constant__ ScanArgs g, bool pairs) {
+constexpr int ALL = NT + 32;         // 8 warps that compute, one that walks
+constexpr int READY = 1, COME = 3;   // named barriers, two each: a tile's maps are there, its warps' first values
+
+// What a warp keeps of a tile between its two sweeps.
+struct Pending {
+    float2 a[SUB], b[SUB];
+    float2 first;                    // the start state, where the first token begins a sequence
+    Borders bd;
+    int tt, tc;
+};
+
+template <typename TI, int MODE, bool GATED, int PER_SM>
+__global__ void __launch_bounds__(ALL, PER_SM) scan_kernel(const __grid_constant__ ScanArgs g, bool pairs) {
     using R = Rows<TI, MODE>;
+    constexpr int STAGES = 3, TENSORS = GATED ? 4 : 3;
     extern __shared__ __align__(128) unsigned char rows_smem[];    // [WARPS][STAGES][x, r, i, z]
-    __shared__ uint32_t tk[STAGES];
-    __shared__ float2 sA[2][WARPS][32], sB[2][WARPS][32], sIn[2][32];
+    __shared__ int2 tk[STAGES];
+    __shared__ float2 sA[2][WARPS][32], sB[2][WARPS][32], sIn[2][WARPS][32];
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-    const uint32_t tiles = (uint32_t)g.tiles_t * (uint32_t)g.tiles_c;
-    unsigned char* const mine = rows_smem + warp * STAGES * 4 * R::BYTES;
+    cudaGridDependencySynchronize();
+    if (tid == 0)
+        for (int k = 0; k < STAGES; ++k) tk[k] = next_tile(g);
+    __syncthreads();
+
+    if (warp == WARPS) {                             // the walk: maps of the tile's warps in, their first values out
+        if (tk[0].x == 0 && tk[0].y == 0 && lane == 0) *g.status = ERR_NONE;
+        int buf = 0;
+        for (int stage = 0; tk[stage].x >= 0; stage = stage + 1 == STAGES ? 0 : stage + 1, buf ^= 1) {
+            const int2 tile = tk[stage];
+            bar_sync(READY + buf, ALL);
+            float2 A[WARPS], B[WARPS];
+#pragma unroll
+            for (int w = 0; w < WARPS; ++w) {
+                A[w] = sA[buf][w][lane];
+                B[w] = sB[buf][w][lane];
+            }
+            float2 At = A[0], Bt = B[0];
+#pragma unroll
+            for (int w = 1; w < WARPS; ++w) {
+                Bt = apply(A[w], B[w], Bt);
+                At = A[w].x < 0.f ? A[w] : At.x < 0.f ? At : mul2(At, A[w]);
+            }
+            float2 h = walk(g, tile.x, tile.y, At, Bt);
+#pragma unroll
+            for (int w = 0; w < WARPS; ++w) {
+                sIn[buf][w][lane] = h;
+                h = apply(A[w], B[w], h);
+            }
+            if (lane == 0) tk[stage] = next_tile(g);   // (read by the others behind the barrier)
+            __syncwarp();
+            bar_arrive(COME + buf, ALL);
+        }
+        return;
+    }
+
+    unsigned char* const mine = rows_smem + warp * STAGES * TENSORS * R::BYTES;
     const uint32_t mine_u = ptx::smem_u32(mine);
-    auto issue = [&](int stage, uint32_t tile) {
-        if (tile < tiles) {
-            const int64_t t = (int64_t)(tile / g.tiles_c) * CHUNK + warp * SUB;
-            const int c0 = (int)(tile % g.tiles_c) * TILE_C;
+    auto issue = [&](int stage) {
+        const int2 tile = tk[stage];
+        if (tile.x >= 0) {
+            const int64_t t = (int64_t)tile.x * CHUNK + warp * SUB;
+            const int c0 = tile.y * TILE_C;
             const int rows = (int)min((int64_t)SUB, g.T - t), cols = min(TILE_C, g.C - c0);
-            const uint32_t s = mine_u + stage * 4 * R::BYTES;
+            const uint32_t s = mine_u + stage * TENSORS * R::BYTES;
             R::load(s, g.x, g.x_s, t, c0, rows, cols);
             R::load(s + R::BYTES, g.r, g.r_s, t, c0, rows, cols);
             R::load(s + 2 * R::BYTES, g.i, g.i_s, t, c0, rows, cols);
-            if (g.z) R::load(s + 3 * R::BYTES, g.z, g.z_s, t, c0, rows, cols);
+            if (GATED) R::load(s + 3 * R::BYTES, g.z, g.z_s, t, c0, rows, cols);
         }
         ptx::cp_async_commit();
     };
-    if (tid == 0)
-        for (int k = 0; k < STAGES; ++k) tk[k] = next_ticket(g);
-    __syncthreads();
-    if (tk[0] == 0 && tid == 0) *g.status = ERR_NONE;
-    for (int k = 0; k < STAGES; ++k) issue(k, tk[k]);
+    auto seq_of = [&](const Borders& bd, int j) { return (size_t)seq_id(g.f, bd.seq + __popc((bd.start >> 1) & ((1u << j) - 1))); };
 
-    int buf = 0;
-    for (int stage = 0;; stage = stage + 1 == STAGES ? 0 : stage + 1, buf ^= 1) {
-        const uint32_t tile = tk[stage];
-        if (tile >= tiles) break;                    // (tickets only grow)
-        const int tt = tile / g.tiles_c, tc = tile % g.tiles_c;
-        const int64_t t = (int64_t)tt * CHUNK + warp * SUB;
-        const int c0 = tc * TILE_C, c = c0 + 2 * lane, rows = (int)min((int64_t)SUB, g.T - t);
-        const Gate k = load_gate(g, c);
-        const Borders bd = borders(g, tt, t);
-        auto seq_of = [&](int j) { return (size_t)seq_id(g.f, bd.seq + __popc((bd.start >> 1) & ((1u << j) - 1))); };
-        asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
+    // a and b of the warp's tokens, and its map
+    auto first_sweep = [&](Pending& p, int stage, int buf) {
+        const int64_t t = (int64_t)p.tt * CHUNK + warp * SUB;
+        const int c0 = p.tc * TILE_C, c = c0 + 2 * lane;
+        const Gate k = load_gate(g, p.tc);
+        p.bd = borders(g, p.tt, t);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
         __syncwarp();
-
-        const unsigned char* s = mine + stage * 4 * R::BYTES;
-        float2 a[SUB], b[SUB], A = f2(1.f), B = f2(0.f), first = f2(0.f);
+        const unsigned char* s = mine + stage * TENSORS * R::BYTES;
         const typename R::Odd ox = R::odd(g.x, g.x_s, t, c0), orr = R::odd(g.r, g.r_s, t, c0), oi = R::odd(g.i, g.i_s, t, c0);
+        float2 A = f2(1.f), B = f2(0.f);
         auto token = [&](int j, auto wide) {
             const Step st = step_of<decltype(wide)::value>(k, R::get(s, j, ox), R::get(s + R::BYTES, j, orr),
                                                            R::get(s + 2 * R::BYTES, j, oi));
-            a[j] = st.a;
-            b[j] = st.b;
+            p.a[j] = st.a;
+            p.b[j] = st.b;
         };
         if (any_wide(k)) {
 #pragma unroll
@@ -75,78 +115,92 @@ __global__ void __launch_bounds__(NT, PER_SM) scan_kernel(const __grid_constant_
 #pragma unroll
             for (int j = 0; j < SUB; ++j) token(j, std::false_type{});
         }
-        if (bd.start == 0) {
+        if (p.bd.start == 0) {
 #pragma unroll
             for (int j = 0; j < SUB; ++j) {
-                A = mul2(A, a[j]);
-                B = fma2(a[j], B, b[j]);
+                A = mul2(A, p.a[j]);
+                B = fma2(p.a[j], B, p.b[j]);
             }
         } else {
 #pragma unroll
             for (int j = 0; j < SUB; ++j) {
-                if (bd.start >> j & 1) {
-                    const float2 h = pair_at(g.S_in, seq_of(j), c, g.C);   // (S_out, written behind the barriers, may be S_in)
-                    if (j == 0) first = h;
-                    b[j] = fma2(a[j], h, b[j]);
+                if (p.bd.start >> j & 1) {           // (S_out, written in second sweeps, may be S_in: read here only)
+                    const float2 h = pair_at(g.S_in, seq_of(p.bd, j), c, g.C);
+                    if (j == 0) p.first = h;
+                    p.b[j] = fma2(p.a[j], h, p.b[j]);
                     A = f2(-1.f);
-                    B = b[j];
+                    B = p.b[j];
                 } else {
-                    A = A.x < 0.f ? A : mul2(A, a[j]);
-                    B = fma2(a[j], B, b[j]);
+                    A = A.x < 0.f ? A : mul2(A, p.a[j]);
+                    B = fma2(p.a[j], B, p.b[j]);
                 }
             }
         }
         sA[buf][warp][lane] = A;
         sB[buf][warp][lane] = B;
-        __syncthreads();
-        if (warp == 0) {
-#pragma unroll
-            for (int w = 1; w < WARPS; ++w) {
-                const float2 Aw = sA[buf][w][lane], Bw = sB[buf][w][lane];
-                B = apply(Aw, Bw, B);
-                A = Aw.x < 0.f ? Aw : A.x < 0.f ? A : mul2(A, Aw);
-            }
-            sIn[buf][lane] = walk(g, tt, tc, A, B);
-        } else if (tid == 32) {
-            tk[stage] = next_ticket(g);
-        }
-        float2 gate[SUB];
-        if (g.z) {
-            const typename R::Odd oz = R::odd(g.z, g.z_s, t, c0);
-#pragma unroll
-            for (int j = 0; j < SUB; ++j) gate[j] = silu(R::get(s + 3 * R::BYTES, j, oz));
-        }
-        __syncthreads();
-        issue(stage, tk[stage]);                     // (the warp has read its rows)
-        float2 h = sIn[buf][lane];
-        if (g.states && warp == 0) put(g.states + (size_t)tt * g.C + c, g.C - c, false, bd.start & 1 ? first : h);
-        for (int w = 0; w < warp; ++w) h = apply(sA[buf][w][lane], sB[buf][w][lane], h);
-        TI* o = static_cast<TI*>(g.o) + t * g.C + c;
-        const bool pair = pairs && c + 1 < g.C;
-        if ((bd.start | bd.end) == 0 && rows == SUB) {
+        bar_arrive(READY + buf, ALL);
+    };
+    // the states and outputs of a tile, once its first value is there
+    auto second_sweep = [&](const Pending& p, int stage, int buf) {
+        const int64_t t = (int64_t)p.tt * CHUNK + warp * SUB;
+        const int c0 = p.tc * TILE_C, c = c0 + 2 * lane, left = g.C - c, rows = (int)min((int64_t)SUB, g.T - t);
+        const unsigned char* s = mine + stage * TENSORS * R::BYTES + 3 * R::BYTES;
+        const typename R::Odd oz = R::odd(g.z, g.z_s, t, c0);
+        TI* const o = static_cast<TI*>(g.o) + t * g.C + c;
+        const bool pair = pairs && left > 1;
+        bar_sync(COME + buf, ALL);
+        float2 h = sIn[buf][warp][lane];
+        if (g.states && warp == 0) put(g.states + (size_t)p.tt * g.C + c, left, false, p.bd.start & 1 ? p.first : h);
+        if ((p.bd.start | p.bd.end) == 0 && rows == SUB) {
 #pragma unroll
             for (int j = 0; j < SUB; ++j) {
-                h = fma2(a[j], h, b[j]);
-                put(o, g.C - c, pair, g.z ? mul2(h, gate[j]) : h);
-                o += g.C;
+                h = fma2(p.a[j], h, p.b[j]);
+                put(o + (int64_t)j * g.C, left, pair, GATED ? mul2(h, silu(R::get(s, j, oz))) : h);
             }
         } else {
 #pragma unroll
             for (int j = 0; j < SUB; ++j) {
-                h = bd.start >> j & 1 ? b[j] : fma2(a[j], h, b[j]);
-                if (j < rows) put(o, g.C - c, pair, g.z ? mul2(h, gate[j]) : h);
-                if (bd.end >> j & 1) put(g.S_out + seq_of(j) * g.C + c, g.C - c, false, h);
-                o += g.C;
+                h = p.bd.start >> j & 1 ? p.b[j] : fma2(p.a[j], h, p.b[j]);
+                if (j < rows) put(o + (int64_t)j * g.C, left, pair, GATED ? mul2(h, silu(R::get(s, j, oz))) : h);
+                if (p.bd.end >> j & 1) put(g.S_out + seq_of(p.bd, j) * g.C + c, left, false, h);
             }
+        }
+    };
+
+    // Tile k's second sweep follows the first of tile k + 1, so the walk has the time of a whole
+    // tile; then the rows of tile k + 3 take the place of its own.
+    for (int k = 0; k < STAGES; ++k) issue(k);
+    Pending p[2];
+    int stage = 0;
+    auto next = [](int x) { return x + 1 == STAGES ? 0 : x + 1; };
+    const int2 t0 = tk[0];
+    if (t0.x < 0) return;
+    p[0].tt = t0.x;
+    p[0].tc = t0.y;
+    first_sweep(p[0], 0, 0);
+    for (;;) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {       // tile k in p[half], tile k + 1 in p[half ^ 1]
+            const int after = next(stage);
+            const int2 tile = tk[after];
+            if (tile.x >= 0) {
+                p[half ^ 1].tt = tile.x;
+                p[half ^ 1].tc = tile.y;
+                first_sweep(p[half ^ 1], after, half ^ 1);
+            }
+            second_sweep(p[half], stage, half);
+            if (tile.x < 0) return;
+            issue(stage);
+            stage = after;
         }
     }
 }
 
-template <typename TI, int MODE>
+template <typename TI, int MODE, bool GATED>
 cudaError_t scan(const ScanArgs& a, bool pairs, cudaStream_t s) {
-    constexpr int STAGES = sizeof(TI) == 2 ? 2 : 1, PER_SM = 3;
-    auto k = scan_kernel<TI, MODE, STAGES, PER_SM>;
-    constexpr int SMEM = WARPS * STAGES * 4 * Rows<TI, MODE>::BYTES;
+    constexpr int PER_SM = sizeof(TI) == 2 ? 2 : 1;
+    auto k = scan_kernel<TI, MODE, GATED, PER_SM>;
+    constexpr int SMEM = WARPS * 3 * (GATED ? 4 : 3) * Rows<TI, MODE>::BYTES;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -157,27 +211,43 @@ cudaError_t scan(const ScanArgs& a, bool pairs, cudaStream_t s) {
         if (e != cudaSuccess) return e;
         done.fetch_or(bit);
     }
-    const int64_t tiles = (int64_t)a.tiles_t * a.tiles_c;
-    k<<<(unsigned)(tiles < SMS * PER_SM ? tiles : SMS * PER_SM), NT, SMEM, s>>>(a, pairs);
-    return cudaGetLastError();
+    return launch_behind(k, std::min<int64_t>((int64_t)a.tiles_t * a.tiles_c, SMS * PER_SM), ALL, SMEM, s, a, pairs);
 }
 
-// The first sequence of each tile along T: the last one that begins at or before its first token.
-__global__ void __launch_bounds__(NT) tile_table_kernel(const int64_t* cu, int n, int32_t* table, int tiles) {
-    const int tt = blockIdx.x * NT + threadIdx.x;
-    if (tt >= tiles) return;
-    int lo = 0, hi = n - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (cu[mid] <= (int64_t)tt * CHUNK) lo = mid; else hi = mid - 1;
+template <typename TI, int MODE> cudaError_t scan(const ScanArgs& a, bool pairs, cudaStream_t s) {
+    return a.z ? scan<TI, MODE, true>(a, pairs, s) : scan<TI, MODE, false>(a, pairs, s);
+}
+
+// Many threads fill; the first ones also make the tables.
+__global__ void __launch_bounds__(NT) setup_kernel(const __grid_constant__ ScanArgs g, size_t empty) {
+    cudaTriggerProgrammaticLaunchCompletion();
+    const size_t id = (size_t)blockIdx.x * NT + threadIdx.x, all = (size_t)gridDim.x * NT;
+    uint4* w = reinterpret_cast<uint4*>(g.ticket);
+    for (size_t k = id; k < empty; k += all) w[k] = make_uint4(EMPTY, EMPTY, EMPTY, EMPTY);
+    for (size_t k = id; k < (size_t)g.tiles_c * (TILE_C / 2); k += all) {
+        const Gate q = make_gate(g, (int)k * 2);
+        float2* p = g.gates + k / (TILE_C / 2) * (3 * TILE_C / 2) + k % (TILE_C / 2);
+        p[0] = q.ea;
+        p[TILE_C / 2] = q.rb;
+        p[TILE_C] = q.ib;
     }
-    table[tt] = lo;
+    if (g.f.n <= INLINE_SEQS) return;
+    // the first sequence of each tile along T: the last one that begins at or before its first token
+    for (size_t tt = id; tt < (size_t)g.tiles_t; tt += all) {
+        int lo = 0, hi = g.f.n - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (g.f.d_cu[mid] <= (int64_t)tt * CHUNK) lo = mid; else hi = mid - 1;
+        }
+        const_cast<int32_t*>(g.f.d_tile)[tt] = lo;
+    }
 }
 
 }  // namespace
 
-cudaError_t launch_tile_table(const int64_t* d_cu, int32_t n, int32_t* d_tile, int32_t tiles_t, cudaStream_t s) {
-    tile_table_kernel<<<(unsigned)((tiles_t + NT - 1) / NT), NT, 0, s>>>(d_cu, n, d_tile, tiles_t);
+cudaError_t launch_setup(const ScanArgs& a, size_t empty, cudaStream_t s) {
+    const size_t most = std::max({empty, (size_t)a.tiles_c * (TILE_C / 2), (size_t)a.tiles_t});
+    setup_kernel<<<(unsigned)std::min<size_t>((most + NT - 1) / NT, SMS * 8), NT, 0, s>>>(a, empty);
     return cudaGetLastError();
 }
 

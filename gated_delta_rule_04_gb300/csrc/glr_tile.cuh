@@ -117,6 +117,12 @@ __device__ __forceinline__ float2 pair_at(const float* p, size_t row, int c, int
     return h;
 }
 
+// The lane's gate constants of tile column tc, as the setup left them.
+__device__ __forceinline__ Gate load_gate(const ScanArgs& g, int tc) {
+    const float2* p = g.gates + (size_t)tc * (3 * TILE_C / 2) + (threadIdx.x & 31);
+    return Gate{p[0], p[TILE_C / 2], p[TILE_C]};
+}
+
 // ---- sequence borders -------------------------------------------------------------------
 // Of the warp's 8 tokens from t on: which begin a sequence, which end one, and the sequence
 // of the first (each start adds one).  Warp-uniform.
@@ -249,8 +255,32 @@ __device__ __forceinline__ float2 walk(const ScanArgs& g, int order, int tile_c,
     return in;
 }
 
-// The next ticket (the counter starts at EMPTY, like everything else that is set before a call).
-__device__ __forceinline__ uint32_t next_ticket(const ScanArgs& g) { return atomicAdd(g.ticket, 1u) + 1u; }
+// The next tile to be taken: its place in the walk and its column, -1 behind the last (the counter starts at
+// EMPTY, like everything else that is set before a call).
+__device__ __forceinline__ int2 next_tile(const ScanArgs& g) {
+    const uint32_t k = atomicAdd(g.ticket, 1u) + 1u;
+    if (k >= (uint32_t)g.tiles_t * (uint32_t)g.tiles_c) return make_int2(-1, 0);
+    return make_int2((int)(k / (uint32_t)g.tiles_c), (int)(k % (uint32_t)g.tiles_c));
+}
+
+__device__ __forceinline__ void bar_arrive(int id, int threads) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
+__device__ __forceinline__ void bar_sync(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
+
+// Launches a kernel that starts beside the end of the one before it in the stream.
+template <typename... Params, typename... Args>
+cudaError_t launch_behind(void (*k)(Params...), int64_t grid, int threads, size_t smem, cudaStream_t s, Args... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k, args...);
+}
 
 }  // namespace glr
 }  // namespace kda
