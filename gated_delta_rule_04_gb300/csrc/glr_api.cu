@@ -26,11 +26,14 @@ kda_status check_params(const kda_glr_params* p) {
     return KDA_OK;
 }
 
+// Row strides in elements: their bytes fit 32 bits.
+constexpr int64_t MAX_STRIDE = (int64_t)1 << 30;
+
 // A token tensor: element alignment, a row stride of 0 (packed) or at least C.
 bool rows(const kda_glr_params* p, const void* base, bool needed, int64_t* stride) {
     if (*stride == 0) *stride = p->channels;
     if (base == nullptr) return !needed;
-    return aligned(base, esize(p)) && *stride >= p->channels && *stride <= (int64_t)INT32_MAX;
+    return aligned(base, esize(p)) && *stride >= p->channels && *stride < MAX_STRIDE;
 }
 
 kda_status check_batch(const int64_t* cu, int32_t n_seqs, int64_t total_tokens) {
@@ -165,9 +168,11 @@ kda_status kda_glr_prefill(const kda_glr_params* p, const void* x, int64_t x_str
     unsigned char* ws = static_cast<unsigned char*>(workspace);
     glr::ScanArgs a{};
     a.x = x; a.r = r; a.i = i; a.z = z;
-    a.x_s = x_stride; a.r_s = r_stride; a.i_s = i_stride; a.z_s = z_stride;
+    const uint32_t es = (uint32_t)esize(p);
+    a.x_s = (uint32_t)x_stride * es; a.r_s = (uint32_t)r_stride * es;
+    a.i_s = (uint32_t)i_stride * es; a.z_s = (uint32_t)z_stride * es;
     a.A_log = p->A_log; a.r_bias = p->r_bias; a.i_bias = p->i_bias;
-    a.S_in = S_in; a.S_out = S_out; a.states = states; a.o = o;
+    a.S_in = S_in; a.S_out = S_out; a.states = states; a.o = o; a.o_s = (uint32_t)p->channels * es;
     a.T = total_tokens; a.C = p->channels;
     // (the setup is the last before the walk, which starts beside its end)
     if (copy_states(p, cu, n_seqs, S_in, S_out, s) != cudaSuccess || glr::prepare(p, cu, n_seqs, ws, L, &a, s) != cudaSuccess)
@@ -208,12 +213,15 @@ kda_status kda_glr_backward(const kda_glr_params* p, const void* x, int64_t x_st
     unsigned char* ws = static_cast<unsigned char*>(workspace);
     glr::ScanArgs a{};
     a.x = x; a.r = r; a.i = i; a.z = z;
-    a.x_s = x_stride; a.r_s = r_stride; a.i_s = i_stride; a.z_s = z_stride;
+    const uint32_t es = (uint32_t)esize(p);
+    a.x_s = (uint32_t)x_stride * es; a.r_s = (uint32_t)r_stride * es;
+    a.i_s = (uint32_t)i_stride * es; a.z_s = (uint32_t)z_stride * es;
     a.A_log = p->A_log; a.r_bias = p->r_bias; a.i_bias = p->i_bias;
     a.S_in = S_in; a.states = const_cast<float*>(states);
-    a.d_o = d_o; a.do_s = do_stride; a.dS_out = dS_out;
+    a.d_o = d_o; a.do_s = (uint32_t)do_stride * es; a.dS_out = dS_out;
     a.dx = dx; a.dr = dr; a.di = di; a.dz = dz;
-    a.dx_s = dx_stride; a.dr_s = dr_stride; a.di_s = di_stride; a.dz_s = dz_stride;
+    a.dx_s = (uint32_t)dx_stride * es; a.dr_s = (uint32_t)dr_stride * es;
+    a.di_s = (uint32_t)di_stride * es; a.dz_s = (uint32_t)dz_stride * es;
     a.dS_in = dS_in; a.dA_log = dA_log; a.dr_bias = dr_bias; a.di_bias = di_bias;
     a.T = total_tokens; a.C = p->channels;
     if ((dS_in && copy_states(p, cu, n_seqs, dS_out, dS_in, s) != cudaSuccess) ||

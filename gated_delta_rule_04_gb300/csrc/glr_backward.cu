@@ -37,9 +37,8 @@ __global__ void __launch_bounds__(NT, PER_SM) backward_kernel(const __grid_const
     auto issue = [&](int stage) {
         const int2 tile = tk[stage];
         if (tile.x >= 0) {
-            const int64_t t = (int64_t)(g.tiles_t - 1 - tile.x) * CHUNK + warp * SUB;
-            const int c0 = tile.y * TILE_C;
-            const int rows = (int)min((int64_t)SUB, g.T - t), cols = min(TILE_C, g.C - c0);
+            const int t = (g.tiles_t - 1 - tile.x) * CHUNK + warp * SUB, c0 = tile.y * TILE_C;
+            const int rows = (int)g.T - t, cols = min(TILE_C, g.C - c0);
             const uint32_t s = mine_u + stage * TENSORS * R::BYTES;
             R::load(s, g.x, g.x_s, t, c0, rows, cols);
             R::load(s + R::BYTES, g.r, g.r_s, t, c0, rows, cols);
@@ -60,8 +59,7 @@ __global__ void __launch_bounds__(NT, PER_SM) backward_kernel(const __grid_const
     for (int stage = 0;; stage = stage + 1 == STAGES ? 0 : stage + 1, buf ^= 1) {
         const int order = tk[stage].x, tc = tk[stage].y, tt = g.tiles_t - 1 - order;
         if (order < 0) break;
-        const int64_t t = (int64_t)tt * CHUNK + warp * SUB;
-        const int c0 = tc * TILE_C, c = c0 + 2 * lane, rows = (int)min((int64_t)SUB, g.T - t), left = g.C - c;
+        const int t = tt * CHUNK + warp * SUB, c0 = tc * TILE_C, c = c0 + 2 * lane, rows = (int)g.T - t, left = g.C - c;
         const Gate k = load_gate(g, tc);
         float2 h = pair_at(g.states, tt, c, g.C);
         const Borders bd = borders(g, tt, t);
@@ -154,8 +152,8 @@ __global__ void __launch_bounds__(NT, PER_SM) backward_kernel(const __grid_const
             tk[stage] = next_tile(g);
         }
         for (int u = 0; u < warp; ++u) h = apply(sA[buf][u][lane], sB[buf][u][lane], h);
-        TI* dz = GATED ? static_cast<TI*>(g.dz) + t * g.dz_s + c : nullptr;
-        const bool whole = (bd.start | bd.end) == 0 && rows == SUB;
+        char* dz = GATED ? row_at<TI>(g.dz, g.dz_s, t, c) : nullptr;
+        const bool whole = (bd.start | bd.end) == 0 && rows >= SUB;
         auto forward = [&](auto plain) {
             constexpr bool PLAIN = decltype(plain)::value;
             const bool pz = (pairs & OUT_Z) && left > 1;
@@ -167,7 +165,8 @@ __global__ void __launch_bounds__(NT, PER_SM) backward_kernel(const __grid_const
                 h = fma2(E[j], x, ah);
                 if (GATED && (PLAIN || j < rows)) {
                     const float2 z = z_of(j), s1 = fma2(e[j], f2(-1.f), f2(1.f));
-                    put(dz + j * g.dz_s, left, pz, mul2(mul2(do_of(j), h), mul2(e[j], fma2(z, s1, f2(1.f)))));
+                    put<TI>(dz, left, pz, mul2(mul2(do_of(j), h), mul2(e[j], fma2(z, s1, f2(1.f)))));
+                    dz += g.dz_s;
                 }
             }
         };
@@ -176,8 +175,8 @@ __global__ void __launch_bounds__(NT, PER_SM) backward_kernel(const __grid_const
         __syncthreads();
         float2 carry = sIn[buf][lane], sa = f2(0.f), sr = f2(0.f), si = f2(0.f);
         for (int u = WARPS - 1; u > warp; --u) carry = apply(sAr[buf][u][lane], sBr[buf][u][lane], carry);
-        TI *dx = static_cast<TI*>(g.dx) + t * g.dx_s + c, *dr = static_cast<TI*>(g.dr) + t * g.dr_s + c,
-           *di = static_cast<TI*>(g.di) + t * g.di_s + c;
+        char *dx = row_at<TI>(g.dx, g.dx_s, t + SUB - 1, c), *dr = row_at<TI>(g.dr, g.dr_s, t + SUB - 1, c),
+             *di = row_at<TI>(g.di, g.di_s, t + SUB - 1, c);
         const bool px = (pairs & OUT_X) && left > 1, pr = (pairs & OUT_R) && left > 1, pi = (pairs & OUT_I) && left > 1;
         auto backward = [&](auto plain) {
             constexpr bool PLAIN = decltype(plain)::value;
@@ -189,13 +188,16 @@ __global__ void __launch_bounds__(NT, PER_SM) backward_kernel(const __grid_const
                 const float2 gi = mul2(mul2(gx, x_of(j)), v_[j]);
                 const float2 gA = mul2(gt, D[j]), gr = mul2(gA, rest_from(ww[j]));
                 if (PLAIN || j < rows) {
-                    put(dx + j * g.dx_s, left, px, gx);
-                    put(dr + j * g.dr_s, left, pr, gr);
-                    put(di + j * g.di_s, left, pi, gi);
+                    put<TI>(dx, left, px, gx);
+                    put<TI>(dr, left, pr, gr);
+                    put<TI>(di, left, pi, gi);
                     sa = add2(sa, gA);
                     sr = add2(sr, gr);
                     si = add2(si, gi);
                 }
+                dx -= g.dx_s;
+                dr -= g.dr_s;
+                di -= g.di_s;
                 if (!PLAIN && g.dS_in && (bd.start >> j & 1)) put(g.dS_in + seq_of(j) * g.C + c, left, false, carry);
             }
         };
@@ -273,8 +275,8 @@ cudaError_t launch_backward(const ScanArgs& a, int io_bf16, cudaStream_t s) {
     const int es = io_bf16 ? 2 : 4;
     cudaError_t e = cudaSuccess;
     if (a.tiles_t > 0) {
-        const int mode = std::max({row_mode(a.x, a.x_s, es), row_mode(a.r, a.r_s, es), row_mode(a.i, a.i_s, es),
-                                   row_mode(a.d_o, a.do_s, es), a.z ? row_mode(a.z, a.z_s, es) : 0});
+        const int mode = std::max({row_mode(a.x, a.x_s), row_mode(a.r, a.r_s), row_mode(a.i, a.i_s),
+                                   row_mode(a.d_o, a.do_s), a.z ? row_mode(a.z, a.z_s) : 0});
         const int pairs = (row_pairs(a.dx, a.dx_s, es) ? OUT_X : 0) | (row_pairs(a.dr, a.dr_s, es) ? OUT_R : 0) |
                           (row_pairs(a.di, a.di_s, es) ? OUT_I : 0) | (a.z && row_pairs(a.dz, a.dz_s, es) ? OUT_Z : 0);
         if (!io_bf16) e = mode == M16 ? backward<float, M16>(a, pairs, s) : backward<float, M4>(a, pairs, s);

@@ -23,20 +23,21 @@ struct Sequences {
 __device__ __forceinline__ int seq_id(const Sequences& f, int s) { return f.n <= INLINE_SEQS ? f.id[s] : f.d_id[s]; }
 
 // One prefill or backward call, as the kernels see it.  Rows of the token
-// tensors are `*_s` elements apart, rows of o packed.
+// tensors are `*_s` bytes apart.
 struct ScanArgs {
     const void *x, *r, *i, *z;
-    int64_t x_s, r_s, i_s, z_s;
+    uint32_t x_s, r_s, i_s, z_s;
     const float *A_log, *r_bias, *i_bias;
     const float* S_in;
     float* S_out;
     float* states;                   // [ceil(T / CHUNK)][C]: written by the prefill, read by the backward pass
     void* o;
+    uint32_t o_s;
     const void* d_o;                 // gradients from here on
-    int64_t do_s;
+    uint32_t do_s;
     const float* dS_out;
     void *dx, *dr, *di, *dz;
-    int64_t dx_s, dr_s, di_s, dz_s;
+    uint32_t dx_s, dr_s, di_s, dz_s;
     float *dS_in, *dA_log, *dr_bias, *di_bias;
     int64_t T;
     int32_t C;

@@ -19,12 +19,14 @@ namespace glr {
 namespace {
 
 constexpr int ALL = NT + 32;         // 8 warps that compute, one that walks
-constexpr int READY = 1, COME = 3;   // named barriers, two each: a tile's maps are there, its warps' first values
+// Named barriers, two each: a tile's maps are there; its warps' first values are.  (The second
+// also keeps the computing warps together: they share what they fetch of the code.  With an
+// mbarrier instead, which does not, 198 us for 189 at 16384 tokens x 4096.)
+constexpr int READY = 1, COME = 3;
 
 // What a warp keeps of a tile between its two sweeps.
 struct Pending {
     float2 a[SUB], b[SUB];
-    float2 first;                    // the start state, where the first token begins a sequence
     Borders bd;
     int tt, tc;
 };
@@ -35,19 +37,43 @@ __global__ void __launch_bounds__(ALL, PER_SM) scan_kernel(const __grid_constant
     constexpr int STAGES = 3, TENSORS = GATED ? 4 : 3;
     extern __shared__ __align__(128) unsigned char rows_smem[];    // [WARPS][STAGES][x, r, i, z]
     __shared__ int2 tk[STAGES];
+    __shared__ float2 sG[STAGES][3][32];             // the gates' constants of the tiles
     __shared__ float2 sA[2][WARPS][32], sB[2][WARPS][32], sIn[2][WARPS][32];
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     cudaGridDependencySynchronize();
-    if (tid == 0)
-        for (int k = 0; k < STAGES; ++k) tk[k] = next_tile(g);
+    auto fetch = [&](int2& tile, Gate& k) {          // the next tile, by the walking warp
+        if (lane == 0) tile = next_tile(g);
+        tile.x = __shfl_sync(0xffffffffu, tile.x, 0);
+        tile.y = __shfl_sync(0xffffffffu, tile.y, 0);
+        k = load_gate(g, tile.y);
+    };
+    auto place = [&](int stage, int2 tile, const Gate& k) {
+        if (lane == 0) tk[stage] = tile;
+        sG[stage][0][lane] = k.ea;
+        sG[stage][1][lane] = k.rb;
+        sG[stage][2][lane] = k.ib;
+    };
+    if (warp == WARPS)
+        for (int k = 0; k < STAGES; ++k) {
+            int2 tile;
+            Gate q;
+            fetch(tile, q);
+            place(k, tile, q);
+        }
     __syncthreads();
 
     if (warp == WARPS) {                             // the walk: maps of the tile's warps in, their first values out
         if (tk[0].x == 0 && tk[0].y == 0 && lane == 0) *g.status = ERR_NONE;
-        int buf = 0;
-        for (int stage = 0; tk[stage].x >= 0; stage = stage + 1 == STAGES ? 0 : stage + 1, buf ^= 1) {
+        uint32_t turn = 0;
+        for (int stage = 0; tk[stage].x >= 0; stage = stage + 1 == STAGES ? 0 : stage + 1, ++turn) {
             const int2 tile = tk[stage];
-            bar_sync(READY + buf, ALL);
+            const int buf = turn & 1;
+            int2 third;
+            Gate q;
+            fetch(third, q);
+            if (buf) bar_sync(READY + 1, ALL);
+            else bar_sync(READY, ALL);
+            place(stage, third, q);                  // (the others have read this tile's; they see it behind COME)
             float2 A[WARPS], B[WARPS];
 #pragma unroll
             for (int w = 0; w < WARPS; ++w) {
@@ -66,9 +92,8 @@ __global__ void __launch_bounds__(ALL, PER_SM) scan_kernel(const __grid_constant
                 sIn[buf][w][lane] = h;
                 h = apply(A[w], B[w], h);
             }
-            if (lane == 0) tk[stage] = next_tile(g);   // (read by the others behind the barrier)
-            __syncwarp();
-            bar_arrive(COME + buf, ALL);
+            if (buf) bar_arrive(COME + 1, ALL);
+            else bar_arrive(COME, ALL);
         }
         return;
     }
@@ -78,9 +103,8 @@ __global__ void __launch_bounds__(ALL, PER_SM) scan_kernel(const __grid_constant
     auto issue = [&](int stage) {
         const int2 tile = tk[stage];
         if (tile.x >= 0) {
-            const int64_t t = (int64_t)tile.x * CHUNK + warp * SUB;
-            const int c0 = tile.y * TILE_C;
-            const int rows = (int)min((int64_t)SUB, g.T - t), cols = min(TILE_C, g.C - c0);
+            const int t = tile.x * CHUNK + warp * SUB, c0 = tile.y * TILE_C;
+            const int rows = (int)g.T - t, cols = min(TILE_C, g.C - c0);
             const uint32_t s = mine_u + stage * TENSORS * R::BYTES;
             R::load(s, g.x, g.x_s, t, c0, rows, cols);
             R::load(s + R::BYTES, g.r, g.r_s, t, c0, rows, cols);
@@ -93,9 +117,10 @@ __global__ void __launch_bounds__(ALL, PER_SM) scan_kernel(const __grid_constant
 
     // a and b of the warp's tokens, and its map
     auto first_sweep = [&](Pending& p, int stage, int buf) {
-        const int64_t t = (int64_t)p.tt * CHUNK + warp * SUB;
-        const int c0 = p.tc * TILE_C, c = c0 + 2 * lane;
-        const Gate k = load_gate(g, p.tc);
+        p.tt = tk[stage].x;
+        p.tc = tk[stage].y;
+        const Gate k{sG[stage][0][lane], sG[stage][1][lane], sG[stage][2][lane]};
+        const int t = p.tt * CHUNK + warp * SUB, c0 = p.tc * TILE_C, c = c0 + 2 * lane;
         p.bd = borders(g, p.tt, t);
         asm volatile("cp.async.wait_group 1;" ::: "memory");
         __syncwarp();
@@ -126,7 +151,7 @@ __global__ void __launch_bounds__(ALL, PER_SM) scan_kernel(const __grid_constant
             for (int j = 0; j < SUB; ++j) {
                 if (p.bd.start >> j & 1) {           // (S_out, written in second sweeps, may be S_in: read here only)
                     const float2 h = pair_at(g.S_in, seq_of(p.bd, j), c, g.C);
-                    if (j == 0) p.first = h;
+                    if (j == 0 && warp == 0 && g.states) put(g.states + (size_t)p.tt * g.C + c, g.C - c, false, h);
                     p.b[j] = fma2(p.a[j], h, p.b[j]);
                     A = f2(-1.f);
                     B = p.b[j];
@@ -142,26 +167,27 @@ __global__ void __launch_bounds__(ALL, PER_SM) scan_kernel(const __grid_constant
     };
     // the states and outputs of a tile, once its first value is there
     auto second_sweep = [&](const Pending& p, int stage, int buf) {
-        const int64_t t = (int64_t)p.tt * CHUNK + warp * SUB;
-        const int c0 = p.tc * TILE_C, c = c0 + 2 * lane, left = g.C - c, rows = (int)min((int64_t)SUB, g.T - t);
+        const int t = p.tt * CHUNK + warp * SUB, c0 = p.tc * TILE_C, c = c0 + 2 * lane, left = g.C - c, rows = (int)g.T - t;
         const unsigned char* s = mine + stage * TENSORS * R::BYTES + 3 * R::BYTES;
         const typename R::Odd oz = R::odd(g.z, g.z_s, t, c0);
-        TI* const o = static_cast<TI*>(g.o) + t * g.C + c;
-        const bool pair = pairs && left > 1;
+        char* o = row_at<TI>(g.o, g.o_s, t, c);
+        const bool pair = pairs && left > 1, whole = pairs && c0 + TILE_C <= g.C && rows >= SUB && (p.bd.start | p.bd.end) == 0;
         bar_sync(COME + buf, ALL);
         float2 h = sIn[buf][warp][lane];
-        if (g.states && warp == 0) put(g.states + (size_t)p.tt * g.C + c, left, false, p.bd.start & 1 ? p.first : h);
-        if ((p.bd.start | p.bd.end) == 0 && rows == SUB) {
+        if (g.states && warp == 0 && !(p.bd.start & 1)) put(g.states + (size_t)p.tt * g.C + c, left, false, h);
+        if (whole) {
 #pragma unroll
             for (int j = 0; j < SUB; ++j) {
                 h = fma2(p.a[j], h, p.b[j]);
-                put(o + (int64_t)j * g.C, left, pair, GATED ? mul2(h, silu(R::get(s, j, oz))) : h);
+                put<TI>(o, 2, true, GATED ? mul2(h, silu(R::get(s, j, oz))) : h);
+                o += g.o_s;
             }
         } else {
 #pragma unroll
             for (int j = 0; j < SUB; ++j) {
                 h = p.bd.start >> j & 1 ? p.b[j] : fma2(p.a[j], h, p.b[j]);
-                if (j < rows) put(o + (int64_t)j * g.C, left, pair, GATED ? mul2(h, silu(R::get(s, j, oz))) : h);
+                if (j < rows) put<TI>(o, left, pair, GATED ? mul2(h, silu(R::get(s, j, oz))) : h);
+                o += g.o_s;
                 if (p.bd.end >> j & 1) put(g.S_out + seq_of(p.bd, j) * g.C + c, left, false, h);
             }
         }
@@ -173,23 +199,16 @@ __global__ void __launch_bounds__(ALL, PER_SM) scan_kernel(const __grid_constant
     Pending p[2];
     int stage = 0;
     auto next = [](int x) { return x + 1 == STAGES ? 0 : x + 1; };
-    const int2 t0 = tk[0];
-    if (t0.x < 0) return;
-    p[0].tt = t0.x;
-    p[0].tc = t0.y;
+    if (tk[0].x < 0) return;
     first_sweep(p[0], 0, 0);
     for (;;) {
 #pragma unroll
         for (int half = 0; half < 2; ++half) {       // tile k in p[half], tile k + 1 in p[half ^ 1]
             const int after = next(stage);
-            const int2 tile = tk[after];
-            if (tile.x >= 0) {
-                p[half ^ 1].tt = tile.x;
-                p[half ^ 1].tc = tile.y;
-                first_sweep(p[half ^ 1], after, half ^ 1);
-            }
+            const bool more = tk[after].x >= 0;
+            if (more) first_sweep(p[half ^ 1], after, half ^ 1);
             second_sweep(p[half], stage, half);
-            if (tile.x < 0) return;
+            if (!more) return;
             issue(stage);
             stage = after;
         }
@@ -253,9 +272,9 @@ cudaError_t launch_setup(const ScanArgs& a, size_t empty, cudaStream_t s) {
 
 cudaError_t launch_scan(const ScanArgs& a, int io_bf16, cudaStream_t s) {
     const int es = io_bf16 ? 2 : 4;
-    const int mode = std::max({row_mode(a.x, a.x_s, es), row_mode(a.r, a.r_s, es), row_mode(a.i, a.i_s, es),
-                               a.z ? row_mode(a.z, a.z_s, es) : 0});
-    const bool pairs = row_pairs(a.o, a.C, es);
+    const int mode = std::max({row_mode(a.x, a.x_s), row_mode(a.r, a.r_s), row_mode(a.i, a.i_s),
+                               a.z ? row_mode(a.z, a.z_s) : 0});
+    const bool pairs = row_pairs(a.o, a.o_s, es);
     if (!io_bf16) return mode == M16 ? scan<float, M16>(a, pairs, s) : scan<float, M4>(a, pairs, s);
     return mode == M16 ? scan<__nv_bfloat16, M16>(a, pairs, s)
          : mode == M4 ? scan<__nv_bfloat16, M4>(a, pairs, s) : scan<__nv_bfloat16, MODD>(a, pairs, s);

@@ -32,47 +32,60 @@ template <typename TI, int MODE> struct Rows {
         else asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(p), "r"(bytes) : "memory");
     }
 
-    // Starts the copies of rows t .. t + rows - 1, channels c0 .. c0 + cols - 1; the rest becomes zero.
-    static __device__ __forceinline__ void load(uint32_t dst, const void* base, int64_t stride, int64_t t, int c0, int rows, int cols) {
+    // Starts the copies of rows t .. t + rows - 1 (`stride` bytes apart), channels c0 .. c0 + cols - 1; the rest
+    // becomes zero.
+    static __device__ __forceinline__ void load(uint32_t dst, const void* base, uint32_t stride, int t, int c0, int rows, int cols) {
         const int lane = threadIdx.x & 31;
         const char* const first = static_cast<const char*>(base);
         if constexpr (MODE == M16) {
             constexpr int PER = PITCH / 16, STEP = 32 / PER;    // pieces of a row, rows of a copy
-            const int piece = lane % PER, row = lane / PER, bytes = min(max(cols * ES - piece * 16, 0), 16);
-            const char* p = first + ((t + row) * stride + c0) * ES + piece * 16;
+            const int piece = lane % PER, row = lane / PER;
+            const char* p = first + (uint64_t)(uint32_t)(t + row) * stride + (uint32_t)(c0 * ES + piece * 16);
+            dst += row * PITCH + piece * 16;
+            if (rows >= SUB && cols == TILE_C) {
 #pragma unroll
-            for (int k = 0; k < SUB / STEP; ++k) {
-                const int n = row + k * STEP < rows ? bytes : 0;
-                copy<16>(dst + (row + k * STEP) * PITCH + piece * 16, n > 0 ? p : first, n);
-                p += STEP * stride * ES;
+                for (int k = 0; k < SUB / STEP; ++k) {
+                    copy<16>(dst + k * STEP * PITCH, p, 16);
+                    p += (uint64_t)stride * STEP;
+                }
+            } else {
+                const int bytes = min(max(cols * ES - piece * 16, 0), 16);
+#pragma unroll
+                for (int k = 0; k < SUB / STEP; ++k) {
+                    const int n = row + k * STEP < rows ? bytes : 0;
+                    copy<16>(dst + k * STEP * PITCH, n > 0 ? p : first, n);
+                    p += (uint64_t)stride * STEP;
+                }
             }
         } else {
             constexpr int PER = PITCH / 4;                      // 32, 33 or 64 words of a row
+            const char* p = first + (uint64_t)(uint32_t)t * stride + (uint32_t)(c0 * ES);
 #pragma unroll
             for (int k = 0; k < SUB; ++k) {
-                const char* p = first + ((t + k) * stride + c0) * ES;
+                const char* q = p;
                 int bytes = k < rows ? cols * ES : 0;
                 if (MODE == MODD) {                             // from the word that holds the first element: the half
                     const int odd = (int)(reinterpret_cast<uintptr_t>(p) & 2);   // before it is copied and not used
-                    p -= odd;
+                    q -= odd;
                     bytes += bytes > 0 ? odd : 0;
                 }
 #pragma unroll
                 for (int w = lane; w < PER; w += 32) {
                     const int n = min(max(bytes - w * 4, 0), 4);
-                    copy<4>(dst + k * PITCH + w * 4, n > 0 ? p + w * 4 : first - (reinterpret_cast<uintptr_t>(first) & 2), n);
+                    copy<4>(dst + k * PITCH + w * 4, n > 0 ? q + w * 4 : first - (reinterpret_cast<uintptr_t>(first) & 2), n);
                 }
+                p += stride;
             }
         }
     }
 
     // Whether the first element of row t (channel c0) is the second of its word, and how that changes by row.
     struct Odd {
-        int first, step;
+        uint32_t first, step;
     };
-    static __device__ __forceinline__ Odd odd(const void* base, int64_t stride, int64_t t, int c0) {
+    static __device__ __forceinline__ Odd odd(const void* base, uint32_t stride, int t, int c0) {
         if (MODE != MODD) return Odd{0, 0};
-        return Odd{(int)((reinterpret_cast<uintptr_t>(base) >> 1) + (uintptr_t)(t * stride + c0)) & 1, (int)(stride & 1)};
+        return Odd{(uint32_t)reinterpret_cast<uintptr_t>(base) + (uint32_t)t * stride + (uint32_t)c0 * ES, stride};
     }
     // The lane's channel pair of a row.
     static __device__ __forceinline__ float2 get(const unsigned char* rows, int row, Odd odd) {
@@ -83,20 +96,20 @@ template <typename TI, int MODE> struct Rows {
         } else {
             const uint32_t* w = reinterpret_cast<const uint32_t*>(p) + lane;
             uint32_t u = w[0];
-            if (MODE == MODD && ((odd.first + row * odd.step) & 1)) u = __funnelshift_r(u, w[1], 16);
+            if (MODE == MODD && ((odd.first + row * odd.step) & 2)) u = __funnelshift_r(u, w[1], 16);
             return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
         }
     }
 };
 static_assert(Rows<float, M16>::PITCH == 256 && Rows<__nv_bfloat16, MODD>::PITCH == 132, "");
 
-// The copies that rows of `es`-byte elements take, and whether channel pairs can be stored as one.
-inline int row_mode(const void* base, int64_t stride, int es) {
-    const uintptr_t p = reinterpret_cast<uintptr_t>(base) | (uintptr_t)(stride * es);
+// The copies that rows take, and whether channel pairs of `es`-byte elements can be stored as one.
+inline int row_mode(const void* base, uint32_t stride) {
+    const uintptr_t p = reinterpret_cast<uintptr_t>(base) | stride;
     return p % 16 == 0 ? M16 : p % 4 == 0 ? M4 : MODD;
 }
-inline bool row_pairs(const void* base, int64_t stride, int es) {
-    return (reinterpret_cast<uintptr_t>(base) | (uintptr_t)(stride * es)) % (2 * es) == 0;
+inline bool row_pairs(const void* base, uint32_t stride, int es) {
+    return (reinterpret_cast<uintptr_t>(base) | stride) % (2 * es) == 0;
 }
 
 // Stores a lane's pair at p; `left` channels are left of the row, `pair`: both go as one.
@@ -108,6 +121,13 @@ template <typename TI> __device__ __forceinline__ void put(TI* p, int left, bool
     }
     if (left > 0) p[0] = from_f32<TI>(v.x);
     if (left > 1) p[1] = from_f32<TI>(v.y);
+}
+// Row t of a tensor whose rows are `stride` bytes apart, from channel c on.
+template <typename TI> __device__ __forceinline__ char* row_at(const void* base, uint32_t stride, int t, int c) {
+    return static_cast<char*>(const_cast<void*>(base)) + (uint64_t)(uint32_t)t * stride + (int64_t)c * (int)sizeof(TI);
+}
+template <typename TI> __device__ __forceinline__ void put(char* p, int left, bool pair, float2 v) {
+    put(reinterpret_cast<TI*>(p), left, pair, v);
 }
 // The lane's pair of row `row` of an fp32 tensor [rows][C] (NULL: zero), or its place.
 __device__ __forceinline__ float2 pair_at(const float* p, size_t row, int c, int C) {
@@ -130,8 +150,9 @@ struct Borders {
     uint32_t start, end;
     int seq;
 };
-__device__ __forceinline__ Borders borders(const ScanArgs& g, int tile_t, int64_t t) {
+__device__ __forceinline__ Borders borders(const ScanArgs& g, int tile_t, int t) {
     const int lane = threadIdx.x & 31, n = g.f.n;
+    if (n == 1 && t > 0 && t + SUB < g.T) return Borders{0, 0, 0};
     int s0 = 0;
     int64_t c1 = INT64_MAX, c2 = INT64_MAX, c0 = 0;            // starts of sequences s0 + 1 + lane, s0 + 33 + lane, s0
     if (n <= INLINE_SEQS) {
@@ -142,7 +163,7 @@ __device__ __forceinline__ Borders borders(const ScanArgs& g, int tile_t, int64_
         if (s0 + 1 + lane <= n) c1 = g.f.d_cu[s0 + 1 + lane];
         if (s0 + 33 + lane <= n) c2 = g.f.d_cu[s0 + 33 + lane];
     }
-    auto of = [&](int64_t x) {                                  // the sequence of token x of this tile, or before / behind it
+    auto of = [&](int x) {                                  // the sequence of token x of this tile, or before / behind it
         int s = s0 + __popc(__ballot_sync(0xffffffffu, c1 <= x)) - (x < c0 ? 1 : 0);
         if (n > INLINE_SEQS) s += __popc(__ballot_sync(0xffffffffu, c2 <= x));
         return s;

@@ -465,7 +465,7 @@ size_t kda_glr_backward_workspace_bytes(const kda_glr_params* p, int32_t n_seqs,
  * Stateful varlen prefill of the gated linear recurrence over n_seqs packed
  * sequences.
  *   x, r, i, z   : device io_dtype, row t at base + t * stride elements, C used;
- *                  strides (below 2^31) as for kda_ssm_prefill, 0 is packed rows
+ *                  strides (below 2^30) as for kda_ssm_prefill, 0 is packed rows
  *   cu_seqlens_host, n_seqs, total_tokens : as for kda_prefill
  *   S_in, S_out  : device [n_seqs][C] fp32; S_in NULL is zero; they may be the
  *                  same buffer

@@ -90,7 +90,7 @@ def test_bad_cu_seqlens(L, kw):
 
 
 ROWS = [dict(x=None), dict(r=None), dict(i=None), dict(x=FAKE + 1), dict(r=FAKE + 1), dict(i=FAKE + 1), dict(z=FAKE + 1),
-        dict(x_s=39), dict(r_s=-40), dict(i_s=1 << 31), dict(z_s=1)]
+        dict(x_s=39), dict(r_s=-40), dict(i_s=1 << 31), dict(x_s=1 << 30), dict(z_s=1)]
 
 
 @pytest.mark.parametrize("kw", ROWS + [dict(o=None), dict(o=FAKE + 1), dict(S_out=None), dict(S_out=FAKE + 2),
