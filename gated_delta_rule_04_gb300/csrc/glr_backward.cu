@@ -26,25 +26,35 @@ enum { OUT_X = 1, OUT_R = 2, OUT_I = 4, OUT_Z = 8 };   // gradients whose rows t
 template <typename TI, int MODE, bool GATED, int STAGES, int PER_SM>
 __global__ void __launch_bounds__(NT, PER_SM) backward_kernel(const __grid_constant__ ScanArgs g, int pairs) {
     using R = Rows<TI, MODE>;
-    constexpr int TENSORS = GATED ? 5 : 4;
-    extern __shared__ __align__(128) unsigned char rows_smem[];    // [WARPS][STAGES][x, r, i, do, z]
+    constexpr int TENSORS = GATED ? 5 : 4, GATES = 3 * TILE_C * 4, WARP_BYTES = TENSORS * R::BYTES + GATES;
+    extern __shared__ __align__(128) unsigned char rows_smem[];    // [WARPS][STAGES][x, r, i, do, z, gates]
     __shared__ int2 tk[STAGES];
-    __shared__ float2 sA[2][WARPS][32], sB[2][WARPS][32], sAr[2][WARPS][32], sBr[2][WARPS][32], sIn[2][32];
-    __shared__ float2 sums[3][WARPS][32];
+    __shared__ float2 sA[WARPS][32], sB[WARPS][32], sAr[WARPS][32], sBr[WARPS][32];   // maps forwards and backwards
+    __shared__ float2 sIn[32], sH[STAGES][32], sums[3][WARPS][32];
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-    unsigned char* const mine = rows_smem + warp * STAGES * TENSORS * R::BYTES;
+    unsigned char* const mine = rows_smem + warp * STAGES * WARP_BYTES;
     const uint32_t mine_u = ptx::smem_u32(mine);
     auto issue = [&](int stage) {
         const int2 tile = tk[stage];
         if (tile.x >= 0) {
-            const int t = (g.tiles_t - 1 - tile.x) * CHUNK + warp * SUB, c0 = tile.y * TILE_C;
+            const int tt = g.tiles_t - 1 - tile.x, t = tt * CHUNK + warp * SUB, c0 = tile.y * TILE_C;
             const int rows = (int)g.T - t, cols = min(TILE_C, g.C - c0);
-            const uint32_t s = mine_u + stage * TENSORS * R::BYTES;
+            const uint32_t s = mine_u + stage * WARP_BYTES;
             R::load(s, g.x, g.x_s, t, c0, rows, cols);
             R::load(s + R::BYTES, g.r, g.r_s, t, c0, rows, cols);
             R::load(s + 2 * R::BYTES, g.i, g.i_s, t, c0, rows, cols);
             R::load(s + 3 * R::BYTES, g.d_o, g.do_s, t, c0, rows, cols);
             if (GATED) R::load(s + 4 * R::BYTES, g.z, g.z_s, t, c0, rows, cols);
+            const char* gates = reinterpret_cast<const char*>(g.gates) + (size_t)tile.y * GATES;
+            for (int k = lane; k < GATES / 16; k += 32)
+                R::template copy<16>(s + TENSORS * R::BYTES + k * 16, gates + k * 16, 16);
+            if (warp == WARPS - 1) {                 // the tile's first state: the others see it behind a barrier
+                const uint32_t h = ptx::smem_u32(&sH[stage][0]);
+                const float* p = g.states + (size_t)tt * g.C + c0;
+#pragma unroll
+                for (int k = lane; k < TILE_C; k += 32)
+                    R::template copy<4>(h + k * 4, reinterpret_cast<const char*>(k < cols ? p + k : g.states), k < cols ? 4 : 0);
+            }
         }
         ptx::cp_async_commit();
     };
@@ -55,38 +65,46 @@ __global__ void __launch_bounds__(NT, PER_SM) backward_kernel(const __grid_const
     if (tk[0].x == 0 && tk[0].y == 0 && tid == 0) *g.status = ERR_NONE;
     for (int k = 0; k < STAGES; ++k) issue(k);
 
-    int buf = 0;
-    for (int stage = 0;; stage = stage + 1 == STAGES ? 0 : stage + 1, buf ^= 1) {
+    for (int stage = 0;; stage = stage + 1 == STAGES ? 0 : stage + 1) {
         const int order = tk[stage].x, tc = tk[stage].y, tt = g.tiles_t - 1 - order;
         if (order < 0) break;
         const int t = tt * CHUNK + warp * SUB, c0 = tc * TILE_C, c = c0 + 2 * lane, rows = (int)g.T - t, left = g.C - c;
-        const Gate k = load_gate(g, tc);
-        float2 h = pair_at(g.states, tt, c, g.C);
         const Borders bd = borders(g, tt, t);
         auto seq_of = [&](int j) { return (size_t)seq_id(g.f, bd.seq + __popc((bd.start >> 1) & ((1u << j) - 1))); };
         asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
         __syncwarp();
 
-        const unsigned char* s = mine + stage * TENSORS * R::BYTES;
+        unsigned char* const s = mine + stage * WARP_BYTES;
+        const float2* const gates = reinterpret_cast<const float2*>(s + TENSORS * R::BYTES) + lane;
+        const Gate k{gates[0], gates[TILE_C / 2], gates[TILE_C]};
         const typename R::Odd ox = R::odd(g.x, g.x_s, t, c0), orr = R::odd(g.r, g.r_s, t, c0), oi = R::odd(g.i, g.i_s, t, c0),
                               od = R::odd(g.d_o, g.do_s, t, c0), oz = R::odd(g.z, g.z_s, t, c0);
         auto x_of = [&](int j) { return R::get(s, j, ox); };
-        auto do_of = [&](int j) { return R::get(s + 3 * R::BYTES, j, od); };
-        auto z_of = [&](int j) { return R::get(s + 4 * R::BYTES, j, oz); };
-        // of each token: a, E = m v, w (with 1 - w), 1 - v, sigmoid(z), and D = dA_log / g
-        float2 a[SUB], E[SUB], ww[SUB], v_[SUB], e[SUB], D[SUB];
-        float2 A = f2(1.f), B = f2(0.f);
+        auto r_of = [&](int j) { return fma2(R::get(s + R::BYTES, j, orr), f2(-LOG2E), k.rb); };
+        // Of each token: a, w, -E = -m v, x (1 - v), K = a (v / m) x, -G.  States and gradients run with
+        // the sign changed, as -E and -G lead to them; what is stored has two such factors.
+        float2 a[SUB], w[SUB], nE[SUB], xv[SUB], K[SUB], nG[SUB];
+        float2 A = f2(1.f), nB = f2(0.f);
         auto token = [&](int j, auto wide) {
-            float2 rest;
-            const float2 w = sigmoid_of(fma2(R::get(s + R::BYTES, j, orr), f2(-LOG2E), k.rb), rest);
-            const float2 v = sigmoid_of(fma2(R::get(s + 2 * R::BYTES, j, oi), f2(-LOG2E), k.ib), v_[j]);
-            ww[j] = smaller(w, rest);
-            float2 m2;
-            const float2 la = mul2(k.ea, w), neg_la = mul2(mul2(k.ea, f2(-1.f)), w);
-            decay_of<decltype(wide)::value>(la, a[j], m2);
-            const float2 im = inv_root(m2);
-            E[j] = mul2(mul2(m2, im), v);
-            D[j] = mul2(mul2(mul2(a[j], a[j]), mul2(neg_la, im)), v);   // -(a / m)^2 b la / x
+            w[j] = sigmoid_of(r_of(j));
+            const float2 ei = ex2_most(fma2(R::get(s + 2 * R::BYTES, j, oi), f2(-LOG2E), k.ib)), di = add2(ei, f2(1.f));
+            const float2 v = make_float2(rcp(di.x), rcp(di.y)), x = x_of(j);
+            xv[j] = mul2(x, mul2(ei, v));
+            float2 nm2;
+            decay_of<decltype(wide)::value>(mul2(k.ea, w[j]), a[j], nm2);
+            const float2 iv = mul2(inv_root(nm2), v);
+            nE[j] = mul2(nm2, iv);
+            K[j] = mul2(mul2(a[j], iv), x);
+            const float2 dO = R::get(s + 3 * R::BYTES, j, od);
+            if (GATED) {
+                const float2 z = R::get(s + 4 * R::BYTES, j, oz), tz = mul2(z, f2(-LOG2E));
+                const float2 dd = fma2(make_float2(ex2(tz.x), ex2(tz.y)), f2(-1.f), f2(-1.f)), ne = make_float2(rcp(dd.x), rcp(dd.y));
+                nG[j] = mul2(dO, mul2(z, ne));
+                // -do SiLU'(z), for dz = do SiLU'(z) h
+                R::keep(s + 3 * R::BYTES, s + 4 * R::BYTES, j, mul2(dO, mul2(ne, fma2(z, add2(ne, f2(1.f)), f2(1.f)))));
+            } else {
+                nG[j] = mul2(dO, f2(-1.f));
+            }
         };
         if (any_wide(k)) {
 #pragma unroll
@@ -95,102 +113,95 @@ __global__ void __launch_bounds__(NT, PER_SM) backward_kernel(const __grid_const
 #pragma unroll
             for (int j = 0; j < SUB; ++j) token(j, std::false_type{});
         }
-        if (GATED) {
-#pragma unroll
-            for (int j = 0; j < SUB; ++j) e[j] = sigmoid_of(mul2(z_of(j), f2(-LOG2E)));
-        }
-        auto G_of = [&](int j) { return GATED ? mul2(do_of(j), mul2(z_of(j), e[j])) : do_of(j); };
-        float2 Ar = f2(1.f), Br = f2(0.f);
-        if ((bd.start | bd.end) == 0) {
+        float2 Ar = f2(1.f), nBr = f2(0.f);
+        const bool plain = (bd.start | bd.end) == 0;
+        if (plain) {
 #pragma unroll
             for (int j = 0; j < SUB; ++j) {
                 A = mul2(A, a[j]);
-                B = fma2(a[j], B, mul2(E[j], x_of(j)));
+                nB = fma2(a[j], nB, mul2(nE[j], x_of(j)));
             }
             Ar = A;
 #pragma unroll
-            for (int j = SUB - 1; j >= 0; --j) Br = mul2(a[j], add2(G_of(j), Br));
+            for (int j = SUB - 1; j >= 0; --j) nBr = mul2(a[j], add2(nG[j], nBr));
         } else {
 #pragma unroll
             for (int j = 0; j < SUB; ++j) {
-                const float2 b = mul2(E[j], x_of(j));
+                const float2 nb = mul2(nE[j], x_of(j));
                 if (bd.start >> j & 1) {
                     A = f2(-1.f);
-                    B = fma2(a[j], pair_at(g.S_in, seq_of(j), c, g.C), b);
+                    nB = fma2(a[j], neg2(pair_at(g.S_in, seq_of(j), c, g.C)), nb);
                 } else {
                     A = A.x < 0.f ? A : mul2(A, a[j]);
-                    B = fma2(a[j], B, b);
+                    nB = fma2(a[j], nB, nb);
                 }
             }
 #pragma unroll
             for (int j = SUB - 1; j >= 0; --j) {
                 if (bd.end >> j & 1) {
                     Ar = f2(-1.f);
-                    Br = pair_at(g.dS_out, seq_of(j), c, g.C);
+                    nBr = neg2(pair_at(g.dS_out, seq_of(j), c, g.C));
                 } else if (Ar.x >= 0.f) {
                     Ar = mul2(Ar, a[j]);
                 }
-                Br = mul2(a[j], add2(G_of(j), Br));
+                nBr = mul2(a[j], add2(nG[j], nBr));
             }
         }
-        sA[buf][warp][lane] = A;
-        sB[buf][warp][lane] = B;
-        sAr[buf][warp][lane] = Ar;
-        sBr[buf][warp][lane] = Br;
+        sA[warp][lane] = A;
+        sB[warp][lane] = nB;
+        sAr[warp][lane] = Ar;
+        sBr[warp][lane] = nBr;
         __syncthreads();
+        float2 nh = neg2(sH[stage][lane]);
         if (warp == 0) {
-            Ar = sAr[buf][WARPS - 1][lane];
-            Br = sBr[buf][WARPS - 1][lane];
+            Ar = sAr[WARPS - 1][lane];
+            nBr = sBr[WARPS - 1][lane];
 #pragma unroll
             for (int u = WARPS - 2; u >= 0; --u) {
-                const float2 Aw = sAr[buf][u][lane], Bw = sBr[buf][u][lane];
-                Br = apply(Aw, Bw, Br);
+                const float2 Aw = sAr[u][lane], Bw = sBr[u][lane];
+                nBr = apply(Aw, Bw, nBr);
                 Ar = Aw.x < 0.f ? Aw : Ar.x < 0.f ? Ar : mul2(Ar, Aw);
             }
-            sIn[buf][lane] = walk(g, order, tc, Ar, Br);
+            sIn[lane] = walk(g, order, tc, Ar, nBr);
         } else if (tid == 32) {
             tk[stage] = next_tile(g);
         }
-        for (int u = 0; u < warp; ++u) h = apply(sA[buf][u][lane], sB[buf][u][lane], h);
+        for (int u = 0; u < warp; ++u) nh = apply(sA[u][lane], sB[u][lane], nh);
+        const bool full = pairs == (GATED ? OUT_X | OUT_R | OUT_I | OUT_Z : OUT_X | OUT_R | OUT_I) && c0 + TILE_C <= g.C;
+        const bool whole = plain && full && rows >= SUB;
         char* dz = GATED ? row_at<TI>(g.dz, g.dz_s, t, c) : nullptr;
-        const bool whole = (bd.start | bd.end) == 0 && rows >= SUB;
-        auto forward = [&](auto plain) {
-            constexpr bool PLAIN = decltype(plain)::value;
-            const bool pz = (pairs & OUT_Z) && left > 1;
+        auto forward = [&](auto fast) {              // K becomes -dA_log / g
+            constexpr bool FAST = decltype(fast)::value;
 #pragma unroll
             for (int j = 0; j < SUB; ++j) {
-                if (!PLAIN && (bd.start >> j & 1)) h = pair_at(g.S_in, seq_of(j), c, g.C);
-                const float2 x = x_of(j), ah = mul2(a[j], h);
-                D[j] = fma2(ah, mul2(k.ea, sigmoid_from(ww[j])), mul2(D[j], x));
-                h = fma2(E[j], x, ah);
-                if (GATED && (PLAIN || j < rows)) {
-                    const float2 z = z_of(j), s1 = fma2(e[j], f2(-1.f), f2(1.f));
-                    put<TI>(dz, left, pz, mul2(mul2(do_of(j), h), mul2(e[j], fma2(z, s1, f2(1.f)))));
-                    dz += g.dz_s;
-                }
+                if (!FAST && (bd.start >> j & 1)) nh = neg2(pair_at(g.S_in, seq_of(j), c, g.C));
+                K[j] = mul2(mul2(mul2(k.ea, w[j]), a[j]), add2(K[j], nh));
+                nh = fma2(nE[j], x_of(j), mul2(a[j], nh));
+                if (GATED && (FAST || j < rows))
+                    put<TI>(dz, FAST ? 2 : left, FAST || ((pairs & OUT_Z) && left > 1),
+                            mul2(R::kept(s + 3 * R::BYTES, s + 4 * R::BYTES, j), nh));
+                if (GATED) dz += g.dz_s;
             }
         };
         if (whole) forward(std::true_type{});
         else forward(std::false_type{});
         __syncthreads();
-        float2 carry = sIn[buf][lane], sa = f2(0.f), sr = f2(0.f), si = f2(0.f);
-        for (int u = WARPS - 1; u > warp; --u) carry = apply(sAr[buf][u][lane], sBr[buf][u][lane], carry);
+        float2 carry = sIn[lane], sa = f2(0.f), sr = f2(0.f), si = f2(0.f);
+        for (int u = WARPS - 1; u > warp; --u) carry = apply(sAr[u][lane], sBr[u][lane], carry);
         char *dx = row_at<TI>(g.dx, g.dx_s, t + SUB - 1, c), *dr = row_at<TI>(g.dr, g.dr_s, t + SUB - 1, c),
              *di = row_at<TI>(g.di, g.di_s, t + SUB - 1, c);
-        const bool px = (pairs & OUT_X) && left > 1, pr = (pairs & OUT_R) && left > 1, pi = (pairs & OUT_I) && left > 1;
-        auto backward = [&](auto plain) {
-            constexpr bool PLAIN = decltype(plain)::value;
+        auto backward = [&](auto fast) {
+            constexpr bool FAST = decltype(fast)::value;
 #pragma unroll
             for (int j = SUB - 1; j >= 0; --j) {
-                if (!PLAIN && (bd.end >> j & 1)) carry = pair_at(g.dS_out, seq_of(j), c, g.C);
-                const float2 gt = add2(G_of(j), carry), gx = mul2(gt, E[j]);
-                carry = mul2(a[j], gt);
-                const float2 gi = mul2(mul2(gx, x_of(j)), v_[j]);
-                const float2 gA = mul2(gt, D[j]), gr = mul2(gA, rest_from(ww[j]));
-                if (PLAIN || j < rows) {
-                    put<TI>(dx, left, px, gx);
-                    put<TI>(dr, left, pr, gr);
-                    put<TI>(di, left, pi, gi);
+                if (!FAST && (bd.end >> j & 1)) carry = neg2(pair_at(g.dS_out, seq_of(j), c, g.C));
+                const float2 ng = add2(nG[j], carry), gx = mul2(ng, nE[j]), gi = mul2(gx, xv[j]), gA = mul2(ng, K[j]);
+                carry = mul2(a[j], ng);
+                const float2 gr = mul2(gA, mul2(ex2_most(r_of(j)), w[j]));
+                if (FAST || j < rows) {
+                    put<TI>(dx, FAST ? 2 : left, FAST || ((pairs & OUT_X) && left > 1), gx);
+                    put<TI>(dr, FAST ? 2 : left, FAST || ((pairs & OUT_R) && left > 1), gr);
+                    put<TI>(di, FAST ? 2 : left, FAST || ((pairs & OUT_I) && left > 1), gi);
                     sa = add2(sa, gA);
                     sr = add2(sr, gr);
                     si = add2(si, gi);
@@ -198,12 +209,12 @@ __global__ void __launch_bounds__(NT, PER_SM) backward_kernel(const __grid_const
                 dx -= g.dx_s;
                 dr -= g.dr_s;
                 di -= g.di_s;
-                if (!PLAIN && g.dS_in && (bd.start >> j & 1)) put(g.dS_in + seq_of(j) * g.C + c, left, false, carry);
+                if (!FAST && g.dS_in && (bd.start >> j & 1)) put(g.dS_in + seq_of(j) * g.C + c, left, false, neg2(carry));
             }
         };
         if (whole) backward(std::true_type{});
         else backward(std::false_type{});
-        issue(stage);                     // (the warp has read its rows)
+        issue(stage);                                // (the warp has read its rows, and all of them the state)
         sums[0][warp][lane] = sa;
         sums[1][warp][lane] = sr;
         sums[2][warp][lane] = si;
@@ -251,7 +262,7 @@ template <typename TI, int MODE, bool GATED>
 cudaError_t backward(const ScanArgs& a, int pairs, cudaStream_t s) {
     constexpr int STAGES = sizeof(TI) == 2 ? 2 : 1, PER_SM = 2;
     auto k = backward_kernel<TI, MODE, GATED, STAGES, PER_SM>;
-    constexpr int SMEM = WARPS * STAGES * (GATED ? 5 : 4) * Rows<TI, MODE>::BYTES;
+    constexpr int SMEM = WARPS * STAGES * ((GATED ? 5 : 4) * Rows<TI, MODE>::BYTES + 3 * TILE_C * 4);
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;

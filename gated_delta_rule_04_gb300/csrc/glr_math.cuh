@@ -41,21 +41,8 @@ __device__ __forceinline__ float2 sigmoid_of(float2 t) {
     const float2 d = add2(make_float2(ex2(t.x), ex2(t.y)), f2(1.f));
     return make_float2(rcp(d.x), rcp(d.y));
 }
-// The same, with 1 - sigmoid(x) = 2^t sigmoid(x) to its own digits.
-__device__ __forceinline__ float2 sigmoid_of(float2 t, float2& rest) {
-    // (up to 2^126, whose reciprocal is not flushed to zero)
-    const float2 e = make_float2(fminf(ex2(t.x), 8.5e37f), fminf(ex2(t.y), 8.5e37f));
-    const float2 d = add2(e, f2(1.f)), s = make_float2(rcp(d.x), rcp(d.y));
-    rest = mul2(e, s);
-    return s;
-}
-// A sigmoid and its rest in one number, both to their digits: the smaller of them, with a minus if it is the rest.
-__device__ __forceinline__ float smaller(float s, float rest) { return s < rest ? s : -rest; }
-__device__ __forceinline__ float sigmoid_from(float k) { return __float_as_int(k) < 0 ? 1.f + k : k; }
-__device__ __forceinline__ float rest_from(float k) { return __float_as_int(k) < 0 ? -k : 1.f - k; }
-__device__ __forceinline__ float2 smaller(float2 s, float2 r) { return make_float2(smaller(s.x, r.x), smaller(s.y, r.y)); }
-__device__ __forceinline__ float2 sigmoid_from(float2 k) { return make_float2(sigmoid_from(k.x), sigmoid_from(k.y)); }
-__device__ __forceinline__ float2 rest_from(float2 k) { return make_float2(rest_from(k.x), rest_from(k.y)); }
+// 2^t up to 2^126, whose reciprocal is not flushed to zero: 1 - sigmoid(x) = 2^t sigmoid(x) to its own digits
+__device__ __forceinline__ float2 ex2_most(float2 t) { return make_float2(fminf(ex2(t.x), 8.5e37f), fminf(ex2(t.y), 8.5e37f)); }
 
 // What a channel needs besides its rows: -exp(A_log), and the biases times -log2(e).
 struct Gate {
@@ -78,10 +65,10 @@ template <typename Args> __device__ __forceinline__ Gate make_gate(const Args& g
 // q = exp(la) - 1 = la P(la): P interpolates (exp(x) - 1) / x at the six Chebyshev points
 // of [-1/2, 0] (relative error 1.5e-9, in fp32 0.8 x 2^-24).  a = 1 + q is then rounded to
 // nearest, where an exponential's error has one sign that a state adds up at every
-// token, and m^2 = -q (2 + q) keeps its digits.  WIDE: la may lie below -1/2; a channel
+// token, and m^2 = -q (2 + q) keeps its digits (its negative is given).  WIDE: la may lie below -1/2; a channel
 // whose exp(A_log) is at most 1/2 never gets there.
 constexpr float NEAR = 0.5f;
-template <bool WIDE> __device__ __forceinline__ void decay_of(float2 la, float2& a, float2& m2) {
+template <bool WIDE> __device__ __forceinline__ void decay_of(float2 la, float2& a, float2& neg_m2) {
     float2 p = fma2(la, f2(-0.0011234042f), f2(-0.0081896139f));   // (of -q)
     p = fma2(la, p, f2(-0.0416300744f));
     p = fma2(la, p, f2(-0.1666624248f));
@@ -89,16 +76,16 @@ template <bool WIDE> __device__ __forceinline__ void decay_of(float2 la, float2&
     p = fma2(la, p, f2(-1.f));
     const float2 q = mul2(la, p);
     a = fma2(q, f2(-1.f), f2(1.f));
-    m2 = mul2(q, fma2(q, f2(-1.f), f2(2.f)));
+    neg_m2 = mul2(q, add2(q, f2(-2.f)));
     if (WIDE) {
-        const float2 t = mul2(la, f2(LOG2E)), e = make_float2(ex2(t.x), ex2(t.y)), em = fma2(mul2(e, f2(-1.f)), e, f2(1.f));
+        const float2 t = mul2(la, f2(LOG2E)), e = make_float2(ex2(t.x), ex2(t.y)), em = fma2(e, e, f2(-1.f));
         a = make_float2(la.x < -NEAR ? e.x : a.x, la.y < -NEAR ? e.y : a.y);
-        m2 = make_float2(la.x < -NEAR ? em.x : m2.x, la.y < -NEAR ? em.y : m2.y);
+        neg_m2 = make_float2(la.x < -NEAR ? em.x : neg_m2.x, la.y < -NEAR ? em.y : neg_m2.y);
     }
 }
 // 1 / m, finite at m = 0 (there m2 / m is 0)
-__device__ __forceinline__ float2 inv_root(float2 m2) {
-    const float2 x = add2(m2, f2(1e-36f));
+__device__ __forceinline__ float2 inv_root(float2 neg_m2) {
+    const float2 x = fma2(neg_m2, f2(-1.f), f2(1e-36f));
     return make_float2(rsq(x.x), rsq(x.y));
 }
 // Whether any of the warp's channels may have a decay's logarithm below -NEAR.
@@ -115,9 +102,9 @@ struct Step {
 template <bool WIDE> __device__ __forceinline__ Step step_of(const Gate& k, float2 x, float2 r, float2 i) {
     const float2 w = sigmoid_of(fma2(r, f2(-LOG2E), k.rb)), v = sigmoid_of(fma2(i, f2(-LOG2E), k.ib));
     Step s;
-    float2 m2;
-    decay_of<WIDE>(mul2(k.ea, w), s.a, m2);
-    s.b = mul2(mul2(make_float2(root(m2.x), root(m2.y)), v), x);
+    float2 n;
+    decay_of<WIDE>(mul2(k.ea, w), s.a, n);
+    s.b = mul2(mul2(make_float2(root(-n.x), root(-n.y)), v), x);
     return s;
 }
 __device__ __forceinline__ float2 silu(float2 z) { return mul2(z, sigmoid_of(mul2(z, f2(-LOG2E)))); }

@@ -100,6 +100,23 @@ template <typename TI, int MODE> struct Rows {
             return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
         }
     }
+    // The lane's pair of numbers in the place of a row's pairs of two tensors, read before (in MODD, whose
+    // pairs lie across words, by all lanes).
+    static __device__ __forceinline__ void keep(unsigned char* rows1, unsigned char* rows2, int row, float2 v) {
+        const int lane = threadIdx.x & 31;
+        if constexpr (ES == 4) {
+            reinterpret_cast<float2*>(rows1 + row * PITCH)[lane] = v;
+        } else {
+            if (MODE == MODD) __syncwarp();
+            reinterpret_cast<float*>(rows1 + row * PITCH)[lane] = v.x;
+            reinterpret_cast<float*>(rows2 + row * PITCH)[lane] = v.y;
+        }
+    }
+    static __device__ __forceinline__ float2 kept(const unsigned char* rows1, const unsigned char* rows2, int row) {
+        const int lane = threadIdx.x & 31;
+        if constexpr (ES == 4) return reinterpret_cast<const float2*>(rows1 + row * PITCH)[lane];
+        return make_float2(reinterpret_cast<const float*>(rows1 + row * PITCH)[lane], reinterpret_cast<const float*>(rows2 + row * PITCH)[lane]);
+    }
 };
 static_assert(Rows<float, M16>::PITCH == 256 && Rows<__nv_bfloat16, MODD>::PITCH == 132, "");
 
