@@ -1,88 +1,137 @@
 // Verification of a round's drafted tokens: the accepted path through each
 // session's nodes and the token that follows it.
 //
-// A cluster of 1 to 16 CTAs per session.  Every warp of it walks alike: lane j
-// holds nodes j and 32 + j with the target's and the drafter's probability of their
+// A cluster of 1 to 16 CTAs per session.  The first warp of each walks alike: lane
+// j holds nodes j and 32 + j with the target's and the drafter's probability of their
 // token, so that the tests of one parent are a few ballots.  What bounds the call
 // is the row behind the last accepted node: V values of p, and of q where a child was
 // refused, read once; each warp of the cluster sums a piece of it.  A row is
-// also summed where a refused child leaves siblings to be tested.  The token is found
-// by halves: CTA, warp, then the warp's piece once more from L2.
+// also summed where a refused child leaves siblings to be tested; then the sums' way
+// through the cluster (a word from each CTA to each, counted by a barrier) is
+// what counts.  The token is found by halves: CTA, warp, then the warp's piece once more from L2.
 //
-// Sums are in pairs of floats (Knuth's two-sum, Dekker's products: 48 bits) within
-// a thread and in 64 bits between threads: next to a random border, in a sum
-// over 10^5 entries, a 32-bit sum would take another token in one session of 30, and
-// this GPU adds 2 doubles a cycle and SM, where the rows arrive at 3 pairs.
+// Sums are pairs of floats (two-sums of Knuth and Dekker: 48 bits) and, where few,
+// doubles: next to a random border, in a sum over 10^5 entries, a 32-bit sum would
+// take another token in one session of 30, and this GPU adds 2 doubles a cycle and
+// SM where the rows arrive at 3 pairs.
 #include <atomic>
 
 #include "draft_verify.cuh"
+#include "tc_ptx.cuh"
 
 namespace kda {
 namespace {
 
 constexpr int NT = 256, WARPS = NT / 32, MAX_CTAS = 16, SMS = 152;
 constexpr uint32_t FULL = 0xffffffffu;
+constexpr uint64_t WAIT_NS = 2000000000ull;
 
 __device__ __forceinline__ float clean(float v) { return v > 0.f && v <= 3.402823466e38f ? v : 0.f; }
 
-// A sum as two floats; adding is exact but for the rounding of `lo`.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 sub2(float2 a, float2 b) { return __ffma2_rn(b, make_float2(-1.f, -1.f), a); }
+
+// A sum as two floats.
 struct Sum {
     float hi = 0.f, lo = 0.f;
-    __device__ __forceinline__ void add(float x) {
+    __device__ __forceinline__ void add(float x, float rest = 0.f) {
         const float s = __fadd_rn(hi, x), b = __fsub_rn(s, hi);
-        lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(x, b)));
+        const float e = __fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(x, b));
+        lo = __fadd_rn(__fadd_rn(lo, rest), e);       // (the same whichever of two sums is added to the other)
         hi = s;
     }
     __device__ __forceinline__ double value() const { return (double)hi + (double)lo; }
 };
+__device__ __forceinline__ Sum shfl_xor(Sum s, int d) {
+    Sum o;
+    o.hi = __shfl_xor_sync(FULL, s.hi, d);
+    o.lo = __shfl_xor_sync(FULL, s.lo, d);
+    return o;
+}
+// Over all lanes, the same bits in each.
+__device__ __forceinline__ Sum warp_sum(Sum s) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+        const Sum o = shfl_xor(s, d);
+        s.add(o.hi, o.lo);
+    }
+    return s;
+}
 
 // The coefficient c of W = max(p - c q, 0).
 struct Coef {
-    double c = 0.0;
     float hi = 0.f, lo = 0.f;
     __device__ __forceinline__ void set(double v) {
-        c = v;
         hi = (float)v;
         lo = (float)(v - (double)hi);
     }
+    __device__ __forceinline__ double value() const { return (double)hi + (double)lo; }
+    __device__ __forceinline__ int kind() const { return hi == 0.f ? 0 : hi == 1.f && lo == 0.f ? 1 : 2; }
 };
 enum Kind { P_ONLY, ONE, ANY };      // c = 0, c = 1 (the first refusal), any
 
-// Adds W of one token: p - c q as a pair of floats, where above zero.
-template <int KIND> __device__ __forceinline__ void add_w(Sum& s, const Coef& k, float p, float q) {
-    p = clean(p);
-    if (KIND == P_ONLY) {
-        s.add(p);
-        return;
-    }
-    q = clean(q);
-    float m = q, e = 0.f;                             // c q = m + e
+// W of one token as two floats, p and q not negative nor NaN: p - c q with c q = m + e cut off at p, so that
+// m <= p and p - m is d + r exactly (Dekker).
+template <int KIND> __device__ __forceinline__ void w_of(const Coef& k, float p, float q, float& d, float& r) {
+    float m = q, e = 0.f;
     if (KIND == ANY) {
         m = __fmul_rn(k.hi, q);
         e = __fmaf_rn(k.lo, q, __fmaf_rn(k.hi, q, -m));
+        if (!(m < p)) e = 0.f;
     }
-    const float d = __fsub_rn(p, m), b = __fsub_rn(d, p);
-    const float r = __fsub_rn(__fsub_rn(__fsub_rn(p, __fsub_rn(d, b)), __fadd_rn(m, b)), e);
-    if (__fadd_rn(d, r) > 0.f) {
-        s.add(d);
-        s.lo = __fadd_rn(s.lo, r);
-    }
+    m = fminf(m, p);
+    d = __fsub_rn(p, m);
+    r = __fsub_rn(__fsub_rn(p, d), m);
+    if (KIND == ANY) r = __fsub_rn(r, e);
 }
+
+// A lane's sums of W, of two tokens at a time side by side.  Infinities are not looked for here: they make
+// `hi` or `seen` infinite or NaN, and the piece is then summed again with cleaned values.
+struct Pairs {
+    float2 hi = make_float2(0.f, 0.f), lo = hi, seen = hi;
+    template <int KIND> __device__ __forceinline__ void add(const Coef& k, float2 p, float2 q) {
+        p = make_float2(fmaxf(p.x, 0.f), fmaxf(p.y, 0.f));        // (NaN counts as zero)
+        float2 d = p;
+        if (KIND != P_ONLY) {
+            q = make_float2(fmaxf(q.x, 0.f), fmaxf(q.y, 0.f));
+            seen = add2(seen, q);
+            float2 r;
+            if (KIND == ONE) {
+                const float2 m = make_float2(fminf(q.x, p.x), fminf(q.y, p.y));
+                d = sub2(p, m);
+                r = sub2(sub2(p, d), m);
+            } else {
+                w_of<ANY>(k, p.x, q.x, d.x, r.x);
+                w_of<ANY>(k, p.y, q.y, d.y, r.y);
+            }
+            lo = add2(lo, r);
+        }
+        const float2 s = add2(hi, d), b = sub2(s, hi);
+        lo = add2(lo, add2(sub2(hi, sub2(s, b)), sub2(d, b)));
+        hi = s;
+    }
+    __device__ __forceinline__ bool finite() const {
+        const float x = fabsf(hi.x) + fabsf(hi.y) + fabsf(seen.x) + fabsf(seen.y);
+        return x <= 3.402823466e38f;
+    }
+};
 
 template <typename TP> struct Vec;
 template <> struct Vec<float> {
     static constexpr int N = 4;
-    static __device__ __forceinline__ float get(const uint4& u, int i) { return __uint_as_float((&u.x)[i]); }
+    static __device__ __forceinline__ float2 pair(const uint4& u, int i) {
+        return make_float2(__uint_as_float((&u.x)[2 * i]), __uint_as_float((&u.x)[2 * i + 1]));
+    }
 };
 template <> struct Vec<__nv_bfloat16> {
     static constexpr int N = 8;
-    static __device__ __forceinline__ float get(const uint4& u, int i) {
-        const uint32_t w = (&u.x)[i / 2];
-        return __uint_as_float(i % 2 ? w & 0xffff0000u : w << 16);
+    static __device__ __forceinline__ float2 pair(const uint4& u, int i) {
+        const uint32_t w = (&u.x)[i];
+        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
     }
 };
 
-// A row (pair) cut into pieces, one for each warp of the cluster: piece i is [lo(i), hi(i)); all
+// A row (pair) cut into pieces, one for each warp of the cluster: piece i is [begin(i), end(i)); all
 // but the first begin on 16 bytes where p and q allow it.
 template <typename TP> struct Row {
     const TP *p, *q;
@@ -99,13 +148,15 @@ template <typename TP> struct Row {
 
 // The lane's share of the sum of W over [a, b): 16 bytes at a time from the first boundary on.
 template <int KIND, typename TP>
-__device__ __forceinline__ void sum_piece(Sum& s, const Coef& k, const Row<TP>& r, int a, int b) {
+__device__ __forceinline__ Sum sum_piece(const Coef& k, const Row<TP>& r, int a, int b) {
     constexpr int N = Vec<TP>::N, U = 4;
     const int lane = threadIdx.x & 31;
+    Pairs s;
+    auto one = [&](int y) { s.add<KIND>(k, make_float2(to_f32(r.p[y]), 0.f), make_float2(KIND ? to_f32(r.q[y]) : 0.f, 0.f)); };
     if (r.head >= 0) {
         const int va = a == 0 ? min(r.head, b) : a, nv = (b - va) / N, vb = va + nv * N;
-        if (lane < va - a) add_w<KIND>(s, k, to_f32(r.p[a + lane]), KIND ? to_f32(r.q[a + lane]) : 0.f);
-        if (lane < b - vb) add_w<KIND>(s, k, to_f32(r.p[vb + lane]), KIND ? to_f32(r.q[vb + lane]) : 0.f);
+        if (lane < va - a) one(a + lane);
+        if (lane < b - vb) one(vb + lane);
         const uint4* pv = reinterpret_cast<const uint4*>(r.p + va);
         const uint4* qv = KIND ? reinterpret_cast<const uint4*>(r.q + va) : nullptr;
         for (int i = lane; i < nv; i += 32 * U) {
@@ -119,7 +170,8 @@ __device__ __forceinline__ void sum_piece(Sum& s, const Coef& k, const Row<TP>& 
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int j = 0; j < N; ++j) add_w<KIND>(s, k, Vec<TP>::get(x[u], j), KIND ? Vec<TP>::get(y[u], j) : 0.f);
+                for (int j = 0; j < N / 2; ++j)
+                    s.add<KIND>(k, Vec<TP>::pair(x[u], j), KIND ? Vec<TP>::pair(y[u], j) : make_float2(0.f, 0.f));
         }
     } else {
         constexpr int E = 2 * U;
@@ -132,17 +184,33 @@ __device__ __forceinline__ void sum_piece(Sum& s, const Coef& k, const Row<TP>& 
                 y[u] = KIND && in ? to_f32(r.q[i + 32 * u]) : 0.f;
             }
 #pragma unroll
-            for (int u = 0; u < E; ++u) add_w<KIND>(s, k, x[u], y[u]);
+            for (int u = 0; u < E; u += 2) s.add<KIND>(k, make_float2(x[u], x[u + 1]), make_float2(y[u], y[u + 1]));
         }
     }
+    Sum t;
+    if (s.finite()) {
+        t.add(s.hi.x, s.lo.x);
+        t.add(s.hi.y, s.lo.y);
+    } else {                                          // the same elements once more, infinities counted as zero
+        const int va = r.head >= 0 ? (a == 0 ? min(r.head, b) : a) : a, step = r.head >= 0 ? N : 1, nv = (b - va) / step;
+        auto again = [&](int y) {
+            float d, e;
+            w_of<ANY>(k, clean(to_f32(r.p[y])), KIND ? clean(to_f32(r.q[y])) : 0.f, d, e);
+            t.add(d, e);
+        };
+        if (lane < va - a) again(a + lane);
+        if (lane < b - va - nv * step) again(va + nv * step + lane);
+        for (int i = lane; i < nv; i += 32)
+            for (int j = 0; j < step; ++j) again(va + i * step + j);
+    }
+    return t;
 }
 
-__device__ __forceinline__ double shfl_up(double v, int d) { return __shfl_up_sync(FULL, v, d); }
 // Inclusive sums over the lanes.
 __device__ __forceinline__ double scan(double v, int lanes) {
     const int lane = threadIdx.x & 31;
     for (int d = 1; d < lanes; d <<= 1) {
-        const double u = shfl_up(v, d);
+        const double u = __shfl_up_sync(FULL, v, d);
         if (lane >= d) v += u;
     }
     return v;
@@ -153,9 +221,23 @@ __device__ __forceinline__ int pick(double incl, double share, double goal) {
     return over ? __ffs(over) - 1 : any ? 31 - __clz(any) : -1;
 }
 
+// What the first warp asks of the others.
+enum Ask { SUM, SEARCH, END };
+struct Order {
+    int ask, then;                   // SUM or END; behind the sum: SUM (another one), SEARCH or END
+    int cur, refused, piece;         // the current node; tokens refused there, taken out of W; (SEARCH) the piece
+    float2 c;
+    double base, goal;               // (SEARCH) the sum before the piece, and the one to be passed
+    int tok[KDA_TREE_MAX_NODES];
+    float p[KDA_TREE_MAX_NODES];
+};
+
 template <typename TP>
 __global__ void __launch_bounds__(NT) verify_kernel(const __grid_constant__ VerifyArgs g, int ctas) {
-    __shared__ double wsum[WARPS], slots[2][MAX_CTAS], twarp[WARPS];
+    __shared__ Order order;
+    __shared__ float2 wsum[WARPS], slots[2][MAX_CTAS];
+    __shared__ uint64_t bars[2];
+    __shared__ double twarp[WARPS];
     __shared__ int best, last;
     const int s = blockIdx.x / ctas, rank = blockIdx.x % ctas, tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int R = g.R, V = g.V, pieces = ctas * WARPS;
@@ -168,179 +250,261 @@ __global__ void __launch_bounds__(NT) verify_kernel(const __grid_constant__ Veri
         if (r >= 0) return static_cast<const TP*>(g.q) + s * g.q_ss + r * g.q_rs;
         return g.q_last ? static_cast<const TP*>(g.q_last) + s * g.ql_s : nullptr;
     };
+    if (tid == 0) {
+        ptx::mbar_init(ptx::smem_u32(&bars[0]), 1);
+        ptx::mbar_init(ptx::smem_u32(&bars[1]), 1);
+        ptx::fence_mbar_init();
+    }
+    __syncthreads();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");   // (the barriers are there; waited for below)
+
+    // ---- the first warp: tests, and what a sum over the row comes to
     const bool hot = g.q == nullptr;                  // chosen tokens: q is one at the child's own
-    // the lane's two nodes; an entry that leaves one out makes its parent -2
-    int tok[2], par[2];
-    float u[2], pt[2], qt[2];
+    int tok[2] = {-1, -1}, par[2] = {-2, -2};         // the lane's two nodes; parent -2: left out
+    float u[2] = {0.f, 0.f}, pt[2] = {0.f, 0.f}, qt[2] = {0.f, 0.f};
+    uint64_t at_once = 0;                             // accepted as the first child that its parent tests (c = 0, T = 1)
+    auto nodes = [&](bool a, bool b) { return (uint64_t)__ballot_sync(FULL, a) | (uint64_t)__ballot_sync(FULL, b) << 32; };
+    auto of = [&](auto (&v)[2], int r) { return __shfl_sync(FULL, r < 32 ? v[0] : v[1], r & 31); };
+    if (warp == 0) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int r = lane + 32 * h;
-        tok[h] = -1;
-        par[h] = -2;
-        u[h] = pt[h] = qt[h] = 0.f;
-        if (r < R) {
-            tok[h] = g.tokens[(size_t)s * R + r];
-            par[h] = g.parents[(size_t)s * R + r];
-            u[h] = g.u[(size_t)s * R + r];
+        for (int h = 0; h < 2; ++h) {
+            const int r = lane + 32 * h;
+            if (r < R) {
+                tok[h] = g.tokens[(size_t)s * R + r];
+                par[h] = g.parents[(size_t)s * R + r];
+                u[h] = g.u[(size_t)s * R + r];
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int r = lane + 32 * h;
             if (par[h] < -1 || par[h] >= r || tok[h] < 0 || tok[h] >= V) par[h] = -2;
             if (par[h] >= -1 && p_row(par[h])) {
                 pt[h] = clean(to_f32(p_row(par[h])[tok[h]]));
                 qt[h] = hot ? 1.f : clean(to_f32(q_row(par[h])[tok[h]]));
             }
         }
+        auto first_test = [&](int h) { return pt[h] > 0.f && (double)u[h] * (double)qt[h] < (double)pt[h]; };
+        at_once = nodes(first_test(0), first_test(1));
     }
-    auto nodes = [&](bool a, bool b) { return (uint64_t)__ballot_sync(FULL, a) | (uint64_t)__ballot_sync(FULL, b) << 32; };
-    auto of = [&](auto (&v)[2], int r) { return __shfl_sync(FULL, r < 32 ? v[0] : v[1], r & 31); };
-    // accepted as the first child that its parent tests (c = 0, T = 1)
-    auto first_test = [&](int h) { return pt[h] > 0.f && (double)u[h] * (double)qt[h] < (double)pt[h]; };
-    const uint64_t at_once = nodes(first_test(0), first_test(1));
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 
-    // W of the current node: all CTAs and warps alike
-    int cur = -1, len = 0, turn = 0;
+    int cur = -1, len = 0;
+    uint32_t turn = 0;
+    uint64_t children = 0, refused = 0;               // to be tested at cur; (chosen tokens) refused, taken out of W
+    bool first = true, arrived = true, ending = false, dead = false;
     Coef c;
-    double T = 1.0;
-    uint64_t refused = 0;                             // (chosen tokens) those that left something out of W
-    double mine = 0.0, incl = 0.0;                    // a pass's sum of CTA `lane`, and the inclusive ones
-    auto pass = [&]() -> double {                     // sums W over the row; leaves wsum, mine and incl
-        const Row<TP> row(p_row(cur), c.c > 0.0 ? q_row(cur) : nullptr, V, pieces);
-        const int piece = rank * WARPS + warp, a = row.begin(piece), b = row.end(piece, pieces);
-        Sum sum;
-        if (c.c == 0.0) sum_piece<P_ONLY>(sum, c, row, a, b);
-        else if (c.c == 1.0) sum_piece<ONE>(sum, c, row, a, b);
-        else sum_piece<ANY>(sum, c, row, a, b);
-#pragma unroll
-        for (int h = 0; h < 2; ++h)                   // (p is what was added: the sum stays exact)
-            if ((refused >> (lane + 32 * h) & 1) && tok[h] >= a && tok[h] < b) sum.add(-pt[h]);
-        double v = sum.value();
-        for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(FULL, v, d);
-        if (lane == 0) wsum[warp] = v;
-        __syncthreads();
-        const int buf = turn++ & 1;
-        if (warp == 0) {
-            v = scan(lane < WARPS ? wsum[lane] : 0.0, WARPS);
-            v = __shfl_sync(FULL, v, WARPS - 1);
-            if (lane < ctas) {
-                uint32_t at = (uint32_t)__cvta_generic_to_shared(&slots[buf][rank]);
-                asm volatile("mapa.shared::cluster.u32 %0, %0, %1;" : "+r"(at) : "r"(lane));
-                asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(at), "d"(v) : "memory");
-            }
-        }
-        asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
-        mine = lane < ctas ? slots[buf][lane] : 0.0;
-        incl = scan(mine, MAX_CTAS);
-        return __shfl_sync(FULL, incl, MAX_CTAS - 1);
-    };
+    double T = 1.0, share = 0.0, total = 0.0;         // share: the sum of CTA `lane`
 
-    while (len < g.max_len) {
-        uint64_t left = nodes(par[0] == cur, par[1] == cur);
-        int to = -1;
-        bool first = true;
-        while (left) {
-            const int r = __ffsll((long long)left) - 1;
-            left &= left - 1;
-            if (p_row(cur) == nullptr) {              // the token that was chosen already
-                to = r;
-                break;
+    // Goes on with the tests until a sum is needed: true, or the walk has ended: false.
+    auto go = [&]() -> bool {
+        for (;;) {
+            if (arrived) {
+                if (len == g.max_len) return false;
+                children = nodes(par[0] == cur, par[1] == cur);
+                arrived = false;
             }
-            double w = (double)of(pt, r);
-            if (first) {
-                if (at_once >> r & 1) to = r;
+            if (!children) return false;
+            const int r = __ffsll((long long)children) - 1;
+            children &= children - 1;
+            bool yes = false;
+            double w = 0.0;
+            if (p_row(cur) == nullptr) {              // the token that was chosen already
+                yes = true;
+            } else if (first) {
+                w = (double)of(pt, r);
+                yes = at_once >> r & 1;
             } else {
                 const double q = (double)of(qt, r);
+                w = (double)of(pt, r);
                 if (hot) {
                     const int x = of(tok, r);
                     if (refused & nodes(tok[0] == x, tok[1] == x)) w = 0.0;
                 } else {
-                    w = fmax(w - c.c * q, 0.0);
+                    w = fmax(w - c.value() * q, 0.0);
                 }
-                if (w > 0.0 && (double)of(u, r) * T * q < w) to = r;
+                yes = w > 0.0 && (double)of(u, r) * T * q < w;
             }
-            if (to >= 0) break;
+            if (yes) {
+                if (rank == 0 && lane == 0) g.path[(size_t)s * g.max_len + len] = r;
+                ++len;
+                cur = r;
+                c = Coef{};
+                T = 1.0;
+                refused = 0;
+                first = arrived = true;
+                continue;
+            }
             first = false;
             if (hot) {
                 T -= w;
                 if (w > 0.0) refused |= (uint64_t)1 << r;
             } else {
-                c.set(c.c + T);
-                if (left) T = pass();
+                c.set(c.value() + T);
+                if (children) return true;
             }
         }
-        if (to < 0) break;
-        if (rank == 0 && tid == 0) g.path[(size_t)s * g.max_len + len] = to;
-        ++len;
-        cur = to;
-        c.set(0.0);
-        T = 1.0;
-        refused = 0;
-    }
-    if (rank == 0) {
-        for (int j = len + tid; j < g.max_len; j += NT) g.path[(size_t)s * g.max_len + j] = -1;
-        if (tid == 0) g.path_len[s] = len;
-    }
-    if (p_row(cur) == nullptr) {                      // not even the chosen token is there
-        if (rank == 0 && tid == 0) g.next[s] = -1;
-        return;
-    }
-    double total = pass();
-    if (!(total > 0.0) && (c.c > 0.0 || refused)) {   // nothing is left: p itself
-        c.set(0.0);
-        refused = 0;
-        total = pass();
-    }
-    const double goal = (double)g.u_next[s] * total;
-    const int owner = pick(incl, mine, goal);
-    if (owner < 0) {
-        if (rank == 0 && tid == 0) g.next[s] = -1;
-        return;
-    }
-    if (owner != rank) return;
-    // the warp's piece that holds the token, once more: a few neighbouring entries a thread
-    double base = __shfl_sync(FULL, incl - mine, owner);
-    {
-        const double w = lane < WARPS ? wsum[lane] : 0.0, in = scan(w, WARPS);
-        const int at = pick(base + in, w, goal);
-        base += __shfl_sync(FULL, in - w, at);
-        const Row<TP> row(p_row(cur), c.c > 0.0 ? q_row(cur) : nullptr, V, pieces);
-        const int a = row.begin(rank * WARPS + at), b = row.end(rank * WARPS + at, pieces), per = (b - a + NT - 1) / NT;
-        const int y0 = (int)min((int64_t)b, a + (int64_t)tid * per), y1 = min(b, y0 + per);
-        auto entry = [&](int y) -> double {           // W(y)
-            for (uint64_t m = refused; m; m &= m - 1)
-                if (g.tokens[(size_t)s * R + __ffsll((long long)m) - 1] == y) return 0.0;
-            Sum e;
-            const float p = to_f32(row.p[y]);
-            if (c.c == 0.0) add_w<P_ONLY>(e, c, p, 0.f);
-            else add_w<ANY>(e, c, p, to_f32(row.q[y]));
-            return e.value();
-        };
-        double v = 0.0;
-        for (int y = y0; y < y1; ++y) v += entry(y);
-        double in2 = scan(v, 32);
-        if (lane == 31) twarp[warp] = in2;
+    };
+    // This CTA's sum to all, all CTAs' sums here: `share` and their `total`.
+    auto exchange = [&]() {
+        const int buf = turn & 1;
+        Sum v;
+        if (lane < WARPS) {
+            v.hi = wsum[lane].x;
+            v.lo = wsum[lane].y;
+        }
+        v = warp_sum(v);
+        if (ctas > 1) {
+            const uint32_t bar = ptx::smem_u32(&bars[buf]);
+            if (lane == 0) ptx::mbar_expect_tx(bar, ctas * 8);
+            __syncwarp();
+            if (lane < ctas) {
+                uint32_t to = ptx::smem_u32(&slots[buf][rank]), tobar = bar;
+                asm volatile("mapa.shared::cluster.u32 %0, %0, %1;" : "+r"(to) : "r"(lane));
+                asm volatile("mapa.shared::cluster.u32 %0, %0, %1;" : "+r"(tobar) : "r"(lane));
+                asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];"
+                             ::"r"(to), "f"(v.hi), "f"(v.lo), "r"(tobar) : "memory");
+            }
+            const bool there = dead || ptx::mbar_wait(bar, turn >> 1 & 1, WAIT_NS);
+            dead = __any_sync(FULL, !there) || dead;  // gave up: the token will be -1
+            const float2 x = lane < ctas ? slots[buf][lane] : make_float2(0.f, 0.f);
+            v.hi = x.x;
+            v.lo = x.y;
+            ++turn;
+        } else if (lane > 0) {
+            v = Sum{};
+        }
+        share = v.value();
+        total = warp_sum(v).value();
+        if (dead) share = total = 0.0;
+    };
+
+    for (;;) {
+        if (warp == 0) {
+            if (!ending && !go()) ending = true;
+            if (lane == 0) {
+                order.ask = ending && p_row(cur) == nullptr ? END : SUM;   // (END: not even the chosen token is there)
+                order.cur = cur;
+                order.c = make_float2(c.hi, c.lo);
+                order.refused = 0;
+            }
+            __syncwarp();
+            if (refused) {                            // a list of the tokens, in the order of the nodes
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int r = lane + 32 * h;
+                    if (refused >> r & 1) {
+                        const int at = __popcll(refused & (((uint64_t)1 << r) - 1));
+                        order.tok[at] = tok[h];
+                        order.p[at] = pt[h];
+                    }
+                }
+                if (lane == 0) order.refused = __popcll(refused);
+            }
+        }
+        __syncthreads();
+        if (order.ask == END) break;
+        const int node = order.cur;
+        Coef k;
+        k.hi = order.c.x;
+        k.lo = order.c.y;
+        const Row<TP> row(p_row(node), k.kind() ? q_row(node) : nullptr, V, pieces);
+        {
+            const int a = row.begin(rank * WARPS + warp), b = row.end(rank * WARPS + warp, pieces);
+            Sum sum = k.kind() == P_ONLY ? sum_piece<P_ONLY>(k, row, a, b)
+                    : k.kind() == ONE ? sum_piece<ONE>(k, row, a, b) : sum_piece<ANY>(k, row, a, b);
+            for (int j = lane; j < order.refused; j += 32)        // (p is what was added: the sum stays exact)
+                if (order.tok[j] >= a && order.tok[j] < b) sum.add(-order.p[j]);
+            sum = warp_sum(sum);
+            if (lane == 0) wsum[warp] = make_float2(sum.hi, sum.lo);
+        }
+        __syncthreads();
+        if (warp == 0) {
+            exchange();
+            int then = SUM;
+            if (!ending) {
+                T = total;
+            } else if (!(total > 0.0) && (k.kind() || refused)) {
+                c = Coef{};                           // nothing is left: p itself
+                refused = 0;
+            } else {
+                const double goal = (double)g.u_next[s] * total, incl = scan(share, MAX_CTAS);
+                const int owner = pick(incl, share, goal);
+                then = END;
+                if (owner < 0) {
+                    if (rank == 0 && lane == 0) g.next[s] = -1;
+                } else if (owner == rank) {           // the warp whose piece holds the token
+                    double base = __shfl_sync(FULL, incl - share, owner);
+                    const double w = lane < WARPS ? (double)wsum[lane].x + (double)wsum[lane].y : 0.0, in = scan(w, WARPS);
+                    const int at = max(pick(base + in, w, goal), 0);
+                    base += __shfl_sync(FULL, in - w, at);
+                    then = SEARCH;
+                    if (lane == 0) {
+                        order.piece = rank * WARPS + at;
+                        order.base = base;
+                        order.goal = goal;
+                    }
+                }
+            }
+            if (lane == 0) order.then = then;
+        }
         if (tid == 0) {
             best = NT;
             last = -1;
         }
         __syncthreads();
-        for (int k = 0; k < warp; ++k) base += twarp[k];
-        if (v > 0.0) {
-            if (base + in2 > goal) atomicMin(&best, tid);
+        if (order.then == END) break;
+        if (order.then == SUM) continue;
+        // the piece that holds the token, once more: a few neighbouring entries a thread
+        const int a = row.begin(order.piece), b = row.end(order.piece, pieces), per = (b - a + NT - 1) / NT;
+        const int y0 = (int)min((int64_t)b, a + (int64_t)tid * per), y1 = min(b, y0 + per);
+        auto entry = [&](int y, float& d, float& r) {             // W(y)
+            w_of<ANY>(k, clean(to_f32(row.p[y])), row.q ? clean(to_f32(row.q[y])) : 0.f, d, r);
+            for (int j = 0; j < order.refused; ++j)
+                if (order.tok[j] == y) d = r = 0.f;
+        };
+        Sum v;
+        for (int y = y0; y < y1; ++y) {
+            float d, r;
+            entry(y, d, r);
+            v.add(d, r);
+        }
+        const double mine = v.value(), in = scan(mine, 32);
+        if (lane == 31) twarp[warp] = in;
+        __syncthreads();
+        double base = order.base;
+        for (int j = 0; j < warp; ++j) base += twarp[j];
+        if (mine > 0.0) {
+            if (base + in > order.goal) atomicMin(&best, tid);
             atomicMax(&last, tid);
         }
         __syncthreads();
-        if (tid == (best < NT ? best : last)) {
-            double run = base + (in2 - v);
+        if (tid == (best < NT ? best : max(last, 0))) {
+            double run = base + (in - mine);
             int next = -1;
             for (int y = y0; y < y1; ++y) {
-                const double x = entry(y);
-                if (!(x > 0.0)) continue;
+                float d, r;
+                entry(y, d, r);
+                if (!(__fadd_rn(d, r) > 0.f)) continue;
                 next = y;
-                run += x;
-                if (run > goal) break;
+                run += (double)d + (double)r;
+                if (run > order.goal) break;
             }
             g.next[s] = next;
         }
-        if (tid == 0 && best == NT && last < 0) g.next[s] = -1;   // (not with a positive sum)
+        break;
     }
+    if (warp == 0 && rank == 0) {
+        for (int j = len + lane; j < g.max_len; j += 32) g.path[(size_t)s * g.max_len + j] = -1;
+        if (lane == 0) {
+            g.path_len[s] = len;
+            if (p_row(cur) == nullptr) g.next[s] = -1;
+        }
+    }
+    __syncwarp();
+    // no CTA leaves while another may still write to it
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 template <typename TP> cudaError_t verify(const VerifyArgs& a, int ctas, cudaStream_t s) {
