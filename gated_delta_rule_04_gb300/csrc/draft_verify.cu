@@ -22,7 +22,7 @@
 namespace kda {
 namespace {
 
-constexpr int NT = 256, WARPS = NT / 32, MAX_CTAS = 16, SMS = 152;
+constexpr int NT = 256, WARPS = NT / 32, MAX_CTAS = 16, SMS = 152, PER_SM = 4;
 constexpr uint32_t FULL = 0xffffffffu;
 constexpr uint64_t WAIT_NS = 2000000000ull;
 
@@ -149,7 +149,7 @@ template <typename TP> struct Row {
 // The lane's share of the sum of W over [a, b): 16 bytes at a time from the first boundary on.
 template <int KIND, typename TP>
 __device__ __forceinline__ Sum sum_piece(const Coef& k, const Row<TP>& r, int a, int b) {
-    constexpr int N = Vec<TP>::N, U = 4;
+    constexpr int N = Vec<TP>::N, U = 2;
     const int lane = threadIdx.x & 31;
     Pairs s;
     auto one = [&](int y) { s.add<KIND>(k, make_float2(to_f32(r.p[y]), 0.f), make_float2(KIND ? to_f32(r.q[y]) : 0.f, 0.f)); };
@@ -159,22 +159,32 @@ __device__ __forceinline__ Sum sum_piece(const Coef& k, const Row<TP>& r, int a,
         if (lane < b - vb) one(vb + lane);
         const uint4* pv = reinterpret_cast<const uint4*>(r.p + va);
         const uint4* qv = KIND ? reinterpret_cast<const uint4*>(r.q + va) : nullptr;
-        for (int i = lane; i < nv; i += 32 * U) {
-            uint4 x[U], y[U];
+        // two batches of loads in turn, one on its way while the other is summed
+        uint4 x[2][U], y[2][U];
+        auto load = [&](uint4 (&px)[U], uint4 (&qx)[U], int i) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const bool in = i + 32 * u < nv;
-                x[u] = in ? __ldcs(pv + i + 32 * u) : make_uint4(0, 0, 0, 0);
-                if (KIND) y[u] = in ? __ldcs(qv + i + 32 * u) : make_uint4(0, 0, 0, 0);
+                px[u] = in ? __ldcs(pv + i + 32 * u) : make_uint4(0, 0, 0, 0);
+                if (KIND) qx[u] = in ? __ldcs(qv + i + 32 * u) : make_uint4(0, 0, 0, 0);
             }
+        };
+        auto sum = [&](const uint4 (&px)[U], const uint4 (&qx)[U]) {
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
                 for (int j = 0; j < N / 2; ++j)
-                    s.add<KIND>(k, Vec<TP>::pair(x[u], j), KIND ? Vec<TP>::pair(y[u], j) : make_float2(0.f, 0.f));
+                    s.add<KIND>(k, Vec<TP>::pair(px[u], j), KIND ? Vec<TP>::pair(qx[u], j) : make_float2(0.f, 0.f));
+        };
+        load(x[0], y[0], lane);
+        for (int i = lane; i < nv; i += 64 * U) {
+            load(x[1], y[1], i + 32 * U);
+            sum(x[0], y[0]);
+            load(x[0], y[0], i + 64 * U);
+            sum(x[1], y[1]);
         }
     } else {
-        constexpr int E = 2 * U;
+        constexpr int E = 8;
         for (int i = a + lane; i < b; i += 32 * E) {
             float x[E], y[E];
 #pragma unroll
@@ -233,7 +243,7 @@ struct Order {
 };
 
 template <typename TP>
-__global__ void __launch_bounds__(NT) verify_kernel(const __grid_constant__ VerifyArgs g, int ctas) {
+__global__ void __launch_bounds__(NT, PER_SM) verify_kernel(const __grid_constant__ VerifyArgs g, int ctas) {
     __shared__ Order order;
     __shared__ float2 wsum[WARPS], slots[2][MAX_CTAS];
     __shared__ uint64_t bars[2];
@@ -537,10 +547,10 @@ template <typename TP> cudaError_t verify(const VerifyArgs& a, int ctas, cudaStr
 }  // namespace
 
 cudaError_t launch_verify(const VerifyArgs& a, int io_bf16, cudaStream_t s) {
-    // CTAs a session: enough for four an SM, while each warp's piece is at least 512 bytes
+    // CTAs a session: as many as all run at once, while each warp's piece is at least 512 bytes
     int ctas = 1;
     const int64_t bytes = (int64_t)a.V * (io_bf16 ? 2 : 4);
-    while (ctas < MAX_CTAS && (int64_t)a.n * ctas < 4 * SMS && bytes >= (int64_t)ctas * 2 * WARPS * 512) ctas *= 2;
+    while (ctas < MAX_CTAS && (int64_t)a.n * ctas * 2 <= PER_SM * SMS && bytes >= (int64_t)ctas * 2 * WARPS * 512) ctas *= 2;
     return io_bf16 ? verify<__nv_bfloat16>(a, ctas, s) : verify<float>(a, ctas, s);
 }
 
