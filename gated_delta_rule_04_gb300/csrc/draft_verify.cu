@@ -24,6 +24,7 @@ namespace {
 
 constexpr int NT = 256, WARPS = NT / 32, MAX_CTAS = 16, SMS = 152, PER_SM = 4;
 constexpr uint32_t FULL = 0xffffffffu;
+constexpr int PARTS = 64, LAST = 128;                // of the search: parts of a piece, entries of a part's step
 constexpr uint64_t WAIT_NS = 2000000000ull;
 
 __device__ __forceinline__ float clean(float v) { return v > 0.f && v <= 3.402823466e38f ? v : 0.f; }
@@ -235,9 +236,10 @@ __device__ __forceinline__ int pick(double incl, double share, double goal) {
 enum Ask { SUM, SEARCH, END };
 struct Order {
     int ask, then;                   // SUM or END; behind the sum: SUM (another one), SEARCH or END
-    int cur, refused, piece;         // the current node; tokens refused there, taken out of W; (SEARCH) the piece
+    int cur, refused;                // the current node; tokens refused there, taken out of W
     float2 c;
-    double base, goal;               // (SEARCH) the sum before the piece, and the one to be passed
+    int a, b;                        // (SEARCH) where the token is,
+    double base, goal;               // the sum before that, and the one to be passed
     int tok[KDA_TREE_MAX_NODES];
     float p[KDA_TREE_MAX_NODES];
 };
@@ -247,8 +249,7 @@ __global__ void __launch_bounds__(NT, PER_SM) verify_kernel(const __grid_constan
     __shared__ Order order;
     __shared__ float2 wsum[WARPS], slots[2][MAX_CTAS];
     __shared__ uint64_t bars[2];
-    __shared__ double twarp[WARPS];
-    __shared__ int best, last;
+    __shared__ float2 psum[PARTS];
     const int s = blockIdx.x / ctas, rank = blockIdx.x % ctas, tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int R = g.R, V = g.V, pieces = ctas * WARPS;
     auto p_row = [&](int r) -> const TP* {
@@ -451,7 +452,9 @@ __global__ void __launch_bounds__(NT, PER_SM) verify_kernel(const __grid_constan
                     base += __shfl_sync(FULL, in - w, at);
                     then = SEARCH;
                     if (lane == 0) {
-                        order.piece = rank * WARPS + at;
+                        const Row<TP> row(p_row(cur), c.kind() ? q_row(cur) : nullptr, V, pieces);
+                        order.a = row.begin(rank * WARPS + at);
+                        order.b = row.end(rank * WARPS + at, pieces);
                         order.base = base;
                         order.goal = goal;
                     }
@@ -459,49 +462,73 @@ __global__ void __launch_bounds__(NT, PER_SM) verify_kernel(const __grid_constan
             }
             if (lane == 0) order.then = then;
         }
-        if (tid == 0) {
-            best = NT;
-            last = -1;
-        }
         __syncthreads();
         if (order.then == END) break;
         if (order.then == SUM) continue;
-        // the piece that holds the token, once more: a few neighbouring entries a thread
-        const int a = row.begin(order.piece), b = row.end(order.piece, pieces), per = (b - a + NT - 1) / NT;
-        const int y0 = (int)min((int64_t)b, a + (int64_t)tid * per), y1 = min(b, y0 + per);
-        auto entry = [&](int y, float& d, float& r) {             // W(y)
-            w_of<ANY>(k, clean(to_f32(row.p[y])), row.q ? clean(to_f32(row.q[y])) : 0.f, d, r);
+        // The warp's piece once more: while it is long, in 64 parts whose sums lie in shared memory; then by
+        // one warp, 16 neighbouring entries a lane.
+        auto entry = [&](int y, bool in, float& d, float& r) {    // W(y)
+            w_of<ANY>(k, in ? clean(to_f32(row.p[y])) : 0.f, in && row.q ? clean(to_f32(row.q[y])) : 0.f, d, r);
             for (int j = 0; j < order.refused; ++j)
                 if (order.tok[j] == y) d = r = 0.f;
         };
-        Sum v;
-        for (int y = y0; y < y1; ++y) {
-            float d, r;
-            entry(y, d, r);
-            v.add(d, r);
-        }
-        const double mine = v.value(), in = scan(mine, 32);
-        if (lane == 31) twarp[warp] = in;
-        __syncthreads();
-        double base = order.base;
-        for (int j = 0; j < warp; ++j) base += twarp[j];
-        if (mine > 0.0) {
-            if (base + in > order.goal) atomicMin(&best, tid);
-            atomicMax(&last, tid);
-        }
-        __syncthreads();
-        if (tid == (best < NT ? best : max(last, 0))) {
-            double run = base + (in - mine);
-            int next = -1;
-            for (int y = y0; y < y1; ++y) {
-                float d, r;
-                entry(y, d, r);
-                if (!(__fadd_rn(d, r) > 0.f)) continue;
-                next = y;
-                run += (double)d + (double)r;
-                if (run > order.goal) break;
+        while (order.b - order.a > 4 * LAST) {
+            const int a = order.a, b = order.b, size = (int)(((int64_t)b - a + PARTS * LAST - 1) / (PARTS * LAST)) * LAST;
+#pragma unroll 4
+            for (int i = 0; i < PARTS / WARPS; ++i) {
+                const int part = i * WARPS + warp;
+                const int from = (int)min((int64_t)b, a + (int64_t)part * size), to = (int)min((int64_t)b, (int64_t)from + size);
+                Sum v;
+                for (int y0 = from; y0 < to; y0 += LAST) {
+                    float d[LAST / 32], r[LAST / 32];
+#pragma unroll
+                    for (int e = 0; e < LAST / 32; ++e) entry(y0 + 32 * e + lane, y0 + 32 * e + lane < to, d[e], r[e]);
+#pragma unroll
+                    for (int e = 0; e < LAST / 32; ++e) v.add(d[e], r[e]);
+                }
+                v = warp_sum(v);
+                if (lane == 0) psum[part] = make_float2(v.hi, v.lo);
             }
-            g.next[s] = next;
+            __syncthreads();
+            if (warp == 0) {                          // lane j has parts 2 j and 2 j + 1
+                const double lo = (double)psum[2 * lane].x + (double)psum[2 * lane].y;
+                const double both = lo + ((double)psum[2 * lane + 1].x + (double)psum[2 * lane + 1].y), in = scan(both, 32);
+                const int at = max(pick(order.base + in, both, order.goal), 0);
+                if (lane == at) {
+                    const double base = order.base + (in - both);
+                    const bool second = !(lo > 0.0 && base + lo > order.goal) && both > lo;
+                    const int from = (int)min((int64_t)b, a + (int64_t)(2 * at + second) * size);
+                    order.a = from;
+                    order.b = (int)min((int64_t)b, (int64_t)from + size);
+                    order.base = second ? base + lo : base;
+                }
+            }
+            __syncthreads();
+        }
+        if (warp == 0) {
+            int a = order.a, b = order.b;
+            const int per = (b - a + 31) / 32;        // at most 16
+            Sum v;
+#pragma unroll
+            for (int e0 = 0; e0 < 16; e0 += 4) {
+                float d[4], r[4];
+                if (e0 >= per) break;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) entry(a + lane * per + e0 + e, e0 + e < per && a + lane * per + e0 + e < b, d[e], r[e]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v.add(d[e], r[e]);
+            }
+            double w = v.value(), in = scan(w, 32), base = order.base;
+            const int at = max(pick(base + in, w, order.goal), 0);
+            base += __shfl_sync(FULL, in - w, at);
+            a += at * per;
+            b = min(b, a + per);
+            float d, r;
+            entry(a + lane, a + lane < b, d, r);
+            w = (double)d + (double)r;
+            in = scan(w, 16);
+            const int y = pick(base + in, w, order.goal);
+            if (lane == 0) g.next[s] = y < 0 ? -1 : a + y;
         }
         break;
     }
