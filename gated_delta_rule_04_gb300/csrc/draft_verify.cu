@@ -22,9 +22,12 @@
 namespace kda {
 namespace {
 
-constexpr int NT = 256, WARPS = NT / 32, MAX_CTAS = 16, SMS = 152, PER_SM = 4;
+constexpr int MAX_CTAS = 16, SMS = 152;
+constexpr int DEPTH = 3;             // steps of copies on their way, of 32 bytes of p and of q a thread
 constexpr uint32_t FULL = 0xffffffffu;
-constexpr int PARTS = 64, LAST = 128;                // of the search: parts of a piece, entries of a part's step
+constexpr int PARTS = 8;             // of a piece, whose sums are kept for the search
+constexpr int FINAL = 512;           // entries that one warp finds the token in, 16 neighbouring ones a lane
+constexpr int LOOSE = 8;             // entries a lane and step where rows lie off 16 bytes
 constexpr uint64_t WAIT_NS = 2000000000ull;
 
 __device__ __forceinline__ float clean(float v) { return v > 0.f && v <= 3.402823466e38f ? v : 0.f; }
@@ -71,7 +74,7 @@ struct Coef {
 };
 enum Kind { P_ONLY, ONE, ANY };      // c = 0, c = 1 (the first refusal), any
 
-// W of one token as two floats, p and q not negative nor NaN: p - c q with c q = m + e cut off at p, so that
+// W of one token as two floats, p and q finite and not negative: p - c q with c q = m + e cut off at p, so that
 // m <= p and p - m is d + r exactly (Dekker).
 template <int KIND> __device__ __forceinline__ void w_of(const Coef& k, float p, float q, float& d, float& r) {
     float m = q, e = 0.f;
@@ -86,35 +89,35 @@ template <int KIND> __device__ __forceinline__ void w_of(const Coef& k, float p,
     if (KIND == ANY) r = __fsub_rn(r, e);
 }
 
-// A lane's sums of W, of two tokens at a time side by side.  Infinities are not looked for here: they make
-// `hi` or `seen` infinite or NaN, and the piece is then summed again with cleaned values.
+// A lane's sums of W, of two tokens at a time side by side, for values that are neither negative nor infinite nor
+// NaN: `most` is the largest of their words, and if it is none of a finite number's the piece is summed again
+// with cleaned values.
 struct Pairs {
-    float2 hi = make_float2(0.f, 0.f), lo = hi, seen = hi;
+    float2 hi = make_float2(0.f, 0.f), lo = hi;
+    uint32_t most = 0;
     template <int KIND> __device__ __forceinline__ void add(const Coef& k, float2 p, float2 q) {
-        p = make_float2(fmaxf(p.x, 0.f), fmaxf(p.y, 0.f));        // (NaN counts as zero)
+        if (KIND == P_ONLY) {
+            most = __vimax3_u32(most, __float_as_uint(p.x), __float_as_uint(p.y));
+        } else {
+            most = __vimax3_u32(most, __float_as_uint(p.x), __float_as_uint(q.x));
+            most = __vimax3_u32(most, __float_as_uint(p.y), __float_as_uint(q.y));
+        }
         float2 d = p;
-        if (KIND != P_ONLY) {
-            q = make_float2(fmaxf(q.x, 0.f), fmaxf(q.y, 0.f));
-            seen = add2(seen, q);
+        if (KIND == ONE) {
+            const float2 m = make_float2(fminf(q.x, p.x), fminf(q.y, p.y));
+            d = sub2(p, m);
+            lo = add2(lo, sub2(sub2(p, d), m));
+        } else if (KIND == ANY) {
             float2 r;
-            if (KIND == ONE) {
-                const float2 m = make_float2(fminf(q.x, p.x), fminf(q.y, p.y));
-                d = sub2(p, m);
-                r = sub2(sub2(p, d), m);
-            } else {
-                w_of<ANY>(k, p.x, q.x, d.x, r.x);
-                w_of<ANY>(k, p.y, q.y, d.y, r.y);
-            }
+            w_of<ANY>(k, p.x, q.x, d.x, r.x);
+            w_of<ANY>(k, p.y, q.y, d.y, r.y);
             lo = add2(lo, r);
         }
         const float2 s = add2(hi, d), b = sub2(s, hi);
         lo = add2(lo, add2(sub2(hi, sub2(s, b)), sub2(d, b)));
         hi = s;
     }
-    __device__ __forceinline__ bool finite() const {
-        const float x = fabsf(hi.x) + fabsf(hi.y) + fabsf(seen.x) + fabsf(seen.y);
-        return x <= 3.402823466e38f;
-    }
+    __device__ __forceinline__ bool good() const { return most <= 0x7f7fffffu; }
 };
 
 template <typename TP> struct Vec;
@@ -140,79 +143,129 @@ template <typename TP> struct Row {
     __device__ __forceinline__ Row(const TP* p_, const TP* q_, int V_, int pieces) : p(p_), q(q_), V(V_) {
         const uint32_t at = (uint32_t)reinterpret_cast<uintptr_t>(p) & 15;
         head = q && ((uint32_t)reinterpret_cast<uintptr_t>(q) & 15) != at ? -1 : (int)((16 - at) % 16 / sizeof(TP));
-        const int unit = 32 * Vec<TP>::N, each = (V + pieces - 1) / pieces;
+        const int unit = 64 * Vec<TP>::N, each = (V + pieces - 1) / pieces;
         size = (each + unit - 1) / unit * unit;
     }
     __device__ __forceinline__ int begin(int i) const { return i == 0 ? 0 : (int)min((int64_t)V, (int64_t)i * size + max(head, 0)); }
     __device__ __forceinline__ int end(int i, int pieces) const { return i + 1 == pieces ? V : begin(i + 1); }
 };
 
-// The lane's share of the sum of W over [a, b): 16 bytes at a time from the first boundary on.
-template <int KIND, typename TP>
-__device__ __forceinline__ Sum sum_piece(const Coef& k, const Row<TP>& r, int a, int b) {
-    constexpr int N = Vec<TP>::N, U = 2;
+// A piece [a, b) in at most 8 parts of whole steps of the loop that sums it: part i ends at end(i).
+struct Parts {
+    int va, b, size;                 // the loop's first element, behind the piece's head
+    template <typename TP> __device__ __forceinline__ Parts(const Row<TP>& r, int a, int b_) : b(b_) {
+        constexpr int N = Vec<TP>::N;
+        va = r.head < 0 ? a : min(b, a + ((r.head - a) & (N - 1)));
+        const int unit = r.head < 0 ? 32 * LOOSE : 64 * N;
+        size = ((b - va + unit - 1) / unit + PARTS - 1) / PARTS * unit;
+    }
+    __device__ __forceinline__ int end(int i) const { return i + 1 == PARTS ? b : (int)min((int64_t)b, va + (int64_t)(i + 1) * size); }
+    __device__ __forceinline__ int begin(int i, int a) const { return i == 0 ? a : end(i - 1); }
+};
+
+// The lane's share of the sum of W over [a, b): 16 bytes at a time from the first boundary on.  With `marks`,
+// the warp's sums up to the end of each part are left there.
+template <int KIND, int NT, typename TP>
+__device__ __forceinline__ Sum sum_piece(const Coef& k, const Row<TP>& r, int a, int b, uint4* ring, float2* marks) {
+    constexpr int N = Vec<TP>::N;
     const int lane = threadIdx.x & 31;
+    const Parts parts(r, a, b);
+    const int va = parts.va;
     Pairs s;
+    auto so_far = [&]() {
+        Sum t;
+        t.add(s.hi.x, s.lo.x);
+        t.add(s.hi.y, s.lo.y);
+        return t;
+    };
+    auto mark = [&](int i, Sum t) {
+        t = warp_sum(t);
+        if (lane == 0) marks[i] = make_float2(t.hi, t.lo);
+    };
     auto one = [&](int y) { s.add<KIND>(k, make_float2(to_f32(r.p[y]), 0.f), make_float2(KIND ? to_f32(r.q[y]) : 0.f, 0.f)); };
+    int part = 0;
     if (r.head >= 0) {
-        const int va = a == 0 ? min(r.head, b) : a, nv = (b - va) / N, vb = va + nv * N;
+        const int nv = (b - va) / N, vb = va + nv * N;
         if (lane < va - a) one(a + lane);
-        if (lane < b - vb) one(vb + lane);
         const uint4* pv = reinterpret_cast<const uint4*>(r.p + va);
         const uint4* qv = KIND ? reinterpret_cast<const uint4*>(r.q + va) : nullptr;
-        // two batches of loads in turn, one on its way while the other is summed
-        uint4 x[2][U], y[2][U];
-        auto load = [&](uint4 (&px)[U], uint4 (&qx)[U], int i) {
+        // Whole steps (two pieces of 16 bytes a lane) are copied DEPTH ahead of the sum; a lane reads what it
+        // copied, so nothing waits for another.
+        const int steps = nv / 64;
+        const uint32_t slot = ptx::smem_u32(ring + threadIdx.x);   // [DEPTH][2][p, q][NT]
+        const uint4 *pn = pv + lane, *qn = KIND ? qv + lane : nullptr;
+        auto issue = [&](int st, bool in) {
+            if (in) {
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const bool in = i + 32 * u < nv;
-                px[u] = in ? __ldcs(pv + i + 32 * u) : make_uint4(0, 0, 0, 0);
-                if (KIND) qx[u] = in ? __ldcs(qv + i + 32 * u) : make_uint4(0, 0, 0, 0);
+                for (int h = 0; h < 2; ++h) {
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(slot + (st * 4 + 2 * h) * NT * 16), "l"(pn + 32 * h) : "memory");
+                    if (KIND)
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(slot + (st * 4 + 2 * h + 1) * NT * 16), "l"(qn + 32 * h) : "memory");
+                }
+                pn += 64;
+                if (KIND) qn += 64;
             }
+            ptx::cp_async_commit();
         };
-        auto sum = [&](const uint4 (&px)[U], const uint4 (&qx)[U]) {
+        auto add = [&](const uint4& x, const uint4& y) {
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int j = 0; j < N / 2; ++j)
-                    s.add<KIND>(k, Vec<TP>::pair(px[u], j), KIND ? Vec<TP>::pair(qx[u], j) : make_float2(0.f, 0.f));
+            for (int j = 0; j < N / 2; ++j)
+                s.add<KIND>(k, Vec<TP>::pair(x, j), KIND ? Vec<TP>::pair(y, j) : make_float2(0.f, 0.f));
         };
-        load(x[0], y[0], lane);
-        for (int i = lane; i < nv; i += 64 * U) {
-            load(x[1], y[1], i + 32 * U);
-            sum(x[0], y[0]);
-            load(x[0], y[0], i + 64 * U);
-            sum(x[1], y[1]);
+#pragma unroll
+        for (int st = 0; st < DEPTH; ++st) issue(st, st < steps);
+        const int each = marks ? parts.size / (64 * N) : INT_MAX;
+        int left = each;
+        for (int i = 0; i < steps;) {
+#pragma unroll
+            for (int st = 0; st < DEPTH; ++st) {
+                if (i == steps) break;
+                asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
+                const uint4* const at = ring + threadIdx.x + st * 4 * NT;
+                add(at[0], KIND ? at[NT] : at[0]);
+                add(at[2 * NT], KIND ? at[3 * NT] : at[0]);
+                ++i;
+                issue(st, i - 1 + DEPTH < steps);
+                if (--left == 0) {
+                    mark(part++, so_far());
+                    left = each;
+                }
+            }
         }
+        for (int i = steps * 64 + lane; i < nv; i += 32) add(__ldcs(pv + i), KIND ? __ldcs(qv + i) : make_uint4(0, 0, 0, 0));
+        if (lane < b - vb) one(vb + lane);
     } else {
-        constexpr int E = 8;
-        for (int i = a + lane; i < b; i += 32 * E) {
-            float x[E], y[E];
+        for (int i0 = a; i0 < b; i0 += 32 * LOOSE) {
+            const int i = i0 + lane;
+            float x[LOOSE], y[LOOSE];
 #pragma unroll
-            for (int u = 0; u < E; ++u) {
+            for (int u = 0; u < LOOSE; ++u) {
                 const bool in = i + 32 * u < b;
                 x[u] = in ? to_f32(r.p[i + 32 * u]) : 0.f;
                 y[u] = KIND && in ? to_f32(r.q[i + 32 * u]) : 0.f;
             }
 #pragma unroll
-            for (int u = 0; u < E; u += 2) s.add<KIND>(k, make_float2(x[u], x[u + 1]), make_float2(y[u], y[u + 1]));
+            for (int u = 0; u < LOOSE; u += 2) s.add<KIND>(k, make_float2(x[u], x[u + 1]), make_float2(y[u], y[u + 1]));
+            if (marks && i0 + 32 * LOOSE == parts.end(part)) mark(part++, so_far());
         }
     }
-    Sum t;
-    if (s.finite()) {
-        t.add(s.hi.x, s.lo.x);
-        t.add(s.hi.y, s.lo.y);
-    } else {                                          // the same elements once more, infinities counted as zero
-        const int va = r.head >= 0 ? (a == 0 ? min(r.head, b) : a) : a, step = r.head >= 0 ? N : 1, nv = (b - va) / step;
-        auto again = [&](int y) {
-            float d, e;
-            w_of<ANY>(k, clean(to_f32(r.p[y])), KIND ? clean(to_f32(r.q[y])) : 0.f, d, e);
-            t.add(d, e);
-        };
-        if (lane < va - a) again(a + lane);
-        if (lane < b - va - nv * step) again(va + nv * step + lane);
-        for (int i = lane; i < nv; i += 32)
-            for (int j = 0; j < step; ++j) again(va + i * step + j);
+    Sum t = so_far();
+    // an infinity, a NaN or a minus somewhere: once more, counted as zero
+    if (__any_sync(FULL, !s.good())) {
+        t = Sum{};
+        int y = a;
+        for (part = 0; part < PARTS; ++part) {
+            const int end = parts.end(part);
+            for (; y < end; y += 32) {
+                float d = 0.f, e = 0.f;
+                if (y + lane < end) w_of<ANY>(k, clean(to_f32(r.p[y + lane])), KIND ? clean(to_f32(r.q[y + lane])) : 0.f, d, e);
+                t.add(d, e);
+            }
+            y = end;
+            if (marks) mark(part, t);
+        }
+    } else if (marks) {
+        for (; part < PARTS; ++part) mark(part, t);
     }
     return t;
 }
@@ -236,7 +289,7 @@ __device__ __forceinline__ int pick(double incl, double share, double goal) {
 enum Ask { SUM, SEARCH, END };
 struct Order {
     int ask, then;                   // SUM or END; behind the sum: SUM (another one), SEARCH or END
-    int cur, refused;                // the current node; tokens refused there, taken out of W
+    int cur, refused, last;          // the current node; tokens refused there, taken out of W; a search follows
     float2 c;
     int a, b;                        // (SEARCH) where the token is,
     double base, goal;               // the sum before that, and the one to be passed
@@ -244,12 +297,14 @@ struct Order {
     float p[KDA_TREE_MAX_NODES];
 };
 
-template <typename TP>
-__global__ void __launch_bounds__(NT, PER_SM) verify_kernel(const __grid_constant__ VerifyArgs g, int ctas) {
+template <typename TP, int NT>
+__global__ void __launch_bounds__(NT, 1024 / NT) verify_kernel(const __grid_constant__ VerifyArgs g, int ctas) {
+    constexpr int WARPS = NT / 32;
+    extern __shared__ __align__(16) uint4 ring[];     // sum_piece's copies
     __shared__ Order order;
     __shared__ float2 wsum[WARPS], slots[2][MAX_CTAS];
     __shared__ uint64_t bars[2];
-    __shared__ float2 psum[PARTS];
+    __shared__ float2 psum[WARPS][PARTS];
     const int s = blockIdx.x / ctas, rank = blockIdx.x % ctas, tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int R = g.R, V = g.V, pieces = ctas * WARPS;
     auto p_row = [&](int r) -> const TP* {
@@ -399,6 +454,7 @@ __global__ void __launch_bounds__(NT, PER_SM) verify_kernel(const __grid_constan
                 order.cur = cur;
                 order.c = make_float2(c.hi, c.lo);
                 order.refused = 0;
+                order.last = ending;
             }
             __syncwarp();
             if (refused) {                            // a list of the tokens, in the order of the nodes
@@ -423,8 +479,9 @@ __global__ void __launch_bounds__(NT, PER_SM) verify_kernel(const __grid_constan
         const Row<TP> row(p_row(node), k.kind() ? q_row(node) : nullptr, V, pieces);
         {
             const int a = row.begin(rank * WARPS + warp), b = row.end(rank * WARPS + warp, pieces);
-            Sum sum = k.kind() == P_ONLY ? sum_piece<P_ONLY>(k, row, a, b)
-                    : k.kind() == ONE ? sum_piece<ONE>(k, row, a, b) : sum_piece<ANY>(k, row, a, b);
+            float2* const marks = order.last && b - a > FINAL ? psum[warp] : nullptr;
+            Sum sum = k.kind() == P_ONLY ? sum_piece<P_ONLY, NT>(k, row, a, b, ring, marks)
+                    : k.kind() == ONE ? sum_piece<ONE, NT>(k, row, a, b, ring, marks) : sum_piece<ANY, NT>(k, row, a, b, ring, marks);
             for (int j = lane; j < order.refused; j += 32)        // (p is what was added: the sum stays exact)
                 if (order.tok[j] >= a && order.tok[j] < b) sum.add(-order.p[j]);
             sum = warp_sum(sum);
@@ -452,11 +509,26 @@ __global__ void __launch_bounds__(NT, PER_SM) verify_kernel(const __grid_constan
                     base += __shfl_sync(FULL, in - w, at);
                     then = SEARCH;
                     if (lane == 0) {
-                        const Row<TP> row(p_row(cur), c.kind() ? q_row(cur) : nullptr, V, pieces);
-                        order.a = row.begin(rank * WARPS + at);
-                        order.b = row.end(rank * WARPS + at, pieces);
-                        order.base = base;
                         order.goal = goal;
+                    }
+                    const Row<TP> row(p_row(cur), c.kind() ? q_row(cur) : nullptr, V, pieces);
+                    int a = row.begin(rank * WARPS + at), b = row.end(rank * WARPS + at, pieces);
+                    if (b - a > FINAL) {              // and the part of it: lane i has the sum up to the end of part i
+                        const Parts parts(row, a, b);
+                        double up_to = lane < PARTS ? (double)psum[at][lane].x + (double)psum[at][lane].y : 0.0;
+                        if (lane < PARTS)
+                            for (int j = 0; j < order.refused; ++j)
+                                if (order.tok[j] >= a && order.tok[j] < parts.end(lane)) up_to -= (double)order.p[j];
+                        const double before = __shfl_up_sync(FULL, up_to, 1), part = up_to - (lane > 0 ? before : 0.0);
+                        const int i = max(pick(base + up_to, lane < PARTS ? part : 0.0, goal), 0);
+                        base += __shfl_sync(FULL, up_to - part, i);
+                        b = parts.end(i);
+                        a = parts.begin(i, a);
+                    }
+                    if (lane == 0) {
+                        order.a = a;
+                        order.b = b;
+                        order.base = base;
                     }
                 }
             }
@@ -465,42 +537,34 @@ __global__ void __launch_bounds__(NT, PER_SM) verify_kernel(const __grid_constan
         __syncthreads();
         if (order.then == END) break;
         if (order.then == SUM) continue;
-        // The warp's piece once more: while it is long, in 64 parts whose sums lie in shared memory; then by
-        // one warp, 16 neighbouring entries a lane.
+        // That part once more: while it is long, an eighth of it by each warp; then by one warp.
         auto entry = [&](int y, bool in, float& d, float& r) {    // W(y)
             w_of<ANY>(k, in ? clean(to_f32(row.p[y])) : 0.f, in && row.q ? clean(to_f32(row.q[y])) : 0.f, d, r);
             for (int j = 0; j < order.refused; ++j)
                 if (order.tok[j] == y) d = r = 0.f;
         };
-        while (order.b - order.a > 4 * LAST) {
-            const int a = order.a, b = order.b, size = (int)(((int64_t)b - a + PARTS * LAST - 1) / (PARTS * LAST)) * LAST;
-#pragma unroll 4
-            for (int i = 0; i < PARTS / WARPS; ++i) {
-                const int part = i * WARPS + warp;
-                const int from = (int)min((int64_t)b, a + (int64_t)part * size), to = (int)min((int64_t)b, (int64_t)from + size);
-                Sum v;
-                for (int y0 = from; y0 < to; y0 += LAST) {
-                    float d[LAST / 32], r[LAST / 32];
+        while (order.b - order.a > FINAL) {
+            const int a = order.a, b = order.b, size = (int)(((int64_t)b - a + WARPS * 32 - 1) / (WARPS * 32)) * 32;
+            const int from = (int)min((int64_t)b, a + (int64_t)warp * size), to = (int)min((int64_t)b, (int64_t)from + size);
+            Sum v;
+            for (int y0 = from; y0 < to; y0 += 32 * 4) {
+                float d[4], r[4];
 #pragma unroll
-                    for (int e = 0; e < LAST / 32; ++e) entry(y0 + 32 * e + lane, y0 + 32 * e + lane < to, d[e], r[e]);
+                for (int e = 0; e < 4; ++e) entry(y0 + 32 * e + lane, y0 + 32 * e + lane < to, d[e], r[e]);
 #pragma unroll
-                    for (int e = 0; e < LAST / 32; ++e) v.add(d[e], r[e]);
-                }
-                v = warp_sum(v);
-                if (lane == 0) psum[part] = make_float2(v.hi, v.lo);
+                for (int e = 0; e < 4; ++e) v.add(d[e], r[e]);
             }
+            v = warp_sum(v);
+            if (lane == 0) wsum[warp] = make_float2(v.hi, v.lo);
             __syncthreads();
-            if (warp == 0) {                          // lane j has parts 2 j and 2 j + 1
-                const double lo = (double)psum[2 * lane].x + (double)psum[2 * lane].y;
-                const double both = lo + ((double)psum[2 * lane + 1].x + (double)psum[2 * lane + 1].y), in = scan(both, 32);
-                const int at = max(pick(order.base + in, both, order.goal), 0);
+            if (warp == 0) {
+                const double w = lane < WARPS ? (double)wsum[lane].x + (double)wsum[lane].y : 0.0, in = scan(w, WARPS);
+                const int at = max(pick(order.base + in, w, order.goal), 0);
+                __syncwarp();
                 if (lane == at) {
-                    const double base = order.base + (in - both);
-                    const bool second = !(lo > 0.0 && base + lo > order.goal) && both > lo;
-                    const int from = (int)min((int64_t)b, a + (int64_t)(2 * at + second) * size);
-                    order.a = from;
-                    order.b = (int)min((int64_t)b, (int64_t)from + size);
-                    order.base = second ? base + lo : base;
+                    order.a = (int)min((int64_t)b, a + (int64_t)at * size);
+                    order.b = (int)min((int64_t)b, (int64_t)order.a + size);
+                    order.base += in - w;
                 }
             }
             __syncthreads();
@@ -544,23 +608,24 @@ __global__ void __launch_bounds__(NT, PER_SM) verify_kernel(const __grid_constan
     asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-template <typename TP> cudaError_t verify(const VerifyArgs& a, int ctas, cudaStream_t s) {
-    auto k = verify_kernel<TP>;
-    if (ctas > 8) {                                   // 16 CTAs are beyond the portable size (set once per device)
-        static std::atomic<uint64_t> done{0};
-        int dev = 0;
-        cudaError_t e = cudaGetDevice(&dev);
+template <typename TP, int NT> cudaError_t verify(const VerifyArgs& a, int ctas, cudaStream_t s) {
+    auto k = verify_kernel<TP, NT>;
+    constexpr int RING_BYTES = DEPTH * 4 * NT * 16;
+    static std::atomic<uint64_t> done{0};             // (set once per device)
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    if (!(done.load() & bit)) {                       // 16 CTAs are beyond the portable size
+        e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, RING_BYTES);
         if (e != cudaSuccess) return e;
-        const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
-        if (!(done.load() & bit)) {
-            e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-            if (e != cudaSuccess) return e;
-            done.fetch_or(bit);
-        }
+        done.fetch_or(bit);
     }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)((int64_t)a.n * ctas));
     cfg.blockDim = dim3(NT);
+    cfg.dynamicSmemBytes = RING_BYTES;
     cfg.stream = s;
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeClusterDimension;
@@ -571,14 +636,23 @@ template <typename TP> cudaError_t verify(const VerifyArgs& a, int ctas, cudaStr
     return cudaLaunchKernelEx(&cfg, k, a, ctas);
 }
 
+// CTAs a session: as many as all run at once (1024 threads an SM), while each warp's piece is at least 512
+// bytes.
+template <typename TP, int NT> cudaError_t verify(const VerifyArgs& a, cudaStream_t s) {
+    int ctas = 1;
+    const int64_t bytes = (int64_t)a.V * (int)sizeof(TP);
+    while (ctas < MAX_CTAS && (int64_t)a.n * ctas * 2 <= 1024 / NT * SMS && bytes >= (int64_t)ctas * 2 * (NT / 32) * 512) ctas *= 2;
+    return verify<TP, NT>(a, ctas, s);
+}
+template <typename TP> cudaError_t verify(const VerifyArgs& a, cudaStream_t s) {
+    // CTAs of 4 warps where they fill the SMs: more evenly
+    return (int64_t)a.n * MAX_CTAS > 4 * SMS ? verify<TP, 128>(a, s) : verify<TP, 256>(a, s);
+}
+
 }  // namespace
 
 cudaError_t launch_verify(const VerifyArgs& a, int io_bf16, cudaStream_t s) {
-    // CTAs a session: as many as all run at once, while each warp's piece is at least 512 bytes
-    int ctas = 1;
-    const int64_t bytes = (int64_t)a.V * (io_bf16 ? 2 : 4);
-    while (ctas < MAX_CTAS && (int64_t)a.n * ctas * 2 <= PER_SM * SMS && bytes >= (int64_t)ctas * 2 * WARPS * 512) ctas *= 2;
-    return io_bf16 ? verify<__nv_bfloat16>(a, ctas, s) : verify<float>(a, ctas, s);
+    return io_bf16 ? verify<__nv_bfloat16>(a, s) : verify<float>(a, s);
 }
 
 }  // namespace kda
