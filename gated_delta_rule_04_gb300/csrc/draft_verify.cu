@@ -14,6 +14,8 @@
 // doubles: next to a random border, in a sum over 10^5 entries, a 32-bit sum would
 // take another token in one session of 30, and this GPU adds 2 doubles a cycle and
 // SM where the rows arrive at 3 pairs.
+#include <limits.h>
+
 #include <atomic>
 
 #include "draft_verify.cuh"
@@ -26,7 +28,8 @@ constexpr int MAX_CTAS = 16, SMS = 152;
 constexpr int DEPTH = 3;             // steps of copies on their way, of 32 bytes of p and of q a thread
 constexpr uint32_t FULL = 0xffffffffu;
 constexpr int PARTS = 8;             // of a piece, whose sums are kept for the search
-constexpr int FINAL = 512;           // entries that one warp finds the token in, 16 neighbouring ones a lane
+constexpr int MARKED = 512;          // a piece longer than this keeps them
+constexpr int FINAL = 128;           // entries that one warp finds the token in, 4 neighbouring ones a lane
 constexpr int LOOSE = 8;             // entries a lane and step where rows lie off 16 bytes
 constexpr uint64_t WAIT_NS = 2000000000ull;
 
@@ -108,10 +111,12 @@ struct Pairs {
             d = sub2(p, m);
             lo = add2(lo, sub2(sub2(p, d), m));
         } else if (KIND == ANY) {
-            float2 r;
-            w_of<ANY>(k, p.x, q.x, d.x, r.x);
-            w_of<ANY>(k, p.y, q.y, d.y, r.y);
-            lo = add2(lo, r);
+            const float2 h = make_float2(k.hi, k.hi), m = __fmul2_rn(h, q);   // (as w_of)
+            float2 e = __ffma2_rn(make_float2(k.lo, k.lo), q, __ffma2_rn(h, q, __fmul2_rn(m, make_float2(-1.f, -1.f))));
+            e = make_float2(m.x < p.x ? e.x : 0.f, m.y < p.y ? e.y : 0.f);
+            const float2 c = make_float2(fminf(m.x, p.x), fminf(m.y, p.y));
+            d = sub2(p, c);
+            lo = add2(lo, sub2(sub2(sub2(p, d), c), e));
         }
         const float2 s = add2(hi, d), b = sub2(s, hi);
         lo = add2(lo, add2(sub2(hi, sub2(s, b)), sub2(d, b)));
@@ -164,9 +169,11 @@ struct Parts {
 };
 
 // The lane's share of the sum of W over [a, b): 16 bytes at a time from the first boundary on.  With `marks`,
-// the warp's sums up to the end of each part are left there.
+// the warp's sums up to the end of each part are left there.  `there`: the pass before was over the same rows,
+// and a piece that fits the ring is still in it.
 template <int KIND, int NT, typename TP>
-__device__ __forceinline__ Sum sum_piece(const Coef& k, const Row<TP>& r, int a, int b, uint4* ring, float2* marks) {
+__device__ __forceinline__ Sum sum_piece(const Coef& k, const Row<TP>& r, int a, int b, uint4* ring, float2* marks,
+                                         bool there) {
     constexpr int N = Vec<TP>::N;
     const int lane = threadIdx.x & 31;
     const Parts parts(r, a, b);
@@ -182,28 +189,33 @@ __device__ __forceinline__ Sum sum_piece(const Coef& k, const Row<TP>& r, int a,
         t = warp_sum(t);
         if (lane == 0) marks[i] = make_float2(t.hi, t.lo);
     };
-    auto one = [&](int y) { s.add<KIND>(k, make_float2(to_f32(r.p[y]), 0.f), make_float2(KIND ? to_f32(r.q[y]) : 0.f, 0.f)); };
     int part = 0;
     if (r.head >= 0) {
         const int nv = (b - va) / N, vb = va + nv * N;
-        if (lane < va - a) one(a + lane);
-        const uint4* pv = reinterpret_cast<const uint4*>(r.p + va);
-        const uint4* qv = KIND ? reinterpret_cast<const uint4*>(r.q + va) : nullptr;
-        // Whole steps (two pieces of 16 bytes a lane) are copied DEPTH ahead of the sum; a lane reads what it
-        // copied, so nothing waits for another.
-        const int steps = nv / 64;
+        // the head's and the tail's entries, a lane each (at most N - 1 of either)
+        const int edge = lane < va - a ? a + lane : lane >= 16 && lane - 16 < b - vb ? vb + lane - 16 : -1;
+        const float pe = edge >= 0 ? to_f32(r.p[edge]) : 0.f, qe = KIND && edge >= 0 ? to_f32(r.q[edge]) : 0.f;
+        // Steps of two pieces of 16 bytes a lane, copied DEPTH ahead of the sum; a lane reads what it copied, so
+        // nothing waits for another.  Behind the last piece a step is filled up with zeros.
+        const int steps = (nv + 63) / 64;
         const uint32_t slot = ptx::smem_u32(ring + threadIdx.x);   // [DEPTH][2][p, q][NT]
-        const uint4 *pn = pv + lane, *qn = KIND ? qv + lane : nullptr;
-        auto issue = [&](int st, bool in) {
-            if (in) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(slot + (st * 4 + 2 * h) * NT * 16), "l"(pn + 32 * h) : "memory");
-                    if (KIND)
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(slot + (st * 4 + 2 * h + 1) * NT * 16), "l"(qn + 32 * h) : "memory");
+        const uint4 *pn = reinterpret_cast<const uint4*>(r.p + va) + lane, *qn = KIND ? reinterpret_cast<const uint4*>(r.q + va) + lane : nullptr;
+        int ahead = lane;                             // the lane's next piece
+        auto copy = [&](int to, const uint4* from, bool in) {
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(slot + to * NT * 16), "l"(from), "r"(in ? 16 : 0) : "memory");
+        };
+        auto issue = [&](int st, bool step) {
+            if (step) {
+                const bool in0 = ahead < nv, in1 = ahead + 32 < nv;
+                copy(st * 4, in0 ? pn : reinterpret_cast<const uint4*>(r.p + va), in0);
+                copy(st * 4 + 2, in1 ? pn + 32 : reinterpret_cast<const uint4*>(r.p + va), in1);
+                if (KIND) {
+                    copy(st * 4 + 1, in0 ? qn : reinterpret_cast<const uint4*>(r.q + va), in0);
+                    copy(st * 4 + 3, in1 ? qn + 32 : reinterpret_cast<const uint4*>(r.q + va), in1);
+                    qn += 64;
                 }
                 pn += 64;
-                if (KIND) qn += 64;
+                ahead += 64;
             }
             ptx::cp_async_commit();
         };
@@ -213,7 +225,7 @@ __device__ __forceinline__ Sum sum_piece(const Coef& k, const Row<TP>& r, int a,
                 s.add<KIND>(k, Vec<TP>::pair(x, j), KIND ? Vec<TP>::pair(y, j) : make_float2(0.f, 0.f));
         };
 #pragma unroll
-        for (int st = 0; st < DEPTH; ++st) issue(st, st < steps);
+        for (int st = 0; st < DEPTH; ++st) issue(st, st < steps && !(there && steps <= DEPTH));
         const int each = marks ? parts.size / (64 * N) : INT_MAX;
         int left = each;
         for (int i = 0; i < steps;) {
@@ -232,8 +244,7 @@ __device__ __forceinline__ Sum sum_piece(const Coef& k, const Row<TP>& r, int a,
                 }
             }
         }
-        for (int i = steps * 64 + lane; i < nv; i += 32) add(__ldcs(pv + i), KIND ? __ldcs(qv + i) : make_uint4(0, 0, 0, 0));
-        if (lane < b - vb) one(vb + lane);
+        s.add<KIND>(k, make_float2(pe, 0.f), make_float2(qe, 0.f));
     } else {
         for (int i0 = a; i0 < b; i0 += 32 * LOOSE) {
             const int i = i0 + lane;
@@ -270,15 +281,23 @@ __device__ __forceinline__ Sum sum_piece(const Coef& k, const Row<TP>& r, int a,
     return t;
 }
 
-// Inclusive sums over the lanes.
-__device__ __forceinline__ double scan(double v, int lanes) {
+// Inclusive sums over the first `lanes` lanes.
+__device__ __forceinline__ Sum scan(Sum v, int lanes) {
     const int lane = threadIdx.x & 31;
+#pragma unroll
     for (int d = 1; d < lanes; d <<= 1) {
-        const double u = __shfl_up_sync(FULL, v, d);
-        if (lane >= d) v += u;
+        const float hi = __shfl_up_sync(FULL, v.hi, d), lo = __shfl_up_sync(FULL, v.lo, d);
+        if (lane >= d) v.add(hi, lo);
     }
     return v;
 }
+__device__ __forceinline__ Sum sum_of(float2 x) {
+    Sum s;
+    s.hi = x.x;
+    s.lo = x.y;
+    return s;
+}
+
 // The first lane whose inclusive sum is above the goal, or (rounding) the last with a share; -1: none has one.
 __device__ __forceinline__ int pick(double incl, double share, double goal) {
     const uint32_t over = __ballot_sync(FULL, share > 0.0 && incl > goal), any = __ballot_sync(FULL, share > 0.0);
@@ -361,7 +380,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) verify_kernel(const __grid_cons
     uint64_t children = 0, refused = 0;               // to be tested at cur; (chosen tokens) refused, taken out of W
     bool first = true, arrived = true, ending = false, dead = false;
     Coef c;
-    double T = 1.0, share = 0.0, total = 0.0;         // share: the sum of CTA `lane`
+    double T = 1.0, total = 0.0;
+    Sum share;                                        // the sum of CTA `lane`
 
     // Goes on with the tests until a sum is needed: true, or the walk has ended: false.
     auto go = [&]() -> bool {
@@ -416,10 +436,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) verify_kernel(const __grid_cons
     auto exchange = [&]() {
         const int buf = turn & 1;
         Sum v;
-        if (lane < WARPS) {
-            v.hi = wsum[lane].x;
-            v.lo = wsum[lane].y;
-        }
+        if (lane < WARPS) v = sum_of(wsum[lane]);
         v = warp_sum(v);
         if (ctas > 1) {
             const uint32_t bar = ptx::smem_u32(&bars[buf]);
@@ -434,18 +451,16 @@ __global__ void __launch_bounds__(NT, 1024 / NT) verify_kernel(const __grid_cons
             }
             const bool there = dead || ptx::mbar_wait(bar, turn >> 1 & 1, WAIT_NS);
             dead = __any_sync(FULL, !there) || dead;  // gave up: the token will be -1
-            const float2 x = lane < ctas ? slots[buf][lane] : make_float2(0.f, 0.f);
-            v.hi = x.x;
-            v.lo = x.y;
+            v = lane < ctas ? sum_of(slots[buf][lane]) : Sum{};
             ++turn;
         } else if (lane > 0) {
             v = Sum{};
         }
-        share = v.value();
-        total = warp_sum(v).value();
-        if (dead) share = total = 0.0;
+        share = dead ? Sum{} : v;
+        total = dead ? 0.0 : warp_sum(v).value();
     };
 
+    int node_before = INT_MIN;                        // whose p and q the pass before went over
     for (;;) {
         if (warp == 0) {
             if (!ending && !go()) ending = true;
@@ -479,9 +494,11 @@ __global__ void __launch_bounds__(NT, 1024 / NT) verify_kernel(const __grid_cons
         const Row<TP> row(p_row(node), k.kind() ? q_row(node) : nullptr, V, pieces);
         {
             const int a = row.begin(rank * WARPS + warp), b = row.end(rank * WARPS + warp, pieces);
-            float2* const marks = order.last && b - a > FINAL ? psum[warp] : nullptr;
-            Sum sum = k.kind() == P_ONLY ? sum_piece<P_ONLY, NT>(k, row, a, b, ring, marks)
-                    : k.kind() == ONE ? sum_piece<ONE, NT>(k, row, a, b, ring, marks) : sum_piece<ANY, NT>(k, row, a, b, ring, marks);
+            const bool there = node == node_before && k.kind();      // (a refusal more at the same node: both rows again)
+            node_before = k.kind() ? node : INT_MIN;
+            float2* const marks = order.last && b - a > MARKED ? psum[warp] : nullptr;
+            Sum sum = k.kind() == P_ONLY ? sum_piece<P_ONLY, NT>(k, row, a, b, ring, marks, there)
+                    : k.kind() == ONE ? sum_piece<ONE, NT>(k, row, a, b, ring, marks, there) : sum_piece<ANY, NT>(k, row, a, b, ring, marks, there);
             for (int j = lane; j < order.refused; j += 32)        // (p is what was added: the sum stays exact)
                 if (order.tok[j] >= a && order.tok[j] < b) sum.add(-order.p[j]);
             sum = warp_sum(sum);
@@ -497,14 +514,15 @@ __global__ void __launch_bounds__(NT, 1024 / NT) verify_kernel(const __grid_cons
                 c = Coef{};                           // nothing is left: p itself
                 refused = 0;
             } else {
-                const double goal = (double)g.u_next[s] * total, incl = scan(share, MAX_CTAS);
-                const int owner = pick(incl, share, goal);
+                const double goal = (double)g.u_next[s] * total, incl = scan(share, MAX_CTAS).value(), one = share.value();
+                const int owner = pick(incl, one, goal);
                 then = END;
                 if (owner < 0) {
                     if (rank == 0 && lane == 0) g.next[s] = -1;
                 } else if (owner == rank) {           // the warp whose piece holds the token
-                    double base = __shfl_sync(FULL, incl - share, owner);
-                    const double w = lane < WARPS ? (double)wsum[lane].x + (double)wsum[lane].y : 0.0, in = scan(w, WARPS);
+                    double base = __shfl_sync(FULL, incl - one, owner);
+                    const Sum mine = lane < WARPS ? sum_of(wsum[lane]) : Sum{};
+                    const double w = mine.value(), in = scan(mine, WARPS).value();
                     const int at = max(pick(base + in, w, goal), 0);
                     base += __shfl_sync(FULL, in - w, at);
                     then = SEARCH;
@@ -513,7 +531,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) verify_kernel(const __grid_cons
                     }
                     const Row<TP> row(p_row(cur), c.kind() ? q_row(cur) : nullptr, V, pieces);
                     int a = row.begin(rank * WARPS + at), b = row.end(rank * WARPS + at, pieces);
-                    if (b - a > FINAL) {              // and the part of it: lane i has the sum up to the end of part i
+                    if (b - a > MARKED) {             // and the part of it: lane i has the sum up to the end of part i
                         const Parts parts(row, a, b);
                         double up_to = lane < PARTS ? (double)psum[at][lane].x + (double)psum[at][lane].y : 0.0;
                         if (lane < PARTS)
@@ -558,7 +576,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) verify_kernel(const __grid_cons
             if (lane == 0) wsum[warp] = make_float2(v.hi, v.lo);
             __syncthreads();
             if (warp == 0) {
-                const double w = lane < WARPS ? (double)wsum[lane].x + (double)wsum[lane].y : 0.0, in = scan(w, WARPS);
+                const Sum mine = lane < WARPS ? sum_of(wsum[lane]) : Sum{};
+                const double w = mine.value(), in = scan(mine, WARPS).value();
                 const int at = max(pick(order.base + in, w, order.goal), 0);
                 __syncwarp();
                 if (lane == at) {
@@ -571,26 +590,22 @@ __global__ void __launch_bounds__(NT, 1024 / NT) verify_kernel(const __grid_cons
         }
         if (warp == 0) {
             int a = order.a, b = order.b;
-            const int per = (b - a + 31) / 32;        // at most 16
+            float d[FINAL / 32], r[FINAL / 32];
+            const int per = (b - a + 31) / 32, y0 = a + lane * per;
+#pragma unroll
+            for (int e = 0; e < FINAL / 32; ++e) entry(y0 + e, e < per && y0 + e < b, d[e], r[e]);
             Sum v;
 #pragma unroll
-            for (int e0 = 0; e0 < 16; e0 += 4) {
-                float d[4], r[4];
-                if (e0 >= per) break;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) entry(a + lane * per + e0 + e, e0 + e < per && a + lane * per + e0 + e < b, d[e], r[e]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) v.add(d[e], r[e]);
-            }
-            double w = v.value(), in = scan(w, 32), base = order.base;
+            for (int e = 0; e < FINAL / 32; ++e) v.add(d[e], r[e]);
+            double w = v.value(), in = scan(v, 32).value(), base = order.base;
             const int at = max(pick(base + in, w, order.goal), 0);
             base += __shfl_sync(FULL, in - w, at);
             a += at * per;
             b = min(b, a + per);
-            float d, r;
-            entry(a + lane, a + lane < b, d, r);
-            w = (double)d + (double)r;
-            in = scan(w, 16);
+            entry(a + lane, a + lane < b, d[0], r[0]);
+            v = sum_of(make_float2(d[0], r[0]));
+            w = v.value();
+            in = scan(v, FINAL / 32).value();
             const int y = pick(base + in, w, order.goal);
             if (lane == 0) g.next[s] = y < 0 ? -1 : a + y;
         }
