@@ -2,6 +2,8 @@
 // 1 to 64 tokens per session, and the accepted paths of a round.  A thread holds
 // the states of V neighbouring channels and walks the tokens, the next one's
 // rows on the way while it computes.  The rows move once and bound the call.
+#include <type_traits>
+
 #include "glr_math.cuh"
 
 namespace kda {
@@ -28,18 +30,39 @@ template <typename TI, int V> struct Values {
         r.w = *reinterpret_cast<const typename Word<V * sizeof(TI)>::T*>(static_cast<const TI*>(base) + at);
     }
     static __device__ __forceinline__ float2 pair(const Raw& r, int p) {
+        if constexpr (sizeof(TI) == 2 && V > 1) {     // (by words: an instruction a value)
+            const uint32_t u = reinterpret_cast<const uint32_t*>(&r.w)[p];
+            return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+        }
         return make_float2(to_f32(r.v[2 * p]), 2 * p + 1 < V ? to_f32(r.v[2 * p + 1 < V ? 2 * p + 1 : 0]) : 0.f);
     }
     static __device__ __forceinline__ void store(void* base, int64_t at, const float2 (&x)[PAIRS]) {
         Raw r;
 #pragma unroll
         for (int p = 0; p < PAIRS; ++p) {
-            r.v[2 * p] = from_f32<TI>(x[p].x);
-            if (2 * p + 1 < V) r.v[2 * p + 1 < V ? 2 * p + 1 : 0] = from_f32<TI>(x[p].y);
+            if constexpr (sizeof(TI) == 2 && V > 1) {
+                const __nv_bfloat162 b = __floats2bfloat162_rn(x[p].x, x[p].y);
+                reinterpret_cast<uint32_t*>(&r.w)[p] = reinterpret_cast<const uint32_t&>(b);
+            } else {
+                r.v[2 * p] = from_f32<TI>(x[p].x);
+                if (2 * p + 1 < V) r.v[2 * p + 1 < V ? 2 * p + 1 : 0] = from_f32<TI>(x[p].y);
+            }
         }
         *reinterpret_cast<typename Word<V * sizeof(TI)>::T*>(static_cast<TI*>(base) + at) = r.w;
     }
 };
+
+// V neighbouring numbers of an fp32 tensor as pairs (NULL: zeros).
+template <int V> __device__ __forceinline__ void load_f32(const float* base, size_t at, float2 (&x)[(V + 1) / 2]) {
+    constexpr int W = V < 4 ? V : 4;
+#pragma unroll
+    for (int q = 0; q < V / W; ++q) {
+        typename Values<float, W>::Raw r;
+        if (base) Values<float, W>::load(r, base, at + W * q);
+#pragma unroll
+        for (int p = 0; p < (W + 1) / 2; ++p) x[q * W / 2 + p] = base ? Values<float, W>::pair(r, p) : f2(0.f);
+    }
+}
 
 template <typename TI, int V>
 __global__ void __launch_bounds__(NT) token_kernel(const __grid_constant__ TokenArgs g, int blocks) {
@@ -62,17 +85,20 @@ __global__ void __launch_bounds__(NT) token_kernel(const __grid_constant__ Token
     const bool in = c < g.C;
     float2 h[PAIRS];
     Gate k[PAIRS];
+    bool wide = false;
     if (in) {
-        const size_t at = (size_t)slot * g.C + c;
-        typename Values<float, V == 8 ? 4 : V>::Raw s[V == 8 ? 2 : 1];
-#pragma unroll
-        for (int q = 0; q < (V == 8 ? 2 : 1); ++q) Values<float, V == 8 ? 4 : V>::load(s[q], g.S_in, at + 4 * q);
+        float2 A[PAIRS], rb[PAIRS], ib[PAIRS];
+        load_f32<V>(g.S_in, (size_t)slot * g.C + c, h);
+        load_f32<V>(g.A_log, c, A);
+        load_f32<V>(g.r_bias, c, rb);
+        load_f32<V>(g.i_bias, c, ib);
 #pragma unroll
         for (int p = 0; p < PAIRS; ++p) {
-            h[p] = Values<float, V == 8 ? 4 : V>::pair(s[p / 2], V == 8 ? p % 2 : p);
-            k[p] = make_gate(g, c + 2 * p);
+            k[p] = Gate{make_float2(-expf(A[p].x), -expf(A[p].y)), mul2(rb[p], f2(-LOG2E)), mul2(ib[p], f2(-LOG2E))};
+            wide |= !(k[p].ea.x >= -NEAR && k[p].ea.y >= -NEAR);
         }
     }
+    wide = __any_sync(0xffffffffu, wide);
     auto row_of = [&](int j) {
         const int node = !g.path ? j : j < 32 ? __shfl_sync(0xffffffffu, p1, j) : __shfl_sync(0xffffffffu, p2, j - 32);
         return (int64_t)n * g.n_tokens + node;
@@ -95,12 +121,16 @@ __global__ void __launch_bounds__(NT) token_kernel(const __grid_constant__ Token
         }
         if (!in) continue;
         float2 o[PAIRS];
+        auto token = [&](auto w) {
 #pragma unroll
-        for (int p = 0; p < PAIRS; ++p) {
-            const Step s = step_of<true>(k[p], X::pair(xj, p), X::pair(rj, p), X::pair(ij, p));
-            h[p] = fma2(s.a, h[p], s.b);
-            o[p] = g.z ? mul2(h[p], silu(X::pair(zj, p))) : h[p];
-        }
+            for (int p = 0; p < PAIRS; ++p) {
+                const Step s = step_of<decltype(w)::value>(k[p], X::pair(xj, p), X::pair(rj, p), X::pair(ij, p));
+                h[p] = fma2(s.a, h[p], s.b);
+                o[p] = g.z ? mul2(h[p], silu(X::pair(zj, p))) : h[p];
+            }
+        };
+        if (wide) token(std::true_type{});
+        else token(std::false_type{});
         if (g.o) X::store(g.o, here * g.C + c, o);
     }
     if (in && g.S_out) {
@@ -123,14 +153,14 @@ cudaError_t tokens(const TokenArgs& a, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-// The most neighbouring channels (1, 2, 4, 8) that every row and state can be taken by.
+// The most neighbouring channels (1, 2, 4, 8) that every row, state and parameter can be taken by.
 int widest(const TokenArgs& a, int es) {
     uint64_t rows = 0, states = 0;                    // the addresses and strides, or'ed
     auto row = [&](const void* p, int64_t stride) {
         if (p) rows |= reinterpret_cast<uintptr_t>(p) | (uint64_t)(stride * es);
     };
     row(a.x, a.x_s); row(a.r, a.r_s); row(a.i, a.i_s); row(a.z, a.z_s); row(a.o, a.C);
-    states |= reinterpret_cast<uintptr_t>(a.S_in) | reinterpret_cast<uintptr_t>(a.S_out);
+    for (const float* p : {a.S_in, (const float*)a.S_out, a.A_log, a.r_bias, a.i_bias}) states |= reinterpret_cast<uintptr_t>(p);
     int v = 16 / es;
     while (v > 1 && (rows % (v * es) != 0 || states % ((v < 4 ? v : 4) * 4) != 0 || a.C % v != 0)) v /= 2;
     return v;
