@@ -244,7 +244,9 @@ static kda_status tokens_call(const kda_glr_params* p, int32_t n_sessions, int32
         !glr::rows(p, z, false, &z_stride) || !aligned(o, esize(p)) || !S_in || !aligned(S_in, 4) || !aligned(S_out, 4))
         return KDA_ERR_INVALID_ARG;
     if ((int64_t)n_sessions * ((p->channels + 127) / 128) > (int64_t)INT32_MAX) return KDA_ERR_UNSUPPORTED;
-    glr::TokenArgs a{x, r, i, z, x_stride, r_stride, i_stride, z_stride, p->A_log, p->r_bias, p->i_bias, path, path_len,
+    const uint32_t es = (uint32_t)esize(p);
+    glr::TokenArgs a{x, r, i, z, (uint32_t)x_stride * es, (uint32_t)r_stride * es, (uint32_t)i_stride * es,
+                     (uint32_t)z_stride * es, p->A_log, p->r_bias, p->i_bias, path, path_len,
                      slots, S_in, S_out, o, n_sessions, n_tokens, max_len, n_slots, p->channels};
     return glr::launch_tokens(a, p->io_dtype == KDA_DTYPE_BF16, static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? KDA_OK : KDA_ERR_CUDA;

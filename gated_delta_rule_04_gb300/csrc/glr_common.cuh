@@ -54,7 +54,7 @@ struct ScanArgs {
 
 struct TokenArgs {
     const void *x, *r, *i, *z;
-    int64_t x_s, r_s, i_s, z_s;
+    uint32_t x_s, r_s, i_s, z_s;     // bytes between rows
     const float *A_log, *r_bias, *i_bias;
     const int32_t *path, *path_len;  // NULL: all tokens in order
     const int32_t* slots;

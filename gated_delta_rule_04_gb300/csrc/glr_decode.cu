@@ -1,7 +1,9 @@
 // Tokens of the gated linear recurrence over a pool of states: straight runs of
 // 1 to 64 tokens per session, and the accepted paths of a round.  A thread holds
-// the states of V neighbouring channels and walks the tokens, the next one's
-// rows on the way while it computes.  The rows move once and bound the call.
+// the states of V neighbouring channels and walks the tokens.  The rows move once and bound
+// the call: a thread copies its share of the next 3 tokens' into shared memory
+// while it computes (with the next token's in registers instead, 256 rounds of 5
+// tokens x 8192 channels took 23 us: too few bytes on their way).
 #include <type_traits>
 
 #include "glr_math.cuh"
@@ -10,7 +12,7 @@ namespace kda {
 namespace glr {
 namespace {
 
-constexpr int NT = 128;
+constexpr int NT = 128, DEPTH = 3;
 
 template <int BYTES> struct Word;
 template <> struct Word<2> { using T = uint16_t; };
@@ -28,6 +30,14 @@ template <typename TI, int V> struct Values {
     };
     static __device__ __forceinline__ void load(Raw& r, const void* base, int64_t at) {
         r.w = *reinterpret_cast<const typename Word<V * sizeof(TI)>::T*>(static_cast<const TI*>(base) + at);
+    }
+    // Into the thread's own place in shared memory.
+    static __device__ __forceinline__ void copy(typename Word<V * sizeof(TI)>::T* to, const char* from) {
+        constexpr int BYTES = V * (int)sizeof(TI);
+        const uint32_t at = (uint32_t)__cvta_generic_to_shared(to);
+        if constexpr (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(from) : "memory");
+        else if constexpr (BYTES >= 4) asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(at), "l"(from), "n"(BYTES) : "memory");
+        else *to = *reinterpret_cast<const typename Word<BYTES>::T*>(from);
     }
     static __device__ __forceinline__ float2 pair(const Raw& r, int p) {
         if constexpr (sizeof(TI) == 2 && V > 1) {     // (by words: an instruction a value)
@@ -65,9 +75,10 @@ template <int V> __device__ __forceinline__ void load_f32(const float* base, siz
 }
 
 template <typename TI, int V>
-__global__ void __launch_bounds__(NT) token_kernel(const __grid_constant__ TokenArgs g, int blocks) {
+__global__ void __launch_bounds__(NT, 7) token_kernel(const __grid_constant__ TokenArgs g, int blocks) {
     using X = Values<TI, V>;
     constexpr int PAIRS = X::PAIRS;
+    __shared__ __align__(16) typename Word<V * sizeof(TI)>::T ring[DEPTH][4][NT];
     const int n = blockIdx.x / blocks, c = (blockIdx.x % blocks * blockDim.x + threadIdx.x) * V, lane = threadIdx.x & 31;
     const int slot = g.slots ? g.slots[n] : n;
     int len = g.n_tokens, p1 = 0, p2 = 0;
@@ -99,39 +110,50 @@ __global__ void __launch_bounds__(NT) token_kernel(const __grid_constant__ Token
         }
     }
     wide = __any_sync(0xffffffffu, wide);
-    auto row_of = [&](int j) {
-        const int node = !g.path ? j : j < 32 ? __shfl_sync(0xffffffffu, p1, j) : __shfl_sync(0xffffffffu, p2, j - 32);
-        return (int64_t)n * g.n_tokens + node;
+    const int64_t row0 = (int64_t)n * g.n_tokens;
+    auto node_of = [&](int j) {
+        return !g.path ? j : j < 32 ? __shfl_sync(0xffffffffu, p1, j) : __shfl_sync(0xffffffffu, p2, j - 32);
     };
-    typename X::Raw x, r, i, z;
-    auto load = [&](int64_t row) {
-        X::load(x, g.x, row * g.x_s + c);
-        X::load(r, g.r, row * g.r_s + c);
-        X::load(i, g.i, row * g.i_s + c);
-        if (g.z) X::load(z, g.z, row * g.z_s + c);
-    };
-    int64_t row = len > 0 ? row_of(0) : 0;
-    if (in && len > 0) load(row);
-    for (int j = 0; j < len; ++j) {
-        const typename X::Raw xj = x, rj = r, ij = i, zj = z;
-        const int64_t here = row;
-        if (j + 1 < len) {
-            row = row_of(j + 1);
-            if (in) load(row);
-        }
-        if (!in) continue;
-        float2 o[PAIRS];
-        auto token = [&](auto w) {
-#pragma unroll
-            for (int p = 0; p < PAIRS; ++p) {
-                const Step s = step_of<decltype(w)::value>(k[p], X::pair(xj, p), X::pair(rj, p), X::pair(ij, p));
-                h[p] = fma2(s.a, h[p], s.b);
-                o[p] = g.z ? mul2(h[p], silu(X::pair(zj, p))) : h[p];
+    auto start = [&](const void* base, uint32_t stride) { return static_cast<const char*>(base) + row0 * stride + (int64_t)c * (int)sizeof(TI); };
+    const char *xp = start(g.x, g.x_s), *rp = start(g.r, g.r_s), *ip = start(g.i, g.i_s), *zp = start(g.z, g.z_s);
+    auto issue = [&](int j) {                         // (a thread reads what it copied: nothing waits for another)
+        if (j < len) {
+            const uint64_t node = (uint32_t)node_of(j);
+            if (in) {
+                X::copy(&ring[j % DEPTH][0][threadIdx.x], xp + node * g.x_s);
+                X::copy(&ring[j % DEPTH][1][threadIdx.x], rp + node * g.r_s);
+                X::copy(&ring[j % DEPTH][2][threadIdx.x], ip + node * g.i_s);
+                if (g.z) X::copy(&ring[j % DEPTH][3][threadIdx.x], zp + node * g.z_s);
             }
-        };
-        if (wide) token(std::true_type{});
-        else token(std::false_type{});
-        if (g.o) X::store(g.o, here * g.C + c, o);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int j = 0; j < DEPTH; ++j) issue(j);
+    char* const op = static_cast<char*>(g.o) + (row0 * g.C + c) * (int64_t)sizeof(TI);
+    for (int j = 0; j < len; ++j) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
+        const int node = node_of(j);
+        if (in) {
+            typename X::Raw x, r, i, z;
+            x.w = ring[j % DEPTH][0][threadIdx.x];
+            r.w = ring[j % DEPTH][1][threadIdx.x];
+            i.w = ring[j % DEPTH][2][threadIdx.x];
+            if (g.z) z.w = ring[j % DEPTH][3][threadIdx.x];
+            float2 o[PAIRS];
+            auto token = [&](auto w) {
+#pragma unroll
+                for (int p = 0; p < PAIRS; ++p) {
+                    const Step s = step_of<decltype(w)::value>(k[p], X::pair(x, p), X::pair(r, p), X::pair(i, p));
+                    h[p] = fma2(s.a, h[p], s.b);
+                    o[p] = g.z ? mul2(h[p], silu(X::pair(z, p))) : h[p];
+                }
+            };
+            if (wide) token(std::true_type{});
+            else token(std::false_type{});
+            if (g.o) X::store(op + (uint64_t)(uint32_t)node * ((uint32_t)g.C * (uint32_t)sizeof(TI)), 0, o);
+        }
+        issue(j + DEPTH);
     }
     if (in && g.S_out) {
         const size_t at = (size_t)slot * g.C + c;
@@ -156,10 +178,10 @@ cudaError_t tokens(const TokenArgs& a, cudaStream_t s) {
 // The most neighbouring channels (1, 2, 4, 8) that every row, state and parameter can be taken by.
 int widest(const TokenArgs& a, int es) {
     uint64_t rows = 0, states = 0;                    // the addresses and strides, or'ed
-    auto row = [&](const void* p, int64_t stride) {
-        if (p) rows |= reinterpret_cast<uintptr_t>(p) | (uint64_t)(stride * es);
+    auto row = [&](const void* p, uint64_t stride) {
+        if (p) rows |= reinterpret_cast<uintptr_t>(p) | stride;
     };
-    row(a.x, a.x_s); row(a.r, a.r_s); row(a.i, a.i_s); row(a.z, a.z_s); row(a.o, a.C);
+    row(a.x, a.x_s); row(a.r, a.r_s); row(a.i, a.i_s); row(a.z, a.z_s); row(a.o, (uint64_t)a.C * es);
     for (const float* p : {a.S_in, (const float*)a.S_out, a.A_log, a.r_bias, a.i_bias}) states |= reinterpret_cast<uintptr_t>(p);
     int v = 16 / es;
     while (v > 1 && (rows % (v * es) != 0 || states % ((v < 4 ? v : 4) * 4) != 0 || a.C % v != 0)) v /= 2;
