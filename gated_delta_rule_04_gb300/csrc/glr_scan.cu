@@ -4,8 +4,8 @@
 // One pass over the data.  Tiles of 64 tokens x 64 channels lie in shared memory
 // in their own type, copied two tiles ahead; a thread holds 8 tokens of 2
 // channels, computes their a and b = m v x once, and the map h -> A h + B of its
-// run.  A ninth warp composes the maps and walks along the tiles (glr_tile.cuh) for the
-// value that comes in, while the others are at the next tile's maps; the second
+// run.  Two more warps compose the maps and walk along the tiles (glr_tile.cuh) for the
+// value that comes in, while those 8 are at the next tile's maps; the second
 // sweep over the 8 tokens is one multiply-add a token and the output gate.
 // Sequences lie anywhere in the tiles: a token that begins one starts its run
 // anew from S_in.
@@ -18,11 +18,13 @@ namespace kda {
 namespace glr {
 namespace {
 
-constexpr int ALL = NT + 32;         // 8 warps that compute, one that walks
-// Named barriers, two each: a tile's maps are there; its warps' first values are.  (The second
+constexpr int ALL = NT + 64;         // 8 warps that compute, two that walk
+constexpr int MEET = NT + 32;        // the computing ones and one that walks
+// Named barriers, two each: READY, a tile's maps are there; COME, its warps' first values are.  (The second
 // also keeps the computing warps together: they share what they fetch of the code.  With an
 // mbarrier instead, which does not, 198 us for 189 at 16384 tokens x 4096.)
 constexpr int READY = 1, COME = 3;
+constexpr int RING = 4;              // tiles whose places are known
 
 // What a warp keeps of a tile between its two sweeps.
 struct Pending {
@@ -36,72 +38,55 @@ __global__ void __launch_bounds__(ALL, PER_SM) scan_kernel(const __grid_constant
     using R = Rows<TI, MODE>;
     constexpr int STAGES = 3, TENSORS = GATED ? 4 : 3;
     extern __shared__ __align__(128) unsigned char rows_smem[];    // [WARPS][STAGES][x, r, i, z]
-    __shared__ int2 tk[STAGES];
-    __shared__ float2 sG[STAGES][3][32];             // the gates' constants of the tiles
+    __shared__ int2 tk[RING];                        // the tiles' places: order and column, -1 behind the last
+    __shared__ float2 sG[RING][3][32];               // and gate constants
     __shared__ float2 sA[2][WARPS][32], sB[2][WARPS][32], sIn[2][WARPS][32];
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    auto place_gates = [&](int slot, const Gate& k) {
+        sG[slot][0][lane] = k.ea;
+        sG[slot][1][lane] = k.rb;
+        sG[slot][2][lane] = k.ib;
+    };
     cudaGridDependencySynchronize();
-    auto fetch = [&](int2& tile, Gate& k) {          // the next tile, by the walking warp
-        if (lane == 0) tile = next_tile(g);
-        tile.x = __shfl_sync(0xffffffffu, tile.x, 0);
-        tile.y = __shfl_sync(0xffffffffu, tile.y, 0);
-        k = load_gate(g, tile.y);
-    };
-    auto place = [&](int stage, int2 tile, const Gate& k) {
-        if (lane == 0) tk[stage] = tile;
-        sG[stage][0][lane] = k.ea;
-        sG[stage][1][lane] = k.rb;
-        sG[stage][2][lane] = k.ib;
-    };
-    if (warp == WARPS)
-        for (int k = 0; k < STAGES; ++k) {
-            int2 tile;
-            Gate q;
-            fetch(tile, q);
-            place(k, tile, q);
-        }
+    if (tid == 0)
+        for (int k = 0; k < STAGES; ++k) tk[k] = place_of(g, take_ticket(g));
     __syncthreads();
 
-    if (warp == WARPS) {                             // the walk: maps of the tile's warps in, their first values out
-        if (tk[0].x == 0 && tk[0].y == 0 && lane == 0) *g.status = ERR_NONE;
-        uint32_t turn = 0;
-        for (int stage = 0; tk[stage].x >= 0; stage = stage + 1 == STAGES ? 0 : stage + 1, ++turn) {
-            const int2 tile = tk[stage];
-            const int buf = turn & 1;
-            int2 third;
-            Gate q;
-            fetch(third, q);
-            if (buf) bar_sync(READY + 1, ALL);
-            else bar_sync(READY, ALL);
-            place(stage, third, q);                  // (the others have read this tile's; they see it behind COME)
-            float2 A[WARPS], B[WARPS];
-#pragma unroll
-            for (int w = 0; w < WARPS; ++w) {
-                A[w] = sA[buf][w][lane];
-                B[w] = sB[buf][w][lane];
-            }
-            float2 At = A[0], Bt = B[0];
+    // The walks, even tiles' by one warp and odd ones' by the other (one warp for all, which also fetched the
+    // tickets, was what the others waited for: 151 us at 16384 tokens x 4096): maps of the
+    // tile's warps in, their first values out.
+    if (warp >= WARPS) {
+        const int buf = warp - WARPS;
+        if (tk[0].x == 0 && tk[0].y == 0 && tid == NT) *g.status = ERR_NONE;
+        place_gates(buf, load_gate(g, tk[buf].y));
+        __syncthreads();
+        for (int k = buf;; k += 2) {
+            bar_sync(READY + buf, MEET);
+            const int2 tile = tk[k % RING], second = tk[(k + 2) % RING];
+            if (tile.x < 0) return;
+            const Gate q = load_gate(g, second.y);   // of the tile after the next
+            float2 At = sA[buf][0][lane], Bt = sB[buf][0][lane];
 #pragma unroll
             for (int w = 1; w < WARPS; ++w) {
-                Bt = apply(A[w], B[w], Bt);
-                At = A[w].x < 0.f ? A[w] : At.x < 0.f ? At : mul2(At, A[w]);
+                const float2 A = sA[buf][w][lane], B = sB[buf][w][lane];
+                Bt = apply(A, B, Bt);
+                At = A.x < 0.f ? A : At.x < 0.f ? At : mul2(At, A);
             }
             float2 h = walk(g, tile.x, tile.y, At, Bt);
 #pragma unroll
             for (int w = 0; w < WARPS; ++w) {
                 sIn[buf][w][lane] = h;
-                h = apply(A[w], B[w], h);
+                h = apply(sA[buf][w][lane], sB[buf][w][lane], h);
             }
-            if (buf) bar_arrive(COME + 1, ALL);
-            else bar_arrive(COME, ALL);
+            place_gates((k + 2) % RING, q);
+            bar_arrive(COME + buf, MEET);
         }
-        return;
     }
 
     unsigned char* const mine = rows_smem + warp * STAGES * TENSORS * R::BYTES;
     const uint32_t mine_u = ptx::smem_u32(mine);
-    auto issue = [&](int stage) {
-        const int2 tile = tk[stage];
+    auto issue = [&](int stage, int k) {
+        const int2 tile = tk[k % RING];
         if (tile.x >= 0) {
             const int t = tile.x * CHUNK + warp * SUB, c0 = tile.y * TILE_C;
             const int rows = (int)g.T - t, cols = min(TILE_C, g.C - c0);
@@ -116,10 +101,10 @@ __global__ void __launch_bounds__(ALL, PER_SM) scan_kernel(const __grid_constant
     auto seq_of = [&](const Borders& bd, int j) { return (size_t)seq_id(g.f, bd.seq + __popc((bd.start >> 1) & ((1u << j) - 1))); };
 
     // a and b of the warp's tokens, and its map
-    auto first_sweep = [&](Pending& p, int stage, int buf) {
-        p.tt = tk[stage].x;
-        p.tc = tk[stage].y;
-        const Gate k{sG[stage][0][lane], sG[stage][1][lane], sG[stage][2][lane]};
+    auto first_sweep = [&](Pending& p, int stage, int slot, int buf) {
+        p.tt = tk[slot].x;
+        p.tc = tk[slot].y;
+        const Gate k{sG[slot][0][lane], sG[slot][1][lane], sG[slot][2][lane]};
         const int t = p.tt * CHUNK + warp * SUB, c0 = p.tc * TILE_C, c = c0 + 2 * lane;
         p.bd = borders(g, p.tt, t);
         asm volatile("cp.async.wait_group 1;" ::: "memory");
@@ -163,7 +148,7 @@ __global__ void __launch_bounds__(ALL, PER_SM) scan_kernel(const __grid_constant
         }
         sA[buf][warp][lane] = A;
         sB[buf][warp][lane] = B;
-        bar_arrive(READY + buf, ALL);
+        bar_arrive(READY + buf, MEET);
     };
     // the states and outputs of a tile, once its first value is there
     auto second_sweep = [&](const Pending& p, int stage, int buf) {
@@ -172,7 +157,7 @@ __global__ void __launch_bounds__(ALL, PER_SM) scan_kernel(const __grid_constant
         const typename R::Odd oz = R::odd(g.z, g.z_s, t, c0);
         char* o = row_at<TI>(g.o, g.o_s, t, c);
         const bool pair = pairs && left > 1, whole = pairs && c0 + TILE_C <= g.C && rows >= SUB && (p.bd.start | p.bd.end) == 0;
-        bar_sync(COME + buf, ALL);
+        bar_sync(COME + buf, MEET);
         float2 h = sIn[buf][warp][lane];
         if (g.states && warp == 0 && !(p.bd.start & 1)) put(g.states + (size_t)p.tt * g.C + c, left, false, h);
         if (whole) {
@@ -195,21 +180,30 @@ __global__ void __launch_bounds__(ALL, PER_SM) scan_kernel(const __grid_constant
 
     // Tile k's second sweep follows the first of tile k + 1, so the walk has the time of a whole
     // tile; then the rows of tile k + 3 take the place of its own.
-    for (int k = 0; k < STAGES; ++k) issue(k);
+    for (int k = 0; k < STAGES; ++k) issue(k, k);
+    uint32_t ticket = 0;                             // of tile k + 3, taken an iteration ahead
+    if (tid == 0) ticket = take_ticket(g);
+    __syncthreads();                                 // (the first tiles' gate constants)
     Pending p[2];
     int stage = 0;
-    auto next = [](int x) { return x + 1 == STAGES ? 0 : x + 1; };
-    if (tk[0].x < 0) return;
-    first_sweep(p[0], 0, 0);
-    for (;;) {
+    if (tk[0].x >= 0) first_sweep(p[0], 0, 0, 0);
+    else bar_arrive(READY, MEET);
+    for (int k0 = 0;; k0 += 2) {
 #pragma unroll
         for (int half = 0; half < 2; ++half) {       // tile k in p[half], tile k + 1 in p[half ^ 1]
-            const int after = next(stage);
-            const bool more = tk[after].x >= 0;
-            if (more) first_sweep(p[half ^ 1], after, half ^ 1);
+            const int k = k0 + half, after = stage + 1 == STAGES ? 0 : stage + 1;
+            if (tk[k % RING].x < 0) {                // no more: the other walk ends too
+                bar_arrive(READY + (half ^ 1), MEET);
+                return;
+            }
+            if (tid == 0) {
+                tk[(k + 3) % RING] = place_of(g, ticket);
+                ticket = take_ticket(g);
+            }
+            if (tk[(k + 1) % RING].x >= 0) first_sweep(p[half ^ 1], after, (k + 1) % RING, half ^ 1);
+            else bar_arrive(READY + (half ^ 1), MEET);
             second_sweep(p[half], stage, half);
-            if (!more) return;
-            issue(stage);
+            issue(stage, k + 3);
             stage = after;
         }
     }

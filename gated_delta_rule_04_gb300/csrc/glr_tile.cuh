@@ -203,7 +203,7 @@ __device__ __forceinline__ Borders borders(const ScanArgs& g, int tile_t, int t)
 // ---- the walk along the tiles -------------------------------------------------------------
 // Tiles are taken in the order of a ticket, all of one place along T before the next, so a
 // tile's predecessors have been taken, by CTAs that are running, and every wait ends.  A
-// tile publishes its map h -> A h + B, then looks back for the nearest of 4
+// tile publishes its map h -> A h + B, then looks back for the nearest of 3
 // predecessors whose outgoing value is known, and applies the maps in between in their order:
 // the same operations in any timing, so results do not depend on it.
 // Maps and values are their own flags: the words are set to EMPTY, a NaN that is never
@@ -212,7 +212,7 @@ __device__ __forceinline__ Borders borders(const ScanArgs& g, int tile_t, int t)
 // more read: 5 us more a tile.)
 constexpr uint64_t WAIT_NS = 2000000000ull;
 constexpr uint32_t EMPTY = 0xffffffffu;
-constexpr int BACK = 4;
+constexpr int BACK = 3;
 
 __device__ __forceinline__ uint32_t word_of(float x) {
     const uint32_t u = __float_as_uint(x);
@@ -293,13 +293,15 @@ __device__ __forceinline__ float2 walk(const ScanArgs& g, int order, int tile_c,
     return in;
 }
 
-// The next tile to be taken: its place in the walk and its column, -1 behind the last (the counter starts at
-// EMPTY, like everything else that is set before a call).
-__device__ __forceinline__ int2 next_tile(const ScanArgs& g) {
-    const uint32_t k = atomicAdd(g.ticket, 1u) + 1u;
+// The next ticket (the counter starts at EMPTY, like everything else that is set before a call), and a ticket's
+// tile: its place in the walk and its column, -1 behind the last.
+__device__ __forceinline__ uint32_t take_ticket(const ScanArgs& g) { return atomicAdd(g.ticket, 1u); }
+__device__ __forceinline__ int2 place_of(const ScanArgs& g, uint32_t ticket) {
+    const uint32_t k = ticket + 1u;
     if (k >= (uint32_t)g.tiles_t * (uint32_t)g.tiles_c) return make_int2(-1, 0);
     return make_int2((int)(k / (uint32_t)g.tiles_c), (int)(k % (uint32_t)g.tiles_c));
 }
+__device__ __forceinline__ int2 next_tile(const ScanArgs& g) { return place_of(g, take_ticket(g)); }
 
 __device__ __forceinline__ void bar_arrive(int id, int threads) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
 __device__ __forceinline__ void bar_sync(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
