@@ -286,12 +286,12 @@ cudaError_t launch_backward(const ScanArgs& a, int io_bf16, cudaStream_t s) {
     const int es = io_bf16 ? 2 : 4;
     cudaError_t e = cudaSuccess;
     if (a.tiles_t > 0) {
-        const int mode = std::max({row_mode(a.x, a.x_s), row_mode(a.r, a.r_s), row_mode(a.i, a.i_s),
-                                   row_mode(a.d_o, a.do_s), a.z ? row_mode(a.z, a.z_s) : 0});
+        const int mode = std::max({row_mode(a.x, a.x_s, a.C), row_mode(a.r, a.r_s, a.C), row_mode(a.i, a.i_s, a.C),
+                                   row_mode(a.d_o, a.do_s, a.C), a.z ? row_mode(a.z, a.z_s, a.C) : 0});
         const int pairs = (row_pairs(a.dx, a.dx_s, es) ? OUT_X : 0) | (row_pairs(a.dr, a.dr_s, es) ? OUT_R : 0) |
                           (row_pairs(a.di, a.di_s, es) ? OUT_I : 0) | (a.z && row_pairs(a.dz, a.dz_s, es) ? OUT_Z : 0);
-        if (!io_bf16) e = mode == M16 ? backward<float, M16>(a, pairs, s) : backward<float, M4>(a, pairs, s);
-        else e = mode == M16 ? backward<__nv_bfloat16, M16>(a, pairs, s)
+        if (!io_bf16) e = mode == MTMA ? backward<float, MTMA>(a, pairs, s) : backward<float, M4>(a, pairs, s);
+        else e = mode == MTMA ? backward<__nv_bfloat16, MTMA>(a, pairs, s)
                : mode == M4 ? backward<__nv_bfloat16, M4>(a, pairs, s) : backward<__nv_bfloat16, MODD>(a, pairs, s);
         if (e != cudaSuccess) return e;
     }

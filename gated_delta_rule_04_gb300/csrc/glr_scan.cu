@@ -22,8 +22,8 @@ constexpr int ALL = NT + 64;         // 8 warps that compute, two that walk
 constexpr int MEET = NT + 32;        // the computing ones and one that walks
 // Named barriers, two each: READY, a tile's maps are there; COME, its warps' first values are.  (The second
 // also keeps the computing warps together: they share what they fetch of the code.  With an
-// mbarrier instead, which does not, 198 us for 189 at 16384 tokens x 4096.)
-constexpr int READY = 1, COME = 3;
+// mbarrier instead, which does not, 198 us for 189 at 16384 tokens x 4096.)  FREE: its rows have been read.
+constexpr int READY = 1, COME = 3, FREE = 5;
 constexpr int RING = 4;              // tiles whose places are known
 
 // What a warp keeps of a tile between its two sweeps.
@@ -34,10 +34,11 @@ struct Pending {
 };
 
 template <typename TI, int MODE, bool GATED, int PER_SM>
-__global__ void __launch_bounds__(ALL, PER_SM) scan_kernel(const __grid_constant__ ScanArgs g, bool pairs) {
+__global__ void __launch_bounds__(ALL, PER_SM)
+    scan_kernel(const __grid_constant__ ScanArgs g, const __grid_constant__ Maps maps, bool pairs) {
     using R = Rows<TI, MODE>;
-    constexpr int STAGES = 3, TENSORS = GATED ? 4 : 3;
-    extern __shared__ __align__(128) unsigned char rows_smem[];    // [WARPS][STAGES][x, r, i, z]
+    constexpr int STAGES = 3, TENSORS = GATED ? 4 : 3, STAGE_BYTES = TENSORS * R::TILE;
+    extern __shared__ __align__(128) unsigned char rows_smem[];    // [STAGES][x, r, i, z][CHUNK]
     __shared__ int2 tk[RING];                        // the tiles' places: order and column, -1 behind the last
     __shared__ float2 sG[RING][3][32];               // and gate constants
     __shared__ float2 sA[2][WARPS][32], sB[2][WARPS][32], sIn[2][WARPS][32];
@@ -47,10 +48,24 @@ __global__ void __launch_bounds__(ALL, PER_SM) scan_kernel(const __grid_constant
         sG[slot][1][lane] = k.rb;
         sG[slot][2][lane] = k.ib;
     };
+    __shared__ uint64_t landed[STAGES];              // (MTMA) a tile's rows are there
+    const uint32_t bars = ptx::smem_u32(landed);
+    if (tid == 0) {
+        for (int k = 0; k < STAGES; ++k) ptx::mbar_init(bars + 8 * k, 1);
+        ptx::fence_mbar_init();
+    }
     cudaGridDependencySynchronize();
     if (tid == 0)
         for (int k = 0; k < STAGES; ++k) tk[k] = place_of(g, take_ticket(g));
     __syncthreads();
+    auto load_tile = [&](int stage, int k) {         // (MTMA) by one thread
+        const int2 tile = tk[k % RING];
+        if (tile.x < 0) return;
+        const uint32_t s = ptx::smem_u32(rows_smem) + stage * STAGE_BYTES, bar = bars + 8 * stage;
+        ptx::mbar_expect_tx(bar, STAGE_BYTES);
+#pragma unroll
+        for (int m = 0; m < TENSORS; ++m) ptx::tma_load_2d(s + m * R::TILE, &maps.m[m], tile.y * TILE_C, tile.x * CHUNK, bar);
+    };
 
     // The walks, even tiles' by one warp and odd ones' by the other (one warp for all, which also fetched the
     // tickets, was what the others waited for: 151 us at 16384 tokens x 4096): maps of the
@@ -58,6 +73,8 @@ __global__ void __launch_bounds__(ALL, PER_SM) scan_kernel(const __grid_constant
     if (warp >= WARPS) {
         const int buf = warp - WARPS;
         if (tk[0].x == 0 && tk[0].y == 0 && tid == NT) *g.status = ERR_NONE;
+        if (MODE == MTMA && tid == NT)
+            for (int k = 0; k < STAGES; ++k) load_tile(k, k);
         place_gates(buf, load_gate(g, tk[buf].y));
         __syncthreads();
         for (int k = buf;; k += 2) {
@@ -80,23 +97,39 @@ __global__ void __launch_bounds__(ALL, PER_SM) scan_kernel(const __grid_constant
             }
             place_gates((k + 2) % RING, q);
             bar_arrive(COME + buf, MEET);
+            if (MODE == MTMA) {                      // tile k + 3 in the place of this one
+                bar_sync(FREE + buf, MEET);
+                if (lane == 0) load_tile(k % STAGES, k + STAGES);
+            }
         }
     }
 
-    unsigned char* const mine = rows_smem + warp * STAGES * TENSORS * R::BYTES;
+    unsigned char* const mine = rows_smem + warp * R::BYTES;
     const uint32_t mine_u = ptx::smem_u32(mine);
+    uint32_t phases = 0;
     auto issue = [&](int stage, int k) {
-        const int2 tile = tk[k % RING];
-        if (tile.x >= 0) {
-            const int t = tile.x * CHUNK + warp * SUB, c0 = tile.y * TILE_C;
-            const int rows = (int)g.T - t, cols = min(TILE_C, g.C - c0);
-            const uint32_t s = mine_u + stage * TENSORS * R::BYTES;
-            R::load(s, g.x, g.x_s, t, c0, rows, cols);
-            R::load(s + R::BYTES, g.r, g.r_s, t, c0, rows, cols);
-            R::load(s + 2 * R::BYTES, g.i, g.i_s, t, c0, rows, cols);
-            if (GATED) R::load(s + 3 * R::BYTES, g.z, g.z_s, t, c0, rows, cols);
+        if constexpr (MODE != MTMA) {
+            const int2 tile = tk[k % RING];
+            if (tile.x >= 0) {
+                const int t = tile.x * CHUNK + warp * SUB, c0 = tile.y * TILE_C;
+                const int rows = (int)g.T - t, cols = min(TILE_C, g.C - c0);
+                const uint32_t s = mine_u + stage * STAGE_BYTES;
+                R::load(s, g.x, g.x_s, t, c0, rows, cols);
+                R::load(s + R::TILE, g.r, g.r_s, t, c0, rows, cols);
+                R::load(s + 2 * R::TILE, g.i, g.i_s, t, c0, rows, cols);
+                if (GATED) R::load(s + 3 * R::TILE, g.z, g.z_s, t, c0, rows, cols);
+            }
+            ptx::cp_async_commit();
         }
-        ptx::cp_async_commit();
+    };
+    auto wait_rows = [&](int stage) {
+        if constexpr (MODE == MTMA) {
+            wait_or(g, bars + 8 * stage, phases >> stage & 1);
+            phases ^= 1u << stage;
+        } else {
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+            __syncwarp();
+        }
     };
     auto seq_of = [&](const Borders& bd, int j) { return (size_t)seq_id(g.f, bd.seq + __popc((bd.start >> 1) & ((1u << j) - 1))); };
 
@@ -107,14 +140,13 @@ __global__ void __launch_bounds__(ALL, PER_SM) scan_kernel(const __grid_constant
         const Gate k{sG[slot][0][lane], sG[slot][1][lane], sG[slot][2][lane]};
         const int t = p.tt * CHUNK + warp * SUB, c0 = p.tc * TILE_C, c = c0 + 2 * lane;
         p.bd = borders(g, p.tt, t);
-        asm volatile("cp.async.wait_group 1;" ::: "memory");
-        __syncwarp();
-        const unsigned char* s = mine + stage * TENSORS * R::BYTES;
+        wait_rows(stage);
+        const unsigned char* s = mine + stage * STAGE_BYTES;
         const typename R::Odd ox = R::odd(g.x, g.x_s, t, c0), orr = R::odd(g.r, g.r_s, t, c0), oi = R::odd(g.i, g.i_s, t, c0);
         float2 A = f2(1.f), B = f2(0.f);
         auto token = [&](int j, auto wide) {
-            const Step st = step_of<decltype(wide)::value>(k, R::get(s, j, ox), R::get(s + R::BYTES, j, orr),
-                                                           R::get(s + 2 * R::BYTES, j, oi));
+            const Step st = step_of<decltype(wide)::value>(k, R::get(s, j, ox), R::get(s + R::TILE, j, orr),
+                                                           R::get(s + 2 * R::TILE, j, oi));
             p.a[j] = st.a;
             p.b[j] = st.b;
         };
@@ -153,7 +185,7 @@ __global__ void __launch_bounds__(ALL, PER_SM) scan_kernel(const __grid_constant
     // the states and outputs of a tile, once its first value is there
     auto second_sweep = [&](const Pending& p, int stage, int buf) {
         const int t = p.tt * CHUNK + warp * SUB, c0 = p.tc * TILE_C, c = c0 + 2 * lane, left = g.C - c, rows = (int)g.T - t;
-        const unsigned char* s = mine + stage * TENSORS * R::BYTES + 3 * R::BYTES;
+        const unsigned char* s = mine + stage * STAGE_BYTES + 3 * R::TILE;
         const typename R::Odd oz = R::odd(g.z, g.z_s, t, c0);
         char* o = row_at<TI>(g.o, g.o_s, t, c);
         const bool pair = pairs && left > 1, whole = pairs && c0 + TILE_C <= g.C && rows >= SUB && (p.bd.start | p.bd.end) == 0;
@@ -203,7 +235,8 @@ __global__ void __launch_bounds__(ALL, PER_SM) scan_kernel(const __grid_constant
             if (tk[(k + 1) % RING].x >= 0) first_sweep(p[half ^ 1], after, (k + 1) % RING, half ^ 1);
             else bar_arrive(READY + (half ^ 1), MEET);
             second_sweep(p[half], stage, half);
-            issue(stage, k + 3);
+            if (MODE == MTMA) bar_arrive(FREE + half, MEET);
+            issue(stage, k + STAGES);
             stage = after;
         }
     }
@@ -211,9 +244,16 @@ __global__ void __launch_bounds__(ALL, PER_SM) scan_kernel(const __grid_constant
 
 template <typename TI, int MODE, bool GATED>
 cudaError_t scan(const ScanArgs& a, bool pairs, cudaStream_t s) {
+    Maps maps;
+    if (MODE == MTMA) {
+        constexpr int es = sizeof(TI);
+        if (!encode(&maps.m[0], a.x, a.x_s, es, a) || !encode(&maps.m[1], a.r, a.r_s, es, a) ||
+            !encode(&maps.m[2], a.i, a.i_s, es, a) || (GATED && !encode(&maps.m[3], a.z, a.z_s, es, a)))
+            return cudaErrorUnknown;
+    }
     constexpr int PER_SM = sizeof(TI) == 2 ? 2 : 1;
     auto k = scan_kernel<TI, MODE, GATED, PER_SM>;
-    constexpr int SMEM = WARPS * 3 * (GATED ? 4 : 3) * Rows<TI, MODE>::BYTES;
+    constexpr int SMEM = 3 * (GATED ? 4 : 3) * Rows<TI, MODE>::TILE;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -224,7 +264,7 @@ cudaError_t scan(const ScanArgs& a, bool pairs, cudaStream_t s) {
         if (e != cudaSuccess) return e;
         done.fetch_or(bit);
     }
-    return launch_behind(k, std::min<int64_t>((int64_t)a.tiles_t * a.tiles_c, SMS * PER_SM), ALL, SMEM, s, a, pairs);
+    return launch_behind(k, std::min<int64_t>((int64_t)a.tiles_t * a.tiles_c, SMS * PER_SM), ALL, SMEM, s, a, maps, pairs);
 }
 
 template <typename TI, int MODE> cudaError_t scan(const ScanArgs& a, bool pairs, cudaStream_t s) {
@@ -266,11 +306,11 @@ cudaError_t launch_setup(const ScanArgs& a, size_t empty, cudaStream_t s) {
 
 cudaError_t launch_scan(const ScanArgs& a, int io_bf16, cudaStream_t s) {
     const int es = io_bf16 ? 2 : 4;
-    const int mode = std::max({row_mode(a.x, a.x_s), row_mode(a.r, a.r_s), row_mode(a.i, a.i_s),
-                               a.z ? row_mode(a.z, a.z_s) : 0});
+    const int mode = std::max({row_mode(a.x, a.x_s, a.C), row_mode(a.r, a.r_s, a.C), row_mode(a.i, a.i_s, a.C),
+                               a.z ? row_mode(a.z, a.z_s, a.C) : 0});
     const bool pairs = row_pairs(a.o, a.o_s, es);
-    if (!io_bf16) return mode == M16 ? scan<float, M16>(a, pairs, s) : scan<float, M4>(a, pairs, s);
-    return mode == M16 ? scan<__nv_bfloat16, M16>(a, pairs, s)
+    if (!io_bf16) return mode == MTMA ? scan<float, MTMA>(a, pairs, s) : scan<float, M4>(a, pairs, s);
+    return mode == MTMA ? scan<__nv_bfloat16, MTMA>(a, pairs, s)
          : mode == M4 ? scan<__nv_bfloat16, M4>(a, pairs, s) : scan<__nv_bfloat16, MODD>(a, pairs, s);
 }
 

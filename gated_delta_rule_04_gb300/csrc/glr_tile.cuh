@@ -6,6 +6,7 @@
 #include <algorithm>
 
 #include "glr_math.cuh"
+#include "ssm_common.cuh"
 #include "tc_ptx.cuh"
 
 namespace kda {
@@ -17,65 +18,48 @@ constexpr int SUB = CHUNK / WARPS;   // tokens of a warp
 static_assert(TILE_C == 64 && SUB == 8, "lanes hold channel pairs, warps 8 tokens");
 
 // ---- tiles in shared memory -------------------------------------------------------------
-// How rows are copied: 16 bytes at a time, 4 bytes at a time, or (16-bit elements whose rows
-// may start on odd ones) 4 bytes at a time from the word that holds the row's first element.
-enum Mode { M16 = 0, M4 = 1, MODD = 2 };
+// How rows are copied: a tile by one tensor copy (rows on 16 bytes, at least a tile's channels), 4
+// bytes at a time, or (16-bit elements whose rows may start on odd ones) 4 bytes at a time from
+// the word that holds the row's first element.
+enum Mode { MTMA = 0, M4 = 1, MODD = 2 };
+constexpr int MAX_TENSORS = 5;
+struct alignas(64) Maps {            // of the tensors, in boxes of a tile; zero fill out of bounds
+    CUtensorMap m[MAX_TENSORS];
+};
 
-// A warp's 8 rows of one tensor.  Each warp copies, waits for and reads its own.
+// A warp's 8 rows of one tensor's tile.  Where the tile is no tensor copy, each warp copies, waits for and reads its own.
 template <typename TI, int MODE> struct Rows {
     static constexpr int ES = sizeof(TI);
     static constexpr int PITCH = TILE_C * ES + (MODE == MODD ? 4 : 0);
-    static constexpr int BYTES = SUB * PITCH;
+    static constexpr int BYTES = SUB * PITCH, TILE = CHUNK * PITCH;
 
     template <int N> static __device__ __forceinline__ void copy(uint32_t dst, const char* p, int bytes) {
         if constexpr (N == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(p), "r"(bytes) : "memory");
         else asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(p), "r"(bytes) : "memory");
     }
 
-    // Starts the copies of rows t .. t + rows - 1 (`stride` bytes apart), channels c0 .. c0 + cols - 1; the rest
-    // becomes zero.
+    // (not MTMA) Starts the copies of rows t .. t + rows - 1 (`stride` bytes apart), channels c0 .. c0 + cols - 1;
+    // the rest becomes zero.
     static __device__ __forceinline__ void load(uint32_t dst, const void* base, uint32_t stride, int t, int c0, int rows, int cols) {
         const int lane = threadIdx.x & 31;
         const char* const first = static_cast<const char*>(base);
-        if constexpr (MODE == M16) {
-            constexpr int PER = PITCH / 16, STEP = 32 / PER;    // pieces of a row, rows of a copy
-            const int piece = lane % PER, row = lane / PER;
-            const char* p = first + (uint64_t)(uint32_t)(t + row) * stride + (uint32_t)(c0 * ES + piece * 16);
-            dst += row * PITCH + piece * 16;
-            if (rows >= SUB && cols == TILE_C) {
+        constexpr int PER = PITCH / 4;                          // 32, 33 or 64 words of a row
+        const char* p = first + (uint64_t)(uint32_t)t * stride + (uint32_t)(c0 * ES);
 #pragma unroll
-                for (int k = 0; k < SUB / STEP; ++k) {
-                    copy<16>(dst + k * STEP * PITCH, p, 16);
-                    p += (uint64_t)stride * STEP;
-                }
-            } else {
-                const int bytes = min(max(cols * ES - piece * 16, 0), 16);
-#pragma unroll
-                for (int k = 0; k < SUB / STEP; ++k) {
-                    const int n = row + k * STEP < rows ? bytes : 0;
-                    copy<16>(dst + k * STEP * PITCH, n > 0 ? p : first, n);
-                    p += (uint64_t)stride * STEP;
-                }
+        for (int k = 0; k < SUB; ++k) {
+            const char* q = p;
+            int bytes = k < rows ? cols * ES : 0;
+            if (MODE == MODD) {                                 // from the word that holds the first element: the half
+                const int odd = (int)(reinterpret_cast<uintptr_t>(p) & 2);   // before it is copied and not used
+                q -= odd;
+                bytes += bytes > 0 ? odd : 0;
             }
-        } else {
-            constexpr int PER = PITCH / 4;                      // 32, 33 or 64 words of a row
-            const char* p = first + (uint64_t)(uint32_t)t * stride + (uint32_t)(c0 * ES);
 #pragma unroll
-            for (int k = 0; k < SUB; ++k) {
-                const char* q = p;
-                int bytes = k < rows ? cols * ES : 0;
-                if (MODE == MODD) {                             // from the word that holds the first element: the half
-                    const int odd = (int)(reinterpret_cast<uintptr_t>(p) & 2);   // before it is copied and not used
-                    q -= odd;
-                    bytes += bytes > 0 ? odd : 0;
-                }
-#pragma unroll
-                for (int w = lane; w < PER; w += 32) {
-                    const int n = min(max(bytes - w * 4, 0), 4);
-                    copy<4>(dst + k * PITCH + w * 4, n > 0 ? q + w * 4 : first - (reinterpret_cast<uintptr_t>(first) & 2), n);
-                }
-                p += stride;
+            for (int w = lane; w < PER; w += 32) {
+                const int n = min(max(bytes - w * 4, 0), 4);
+                copy<4>(dst + k * PITCH + w * 4, n > 0 ? q + w * 4 : first - (reinterpret_cast<uintptr_t>(first) & 2), n);
             }
+            p += stride;
         }
     }
 
@@ -118,12 +102,15 @@ template <typename TI, int MODE> struct Rows {
         return make_float2(reinterpret_cast<const float*>(rows1 + row * PITCH)[lane], reinterpret_cast<const float*>(rows2 + row * PITCH)[lane]);
     }
 };
-static_assert(Rows<float, M16>::PITCH == 256 && Rows<__nv_bfloat16, MODD>::PITCH == 132, "");
+static_assert(Rows<float, MTMA>::PITCH == 256 && Rows<__nv_bfloat16, MODD>::PITCH == 132, "");
 
 // The copies that rows take, and whether channel pairs of `es`-byte elements can be stored as one.
-inline int row_mode(const void* base, uint32_t stride) {
+inline int row_mode(const void* base, uint32_t stride, int C) {
     const uintptr_t p = reinterpret_cast<uintptr_t>(base) | stride;
-    return p % 16 == 0 ? M16 : p % 4 == 0 ? M4 : MODD;
+    return p % 16 == 0 && C >= TILE_C ? MTMA : p % 4 == 0 ? M4 : MODD;
+}
+inline bool encode(CUtensorMap* m, const void* base, uint32_t stride, int es, const ScanArgs& a) {
+    return ssm::encode_rows(m, base, es, a.T, a.C, stride / es, CHUNK, TILE_C);
 }
 inline bool row_pairs(const void* base, uint32_t stride, int es) {
     return (reinterpret_cast<uintptr_t>(base) | stride) % (2 * es) == 0;
@@ -303,6 +290,15 @@ __device__ __forceinline__ int2 place_of(const ScanArgs& g, uint32_t ticket) {
 }
 __device__ __forceinline__ int2 next_tile(const ScanArgs& g) { return place_of(g, take_ticket(g)); }
 
+// Waits for a phase of a barrier of this CTA; past a limit of turns (each waits a while itself) the error word
+// is set.
+__device__ __forceinline__ void wait_or(const ScanArgs& g, uint32_t bar, uint32_t parity) {
+    for (uint32_t turn = 0; !ptx::mbar_try_wait(bar, parity);)
+        if (++turn >> 24) {
+            atomicExch(g.status, ERR_TIMEOUT);
+            break;
+        }
+}
 __device__ __forceinline__ void bar_arrive(int id, int threads) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
 __device__ __forceinline__ void bar_sync(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
 
