@@ -24,31 +24,46 @@ namespace {
 enum { OUT_X = 1, OUT_R = 2, OUT_I = 4, OUT_Z = 8 };   // gradients whose rows take pairs
 
 template <typename TI, int MODE, bool GATED, int STAGES, int PER_SM>
-__global__ void __launch_bounds__(NT, PER_SM) backward_kernel(const __grid_constant__ ScanArgs g, int pairs) {
+__global__ void __launch_bounds__(NT, PER_SM)
+    backward_kernel(const __grid_constant__ ScanArgs g, const __grid_constant__ Maps maps, int pairs) {
     using R = Rows<TI, MODE>;
-    constexpr int TENSORS = GATED ? 5 : 4, GATES = 3 * TILE_C * 4, WARP_BYTES = TENSORS * R::BYTES + GATES;
-    extern __shared__ __align__(128) unsigned char rows_smem[];    // [WARPS][STAGES][x, r, i, do, z, gates]
+    constexpr int TENSORS = GATED ? 5 : 4, GATES = 3 * TILE_C * 4, STAGE_BYTES = TENSORS * R::TILE;
+    extern __shared__ __align__(128) unsigned char rows_smem[];    // [STAGES][x, r, i, do, z][CHUNK]
     __shared__ int2 tk[STAGES];
+    __shared__ __align__(16) float2 sG[STAGES][3][32];             // the tiles' gate constants
+    __shared__ uint64_t landed[STAGES];                            // (MTMA) a tile's rows and constants are there
     __shared__ float2 sA[WARPS][32], sB[WARPS][32], sAr[WARPS][32], sBr[WARPS][32];   // maps forwards and backwards
     __shared__ float2 sIn[32], sH[STAGES][32], sums[3][WARPS][32];
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-    unsigned char* const mine = rows_smem + warp * STAGES * WARP_BYTES;
-    const uint32_t mine_u = ptx::smem_u32(mine);
+    unsigned char* const mine = rows_smem + warp * R::BYTES;
+    const uint32_t bars = ptx::smem_u32(landed);
+    uint32_t phases = 0;
+    // (MTMA) The tile's rows and constants, by one thread.
+    auto load_tile = [&](int stage) {
+        const int2 tile = tk[stage];
+        if (tile.x < 0) return;
+        const uint32_t s = ptx::smem_u32(rows_smem) + stage * STAGE_BYTES, bar = bars + 8 * stage;
+        ptx::mbar_expect_tx(bar, STAGE_BYTES + GATES);
+#pragma unroll
+        for (int m = 0; m < TENSORS; ++m)
+            ptx::tma_load_2d(s + m * R::TILE, &maps.m[m], tile.y * TILE_C, (g.tiles_t - 1 - tile.x) * CHUNK, bar);
+        ptx::bulk_g2s(ptx::smem_u32(&sG[stage][0][0]), g.gates + (size_t)tile.y * (GATES / 8), GATES, bar);
+    };
+    // Each warp: its own rows (not MTMA); the last warp: the tile's first state, and (not MTMA) the constants.
     auto issue = [&](int stage) {
         const int2 tile = tk[stage];
         if (tile.x >= 0) {
             const int tt = g.tiles_t - 1 - tile.x, t = tt * CHUNK + warp * SUB, c0 = tile.y * TILE_C;
             const int rows = (int)g.T - t, cols = min(TILE_C, g.C - c0);
-            const uint32_t s = mine_u + stage * WARP_BYTES;
-            R::load(s, g.x, g.x_s, t, c0, rows, cols);
-            R::load(s + R::BYTES, g.r, g.r_s, t, c0, rows, cols);
-            R::load(s + 2 * R::BYTES, g.i, g.i_s, t, c0, rows, cols);
-            R::load(s + 3 * R::BYTES, g.d_o, g.do_s, t, c0, rows, cols);
-            if (GATED) R::load(s + 4 * R::BYTES, g.z, g.z_s, t, c0, rows, cols);
-            const char* gates = reinterpret_cast<const char*>(g.gates) + (size_t)tile.y * GATES;
-            for (int k = lane; k < GATES / 16; k += 32)
-                R::template copy<16>(s + TENSORS * R::BYTES + k * 16, gates + k * 16, 16);
-            if (warp == WARPS - 1) {                 // the tile's first state: the others see it behind a barrier
+            if constexpr (MODE != MTMA) {
+                const uint32_t s = ptx::smem_u32(mine) + stage * STAGE_BYTES;
+                R::load(s, g.x, g.x_s, t, c0, rows, cols);
+                R::load(s + R::TILE, g.r, g.r_s, t, c0, rows, cols);
+                R::load(s + 2 * R::TILE, g.i, g.i_s, t, c0, rows, cols);
+                R::load(s + 3 * R::TILE, g.d_o, g.do_s, t, c0, rows, cols);
+                if (GATED) R::load(s + 4 * R::TILE, g.z, g.z_s, t, c0, rows, cols);
+            }
+            if (warp == WARPS - 1) {
                 const uint32_t h = ptx::smem_u32(&sH[stage][0]);
                 const float* p = g.states + (size_t)tt * g.C + c0;
 #pragma unroll
@@ -58,10 +73,16 @@ __global__ void __launch_bounds__(NT, PER_SM) backward_kernel(const __grid_const
         }
         ptx::cp_async_commit();
     };
+    if (tid == 0) {
+        for (int k = 0; k < STAGES; ++k) ptx::mbar_init(bars + 8 * k, 1);
+        ptx::fence_mbar_init();
+    }
     cudaGridDependencySynchronize();
     if (tid == 0)
         for (int k = 0; k < STAGES; ++k) tk[k] = next_tile(g);
     __syncthreads();
+    if (MODE == MTMA && tid == NT - 1)
+        for (int k = 0; k < STAGES; ++k) load_tile(k);
     if (tk[0].x == 0 && tk[0].y == 0 && tid == 0) *g.status = ERR_NONE;
     for (int k = 0; k < STAGES; ++k) issue(k);
 
@@ -71,23 +92,28 @@ __global__ void __launch_bounds__(NT, PER_SM) backward_kernel(const __grid_const
         const int t = tt * CHUNK + warp * SUB, c0 = tc * TILE_C, c = c0 + 2 * lane, rows = (int)g.T - t, left = g.C - c;
         const Borders bd = borders(g, tt, t);
         auto seq_of = [&](int j) { return (size_t)seq_id(g.f, bd.seq + __popc((bd.start >> 1) & ((1u << j) - 1))); };
+        Gate k;
+        if (MODE != MTMA) k = load_gate(g, tc);
         asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
         __syncwarp();
+        if (MODE == MTMA) {
+            wait_or(g, bars + 8 * stage, phases >> stage & 1);
+            phases ^= 1u << stage;
+            k = Gate{sG[stage][0][lane], sG[stage][1][lane], sG[stage][2][lane]};
+        }
 
-        unsigned char* const s = mine + stage * WARP_BYTES;
-        const float2* const gates = reinterpret_cast<const float2*>(s + TENSORS * R::BYTES) + lane;
-        const Gate k{gates[0], gates[TILE_C / 2], gates[TILE_C]};
+        unsigned char* const s = mine + stage * STAGE_BYTES;
         const typename R::Odd ox = R::odd(g.x, g.x_s, t, c0), orr = R::odd(g.r, g.r_s, t, c0), oi = R::odd(g.i, g.i_s, t, c0),
                               od = R::odd(g.d_o, g.do_s, t, c0), oz = R::odd(g.z, g.z_s, t, c0);
         auto x_of = [&](int j) { return R::get(s, j, ox); };
-        auto r_of = [&](int j) { return fma2(R::get(s + R::BYTES, j, orr), f2(-LOG2E), k.rb); };
+        auto r_of = [&](int j) { return fma2(R::get(s + R::TILE, j, orr), f2(-LOG2E), k.rb); };
         // Of each token: a, w, -E = -m v, x (1 - v), K = a (v / m) x, -G.  States and gradients run with
         // the sign changed, as -E and -G lead to them; what is stored has two such factors.
         float2 a[SUB], w[SUB], nE[SUB], xv[SUB], K[SUB], nG[SUB];
         float2 A = f2(1.f), nB = f2(0.f);
         auto token = [&](int j, auto wide) {
             w[j] = sigmoid_of(r_of(j));
-            const float2 ei = ex2_most(fma2(R::get(s + 2 * R::BYTES, j, oi), f2(-LOG2E), k.ib)), di = add2(ei, f2(1.f));
+            const float2 ei = ex2_most(fma2(R::get(s + 2 * R::TILE, j, oi), f2(-LOG2E), k.ib)), di = add2(ei, f2(1.f));
             const float2 v = make_float2(rcp(di.x), rcp(di.y)), x = x_of(j);
             xv[j] = mul2(x, mul2(ei, v));
             float2 nm2;
@@ -95,13 +121,13 @@ __global__ void __launch_bounds__(NT, PER_SM) backward_kernel(const __grid_const
             const float2 iv = mul2(inv_root(nm2), v);
             nE[j] = mul2(nm2, iv);
             K[j] = mul2(mul2(a[j], iv), x);
-            const float2 dO = R::get(s + 3 * R::BYTES, j, od);
+            const float2 dO = R::get(s + 3 * R::TILE, j, od);
             if (GATED) {
-                const float2 z = R::get(s + 4 * R::BYTES, j, oz), tz = mul2(z, f2(-LOG2E));
+                const float2 z = R::get(s + 4 * R::TILE, j, oz), tz = mul2(z, f2(-LOG2E));
                 const float2 dd = fma2(make_float2(ex2(tz.x), ex2(tz.y)), f2(-1.f), f2(-1.f)), ne = make_float2(rcp(dd.x), rcp(dd.y));
                 nG[j] = mul2(dO, mul2(z, ne));
                 // -do SiLU'(z), for dz = do SiLU'(z) h
-                R::keep(s + 3 * R::BYTES, s + 4 * R::BYTES, j, mul2(dO, mul2(ne, fma2(z, add2(ne, f2(1.f)), f2(1.f)))));
+                R::keep(s + 3 * R::TILE, s + 4 * R::TILE, j, mul2(dO, mul2(ne, fma2(z, add2(ne, f2(1.f)), f2(1.f)))));
             } else {
                 nG[j] = mul2(dO, f2(-1.f));
             }
@@ -179,7 +205,7 @@ __global__ void __launch_bounds__(NT, PER_SM) backward_kernel(const __grid_const
                 nh = fma2(nE[j], x_of(j), mul2(a[j], nh));
                 if (GATED && (FAST || j < rows))
                     put<TI>(dz, FAST ? 2 : left, FAST || ((pairs & OUT_Z) && left > 1),
-                            mul2(R::kept(s + 3 * R::BYTES, s + 4 * R::BYTES, j), nh));
+                            mul2(R::kept(s + 3 * R::TILE, s + 4 * R::TILE, j), nh));
                 if (GATED) dz += g.dz_s;
             }
         };
@@ -215,10 +241,12 @@ __global__ void __launch_bounds__(NT, PER_SM) backward_kernel(const __grid_const
         if (whole) backward(std::true_type{});
         else backward(std::false_type{});
         issue(stage);                                // (the warp has read its rows, and all of them the state)
+        if (MODE == MTMA) ptx::fence_async_smem();   // (it has also written on them)
         sums[0][warp][lane] = sa;
         sums[1][warp][lane] = sr;
         sums[2][warp][lane] = si;
         __syncthreads();
+        if (MODE == MTMA && tid == NT - 1) load_tile(stage);
         if (tid < 96) {
             const int q = tid / 32;
             float2 sum = sums[q][0][lane];
@@ -260,9 +288,17 @@ __global__ void __launch_bounds__(256) params_kernel(const __grid_constant__ Sca
 
 template <typename TI, int MODE, bool GATED>
 cudaError_t backward(const ScanArgs& a, int pairs, cudaStream_t s) {
+    Maps maps;
+    if (MODE == MTMA) {
+        constexpr int es = sizeof(TI);
+        if (!encode(&maps.m[0], a.x, a.x_s, es, a) || !encode(&maps.m[1], a.r, a.r_s, es, a) ||
+            !encode(&maps.m[2], a.i, a.i_s, es, a) || !encode(&maps.m[3], a.d_o, a.do_s, es, a) ||
+            (GATED && !encode(&maps.m[4], a.z, a.z_s, es, a)))
+            return cudaErrorUnknown;
+    }
     constexpr int STAGES = sizeof(TI) == 2 ? 2 : 1, PER_SM = 2;
     auto k = backward_kernel<TI, MODE, GATED, STAGES, PER_SM>;
-    constexpr int SMEM = WARPS * STAGES * ((GATED ? 5 : 4) * Rows<TI, MODE>::BYTES + 3 * TILE_C * 4);
+    constexpr int SMEM = STAGES * (GATED ? 5 : 4) * Rows<TI, MODE>::TILE;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -273,7 +309,7 @@ cudaError_t backward(const ScanArgs& a, int pairs, cudaStream_t s) {
         if (e != cudaSuccess) return e;
         done.fetch_or(bit);
     }
-    return launch_behind(k, std::min<int64_t>((int64_t)a.tiles_t * a.tiles_c, SMS * PER_SM), NT, SMEM, s, a, pairs);
+    return launch_behind(k, std::min<int64_t>((int64_t)a.tiles_t * a.tiles_c, SMS * PER_SM), NT, SMEM, s, a, maps, pairs);
 }
 
 template <typename TI, int MODE> cudaError_t backward(const ScanArgs& a, int pairs, cudaStream_t s) {
