@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(NT, PER_SM)
                 nBr = apply(Aw, Bw, nBr);
                 Ar = Aw.x < 0.f ? Aw : Ar.x < 0.f ? Ar : mul2(Ar, Aw);
             }
-            sIn[lane] = walk(g, order, tc, Ar, nBr);
+            walk_map(g, order, tc, Ar, nBr);
         } else if (tid == 32) {
             tk[stage] = next_tile(g);
         }
@@ -211,6 +211,8 @@ __global__ void __launch_bounds__(NT, PER_SM)
         };
         if (whole) forward(std::true_type{});
         else forward(std::false_type{});
+        // (the first warp's own states come before its look back: by then the value is mostly there)
+        if (warp == 0) sIn[lane] = walk_value(g, order, tc, Ar, nBr);
         __syncthreads();
         float2 carry = sIn[lane], sa = f2(0.f), sr = f2(0.f), si = f2(0.f);
         for (int u = WARPS - 1; u > warp; --u) carry = apply(sAr[u][lane], sBr[u][lane], carry);
@@ -262,7 +264,8 @@ __global__ void __launch_bounds__(NT, PER_SM)
 // every eighth tile.
 __global__ void __launch_bounds__(256) params_kernel(const __grid_constant__ ScanArgs g) {
     __shared__ float2 part[8][32];
-    const int c = blockIdx.x * 32 + threadIdx.x % 32, q = blockIdx.y, w = threadIdx.x / 32;
+    cudaGridDependencySynchronize();
+    const int c = blockIdx.x / 3 * 32 + threadIdx.x % 32, q = blockIdx.x % 3, w = threadIdx.x / 32;
     float* out = q == 0 ? g.dA_log : q == 1 ? g.dr_bias : g.di_bias;
     if (out == nullptr) return;
     float s = 0.f, err = 0.f;
@@ -331,8 +334,7 @@ cudaError_t launch_backward(const ScanArgs& a, int io_bf16, cudaStream_t s) {
                : mode == M4 ? backward<__nv_bfloat16, M4>(a, pairs, s) : backward<__nv_bfloat16, MODD>(a, pairs, s);
         if (e != cudaSuccess) return e;
     }
-    params_kernel<<<dim3((unsigned)((a.C + 31) / 32), 3), 256, 0, s>>>(a);
-    return cudaGetLastError();
+    return launch_behind(params_kernel, (int64_t)((a.C + 31) / 32) * 3, 256, 0, s, a);
 }
 
 }  // namespace glr

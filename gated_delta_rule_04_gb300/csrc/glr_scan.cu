@@ -89,7 +89,8 @@ __global__ void __launch_bounds__(ALL, PER_SM)
                 Bt = apply(A, B, Bt);
                 At = A.x < 0.f ? A : At.x < 0.f ? At : mul2(At, A);
             }
-            float2 h = walk(g, tile.x, tile.y, At, Bt);
+            walk_map(g, tile.x, tile.y, At, Bt);
+            float2 h = walk_value(g, tile.x, tile.y, At, Bt);
 #pragma unroll
             for (int w = 0; w < WARPS; ++w) {
                 sIn[buf][w][lane] = h;

@@ -223,15 +223,21 @@ __device__ __forceinline__ uint4 peek4(const float* p) {
     return v;
 }
 
-// By one whole warp.  order: the tile's place in the walk (0: the first).  Returns the value
-// that comes into the tile.
-__device__ __forceinline__ float2 walk(const ScanArgs& g, int order, int tile_c, float2 A, float2 B) {
-    const int lane = threadIdx.x & 31;
-    const size_t me = ((size_t)order * g.tiles_c + tile_c) * TILE_C + 2 * lane;
-    const size_t step = (size_t)g.tiles_c * TILE_C;
-    const bool anew = A.x < 0.f;                                // (in all channels: borders are the tokens')
-    if (anew) publish(g.val + me, B);
+// By one whole warp.  order: the tile's place in the walk (0: the first).
+__device__ __forceinline__ size_t walk_place(const ScanArgs& g, int order, int tile_c) {
+    return ((size_t)order * g.tiles_c + tile_c) * TILE_C + 2 * (threadIdx.x & 31);
+}
+// First: the tile's map, or (it begins anew, in all channels: borders are the tokens') its value.
+__device__ __forceinline__ void walk_map(const ScanArgs& g, int order, int tile_c, float2 A, float2 B) {
+    const size_t me = walk_place(g, order, tile_c);
+    if (A.x < 0.f) publish(g.val + me, B);
     else publish(g.map + 2 * me, A, B);
+}
+// Then: the value that comes into the tile, returned, and the one that leaves it.
+__device__ __forceinline__ float2 walk_value(const ScanArgs& g, int order, int tile_c, float2 A, float2 B) {
+    const int lane = threadIdx.x & 31;
+    const size_t me = walk_place(g, order, tile_c);
+    const size_t step = (size_t)g.tiles_c * TILE_C;
     float2 in = f2(0.f);
     if (order == 0) return in;
     bool done = false;
@@ -276,7 +282,7 @@ __device__ __forceinline__ float2 walk(const ScanArgs& g, int order, int tile_c,
             }
         }
     }
-    if (!anew) publish(g.val + me, make_float2(fmaf(A.x, in.x, B.x), fmaf(A.y, in.y, B.y)));
+    if (!(A.x < 0.f)) publish(g.val + me, make_float2(fmaf(A.x, in.x, B.x), fmaf(A.y, in.y, B.y)));
     return in;
 }
 
