@@ -69,13 +69,13 @@ Layout layout(const kda_glr_params* p, int32_t n_seqs, int64_t total_tokens, boo
     return L;
 }
 
-// What the two walks share: the sequences with tokens, and the workspace's parts, set up.
-// The walk clears the error word.
+// What the two walks share: the sequences with tokens, and the workspace's parts.
+// (The walks set the workspace up themselves.)
 cudaError_t prepare(const kda_glr_params* p, const int64_t* cu, int32_t n_seqs, unsigned char* ws, const Layout& L,
                     ScanArgs* a, cudaStream_t s) {
     a->status = reinterpret_cast<int32_t*>(ws);
-    a->ticket = reinterpret_cast<uint32_t*>(ws + L.ticket);
     a->gates = reinterpret_cast<float2*>(ws + L.gates);
+    a->ticket = reinterpret_cast<uint32_t*>(ws + L.ticket);
     a->map = reinterpret_cast<float*>(ws + L.map);
     a->val = reinterpret_cast<float*>(ws + L.val);
     a->part = reinterpret_cast<float*>(ws + L.part);
@@ -84,7 +84,7 @@ cudaError_t prepare(const kda_glr_params* p, const int64_t* cu, int32_t n_seqs, 
     if (L.tiles_t == 0) return cudaMemsetAsync(ws, 0, WS_ALIGN, s);
     Sequences& f = a->f;
     // one place along T waits for nothing: the ticket alone
-    const size_t empty = L.tiles_t > 1 ? L.val + sizeof(float) * TILE_C * (size_t)(L.tiles_t * L.tiles_c) - L.ticket : WS_ALIGN;
+    a->empty = (L.tiles_t > 1 ? L.val - L.ticket + sizeof(float) * TILE_C * (size_t)(L.tiles_t * L.tiles_c) : WS_ALIGN) / sizeof(uint4);
     f.d_cu = reinterpret_cast<int64_t*>(ws + L.cu);
     f.d_id = reinterpret_cast<int32_t*>(ws + L.id);
     f.d_tile = reinterpret_cast<int32_t*>(ws + L.tile);
@@ -98,7 +98,7 @@ cudaError_t prepare(const kda_glr_params* p, const int64_t* cu, int32_t n_seqs, 
                 f.id[k++] = i;
             }
         f.cu[k] = (int32_t)cu[n_seqs];
-        return launch_setup(*a, empty / sizeof(uint4), s);
+        return cudaSuccess;
     }
     std::vector<int64_t> start;
     std::vector<int32_t> id;
@@ -114,9 +114,8 @@ cudaError_t prepare(const kda_glr_params* p, const int64_t* cu, int32_t n_seqs, 
     } catch (const std::bad_alloc&) {
         return cudaErrorMemoryAllocation;
     }
-    const cudaError_t e = build_meta(start.data(), id.data(), f.n, 0, const_cast<int64_t*>(f.d_cu), nullptr, const_cast<int32_t*>(f.d_id),
+    return build_meta(start.data(), id.data(), f.n, 0, const_cast<int64_t*>(f.d_cu), nullptr, const_cast<int32_t*>(f.d_id),
                    nullptr, s);
-    return e != cudaSuccess ? e : launch_setup(*a, empty / sizeof(uint4), s);
 }
 
 // Copies the state of sequences without tokens, if there are any (all states: the walk then
@@ -174,7 +173,6 @@ kda_status kda_glr_prefill(const kda_glr_params* p, const void* x, int64_t x_str
     a.A_log = p->A_log; a.r_bias = p->r_bias; a.i_bias = p->i_bias;
     a.S_in = S_in; a.S_out = S_out; a.states = states; a.o = o; a.o_s = (uint32_t)p->channels * es;
     a.T = total_tokens; a.C = p->channels;
-    // (the setup is the last before the walk, which starts beside its end)
     if (copy_states(p, cu, n_seqs, S_in, S_out, s) != cudaSuccess || glr::prepare(p, cu, n_seqs, ws, L, &a, s) != cudaSuccess)
         return KDA_ERR_CUDA;
     if (!any) return KDA_OK;
@@ -200,16 +198,16 @@ kda_status kda_glr_backward(const kda_glr_params* p, const void* x, int64_t x_st
     if (!dA_log || !aligned(S_in, 4) || !aligned(states, 4) || !aligned(dS_out, 4) || !aligned(dS_in, 4) ||
         !aligned(dA_log, 4) || !aligned(dr_bias, 4) || !aligned(di_bias, 4))
         return KDA_ERR_INVALID_ARG;
-    if (n_seqs == 0) {                                // empty sums
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    auto empty_sums = [&]() {
         for (float* sum : {dA_log, dr_bias, di_bias})
-            if (sum && cudaMemsetAsync(sum, 0, sizeof(float) * p->channels, static_cast<cudaStream_t>(stream)) != cudaSuccess)
-                return KDA_ERR_CUDA;
+            if (sum && cudaMemsetAsync(sum, 0, sizeof(float) * p->channels, s) != cudaSuccess) return KDA_ERR_CUDA;
         return KDA_OK;
-    }
+    };
+    if (n_seqs == 0) return empty_sums();
     const Layout L = glr::layout(p, n_seqs, total_tokens, true);
     if (L.tiles_t * L.tiles_c > (int64_t)INT32_MAX / 2) return KDA_ERR_UNSUPPORTED;
     if (workspace == nullptr || !aligned(workspace, WS_ALIGN) || workspace_bytes < L.total) return KDA_ERR_WORKSPACE;
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
     unsigned char* ws = static_cast<unsigned char*>(workspace);
     glr::ScanArgs a{};
     a.x = x; a.r = r; a.i = i; a.z = z;
@@ -227,6 +225,7 @@ kda_status kda_glr_backward(const kda_glr_params* p, const void* x, int64_t x_st
     if ((dS_in && copy_states(p, cu, n_seqs, dS_out, dS_in, s) != cudaSuccess) ||
         glr::prepare(p, cu, n_seqs, ws, L, &a, s) != cudaSuccess)
         return KDA_ERR_CUDA;
+    if (!any) return empty_sums();
     return glr::launch_backward(a, p->io_dtype == KDA_DTYPE_BF16, s) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 

@@ -11,8 +11,7 @@
 // for nothing, while one warp walks along the tiles for the gradient a g that comes
 // in from the right.  What the gates give is computed once and held in
 // registers between the sweeps.  Sums over the tokens go to the workspace by tile
-// and are added up in order by a second kernel.
-#include <atomic>
+// and are added up in order when all tiles are done.
 #include <type_traits>
 
 #include "glr_tile.cuh"
@@ -23,11 +22,48 @@ namespace {
 
 enum { OUT_X = 1, OUT_R = 2, OUT_I = 4, OUT_Z = 8 };   // gradients whose rows take pairs
 
+// The parameters' gradients: the tiles' sums, added up in order with the error of each
+// addition kept (Knuth's two-sum).  A CTA takes 32 channels of one gradient, its 8 warps every
+// eighth tile.
+__device__ __forceinline__ void add_up(const ScanArgs& g, float2 (&part)[WARPS][32]) {
+    const int w = threadIdx.x / 32, lane = threadIdx.x % 32, units = (g.C + 31) / 32 * 3;
+    for (int unit = blockIdx.x; unit < units; unit += gridDim.x) {
+        const int c = unit / 3 * 32 + lane, q = unit % 3;
+        float* out = q == 0 ? g.dA_log : q == 1 ? g.dr_bias : g.di_bias;
+        if (out == nullptr) continue;
+        float s = 0.f, err = 0.f;
+        auto add = [&](float x) {
+            const float n = __fadd_rn(s, x), b = __fsub_rn(n, s);
+            err += __fadd_rn(__fsub_rn(s, __fsub_rn(n, b)), __fsub_rn(x, b));
+            s = n;
+        };
+        if (c < g.C) {
+#pragma unroll 16
+            for (int tt = w; tt < g.tiles_t; tt += WARPS) add(__ldcg(g.part + ((size_t)tt * 3 + q) * g.C + c));
+        }
+        part[w][lane] = make_float2(s, err);
+        __syncthreads();
+        if (w == 0 && c < g.C) {
+            for (int u = 1; u < WARPS; ++u) {
+                add(part[u][lane].x);
+                err += part[u][lane].y;
+            }
+            out[c] = s + err;
+        }
+        __syncthreads();
+    }
+}
+
+__global__ void __launch_bounds__(NT) add_up_kernel(const __grid_constant__ ScanArgs g) {
+    __shared__ float2 part[WARPS][32];
+    add_up(g, part);
+}
+
 template <typename TI, int MODE, bool GATED, int STAGES, int PER_SM>
 __global__ void __launch_bounds__(NT, PER_SM)
     backward_kernel(const __grid_constant__ ScanArgs g, const __grid_constant__ Maps maps, int pairs) {
     using R = Rows<TI, MODE>;
-    constexpr int TENSORS = GATED ? 5 : 4, GATES = 3 * TILE_C * 4, STAGE_BYTES = TENSORS * R::TILE;
+    constexpr int TENSORS = GATED ? 5 : 4, STAGE_BYTES = TENSORS * R::TILE;
     extern __shared__ __align__(128) unsigned char rows_smem[];    // [STAGES][x, r, i, do, z][CHUNK]
     __shared__ int2 tk[STAGES];
     __shared__ __align__(16) float2 sG[STAGES][3][32];             // the tiles' gate constants
@@ -38,18 +74,18 @@ __global__ void __launch_bounds__(NT, PER_SM)
     unsigned char* const mine = rows_smem + warp * R::BYTES;
     const uint32_t bars = ptx::smem_u32(landed);
     uint32_t phases = 0;
-    // (MTMA) The tile's rows and constants, by one thread.
+    // (MTMA) The tile's rows and gate constants, by one thread.
     auto load_tile = [&](int stage) {
         const int2 tile = tk[stage];
         if (tile.x < 0) return;
         const uint32_t s = ptx::smem_u32(rows_smem) + stage * STAGE_BYTES, bar = bars + 8 * stage;
-        ptx::mbar_expect_tx(bar, STAGE_BYTES + GATES);
+        ptx::mbar_expect_tx(bar, STAGE_BYTES + sizeof sG[0]);
 #pragma unroll
         for (int m = 0; m < TENSORS; ++m)
             ptx::tma_load_2d(s + m * R::TILE, &maps.m[m], tile.y * TILE_C, (g.tiles_t - 1 - tile.x) * CHUNK, bar);
-        ptx::bulk_g2s(ptx::smem_u32(&sG[stage][0][0]), g.gates + (size_t)tile.y * (GATES / 8), GATES, bar);
+        ptx::bulk_g2s(ptx::smem_u32(&sG[stage][0][0]), g.gates + (size_t)tile.y * (3 * TILE_C / 2), sizeof sG[0], bar);
     };
-    // Each warp: its own rows (not MTMA); the last warp: the tile's first state, and (not MTMA) the constants.
+    // Each warp: its own rows (not MTMA); the last warp: the tile's first state.
     auto issue = [&](int stage) {
         const int2 tile = tk[stage];
         if (tile.x >= 0) {
@@ -77,13 +113,14 @@ __global__ void __launch_bounds__(NT, PER_SM)
         for (int k = 0; k < STAGES; ++k) ptx::mbar_init(bars + 8 * k, 1);
         ptx::fence_mbar_init();
     }
-    cudaGridDependencySynchronize();
+    begin(g);
     if (tid == 0)
-        for (int k = 0; k < STAGES; ++k) tk[k] = next_tile(g);
+        for (int k = 0; k < STAGES; ++k) tk[k] = place_of(g, take_ticket(g));
     __syncthreads();
-    if (MODE == MTMA && tid == NT - 1)
+    if (MODE == MTMA && tid == NT - 1) {
+        asm volatile("fence.proxy.async;" ::: "memory");           // (the constants were written by ordinary stores)
         for (int k = 0; k < STAGES; ++k) load_tile(k);
-    if (tk[0].x == 0 && tk[0].y == 0 && tid == 0) *g.status = ERR_NONE;
+    }
     for (int k = 0; k < STAGES; ++k) issue(k);
 
     for (int stage = 0;; stage = stage + 1 == STAGES ? 0 : stage + 1) {
@@ -92,15 +129,13 @@ __global__ void __launch_bounds__(NT, PER_SM)
         const int t = tt * CHUNK + warp * SUB, c0 = tc * TILE_C, c = c0 + 2 * lane, rows = (int)g.T - t, left = g.C - c;
         const Borders bd = borders(g, tt, t);
         auto seq_of = [&](int j) { return (size_t)seq_id(g.f, bd.seq + __popc((bd.start >> 1) & ((1u << j) - 1))); };
-        Gate k;
-        if (MODE != MTMA) k = load_gate(g, tc);
         asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
         __syncwarp();
         if (MODE == MTMA) {
             wait_or(g, bars + 8 * stage, phases >> stage & 1);
             phases ^= 1u << stage;
-            k = Gate{sG[stage][0][lane], sG[stage][1][lane], sG[stage][2][lane]};
         }
+        const Gate k = MODE == MTMA ? Gate{sG[stage][0][lane], sG[stage][1][lane], sG[stage][2][lane]} : load_gate(g, tc);
 
         unsigned char* const s = mine + stage * STAGE_BYTES;
         const typename R::Odd ox = R::odd(g.x, g.x_s, t, c0), orr = R::odd(g.r, g.r_s, t, c0), oi = R::odd(g.i, g.i_s, t, c0),
@@ -190,7 +225,7 @@ __global__ void __launch_bounds__(NT, PER_SM)
             }
             walk_map(g, order, tc, Ar, nBr);
         } else if (tid == 32) {
-            tk[stage] = next_tile(g);
+            tk[stage] = place_of(g, take_ticket(g));
         }
         for (int u = 0; u < warp; ++u) nh = apply(sA[u][lane], sB[u][lane], nh);
         const bool full = pairs == (GATED ? OUT_X | OUT_R | OUT_I | OUT_Z : OUT_X | OUT_R | OUT_I) && c0 + TILE_C <= g.C;
@@ -257,35 +292,9 @@ __global__ void __launch_bounds__(NT, PER_SM)
             put(g.part + ((size_t)tt * 3 + q) * g.C + c, left, false, sum);
         }
     }
-}
-
-// The parameters' gradients: the tiles' sums, added up in order with the error of each
-// addition kept (Knuth's two-sum).  A block takes 32 channels of one gradient, its 8 warps
-// every eighth tile.
-__global__ void __launch_bounds__(256) params_kernel(const __grid_constant__ ScanArgs g) {
-    __shared__ float2 part[8][32];
-    cudaGridDependencySynchronize();
-    const int c = blockIdx.x / 3 * 32 + threadIdx.x % 32, q = blockIdx.x % 3, w = threadIdx.x / 32;
-    float* out = q == 0 ? g.dA_log : q == 1 ? g.dr_bias : g.di_bias;
-    if (out == nullptr) return;
-    float s = 0.f, err = 0.f;
-    auto add = [&](float x) {
-        const float n = __fadd_rn(s, x), b = __fsub_rn(n, s);
-        err += __fadd_rn(__fsub_rn(s, __fsub_rn(n, b)), __fsub_rn(x, b));
-        s = n;
-    };
-    if (c < g.C) {
-#pragma unroll 8
-        for (int tt = w; tt < g.tiles_t; tt += 8) add(g.part[((size_t)tt * 3 + q) * g.C + c]);
-    }
-    part[w][threadIdx.x % 32] = make_float2(s, err);
-    __syncthreads();
-    if (w == 0 && c < g.C) {
-        for (int u = 1; u < 8; ++u) {
-            add(part[u][threadIdx.x].x);
-            err += part[u][threadIdx.x].y;
-        }
-        out[c] = s + err;
+    if (g.alone) {
+        cooperative_groups::this_grid().sync();
+        add_up(g, sums[0]);
     }
 }
 
@@ -302,17 +311,12 @@ cudaError_t backward(const ScanArgs& a, int pairs, cudaStream_t s) {
     constexpr int STAGES = sizeof(TI) == 2 ? 2 : 1, PER_SM = 2;
     auto k = backward_kernel<TI, MODE, GATED, STAGES, PER_SM>;
     constexpr int SMEM = STAGES * (GATED ? 5 : 4) * Rows<TI, MODE>::TILE;
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    static std::atomic<uint64_t> done{0};            // (set once per device)
-    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
-    if (!(done.load() & bit)) {
-        e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
-        if (e != cudaSuccess) return e;
-        done.fetch_or(bit);
-    }
-    return launch_behind(k, std::min<int64_t>((int64_t)a.tiles_t * a.tiles_c, SMS * PER_SM), NT, SMEM, s, a, maps, pairs);
+    static std::atomic<int> most[64];
+    bool alone;
+    const cudaError_t e = launch_walk(k, most, a, NT, SMEM, s, &alone, maps, pairs);
+    if (e != cudaSuccess || alone) return e;
+    add_up_kernel<<<(unsigned)((a.C + 31) / 32 * 3), NT, 0, s>>>(a);
+    return cudaGetLastError();
 }
 
 template <typename TI, int MODE> cudaError_t backward(const ScanArgs& a, int pairs, cudaStream_t s) {
@@ -323,18 +327,13 @@ template <typename TI, int MODE> cudaError_t backward(const ScanArgs& a, int pai
 
 cudaError_t launch_backward(const ScanArgs& a, int io_bf16, cudaStream_t s) {
     const int es = io_bf16 ? 2 : 4;
-    cudaError_t e = cudaSuccess;
-    if (a.tiles_t > 0) {
-        const int mode = std::max({row_mode(a.x, a.x_s, a.C), row_mode(a.r, a.r_s, a.C), row_mode(a.i, a.i_s, a.C),
-                                   row_mode(a.d_o, a.do_s, a.C), a.z ? row_mode(a.z, a.z_s, a.C) : 0});
-        const int pairs = (row_pairs(a.dx, a.dx_s, es) ? OUT_X : 0) | (row_pairs(a.dr, a.dr_s, es) ? OUT_R : 0) |
-                          (row_pairs(a.di, a.di_s, es) ? OUT_I : 0) | (a.z && row_pairs(a.dz, a.dz_s, es) ? OUT_Z : 0);
-        if (!io_bf16) e = mode == MTMA ? backward<float, MTMA>(a, pairs, s) : backward<float, M4>(a, pairs, s);
-        else e = mode == MTMA ? backward<__nv_bfloat16, MTMA>(a, pairs, s)
-               : mode == M4 ? backward<__nv_bfloat16, M4>(a, pairs, s) : backward<__nv_bfloat16, MODD>(a, pairs, s);
-        if (e != cudaSuccess) return e;
-    }
-    return launch_behind(params_kernel, (int64_t)((a.C + 31) / 32) * 3, 256, 0, s, a);
+    const int mode = std::max({row_mode(a.x, a.x_s, a.C), row_mode(a.r, a.r_s, a.C), row_mode(a.i, a.i_s, a.C),
+                               row_mode(a.d_o, a.do_s, a.C), a.z ? row_mode(a.z, a.z_s, a.C) : 0});
+    const int pairs = (row_pairs(a.dx, a.dx_s, es) ? OUT_X : 0) | (row_pairs(a.dr, a.dr_s, es) ? OUT_R : 0) |
+                      (row_pairs(a.di, a.di_s, es) ? OUT_I : 0) | (a.z && row_pairs(a.dz, a.dz_s, es) ? OUT_Z : 0);
+    if (!io_bf16) return mode == MTMA ? backward<float, MTMA>(a, pairs, s) : backward<float, M4>(a, pairs, s);
+    return mode == MTMA ? backward<__nv_bfloat16, MTMA>(a, pairs, s)
+         : mode == M4 ? backward<__nv_bfloat16, M4>(a, pairs, s) : backward<__nv_bfloat16, MODD>(a, pairs, s);
 }
 
 }  // namespace glr

@@ -44,10 +44,12 @@ struct ScanArgs {
     Sequences f;
     // workspace
     int32_t* status;                 // error word
-    uint32_t* ticket;                // the next tile to be taken
     float2* gates;                   // [tiles along C][3][TILE_C / 2]: see load_gate
+    uint32_t* ticket;                // the next tile to be taken, and behind it
     float* map;                      // [tiles along T][tiles along C][TILE_C][2]
     float* val;                      // [tiles along T][tiles along C][TILE_C]
+    size_t empty;                    // 16-byte words, from the ticket on, that are set to EMPTY first
+    int32_t alone;                   // the walk's kernel sets up and adds up by itself
     float* part;                     // [tiles along T][3][C]: partial sums of the parameters' gradients
     int32_t tiles_t, tiles_c;
 };
@@ -67,10 +69,6 @@ struct TokenArgs {
 cudaError_t launch_scan(const ScanArgs& a, int io_bf16, cudaStream_t s);
 cudaError_t launch_backward(const ScanArgs& a, int io_bf16, cudaStream_t s);
 cudaError_t launch_tokens(const TokenArgs& a, int io_bf16, cudaStream_t s);
-
-// What a walk finds in its workspace: ticket, maps and values set to EMPTY (`empty` words from the
-// ticket on), the gates' table, and for many sequences that of the tiles' first ones.
-cudaError_t launch_setup(const ScanArgs& a, size_t empty, cudaStream_t s);
 
 }  // namespace glr
 }  // namespace kda

@@ -9,7 +9,6 @@
 // sweep over the 8 tokens is one multiply-add a token and the output gate.
 // Sequences lie anywhere in the tiles: a token that begins one starts its run
 // anew from S_in.
-#include <atomic>
 #include <type_traits>
 
 #include "glr_tile.cuh"
@@ -54,7 +53,7 @@ __global__ void __launch_bounds__(ALL, PER_SM)
         for (int k = 0; k < STAGES; ++k) ptx::mbar_init(bars + 8 * k, 1);
         ptx::fence_mbar_init();
     }
-    cudaGridDependencySynchronize();
+    begin(g);
     if (tid == 0)
         for (int k = 0; k < STAGES; ++k) tk[k] = place_of(g, take_ticket(g));
     __syncthreads();
@@ -67,12 +66,11 @@ __global__ void __launch_bounds__(ALL, PER_SM)
         for (int m = 0; m < TENSORS; ++m) ptx::tma_load_2d(s + m * R::TILE, &maps.m[m], tile.y * TILE_C, tile.x * CHUNK, bar);
     };
 
-    // The walks, even tiles' by one warp and odd ones' by the other (one warp for all, which also fetched the
-    // tickets, was what the others waited for: 151 us at 16384 tokens x 4096): maps of the
-    // tile's warps in, their first values out.
+    // The walks, even tiles' by one warp and odd ones' by the other (one warp for all was what the others
+    // waited for: 151 us for 145 at 16384 tokens x 4096): maps of the tile's warps in, their first
+    // values out.
     if (warp >= WARPS) {
         const int buf = warp - WARPS;
-        if (tk[0].x == 0 && tk[0].y == 0 && tid == NT) *g.status = ERR_NONE;
         if (MODE == MTMA && tid == NT)
             for (int k = 0; k < STAGES; ++k) load_tile(k, k);
         place_gates(buf, load_gate(g, tk[buf].y));
@@ -255,54 +253,20 @@ cudaError_t scan(const ScanArgs& a, bool pairs, cudaStream_t s) {
     constexpr int PER_SM = sizeof(TI) == 2 ? 2 : 1;
     auto k = scan_kernel<TI, MODE, GATED, PER_SM>;
     constexpr int SMEM = 3 * (GATED ? 4 : 3) * Rows<TI, MODE>::TILE;
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    static std::atomic<uint64_t> done{0};            // (set once per device)
-    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
-    if (!(done.load() & bit)) {
-        e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
-        if (e != cudaSuccess) return e;
-        done.fetch_or(bit);
-    }
-    return launch_behind(k, std::min<int64_t>((int64_t)a.tiles_t * a.tiles_c, SMS * PER_SM), ALL, SMEM, s, a, maps, pairs);
+    static std::atomic<int> most[64];
+    bool alone;
+    return launch_walk(k, most, a, ALL, SMEM, s, &alone, maps, pairs);
 }
 
 template <typename TI, int MODE> cudaError_t scan(const ScanArgs& a, bool pairs, cudaStream_t s) {
     return a.z ? scan<TI, MODE, true>(a, pairs, s) : scan<TI, MODE, false>(a, pairs, s);
 }
 
-// Many threads fill; the first ones also make the tables.
-__global__ void __launch_bounds__(NT) setup_kernel(const __grid_constant__ ScanArgs g, size_t empty) {
-    cudaTriggerProgrammaticLaunchCompletion();
-    const size_t id = (size_t)blockIdx.x * NT + threadIdx.x, all = (size_t)gridDim.x * NT;
-    uint4* w = reinterpret_cast<uint4*>(g.ticket);
-    for (size_t k = id; k < empty; k += all) w[k] = make_uint4(EMPTY, EMPTY, EMPTY, EMPTY);
-    for (size_t k = id; k < (size_t)g.tiles_c * (TILE_C / 2); k += all) {
-        const Gate q = make_gate(g, (int)k * 2);
-        float2* p = g.gates + k / (TILE_C / 2) * (3 * TILE_C / 2) + k % (TILE_C / 2);
-        p[0] = q.ea;
-        p[TILE_C / 2] = q.rb;
-        p[TILE_C] = q.ib;
-    }
-    if (g.f.n <= INLINE_SEQS) return;
-    // the first sequence of each tile along T: the last one that begins at or before its first token
-    for (size_t tt = id; tt < (size_t)g.tiles_t; tt += all) {
-        int lo = 0, hi = g.f.n - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (g.f.d_cu[mid] <= (int64_t)tt * CHUNK) lo = mid; else hi = mid - 1;
-        }
-        const_cast<int32_t*>(g.f.d_tile)[tt] = lo;
-    }
-}
-
 }  // namespace
 
-cudaError_t launch_setup(const ScanArgs& a, size_t empty, cudaStream_t s) {
-    const size_t most = std::max({empty, (size_t)a.tiles_c * (TILE_C / 2), (size_t)a.tiles_t});
-    setup_kernel<<<(unsigned)std::min<size_t>((most + NT - 1) / NT, SMS * 8), NT, 0, s>>>(a, empty);
-    return cudaGetLastError();
+__global__ void __launch_bounds__(256) setup_kernel(const __grid_constant__ ScanArgs g) {
+    cudaTriggerProgrammaticLaunchCompletion();
+    set_up(g);
 }
 
 cudaError_t launch_scan(const ScanArgs& a, int io_bf16, cudaStream_t s) {

@@ -3,7 +3,10 @@
 // borders inside a tile, and the walk along the tiles.
 #pragma once
 
+#include <cooperative_groups.h>
+
 #include <algorithm>
+#include <atomic>
 
 #include "glr_math.cuh"
 #include "ssm_common.cuh"
@@ -23,7 +26,7 @@ static_assert(TILE_C == 64 && SUB == 8, "lanes hold channel pairs, warps 8 token
 // the word that holds the row's first element.
 enum Mode { MTMA = 0, M4 = 1, MODD = 2 };
 constexpr int MAX_TENSORS = 5;
-struct alignas(64) Maps {            // of the tensors, in boxes of a tile; zero fill out of bounds
+struct alignas(128) Maps {           // of the tensors, in boxes of a tile; zero fill out of bounds
     CUtensorMap m[MAX_TENSORS];
 };
 
@@ -141,12 +144,6 @@ __device__ __forceinline__ float2 pair_at(const float* p, size_t row, int c, int
     return h;
 }
 
-// The lane's gate constants of tile column tc, as the setup left them.
-__device__ __forceinline__ Gate load_gate(const ScanArgs& g, int tc) {
-    const float2* p = g.gates + (size_t)tc * (3 * TILE_C / 2) + (threadIdx.x & 31);
-    return Gate{p[0], p[TILE_C / 2], p[TILE_C]};
-}
-
 // ---- sequence borders -------------------------------------------------------------------
 // Of the warp's 8 tokens from t on: which begin a sequence, which end one, and the sequence
 // of the first (each start adds one).  Warp-uniform.
@@ -189,12 +186,11 @@ __device__ __forceinline__ Borders borders(const ScanArgs& g, int tile_t, int t)
 
 // ---- the walk along the tiles -------------------------------------------------------------
 // Tiles are taken in the order of a ticket, all of one place along T before the next, so a
-// tile's predecessors have been taken, by CTAs that are running, and every wait ends.  A
-// tile publishes its map h -> A h + B, then looks back for the nearest of 3
+// tile's predecessors have been taken, by CTAs that are running, and every wait ends.  A tile publishes its map h -> A h + B, then looks back for the nearest of 3
 // predecessors whose outgoing value is known, and applies the maps in between in their order:
 // the same operations in any timing, so results do not depend on it.
 // Maps and values are their own flags: the words are set to EMPTY, a NaN that is never
-// published, before the call, and a reader takes each as soon as it is another one, so no
+// published, before the first tile, and a reader takes each as soon as it is another one, so no
 // fence stands between a tile and the next.  (With flags beside them, two fences and one
 // more read: 5 us more a tile.)
 constexpr uint64_t WAIT_NS = 2000000000ull;
@@ -286,15 +282,54 @@ __device__ __forceinline__ float2 walk_value(const ScanArgs& g, int order, int t
     return in;
 }
 
-// The next ticket (the counter starts at EMPTY, like everything else that is set before a call), and a ticket's
-// tile: its place in the walk and its column, -1 behind the last.
+// The next tile: its place in the walk and its column, -1 behind the last (the counter starts at EMPTY, like
+// everything else that is set before the first tile).
 __device__ __forceinline__ uint32_t take_ticket(const ScanArgs& g) { return atomicAdd(g.ticket, 1u); }
 __device__ __forceinline__ int2 place_of(const ScanArgs& g, uint32_t ticket) {
     const uint32_t k = ticket + 1u;
     if (k >= (uint32_t)g.tiles_t * (uint32_t)g.tiles_c) return make_int2(-1, 0);
     return make_int2((int)(k / (uint32_t)g.tiles_c), (int)(k % (uint32_t)g.tiles_c));
 }
-__device__ __forceinline__ int2 next_tile(const ScanArgs& g) { return place_of(g, take_ticket(g)); }
+
+// What a walk finds in its workspace: a cleared error word, ticket, maps and values EMPTY, the gates' table, and
+// for many sequences that of the tiles' first ones.  By all threads of the grid.
+__device__ __forceinline__ void set_up(const ScanArgs& g) {
+    const size_t id = (size_t)blockIdx.x * blockDim.x + threadIdx.x, all = (size_t)gridDim.x * blockDim.x;
+    if (id == 0) *g.status = ERR_NONE;
+    uint4* w = reinterpret_cast<uint4*>(g.ticket);
+    for (size_t k = id; k < g.empty; k += all) w[k] = make_uint4(EMPTY, EMPTY, EMPTY, EMPTY);
+    for (size_t k = id; k < (size_t)g.tiles_c * (TILE_C / 2); k += all) {
+        const Gate q = make_gate(g, (int)k * 2);
+        float2* p = g.gates + k / (TILE_C / 2) * (3 * TILE_C / 2) + k % (TILE_C / 2);
+        p[0] = q.ea;
+        p[TILE_C / 2] = q.rb;
+        p[TILE_C] = q.ib;
+    }
+    if (g.f.n <= INLINE_SEQS) return;
+    // the first sequence of each tile along T: the last one that begins at or before its first token
+    for (size_t tt = id; tt < (size_t)g.tiles_t; tt += all) {
+        int lo = 0, hi = g.f.n - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (g.f.d_cu[mid] <= (int64_t)tt * CHUNK) lo = mid; else hi = mid - 1;
+        }
+        const_cast<int32_t*>(g.f.d_tile)[tt] = lo;
+    }
+}
+// At the start of a walk: it sets up by itself, or a kernel before it has.
+__device__ __forceinline__ void begin(const ScanArgs& g) {
+    if (g.alone) {
+        set_up(g);
+        cooperative_groups::this_grid().sync();
+    } else {
+        cudaGridDependencySynchronize();
+    }
+}
+// The lane's gate constants of tile column tc, from the table.
+__device__ __forceinline__ Gate load_gate(const ScanArgs& g, int tc) {
+    const float2* p = g.gates + (size_t)tc * (3 * TILE_C / 2) + (threadIdx.x & 31);
+    return Gate{p[0], p[TILE_C / 2], p[TILE_C]};
+}
 
 // Waits for a phase of a barrier of this CTA; past a limit of turns (each waits a while itself) the error word
 // is set.
@@ -308,20 +343,53 @@ __device__ __forceinline__ void wait_or(const ScanArgs& g, uint32_t bar, uint32_
 __device__ __forceinline__ void bar_arrive(int id, int threads) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
 __device__ __forceinline__ void bar_sync(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
 
-// Launches a kernel that starts beside the end of the one before it in the stream.
-template <typename... Params, typename... Args>
-cudaError_t launch_behind(void (*k)(Params...), int64_t grid, int threads, size_t smem, cudaStream_t s, Args... args) {
+// Launches a walk with a CTA for each of its tiles, but no more than run at once.  Up to four such rounds
+// the kernel does everything (as a cooperative launch, whose CTAs may wait for all others): a
+// launch more takes the host 6 us, and the GPU is done sooner (601 tokens x 512: 22 us a call
+// for 24, backward 777 x 321: 45 for 53).  Otherwise `before` is a kernel of its own
+// that sets up, and the walk starts beside its end: many CTAs that wait for all others, and
+// few that add up, cost the GPU more (backward 32768 x 4096: 600 us for 543).
+__global__ void __launch_bounds__(256) setup_kernel(const __grid_constant__ ScanArgs g);
+template <typename... Rest>
+cudaError_t launch_walk(void (*k)(ScanArgs, Rest...), std::atomic<int> (&most)[64], ScanArgs a, int threads, size_t smem,
+                        cudaStream_t s, bool* alone, Rest... rest) {
+    int dev = 0, blocks = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) blocks = most[dev].load();
+    if (blocks == 0) {                               // (once per kernel and device)
+        int sms = 0, per = 0;
+        e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+        if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, k, threads, smem);
+        if (e != cudaSuccess) return e;
+        blocks = sms * per;
+        if (blocks < 1) return cudaErrorLaunchOutOfResources;
+        if (dev < 64) most[dev].store(blocks);
+    }
+    const int64_t tiles = (int64_t)a.tiles_t * a.tiles_c;
+    a.alone = *alone = tiles <= 4 * (int64_t)blocks;
+    if (!a.alone) {
+        const size_t work = std::max({a.empty, (size_t)a.tiles_c * (TILE_C / 2), (size_t)a.tiles_t});
+        setup_kernel<<<(unsigned)std::min<size_t>((work + 255) / 256, SMS * 8), 256, 0, s>>>(a);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)grid);
+    cfg.gridDim = dim3((unsigned)std::min<int64_t>(tiles, blocks));
     cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
+    if (a.alone) {
+        at.id = cudaLaunchAttributeCooperative;
+        at.val.cooperative = 1;
+    } else {
+        at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at.val.programmaticStreamSerializationAllowed = 1;
+    }
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k, args...);
+    return cudaLaunchKernelEx(&cfg, k, a, rest...);
 }
 
 }  // namespace glr
