@@ -416,3 +416,123 @@ def test_commit_is_decode_of_the_path():
     path = torch.arange(R, dtype=torch.int32, device=DEV).expand(n, R).contiguous()
     kda.kda_glr_commit(params(i, "bf16"), *rows, path, torch.full((n,), R, dtype=torch.int32, device=DEV), S2)
     assert torch.equal(S, S2)
+
+
+# ---- batches of many tiles: set up by a kernel of their own, tickets over several rounds ----
+
+def forward64(i, cu):
+    """As glr_ref.mixer on the GPU: (o, S, state before each token), sequences side by side."""
+    j = {k: v.to(DEV) if torch.is_tensor(v) else v for k, v in i.items()}
+    s = steps(j)
+    n, T, C = len(cu) - 1, cu[-1], i["C"]
+    order = sorted(range(n), key=lambda k: cu[k] - cu[k + 1])
+    S = torch.zeros(n, C, dtype=torch.float64, device=DEV) if j["S"] is None else j["S"].double()[order].clone()
+    start, h, before = torch.tensor([cu[k] for k in order], device=DEV), *(torch.empty(T, C, dtype=torch.float64, device=DEV) for _ in range(2))
+    for t in range(max(cu[k + 1] - cu[k] for k in range(n))):
+        m = sum(cu[k + 1] - cu[k] > t for k in order)
+        at = start[:m] + t
+        before[at] = S[:m]
+        S[:m] = s["a"][at] * S[:m] + s["b"][at]
+        h[at] = S[:m]
+    o = h if j["z"] is None else h * j["z"].double() * torch.sigmoid(j["z"].double())
+    return s, j, o, S[torch.argsort(torch.tensor(order, device=DEV))], before, h
+
+
+def gradients64(i, cu):
+    s, j, _, _, before, h = forward64(i, cu)
+    n, T, C = len(cu) - 1, cu[-1], i["C"]
+    z = j["z"].double()
+    e = torch.sigmoid(z)
+    G = j["do"].double()
+    out = {"dz": G * h * (e + z * e * torch.sigmoid(-z))}
+    G = G * z * e
+    carry = j["dS"].double().clone()
+    for k in range(n):
+        for t in range(cu[k + 1] - 1, cu[k] - 1, -1):
+            G[t] += carry[k]
+            carry[k] = s["a"][t] * G[t]
+    dA = G * (s["a"] * before * s["la"] - s["a"] ** 2 * s["v"] * j["x"].double() * s["la"] / s["m"])
+    out.update(dx=G * s["m"] * s["v"], di=G * s["b"] * s["v_"], dr=dA * s["w_"], dS_in=carry)
+    out.update(dA_log=dA.sum(0), dr_bias=out["dr"].sum(0), di_bias=out["di"].sum(0))
+    return out
+
+
+@pytest.mark.parametrize("io, T, C, pad", [("bf16", 9000, 1024, 0), ("bf16", 20500, 300, 0), ("bf16", 9000, 1023, 1),
+                                           ("bf16", 9000, 1000, 2), ("f32", 6000, 512, 0), ("f32", 6000, 519, 1)])
+def test_many_tiles(io, T, C, pad):
+    """Every way of copying rows (tensor copies, 4 bytes at a time, odd rows: `pad` widens the rows), over
+    several rounds of tiles, with sequence borders in some of them."""
+    cu = [0, 1, 77, 77, 4000, T - 13, T]
+    i = make_inputs(T, len(cu) - 1, C, IO[io], 40 + C)
+    i["A_log"] -= 0.7
+    wide = {k: torch.empty(T, C + pad, dtype=IO[io], device=DEV)[:, :C].copy_(i[k]) for k in ("x", "r", "i", "z", "do")}
+    p, S = params(i, io), dev(i["S"])
+    st = torch.empty(-(-T // kda.KDA_GLR_CHUNK), C, device=DEV)
+    ws = torch.full((kda.kda_glr_backward_workspace_bytes(p, len(cu) - 1, T),), 255, dtype=torch.uint8, device=DEV)
+    _, _, wo, wS, before, _ = forward64(i, cu)
+    runs = []
+    for fill in (255, 0):                       # whatever the workspace holds
+        ws.fill_(fill)
+        o, So = kda.kda_glr_prefill(p, wide["x"], wide["r"], wide["i"], cu, z=wide["z"], S_in=S, states=st, workspace=ws)
+        ws.fill_(fill)
+        g = kda.kda_glr_backward(p, wide["x"], wide["r"], wide["i"], cu, st, wide["do"], z=wide["z"], S_in=S, dS_out=dev(i["dS"]),
+                                 workspace=ws)
+        assert kda.kda_workspace_status(ws) == kda.KDA_OK
+        runs.append([o, So, st.clone()] + [getattr(g, k) for k in GRADS])
+    for a, b in zip(*runs):
+        assert torch.equal(a, b)
+    close("o", o, wo.cpu())
+    close("S", So, wS.cpu())
+    close("states", st, before[::kda.KDA_GLR_CHUNK].cpu())
+    want = gradients64(i, cu)
+    for k in GRADS:   # sums of T terms: (T / 700)^1/2 times the usual tolerance of a sum
+        close(k, getattr(g, k), want[k].cpu(), SUM_TOL * (T / 700) ** 0.5 if k in ("dA_log", "dr_bias", "di_bias") else None)
+
+
+def test_two_large_calls_at_once():
+    """Two walks of several rounds and a cooperative one beside them, each on its stream."""
+    T, C = 6000, 2048
+    i = make_inputs(T, 2, C, torch.bfloat16, 50)
+    cu = [0, 2500, T]
+    p = params(i, "bf16")
+    x, r, s, z, S, do, dS = (dev(i[k]) for k in ("x", "r", "i", "z", "S", "do", "dS"))
+    small = [t[:300].contiguous() for t in (x, r, s, z)]
+    st = torch.empty(-(-T // 64), C, device=DEV)
+    want = kda.kda_glr_prefill(p, x, r, s, cu, z=z, S_in=S, states=st)
+    gw = kda.kda_glr_backward(p, x, r, s, cu, st, do, z=z, S_in=S, dS_out=dS)
+    sw = kda.kda_glr_prefill(p, *small[:3], [0, 300], z=small[3])
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(3):
+        outs.append((kda.kda_glr_prefill(p, x, r, s, cu, z=z, S_in=S, stream=streams[0]),
+                     kda.kda_glr_backward(p, x, r, s, cu, st, do, z=z, S_in=S, dS_out=dS, stream=streams[1]),
+                     kda.kda_glr_prefill(p, *small[:3], [0, 300], z=small[3], stream=streams[2])))
+    torch.cuda.synchronize()
+    for a, g, b in outs:
+        assert torch.equal(a[0], want[0]) and torch.equal(a[1], want[1]) and torch.equal(b[0], sw[0]) and torch.equal(b[1], sw[1])
+        for k in GRADS:
+            assert torch.equal(getattr(g, k), getattr(gw, k))
+
+
+def test_rows_past_32_bits_of_elements():
+    """Row offsets past 2^31 elements and 2^32 bytes: the last of 600000 tokens whose rows lie 4100 elements apart."""
+    T, C, stride = 600000, 64, 4100
+    base = torch.zeros(T * stride, dtype=torch.bfloat16, device=DEV).view(T, stride)
+    i = make_inputs(2000, 1, C, torch.bfloat16, 51, state=False)
+    parts = {k: base[:, j * 64:(j + 1) * 64] for j, k in enumerate(("x", "r", "i", "z", "do"))}
+    for k, t in parts.items():
+        t[-2000:] = dev(i[k])
+        if k == "r":
+            t[-2001] = float("inf")            # a token whose decay is e^-1 or less, and whose input is zero, like all before
+    p = params(i, "bf16")
+    st = torch.empty(-(-T // 64), C, device=DEV)
+    o, S = kda.kda_glr_prefill(p, parts["x"], parts["r"], parts["i"], [0, T], z=parts["z"], states=st)
+    wo, wS = mixer(i, [0, 2000])
+    close("o", o[-2000:], wo)
+    close("S", S, wS)
+    assert not o[:-2000].any()
+    g = kda.kda_glr_backward(p, parts["x"], parts["r"], parts["i"], [0, T], st, parts["do"], z=parts["z"])
+    want = gradients(i, [0, 2000])
+    for k in ("dx", "dr", "di", "dz"):
+        close(k, getattr(g, k)[-2000:], want[k])
