@@ -98,6 +98,12 @@ __global__ void __launch_bounds__(NT, PER_SM)
                 R::load(s + 2 * R::TILE, g.i, g.i_s, t, c0, rows, cols);
                 R::load(s + 3 * R::TILE, g.d_o, g.do_s, t, c0, rows, cols);
                 if (GATED) R::load(s + 4 * R::TILE, g.z, g.z_s, t, c0, rows, cols);
+                if (MODE == MODD) {
+                    const int m = lane / 8;
+                    R::last_word(s + m * R::TILE, m == 0 ? g.x : m == 1 ? g.r : m == 2 ? g.i : g.d_o,
+                                 m == 0 ? g.x_s : m == 1 ? g.r_s : m == 2 ? g.i_s : g.do_s, t, c0, rows, cols);
+                    if (GATED && m == 0) R::last_word(s + 4 * R::TILE, g.z, g.z_s, t, c0, rows, cols);
+                }
             }
             if (warp == WARPS - 1) {
                 const uint32_t h = ptx::smem_u32(&sH[stage][0]);
@@ -247,7 +253,7 @@ __global__ void __launch_bounds__(NT, PER_SM)
         if (whole) forward(std::true_type{});
         else forward(std::false_type{});
         // (the first warp's own states come before its look back: by then the value is mostly there)
-        if (warp == 0) sIn[lane] = walk_value(g, order, tc, Ar, nBr);
+        if (warp == 0) sIn[lane] = walk_back<3>(g, order, tc, Ar, nBr);   // (8 cost registers: 612 us for 545)
         __syncthreads();
         float2 carry = sIn[lane], sa = f2(0.f), sr = f2(0.f), si = f2(0.f);
         for (int u = WARPS - 1; u > warp; --u) carry = apply(sAr[u][lane], sBr[u][lane], carry);

@@ -88,7 +88,9 @@ __global__ void __launch_bounds__(ALL, PER_SM)
                 At = A.x < 0.f ? A : At.x < 0.f ? At : mul2(At, A);
             }
             walk_map(g, tile.x, tile.y, At, Bt);
-            float2 h = walk_value(g, tile.x, tile.y, At, Bt);
+            // (where there are few columns, and so many tiles of each under way, 8 predecessors: 32768 tokens x 512
+            // channels 64 us for 97, but 16384 x 4096 158 for 139)
+            float2 h = g.tiles_c <= 8 ? walk_back<8>(g, tile.x, tile.y, At, Bt) : walk_back<3>(g, tile.x, tile.y, At, Bt);
 #pragma unroll
             for (int w = 0; w < WARPS; ++w) {
                 sIn[buf][w][lane] = h;
@@ -117,6 +119,11 @@ __global__ void __launch_bounds__(ALL, PER_SM)
                 R::load(s + R::TILE, g.r, g.r_s, t, c0, rows, cols);
                 R::load(s + 2 * R::TILE, g.i, g.i_s, t, c0, rows, cols);
                 if (GATED) R::load(s + 3 * R::TILE, g.z, g.z_s, t, c0, rows, cols);
+                if (MODE == MODD) {
+                    const int m = lane / 8;
+                    R::last_word(s + m * R::TILE, m == 0 ? g.x : m == 1 ? g.r : m == 2 ? g.i : GATED ? g.z : nullptr,
+                                 m == 0 ? g.x_s : m == 1 ? g.r_s : m == 2 ? g.i_s : g.z_s, t, c0, rows, cols);
+                }
             }
             ptx::cp_async_commit();
         }

@@ -42,28 +42,46 @@ template <typename TI, int MODE> struct Rows {
     }
 
     // (not MTMA) Starts the copies of rows t .. t + rows - 1 (`stride` bytes apart), channels c0 .. c0 + cols - 1;
-    // the rest becomes zero.
+    // the rest becomes zero.  MODD: a row's words from the one that holds its first element; the last of
+    // them, whose first half is the row's last element, comes by `last_words`.
     static __device__ __forceinline__ void load(uint32_t dst, const void* base, uint32_t stride, int t, int c0, int rows, int cols) {
         const int lane = threadIdx.x & 31;
         const char* const first = static_cast<const char*>(base);
-        constexpr int PER = PITCH / 4;                          // 32, 33 or 64 words of a row
-        const char* p = first + (uint64_t)(uint32_t)t * stride + (uint32_t)(c0 * ES);
+        constexpr int PER = TILE_C * ES / 128;                  // words of a row, a lane
+        const char* p = first + (uint64_t)(uint32_t)t * stride + (uint32_t)(c0 * ES) + lane * 4;
+        dst += lane * 4;
+        if (rows >= SUB && cols == TILE_C) {
 #pragma unroll
-        for (int k = 0; k < SUB; ++k) {
-            const char* q = p;
-            int bytes = k < rows ? cols * ES : 0;
-            if (MODE == MODD) {                                 // from the word that holds the first element: the half
-                const int odd = (int)(reinterpret_cast<uintptr_t>(p) & 2);   // before it is copied and not used
-                q -= odd;
-                bytes += bytes > 0 ? odd : 0;
+            for (int k = 0; k < SUB; ++k) {
+#pragma unroll
+                for (int w = 0; w < PER; ++w)
+                    copy<4>(dst + k * PITCH + w * 128, (MODE == MODD ? down(p) : p) + w * 128, 4);
+                p += stride;
             }
+            return;
+        }
+#pragma unroll 1
+        for (int k = 0; k < SUB; ++k) {
+            const int odd = MODE == MODD ? (int)(reinterpret_cast<uintptr_t>(p) & 2) : 0;
+            const int bytes = k < rows ? cols * ES + odd : 0;
 #pragma unroll
-            for (int w = lane; w < PER; w += 32) {
-                const int n = min(max(bytes - w * 4, 0), 4);
-                copy<4>(dst + k * PITCH + w * 4, n > 0 ? q + w * 4 : first - (reinterpret_cast<uintptr_t>(first) & 2), n);
+            for (int w = 0; w < PER; ++w) {
+                const int n = min(max(bytes - (lane + 32 * w) * 4, 0), 4);
+                copy<4>(dst + k * PITCH + w * 128, n > 0 ? p - odd + w * 128 : down(first), n);
             }
             p += stride;
         }
+    }
+    static __device__ __forceinline__ const char* down(const char* p) {   // to the word
+        return reinterpret_cast<const char*>(reinterpret_cast<uintptr_t>(p) & ~(uintptr_t)3);
+    }
+    // (MODD) The 33rd word of a row, a lane each for 8 rows of four tensors (`base` and `stride` by lane / 8).
+    static __device__ __forceinline__ void last_word(uint32_t dst, const void* base, uint32_t stride, int t, int c0, int rows, int cols) {
+        const int row = threadIdx.x & 7;
+        const char* p = static_cast<const char*>(base) + (uint64_t)(uint32_t)(t + row) * stride + (uint32_t)((c0 + TILE_C) * ES);
+        const bool in = base != nullptr && row < rows && cols == TILE_C && (reinterpret_cast<uintptr_t>(p) & 2) != 0;
+        // (the word before p's holds the row's last element as its first half: p is the half behind it)
+        if (in) copy<4>(dst + row * PITCH + TILE_C * ES, p - 2, 2);
     }
 
     // Whether the first element of row t (channel c0) is the second of its word, and how that changes by row.
@@ -186,16 +204,14 @@ __device__ __forceinline__ Borders borders(const ScanArgs& g, int tile_t, int t)
 
 // ---- the walk along the tiles -------------------------------------------------------------
 // Tiles are taken in the order of a ticket, all of one place along T before the next, so a
-// tile's predecessors have been taken, by CTAs that are running, and every wait ends.  A tile publishes its map h -> A h + B, then looks back for the nearest of 3
+// tile's predecessors have been taken, by CTAs that are running, and every wait ends.  A tile publishes its map h -> A h + B, then looks back for the nearest of BACK
 // predecessors whose outgoing value is known, and applies the maps in between in their order:
 // the same operations in any timing, so results do not depend on it.
 // Maps and values are their own flags: the words are set to EMPTY, a NaN that is never
 // published, before the first tile, and a reader takes each as soon as it is another one, so no
 // fence stands between a tile and the next.  (With flags beside them, two fences and one
-// more read: 5 us more a tile.)
-constexpr uint64_t WAIT_NS = 2000000000ull;
+// more read: 5 us more a tile.)constexpr uint64_t WAIT_NS = 2000000000ull;
 constexpr uint32_t EMPTY = 0xffffffffu;
-constexpr int BACK = 3;
 
 __device__ __forceinline__ uint32_t word_of(float x) {
     const uint32_t u = __float_as_uint(x);
@@ -230,7 +246,7 @@ __device__ __forceinline__ void walk_map(const ScanArgs& g, int order, int tile_
     else publish(g.map + 2 * me, A, B);
 }
 // Then: the value that comes into the tile, returned, and the one that leaves it.
-__device__ __forceinline__ float2 walk_value(const ScanArgs& g, int order, int tile_c, float2 A, float2 B) {
+template <int BACK> __device__ __forceinline__ float2 walk_back(const ScanArgs& g, int order, int tile_c, float2 A, float2 B) {
     const int lane = threadIdx.x & 31;
     const size_t me = walk_place(g, order, tile_c);
     const size_t step = (size_t)g.tiles_c * TILE_C;
