@@ -42,8 +42,8 @@ template <typename TI, int MODE> struct Rows {
     }
 
     // (not MTMA) Starts the copies of rows t .. t + rows - 1 (`stride` bytes apart), channels c0 .. c0 + cols - 1;
-    // the rest becomes zero.  MODD: a row's words from the one that holds its first element; the last of
-    // them, whose first half is the row's last element, comes by `last_words`.
+    // the rest becomes zero.  MODD: a row's words from the one that holds its first element; the 33rd
+    // of them, whose first half is the row's last element, comes by `last_word`.
     static __device__ __forceinline__ void load(uint32_t dst, const void* base, uint32_t stride, int t, int c0, int rows, int cols) {
         const int lane = threadIdx.x & 31;
         const char* const first = static_cast<const char*>(base);
@@ -204,13 +204,15 @@ __device__ __forceinline__ Borders borders(const ScanArgs& g, int tile_t, int t)
 
 // ---- the walk along the tiles -------------------------------------------------------------
 // Tiles are taken in the order of a ticket, all of one place along T before the next, so a
-// tile's predecessors have been taken, by CTAs that are running, and every wait ends.  A tile publishes its map h -> A h + B, then looks back for the nearest of BACK
-// predecessors whose outgoing value is known, and applies the maps in between in their order:
-// the same operations in any timing, so results do not depend on it.
+// tile's predecessors have been taken, by CTAs that are running, and every wait ends.  A tile
+// publishes its map h -> A h + B, then looks back for the nearest of BACK predecessors whose
+// outgoing value is known, and applies the maps in between in their order.  How far back a value
+// was found changes neither the maps nor their order, so results do not depend on the timing.
 // Maps and values are their own flags: the words are set to EMPTY, a NaN that is never
 // published, before the first tile, and a reader takes each as soon as it is another one, so no
 // fence stands between a tile and the next.  (With flags beside them, two fences and one
-// more read: 5 us more a tile.)constexpr uint64_t WAIT_NS = 2000000000ull;
+// more read: 5 us more a tile.)
+constexpr uint64_t WAIT_NS = 2000000000ull;
 constexpr uint32_t EMPTY = 0xffffffffu;
 
 __device__ __forceinline__ uint32_t word_of(float x) {
