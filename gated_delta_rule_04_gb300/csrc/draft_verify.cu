@@ -226,6 +226,8 @@ __device__ __forceinline__ Sum sum_piece(const Coef& k, const Row<TP>& r, int a,
         };
 #pragma unroll
         for (int st = 0; st < DEPTH; ++st) issue(st, st < steps && !(there && steps <= DEPTH));
+        // (the head belongs to the first part, the tail to the last)
+        s.add<KIND>(k, make_float2(lane < 16 ? pe : 0.f, 0.f), make_float2(lane < 16 ? qe : 0.f, 0.f));
         const int each = marks ? parts.size / (64 * N) : INT_MAX;
         int left = each;
         for (int i = 0; i < steps;) {
@@ -238,13 +240,13 @@ __device__ __forceinline__ Sum sum_piece(const Coef& k, const Row<TP>& r, int a,
                 add(at[2 * NT], KIND ? at[3 * NT] : at[0]);
                 ++i;
                 issue(st, i - 1 + DEPTH < steps);
-                if (--left == 0) {
+                if (--left == 0 && i < steps) {
                     mark(part++, so_far());
                     left = each;
                 }
             }
         }
-        s.add<KIND>(k, make_float2(pe, 0.f), make_float2(qe, 0.f));
+        s.add<KIND>(k, make_float2(lane < 16 ? 0.f : pe, 0.f), make_float2(lane < 16 ? 0.f : qe, 0.f));
     } else {
         for (int i0 = a; i0 < b; i0 += 32 * LOOSE) {
             const int i = i0 + lane;

@@ -210,3 +210,18 @@ def test_a_round_of_both_mixers():
             assert torch.equal(h[0, 0], hrows[s, j])
         assert (S[s] - S1[0]).norm() <= 1e-4 * S1.norm() and torch.equal(ring[s], r1[0])
         assert (hS[s] - h1[0]).norm() <= 2e-5 * h1.norm()
+
+
+@pytest.mark.parametrize("io,V,n", [("bf16", 131072, 3), ("f32", 131071, 2), ("f32", 40001, 90), ("bf16", 32768, 160), ("bf16", 30011, 330)])
+@pytest.mark.parametrize("drawn", [True, False])
+def test_long_rows(io, V, n, drawn):
+    """Several steps of copies a warp, pieces long enough to keep their parts' sums, in one CTA to 16; a
+    few entries that count as zero among them."""
+    d = make_draft(n, 3, V, IO[io], 22, "star" if drawn else "chain", drawn)
+    d["u"] = 0.5 + 0.5 * d["u"]
+    for t in ("p", "p_last", "q", "q_last"):
+        if d[t] is not None:
+            d[t][1, ..., 1000] = float("nan")
+            d[t][1, ..., V - 2] = -1.0
+    d["p_last"][0, 5] = float("inf")
+    check(d)
