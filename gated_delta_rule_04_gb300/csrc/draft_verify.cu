@@ -312,7 +312,8 @@ struct Order {
     int ask, then;                   // SUM or END; behind the sum: SUM (another one), SEARCH or END
     int cur, refused, last;          // the current node; tokens refused there, taken out of W; a search follows
     float2 c;
-    int a, b;                        // (SEARCH) where the token is,
+    int a, b;                        // (SEARCH) where the token is, in the part that
+    int whole;                       // the sums gave (0), the whole row (1), or p itself (2); 3: found
     double base, goal;               // the sum before that, and the one to be passed
     int tok[KDA_TREE_MAX_NODES];
     float p[KDA_TREE_MAX_NODES];
@@ -512,9 +513,17 @@ __global__ void __launch_bounds__(NT, 1024 / NT) verify_kernel(const __grid_cons
             int then = SUM;
             if (!ending) {
                 T = total;
-            } else if (!(total > 0.0) && (k.kind() || refused)) {
+            } else if (!(total > 0.0) && k.kind()) {
                 c = Coef{};                           // nothing is left: p itself
-                refused = 0;
+            } else if (refused && !dead && total <= 1e-9 * (1.0 - T)) {
+                // what is left may be the rounding of what was taken out: the row once more, by one CTA
+                then = rank == 0 ? SEARCH : END;
+                if (lane == 0) {
+                    order.whole = 1;
+                    order.a = 0;
+                    order.b = V;
+                    order.base = 0.0;
+                }
             } else {
                 const double goal = (double)g.u_next[s] * total, incl = scan(share, MAX_CTAS).value(), one = share.value();
                 const int owner = pick(incl, one, goal);
@@ -530,6 +539,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) verify_kernel(const __grid_cons
                     then = SEARCH;
                     if (lane == 0) {
                         order.goal = goal;
+                        order.whole = 0;
                     }
                     const Row<TP> row(p_row(cur), c.kind() ? q_row(cur) : nullptr, V, pieces);
                     int a = row.begin(rank * WARPS + at), b = row.end(rank * WARPS + at, pieces);
@@ -557,59 +567,78 @@ __global__ void __launch_bounds__(NT, 1024 / NT) verify_kernel(const __grid_cons
         __syncthreads();
         if (order.then == END) break;
         if (order.then == SUM) continue;
-        // That part once more: while it is long, an eighth of it by each warp; then by one warp.
-        auto entry = [&](int y, bool in, float& d, float& r) {    // W(y)
-            w_of<ANY>(k, in ? clean(to_f32(row.p[y])) : 0.f, in && row.q ? clean(to_f32(row.q[y])) : 0.f, d, r);
-            for (int j = 0; j < order.refused; ++j)
-                if (order.tok[j] == y) d = r = 0.f;
-        };
-        while (order.b - order.a > FINAL) {
-            const int a = order.a, b = order.b, size = (int)(((int64_t)b - a + WARPS * 32 - 1) / (WARPS * 32)) * 32;
-            const int from = (int)min((int64_t)b, a + (int64_t)warp * size), to = (int)min((int64_t)b, (int64_t)from + size);
-            Sum v;
-            for (int y0 = from; y0 < to; y0 += 32 * 4) {
-                float d[4], r[4];
+        // That part once more: while it is long, an eighth of it by each warp; then by one warp.  Where rounding
+        // (of sums that tokens were taken out of) led to a part with nothing in it, the whole row; if
+        // that has nothing, p itself.
+        for (int whole = order.whole; whole < 3;) {
+            const TP* const q = whole == 2 ? nullptr : row.q;
+            const int out = whole == 2 ? 0 : order.refused;
+            auto entry = [&](int y, bool in, float& d, float& r) {    // W(y)
+                w_of<ANY>(k, in ? clean(to_f32(row.p[y])) : 0.f, in && q ? clean(to_f32(q[y])) : 0.f, d, r);
+                for (int j = 0; j < out; ++j)
+                    if (order.tok[j] == y) d = r = 0.f;
+            };
+            for (bool sum = whole > 0; sum || order.b - order.a > FINAL; sum = false) {   // (sum: the row's comes first)
+                const int a = order.a, b = order.b, size = (int)(((int64_t)b - a + WARPS * 32 - 1) / (WARPS * 32)) * 32;
+                const int from = (int)min((int64_t)b, a + (int64_t)warp * size), to = (int)min((int64_t)b, (int64_t)from + size);
+                Sum v;
+                for (int y0 = from; y0 < to; y0 += 32 * 4) {
+                    float d[4], r[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) entry(y0 + 32 * e + lane, y0 + 32 * e + lane < to, d[e], r[e]);
+                    for (int e = 0; e < 4; ++e) entry(y0 + 32 * e + lane, y0 + 32 * e + lane < to, d[e], r[e]);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v.add(d[e], r[e]);
-            }
-            v = warp_sum(v);
-            if (lane == 0) wsum[warp] = make_float2(v.hi, v.lo);
-            __syncthreads();
-            if (warp == 0) {
-                const Sum mine = lane < WARPS ? sum_of(wsum[lane]) : Sum{};
-                const double w = mine.value(), in = scan(mine, WARPS).value();
-                const int at = max(pick(order.base + in, w, order.goal), 0);
-                __syncwarp();
-                if (lane == at) {
-                    order.a = (int)min((int64_t)b, a + (int64_t)at * size);
-                    order.b = (int)min((int64_t)b, (int64_t)order.a + size);
-                    order.base += in - w;
+                    for (int e = 0; e < 4; ++e) v.add(d[e], r[e]);
                 }
+                v = warp_sum(v);
+                if (lane == 0) wsum[warp] = make_float2(v.hi, v.lo);
+                __syncthreads();
+                if (warp == 0) {
+                    const Sum mine = lane < WARPS ? sum_of(wsum[lane]) : Sum{};
+                    const double w = mine.value(), in = scan(mine, WARPS).value();
+                    const double goal = sum ? (double)g.u_next[s] * __shfl_sync(FULL, in, WARPS - 1) : order.goal;
+                    const int at = max(pick(order.base + in, w, goal), 0);
+                    __syncwarp();
+                    if (lane == at) {
+                        order.a = (int)min((int64_t)b, a + (int64_t)at * size);
+                        order.b = (int)min((int64_t)b, (int64_t)order.a + size);
+                        order.base += in - w;
+                        order.goal = goal;
+                    }
+                }
+                __syncthreads();
+            }
+            int found = -1;
+            if (warp == 0) {
+                int a = order.a, b = order.b;
+                float d[FINAL / 32], r[FINAL / 32];
+                const int per = (b - a + 31) / 32, y0 = a + lane * per;
+#pragma unroll
+                for (int e = 0; e < FINAL / 32; ++e) entry(y0 + e, e < per && y0 + e < b, d[e], r[e]);
+                Sum v;
+#pragma unroll
+                for (int e = 0; e < FINAL / 32; ++e) v.add(d[e], r[e]);
+                double w = v.value(), in = scan(v, 32).value(), base = order.base;
+                const int at = max(pick(base + in, w, order.goal), 0);
+                base += __shfl_sync(FULL, in - w, at);
+                a += at * per;
+                b = min(b, a + per);
+                entry(a + lane, a + lane < b, d[0], r[0]);
+                v = sum_of(make_float2(d[0], r[0]));
+                w = v.value();
+                in = scan(v, FINAL / 32).value();
+                const int y = pick(base + in, w, order.goal);
+                if (y >= 0) found = a + y;
+            }
+            __syncthreads();                          // (all have read what changes now)
+            if (tid == 0) {
+                if (found >= 0 || whole == 2) g.next[s] = found;
+                order.whole = found >= 0 ? 3 : whole + 1;
+                order.a = 0;
+                order.b = V;
+                order.base = 0.0;
             }
             __syncthreads();
-        }
-        if (warp == 0) {
-            int a = order.a, b = order.b;
-            float d[FINAL / 32], r[FINAL / 32];
-            const int per = (b - a + 31) / 32, y0 = a + lane * per;
-#pragma unroll
-            for (int e = 0; e < FINAL / 32; ++e) entry(y0 + e, e < per && y0 + e < b, d[e], r[e]);
-            Sum v;
-#pragma unroll
-            for (int e = 0; e < FINAL / 32; ++e) v.add(d[e], r[e]);
-            double w = v.value(), in = scan(v, 32).value(), base = order.base;
-            const int at = max(pick(base + in, w, order.goal), 0);
-            base += __shfl_sync(FULL, in - w, at);
-            a += at * per;
-            b = min(b, a + per);
-            entry(a + lane, a + lane < b, d[0], r[0]);
-            v = sum_of(make_float2(d[0], r[0]));
-            w = v.value();
-            in = scan(v, FINAL / 32).value();
-            const int y = pick(base + in, w, order.goal);
-            if (lane == 0) g.next[s] = y < 0 ? -1 : a + y;
+            whole = order.whole;
         }
         break;
     }

@@ -212,6 +212,28 @@ def test_a_round_of_both_mixers():
         assert (hS[s] - h1[0]).norm() <= 2e-5 * h1.norm()
 
 
+@pytest.mark.parametrize("V", [100, 5000, 40001])
+def test_a_rest_lost_in_rounding(V):
+    """Chosen tokens that hold all of the target but nothing or a trace, of very different sizes: what is left
+    of the sums once they are refused is rounding.  The next token is the trace, or drawn from p itself."""
+    g = torch.Generator().manual_seed(V)
+    n, R = 60, 24
+    d = make_draft(n, R, V, torch.float32, 21, "star", drawn=False)
+    d["p_last"][:] = 0
+    d["u"][:] = 1.0
+    d["u_next"][::3] = 0
+    for s in range(n):
+        where = torch.randperm(V, generator=g)[:R + 1]
+        d["tokens"][s] = where[:R]
+        values = torch.rand(R, generator=g) * 2.0 ** -torch.arange(2, R + 2) * 2.0 ** -torch.randint(0, 20, (R,), generator=g)
+        d["p_last"][s, where[:R]] = values[torch.randperm(R, generator=g)]
+        if s % 2:
+            d["p_last"][s, where[R]] = 1e-25
+    wp, wn = check(d)
+    assert all(p == [] for p in wp)
+    assert all(d["p_last"][s, wn[s]] == torch.tensor(1e-25) for s in range(1, n, 2))
+
+
 @pytest.mark.parametrize("io,V,n", [("bf16", 131072, 3), ("f32", 131071, 2), ("f32", 40001, 90), ("bf16", 32768, 160), ("bf16", 30011, 330)])
 @pytest.mark.parametrize("drawn", [True, False])
 def test_long_rows(io, V, n, drawn):
