@@ -714,6 +714,7 @@ def kda_glr_backward(params: GlrParams, x, r, i, cu_seqlens, states, do, z=None,
     def out(name, v):
         if v is None:
             v = _empty(x, (T, C), t, stream)
+            return v, v.data_ptr(), 0
         return v, *_rows(name, v, t, T, C, dev)
 
     def sums(name, v, shape):

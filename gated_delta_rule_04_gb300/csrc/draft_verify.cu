@@ -8,12 +8,17 @@
 // refused, read once; each warp of the cluster sums a piece of it.  A row is
 // also summed where a refused child leaves siblings to be tested; then the sums' way
 // through the cluster (a word from each CTA to each, counted by a barrier) is
-// what counts.  The token is found by halves: CTA, warp, then the warp's piece once more from L2.
+// what counts.  The token is found level by level: CTA, warp, part of its piece, then the
+// part's entries once more from L2.
 //
 // Sums are pairs of floats (two-sums of Knuth and Dekker: 48 bits) and, where few,
 // doubles: next to a random border, in a sum over 10^5 entries, a 32-bit sum would
 // take another token in one session of 30, and this GPU adds 2 doubles a cycle and
 // SM where the rows arrive at 3 pairs.
+//
+// 256 sessions x 5 nodes x 131072, fp32: 55 to 59 us (4.1 TB/s of a copy's 6.8; memory 50 %, issue slots
+// 33 %): a session's tests, exchange and search are waits that only other sessions' rows fill.  1 x 6
+// nodes 10 us, a chain of latencies.
 #include <limits.h>
 
 #include <atomic>

@@ -2,8 +2,8 @@
 // 1 to 64 tokens per session, and the accepted paths of a round.  A thread holds
 // the states of V neighbouring channels and walks the tokens.  The rows move once and bound
 // the call: a thread copies its share of the next 3 tokens' into shared memory
-// while it computes (with the next token's in registers instead, 256 rounds of 5
-// tokens x 8192 channels took 23 us: too few bytes on their way).
+// while it computes.  256 rounds of 5 tokens x 8192 channels, bf16: 22 us in a graph (4.2 TB/s of a
+// copy's 6.8; with the next token's rows in registers instead 23), one token 2.5 us.
 #include <type_traits>
 
 #include "glr_math.cuh"

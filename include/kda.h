@@ -442,7 +442,7 @@ kda_status kda_ssm_decode(const kda_ssm_params* p, int32_t n_sessions, const voi
  * layer's projections.  An interface addition of this library; the conventions
  * above hold, but for the alignment: tensors of this mixer need that of their
  * elements only.  Rows that start on 16 bytes (address and stride) are read
- * and written 16 bytes at a time, others an element at a time.
+ * and written fastest.
  */
 typedef struct {
     int32_t channels;    /* C >= 1 */
@@ -569,7 +569,8 @@ kda_status kda_glr_commit(const kda_glr_params* p, int32_t n_sessions, int32_t n
  * or the path holds max_len nodes, the walk ends, and the token that follows is the smallest y with
  * W(y) > 0 and W(0) + ... + W(y) > u_next (W(0) + ... + W(V - 1)); if rounding leaves none, the
  * last with W(y) > 0.  If W is zero everywhere it is p itself; if that is, the token is -1.
- * Sums and tests are as good as in 64 bits.
+ * Sums and tests are as good as in 64 bits.  The call takes no workspace; should its
+ * bounded wait between a session's CTAs ever run out, next_token is -1.
  *
  *   dtype        : kda_dtype of p, p_last, q and q_last
  *   n_nodes      : 1 to KDA_TREE_MAX_NODES
