@@ -11,10 +11,10 @@
 // what counts.  The token is found level by level: CTA, warp, part of its piece, then the
 // part's entries once more from L2.
 //
-// Sums are pairs of floats (two-sums of Knuth and Dekker: 48 bits) and, where few,
-// doubles: next to a random border, in a sum over 10^5 entries, a 32-bit sum would
-// take another token in one session of 30, and this GPU adds 2 doubles a cycle and
-// SM where the rows arrive at 3 pairs.
+// Sums, borders and tests are pairs of floats (two-sums and products of Knuth and Dekker: 48 bits): next to a
+// random border, in a sum over 10^5 entries, a 32-bit sum would take another token in one
+// session of 30, and this GPU adds 2 doubles a cycle and SM where the rows arrive at 3 pairs; each
+// operation on doubles also holds a warp up for 64 cycles and more.
 //
 // 256 sessions x 5 nodes x 131072, fp32: 55 to 59 us (4.1 TB/s of a copy's 6.8; memory 50 %, issue slots
 // 33 %): a session's tests, exchange and search are waits that only other sessions' rows fill.  1 x 6
@@ -34,7 +34,7 @@ constexpr int DEPTH = 3;             // steps of copies on their way, of 32 byte
 constexpr uint32_t FULL = 0xffffffffu;
 constexpr int PARTS = 8;             // of a piece, whose sums are kept for the search
 constexpr int MARKED = 512;          // a piece longer than this keeps them
-constexpr int FINAL = 128;           // entries that one warp finds the token in, 4 neighbouring ones a lane
+constexpr int STAGED = 22;           // entries a thread that the token is found in without another read
 constexpr int LOOSE = 8;             // entries a lane and step where rows lie off 16 bytes
 constexpr uint64_t WAIT_NS = 2000000000ull;
 
@@ -52,8 +52,35 @@ struct Sum {
         lo = __fadd_rn(__fadd_rn(lo, rest), e);       // (the same whichever of two sums is added to the other)
         hi = s;
     }
-    __device__ __forceinline__ double value() const { return (double)hi + (double)lo; }
+    __device__ __forceinline__ void add(const Sum& o) { add(o.hi, o.lo); }
+    __device__ __forceinline__ void sub(const Sum& o) { add(-o.hi, -o.lo); }
+    // hi to be the sum to its own digits: behind a difference lo can be as large.
+    __device__ __forceinline__ void settle() {
+        const float s = __fadd_rn(hi, lo), b = __fsub_rn(s, hi);
+        lo = __fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(lo, b));
+        hi = s;
+    }
+    __device__ __forceinline__ bool positive() const { return hi + lo > 0.f; }
 };
+__device__ __forceinline__ Sum sum_of(float hi, float lo) {
+    Sum s;
+    s.hi = hi;
+    s.lo = lo;
+    return s;
+}
+__device__ __forceinline__ Sum sum_of(float2 x) { return sum_of(x.x, x.y); }
+// Whether a > b: where the large parts are near, their difference is exact.
+__device__ __forceinline__ bool above(const Sum& a, const Sum& b) { return (a.hi - b.hi) + (a.lo - b.lo) > 0.f; }
+__device__ __forceinline__ Sum times(float u, const Sum& t) {
+    const float m = __fmul_rn(u, t.hi);
+    return sum_of(m, __fmaf_rn(u, t.lo, __fmaf_rn(u, t.hi, -m)));
+}
+__device__ __forceinline__ Sum times(const Sum& u, const Sum& t) {
+    Sum r = times(u.hi, t);
+    r.lo = __fmaf_rn(u.lo, t.hi, r.lo);
+    return r;
+}
+__device__ __forceinline__ Sum shfl(const Sum& s, int lane) { return sum_of(__shfl_sync(FULL, s.hi, lane), __shfl_sync(FULL, s.lo, lane)); }
 __device__ __forceinline__ Sum shfl_xor(Sum s, int d) {
     Sum o;
     o.hi = __shfl_xor_sync(FULL, s.hi, d);
@@ -73,11 +100,15 @@ __device__ __forceinline__ Sum warp_sum(Sum s) {
 // The coefficient c of W = max(p - c q, 0).
 struct Coef {
     float hi = 0.f, lo = 0.f;
-    __device__ __forceinline__ void set(double v) {
-        hi = (float)v;
-        lo = (float)(v - (double)hi);
+    __device__ __forceinline__ void add(const Sum& t) {
+        Sum v;
+        v.hi = hi;
+        v.lo = lo;
+        v.add(t);
+        v.settle();
+        hi = v.hi;
+        lo = v.lo;
     }
-    __device__ __forceinline__ double value() const { return (double)hi + (double)lo; }
     __device__ __forceinline__ int kind() const { return hi == 0.f ? 0 : hi == 1.f && lo == 0.f ? 1 : 2; }
 };
 enum Kind { P_ONLY, ONE, ANY };      // c = 0, c = 1 (the first refusal), any
@@ -298,16 +329,11 @@ __device__ __forceinline__ Sum scan(Sum v, int lanes) {
     }
     return v;
 }
-__device__ __forceinline__ Sum sum_of(float2 x) {
-    Sum s;
-    s.hi = x.x;
-    s.lo = x.y;
-    return s;
-}
 
-// The first lane whose inclusive sum is above the goal, or (rounding) the last with a share; -1: none has one.
-__device__ __forceinline__ int pick(double incl, double share, double goal) {
-    const uint32_t over = __ballot_sync(FULL, share > 0.0 && incl > goal), any = __ballot_sync(FULL, share > 0.0);
+// The first lane with a share whose inclusive sum (behind base) is above the goal, or (rounding) the last with a share; -1: none has one.
+__device__ __forceinline__ int pick(Sum base, const Sum& incl, const Sum& share, const Sum& goal) {
+    base.add(incl);
+    const uint32_t any = __ballot_sync(FULL, share.positive()), over = __ballot_sync(FULL, above(base, goal)) & any;
     return over ? __ffs(over) - 1 : any ? 31 - __clz(any) : -1;
 }
 
@@ -319,7 +345,7 @@ struct Order {
     float2 c;
     int a, b;                        // (SEARCH) where the token is, in the part that
     int whole;                       // the sums gave (0), the whole row (1), or p itself (2); 3: found
-    double base, goal;               // the sum before that, and the one to be passed
+    Sum base, goal;                  // the sum before that, and the one to be passed
     int tok[KDA_TREE_MAX_NODES];
     float p[KDA_TREE_MAX_NODES];
 };
@@ -328,7 +354,8 @@ template <typename TP, int NT>
 __global__ void __launch_bounds__(NT, 1024 / NT) verify_kernel(const __grid_constant__ VerifyArgs g, int ctas) {
     constexpr int WARPS = NT / 32;
     extern __shared__ __align__(16) uint4 ring[];     // sum_piece's copies
-    __shared__ Order order;
+    __shared__ __align__(16) unsigned char order_smem[sizeof(Order)];
+    Order& order = *reinterpret_cast<Order*>(order_smem);
     __shared__ float2 wsum[WARPS], slots[2][MAX_CTAS];
     __shared__ uint64_t bars[2];
     __shared__ float2 psum[WARPS][PARTS];
@@ -377,7 +404,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) verify_kernel(const __grid_cons
                 qt[h] = hot ? 1.f : clean(to_f32(q_row(par[h])[tok[h]]));
             }
         }
-        auto first_test = [&](int h) { return pt[h] > 0.f && (double)u[h] * (double)qt[h] < (double)pt[h]; };
+        auto first_test = [&](int h) { return pt[h] > 0.f && above(sum_of(pt[h], 0.f), times(u[h], sum_of(qt[h], 0.f))); };
         at_once = nodes(first_test(0), first_test(1));
     }
     __syncwarp();
@@ -388,7 +415,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) verify_kernel(const __grid_cons
     uint64_t children = 0, refused = 0;               // to be tested at cur; (chosen tokens) refused, taken out of W
     bool first = true, arrived = true, ending = false, dead = false;
     Coef c;
-    double T = 1.0, total = 0.0;
+    Sum T = sum_of(1.f, 0.f), total;
+    float taken = 0.f;                                // (chosen tokens) their p
     Sum share;                                        // the sum of CTA `lane`
 
     // Goes on with the tests until a sum is needed: true, or the walk has ended: false.
@@ -403,39 +431,41 @@ __global__ void __launch_bounds__(NT, 1024 / NT) verify_kernel(const __grid_cons
             const int r = __ffsll((long long)children) - 1;
             children &= children - 1;
             bool yes = false;
-            double w = 0.0;
+            Sum w;
             if (p_row(cur) == nullptr) {              // the token that was chosen already
                 yes = true;
             } else if (first) {
-                w = (double)of(pt, r);
+                w.hi = of(pt, r);
                 yes = at_once >> r & 1;
             } else {
-                const double q = (double)of(qt, r);
-                w = (double)of(pt, r);
+                const float p = of(pt, r), q = of(qt, r);
                 if (hot) {
                     const int x = of(tok, r);
-                    if (refused & nodes(tok[0] == x, tok[1] == x)) w = 0.0;
+                    w.hi = refused & nodes(tok[0] == x, tok[1] == x) ? 0.f : p;
                 } else {
-                    w = fmax(w - c.value() * q, 0.0);
+                    w_of<ANY>(c, p, q, w.hi, w.lo);
                 }
-                yes = w > 0.0 && (double)of(u, r) * T * q < w;
+                yes = w.positive() && above(w, times(times(of(u, r), sum_of(q, 0.f)), T));
             }
             if (yes) {
                 if (rank == 0 && lane == 0) g.path[(size_t)s * g.max_len + len] = r;
                 ++len;
                 cur = r;
                 c = Coef{};
-                T = 1.0;
+                T = sum_of(1.f, 0.f);
                 refused = 0;
+                taken = 0.f;
                 first = arrived = true;
                 continue;
             }
             first = false;
             if (hot) {
-                T -= w;
-                if (w > 0.0) refused |= (uint64_t)1 << r;
+                T.sub(w);
+                T.settle();
+                taken += w.hi;
+                if (w.positive()) refused |= (uint64_t)1 << r;
             } else {
-                c.set(c.value() + T);
+                c.add(T);
                 if (children) return true;
             }
         }
@@ -446,6 +476,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) verify_kernel(const __grid_cons
         Sum v;
         if (lane < WARPS) v = sum_of(wsum[lane]);
         v = warp_sum(v);
+        v.settle();
         if (ctas > 1) {
             const uint32_t bar = ptx::smem_u32(&bars[buf]);
             if (lane == 0) ptx::mbar_expect_tx(bar, ctas * 8);
@@ -465,7 +496,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) verify_kernel(const __grid_cons
             v = Sum{};
         }
         share = dead ? Sum{} : v;
-        total = dead ? 0.0 : warp_sum(v).value();
+        total = dead ? Sum{} : warp_sum(v);
+        total.settle();
     };
 
     int node_before = INT_MIN;                        // whose p and q the pass before went over
@@ -518,29 +550,33 @@ __global__ void __launch_bounds__(NT, 1024 / NT) verify_kernel(const __grid_cons
             int then = SUM;
             if (!ending) {
                 T = total;
-            } else if (!(total > 0.0) && k.kind()) {
+            } else if (!total.positive() && k.kind()) {
                 c = Coef{};                           // nothing is left: p itself
-            } else if (refused && !dead && total <= 1e-9 * (1.0 - T)) {
+            } else if (refused && !dead && total.hi <= 1e-9f * taken) {
                 // what is left may be the rounding of what was taken out: the row once more, by one CTA
                 then = rank == 0 ? SEARCH : END;
                 if (lane == 0) {
                     order.whole = 1;
                     order.a = 0;
                     order.b = V;
-                    order.base = 0.0;
+                    order.base = Sum{};
                 }
             } else {
-                const double goal = (double)g.u_next[s] * total, incl = scan(share, MAX_CTAS).value(), one = share.value();
-                const int owner = pick(incl, one, goal);
+                const Sum goal = times(g.u_next[s], total), incl = scan(share, MAX_CTAS);
+                const int owner = pick(Sum{}, incl, share, goal);
                 then = END;
                 if (owner < 0) {
                     if (rank == 0 && lane == 0) g.next[s] = -1;
                 } else if (owner == rank) {           // the warp whose piece holds the token
-                    double base = __shfl_sync(FULL, incl - one, owner);
+                    Sum before = incl;
+                    before.sub(share);
+                    Sum base = shfl(before, owner);
                     const Sum mine = lane < WARPS ? sum_of(wsum[lane]) : Sum{};
-                    const double w = mine.value(), in = scan(mine, WARPS).value();
-                    const int at = max(pick(base + in, w, goal), 0);
-                    base += __shfl_sync(FULL, in - w, at);
+                    const Sum in = scan(mine, WARPS);
+                    const int at = max(pick(base, in, mine, goal), 0);
+                    before = in;
+                    before.sub(mine);
+                    base.add(shfl(before, at));
                     then = SEARCH;
                     if (lane == 0) {
                         order.goal = goal;
@@ -550,13 +586,17 @@ __global__ void __launch_bounds__(NT, 1024 / NT) verify_kernel(const __grid_cons
                     int a = row.begin(rank * WARPS + at), b = row.end(rank * WARPS + at, pieces);
                     if (b - a > MARKED) {             // and the part of it: lane i has the sum up to the end of part i
                         const Parts parts(row, a, b);
-                        double up_to = lane < PARTS ? (double)psum[at][lane].x + (double)psum[at][lane].y : 0.0;
+                        Sum up_to = lane < PARTS ? sum_of(psum[at][lane]) : Sum{};
                         if (lane < PARTS)
                             for (int j = 0; j < order.refused; ++j)
-                                if (order.tok[j] >= a && order.tok[j] < parts.end(lane)) up_to -= (double)order.p[j];
-                        const double before = __shfl_up_sync(FULL, up_to, 1), part = up_to - (lane > 0 ? before : 0.0);
-                        const int i = max(pick(base + up_to, lane < PARTS ? part : 0.0, goal), 0);
-                        base += __shfl_sync(FULL, up_to - part, i);
+                                if (order.tok[j] >= a && order.tok[j] < parts.end(lane)) up_to.add(-order.p[j]);
+                        before = shfl(up_to, max(lane - 1, 0));
+                        if (lane == 0) before = Sum{};
+                        Sum part = up_to;
+                        part.sub(before);
+                        part.settle();
+                        const int i = max(pick(base, up_to, lane < PARTS ? part : Sum{}, goal), 0);
+                        base.add(shfl(before, i));
                         b = parts.end(i);
                         a = parts.begin(i, a);
                     }
@@ -572,8 +612,9 @@ __global__ void __launch_bounds__(NT, 1024 / NT) verify_kernel(const __grid_cons
         __syncthreads();
         if (order.then == END) break;
         if (order.then == SUM) continue;
-        // That part once more: while it is long, an eighth of it by each warp; then by one warp.  Where rounding
-        // (of sums that tokens were taken out of) led to a part with nothing in it, the whole row; if
+        // That part once more: while it is long, a warp's share of it; then its W in shared memory (where
+        // the copies were), so that of reads in a row, 1 to 3 us each while others sum, there is one.  Where
+        // rounding (of sums that tokens were taken out of) led to a part with nothing in it, the whole row; if
         // that has nothing, p itself.
         for (int whole = order.whole; whole < 3;) {
             const TP* const q = whole == 2 ? nullptr : row.q;
@@ -583,7 +624,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) verify_kernel(const __grid_cons
                 for (int j = 0; j < out; ++j)
                     if (order.tok[j] == y) d = r = 0.f;
             };
-            for (bool sum = whole > 0; sum || order.b - order.a > FINAL; sum = false) {   // (sum: the row's comes first)
+            for (bool sum = whole > 0; sum || order.b - order.a > STAGED * NT; sum = false) {   // (sum: the row's comes first)
                 const int a = order.a, b = order.b, size = (int)(((int64_t)b - a + WARPS * 32 - 1) / (WARPS * 32)) * 32;
                 const int from = (int)min((int64_t)b, a + (int64_t)warp * size), to = (int)min((int64_t)b, (int64_t)from + size);
                 Sum v;
@@ -599,40 +640,57 @@ __global__ void __launch_bounds__(NT, 1024 / NT) verify_kernel(const __grid_cons
                 __syncthreads();
                 if (warp == 0) {
                     const Sum mine = lane < WARPS ? sum_of(wsum[lane]) : Sum{};
-                    const double w = mine.value(), in = scan(mine, WARPS).value();
-                    const double goal = sum ? (double)g.u_next[s] * __shfl_sync(FULL, in, WARPS - 1) : order.goal;
-                    const int at = max(pick(order.base + in, w, goal), 0);
+                    const Sum in = scan(mine, WARPS), goal = sum ? times(g.u_next[s], shfl(in, WARPS - 1)) : order.goal;
+                    const int at = max(pick(order.base, in, mine, goal), 0);
                     __syncwarp();
                     if (lane == at) {
                         order.a = (int)min((int64_t)b, a + (int64_t)at * size);
                         order.b = (int)min((int64_t)b, (int64_t)order.a + size);
-                        order.base += in - w;
+                        order.base.add(in);
+                        order.base.sub(mine);
                         order.goal = goal;
                     }
                 }
                 __syncthreads();
             }
+            float2* const W = reinterpret_cast<float2*>(ring);        // [STAGED * NT], then a thread's sums each
+            float4* const sums = reinterpret_cast<float4*>(W + STAGED * NT);
+            static_assert(DEPTH * 4 * 16 >= STAGED * 8 + 16, "they fit where the copies were");
+            const int a = order.a, n = order.b - a, per = (n + NT - 1) / NT | 1;   // neighbouring entries a thread (odd: banks)
+            for (int y0 = tid; y0 < n; y0 += 8 * NT) {
+                float d[8], r[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) entry(a + y0 + e * NT, y0 + e * NT < n, d[e], r[e]);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (y0 + e * NT < n) W[y0 + e * NT] = make_float2(d[e], r[e]);
+            }
+            __syncthreads();
+            Sum one;
+            for (int y = tid * per; y < min(n, tid * per + per); ++y) one.add(W[y].x, W[y].y);
+            const Sum up_to = scan(one, 32);
+            sums[tid] = make_float4(up_to.hi, up_to.lo, one.hi, one.lo);
+            if (lane == 31) wsum[warp] = make_float2(up_to.hi, up_to.lo);
+            __syncthreads();
             int found = -1;
             if (warp == 0) {
-                int a = order.a, b = order.b;
-                float d[FINAL / 32], r[FINAL / 32];
-                const int per = (b - a + 31) / 32, y0 = a + lane * per;
-#pragma unroll
-                for (int e = 0; e < FINAL / 32; ++e) entry(y0 + e, e < per && y0 + e < b, d[e], r[e]);
-                Sum v;
-#pragma unroll
-                for (int e = 0; e < FINAL / 32; ++e) v.add(d[e], r[e]);
-                double w = v.value(), in = scan(v, 32).value(), base = order.base;
-                const int at = max(pick(base + in, w, order.goal), 0);
-                base += __shfl_sync(FULL, in - w, at);
-                a += at * per;
-                b = min(b, a + per);
-                entry(a + lane, a + lane < b, d[0], r[0]);
-                v = sum_of(make_float2(d[0], r[0]));
-                w = v.value();
-                in = scan(v, FINAL / 32).value();
-                const int y = pick(base + in, w, order.goal);
-                if (y >= 0) found = a + y;
+                const Sum mine = lane < WARPS ? sum_of(wsum[lane]) : Sum{};
+                const Sum goal = order.goal;
+                Sum base = order.base, before = scan(mine, WARPS);
+                int at = max(pick(base, before, mine, goal), 0);           // the warp,
+                before.sub(mine);
+                base.add(shfl(before, at));
+                at = at * 32;
+                const float4 t = sums[at + lane];
+                const Sum share = sum_of(t.z, t.w);
+                before = sum_of(t.x, t.y);
+                const int from = max(pick(base, before, share, goal), 0);  // its lane,
+                before.sub(share);
+                base.add(shfl(before, from));
+                const int y = (at + from) * per + lane;
+                const Sum v = lane < per && y < n ? sum_of(W[y]) : Sum{};
+                const int k0 = pick(base, scan(v, 32), v, goal);           // and its entry
+                if (k0 >= 0) found = a + (at + from) * per + k0;
             }
             __syncthreads();                          // (all have read what changes now)
             if (tid == 0) {
@@ -640,7 +698,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) verify_kernel(const __grid_cons
                 order.whole = found >= 0 ? 3 : whole + 1;
                 order.a = 0;
                 order.b = V;
-                order.base = 0.0;
+                order.base = Sum{};
             }
             __syncthreads();
             whole = order.whole;
