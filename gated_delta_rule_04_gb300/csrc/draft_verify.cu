@@ -359,7 +359,10 @@ __global__ void __launch_bounds__(NT, 1024 / NT) verify_kernel(const __grid_cons
     __shared__ float2 wsum[WARPS], slots[2][MAX_CTAS];
     __shared__ uint64_t bars[2];
     __shared__ float2 psum[WARPS][PARTS];
-    const int s = blockIdx.x / ctas, rank = blockIdx.x % ctas, tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    const int s = blockIdx.x / ctas, rank = blockIdx.x % ctas, tid = threadIdx.x, lane = tid % 32;
+    // (the same in all lanes, which the compiler cannot see from tid / 32: what the first warp alone does, with its
+    // many shuffles and ballots, then needs no code for lanes that part ways: 256 sessions 49.5 us for 54.7, 37 of 23 nodes 25 for 29)
+    const int warp = __shfl_sync(FULL, tid / 32, 0);
     const int R = g.R, V = g.V, pieces = ctas * WARPS;
     auto p_row = [&](int r) -> const TP* {
         if (r >= 0) return static_cast<const TP*>(g.p) + s * g.p_ss + r * g.p_rs;
