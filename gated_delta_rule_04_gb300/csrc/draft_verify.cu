@@ -33,7 +33,7 @@ constexpr int MAX_CTAS = 16, SMS = 152;
 constexpr int DEPTH = 3;             // steps of copies on their way, of 32 bytes of p and of q a thread
 constexpr uint32_t FULL = 0xffffffffu;
 constexpr int PARTS = 8;             // of a piece, whose sums are kept for the search
-constexpr int MARKED = 512;          // a piece longer than this keeps them
+constexpr int MARKED = 2048;         // a piece longer than this keeps them
 constexpr int STAGED = 22;           // entries a thread that the token is found in without another read
 constexpr int LOOSE = 8;             // entries a lane and step where rows lie off 16 bytes
 constexpr uint64_t WAIT_NS = 2000000000ull;
