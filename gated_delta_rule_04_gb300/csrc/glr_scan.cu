@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(ALL, PER_SM)
         bar_sync(COME + buf, MEET);
         float2 h = sIn[buf][warp][lane];
         if (g.states && warp == 0 && !(p.bd.start & 1)) put(g.states + (size_t)p.tt * g.C + c, left, false, h);
-        if (whole) {
+        if (__shfl_sync(0xffffffffu, (int)whole, 0)) {   // (as above: 992 us for 1024)
 #pragma unroll
             for (int j = 0; j < SUB; ++j) {
                 h = fma2(p.a[j], h, p.b[j]);
