@@ -44,8 +44,8 @@ kda_status check_batch(const int64_t* cu, int32_t n_seqs, int64_t total_tokens) 
     return total_tokens > (int64_t)INT32_MAX ? KDA_ERR_UNSUPPORTED : KDA_OK;
 }
 
-// Workspace: error word | gates | ticket | the tiles' maps and values | token offsets, rows and tile table
-// of the sequences | partial sums (backward pass).
+// Workspace: error word | gates | ticket | the tiles' maps and values | token offsets and rows
+// of the sequences | the tiles' borders | partial sums (backward pass).
 struct Layout {
     size_t gates = 0, ticket = 0, map = 0, val = 0, cu = 0, id = 0, tile = 0, part = 0, total = 0;
     int64_t tiles_t = 0, tiles_c = 0;
@@ -63,7 +63,7 @@ Layout layout(const kda_glr_params* p, int32_t n_seqs, int64_t total_tokens, boo
     L.val = take(sizeof(float) * TILE_C * tiles);
     L.cu = take(sizeof(int64_t) * ((size_t)n_seqs + 1));
     L.id = take(sizeof(int32_t) * (size_t)n_seqs);
-    L.tile = take(sizeof(int32_t) * (size_t)L.tiles_t);
+    L.tile = take(sizeof(uint4) * (size_t)L.tiles_t);
     if (backward) L.part = take(sizeof(float) * 3 * (size_t)L.tiles_t * p->channels);
     L.total = off;
     return L;
@@ -76,6 +76,7 @@ cudaError_t prepare(const kda_glr_params* p, const int64_t* cu, int32_t n_seqs, 
     a->status = reinterpret_cast<int32_t*>(ws);
     a->gates = reinterpret_cast<float2*>(ws + L.gates);
     a->ticket = reinterpret_cast<uint32_t*>(ws + L.ticket);
+    a->borders = reinterpret_cast<uint4*>(ws + L.tile);
     a->map = reinterpret_cast<float*>(ws + L.map);
     a->val = reinterpret_cast<float*>(ws + L.val);
     a->part = reinterpret_cast<float*>(ws + L.part);
@@ -87,7 +88,6 @@ cudaError_t prepare(const kda_glr_params* p, const int64_t* cu, int32_t n_seqs, 
     a->empty = (L.tiles_t > 1 ? L.val - L.ticket + sizeof(float) * TILE_C * (size_t)(L.tiles_t * L.tiles_c) : WS_ALIGN) / sizeof(uint4);
     f.d_cu = reinterpret_cast<int64_t*>(ws + L.cu);
     f.d_id = reinterpret_cast<int32_t*>(ws + L.id);
-    f.d_tile = reinterpret_cast<int32_t*>(ws + L.tile);
     f.n = 0;
     for (int32_t i = 0; i < n_seqs; ++i) f.n += cu[i + 1] > cu[i];
     if (f.n <= INLINE_SEQS) {

@@ -71,7 +71,8 @@ __global__ void __launch_bounds__(NT, PER_SM)
     extern __shared__ __align__(128) unsigned char rows_smem[];    // [STAGES][x, r, i, do, z][CHUNK]
     __shared__ int2 tk[STAGES];
     __shared__ __align__(16) float2 sG[STAGES][3][32];             // the tiles' gate constants
-    __shared__ uint64_t landed[STAGES];                            // (MTMA) a tile's rows and constants are there
+    __shared__ uint4 sBd[STAGES];                                  // and borders
+    __shared__ uint64_t landed[STAGES];                            // (MTMA) a tile's rows and these are there
     __shared__ float2 sA[WARPS][32], sB[WARPS][32], sAr[WARPS][32], sBr[WARPS][32];   // maps forwards and backwards
     __shared__ float2 sIn[32], sH[STAGES][32], sums[3][WARPS][32];
     const int tid = threadIdx.x, lane = tid % 32;
@@ -85,10 +86,11 @@ __global__ void __launch_bounds__(NT, PER_SM)
         const int2 tile = tk[stage];
         if (tile.x < 0) return;
         const uint32_t s = ptx::smem_u32(rows_smem) + stage * STAGE_BYTES, bar = bars + 8 * stage;
-        ptx::mbar_expect_tx(bar, STAGE_BYTES + sizeof sG[0]);
+        ptx::mbar_expect_tx(bar, STAGE_BYTES + sizeof sG[0] + sizeof sBd[0]);
 #pragma unroll
         for (int m = 0; m < TENSORS; ++m)
             ptx::tma_load_2d(s + m * R::TILE, &maps.m[m], tile.y * TILE_C, (g.tiles_t - 1 - tile.x) * CHUNK, bar);
+        ptx::bulk_g2s(ptx::smem_u32(&sBd[stage]), g.borders + (g.tiles_t - 1 - tile.x), sizeof sBd[0], bar);
         ptx::bulk_g2s(ptx::smem_u32(&sG[stage][0][0]), g.gates + (size_t)tile.y * (3 * TILE_C / 2), sizeof sG[0], bar);
     };
     // Each warp: its own rows (not MTMA); the last warp: the tile's first state.
@@ -139,14 +141,14 @@ __global__ void __launch_bounds__(NT, PER_SM)
         const int order = tk[stage].x, tc = tk[stage].y, tt = g.tiles_t - 1 - order;
         if (order < 0) break;
         const int t = tt * CHUNK + warp * SUB, c0 = tc * TILE_C, c = c0 + 2 * lane, rows = (int)g.T - t, left = g.C - c;
-        const Borders bd = borders(g, tt, t);
-        auto seq_of = [&](int j) { return (size_t)seq_id(g.f, bd.seq + __popc((bd.start >> 1) & ((1u << j) - 1))); };
         asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
         __syncwarp();
         if (MODE == MTMA) {
             wait_or(g, bars + 8 * stage, phases >> stage & 1);
             phases ^= 1u << stage;
         }
+        const Borders bd = borders(g, MODE == MTMA ? sBd[stage] : g.borders[tt], t);
+        auto seq_of = [&](int j) { return (size_t)seq_id(g.f, bd.seq + __popc((bd.start >> 1) & ((1u << j) - 1))); };
         const Gate k = MODE == MTMA ? Gate{sG[stage][0][lane], sG[stage][1][lane], sG[stage][2][lane]} : load_gate(g, tc);
 
         unsigned char* const s = mine + stage * STAGE_BYTES;

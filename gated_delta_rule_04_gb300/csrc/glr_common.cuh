@@ -11,14 +11,13 @@ constexpr int INLINE_SEQS = 16;
 constexpr int TILE_C = 64;           // channels of a tile; its tokens are a CHUNK
 
 // The sequences of a call that have tokens, in order.  Few travel in the kernel
-// arguments; more are built on the device, with the sequence of each tile's first token.
+// arguments; more are built on the device.
 struct Sequences {
     int32_t n;                       // sequences with tokens
     int32_t cu[INLINE_SEQS + 1];     // where n <= INLINE_SEQS: their first tokens, and T
     int32_t id[INLINE_SEQS];         // their rows of S_in and S_out
     const int64_t* d_cu;             // device [n + 1] and [n] otherwise
     const int32_t* d_id;
-    const int32_t* d_tile;           // device [tiles along T]
 };
 __device__ __forceinline__ int seq_id(const Sequences& f, int s) { return f.n <= INLINE_SEQS ? f.id[s] : f.d_id[s]; }
 
@@ -45,6 +44,7 @@ struct ScanArgs {
     // workspace
     int32_t* status;                 // error word
     float2* gates;                   // [tiles along C][3][TILE_C / 2]: see load_gate
+    uint4* borders;                  // [tiles along T]: see borders()
     uint32_t* ticket;                // the next tile to be taken, and behind it
     float* map;                      // [tiles along T][tiles along C][TILE_C][2]
     float* val;                      // [tiles along T][tiles along C][TILE_C]

@@ -45,6 +45,7 @@ __global__ void __launch_bounds__(ALL, PER_SM)
     extern __shared__ __align__(128) unsigned char rows_smem[];    // [STAGES][x, r, i, z][CHUNK]
     __shared__ int2 tk[RING];                        // the tiles' places: order and column, -1 behind the last
     __shared__ float2 sG[RING][3][32];               // and gate constants
+    __shared__ uint4 sBd[RING];                      // and borders
     __shared__ float2 sA[2][WARPS][32], sB[2][WARPS][32], sIn[2][WARPS][32];
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     auto place_gates = [&](int slot, const Gate& k) {
@@ -52,6 +53,7 @@ __global__ void __launch_bounds__(ALL, PER_SM)
         sG[slot][1][lane] = k.rb;
         sG[slot][2][lane] = k.ib;
     };
+    auto borders_of = [&](int2 tile) { return g.borders[max(tile.x, 0)]; };
     __shared__ uint64_t landed[STAGES];              // (MTMA) a tile's rows are there
     const uint32_t bars = ptx::smem_u32(landed);
     if (tid == 0) {
@@ -80,12 +82,14 @@ __global__ void __launch_bounds__(ALL, PER_SM)
         if (MODE == MTMA && tid == NT)
             for (int k = 0; k < STAGES; ++k) load_tile(k, k);
         place_gates(buf, load_gate(g, tk[buf].y));
+        if (lane == 0) sBd[buf] = borders_of(tk[buf]);
         __syncthreads();
         for (int k = buf;; k += 2) {
             bar_sync(READY + buf, MEET);
             const int2 tile = tk[k % RING], second = tk[(k + 2) % RING];
             if (tile.x < 0) return;
             const Gate q = load_gate(g, second.y);   // of the tile after the next
+            const uint4 bd = borders_of(second);
             float2 At = sA[buf][0][lane], Bt = sB[buf][0][lane];
 #pragma unroll
             for (int w = 1; w < WARPS; ++w) {
@@ -103,6 +107,7 @@ __global__ void __launch_bounds__(ALL, PER_SM)
                 h = apply(sA[buf][w][lane], sB[buf][w][lane], h);
             }
             place_gates((k + 2) % RING, q);
+            if (lane == 0) sBd[(k + 2) % RING] = bd;
             bar_arrive(COME + buf, MEET);
             if (MODE == MTMA) {                      // tile k + 3 in the place of this one
                 bar_sync(FREE + buf, MEET);
@@ -151,7 +156,7 @@ __global__ void __launch_bounds__(ALL, PER_SM)
         p.tc = tk[slot].y;
         const Gate k{sG[slot][0][lane], sG[slot][1][lane], sG[slot][2][lane]};
         const int t = p.tt * CHUNK + warp * SUB, c0 = p.tc * TILE_C, c = c0 + 2 * lane;
-        p.bd = borders(g, p.tt, t);
+        p.bd = borders(g, sBd[slot], t);
         wait_rows(stage);
         const unsigned char* s = mine + stage * STAGE_BYTES;
         const typename R::Odd ox = R::odd(g.x, g.x_s, t, c0), orr = R::odd(g.r, g.r_s, t, c0), oi = R::odd(g.i, g.i_s, t, c0);

@@ -164,42 +164,43 @@ __device__ __forceinline__ float2 pair_at(const float* p, size_t row, int c, int
 
 // ---- sequence borders -------------------------------------------------------------------
 // Of the warp's 8 tokens from t on: which begin a sequence, which end one, and the sequence
-// of the first (each start adds one).  Warp-uniform.
+// of the first (each start adds one).  Warp-uniform.  From a table by tile, made once: a bit for each of
+// its tokens that begins a sequence, the sequence of its first token, and whether the next tile begins
+// with one.
 struct Borders {
     uint32_t start, end;
     int seq;
 };
-__device__ __forceinline__ Borders borders(const ScanArgs& g, int tile_t, int t) {
-    const int lane = threadIdx.x & 31, n = g.f.n;
-    if (n == 1 && t > 0 && t + SUB < g.T) return Borders{0, 0, 0};
-    int s0 = 0;
-    int64_t c1 = INT64_MAX, c2 = INT64_MAX, c0 = 0;            // starts of sequences s0 + 1 + lane, s0 + 33 + lane, s0
-    if (n <= INLINE_SEQS) {
-        if (lane < n) c1 = g.f.cu[1 + lane];
-    } else {
-        s0 = g.f.d_tile[tile_t];
-        c0 = g.f.d_cu[s0];
-        if (s0 + 1 + lane <= n) c1 = g.f.d_cu[s0 + 1 + lane];
-        if (s0 + 33 + lane <= n) c2 = g.f.d_cu[s0 + 33 + lane];
-    }
-    auto of = [&](int x) {                                  // the sequence of token x of this tile, or before / behind it
-        int s = s0 + __popc(__ballot_sync(0xffffffffu, c1 <= x)) - (x < c0 ? 1 : 0);
-        if (n > INLINE_SEQS) s += __popc(__ballot_sync(0xffffffffu, c2 <= x));
-        return s;
-    };
-    int prev = of(t - 1);
-    if (of(t + SUB) == prev) return Borders{0, 0, prev};        // (t = 0: before the first sequence, -1)
-    int cur = of(t);
-    Borders b{0, 0, cur};
-#pragma unroll 1
-    for (int j = 0; j < SUB && t + j < g.T; ++j) {
-        const int next = of(t + j + 1);
-        b.start |= (cur != prev ? 1u : 0u) << j;
-        b.end |= (next != cur ? 1u : 0u) << j;
-        prev = cur;
-        cur = next;
-    }
+__device__ __forceinline__ Borders borders(const ScanArgs& g, const uint4& tile, int t) {
+    const int at = t % CHUNK, rows = (int)g.T - t;
+    const uint64_t starts = tile.x | (uint64_t)tile.y << 32;
+    const uint32_t after = at + SUB < CHUNK ? (uint32_t)(starts >> (at + SUB)) & 1u : tile.w;
+    Borders b;
+    b.start = (uint32_t)(starts >> at) & ((1u << SUB) - 1);
+    b.end = b.start >> 1 | after << (SUB - 1);
+    if (rows > 0 && rows <= SUB) b.end |= 1u << (rows - 1);
+    b.seq = (int)tile.z + __popcll(starts & (((uint64_t)2 << at) - 2));
     return b;
+}
+// Makes it, by all warps of the grid.
+__device__ __forceinline__ void make_borders(const ScanArgs& g, size_t warp, size_t warps) {
+    const int lane = threadIdx.x & 31, n = g.f.n;
+    auto start = [&](int s) -> int64_t { return s >= n ? INT64_MAX : n <= INLINE_SEQS ? (int64_t)g.f.cu[s] : g.f.d_cu[s]; };
+    for (size_t tt = warp; tt < (size_t)g.tiles_t; tt += warps) {
+        const int64_t t0 = (int64_t)tt * CHUNK;
+        int lo = 0, hi = n - 1;                                // the last sequence that begins at or before t0
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (start(mid) <= t0) lo = mid; else hi = mid - 1;
+        }
+        const int64_t c1 = start(lo + 1 + lane) - t0, c2 = start(lo + 33 + lane) - t0;
+        const uint64_t bits = (c1 < CHUNK ? (uint64_t)1 << c1 : 0) | (c2 < CHUNK ? (uint64_t)1 << c2 : 0);
+        const uint32_t first = start(lo) == t0 ? 1u : 0u;
+        const uint4 b = make_uint4(__reduce_or_sync(0xffffffffu, (uint32_t)bits) | first,
+                                   __reduce_or_sync(0xffffffffu, (uint32_t)(bits >> 32)), (uint32_t)lo,
+                                   __any_sync(0xffffffffu, c1 == CHUNK || c2 == CHUNK) ? 1u : 0u);
+        if (lane == 0) g.borders[tt] = b;
+    }
 }
 
 // ---- the walk along the tiles -------------------------------------------------------------
@@ -309,8 +310,8 @@ __device__ __forceinline__ int2 place_of(const ScanArgs& g, uint32_t ticket) {
     return make_int2((int)(k / (uint32_t)g.tiles_c), (int)(k % (uint32_t)g.tiles_c));
 }
 
-// What a walk finds in its workspace: a cleared error word, ticket, maps and values EMPTY, the gates' table, and
-// for many sequences that of the tiles' first ones.  By all threads of the grid.
+// What a walk finds in its workspace: a cleared error word, ticket, maps and values EMPTY, the gates' table and
+// that of the tiles' borders.  By all threads of the grid.
 __device__ __forceinline__ void set_up(const ScanArgs& g) {
     const size_t id = (size_t)blockIdx.x * blockDim.x + threadIdx.x, all = (size_t)gridDim.x * blockDim.x;
     if (id == 0) *g.status = ERR_NONE;
@@ -323,16 +324,7 @@ __device__ __forceinline__ void set_up(const ScanArgs& g) {
         p[TILE_C / 2] = q.rb;
         p[TILE_C] = q.ib;
     }
-    if (g.f.n <= INLINE_SEQS) return;
-    // the first sequence of each tile along T: the last one that begins at or before its first token
-    for (size_t tt = id; tt < (size_t)g.tiles_t; tt += all) {
-        int lo = 0, hi = g.f.n - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (g.f.d_cu[mid] <= (int64_t)tt * CHUNK) lo = mid; else hi = mid - 1;
-        }
-        const_cast<int32_t*>(g.f.d_tile)[tt] = lo;
-    }
+    make_borders(g, id / 32, all / 32);
 }
 // At the start of a walk: it sets up by itself, or a kernel before it has.
 __device__ __forceinline__ void begin(const ScanArgs& g) {
