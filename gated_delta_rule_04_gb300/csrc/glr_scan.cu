@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(ALL, PER_SM)
     // The walks, even tiles' by one warp and odd ones' by the other (one warp for all was what the others
     // waited for: 151 us for 145 at 16384 tokens x 4096): maps of the tile's warps in, their first
     // values out.
-    // (The shuffle tells the compiler that the lanes go together: 1028 us for 1042 at 65273 x 8192.)
+    // (The shuffle tells the compiler that the lanes go together: 1 to 2 % at 65273 x 8192.)
     if (__shfl_sync(0xffffffffu, warp, 0) >= WARPS) {
         const int buf = warp - WARPS;
         if (MODE == MTMA && tid == NT)
@@ -199,6 +199,13 @@ __global__ void __launch_bounds__(ALL, PER_SM)
         sB[buf][warp][lane] = B;
         bar_arrive(READY + buf, MEET);
     };
+    // Where a border lies in a warp's tokens the second sweep takes other code, not at hand in the instruction
+    // cache: it is short (a loop that stays one) and passes the states through shared memory, in the place
+    // of the rows of x (and r), done with.  (16384 x 4096 in 128 sequences 191 us for 232.)
+    auto place = [&](int stage, int j) {
+        constexpr int PER = R::BYTES / 256;
+        return reinterpret_cast<float2*>(mine + stage * STAGE_BYTES + j / PER * R::TILE + j % PER * 256 + lane * 8);
+    };
     // the states and outputs of a tile, once its first value is there
     auto second_sweep = [&](const Pending& p, int stage, int buf) {
         const int t = p.tt * CHUNK + warp * SUB, c0 = p.tc * TILE_C, c = c0 + 2 * lane, left = g.C - c, rows = (int)g.T - t;
@@ -209,7 +216,7 @@ __global__ void __launch_bounds__(ALL, PER_SM)
         bar_sync(COME + buf, MEET);
         float2 h = sIn[buf][warp][lane];
         if (g.states && warp == 0 && !(p.bd.start & 1)) put(g.states + (size_t)p.tt * g.C + c, left, false, h);
-        if (__shfl_sync(0xffffffffu, (int)whole, 0)) {   // (as above: 992 us for 1024)
+        if (__shfl_sync(0xffffffffu, (int)whole, 0)) {   // (as above: 959 us for 964)
 #pragma unroll
             for (int j = 0; j < SUB; ++j) {
                 h = fma2(p.a[j], h, p.b[j]);
@@ -220,10 +227,17 @@ __global__ void __launch_bounds__(ALL, PER_SM)
 #pragma unroll
             for (int j = 0; j < SUB; ++j) {
                 h = p.bd.start >> j & 1 ? p.b[j] : fma2(p.a[j], h, p.b[j]);
-                if (j < rows) put<TI>(o, left, pair, GATED ? mul2(h, silu(R::get(s, j, oz))) : h);
+                *place(stage, j) = h;
+            }
+#pragma unroll 1
+            for (int j = 0; j < SUB && j < rows; ++j) {
+                h = *place(stage, j);
+                put<TI>(o, left, pair, GATED ? mul2(h, silu(R::get(s, j, oz))) : h);
                 o += g.o_s;
                 if (p.bd.end >> j & 1) put(g.S_out + seq_of(p.bd, j) * g.C + c, left, false, h);
             }
+            __syncwarp();
+            if (MODE == MTMA) ptx::fence_async_smem();   // (the next rows come here)
         }
     };
 
