@@ -16,9 +16,9 @@
 // session of 30, and this GPU adds 2 doubles a cycle and SM where the rows arrive at 3 pairs; each
 // operation on doubles also holds a warp up for 64 cycles and more.
 //
-// 256 sessions x 5 nodes x 131072, fp32: 55 to 59 us (4.1 TB/s of a copy's 6.8; memory 50 %, issue slots
-// 33 %): a session's tests, exchange and search are waits that only other sessions' rows fill.  1 x 6
-// nodes 10 us, a chain of latencies.
+// 256 sessions x 5 nodes x 131072, fp32: 49 to 54 us (4.5 TB/s of a copy's 6.8; memory 54 %, issue slots
+// 34 %): the pass over the rows takes 35 of them, the tests before it 4 and the exchange and search behind
+// it 5 to 10, in all sessions at about the same time.  1 x 6 nodes 9.3 us, a chain of latencies.
 #include <limits.h>
 
 #include <atomic>

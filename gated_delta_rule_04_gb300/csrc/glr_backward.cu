@@ -13,8 +13,8 @@
 // registers between the sweeps.  Sums over the tokens go to the workspace by tile
 // and are added up in order when all tiles are done.
 //
-// 16384 tokens x 4096, bf16: 287 us (4.2 TB/s of a copy's 6.8), 32768 x 4096: 545 to 549 (4.4).  Issue
-// slots 52 %, memory 56 %: with two CTAs of 8 warps an SM (registers) one other CTA covers the
+// 16384 tokens x 4096, bf16: 268 us (4.5 TB/s of a copy's 6.8), 32768 x 4096: 492 to 500 (4.9).  Issue
+// slots 56 %, memory 59 %: with two CTAs of 8 warps an SM (registers) one other CTA covers the
 // waits at a barrier.  Without the walk 253 us of then 292, without arithmetic 251, without the stores 195.
 #include <type_traits>
 

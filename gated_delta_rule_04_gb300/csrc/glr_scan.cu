@@ -10,8 +10,8 @@
 // Sequences lie anywhere in the tiles: a token that begins one starts its run
 // anew from S_in.
 //
-// 16384 tokens x 4096, bf16: 140 us (4.8 TB/s of a copy's 6.8), 65273 x 8192: 1020 to 1040 (5.2).
-// No unit is near its peak: memory 62 %, the exponentials' unit 54 %, issue slots 53 %; without
+// 16384 tokens x 4096, bf16: 141 us (4.8 TB/s of a copy's 6.8), 65273 x 8192: 960 (5.6).
+// No unit is near its peak: memory 61 %, the exponentials' unit 55 %, issue slots 54 %; without
 // arithmetic, loads or walk alone it is 139, 132 or 139 us of then 145, without all three 90.  Two CTAs an
 // SM (f32: one) are what the registers of a tile's pending sweep leave.
 #include <type_traits>
