@@ -185,15 +185,15 @@ __device__ __forceinline__ Borders borders(const ScanArgs& g, const uint4& tile,
 // Makes it, by all warps of the grid.
 __device__ __forceinline__ void make_borders(const ScanArgs& g, size_t warp, size_t warps) {
     const int lane = threadIdx.x & 31, n = g.f.n;
-    auto start = [&](int s) -> int64_t { return s >= n ? INT64_MAX : n <= INLINE_SEQS ? (int64_t)g.f.cu[s] : g.f.d_cu[s]; };
+    auto start = [&](int s) -> int64_t { return (uint32_t)s >= (uint32_t)n ? INT64_MAX : n <= INLINE_SEQS ? (int64_t)g.f.cu[s] : g.f.d_cu[s]; };
     for (size_t tt = warp; tt < (size_t)g.tiles_t; tt += warps) {
         const int64_t t0 = (int64_t)tt * CHUNK;
         int lo = 0, hi = n - 1;                                // the last sequence that begins at or before t0
         while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
+            const int mid = hi - (hi - lo) / 2;
             if (start(mid) <= t0) lo = mid; else hi = mid - 1;
         }
-        const int64_t c1 = start(lo + 1 + lane) - t0, c2 = start(lo + 33 + lane) - t0;
+        const int64_t c1 = start((int)((uint32_t)lo + 1 + lane)) - t0, c2 = start((int)((uint32_t)lo + 33 + lane)) - t0;
         const uint64_t bits = (c1 < CHUNK ? (uint64_t)1 << c1 : 0) | (c2 < CHUNK ? (uint64_t)1 << c2 : 0);
         const uint32_t first = start(lo) == t0 ? 1u : 0u;
         const uint4 b = make_uint4(__reduce_or_sync(0xffffffffu, (uint32_t)bits) | first,

@@ -536,3 +536,21 @@ def test_rows_past_32_bits_of_elements():
     want = gradients(i, [0, 2000])
     for k in ("dx", "dr", "di", "dz"):
         close(k, getattr(g, k)[-2000:], want[k])
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("C", [77, 128, 130])
+@pytest.mark.parametrize("most", [5, 40, 90])
+def test_many_short_sequences(io, C, most):
+    """More sequences than travel in a launch's arguments, several borders to a warp's tokens or a few to a tile;
+    borders on the tiles', sequences without tokens; the states in place."""
+    g = torch.Generator().manual_seed(most)
+    lens = torch.randint(0, most, (60,), generator=g).tolist()
+    lens += [-sum(lens) % 64, 64, 0, 63, 1, 64 - 8, 8]
+    cu = cumsum(lens)
+    i = make_inputs(cu[-1], len(lens), C, IO[io], 31 + most)
+    _, S, _, _ = check(i, io, cu)
+    own = i["S"].to(DEV)
+    prefill({**i, "S": None}, io, cu)                                   # (another call in between)
+    o, same = kda.kda_glr_prefill(params(i, io), dev(i["x"]), dev(i["r"]), dev(i["i"]), cu, z=dev(i["z"]), S_in=own, S_out=own)
+    assert same is own and torch.equal(own, S)
