@@ -13,7 +13,7 @@
 // registers between the sweeps.  Sums over the tokens go to the workspace by tile
 // and are added up in order when all tiles are done.
 //
-// 16384 tokens x 4096, bf16: 268 us (4.5 TB/s of a copy's 6.8), 32768 x 4096: 492 to 500 (4.9).  Issue
+// 16384 tokens x 4096, bf16: 264 us (4.6 TB/s of a copy's 6.8), 32768 x 4096: 484 to 490 (5.0).  Issue
 // slots 56 %, memory 59 %: with two CTAs of 8 warps an SM (registers) one other CTA covers the
 // waits at a barrier.  Without the walk 253 us of then 292, without arithmetic 251, without the stores 195.
 #include <type_traits>
@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(NT, PER_SM)
         }
         for (int u = 0; u < warp; ++u) nh = apply(sA[u][lane], sB[u][lane], nh);
         const bool full = pairs == (GATED ? OUT_X | OUT_R | OUT_I | OUT_Z : OUT_X | OUT_R | OUT_I) && c0 + TILE_C <= g.C;
-        const bool whole = plain && full && rows >= SUB;
+        const bool whole = __shfl_sync(0xffffffffu, (int)(plain && full && rows >= SUB), 0);   // (as `warp`: 484 us for 496)
         char* dz = GATED ? row_at<TI>(g.dz, g.dz_s, t, c) : nullptr;
         auto forward = [&](auto fast) {              // K becomes -dA_log / g
             constexpr bool FAST = decltype(fast)::value;
@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(NT, PER_SM)
         if (whole) forward(std::true_type{});
         else forward(std::false_type{});
         // (the first warp's own states come before its look back: by then the value is mostly there)
-        if (warp == 0) sIn[lane] = walk_back<3>(g, order, tc, Ar, nBr);   // (8 cost registers: 612 us for 545)
+        if (warp == 0) sIn[lane] = walk_back<3>(g, order, tc, Ar, nBr);   // (8 cost registers: 612 us for then 545)
         __syncthreads();
         float2 carry = sIn[lane], sa = f2(0.f), sr = f2(0.f), si = f2(0.f);
         for (int u = WARPS - 1; u > warp; --u) carry = apply(sAr[u][lane], sBr[u][lane], carry);
