@@ -276,7 +276,7 @@ __device__ __forceinline__ Sum sum_piece(const Coef& k, const Row<TP>& r, int a,
                 add(at[2 * NT], KIND ? at[3 * NT] : at[0]);
                 ++i;
                 issue(st, i - 1 + DEPTH < steps);
-                if (--left == 0 && i < steps) {
+                if (--left == 0 && parts.end(part) < b) {   // (the tail's entries may be a part of their own)
                     mark(part++, so_far());
                     left = each;
                 }

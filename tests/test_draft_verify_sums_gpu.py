@@ -1,0 +1,70 @@
+"""Sums of the verification of drafts (kda_draft_verify) that decide the next token: pieces of
+a row whose parts are marked, products next to the target, long rows."""
+import pytest
+import torch
+
+import gated_delta_rule_04_gb300 as kda
+from glr_ref import verify
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+IO = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from gated_delta_rule_04_gb300 import build as kbuild
+    kbuild.build()
+    kda.lib()
+
+
+def dev(x):
+    return x.to(DEV)
+
+
+def one_row(row, n, off=0):
+    """The row for n sessions (they share its memory), `off` elements behind a 256-byte boundary."""
+    at = torch.zeros(row.numel() + off, dtype=row.dtype, device=DEV)
+    at[off:] = row.to(DEV)
+    return at[off:].expand(n, row.numel())
+
+
+def draft(n, tokens, u):
+    """n sessions of the same children of the last token."""
+    R = len(tokens)
+    return (torch.tensor(tokens, dtype=torch.int32, device=DEV).expand(n, R).contiguous(),
+            torch.full((n, R), -1, dtype=torch.int32, device=DEV), torch.full((n, R), u, device=DEV))
+
+
+@pytest.mark.parametrize("io, V, n", [("f32", 8961, 700), ("f32", 128257, 256), ("f32", 33793, 256), ("bf16", 32769, 256),
+                                      ("bf16", 9729, 1300), ("bf16", 9735, 1300),
+                                      ("f32", 16381, 700), ("bf16", 16381, 1300)])
+@pytest.mark.parametrize("drawn", [True, False])
+@pytest.mark.parametrize("off", [0, 3])
+def test_tokens_behind_the_last_whole_16_bytes(io, V, n, drawn, off):
+    """Pieces whose whole steps end with a marked part and entries behind them (a part of their own), or in the middle of
+    the last part: half of the rest lies on the row's last 7 tokens, the other half all over it.  One refused child."""
+    g = torch.Generator().manual_seed(V + off)
+    w = torch.rand(V, generator=g) + 0.1
+    w[-7:] = 0
+    p = w / w.sum() * 0.5
+    p[-7:] = 0.5 / 7
+    q = p * (0.5 + torch.rand(V, generator=g))
+    q[-7:] *= 0.25
+    p[11] = 0                                            # the child's token: refused
+    p, q = p.to(IO[io]), q.to(IO[io])
+    u_next = torch.rand(n, generator=g)
+    u_next[:64] = 1 - torch.rand(64, generator=g) * 0.1
+    tokens, parents, u = draft(n, [11], 0.5)
+    rows = one_row(p, n, off)
+    path, length, nxt = kda.kda_draft_verify(torch.zeros(1, 1, V, dtype=IO[io], device=DEV).expand(n, 1, V), tokens, parents, u,
+                                             dev(u_next), p_last=rows,
+                                             q=torch.zeros(1, 1, V, dtype=IO[io], device=DEV).expand(n, 1, V) if drawn else None,
+                                             q_last=one_row(q, n, off) if drawn else None)
+    W = (p.double() - q.double()).clamp(min=0) if drawn else p.double()
+    cum = W.cumsum(0)
+    goal = u_next.double() * cum[-1]
+    want = torch.searchsorted(cum, goal, right=True)
+    assert not length.any() and bool((path == -1).all())
+    assert nxt.tolist() == want.tolist()
+    assert len(set(want[want >= V - 7].tolist())) == 7
