@@ -113,14 +113,17 @@ struct Coef {
 };
 enum Kind { P_ONLY, ONE, ANY };      // c = 0, c = 1 (the first refusal), any
 
+// What of e is taken off p beside m, where c q = m + e: at m = p, where c q may lie below p still, no more than
+// leaves W at zero; above it p is used up.
+__device__ __forceinline__ float rest_of(float m, float p, float e) { return m < p ? e : m == p ? fminf(e, 0.f) : 0.f; }
+
 // W of one token as two floats, p and q finite and not negative: p - c q with c q = m + e cut off at p, so that
 // m <= p and p - m is d + r exactly (Dekker).
 template <int KIND> __device__ __forceinline__ void w_of(const Coef& k, float p, float q, float& d, float& r) {
     float m = q, e = 0.f;
     if (KIND == ANY) {
         m = __fmul_rn(k.hi, q);
-        e = __fmaf_rn(k.lo, q, __fmaf_rn(k.hi, q, -m));
-        if (!(m < p)) e = 0.f;
+        e = rest_of(m, p, __fmaf_rn(k.lo, q, __fmaf_rn(k.hi, q, -m)));
     }
     m = fminf(m, p);
     d = __fsub_rn(p, m);
@@ -149,7 +152,7 @@ struct Pairs {
         } else if (KIND == ANY) {
             const float2 h = make_float2(k.hi, k.hi), m = __fmul2_rn(h, q);   // (as w_of)
             float2 e = __ffma2_rn(make_float2(k.lo, k.lo), q, __ffma2_rn(h, q, __fmul2_rn(m, make_float2(-1.f, -1.f))));
-            e = make_float2(m.x < p.x ? e.x : 0.f, m.y < p.y ? e.y : 0.f);
+            e = make_float2(rest_of(m.x, p.x, e.x), rest_of(m.y, p.y, e.y));
             const float2 c = make_float2(fminf(m.x, p.x), fminf(m.y, p.y));
             d = sub2(p, c);
             lo = add2(lo, sub2(sub2(sub2(p, d), c), e));

@@ -68,3 +68,40 @@ def test_tokens_behind_the_last_whole_16_bytes(io, V, n, drawn, off):
     assert not length.any() and bool((path == -1).all())
     assert nxt.tolist() == want.tolist()
     assert len(set(want[want >= V - 7].tolist())) == 7
+
+
+@pytest.mark.parametrize("V", [8, 5000])
+@pytest.mark.parametrize("accept", [False, True])
+def test_a_product_rounded_to_the_target(V, accept):
+    """c q just below p, by less than half a step of fp32: what is left of that token is positive, 2^-25 of p or
+    less, and all that is left after two refusals.  The next token is that one; a third child with it is accepted."""
+    import random
+    from fractions import Fraction as F
+    rng = random.Random(V)
+    f32 = lambda x: float(torch.tensor(float(x)))
+    found = []
+    while len(found) < 40:
+        q = f32(rng.uniform(2 ** -6, 2 ** -5))
+        p = q
+        for _ in range(50):                              # p = c q rounded, where c = 1 + T and T = (5/4 - 1) + (p - q)
+            c = 1 + F(1, 4) + F(p) - F(q)
+            p = f32(c * F(q))
+        c = 1 + F(1, 4) + F(p) - F(q)
+        if p == f32(c * F(q)) and F(p) - c * F(q) > F(p) / 2 ** 36:
+            found.append((p, q))
+    n = len(found)
+    P, Q = torch.zeros(n, V), torch.zeros(n, V)
+    P[:, 1], Q[:, 1] = 1.25, 1.0                         # left of it after the first refusal: 1/4, after the second: nothing
+    Q[:, 2], Q[:, 3] = 0.5, 0.25                         # the refused ones
+    at = V - 2
+    P[:, at], Q[:, at] = torch.tensor([x for x, _ in found]), torch.tensor([y for _, y in found])
+    tokens, parents, u = draft(n, [2, 3, at] if accept else [2, 3], 0.9)
+    R = tokens.shape[1]
+    none = torch.zeros(n, R, V)
+    none[:, :, 5] = 1.0
+    u_next = torch.linspace(0, 0.99, n)
+    path, length, nxt = kda.kda_draft_verify(dev(none), tokens, parents, u, dev(u_next), q=dev(none), p_last=dev(P), q_last=dev(Q))
+    wp, wn = verify(none, tokens.cpu(), parents.cpu(), u.cpu(), u_next, q=none, p_last=P, q_last=Q)
+    assert wp == ([[2]] * n if accept else [[]] * n) and wn == [5 if accept else at] * n
+    assert length.tolist() == [len(w) for w in wp]
+    assert nxt.tolist() == wn
