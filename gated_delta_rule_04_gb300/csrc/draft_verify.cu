@@ -94,6 +94,7 @@ __device__ __forceinline__ Sum warp_sum(Sum s) {
         const Sum o = shfl_xor(s, d);
         s.add(o.hi, o.lo);
     }
+    s.settle();
     return s;
 }
 
@@ -159,6 +160,13 @@ struct Pairs {
         }
         const float2 s = add2(hi, d), b = sub2(s, hi);
         lo = add2(lo, add2(sub2(hi, sub2(s, b)), sub2(d, b)));
+        hi = s;
+    }
+    // hi to be the sums to their own digits.  Between, lo is added up in plain fp32: were it never taken in, it
+    // would outgrow its digits over thousands of entries a lane.
+    __device__ __forceinline__ void settle() {
+        const float2 s = add2(hi, lo), b = sub2(s, hi);
+        lo = add2(sub2(hi, sub2(s, b)), sub2(lo, b));
         hi = s;
     }
     __device__ __forceinline__ bool good() const { return most <= 0x7f7fffffu; }
@@ -284,6 +292,7 @@ __device__ __forceinline__ Sum sum_piece(const Coef& k, const Row<TP>& r, int a,
                     left = each;
                 }
             }
+            s.settle();
         }
         s.add<KIND>(k, make_float2(lane < 16 ? 0.f : pe, 0.f), make_float2(lane < 16 ? 0.f : qe, 0.f));
     } else {
@@ -298,6 +307,7 @@ __device__ __forceinline__ Sum sum_piece(const Coef& k, const Row<TP>& r, int a,
             }
 #pragma unroll
             for (int u = 0; u < LOOSE; u += 2) s.add<KIND>(k, make_float2(x[u], x[u + 1]), make_float2(y[u], y[u + 1]));
+            s.settle();
             if (marks && i0 + 32 * LOOSE == parts.end(part)) mark(part++, so_far());
         }
     }
@@ -312,6 +322,7 @@ __device__ __forceinline__ Sum sum_piece(const Coef& k, const Row<TP>& r, int a,
                 float d = 0.f, e = 0.f;
                 if (y + lane < end) w_of<ANY>(k, clean(to_f32(r.p[y + lane])), KIND ? clean(to_f32(r.q[y + lane])) : 0.f, d, e);
                 t.add(d, e);
+                t.settle();
             }
             y = end;
             if (marks) mark(part, t);
@@ -482,7 +493,6 @@ __global__ void __launch_bounds__(NT, 1024 / NT) verify_kernel(const __grid_cons
         Sum v;
         if (lane < WARPS) v = sum_of(wsum[lane]);
         v = warp_sum(v);
-        v.settle();
         if (ctas > 1) {
             const uint32_t bar = ptx::smem_u32(&bars[buf]);
             if (lane == 0) ptx::mbar_expect_tx(bar, ctas * 8);
@@ -503,7 +513,6 @@ __global__ void __launch_bounds__(NT, 1024 / NT) verify_kernel(const __grid_cons
         }
         share = dead ? Sum{} : v;
         total = dead ? Sum{} : warp_sum(v);
-        total.settle();
     };
 
     int node_before = INT_MIN;                        // whose p and q the pass before went over
@@ -640,6 +649,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) verify_kernel(const __grid_cons
                     for (int e = 0; e < 4; ++e) entry(y0 + 32 * e + lane, y0 + 32 * e + lane < to, d[e], r[e]);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) v.add(d[e], r[e]);
+                    v.settle();
                 }
                 v = warp_sum(v);
                 if (lane == 0) wsum[warp] = make_float2(v.hi, v.lo);

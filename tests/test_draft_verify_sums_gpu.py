@@ -105,3 +105,30 @@ def test_a_product_rounded_to_the_target(V, accept):
     assert wp == ([[2]] * n if accept else [[]] * n) and wn == [5 if accept else at] * n
     assert length.tolist() == [len(w) for w in wp]
     assert nxt.tolist() == wn
+
+
+@pytest.mark.parametrize("io, value", [("f32", 0.1), ("f32", 1e-5), ("bf16", 0.1)])
+@pytest.mark.parametrize("V, n", [(1 << 22, 700), (1 << 24, 300), (1 << 24, 1)])
+@pytest.mark.parametrize("off", [0, 1])
+def test_even_rows(io, value, V, n, off):
+    """Rows of one value: every sum is a multiple of it, and u_next times the whole is a whole number of entries, so
+    the next token is u_next V exactly.
+
+    A sum is a pair hi + lo of fp32.  Behind a lane's own sum (settled: |lo| is half a step U of hi at most) 32 lanes are
+    joined in five additions: their lo and the additions' errors come to at most 1.5 U + 5 U / 2 = 4 U before the
+    sum is settled, warps and CTAs to less.  A sum below 2^46 units of the value's last place has U <= 2^22 units, so
+    lo stays within 2^24 of them and no addition rounds: with 24 bits for the value up to V = 2^22 the token is exact.
+    Above, each of fewer than 24 additions rounds lo by 2^-24 4 U <= 2^-45 of the sum, together less than 2^-40 of it,
+    where an entry is 2^-24 of it: u_next V is a border between two tokens, and either may follow."""
+    row = torch.full((V,), value, dtype=IO[io])
+    k = torch.arange(n) * 1021 % 1024 if n > 1 else torch.tensor([341])
+    u_next = k.float() / 1024
+    tokens = torch.zeros(n, 1, dtype=torch.int32, device=DEV)
+    parents = torch.full((n, 1), -1, dtype=torch.int32, device=DEV)
+    rows = one_row(row, n, off)
+    nxt = kda.kda_draft_verify(rows[:, None], tokens, parents, torch.zeros(n, 1, device=DEV), dev(u_next))[2].cpu()
+    want = k * (V // 1024)
+    if V <= 1 << 22 or io == "bf16":                     # (bf16: 8 bits for the value)
+        assert nxt.tolist() == want.tolist()
+    else:
+        assert bool(((nxt == want) | (nxt == (want - 1).clamp(min=0))).all())
