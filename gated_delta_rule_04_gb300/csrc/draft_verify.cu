@@ -114,22 +114,13 @@ struct Coef {
 };
 enum Kind { P_ONLY, ONE, ANY };      // c = 0, c = 1 (the first refusal), any
 
-// What of e is taken off p beside m, where c q = m + e: at m = p, where c q may lie below p still, no more than
-// leaves W at zero; above it p is used up.
-__device__ __forceinline__ float rest_of(float m, float p, float e) { return m < p ? e : m == p ? fminf(e, 0.f) : 0.f; }
-
-// W of one token as two floats, p and q finite and not negative: p - c q with c q = m + e cut off at p, so that
-// m <= p and p - m is d + r exactly (Dekker).
+// W of one token as two floats, p and q finite and not negative: p - c q with c q = m + e, m <= p, so that p - m is
+// d + r exactly (Dekker).  Where the product is above p, by however little, e takes r below -d: W is then zero.
 template <int KIND> __device__ __forceinline__ void w_of(const Coef& k, float p, float q, float& d, float& r) {
-    float m = q, e = 0.f;
-    if (KIND == ANY) {
-        m = __fmul_rn(k.hi, q);
-        e = rest_of(m, p, __fmaf_rn(k.lo, q, __fmaf_rn(k.hi, q, -m)));
-    }
-    m = fminf(m, p);
+    const float m = fminf(KIND == ANY ? __fmul_rn(k.hi, q) : q, p);
     d = __fsub_rn(p, m);
     r = __fsub_rn(__fsub_rn(p, d), m);
-    if (KIND == ANY) r = __fsub_rn(r, e);
+    if (KIND == ANY) r = fmaxf(__fsub_rn(r, __fmaf_rn(k.lo, q, __fmaf_rn(k.hi, q, -m))), -d);
 }
 
 // A lane's sums of W, of two tokens at a time side by side, for values that are neither negative nor infinite nor
@@ -151,12 +142,12 @@ struct Pairs {
             d = sub2(p, m);
             lo = add2(lo, sub2(sub2(p, d), m));
         } else if (KIND == ANY) {
-            const float2 h = make_float2(k.hi, k.hi), m = __fmul2_rn(h, q);   // (as w_of)
-            float2 e = __ffma2_rn(make_float2(k.lo, k.lo), q, __ffma2_rn(h, q, __fmul2_rn(m, make_float2(-1.f, -1.f))));
-            e = make_float2(rest_of(m.x, p.x, e.x), rest_of(m.y, p.y, e.y));
-            const float2 c = make_float2(fminf(m.x, p.x), fminf(m.y, p.y));
-            d = sub2(p, c);
-            lo = add2(lo, sub2(sub2(sub2(p, d), c), e));
+            const float2 h = make_float2(k.hi, k.hi), v = __fmul2_rn(h, q);   // (as w_of)
+            const float2 m = make_float2(fminf(v.x, p.x), fminf(v.y, p.y));
+            const float2 e = __ffma2_rn(make_float2(k.lo, k.lo), q, __ffma2_rn(h, q, __fmul2_rn(m, make_float2(-1.f, -1.f))));
+            d = sub2(p, m);
+            const float2 r = sub2(sub2(sub2(p, d), m), e);
+            lo = add2(lo, make_float2(fmaxf(r.x, -d.x), fmaxf(r.y, -d.y)));
         }
         const float2 s = add2(hi, d), b = sub2(s, hi);
         lo = add2(lo, add2(sub2(hi, sub2(s, b)), sub2(d, b)));
