@@ -100,6 +100,7 @@ __global__ void __launch_bounds__(NT, PER_SM)
             const int tt = g.tiles_t - 1 - tile.x, t = tt * CHUNK + warp * SUB, c0 = tile.y * TILE_C;
             const int rows = (int)g.T - t, cols = min(TILE_C, g.C - c0);
             if constexpr (MODE != MTMA) {
+                __syncwarp();                        // (a lane's copies come where others have read)
                 const uint32_t s = ptx::smem_u32(mine) + stage * STAGE_BYTES;
                 R::load(s, g.x, g.x_s, t, c0, rows, cols);
                 R::load(s + R::TILE, g.r, g.r_s, t, c0, rows, cols);

@@ -121,6 +121,7 @@ __global__ void __launch_bounds__(ALL, PER_SM)
     uint32_t phases = 0;
     auto issue = [&](int stage, int k) {
         if constexpr (MODE != MTMA) {
+            __syncwarp();                            // (a lane's copies come where others have read)
             const int2 tile = tk[k % RING];
             if (tile.x >= 0) {
                 const int t = tile.x * CHUNK + warp * SUB, c0 = tile.y * TILE_C;
