@@ -36,7 +36,8 @@ constexpr int PARTS = 8;             // of a piece, whose sums are kept for the 
 constexpr int MARKED = 2048;         // a piece longer than this keeps them
 constexpr int STAGED = 22;           // entries a thread that the token is found in without another read
 constexpr int LOOSE = 8;             // entries a lane and step where rows lie off 16 bytes
-constexpr uint64_t WAIT_NS = 2000000000ull;
+constexpr uint64_t WAIT_NS = 2000000000ull;   // the limit of a wait for the other CTAs' sums
+constexpr uint64_t DRAIN_NS = 100000;         // a store to another CTA's shared memory has arrived long before
 
 __device__ __forceinline__ float clean(float v) { return v > 0.f && v <= 3.402823466e38f ? v : 0.f; }
 
@@ -363,6 +364,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) verify_kernel(const __grid_cons
     Order& order = *reinterpret_cast<Order*>(order_smem);
     __shared__ float2 wsum[WARPS], slots[2][MAX_CTAS];
     __shared__ uint64_t bars[2];
+    __shared__ uint32_t given_up;                     // a CTA of the session waited in vain
     __shared__ float2 psum[WARPS][PARTS];
     const int s = blockIdx.x / ctas, rank = blockIdx.x % ctas, tid = threadIdx.x, lane = tid % 32;
     // (the same in all lanes, which the compiler cannot see from tid / 32: what the first warp alone does, with its
@@ -382,6 +384,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) verify_kernel(const __grid_cons
         ptx::mbar_init(ptx::smem_u32(&bars[0]), 1);
         ptx::mbar_init(ptx::smem_u32(&bars[1]), 1);
         ptx::fence_mbar_init();
+        given_up = 0;
     }
     __syncthreads();
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");   // (the barriers are there; waited for below)
@@ -495,15 +498,15 @@ __global__ void __launch_bounds__(NT, 1024 / NT) verify_kernel(const __grid_cons
                 asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];"
                              ::"r"(to), "f"(v.hi), "f"(v.lo), "r"(tobar) : "memory");
             }
-            const bool there = dead || ptx::mbar_wait(bar, turn >> 1 & 1, WAIT_NS);
-            dead = __any_sync(FULL, !there) || dead;  // gave up: the token will be -1
+            const bool there = ptx::mbar_wait(bar, turn >> 1 & 1, g.wait_ns);
+            dead = __any_sync(FULL, !there);          // gives up: see below
             v = lane < ctas ? sum_of(slots[buf][lane]) : Sum{};
             ++turn;
         } else if (lane > 0) {
             v = Sum{};
         }
-        share = dead ? Sum{} : v;
-        total = dead ? Sum{} : warp_sum(v);
+        share = v;
+        total = warp_sum(v);
     };
 
     int node_before = INT_MIN;                        // whose p and q the pass before went over
@@ -554,11 +557,13 @@ __global__ void __launch_bounds__(NT, 1024 / NT) verify_kernel(const __grid_cons
         if (warp == 0) {
             exchange();
             int then = SUM;
-            if (!ending) {
+            if (dead) {
+                then = END;                           // no sum, no further test: the others will wait in vain too, or are done
+            } else if (!ending) {
                 T = total;
             } else if (!total.positive() && k.kind()) {
                 c = Coef{};                           // nothing is left: p itself
-            } else if (refused && !dead && total.hi <= 1e-9f * taken) {
+            } else if (refused && total.hi <= 1e-9f * taken) {
                 // what is left may be the rounding of what was taken out: the row once more, by one CTA
                 then = rank == 0 ? SEARCH : END;
                 if (lane == 0) {
@@ -719,9 +724,18 @@ __global__ void __launch_bounds__(NT, 1024 / NT) verify_kernel(const __grid_cons
             if (p_row(cur) == nullptr) g.next[s] = -1;
         }
     }
+    if (warp == 0 && dead && lane < ctas) {           // all of them know
+        uint32_t to = ptx::smem_u32(&given_up);
+        asm volatile("mapa.shared::cluster.u32 %0, %0, %1;\n st.shared::cluster.u32 [%0], %2;" : "+r"(to) : "r"(lane), "r"(1) : "memory");
+    }
     __syncwarp();
     // no CTA leaves while another may still write to it
     asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (given_up) {                                   // whatever token another CTA found: it is not valid
+        if (rank == 0 && tid == 0) g.next[s] = -1;
+        // sums that nobody waited for may be on their way here
+        for (const uint64_t t0 = ptx::globaltimer_ns(); ptx::globaltimer_ns() - t0 < DRAIN_NS;) {}
+    }
 }
 
 template <typename TP, int NT> cudaError_t verify(const VerifyArgs& a, int ctas, cudaStream_t s) {
@@ -775,13 +789,13 @@ cudaError_t launch_verify(const VerifyArgs& a, int io_bf16, cudaStream_t s) {
 
 using namespace kda;
 
-extern "C" kda_status kda_draft_verify(int32_t dtype, int32_t n_sessions, int32_t n_nodes, int32_t vocab, const void* p,
-                                       int64_t p_session_stride, int64_t p_row_stride, const void* p_last,
-                                       int64_t p_last_stride, const void* q, int64_t q_session_stride,
-                                       int64_t q_row_stride, const void* q_last, int64_t q_last_stride,
-                                       const int32_t* tokens, const int32_t* parents, const float* u,
-                                       const float* u_next, int32_t max_len, int32_t* path, int32_t* path_len,
-                                       int32_t* next_token, void* stream) {
+static kda_status draft_verify(int32_t dtype, int32_t n_sessions, int32_t n_nodes, int32_t vocab, const void* p,
+                               int64_t p_session_stride, int64_t p_row_stride, const void* p_last,
+                               int64_t p_last_stride, const void* q, int64_t q_session_stride,
+                               int64_t q_row_stride, const void* q_last, int64_t q_last_stride,
+                               const int32_t* tokens, const int32_t* parents, const float* u,
+                               const float* u_next, int32_t max_len, int32_t* path, int32_t* path_len,
+                               int32_t* next_token, void* stream, uint64_t wait_ns) {
     if (dtype != KDA_DTYPE_F32 && dtype != KDA_DTYPE_BF16) return KDA_ERR_INVALID_ARG;
     if (n_sessions < 0 || n_nodes < 1 || n_nodes > KDA_TREE_MAX_NODES || vocab < 1 || max_len < 1 ||
         max_len > KDA_TREE_MAX_NODES)
@@ -800,6 +814,33 @@ extern "C" kda_status kda_draft_verify(int32_t dtype, int32_t n_sessions, int32_
         q_last_stride < 0)
         return KDA_ERR_INVALID_ARG;
     VerifyArgs a{p, p_last, q, q_last, p_session_stride, p_row_stride, p_last_stride, q_session_stride, q_row_stride,
-                 q_last_stride, tokens, parents, u, u_next, path, path_len, next_token, n_sessions, n_nodes, vocab, max_len};
+                 q_last_stride, tokens, parents, u, u_next, path, path_len, next_token, n_sessions, n_nodes, vocab, max_len, wait_ns};
     return launch_verify(a, dtype == KDA_DTYPE_BF16, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
+
+extern "C" {
+
+kda_status kda_draft_verify(int32_t dtype, int32_t n_sessions, int32_t n_nodes, int32_t vocab, const void* p,
+                            int64_t p_session_stride, int64_t p_row_stride, const void* p_last, int64_t p_last_stride,
+                            const void* q, int64_t q_session_stride, int64_t q_row_stride, const void* q_last,
+                            int64_t q_last_stride, const int32_t* tokens, const int32_t* parents, const float* u,
+                            const float* u_next, int32_t max_len, int32_t* path, int32_t* path_len, int32_t* next_token,
+                            void* stream) {
+    return draft_verify(dtype, n_sessions, n_nodes, vocab, p, p_session_stride, p_row_stride, p_last, p_last_stride, q,
+                        q_session_stride, q_row_stride, q_last, q_last_stride, tokens, parents, u, u_next, max_len, path,
+                        path_len, next_token, stream, WAIT_NS);
+}
+
+// As kda_draft_verify with another limit of the waits between a session's CTAs, for tests (the interface has none).
+kda_status kda_draft_verify_wait(int32_t dtype, int32_t n_sessions, int32_t n_nodes, int32_t vocab, const void* p,
+                                 int64_t p_session_stride, int64_t p_row_stride, const void* p_last, int64_t p_last_stride,
+                                 const void* q, int64_t q_session_stride, int64_t q_row_stride, const void* q_last,
+                                 int64_t q_last_stride, const int32_t* tokens, const int32_t* parents, const float* u,
+                                 const float* u_next, int32_t max_len, int32_t* path, int32_t* path_len, int32_t* next_token,
+                                 void* stream, uint64_t wait_ns) {
+    return draft_verify(dtype, n_sessions, n_nodes, vocab, p, p_session_stride, p_row_stride, p_last, p_last_stride, q,
+                        q_session_stride, q_row_stride, q_last, q_last_stride, tokens, parents, u, u_next, max_len, path,
+                        path_len, next_token, stream, wait_ns);
+}
+
+}  // extern "C"

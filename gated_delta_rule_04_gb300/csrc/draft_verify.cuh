@@ -12,6 +12,7 @@ struct VerifyArgs {
     const float *u, *u_next;                      // [n][R], [n]
     int32_t *path, *path_len, *next;              // [n][max_len], [n], [n]
     int32_t n, R, V, max_len;
+    uint64_t wait_ns;                             // the limit of a wait between a session's CTAs
 };
 cudaError_t launch_verify(const VerifyArgs& a, int io_bf16, cudaStream_t s);
 

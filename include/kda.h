@@ -569,8 +569,9 @@ kda_status kda_glr_commit(const kda_glr_params* p, int32_t n_sessions, int32_t n
  * or the path holds max_len nodes, the walk ends, and the token that follows is the smallest y with
  * W(y) > 0 and W(0) + ... + W(y) > u_next (W(0) + ... + W(V - 1)); if rounding leaves none, the
  * last with W(y) > 0.  If W is zero everywhere it is p itself; if that is, the token is -1.
- * Sums and tests carry 48 bits.  The call takes no workspace; should its
- * bounded wait between a session's CTAs ever run out, next_token is -1.
+ * Sums and tests carry 48 bits.  The call takes no workspace; should a
+ * bounded wait between a session's CTAs ever run out, its next_token is -1, and its path
+ * holds what had been accepted by then.
  *
  *   dtype        : kda_dtype of p, p_last, q and q_last
  *   n_nodes      : 1 to KDA_TREE_MAX_NODES
