@@ -105,7 +105,8 @@ __global__ void __launch_bounds__(NT, 7) token_kernel(const __grid_constant__ To
         load_f32<V>(g.i_bias, c, ib);
 #pragma unroll
         for (int p = 0; p < PAIRS; ++p) {
-            k[p] = Gate{make_float2(-expf(A[p].x), -expf(A[p].y)), mul2(rb[p], f2(-LOG2E)), mul2(ib[p], f2(-LOG2E))};
+            // (V = 1: the second of the pair is no channel, and asks for no exponential)
+            k[p] = Gate{make_float2(-expf(A[p].x), V > 1 ? -expf(A[p].y) : 0.f), mul2(rb[p], f2(-LOG2E)), mul2(ib[p], f2(-LOG2E))};
             wide |= !(k[p].ea.x >= -NEAR && k[p].ea.y >= -NEAR);
         }
     }

@@ -1,11 +1,12 @@
 """The gated linear recurrence over many tiles whose rows are no tensor copies: a warp's own copies take the
-place of rows that its lanes have just read, tile after tile in the same CTA."""
+place of rows that its lanes have just read, tile after tile in the same CTA.  Tokens whose channels are taken one
+by one."""
 import pytest
 import torch
 
 import gated_delta_rule_04_gb300 as kda
 from glr_ref import SUM_TOL, close, make_inputs
-from test_glr_gpu import GRADS, IO, cumsum, dev, forward64, params
+from test_glr_gpu import GRADS, IO, cumsum, dev, forward64, params, tokens_ref
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -65,3 +66,22 @@ def test_rows_that_follow_one_another(io, C, pad):
     want = gradients64(i, n, s, j, before, h)
     for k in GRADS:
         close(k, getattr(g, k), want[k].cpu(), SUM_TOL * (T / 700) ** 0.5 if k in ("dA_log", "dr_bias", "di_bias") else None)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("C", [1, 31, 129])
+@pytest.mark.parametrize("faster", [False, True])
+def test_tokens_of_single_channels(io, C, faster):
+    """Channels that are taken one by one (odd rows): decays that no exponential is needed for, and one channel
+    among them whose decay may need it."""
+    n, R = 3, 5
+    i = make_inputs(n * R, n, C, IO[io], 80 + C)
+    i["A_log"] -= 1.0                                    # exp(A_log) is at most e^-1
+    if faster:
+        i["A_log"][C // 2] = 1.5
+    x, r, s, z = (dev(i[k]).view(n, R, C) for k in ("x", "r", "i", "z"))
+    wo, wS = tokens_ref(i, n, R, i["S"], [range(R)] * n)
+    S = dev(i["S"])
+    o = kda.kda_glr_decode(params(i, io), x, r, s, S, z=z)
+    close("o", o, wo)
+    close("S", S, wS)
