@@ -760,7 +760,8 @@ def kda_glr_decode(params: GlrParams, x, r, i, S, z=None, slots=None, S_out=None
     rows may be column ranges of projection rows.  The pool S [n_slots][C] is
     updated in place, or S_out is written instead; with ``keep_state`` no state
     is written (a verify round, whose accepted tokens kda_glr_commit applies).
-    ``slots`` (int32 [n]) maps sessions to pool slots.  Returns o [n][n_tokens][C]."""
+    ``slots`` (int32 [n]) maps sessions to pool slots; with ``keep_state`` they may
+    repeat (a draft tree's rows: a run for each way from the root to a leaf).  Returns o [n][n_tokens][C]."""
     import torch
     if x.dim() != 3:
         raise ValueError(f"x: expected [n][n_tokens][C], got {list(x.shape)}")

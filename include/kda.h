@@ -519,7 +519,10 @@ kda_status kda_glr_backward(const kda_glr_params* p, const void* x, int64_t x_st
  *                  and output rows left untouched
  *   S_in, S_out  : device pools [n_slots][C] fp32; they may alias.  S_out NULL
  *                  keeps the states: the rows of a verify round, whose accepted
- *                  tokens kda_glr_commit applies
+ *                  tokens kda_glr_commit applies.  Slots may repeat then: the rows
+ *                  of a draft tree are straight runs from one state, a run for each
+ *                  way from the root to a leaf (what lies behind a shorter one's
+ *                  leaf is not used)
  *   o            : device [n_sessions][n_tokens][C] io_dtype, packed
  */
 kda_status kda_glr_decode(const kda_glr_params* p, int32_t n_sessions, int32_t n_tokens, const void* x, int64_t x_stride,
@@ -530,8 +533,9 @@ kda_status kda_glr_decode(const kda_glr_params* p, int32_t n_sessions, int32_t n
 /*
  * Advances each session's state by the accepted tokens of a round: as
  * kda_tree_commit, for this mixer.
- *   x, r, i      : the round's rows, as for kda_glr_decode with n_nodes tokens
- *                  (1 to KDA_TREE_MAX_NODES)
+ *   x, r, i      : the round's rows, one for each node: strided as for kda_glr_decode
+ *                  with n_nodes tokens (1 to KDA_TREE_MAX_NODES); a path may be any
+ *                  of the nodes in any order
  *   path, path_len, max_len, slots, n_slots, S_in, S_out : as for kda_tree_commit;
  *                  a session with a slot, path_len or accepted node out of range
  *                  is skipped
