@@ -63,7 +63,7 @@ template <typename Args> __device__ __forceinline__ Gate make_gate(const Args& g
 
 // A token's decay a = exp(la) and m^2 = 1 - a^2, for la <= 0.  Near 1 both come from
 // q = exp(la) - 1 = la P(la): P interpolates (exp(x) - 1) / x at the six Chebyshev points
-// of [-1/2, 0] (relative error 1.5e-9, in fp32 0.8 x 2^-24).  a = 1 + q is then rounded to
+// of [-1/2, 0], its last constant set to 1 (relative error 3.1e-9, in fp32 1.7 x 2^-24).  a = 1 + q is then rounded to
 // nearest, where an exponential's error has one sign that a state adds up at every
 // token, and m^2 = -q (2 + q) keeps its digits (its negative is given).  WIDE: la may lie below -1/2; a channel
 // whose exp(A_log) is at most 1/2 never gets there.
