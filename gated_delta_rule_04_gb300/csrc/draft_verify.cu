@@ -209,14 +209,25 @@ struct Parts {
 
 // The lane's share of the sum of W over [a, b): 16 bytes at a time from the first boundary on.  With `marks`,
 // the warp's sums up to the end of each part are left there.  `there`: the pass before was over the same rows,
-// and a piece that fits the ring is still in it.
+// and a piece that fits the ring is still in it.  (Chosen tokens) the n_gone tokens `gone` count as zero: next
+// to what they hold the rest may be less than a sum's rounding, so they are never in it.
 template <int KIND, int NT, typename TP>
 __device__ __forceinline__ Sum sum_piece(const Coef& k, const Row<TP>& r, int a, int b, uint4* ring, float2* marks,
-                                         bool there) {
+                                         bool there, const int* gone, int n_gone) {
     constexpr int N = Vec<TP>::N;
     const int lane = threadIdx.x & 31;
     const Parts parts(r, a, b);
     const int va = parts.va;
+    uint64_t inside = 0;                              // of them, those in this piece: few warps have any
+    if (KIND == P_ONLY && n_gone > 0) {
+        auto in = [&](int j) { return j < n_gone && gone[j] >= a && gone[j] < b; };
+        inside = (uint64_t)__ballot_sync(FULL, in(lane)) | (uint64_t)__ballot_sync(FULL, in(lane + 32)) << 32;
+    }
+    auto is_gone = [&](int y) {
+        bool is = false;
+        for (uint64_t w = inside; w; w &= w - 1) is |= gone[__ffsll((long long)w) - 1] == y;
+        return is;
+    };
     Pairs s;
     auto so_far = [&]() {
         Sum t;
@@ -233,7 +244,7 @@ __device__ __forceinline__ Sum sum_piece(const Coef& k, const Row<TP>& r, int a,
         const int nv = (b - va) / N, vb = va + nv * N;
         // the head's and the tail's entries, a lane each (at most N - 1 of either)
         const int edge = lane < va - a ? a + lane : lane >= 16 && lane - 16 < b - vb ? vb + lane - 16 : -1;
-        const float pe = edge >= 0 ? to_f32(r.p[edge]) : 0.f, qe = KIND && edge >= 0 ? to_f32(r.q[edge]) : 0.f;
+        const float pe = edge >= 0 && !is_gone(edge) ? to_f32(r.p[edge]) : 0.f, qe = KIND && edge >= 0 ? to_f32(r.q[edge]) : 0.f;
         // Steps of two pieces of 16 bytes a lane, copied DEPTH ahead of the sum; a lane reads what it copied, so
         // nothing waits for another.  Behind the last piece a step is filled up with zeros.
         const int steps = (nv + 63) / 64;
@@ -263,6 +274,16 @@ __device__ __forceinline__ Sum sum_piece(const Coef& k, const Row<TP>& r, int a,
             for (int j = 0; j < N / 2; ++j)
                 s.add<KIND>(k, Vec<TP>::pair(x, j), KIND ? Vec<TP>::pair(y, j) : make_float2(0.f, 0.f));
         };
+        // Sets those of a step to zero where it lies copied, by the lane that reads them.
+        auto take_out = [&](int st, int step) {
+            for (uint64_t w = inside; w; w &= w - 1) {
+                const int e = gone[__ffsll((long long)w) - 1] - va;
+                if (e < 0 || e >= nv * N || e / (64 * N) != step || (e / N & 31) != lane) continue;
+                unsigned char* z = reinterpret_cast<unsigned char*>(ring + threadIdx.x + (st * 4 + (e / (32 * N) & 1) * 2) * NT) +
+                                   e % N * (int)sizeof(TP);
+                for (int j = 0; j < (int)sizeof(TP); ++j) z[j] = 0;
+            }
+        };
 #pragma unroll
         for (int st = 0; st < DEPTH; ++st) issue(st, st < steps && !(there && steps <= DEPTH));
         // (the head belongs to the first part, the tail to the last)
@@ -274,6 +295,7 @@ __device__ __forceinline__ Sum sum_piece(const Coef& k, const Row<TP>& r, int a,
             for (int st = 0; st < DEPTH; ++st) {
                 if (i == steps) break;
                 asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
+                if (KIND == P_ONLY && inside) take_out(st, i);
                 const uint4* const at = ring + threadIdx.x + st * 4 * NT;
                 add(at[0], KIND ? at[NT] : at[0]);
                 add(at[2 * NT], KIND ? at[3 * NT] : at[0]);
@@ -312,7 +334,7 @@ __device__ __forceinline__ Sum sum_piece(const Coef& k, const Row<TP>& r, int a,
             const int end = parts.end(part);
             for (; y < end; y += 32) {
                 float d = 0.f, e = 0.f;
-                if (y + lane < end) w_of<ANY>(k, clean(to_f32(r.p[y + lane])), KIND ? clean(to_f32(r.q[y + lane])) : 0.f, d, e);
+                if (y + lane < end && !is_gone(y + lane)) w_of<ANY>(k, clean(to_f32(r.p[y + lane])), KIND ? clean(to_f32(r.q[y + lane])) : 0.f, d, e);
                 t.add(d, e);
                 t.settle();
             }
@@ -353,7 +375,6 @@ struct Order {
     int whole;                       // the sums gave (0), the whole row (1), or p itself (2); 3: found
     Sum base, goal;                  // the sum before that, and the one to be passed
     int tok[KDA_TREE_MAX_NODES];
-    float p[KDA_TREE_MAX_NODES];
 };
 
 template <typename TP, int NT>
@@ -427,7 +448,6 @@ __global__ void __launch_bounds__(NT, 1024 / NT) verify_kernel(const __grid_cons
     bool first = true, arrived = true, ending = false, dead = false;
     Coef c;
     Sum T = sum_of(1.f, 0.f), total;
-    float taken = 0.f;                                // (chosen tokens) their p
     Sum share;                                        // the sum of CTA `lane`
 
     // Goes on with the tests until a sum is needed: true, or the walk has ended: false.
@@ -465,7 +485,6 @@ __global__ void __launch_bounds__(NT, 1024 / NT) verify_kernel(const __grid_cons
                 c = Coef{};
                 T = sum_of(1.f, 0.f);
                 refused = 0;
-                taken = 0.f;
                 first = arrived = true;
                 continue;
             }
@@ -473,7 +492,6 @@ __global__ void __launch_bounds__(NT, 1024 / NT) verify_kernel(const __grid_cons
             if (hot) {
                 T.sub(w);
                 T.settle();
-                taken += w.hi;
                 if (w.positive()) refused |= (uint64_t)1 << r;
             } else {
                 c.add(T);
@@ -528,7 +546,6 @@ __global__ void __launch_bounds__(NT, 1024 / NT) verify_kernel(const __grid_cons
                     if (refused >> r & 1) {
                         const int at = __popcll(refused & (((uint64_t)1 << r) - 1));
                         order.tok[at] = tok[h];
-                        order.p[at] = pt[h];
                     }
                 }
                 if (lane == 0) order.refused = __popcll(refused);
@@ -546,10 +563,9 @@ __global__ void __launch_bounds__(NT, 1024 / NT) verify_kernel(const __grid_cons
             const bool there = node == node_before && k.kind();      // (a refusal more at the same node: both rows again)
             node_before = k.kind() ? node : INT_MIN;
             float2* const marks = order.last && b - a > MARKED ? psum[warp] : nullptr;
-            Sum sum = k.kind() == P_ONLY ? sum_piece<P_ONLY, NT>(k, row, a, b, ring, marks, there)
-                    : k.kind() == ONE ? sum_piece<ONE, NT>(k, row, a, b, ring, marks, there) : sum_piece<ANY, NT>(k, row, a, b, ring, marks, there);
-            for (int j = lane; j < order.refused; j += 32)        // (p is what was added: the sum stays exact)
-                if (order.tok[j] >= a && order.tok[j] < b) sum.add(-order.p[j]);
+            Sum sum = k.kind() == P_ONLY ? sum_piece<P_ONLY, NT>(k, row, a, b, ring, marks, there, order.tok, order.refused)
+                    : k.kind() == ONE ? sum_piece<ONE, NT>(k, row, a, b, ring, marks, there, order.tok, 0)
+                                      : sum_piece<ANY, NT>(k, row, a, b, ring, marks, there, order.tok, 0);
             sum = warp_sum(sum);
             if (lane == 0) wsum[warp] = make_float2(sum.hi, sum.lo);
         }
@@ -561,17 +577,9 @@ __global__ void __launch_bounds__(NT, 1024 / NT) verify_kernel(const __grid_cons
                 then = END;                           // no sum, no further test: the others will wait in vain too, or are done
             } else if (!ending) {
                 T = total;
-            } else if (!total.positive() && k.kind()) {
+            } else if (!total.positive() && (k.kind() || refused)) {
                 c = Coef{};                           // nothing is left: p itself
-            } else if (refused && total.hi <= 1e-9f * taken) {
-                // what is left may be the rounding of what was taken out: the row once more, by one CTA
-                then = rank == 0 ? SEARCH : END;
-                if (lane == 0) {
-                    order.whole = 1;
-                    order.a = 0;
-                    order.b = V;
-                    order.base = Sum{};
-                }
+                refused = 0;
             } else {
                 const Sum goal = times(g.u_next[s], total), incl = scan(share, MAX_CTAS);
                 const int owner = pick(Sum{}, incl, share, goal);
@@ -597,10 +605,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) verify_kernel(const __grid_cons
                     int a = row.begin(rank * WARPS + at), b = row.end(rank * WARPS + at, pieces);
                     if (b - a > MARKED) {             // and the part of it: lane i has the sum up to the end of part i
                         const Parts parts(row, a, b);
-                        Sum up_to = lane < PARTS ? sum_of(psum[at][lane]) : Sum{};
-                        if (lane < PARTS)
-                            for (int j = 0; j < order.refused; ++j)
-                                if (order.tok[j] >= a && order.tok[j] < parts.end(lane)) up_to.add(-order.p[j]);
+                        const Sum up_to = lane < PARTS ? sum_of(psum[at][lane]) : Sum{};
                         before = shfl(up_to, max(lane - 1, 0));
                         if (lane == 0) before = Sum{};
                         Sum part = up_to;
@@ -625,7 +630,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) verify_kernel(const __grid_cons
         if (order.then == SUM) continue;
         // That part once more: while it is long, a warp's share of it; then its W in shared memory (where
         // the copies were), so that of reads in a row, 1 to 3 us each while others sum, there is one.  Where
-        // rounding (of sums that tokens were taken out of) led to a part with nothing in it, the whole row; if
+        // rounding (of the difference of two marks) led to a part with nothing in it, the whole row; if
         // that has nothing, p itself.
         for (int whole = order.whole; whole < 3;) {
             const TP* const q = whole == 2 ? nullptr : row.q;

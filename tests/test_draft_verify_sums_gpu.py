@@ -132,3 +132,23 @@ def test_even_rows(io, value, V, n, off):
         assert nxt.tolist() == want.tolist()
     else:
         assert bool(((nxt == want) | (nxt == (want - 1).clamp(min=0))).all())
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("V, n, small", [(1 << 17, 8, 1e-13), (1 << 17, 200, 1e-13), (1 << 15, 700, 1e-12), (1 << 20, 3, 1e-14), (1 << 10, 30, 1e-16)])
+def test_a_rest_beside_large_refused_tokens(io, V, n, small):
+    """Chosen tokens that hold nearly all of the target are refused: the others have next to nothing each, all the same,
+    so their sums are exact, and u_next times the whole is a whole number of them."""
+    R = 6
+    tokens = torch.tensor([0, 3, V // 2, V // 2 + 1, V + R - 2, V + R - 1])
+    row = torch.full((V + R,), small, dtype=IO[io])
+    row[tokens] = (torch.tensor([0.3, 0.2, 0.3, 0.1, 0.05, 0.04])).to(IO[io])
+    t, parents, u = draft(n, tokens.tolist(), 1.0)   # (u T is at least what the target has)
+    k = torch.arange(n) * 1021 % 1024
+    nothing = torch.zeros(1, 1, V + R, dtype=IO[io], device=DEV).expand(n, R, V + R)
+    path, length, nxt = kda.kda_draft_verify(nothing, t, parents, u, dev(k.float() / 1024), p_last=one_row(row, n))
+    left = torch.ones(V + R)
+    left[tokens] = 0
+    want = torch.searchsorted(left.cumsum(0), (k * (V // 1024)).float(), right=True)
+    assert not length.any()
+    assert nxt.tolist() == want.tolist()
