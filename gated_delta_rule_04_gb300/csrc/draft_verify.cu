@@ -11,14 +11,16 @@
 // what counts.  The token is found level by level: CTA, warp, part of its piece, then the
 // part's entries once more from L2.
 //
-// Sums, borders and tests are pairs of floats (two-sums and products of Knuth and Dekker: 48 bits): next to a
+// Sums, borders and tests are pairs of floats (two-sums and products of Knuth and Dekker): next to a
 // random border, in a sum over 10^5 entries, a 32-bit sum would take another token in one
 // session of 30, and this GPU adds 2 doubles a cycle and SM where the rows arrive at 3 pairs; each
-// operation on doubles also holds a warp up for 64 cycles and more.
+// operation on doubles also holds a warp up for 64 cycles and more.  A lane adds n entries to a pair of which the
+// second float's last place is 2^-48 of the sum: at most n^1/2 2^-49 or so off (softmax rows on the CPU: 2^-45 over
+// 4096), all lanes' sum less: 2^-48 of a row of 2^20 entries in one CTA.
 //
-// 256 sessions x 5 nodes x 131072, fp32: 49 to 54 us (4.5 TB/s of a copy's 6.8; memory 54 %, issue slots
-// 34 %): the pass over the rows takes 35 of them, the tests before it 4 and the exchange and search behind
-// it 5 to 10, in all sessions at about the same time.  1 x 6 nodes 9.3 us, a chain of latencies.
+// 256 sessions x 5 nodes x 131072, fp32: 48 us in a graph, 51 to 54 a call (4.6 TB/s of a copy's 6.8; memory
+// 57 %, issue slots 40 %): the pass over the rows takes about two thirds, the tests before it and the exchange and
+// search behind it the rest, in all sessions at about the same time.  1 x 6 nodes 9.0 us, a chain of latencies.
 #include <limits.h>
 
 #include <atomic>

@@ -495,8 +495,9 @@ kda_status kda_glr_prefill(const kda_glr_params* p, const void* x, int64_t x_str
  *                  di can be the halves of one row); dz is written where z is
  *                  given, and both are NULL otherwise
  *   dS_in        : device [n_seqs][C] fp32 or NULL (skipped)
- *   dA_log, dr_bias, di_bias : device [C] fp32, sums over all tokens; the last two
- *                  may be NULL (skipped)
+ *   dA_log, dr_bias, di_bias : device [C] fp32, sums over all tokens (of KDA_GLR_CHUNK
+ *                  tokens in fp32, of those with each addition's error kept); the
+ *                  last two may be NULL (skipped)
  *   workspace    : as for the prefill, of kda_glr_backward_workspace_bytes()
  * The gradients may not overlap one another, the inputs or dS_out; each is
  * overwritten.
@@ -573,7 +574,9 @@ kda_status kda_glr_commit(const kda_glr_params* p, int32_t n_sessions, int32_t n
  * or the path holds max_len nodes, the walk ends, and the token that follows is the smallest y with
  * W(y) > 0 and W(0) + ... + W(y) > u_next (W(0) + ... + W(V - 1)); if rounding leaves none, the
  * last with W(y) > 0.  If W is zero everywhere it is p itself; if that is, the token is -1.
- * Sums and tests carry 48 bits.  The call takes no workspace; should a
+ * Sums and tests are pairs of fp32: a row's sum is right to about 2^-48 of it up to 2^20 entries
+ * and to 2^-47 up to 2^23 (softmax rows; where more of the GPU shares a row, further).  Refused
+ * chosen tokens are in no sum, whatever they hold.  The call takes no workspace; should a
  * bounded wait between a session's CTAs ever run out, its next_token is -1, and its path
  * holds what had been accepted by then.
  *
